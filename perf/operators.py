@@ -103,7 +103,7 @@ def _lens(case):
 # V codes, V scales.  Codes are Q4_0 blocks of 32 dims: byte j holds dims j (low nibble) and j + 16.
 
 def _orders(d, device):
-    """Byte offset in a tile of byte j of block b of token t, for K and V codes, and half index of the scales."""
+    """Byte offset in its part of a tile of byte j of block b of token t, for K and V codes, and half index of their scales."""
     nb = d // 32
     t = torch.arange(32, device=device).view(32, 1, 1)
     b = torch.arange(nb, device=device).view(1, nb, 1)
@@ -111,10 +111,11 @@ def _orders(d, device):
     u = (t // 8) * nb + b
     kc = ((u // 4) * 32 + (t % 8) * 4 + j // 4) * 16 + (u % 4) * 4 + j % 4
     x = t % 16
-    w = ((t // 16) * nb + b) * 2 + x // 8
-    vc = ((w // 4) * 32 + (j % 8) * 4 + (x % 8) // 2) * 16 + (w % 4) * 4 + (x % 2) * 2 + j // 8
-    sc = ((t // 2) * nb + b) * 2 + t % 2
-    return kc.reshape(-1), vc.reshape(-1), sc.reshape(-1)
+    w = ((t // 16) * nb + b) * 2 + x % 4 // 2
+    vc = ((w // 4) * 32 + (j % 8) * 4 + x // 4) * 16 + (w % 4) * 4 + (x % 2) * 2 + j // 8
+    ks = ((t // 16 * 8 + t % 8) * nb + b) * 2 + t // 8 % 2
+    vs = ((t // 4) * nb + b) * 4 + t % 4
+    return kc.reshape(-1), vc.reshape(-1), ks.reshape(-1), vs.reshape(-1)
 
 
 def _quantise(x):
@@ -133,9 +134,9 @@ def _quantise(x):
 def _tiles(k, v):
     """Tiles [n, 36 d] (uint8) of K and V rows [n, 32, d]."""
     n, _, d = k.shape
-    kc, vc, sc = _orders(d, k.device)
+    kc, vc, ks, vs = _orders(d, k.device)
     out = torch.empty((n, 36 * d), dtype=torch.uint8, device=k.device)
-    for x, code_at, scale_at, order in ((k, 0, 16 * d, kc), (v, 18 * d, 34 * d, vc)):
+    for x, code_at, scale_at, order, sc in ((k, 0, 16 * d, kc, ks), (v, 18 * d, 34 * d, vc, vs)):
         codes, scales = _quantise(x)
         byte = (codes[..., :16] | (codes[..., 16:] << 4)).reshape(n, -1)
         part = torch.empty_like(byte)
@@ -149,9 +150,9 @@ def _tiles(k, v):
 
 def _values(tiles, d):
     """K and V values (fp32) [..., 32, d] of tiles [..., 36 d]."""
-    kc, vc, sc = _orders(d, tiles.device)
+    kc, vc, ks, vs = _orders(d, tiles.device)
     got = []
-    for code_at, scale_at, order in ((0, 16 * d, kc), (18 * d, 34 * d, vc)):
+    for code_at, scale_at, order, sc in ((0, 16 * d, kc, ks), (18 * d, 34 * d, vc, vs)):
         byte = tiles[..., code_at:code_at + 16 * d][..., order].unflatten(-1, (32, d // 32, 16))
         codes = torch.cat([byte & 15, byte >> 4], -1).float() - 8.0
         scale = tiles[..., scale_at:scale_at + 2 * d].contiguous().view(torch.float16)[..., sc].float()
@@ -336,12 +337,12 @@ def _weights_plain(st):
 def _append_plain(st):
     c = st["case"]
     hk, d, page = c["hk"], c["d"], c["page"]
-    kc, vc, sc = (x.view(32, -1) for x in _orders(d, st["k"].device))
+    kc, vc, ks, vs = (x.view(32, -1) for x in _orders(d, st["k"].device))
     tiles = st["pages"].view(-1, hk, page // 32, 36 * d)
     at = st["slots"]
     row = (at % 32).view(-1, 1, 1)
     base = (at // page).view(-1, 1, 1), torch.arange(hk, device=at.device).view(1, -1, 1), ((at % page) // 32).view(-1, 1, 1)
-    for x, code_at, scale_at, order in ((st["k"], 0, 16 * d, kc), (st["v"], 18 * d, 34 * d, vc)):
+    for x, code_at, scale_at, order, sc in ((st["k"], 0, 16 * d, kc, ks), (st["v"], 18 * d, 34 * d, vc, vs)):
         codes, scales = _quantise(x)
         tiles[(*base, code_at + order[row.flatten()].unsqueeze(1))] = (codes[..., :16] | (codes[..., 16:] << 4)).flatten(2)
         where = scale_at + 2 * sc[row.flatten()].unsqueeze(1)
@@ -372,7 +373,7 @@ def _evict_plain(st):
     src = st["table"].long().gather(1, (safe // page).flatten(1)).view(n, hk, keep) * page + safe % page
     tiles = st["pages"].view(-1, hk, page // 32, 36 * d)
     head = torch.arange(hk, device=w.device).view(1, hk, 1)
-    kc, vc, sc = (x.view(32, -1) for x in _orders(d, w.device))
+    kc, vc, ks, vs = (x.view(32, -1) for x in _orders(d, w.device))
     dst = (st["dst"].long().gather(1, (torch.arange(keep, device=w.device) // page).expand(n, -1)) * page
            + torch.arange(keep, device=w.device) % page).unsqueeze(1).expand(n, hk, keep)
     src, dst, head = src[there], dst[there], head.expand(n, hk, keep)[there]
@@ -380,7 +381,7 @@ def _evict_plain(st):
         got = tiles[(src // page).unsqueeze(1), head.unsqueeze(1), (src % page // 32).unsqueeze(1), first + order[src % 32]]
         tiles[(dst // page).unsqueeze(1), head.unsqueeze(1), (dst % page // 32).unsqueeze(1), first + order[dst % 32]] = got
     halves = st["pages"].view(torch.float16).view(-1, hk, page // 32, 18 * d)
-    for first in (8 * d, 17 * d):
+    for first, sc in ((8 * d, ks), (17 * d, vs)):
         got = halves[(src // page).unsqueeze(1), head.unsqueeze(1), (src % page // 32).unsqueeze(1), first + sc[src % 32]]
         halves[(dst // page).unsqueeze(1), head.unsqueeze(1), (dst % page // 32).unsqueeze(1), first + sc[dst % 32]] = got
     k, v = _slots(st["pages"], st["dst_slots"], page, hk, d)
@@ -472,15 +473,16 @@ def _exact_values(tiles, d):
         val = torch.empty((tiles.shape[0], 32, d), dtype=torch.float64, device=tiles.device)
         for t in range(32):
             for b in range(nb):
-                s = scales[:, ((t // 2) * nb + b) * 2 + t % 2, None]
+                half = ((t // 16 * 8 + t % 8) * nb + b) * 2 + t // 8 % 2 if kind == 0 else ((t // 4) * nb + b) * 4 + t % 4
+                s = scales[:, half, None]
                 offs = []
                 for j in range(16):
                     if kind == 0:
                         u = (t // 8) * nb + b
                         offs.append(((u // 4) * 32 + (t % 8) * 4 + j // 4) * 16 + (u % 4) * 4 + j % 4)
                     else:
-                        u = ((t // 16) * nb + b) * 2 + (t % 16) // 8
-                        offs.append(((u // 4) * 32 + (j % 8) * 4 + (t % 8) // 2) * 16 + (u % 4) * 4 + (t % 2) * 2 + j // 8)
+                        u = ((t // 16) * nb + b) * 2 + t % 4 // 2
+                        offs.append(((u // 4) * 32 + (j % 8) * 4 + t % 16 // 4) * 16 + (u % 4) * 4 + (t % 2) * 2 + j // 8)
                 raw = tiles[:, torch.tensor(offs, device=tiles.device) + base].to(torch.int32)
                 val[:, t, b * 32:b * 32 + 16] = (raw % 16 - 8) * s
                 val[:, t, b * 32 + 16:b * 32 + 32] = (raw // 16 - 8) * s
