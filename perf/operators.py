@@ -414,7 +414,7 @@ def _run_own(st):
     if kind == "attend":
         return cache.attend(st["table"], st["lens_t"], st["q"])
     if kind == "weights":
-        return cache.weights(st["table"], st["lens_t"], st["q"], st["lse"], prev=st["sum"])
+        return cache.weights(st["table"], st["lens_t"], st["q"], st["lse"].contiguous(), prev=st["sum"])
     kept, lens, w = cache.evict(st["table"], st["dst"], st["lens_t"], st["weights"], c["keep"], sinks=c["sinks"],
                                 recent=c["recent"])
     k, v = cache.read(st["dst_slots"], torch.float16)
