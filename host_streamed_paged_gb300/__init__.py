@@ -5,4 +5,4 @@ The product is the C-ABI CUDA library built from ``csrc/`` (declared in
 """
 from . import build  # noqa: F401
 from .kvs import *  # noqa: F401,F403
-from .kvs import KVStream, KVSError, load  # noqa: F401
+from .kvs import KVStream, KVSError, Q4Cache, load, prompt_attend, prompt_weights  # noqa: F401

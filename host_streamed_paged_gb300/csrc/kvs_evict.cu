@@ -1,0 +1,344 @@
+// Eviction from the 4-bit page cache by accumulated attention weight
+// (include/kvs.h, kvs_q4_evict): per (sequence, kv head) a selection of the
+// tokens that stay, then a gather of their encoded rows into other pages.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "kvs.h"
+#include "kvs_internal.h"
+
+namespace kvs {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kMaxSeq = 4096;
+constexpr int kBins = 256;
+
+struct EvictParams {
+    uint8_t *pages;
+    int64_t n_pages, page_bytes, head_bytes;
+    int P, lgP, Hk;
+    const int32_t *table, *dst_table, *lens;
+    int table_width, dst_width, n_seq;
+    const float *weights;
+    int64_t width;
+    int keep, sinks, recent;
+    int32_t *kept;
+    float *kept_weights;
+    int32_t *new_lens;
+    int cached;  // keys of a CTA's share that fit its shared memory
+};
+
+__device__ __forceinline__ int seq_len(const EvictParams &p, int s) {
+    int64_t cap = (int64_t)p.table_width << p.lgP;
+    if (p.width < cap) cap = p.width;
+    const int n = p.lens[s];
+    return n < 0 ? 0 : (int)(n < cap ? n : cap);
+}
+
+// fp32 order as unsigned order; -0 equals 0, NaN is below every number
+__device__ __forceinline__ uint32_t key_of(float x) {
+    if (isnan(x)) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+// One cluster per (sequence, kv head); each CTA has a contiguous share of the
+// candidates (tokens between the sinks and the recent ones).  The smallest key
+// that stays is found digit by digit, 8 bits at a time from the top: a
+// histogram of the candidates that match the digits so far, summed over the
+// cluster, gives the next digit.  Then every CTA writes its tokens in order:
+// keys above the threshold, and of those equal to it the first ones.
+__global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[2][kBins];  // a digit's counts; the other is being cleared
+    __shared__ uint32_t total[kBins];
+    __shared__ uint32_t warp_count[2][kThreads / 32];
+    __shared__ uint32_t mine[2];  // this CTA's tokens above the threshold, and equal to it
+    __shared__ uint32_t digit[2];
+    cg::cluster_group cl = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
+    const int id = blockIdx.x / ranks, s = id / p.Hk, h = id % p.Hk;
+    const int T = seq_len(p, s);
+    int32_t *kept = p.kept + (int64_t)id * p.keep;
+    float *kw = p.kept_weights ? p.kept_weights + (int64_t)id * p.keep : nullptr;
+    const float *w = p.weights + (int64_t)id * p.width;
+    if (h == 0 && rank == 0 && tid == 0) p.new_lens[s] = T < p.keep ? T : p.keep;
+    if (T <= p.keep) {  // all stay (the same decision in every CTA of the cluster)
+        for (int i = rank * kThreads + tid; i < p.keep; i += ranks * kThreads) {
+            kept[i] = i < T ? i : -1;
+            if (kw) kw[i] = i < T ? w[i] : 0.f;
+        }
+        return;
+    }
+    const int n = T - p.sinks - p.recent;       // candidates
+    const int want = p.keep - p.sinks - p.recent;  // of which these stay
+    const int share = (n + ranks - 1) / ranks;
+    const int c0 = min(rank * share, n), c1 = min(c0 + share, n), cn = c1 - c0;
+    const float *wc = w + p.sinks + c0;
+    auto key_at = [&](int i) { return i < p.cached ? keys[i] : key_of(wc[i]); };
+    for (int i = tid; i < kBins; i += kThreads) hist[0][i] = hist[1][i] = 0;
+    __syncthreads();
+    uint32_t prefix = 0;
+    uint32_t left = (uint32_t)want;  // still to be found among the keys that match the prefix
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        uint32_t *hs = hist[pass & 1];
+        for (int i = tid; i < cn; i += kThreads) {
+            uint32_t k;
+            if (pass == 0) {
+                k = key_of(wc[i]);
+                if (i < p.cached) keys[i] = k;
+            } else {
+                k = key_at(i);
+            }
+            if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hs[k >> shift & 255], 1u);
+        }
+        cl.sync();
+        if (tid < kBins) {
+            uint32_t sum = 0;
+            for (int r = 0; r < ranks; ++r) sum += *cl.map_shared_rank(&hs[tid], r);
+            total[tid] = sum;
+            hist[(pass + 1) & 1][tid] = 0;
+        }
+        __syncthreads();
+        if (warp == 0) {  // from the top: the digit at which the count reaches `left`
+            uint32_t v[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[i] = total[255 - (lane * 8 + i)];
+            uint32_t inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            uint32_t before = inc - sum;
+            if (before < left && inc >= left) {
+                int i = 0;
+                for (; i < 7 && before + v[i] < left; ++i) before += v[i];
+                digit[0] = 255 - (lane * 8 + i);
+                digit[1] = before;
+            }
+        }
+        __syncthreads();
+        if (want > 0) {
+            prefix = prefix << 8 | digit[0];
+            left -= digit[1];
+        }
+    }
+    // prefix is the threshold key; `left` tokens equal to it stay
+    if (want == 0) prefix = 0xffffffffu, left = 0;
+    uint32_t above = 0, equal = 0;
+    for (int i = tid; i < cn; i += kThreads) {
+        const uint32_t k = key_at(i);
+        above += k > prefix;
+        equal += k == prefix;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) warp_count[0][warp] = above, warp_count[1][warp] = equal;
+    __syncthreads();
+    if (tid < 2) {
+        uint32_t sum = 0;
+        for (int i = 0; i < kThreads / 32; ++i) sum += warp_count[tid][i];
+        mine[tid] = sum;
+    }
+    cl.sync();
+    uint32_t out = (uint32_t)p.sinks, eq_before = 0;  // places taken and equals seen before this CTA's share
+    for (int r = 0; r < rank; ++r) {
+        const uint32_t *m = cl.map_shared_rank(mine, r);
+        out += m[0];
+        eq_before += m[1];
+    }
+    out += min(eq_before, left);
+    for (int i0 = 0; i0 < cn; i0 += kThreads) {
+        const int i = i0 + tid;
+        const uint32_t k = i < cn ? key_at(i) : 0u;
+        const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
+        const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+        __syncthreads();
+        if (lane == 0) warp_count[0][warp] = __popc(ba), warp_count[1][warp] = __popc(be);
+        __syncthreads();
+        uint32_t na = 0, ne = 0, ta = 0, te = 0;
+        for (int x = 0; x < kThreads / 32; ++x) {
+            if (x < warp) na += warp_count[0][x], ne += warp_count[1][x];
+            ta += warp_count[0][x];
+            te += warp_count[1][x];
+        }
+        const uint32_t below = (1u << lane) - 1;
+        na += __popc(ba & below);
+        ne += eq_before + __popc(be & below);
+        if (a || (e && ne < left)) {
+            const uint32_t at = out + na + min(ne, left) - min(eq_before, left);
+            const int tok = p.sinks + c0 + i;
+            kept[at] = tok;
+            if (kw) kw[at] = w[tok];
+        }
+        out += ta + min(eq_before + te, left) - min(eq_before, left);
+        eq_before += te;
+    }
+    // the ones that always stay
+    for (int i = rank * kThreads + tid; i < p.sinks + p.recent; i += ranks * kThreads) {
+        const int tok = i < p.sinks ? i : T - p.recent + (i - p.sinks);
+        const int at = i < p.sinks ? i : p.keep - p.recent + (i - p.sinks);
+        kept[at] = tok;
+        if (kw) kw[at] = w[tok];
+    }
+    cl.sync();  // no CTA leaves while another may read its shared memory
+}
+
+// Gather: a warp builds one destination tile (32 tokens of one head) in shared
+// memory, lane = token, and stores it in whole lines.
+template <int D>
+__global__ void __launch_bounds__(128) gather_kernel(const EvictParams p) {
+    constexpr int NB = D / 32, BYTES = 36 * D;
+    __shared__ __align__(16) uint8_t stage[4][BYTES];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tiles = (p.keep + 31) / 32;
+    const int64_t id = (int64_t)blockIdx.x * 4 + warp;
+    const int k = (int)(id % tiles);
+    const int64_t sh = id / tiles;
+    if (sh >= (int64_t)p.n_seq * p.Hk) return;
+    const int s = (int)(sh / p.Hk), h = (int)(sh % p.Hk);
+    const int T = seq_len(p, s), count = T < p.keep ? T : p.keep;
+    if (k * 32 >= count) return;
+    const int dpage = p.dst_table[(int64_t)s * p.dst_width + (k * 32 >> p.lgP)];
+    if (dpage < 0 || dpage >= p.n_pages) return;
+    uint8_t *dst = p.pages + dpage * p.page_bytes + h * p.head_bytes + (int64_t)((k * 32 & (p.P - 1)) >> 5) * BYTES;
+    const int i = k * 32 + lane;
+    const uint8_t *src = nullptr;
+    int st = 0;
+    if (i < count) {
+        const int tok = p.kept[sh * p.keep + i];
+        const int page = p.table[(int64_t)s * p.table_width + (tok >> p.lgP)];
+        if (page >= 0 && page < p.n_pages)
+            src = p.pages + page * p.page_bytes + h * p.head_bytes + (int64_t)((tok & (p.P - 1)) >> 5) * BYTES;
+        st = tok & 31;
+    }
+    uint8_t *out = stage[warp];
+    const int t = lane;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        uint32_t kw[4];
+        uint16_t vw[8], ks = 0, vs = 0;
+        const int su = (st >> 3) * NB + b, sw = ((st >> 4) * NB + b) * 2 + ((st & 3) >> 1);
+        const int k_src = ((su >> 2) * 32 + (st & 7) * 4) * 16 + (su & 3) * 4;
+        const int v_src = 18 * D + ((sw >> 2) * 32 + ((st & 15) >> 2)) * 16 + (sw & 3) * 4 + (st & 1) * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) kw[q] = src ? *reinterpret_cast<const uint32_t *>(src + k_src + q * 16) : 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vw[j] = src ? *reinterpret_cast<const uint16_t *>(src + v_src + j * 64) : (uint16_t)0;
+        if (src) {
+            ks = reinterpret_cast<const uint16_t *>(src + 16 * D)[((st >> 4) * 8 + (st & 7)) * NB * 2 + b * 2 + (st >> 3 & 1)];
+            vs = reinterpret_cast<const uint16_t *>(src + 34 * D)[((st >> 2) * NB + b) * 4 + (st & 3)];
+        }
+        const int u = (t >> 3) * NB + b, w = ((t >> 4) * NB + b) * 2 + ((t & 3) >> 1);
+        const int k_dst = ((u >> 2) * 32 + (t & 7) * 4) * 16 + (u & 3) * 4;
+        const int v_dst = 18 * D + ((w >> 2) * 32 + ((t & 15) >> 2)) * 16 + (w & 3) * 4 + (t & 1) * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(out + k_dst + q * 16) = kw[q];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint16_t *>(out + v_dst + j * 64) = vw[j];
+        reinterpret_cast<uint16_t *>(out + 16 * D)[((t >> 4) * 8 + (t & 7)) * NB * 2 + b * 2 + (t >> 3 & 1)] = ks;
+        reinterpret_cast<uint16_t *>(out + 34 * D)[((t >> 2) * NB + b) * 4 + (t & 3)] = vs;
+    }
+    __syncwarp();
+    for (int x = lane; x < BYTES / 16; x += 32) reinterpret_cast<uint4 *>(dst)[x] = reinterpret_cast<const uint4 *>(out)[x];
+}
+
+kvs_status bad(kvs_status s, const char *why) {
+    set_thread_error(why);
+    return s;
+}
+kvs_status cuda_failed(const char *what, cudaError_t e) {
+    set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return KVS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width,
+                                   const int32_t *dst_table, uint32_t dst_width, const int32_t *lens, uint32_t n_seq,
+                                   const float *weights, uint64_t width, uint32_t keep, uint32_t sinks, uint32_t recent,
+                                   int32_t *kept, float *kept_weights, int32_t *new_lens, void *stream) {
+    if (!pool) return bad(KVS_ERR_INVALID, "null pool");
+    const uint32_t P = pool->page_tokens, D = pool->head_dim;
+    if (!(P == 32 || P == 64 || P == 128 || P == 256) || !(D == 64 || D == 128 || D == 256))
+        return bad(KVS_ERR_UNSUPPORTED, "page_tokens must be 32..256 (power of two), head_dim 64, 128 or 256");
+    if (pool->n_kv_head == 0 || pool->n_kv_head > 65535) return bad(KVS_ERR_INVALID, "n_kv_head must be 1 .. 65535");
+    if (!pool->pages || (reinterpret_cast<uintptr_t>(pool->pages) & 15)) return bad(KVS_ERR_INVALID, "pages null or not 16-byte aligned");
+    if (pool->n_pages == 0 || pool->n_pages > 0x7fffffffull) return bad(KVS_ERR_INVALID, "n_pages must be 1 .. 2^31 - 1");
+    if (n_seq > (uint32_t)kMaxSeq) return bad(KVS_ERR_UNSUPPORTED, "n_seq must be at most 4096");
+    if (!table || !dst_table || !lens || !weights || !kept || !new_lens) return bad(KVS_ERR_INVALID, "null table, dst_table, lens, weights, kept or new_lens");
+    if (table_width < 1 || (uint64_t)table_width * P > 0x7fffffc0ull) return bad(KVS_ERR_INVALID, "table_width * page_tokens must be 1 .. 2^31 - 64");
+    if (width < 1 || width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be 1 .. 2^31 - 1");
+    if (keep < 1 || (uint64_t)sinks + recent > keep) return bad(KVS_ERR_INVALID, "need keep >= 1 and sinks + recent <= keep");
+    if (keep > 0x7fffffc0u || (uint64_t)dst_width * P < keep) return bad(KVS_ERR_CAPACITY, "dst_width * page_tokens must reach keep");
+    if (kept_weights == weights) return bad(KVS_ERR_INVALID, "kept_weights must not be weights");
+    if (new_lens == lens) return bad(KVS_ERR_INVALID, "new_lens must not be lens");
+    if (n_seq == 0) return KVS_OK;
+    EvictParams p = {};
+    p.pages = static_cast<uint8_t *>(pool->pages);
+    p.n_pages = (int64_t)pool->n_pages;
+    p.P = (int)P;
+    p.lgP = P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : 8;
+    p.Hk = (int)pool->n_kv_head;
+    p.head_bytes = (int64_t)P * D * 9 / 8;
+    p.page_bytes = p.head_bytes * p.Hk;
+    p.table = table;
+    p.dst_table = dst_table;
+    p.lens = lens;
+    p.table_width = (int)table_width;
+    p.dst_width = (int)(dst_width > 0x7fffffffu ? 0x7fffffffu : dst_width);
+    p.n_seq = (int)n_seq;
+    p.weights = weights;
+    p.width = (int64_t)width;
+    p.keep = (int)keep;
+    p.sinks = (int)sinks;
+    p.recent = (int)recent;
+    p.kept = kept;
+    p.kept_weights = kept_weights;
+    p.new_lens = new_lens;
+    const uint64_t sh = (uint64_t)n_seq * pool->n_kv_head;
+    // a cluster that gives each CTA about 8192 keys, up to the 8 CTAs every launch may have
+    uint64_t most = (uint64_t)table_width * P;
+    if (width < most) most = width;
+    int ranks = 1;
+    while (ranks < 8 && (uint64_t)ranks * 8192 < most) ranks *= 2;
+    if (sh * ranks > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head too large");
+    uint64_t share = (most + ranks - 1) / ranks;
+    p.cached = (int)(share < 49152 ? share : 49152);  // 192 KB of keys at most; the rest are read again
+    const int smem = (p.cached * 4 + 15) / 16 * 16;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(select_kernel), smem);
+    if (e != cudaSuccess) return cuda_failed("evict launch", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sh * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    if (e != cudaSuccess) return cuda_failed("evict launch", e);
+    const uint64_t tiles = sh * ((keep + 31) / 32);
+    if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
+    void (*g)(EvictParams) = D == 64 ? gather_kernel<64> : D == 128 ? gather_kernel<128> : gather_kernel<256>;
+    g<<<(unsigned)((tiles + 3) / 4), 128, 0, st>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? KVS_OK : cuda_failed("evict launch", e);
+}

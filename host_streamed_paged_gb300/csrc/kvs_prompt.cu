@@ -1,0 +1,919 @@
+// Attention over packed prompts, and the attention weight that their keys
+// receive, on the 5th-generation tensor cores (include/kvs.h, kvs_prompt_*).
+//
+// Rows.  A kv head's query rows are its tokens' G query heads, token by token:
+// a 128-row MMA tile holds floor(128 / G) tokens of all G heads, read by one
+// TMA box.  So K and V are read once per kv head, short prompts fill tiles,
+// and the causal edge of a tile spans 128 / G keys instead of 128.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+#include <string>
+
+#include "kvs.h"
+#include "kvs_internal.h"
+
+namespace kvs {
+namespace {
+
+constexpr int kThreads = 384;  // warps 0-3, 4-7: one softmax warpgroup per tile; warp 8: MMA issue; warp 9: TMA
+constexpr int kMaxSeq = 4096;
+constexpr int kMaxGroup = 64;
+constexpr int kTileRows = 128;
+constexpr uint32_t kSpinLimit = 1u << 22;
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+// bounded wait for phase `parity`; false on timeout or once *abort is raised (a timeout raises it)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 255) == 255 && *abort) return false;
+    }
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// 128-byte-swizzled tiles of 128-byte rows.  K-major (rows = M or N, the row's 64 elements = k): 8-row groups 1024
+// bytes apart.  N-major (rows = k, the row's 64 elements = n): 8-row groups of k 1024 bytes apart, the next 64
+// elements of n `lead` bytes on.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+    d |= (uint64_t)(lead >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// kind::f16 instruction descriptor: D f32, A K-major, B K-major or N-major
+__device__ constexpr uint32_t idesc(bool bf16, int M, int N, bool b_n_major) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 lanes x 32 columns, one row per thread
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&r))
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)),
+          "l"(*reinterpret_cast<const uint64_t *>(&c)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&r))
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- which prompt, which tile
+
+struct PromptParams {
+    const int32_t *cu;
+    int n_seq, total, Hk, G;
+    float scale_log2;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    // weights
+    const float *lse_in;
+    const float *prev;
+    float *w;
+    int64_t width;
+    int last_rows;
+};
+
+__device__ __forceinline__ int cu_begin(const PromptParams &p, int s) {
+    const int a = p.cu[s];
+    return a < 0 ? 0 : (a < p.total ? a : p.total);
+}
+__device__ __forceinline__ int cu_end(const PromptParams &p, int s) {
+    const int a = cu_begin(p, s), b = p.cu[s + 1];
+    return b < a ? a : (b < p.total ? b : p.total);
+}
+
+// The unit-th group of `per` tokens over all prompts: prompt s, group x of it
+// (place = {s, x, begin, end}; s < 0 past the last).  Every thread calls it;
+// `place` and `sums` are in shared memory.
+__device__ void find_unit(const PromptParams &p, int64_t unit, int per, int *place, int64_t *sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int each = (p.n_seq + nt - 1) / nt;
+    int64_t mine = 0;
+    for (int k = 0; k < each; ++k) {
+        const int s = tid * each + k;
+        if (s < p.n_seq) mine += (cu_end(p, s) - cu_begin(p, s) + per - 1) / per;
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sums[warp] = inc;
+    if (tid == 0) place[0] = -1;
+    __syncthreads();
+    int64_t base = inc - mine;
+    for (int w = 0; w < warp; ++w) base += sums[w];
+    if (unit >= base && unit < base + mine) {
+        for (int k = 0; k < each; ++k) {
+            const int s = tid * each + k;
+            if (s >= p.n_seq) break;
+            const int a = cu_begin(p, s), b = cu_end(p, s), n = (b - a + per - 1) / per;
+            if (unit < base + n) {
+                place[0] = s;
+                place[1] = (int)(unit - base);
+                place[2] = a;
+                place[3] = b;
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- attention
+// Per CTA and kv head: two 128-row query tiles (D <= 128) or one (D = 256: its
+// O takes the tensor memory of two) against the prompt's key blocks.
+//   warp 9 loads Q, then K_j, V_j through a ring of block-sized stages (TMA);
+//   warp 8 issues S = Q K^T into tensor memory and O += P V, P as the
+//     tensor-memory A operand over S's columns; the two tiles (or the two score
+//     buffers of one) alternate, so one's softmax runs under the other's MMAs;
+//   each softmax warpgroup (one thread per row) turns its tile's S into P and
+//     rescales O only when a row's maximum grew by more than 2^8.
+template <int D>
+struct AttendShape {
+    static constexpr int NQ = D <= 128 ? 2 : 1;
+    static constexpr int BN = D <= 128 ? 128 : 64;
+    static constexpr int kQBytes = kTileRows * D * 2;
+    static constexpr int kBlock = BN * D * 2;
+    static constexpr int kStages = D == 64 ? 6 : 5;
+    static constexpr int kOffRing = NQ * kQBytes;
+    static constexpr int kOffBar = kOffRing + kStages * kBlock;
+    static constexpr int kSmem = kOffBar + 256 + 128 + 1024;
+    static constexpr uint32_t kColO = 256;
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attend_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
+                         const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using S = AttendShape<D>;
+    constexpr int NQ = S::NQ, BN = S::BN, NST = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bars = smem_u32(smem + S::kOffBar);
+    // barriers: ring full / empty, Q full, S full (2), P full (2), O done (2 x parity), final
+    auto b_full = [&](int s) { return bars + 8u * s; };
+    auto b_empty = [&](int s) { return bars + 8u * (6 + s); };
+    const uint32_t b_q = bars + 8u * 12, b_final = bars + 8u * 13;
+    auto b_s = [&](int i) { return bars + 8u * (14 + i); };
+    auto b_p = [&](int i) { return bars + 8u * (16 + i); };
+    auto b_o = [&](int i, int par) { return bars + 8u * (18 + 2 * i + par); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
+    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + S::kOffBar + 256);
+
+    const int G = p.G, TQ = kTileRows / G;
+    const int head = blockIdx.x % p.Hk;
+    const int64_t n_units = gridDim.x / p.Hk;
+    find_unit(p, n_units - 1 - blockIdx.x / p.Hk, NQ * TQ, place, sums);
+    if (place[0] < 0) return;
+    const int begin = place[2], L = place[3] - begin;
+    const int t0 = place[1] * NQ * TQ;  // first token of tile 0, within the prompt
+    int nblk[2] = {0, 0}, n_max = 0;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int a = t0 + i * TQ, last = (a + TQ < L ? a + TQ : L) - 1;
+        nblk[i] = a < L ? last / BN + 1 : 0;
+        n_max = nblk[i] > n_max ? nblk[i] : n_max;
+    }
+
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(b_full(s), 1);
+            mbar_init(b_empty(s), 1);
+        }
+        mbar_init(b_q, 1);
+        mbar_init(b_final, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_s(i), 1);
+            mbar_init(b_p(i), 4);
+            mbar_init(b_o(i, 0), 1);
+            mbar_init(b_o(i, 1), 1);
+        }
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    // ring order: K_0, then (D <= 128) V_0, K_1, V_1, ... or (D = 256, scores one block ahead) K_1, V_0, K_2, V_1, ...
+    auto ring_k = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+    auto ring_v = [&](int j) { return NQ == 2 ? 2 * j + 1 : (j == n_max - 1 ? 2 * j + 1 : 2 * j + 2); };
+
+    if (warp == 9) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            constexpr int kChunks = D / 64;
+            mbar_expect(b_q, (uint32_t)(NQ * kChunks * 128 * G * TQ));
+            for (int i = 0; i < NQ; ++i)
+                for (int c = 0; c < kChunks; ++c)
+                    tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
+            const int n = 2 * n_max;
+            int issued = 0;
+            for (int r = 0; r < n; ++r) {
+                const int st = r % NST, use = r / NST;
+                if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort)) break;
+                // the r-th block of the ring
+                bool is_v;
+                int j;
+                if (NQ == 2) {
+                    is_v = r & 1;
+                    j = r >> 1;
+                } else {
+                    is_v = r == n - 1 || (r >= 2 && !(r & 1));
+                    j = r == 0 ? 0 : (r == n - 1 ? n_max - 1 : (r & 1 ? (r + 1) / 2 : r / 2 - 1));
+                }
+                mbar_expect(b_full(st), (uint32_t)S::kBlock);
+                for (int c = 0; c < kChunks; ++c)
+                    tma_load(smem_u32(smem + S::kOffRing + st * S::kBlock + c * BN * 128), is_v ? &mv : &mk, b_full(st), c * 64,
+                             head, begin + j * BN);
+                issued = r + 1;
+            }
+            if (*abort) {  // copies in flight still land in this CTA's shared memory
+                volatile int none = 0;
+                mbar_wait(b_q, 0, &none);
+                for (int st = 0; st < NST; ++st)
+                    if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            const uint32_t id_s = idesc(BF16, kTileRows, BN, false), id_o = idesc(BF16, kTileRows, D, true);
+            const uint32_t sq = smem_u32(smem), sr = smem_u32(smem + S::kOffRing);
+            bool ok = mbar_wait(b_q, 0, abort);
+            auto wait_ring = [&](int r) { return mbar_wait(b_full(r % NST), (uint32_t)((r / NST) & 1), abort); };
+            auto issue_s = [&](int i, int buf, int r) {
+                const uint64_t da = smem_desc(sq + (uint32_t)(i * S::kQBytes), 16), db = smem_desc(sr + (uint32_t)(r % NST * S::kBlock), 16);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint64_t oa = (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4);
+                    const uint64_t ob = (uint64_t)(((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4);
+                    mma_ss(tmem + (uint32_t)(buf * BN), da + oa, db + ob, id_s, s > 0);
+                }
+                mma_commit(b_s(buf));
+            };
+            auto issue_o = [&](int i, int buf, int r, int j) {
+                const uint64_t db = smem_desc(sr + (uint32_t)(r % NST * S::kBlock), BN * 128);
+#pragma unroll
+                for (int s = 0; s < BN / 16; ++s)
+                    mma_ts(tmem + S::kColO + (uint32_t)(i * D), tmem + (uint32_t)(buf * BN + 8 * s), db + (uint64_t)(s * 2048 >> 4),
+                           id_o, (j > 0 || s > 0) ? 1u : 0u);
+                mma_commit(b_o(i, j & 1));
+            };
+            if (NQ == 2) {
+                for (int j = 0; j <= n_max && ok; ++j) {
+                    if (j >= 1) ok = wait_ring(ring_v(j - 1));
+                    if (ok && j < n_max) ok = wait_ring(ring_k(j));
+                    if (!ok) break;
+                    tc_after();
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) {
+                        if (j >= 1 && j - 1 < nblk[i]) {
+                            ok = ok && mbar_wait(b_p(i), (uint32_t)((j - 1) & 1), abort);
+                            if (!ok) break;
+                            tc_after();
+                            issue_o(i, i, ring_v(j - 1), j - 1);
+                        }
+                        if (j < nblk[i]) issue_s(i, i, ring_k(j));
+                    }
+                    if (!ok) break;
+                    if (j >= 1) mma_commit(b_empty(ring_v(j - 1) % NST));
+                    if (j < n_max) mma_commit(b_empty(ring_k(j) % NST));
+                }
+            } else {
+                for (int j = 0; j <= n_max && ok; ++j) {
+                    if (j < n_max) {
+                        ok = wait_ring(ring_k(j));
+                        if (!ok) break;
+                        tc_after();
+                        issue_s(0, j & 1, ring_k(j));
+                        mma_commit(b_empty(ring_k(j) % NST));
+                    }
+                    if (j >= 1) {
+                        ok = wait_ring(ring_v(j - 1)) && mbar_wait(b_p((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
+                        if (!ok) break;
+                        tc_after();
+                        issue_o(0, (j - 1) & 1, ring_v(j - 1), j - 1);
+                        mma_commit(b_empty(ring_v(j - 1) % NST));
+                    }
+                }
+            }
+            mma_commit(b_final);  // on every path: tensor memory is freed only after it
+        }
+    } else if (warp < 4 * NQ) {
+        // ------------------------------------------------------------ softmax, one thread per row
+        const int i = warp >> 2, row = tid & 127, n = nblk[i];
+        const int tok = t0 + i * TQ + row / G;  // within the prompt
+        const bool valid = row < TQ * G && tok < L;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sc = p.scale_log2;
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        const int first_tok = t0 + i * TQ;
+        for (int j = 0; j < n; ++j) {
+            const int buf = NQ == 2 ? i : (j & 1);
+            const uint32_t par = NQ == 2 ? (uint32_t)(j & 1) : (uint32_t)((j >> 1) & 1);
+            ok = mbar_wait_warp(b_s(buf), par, abort);
+            if (!ok) break;
+            tc_after();
+            const uint32_t ts = lanes + (uint32_t)(buf * BN);
+            uint32_t sr[BN];
+#pragma unroll
+            for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, sr + c);
+            tmem_wait_ld();
+            float *s = reinterpret_cast<float *>(sr);
+            if ((j + 1) * BN > first_tok + 1) {  // some row of the tile ends inside the block
+                const int lim = tok - j * BN;
+#pragma unroll
+                for (int c = 0; c < BN; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+            bool grow = false;
+            float alpha = 1.f;
+            if (mx > m + 8.f || (m == -INFINITY && mx != -INFINITY)) {
+                alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+                l2.x *= alpha;
+                l2.y *= alpha;
+                m = mx;
+                grow = true;
+            }
+            const float neg = m == -INFINITY ? 0.f : -m;
+            const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+            uint32_t pk[BN / 2];
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int half = 0; half < BN / 64; ++half) {
+#pragma unroll
+                for (int c = half * 64; c < half * 64 + 64; c += 2) {
+                    const float2 y = fma2(make_float2(s[c], s[c + 1]), sc2, neg2);
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
+                    pk[c / 2] = pack<BF16>(e.x, e.y);
+                }
+                tmem_st32(ts + 32 * half, pk + 32 * half);
+            }
+            l2 = add2(l2, add2(sum[0], sum[1]));
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
+                if (!ok) {
+                    tmem_wait_st();
+                    break;
+                }
+                tc_after();
+                const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(to + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                    tmem_st32(to + c, v);
+                }
+            }
+            if ((j + 1) * BN > L) {
+                // the block reaches past the prompt: its last rows are another prompt's (or nobody's), and a weight
+                // of zero times what stands there must be zero
+                const int r = ring_v(j), st = r % NST;
+                ok = mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
+                if (!ok) {
+                    tmem_wait_st();
+                    break;
+                }
+                if (row < BN && j * BN + row >= L) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4 *>(smem + S::kOffRing + st * S::kBlock + c * BN * 128 + row * 128 + k * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                proxy_fence();
+            }
+            tmem_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_p(buf));
+        }
+        if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), abort);
+        if (n > 0) {
+            tc_after();
+            const float l = l2.x + l2.y;
+            const float inv = ok ? 1.f / l : __int_as_float(0x7fc00000);
+            const int64_t trow = begin + tok;
+            const int hq = head * G + row % G;
+            const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D));
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(to + c, v);
+                tmem_wait_ld();
+                if (valid) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            o[x] = pack<BF16>(__uint_as_float(v[k + 2 * x]) * inv, __uint_as_float(v[k + 2 * x + 1]) * inv);
+                        dst[(c + k) / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            if (valid && p.lse) p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l)) * 0.693147180559945309f : inv;
+        }
+    }
+    // tensor memory is freed once every MMA is done and every row was read
+    if (tid == 0) {
+        volatile int none = 0;
+        mbar_wait(b_final, 0, &none);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------- weights
+// w_j = sum over rows of exp(s_ij - lse_i).  Keys are the M rows here, so a
+// thread owns one key: S^T = K Q^T, two 128-key tiles per CTA against a stream
+// of query tiles, each read from tensor memory once, exponentiated against
+// the rows' lse and added up in one register; nothing is joined between CTAs.
+template <int D>
+struct WeightShape {
+    static constexpr int BQ = D <= 128 ? 128 : 64;  // query rows per tile
+    static constexpr int kKBytes = kTileRows * D * 2;
+    static constexpr int kBlock = BQ * D * 2;
+    static constexpr int kStages = D == 64 ? 4 : (D == 128 ? 4 : 3);
+    static constexpr int kOffRing = 2 * kKBytes;
+    static constexpr int kOffLse = kOffRing + kStages * kBlock;
+    static constexpr int kOffBar = kOffLse + 2 * 2 * BQ * 4;
+    static constexpr int kSmem = kOffBar + 256 + 128 + 1024;
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_weights_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
+                          const __grid_constant__ CUtensorMap mk) {
+    using S = WeightShape<D>;
+    constexpr int BQ = S::BQ, NST = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bars = smem_u32(smem + S::kOffBar);
+    auto b_full = [&](int s) { return bars + 8u * s; };
+    auto b_empty = [&](int s) { return bars + 8u * (4 + s); };
+    const uint32_t b_k = bars + 8u * 8, b_final = bars + 8u * 9;
+    auto b_s = [&](int i, int buf) { return bars + 8u * (10 + 2 * i + buf); };     // scores in tensor memory
+    auto b_read = [&](int i, int buf) { return bars + 8u * (14 + 2 * i + buf); };  // scores read
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
+    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + S::kOffBar + 256);
+
+    const int G = p.G, TQ = BQ / G;
+    const int head = blockIdx.x % p.Hk;
+    find_unit(p, blockIdx.x / p.Hk, 2 * kTileRows, place, sums);
+    if (place[0] < 0) return;
+    const int seq = place[0], begin = place[2], L = place[3] - begin;
+    const int k0 = place[1] * 2 * kTileRows;
+    int start = p.last_rows > 0 && L > p.last_rows ? L - p.last_rows : 0;  // first query token counted
+    if (start < k0) start = k0;
+    const int ntile = (L - start + TQ - 1) / TQ;
+    const bool second = k0 + kTileRows < L;
+
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(b_full(s), 1);
+            mbar_init(b_empty(s), 1);
+        }
+        mbar_init(b_k, 1);
+        mbar_init(b_final, 1);
+        for (int i = 0; i < 2; ++i)
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(b_s(i, b), 1);
+                mbar_init(b_read(i, b), 4);
+            }
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // query-tile rows that no box writes (BQ not a multiple of G) stay zero: their scores are finite
+    for (int x = tid; x < NST * (D / 64) * (BQ - TQ * G) * 8; x += kThreads) {
+        const int c = x & 7, r = (x >> 3) % (BQ - TQ * G), a = (x >> 3) / (BQ - TQ * G);
+        *reinterpret_cast<uint4 *>(smem + S::kOffRing + a * (BQ * 128) + (TQ * G + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    proxy_fence();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            constexpr int kChunks = D / 64;
+            mbar_expect(b_k, (uint32_t)((second ? 2 : 1) * S::kKBytes));
+            for (int i = 0; i < (second ? 2 : 1); ++i)
+                for (int c = 0; c < kChunks; ++c)
+                    tma_load(smem_u32(smem + i * S::kKBytes + c * kTileRows * 128), &mk, b_k, c * 64, head, begin + k0 + i * kTileRows);
+            int issued = 0;
+            for (int r = 0; r < ntile; ++r) {
+                const int st = r % NST, use = r / NST;
+                if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort)) break;
+                mbar_expect(b_full(st), (uint32_t)(kChunks * 128 * G * TQ));
+                for (int c = 0; c < kChunks; ++c)
+                    tma_load(smem_u32(smem + S::kOffRing + st * S::kBlock + c * BQ * 128), &mq, b_full(st), c * 64, head * G,
+                             begin + start + r * TQ);
+                issued = r + 1;
+            }
+            if (*abort) {
+                volatile int none = 0;
+                mbar_wait(b_k, 0, &none);
+                for (int st = 0; st < NST; ++st)
+                    if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            const uint32_t id = idesc(BF16, kTileRows, BQ, false);
+            const uint32_t sk = smem_u32(smem), sr = smem_u32(smem + S::kOffRing);
+            bool ok = mbar_wait(b_k, 0, abort);
+            for (int r = 0; r < ntile && ok; ++r) {
+                const int st = r % NST, buf = r & 1;
+                ok = mbar_wait(b_full(st), (uint32_t)((r / NST) & 1), abort);
+                if (!ok) break;
+                for (int i = 0; i < (second ? 2 : 1); ++i) {
+                    if (r >= 2) ok = mbar_wait(b_read(i, buf), (uint32_t)(((r - 2) >> 1) & 1), abort);
+                    if (!ok) break;
+                    tc_after();
+                    const uint64_t da = smem_desc(sk + (uint32_t)(i * S::kKBytes), 16), db = smem_desc(sr + (uint32_t)(st * S::kBlock), 16);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint64_t oa = (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4);
+                        const uint64_t ob = (uint64_t)(((s >> 2) * (BQ * 128) + (s & 3) * 32) >> 4);
+                        mma_ss(tmem + (uint32_t)((2 * i + buf) * BQ), da + oa, db + ob, id, s > 0);
+                    }
+                    mma_commit(b_s(i, buf));
+                }
+                mma_commit(b_empty(st));
+            }
+            mma_commit(b_final);
+        }
+    } else if (warp < 8 && (warp < 4 || second)) {
+        const int i = warp >> 2, row = tid & 127;
+        const int key = k0 + i * kTileRows + row;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + i * 2 * BQ;  // this warpgroup's two buffers of -lse
+        const float sc = p.scale_log2;
+        auto lse_of = [&](int r) {  // -lse (log2 units) of query row `row` of tile r; rows that count for nothing: -inf
+            const int tok = start + r * TQ + row / G;
+            float z = INFINITY;
+            if (row < TQ * G && tok < L) {
+                z = p.lse_in[(int64_t)(begin + tok) * (p.Hk * G) + head * G + row % G] * 1.4426950408889634f;
+                if (z == -INFINITY) z = INFINITY;
+            }
+            return -z;
+        };
+        float next = row < BQ ? lse_of(0) : 0.f;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        bool ok = true;
+        for (int r = 0; r < ntile; ++r) {
+            const int buf = r & 1;
+            if (row < BQ) sl[buf * BQ + row] = next;
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+            if (r + 1 < ntile && row < BQ) next = lse_of(r + 1);
+            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((r >> 1) & 1), abort);
+            if (!ok) break;
+            tc_after();
+            const int tok0 = start + r * TQ;
+            // columns this key counts: rows of tokens from the key on, and none past the prompt
+            const bool edge = tok0 < k0 + (i + 1) * kTileRows - 1 || tok0 + TQ > L;
+            int c_lo = (key - tok0) * G, c_hi = (L - tok0) * G;
+            if (c_hi > TQ * G) c_hi = TQ * G;
+            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ);
+            uint32_t sr[BQ];
+#pragma unroll
+            for (int c = 0; c < BQ; c += 32) tmem_ld32(ts + c, sr + c);
+            tmem_wait_ld();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_read(i, buf));
+            const float *s = reinterpret_cast<const float *>(sr);
+            const float4 *z4 = reinterpret_cast<const float4 *>(sl + buf * BQ);
+            const float2 sc2 = make_float2(sc, sc);
+#pragma unroll
+            for (int c = 0; c < BQ; c += 4) {
+                const float4 z = z4[c / 4];
+                float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z.x, z.y));
+                float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z.z, z.w));
+                if (edge) {
+                    a.x = c >= c_lo && c < c_hi ? a.x : -INFINITY;
+                    a.y = c + 1 >= c_lo && c + 1 < c_hi ? a.y : -INFINITY;
+                    b.x = c + 2 >= c_lo && c + 2 < c_hi ? b.x : -INFINITY;
+                    b.y = c + 3 >= c_lo && c + 3 < c_hi ? b.y : -INFINITY;
+                }
+                sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
+                sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+            }
+        }
+        if (key < L && key < p.width) {
+            const int64_t at = ((int64_t)seq * p.Hk + head) * p.width + key;
+            const float2 t2 = add2(sum[0], sum[1]);
+            p.w[at] = (p.prev ? p.prev[at] : 0.f) + (ok ? t2.x + t2.y : __int_as_float(0x7fc00000));
+        }
+    }
+    if (tid == 0) {
+        volatile int none = 0;
+        mbar_wait(b_final, 0, &none);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// entries past a prompt's length: prev's (or zero)
+__global__ void __launch_bounds__(256) prompt_rest_kernel(const PromptParams p) {
+    const int s = blockIdx.y / p.Hk;
+    const int len = cu_end(p, s) - cu_begin(p, s);
+    for (int64_t i = len + (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.width; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = (int64_t)blockIdx.y * p.width + i;
+        p.w[at] = p.prev ? p.prev[at] : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+kvs_status bad(kvs_status s, const char *why) {
+    set_thread_error(why);
+    return s;
+}
+kvs_status cuda_failed(const char *what, cudaError_t e) {
+    set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return KVS_ERR_CUDA;
+}
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {  // the driver's entry point, looked up once
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+// [rows][heads][D] of 16-bit elements as boxes of 64 elements x box_heads x box_rows, 128-byte swizzle
+kvs_status make_map(CUtensorMap *m, const void *base, bool bf16, uint64_t rows, uint64_t heads, uint64_t D, uint64_t stride,
+                    uint32_t box_heads, uint32_t box_rows) {
+    EncodeFn fn = encoder();
+    if (!fn) return bad(KVS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[3] = {D, heads, rows}, strides[2] = {D * 2, stride * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_rows}, es[3] = {1, 1, 1};
+    const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base),
+                          dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return bad(KVS_ERR_CUDA, "cuTensorMapEncodeTiled refused a row layout");
+    return KVS_OK;
+}
+
+kvs_status check_prompt(const kvs_prompt *p, bool need_v, PromptParams *o) {
+    if (!p) return bad(KVS_ERR_INVALID, "null prompt");
+    if (!(p->head_dim == 64 || p->head_dim == 128 || p->head_dim == 256)) return bad(KVS_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+    if (p->dtype != KVS_F16 && p->dtype != KVS_BF16) {
+        if (p->dtype == KVS_F32) return bad(KVS_ERR_UNSUPPORTED, "prompts are KVS_F16 or KVS_BF16");
+        return bad(KVS_ERR_INVALID, "dtype must be KVS_F16 or KVS_BF16");
+    }
+    if (p->n_kv_head == 0 || p->n_q_head < p->n_kv_head || p->n_q_head % p->n_kv_head != 0 || p->n_q_head > 65535)
+        return bad(KVS_ERR_INVALID, "n_q_head must be a positive multiple of n_kv_head, at most 65535");
+    if (p->n_q_head / p->n_kv_head > (uint32_t)kMaxGroup) return bad(KVS_ERR_UNSUPPORTED, "n_q_head / n_kv_head must be at most 64");
+    if (p->n_seq > (uint32_t)kMaxSeq) return bad(KVS_ERR_UNSUPPORTED, "n_seq must be at most 4096");
+    if (p->total_rows > 0x7fffffffu - 256u) return bad(KVS_ERR_INVALID, "total_rows must be at most 2^31 - 1 - 256");
+    if (!(p->scale > 0.f) || !isfinite(p->scale)) return bad(KVS_ERR_INVALID, "scale must be positive and finite");
+    if (!p->cu) return bad(KVS_ERR_INVALID, "null cu");
+    if (p->total_rows) {
+        const uint64_t q_row = (uint64_t)p->n_q_head * p->head_dim, k_row = (uint64_t)p->n_kv_head * p->head_dim;
+        if (!p->q || !p->k || (need_v && !p->v)) return bad(KVS_ERR_INVALID, "null q, k or v");
+        if (!aligned(p->q, 16) || !aligned(p->k, 16) || (need_v && !aligned(p->v, 16)) || p->q_stride % 8 || p->k_stride % 8 ||
+            (need_v && p->v_stride % 8) || p->q_stride < q_row || p->k_stride < k_row || (need_v && p->v_stride < k_row))
+            return bad(KVS_ERR_INVALID, "rows must start on 16-byte boundaries, at least heads * head_dim apart");
+        const uint64_t most = 1ull << 38;  // bytes between rows that a tensor map holds (below 2^40)
+        if (p->q_stride > most || p->k_stride > most || (need_v && p->v_stride > most)) return bad(KVS_ERR_INVALID, "row stride too large");
+    }
+    o->cu = p->cu;
+    o->n_seq = (int)p->n_seq;
+    o->total = (int)p->total_rows;
+    o->Hk = (int)p->n_kv_head;
+    o->G = (int)(p->n_q_head / p->n_kv_head);
+    o->scale_log2 = p->scale * 1.4426950408889634f;
+    return KVS_OK;
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, int smem, cudaStream_t s, const A &...a) {
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, smem, s>>>(a...);
+    return cudaGetLastError();
+}
+
+template <int D>
+kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
+    using S = AttendShape<D>;
+    const bool bf = p->dtype == KVS_BF16;
+    const uint32_t TQ = kTileRows / pp.G;
+    CUtensorMap mq, mk, mv;
+    kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, TQ);
+    if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, S::BN);
+    if (r == KVS_OK) r = make_map(&mv, p->v, bf, p->total_rows, p->n_kv_head, D, p->v_stride, 1, S::BN);
+    if (r != KVS_OK) return r;
+    const uint64_t units = (uint64_t)p->total_rows / (S::NQ * TQ) + p->n_seq;  // at least the prompts' tile groups
+    if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
+    const cudaError_t e = launch(bf ? prompt_attend_kernel<D, true> : prompt_attend_kernel<D, false>,
+                                 dim3((unsigned)(units * p->n_kv_head)), S::kSmem, s, pp, mq, mk, mv);
+    return e == cudaSuccess ? KVS_OK : cuda_failed("prompt attention launch", e);
+}
+
+template <int D>
+kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
+    using S = WeightShape<D>;
+    const bool bf = p->dtype == KVS_BF16;
+    CUtensorMap mq, mk;
+    kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, (uint32_t)(S::BQ / pp.G));
+    if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
+    if (r != KVS_OK) return r;
+    const uint64_t units = (uint64_t)p->total_rows / (2 * kTileRows) + p->n_seq;
+    if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
+    const cudaError_t e = launch(bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>,
+                                 dim3((unsigned)(units * p->n_kv_head)), S::kSmem, s, pp, mq, mk);
+    return e == cudaSuccess ? KVS_OK : cuda_failed("prompt weights launch", e);
+}
+
+}  // namespace
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream) {
+    PromptParams pp = {};
+    const kvs_status s = check_prompt(p, true, &pp);
+    if (s != KVS_OK) return s;
+    if (p->total_rows && (!out || !aligned(out, 16) || out_stride % 8 || out_stride < (uint64_t)p->n_q_head * p->head_dim))
+        return bad(KVS_ERR_INVALID, "out rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
+    if (p->total_rows == 0 || p->n_seq == 0) return KVS_OK;
+    pp.out = out;
+    pp.out_stride = (int64_t)out_stride;
+    pp.lse = lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return p->head_dim == 64 ? attend_for<64>(p, pp, st) : p->head_dim == 128 ? attend_for<128>(p, pp, st) : attend_for<256>(p, pp, st);
+}
+
+extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,
+                                         float *weights, uint64_t width, void *stream) {
+    PromptParams pp = {};
+    kvs_status s = check_prompt(p, false, &pp);
+    if (s != KVS_OK) return s;
+    if (!lse || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
+    if ((uint64_t)p->n_seq * p->n_kv_head > 65535) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head must be at most 65535");
+    if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
+    if (p->n_seq == 0 || width == 0) return KVS_OK;
+    pp.lse_in = lse;
+    pp.prev = prev;
+    pp.w = weights;
+    pp.width = (int64_t)width;
+    pp.last_rows = last_rows > 0x7fffffffu ? 0x7fffffff : (int)last_rows;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p->total_rows) {
+        s = p->head_dim == 64 ? weights_for<64>(p, pp, st) : p->head_dim == 128 ? weights_for<128>(p, pp, st) : weights_for<256>(p, pp, st);
+        if (s != KVS_OK) return s;
+    }
+    if (prev != weights) {
+        const unsigned gx = (unsigned)((width + 8191) / 8192);
+        prompt_rest_kernel<<<dim3(gx < 64 ? gx : 64, p->n_seq * p->n_kv_head), 256, 0, st>>>(pp);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
+    }
+    return KVS_OK;
+}

@@ -1,0 +1,1299 @@
+// The 4-bit page cache of the batch operators (include/kvs.h): Q4_0 rows in,
+// values out, attention over the pages, accumulated attention weight.
+//
+// Attention over a cache is bound by the bytes of the cache: 9/16 byte per
+// element, each used by the few query rows of its sequence only.  At the card's
+// copy rate an SM gets 23 bytes per clock, 40 cached elements, so what counts
+// beside the copies is the instructions spent per element.  The layout and the
+// arithmetic keep those low:
+//  - A nibble ANDed out of a word and read as f16 is the subnormal n * 2^-24
+//    (or 16 n * 2^-24 for the high nibble of a byte), exactly.  It goes into
+//    the tensor core like that: one AND per two elements, no conversion.  The
+//    factors are powers of two, taken back from the query (high-nibble dims
+//    / 16) and once from the result.
+//  - The codes' offset 8 leaves the sum: sum q (n - 8) = sum q n - 8 sum q.
+//    For scores -8 sum q is the accumulator's initial value per block; for
+//    outputs -8 sum p is one more MMA per block, over the same rounded p.
+//    (fp32 calls subtract it from V's codes: over a long flat softmax sum p n
+//    exceeds sum p (n - 8) a hundredfold, and its fp32 rounding would show.)
+//  - K's block scales multiply the fp32 block sums; V's multiply the softmax
+//    weights before those are rounded to f16, with a running power-of-two
+//    reference that keeps weight x scale at 2^8 .. 2^14 at its largest.
+// Scores are S^T = K Q^T (16 tokens x 8 query rows per MMA), outputs O^T = V^T P^T
+// (16 dims x 8 query rows): the query rows are the narrow side of both, so 8 rows
+// fill them.  Between the two a tile's scores turn from a thread's (token, two
+// rows) to (row, four tokens) through 1 KB of shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "kvs.h"
+#include "kvs_internal.h"
+
+namespace kvs {
+namespace {
+
+constexpr int kTile = 32;          // tokens per tile (one bulk copy)
+constexpr int kWarps = 4;          // warps per CTA; each works on its own
+constexpr int kMaxSeq = 4096;      // sequences per call (their prefix sums live in shared memory)
+constexpr int kMaxGroupRows = 64;  // n_rows * group bound
+constexpr uint32_t kWaitLimit = 1u << 22;
+
+struct Pool {
+    uint8_t *pages;
+    int64_t n_pages, page_bytes, head_bytes;
+    int P, lgP, Hk;
+};
+
+// ---------------------------------------------------------------- elements
+
+__device__ __forceinline__ void put(void *p, int dtype, int64_t i, float x) {
+    if (dtype == KVS_F32) static_cast<float *>(p)[i] = x;
+    else if (dtype == KVS_F16) static_cast<__half *>(p)[i] = __float2half_rn(x);
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+}
+__device__ __forceinline__ float2 two(uint32_t w, int dtype) {
+    if (dtype == KVS_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+// N consecutive elements from a 16-byte (8-byte for N = 4 of 16 bits) aligned place
+template <int N>
+__device__ __forceinline__ void load_row(const void *p, int dtype, int64_t i, float *x) {
+    if (dtype == KVS_F32) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + j);
+            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i + j);
+            const float2 a = two(v.x, dtype), b = two(v.y, dtype);
+            x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- layout (include/kvs.h, "Q4 page layout")
+
+__device__ __forceinline__ int k_word(int t, int b, int q, int NB) {  // byte offset of K bytes 4q .. 4q+3
+    const int u = (t >> 3) * NB + b;
+    return (((u >> 2) * 32) + (t & 7) * 4 + q) * 16 + (u & 3) * 4;
+}
+__device__ __forceinline__ int v_half(int t, int b, int j, int NB) {  // byte offset of V bytes j and j + 8 (j < 8)
+    const int w = ((t >> 4) * NB + b) * 2 + ((t & 3) >> 1);
+    return (((w >> 2) * 32) + j * 4 + ((t & 15) >> 2)) * 16 + (w & 3) * 4 + (t & 1) * 2;
+}
+__device__ __forceinline__ int k_scale(int t, int b, int NB) { return (((t >> 4) * 8 + (t & 7)) * NB + b) * 2 + (t >> 3 & 1); }
+__device__ __forceinline__ int v_scale(int t, int b, int NB) { return ((t >> 2) * NB + b) * 4 + (t & 3); }
+
+// ---------------------------------------------------------------- append / read
+// One thread per (row, head, block of 32, K or V).  Bound by bytes: rows in at
+// 2 or 4 bytes per element, 9/16 byte out.
+
+// Q4_0 in IEEE fp32 steps in a fixed order, the same as kvs_append's V: m = the
+// element of largest |x| (lowest index on ties), d = m / -8, id = 1/d (0 if
+// d == 0), code = trunc(x * id + 8.5) within 0 .. 15.
+__device__ __forceinline__ float q4_block(const float *x, uint32_t *w) {
+    float best = x[0], mag = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 32; ++i) {
+        const float a = fabsf(x[i]);
+        if (a > mag) {
+            mag = a;
+            best = x[i];
+        }
+    }
+    const float d = __fdiv_rn(best, -8.0f);
+    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        int c = __float2int_rz(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
+        c = c > 15 ? 15 : (c < 0 ? 0 : c);
+        const int j = i & 15;
+        w[j >> 2] |= (uint32_t)c << ((j & 3) * 8 + (i >> 4) * 4);
+    }
+    return d;
+}
+
+struct RowsParams {
+    Pool pool;
+    const int64_t *slots;
+    int64_t n;
+    const void *k, *v;
+    void *ko, *vo;
+    int64_t k_stride, v_stride;
+    int dtype;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const RowsParams p) {
+    constexpr int NB = D / 32;
+    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const bool is_v = blockIdx.y != 0;
+    const int b = (int)(u % NB);
+    const int h = (int)(u / NB % p.pool.Hk);
+    const int64_t i = u / NB / p.pool.Hk;
+    if (i >= p.n) return;
+    const int64_t slot = p.slots[i];
+    if (slot < 0 || (slot >> p.pool.lgP) >= p.pool.n_pages) return;
+    float x[32];
+    load_row<32>(is_v ? p.v : p.k, p.dtype, i * (is_v ? p.v_stride : p.k_stride) + (int64_t)h * D + b * 32, x);
+    uint32_t w[4];
+    const float d = q4_block(x, w);
+    const int tp = (int)(slot & (p.pool.P - 1)), t = tp & 31;
+    uint8_t *tile = p.pool.pages + (slot >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes +
+                    (int64_t)(tp >> 5) * (36 * D);
+    if (!is_v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(tile + k_word(t, b, q, NB)) = w[q];
+        reinterpret_cast<__half *>(tile + 16 * D)[k_scale(t, b, NB)] = __float2half_rn(d);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t lo = w[j >> 2] >> ((j & 3) * 8) & 0xff, hi = w[(j + 8) >> 2] >> ((j & 3) * 8) & 0xff;
+            *reinterpret_cast<uint16_t *>(tile + 18 * D + v_half(t, b, j, NB)) = (uint16_t)(lo | hi << 8);
+        }
+        reinterpret_cast<__half *>(tile + 34 * D)[v_scale(t, b, NB)] = __float2half_rn(d);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
+    constexpr int NB = D / 32;
+    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const bool is_v = blockIdx.y != 0;
+    void *out = is_v ? p.vo : p.ko;
+    const int b = (int)(u % NB);
+    const int h = (int)(u / NB % p.pool.Hk);
+    const int64_t i = u / NB / p.pool.Hk;
+    if (i >= p.n || !out) return;
+    const int64_t slot = p.slots[i], at = (i * p.pool.Hk + h) * D + b * 32;
+    uint32_t w[4] = {0, 0, 0, 0};
+    float d = 0.f;
+    if (slot >= 0 && (slot >> p.pool.lgP) < p.pool.n_pages) {
+        const int tp = (int)(slot & (p.pool.P - 1)), t = tp & 31;
+        const uint8_t *tile = p.pool.pages + (slot >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes +
+                              (int64_t)(tp >> 5) * (36 * D);
+        d = __half2float(reinterpret_cast<const __half *>(tile + (is_v ? 34 : 16) * D)[is_v ? v_scale(t, b, NB) : k_scale(t, b, NB)]);
+        if (!is_v) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, q, NB));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t x = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, j, NB));
+                w[j >> 2] |= (x & 0xff) << ((j & 3) * 8);
+                w[(j + 8) >> 2] |= (x >> 8) << ((j & 3) * 8);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        float f[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int j = (e + m) & 15;
+            f[m] = (float)((int)(w[j >> 2] >> ((j & 3) * 8 + ((e + m) >> 4) * 4) & 15) - 8) * d;
+        }
+        if (d == 0.f) f[0] = f[1] = f[2] = f[3] = 0.f;
+        if (p.dtype == KVS_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(out) + at + e) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            uint2 o;
+            if (p.dtype == KVS_F16) {
+                const __half2 a = __floats2half2_rn(f[0], f[1]), c = __floats2half2_rn(f[2], f[3]);
+                o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+            } else {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), c = __floats2bfloat162_rn(f[2], f[3]);
+                o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+            }
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at + e) = o;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- attention
+// Work: the tiles of every (sequence, kv head) in one line, cut into equal
+// contiguous ranges, one per warp ("worker"), whatever the sequences' lengths.
+// A worker runs the online softmax over its tiles; where its range ends inside
+// a (sequence, head) it leaves a partial (O, reference exponent, sum), at most
+// two per worker, and the combine joins them in range order.  Query rows
+// beyond one pass's 8 or 16 go to further workers over the same ranges, next
+// to each other in the grid so that they share the tiles through L2.
+
+struct AttendParams {
+    Pool pool;
+    const int32_t *table;
+    const int32_t *lens;
+    int64_t q_stride;
+    const void *q;
+    void *out;
+    float *lse;
+    float *part_o;   // [row block][worker][2][8 NT][D]
+    float2 *part_rl; // [row block][worker][2][8 NT]
+    int table_width, n_seq, R, Hq, G;
+    int dtype, row_blocks, workers;
+    float scale_log2;
+};
+
+__device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, int table_width, int s) {
+    const int64_t cap = (int64_t)table_width << pool.lgP;
+    const int n = lens[s];
+    return n < 0 ? 0 : (int)(n < cap ? n : cap);
+}
+
+// prefix[s] = tiles of one head of sequences 0 .. s-1; every thread of the CTA calls it
+__device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_width, int n_seq, int *prefix) {
+    __shared__ int warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int per = (n_seq + nt - 1) / nt;
+    int sum = 0;
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s < n_seq) sum += (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s < n_seq) {
+            prefix[s] = base;
+            base += (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+        }
+    }
+    if (tid == nt - 1) prefix[n_seq] = base;
+    __syncthreads();
+}
+
+// largest s with prefix[s] * Hk <= unit (and tiles of its own)
+__device__ __forceinline__ int find_seq(const int *prefix, int n_seq, int Hk, int64_t unit) {
+    int lo = 0, hi = n_seq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)prefix[mid] * Hk <= unit) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Ranges: W workers share `total` units; at least kMinUnits each while that leaves some idle.
+constexpr int kMinUnits = 2;
+__device__ __forceinline__ int active_workers(int64_t total, int workers) {
+    const int64_t w = (total + kMinUnits - 1) / kMinUnits;
+    return (int)(w < workers ? w : workers);
+}
+__device__ __forceinline__ int64_t range_begin(int64_t total, int W, int w) {
+    const int64_t q = total / W, r = total % W;
+    return w * q + (w < r ? w : r);
+}
+__device__ __forceinline__ int worker_of(int64_t total, int W, int64_t unit) {
+    const int64_t q = total / W, r = total % W, cut = r * (q + 1);
+    return (int)(unit < cut ? unit / (q + 1) : r + (unit - cut) / q);
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(*reinterpret_cast<const __half2 *>(&w)); }
+
+constexpr uint32_t kLoNib = 0x000f000fu, kHiNib = 0x00f000f0u;
+constexpr uint32_t kLoOff = 0x00080008u, kHiOff = 0x00800080u;  // 8 * 2^-24 and 128 * 2^-24 as f16 subnormals
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Query fragments of one pass: NT times 8 rows as the N side of the MMAs,
+// fp32 queries as f16 hi + lo (HL).
+template <int D, int NT, bool HL>
+struct Query {
+    static constexpr int NB = D / 32;
+    uint32_t hi[NT][NB][2][2];             // row g: [block][k-step][low nibbles' dims, high nibbles' dims / 16]
+    uint32_t lo[HL ? NT : 1][NB][2][2];
+    float2 bias[NT][NB];                   // rows 2t, 2t + 1: -8 * 2^-24 * sum of the block's operands
+    float fac[NT];                         // row g: accumulator -> log2 units
+
+    // row rho of (sequence, kv head): query row rho / G, head h G + rho % G
+    __device__ __forceinline__ void load(const AttendParams &p, int s, int h, int rho0) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int rho = rho0 + 8 * n + g;
+            const bool valid = rho < p.R * p.G;
+            const int r = rho / p.G, hq = h * p.G + rho % p.G;
+            const int64_t base = ((int64_t)s * p.R + r) * p.q_stride + (int64_t)hq * D + 4 * t;
+            float x[NB][8], top = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (valid) {
+                    load_row<4>(p.q, p.dtype, base + b * 32, x[b]);
+                    load_row<4>(p.q, p.dtype, base + b * 32 + 16, x[b] + 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // a power of two that brings the row's largest element to 2^14 .. 2^15 (exact for
+            // 16-bit elements down to 2^-28 of it; f16 then holds 2^-24 more below)
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e < -100 ? -100 : (e > 100 ? 100 : e);
+            const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            fac[n] = p.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - 14 + e) << 23);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float sum = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    // k-step ks: low nibbles are dims 4t + ks and 4t + 2 + ks, high ones 16 further
+                    const float y[4] = {x[b][ks] * f, x[b][2 + ks] * f, x[b][4 + ks] * f, x[b][6 + ks] * f};
+                    const uint32_t a0 = pack(y[0], y[1]), a1 = pack(y[2] * 0.0625f, y[3] * 0.0625f);
+                    sum += half_lo(a0) + half_hi(a0) + 16.f * (half_lo(a1) + half_hi(a1));
+                    hi[n][b][ks][0] = a0;
+                    hi[n][b][ks][1] = a1;
+                    if (HL) {
+                        const uint32_t l0 = pack(y[0] - half_lo(a0), y[1] - half_hi(a0));
+                        const uint32_t l1 = pack(y[2] * 0.0625f - half_lo(a1), y[3] * 0.0625f - half_hi(a1));
+                        sum += half_lo(l0) + half_hi(l0) + 16.f * (half_lo(l1) + half_hi(l1));
+                        lo[n][b][ks][0] = l0;
+                        lo[n][b][ks][1] = l1;
+                    }
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum *= -8.f * 5.9604644775390625e-8f;
+                bias[n][b] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+            }
+        }
+    }
+
+    // scores, not yet times fac, of the tile's tokens 16 c + g and 16 c + 8 + g:
+    // acc[n] = {(g, row 2t), (g, row 2t + 1), (g + 8, row 2t), (g + 8, row 2t + 1)}
+    __device__ __forceinline__ void scores(const uint8_t *tile, int c, float (*acc)[4]) const {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        uint32_t sc[NB], w[2][NB];
+        const uint8_t *ps = tile + 16 * D + (c * 8 + g) * NB * 4;
+        if constexpr (NB == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(ps);
+            sc[0] = v.x, sc[1] = v.y;
+            const uint4 k = *reinterpret_cast<const uint4 *>(tile + (c * 32 + lane) * 16);
+            w[0][0] = k.x, w[0][1] = k.y, w[1][0] = k.z, w[1][1] = k.w;
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; b += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(ps + b * 4);
+                sc[b] = v.x, sc[b + 1] = v.y, sc[b + 2] = v.z, sc[b + 3] = v.w;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(tile + (((2 * c + o) * (NB / 4) + b / 4) * 32 + lane) * 16);
+                    w[o][b] = k.x, w[o][b + 1] = k.y, w[o][b + 2] = k.z, w[o][b + 3] = k.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t x0 = w[0][b] >> 8, x1 = w[1][b] >> 8;
+            const uint32_t a0 = w[0][b] & kLoNib, a1 = w[1][b] & kLoNib, a2 = w[0][b] & kHiNib, a3 = w[1][b] & kHiNib;
+            const uint32_t e0 = x0 & kLoNib, e1 = x1 & kLoNib, e2 = x0 & kHiNib, e3 = x1 & kHiNib;
+            const float s0 = half_lo(sc[b]), s1 = half_hi(sc[b]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float d[4] = {bias[n][b].x, bias[n][b].y, bias[n][b].x, bias[n][b].y};
+                mma(d, a0, a1, a2, a3, hi[n][b][0][0], hi[n][b][0][1]);
+                mma(d, e0, e1, e2, e3, hi[n][b][1][0], hi[n][b][1][1]);
+                if constexpr (HL) {
+                    mma(d, a0, a1, a2, a3, lo[n][b][0][0], lo[n][b][0][1]);
+                    mma(d, e0, e1, e2, e3, lo[n][b][1][0], lo[n][b][1][1]);
+                }
+                acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+                acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+                acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+                acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+            }
+        }
+    }
+};
+
+// Row r's scores of a tile in shared memory: 32 floats, its 16-byte chunk c at
+// place c ^ turn(r).  Writes (rows 2t or 2t + 1, tokens g) and reads (rows g,
+// chunks t) of a warp both hit every bank once.
+__device__ __forceinline__ int turn(int r) { return (r & 6) ^ ((r & 1) << 2); }
+
+// A warp's stages in shared memory and the bulk copies into them.
+template <int BYTES, int NST>
+struct Stages {
+    uint32_t bar0, buf0;
+    const uint8_t *buf;
+    uint32_t bad;   // stage holds no tile: its page number was outside the pool
+    bool gave_up;
+
+    __device__ __forceinline__ void init(uint8_t *smem, uint64_t *bars) {
+        buf = smem;
+        buf0 = smem_addr(smem);
+        bar0 = smem_addr(bars);
+        bad = 0;
+        gave_up = false;
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < NST; ++i)
+                asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8 * i));
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void fetch(int stage, const uint8_t *src) {  // src null: a bad page (warp-uniform)
+        if (!src) {
+            bad |= 1u << stage;
+            return;
+        }
+        bad &= ~(1u << stage);
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t bar = bar0 + 8 * stage;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(BYTES) : "memory");
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    buf0 + stage * BYTES),
+                "l"(src), "r"(BYTES), "r"(bar)
+                : "memory");
+        }
+    }
+    // the stage's tile, or false: bad page, or the copy never landed
+    __device__ __forceinline__ bool wait(int stage, uint32_t &phases) {
+        if (gave_up || (bad >> stage & 1)) return false;
+        const uint32_t parity = phases >> stage & 1;
+        phases ^= 1u << stage;
+        for (uint32_t i = 0; i < kWaitLimit; ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(done)
+                : "r"(bar0 + 8 * stage), "r"(parity)
+                : "memory");
+            if (__all_sync(0xffffffffu, done)) return true;
+        }
+        gave_up = true;
+        return false;
+    }
+};
+
+// A worker's place in the line of tiles: sequence, head, tile, and the pages ahead.
+struct Cursor {
+    int s, h, k, T;       // tile k of T of (s, h)
+    int page_base, page;  // lane l holds page number page_base + l of the sequence
+    __device__ __forceinline__ void load_pages(const Pool &pool, const int32_t *table, int width, int tiles_per_page_lg) {
+        const int lane = threadIdx.x & 31;
+        page_base = k >> tiles_per_page_lg;
+        const int at = page_base + lane;
+        page = at < width ? table[(int64_t)s * width + at] : -1;
+    }
+    __device__ __forceinline__ void seek(const Pool &pool, const int *prefix, const int32_t *table, int width, int n_seq,
+                                         int64_t unit, int lg) {
+        s = find_seq(prefix, n_seq, pool.Hk, unit);
+        T = prefix[s + 1] - prefix[s];
+        const int64_t in = unit - (int64_t)prefix[s] * pool.Hk;
+        h = (int)(in / T);
+        k = (int)(in % T);
+        load_pages(pool, table, width, lg);
+    }
+    // the tile's bytes (null: a page number outside the pool), warp-uniform
+    __device__ __forceinline__ const uint8_t *tile(const Pool &pool, const int32_t *table, int width, int lg, int tile_bytes) {
+        const int at = k >> lg;
+        if (at - page_base >= 32) load_pages(pool, table, width, lg);
+        const int pg = __shfl_sync(0xffffffffu, page, at - page_base);
+        if (pg < 0 || pg >= pool.n_pages) return nullptr;
+        return pool.pages + pg * pool.page_bytes + h * pool.head_bytes + (int64_t)(k & ((1 << lg) - 1)) * tile_bytes;
+    }
+    __device__ __forceinline__ void next(const Pool &pool, const int *prefix, const int32_t *table, int width, int n_seq, int lg) {
+        if (++k < T) return;
+        k = 0;
+        if (++h < pool.Hk) {
+            load_pages(pool, table, width, lg);
+            return;
+        }
+        h = 0;
+        do {
+            ++s;
+        } while (s < n_seq && prefix[s + 1] == prefix[s]);
+        if (s >= n_seq) {  // past the last tile: never fetched
+            s = n_seq - 1;
+            T = 1 << 30;
+            return;
+        }
+        T = prefix[s + 1] - prefix[s];
+        load_pages(pool, table, width, lg);
+    }
+};
+
+template <int D>
+__host__ __device__ constexpr int stages_of() {
+    return D == 64 ? 4 : 3;
+}
+template <int D, int NT, bool HL>
+__host__ __device__ constexpr int ctas_per_sm() {
+    return D == 256 ? 2 : (NT == 2 ? 3 : (D == 128 && HL ? 3 : 4));
+}
+
+template <int D, int NT, bool HL>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_kernel(const AttendParams p) {
+    constexpr int NB = D / 32, NST = stages_of<D>(), BYTES = 36 * D;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps * NST];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    int *prefix = reinterpret_cast<int *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
+    const int W = active_workers(total, p.workers);
+    const int rb = blockIdx.x % p.row_blocks;
+    const int w = (int)(blockIdx.x / p.row_blocks) * kWarps + warp;
+    if (w >= W) return;
+    const int64_t u0 = range_begin(total, W, w), u1 = range_begin(total, W, w + 1);
+    const int lg = p.pool.lgP - 5;
+    const int rho0 = rb * 8 * NT;
+
+    Stages<BYTES, NST> st;
+    st.init(smem + warp * NST * BYTES, bars + warp * NST);
+    uint32_t phases = 0;
+    Cursor ahead, at;
+    ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+    at = ahead;
+    const int units = (int)(u1 - u0);
+    int fetched = 0;
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+        if (fetched < units) {
+            st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
+            ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            ++fetched;
+        }
+    }
+    Query<D, NT, HL> q;
+    float O[NT][NB][2][4], cs[NT][4], ref[NT], l[NT];  // cs: row b (< 8) holds block b's -8 * 2^-24 * sum p s
+    bool fresh = true;
+    int k_first = 0;
+    int stage = 0;
+    for (int unit = 0; unit < units; ++unit) {
+        if (fresh) {  // a new (sequence, head)
+            q.load(p, at.s, at.h, rho0);
+            k_first = at.k;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                ref[n] = -INFINITY;
+                l[n] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[n][i] = 0.f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[n][b][0][i] = O[n][b][1][i] = 0.f;
+            }
+            fresh = false;
+        }
+        if (!st.wait(stage, phases)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) l[n] = __int_as_float(0x7fc00000);
+            if (st.gave_up) break;
+        } else {
+            const uint8_t *tile = st.buf + stage * BYTES;
+            // the turned scores take the place of the tile's K codes once those are read (at D = 64 they are too small)
+            float *turned = reinterpret_cast<float *>(D == 64 ? smem + kWarps * NST * BYTES + warp * 1024 : const_cast<uint8_t *>(tile));
+            const int len = seq_len(p.pool, p.lens, p.table_width, at.s);
+            const int in_tile = len - at.k * kTile;  // tokens of the sequence from this tile on
+            float x[NT][8];  // row g, tokens 16 c + 4 t + (0 .. 3) at 4 c
+            {
+                float acc[2][NT][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) q.scores(tile, c, acc[c]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    __syncwarp();  // the area's last readers are done (for n = 0: of the K codes)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 2 * t + (i & 1), tok = 16 * c + 8 * (i >> 1) + g;
+                            turned[row * 32 + (((tok >> 2) ^ turn(row)) << 2) + (tok & 3)] = acc[c][n][i];
+                        }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float4 v = *reinterpret_cast<const float4 *>(turned + g * 32 + (((4 * c + t) ^ turn(g)) << 2));
+                        x[n][4 * c] = v.x * q.fac[n], x[n][4 * c + 1] = v.y * q.fac[n];
+                        x[n][4 * c + 2] = v.z * q.fac[n], x[n][4 * c + 3] = v.w * q.fac[n];
+                    }
+                }
+            }
+            // V scales: tokens 16 c + 4 t + (0 .. 3)
+            uint2 vs[2][NB];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; b += 2) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + 34 * D + ((c * 4 + t) * NB + b) * 8);
+                    vs[c][b] = make_uint2(v.x, v.y);
+                    vs[c][b + 1] = make_uint2(v.z, v.w);
+                }
+            if (in_tile - (p.R - 1) < kTile) {  // some row does not see the whole tile
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int see = in_tile - (p.R - 1) + (rho0 + 8 * n + g) / p.G;  // tokens of the tile this row sees
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (16 * (i >> 2) + 4 * t + (i & 3) >= see) x[n][i] = -INFINITY;
+                }
+                if (in_tile < kTile) {  // tokens never written: their scales may be anything
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int left = in_tile - 16 * c - 4 * t;
+                        const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                        const uint32_t k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            vs[c][b].x &= k0;
+                            vs[c][b].y &= k1;
+                        }
+                    }
+                }
+            }
+            // the tile's largest |V scale| as a power of two, rounded up
+            __half2 sm = __float2half2_rn(0.f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[c][b].x)));
+                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[c][b].y)));
+                }
+            float smax = fmaxf(__low2float(sm), __high2float(sm));
+            smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 1));
+            smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 2));
+            const float lg_s = (float)((int)(__float_as_uint(fmaxf(smax, 5.9604644775390625e-8f)) >> 23) - 126);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float mx = x[n][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[n][i]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // largest weight x scale of the tile is below 2^(need - ref): kept at 2^14 at most
+                const float need = mx + lg_s;
+                const bool grow = need - 14.f > ref[n];
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? need - 8.f : ref[n];
+                    const float alpha = ref[n] == -INFINITY ? 0.f : exp2f(ref[n] - to);
+                    ref[n] = to;
+                    l[n] *= alpha;
+                    const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float al = (i & 1) ? a1 : a0;
+                        cs[n][i] *= al;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            O[n][b][0][i] *= al;
+                            O[n][b][1][i] *= al;
+                        }
+                    }
+                }
+                const float r0 = ref[n] == -INFINITY ? 0.f : ref[n];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[n][i] = ex2(x[n][i] - r0);
+                    l[n] += x[n][i];
+                }
+            }
+            // O^T += V^T (p s)^T, 16 tokens at a time
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t vw[2 * NB];
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + 18 * D + ((c * (NB / 2) + i) * 32 + lane) * 16);
+                    vw[4 * i] = v.x, vw[4 * i + 1] = v.y, vw[4 * i + 2] = v.z, vw[4 * i + 3] = v.w;
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const float s0 = half_lo(vs[c][b].x), s1 = half_hi(vs[c][b].x);
+                    const float s2 = half_lo(vs[c][b].y), s3 = half_hi(vs[c][b].y);
+                    const uint32_t w0 = vw[2 * b], w1 = vw[2 * b + 1];
+                    uint32_t a0 = w0 & kLoNib, a1 = w0 & kHiNib, a2 = w1 & kLoNib, a3 = w1 & kHiNib;
+                    uint32_t e0 = (w0 >> 8) & kLoNib, e1 = (w0 >> 8) & kHiNib, e2 = (w1 >> 8) & kLoNib, e3 = (w1 >> 8) & kHiNib;
+                    if constexpr (HL) {  // n - 8 as it stands: sums of 0 .. 15 codes would leave their own rounding
+                        a0 = hsub2(a0, kLoOff), a2 = hsub2(a2, kLoOff), a1 = hsub2(a1, kHiOff), a3 = hsub2(a3, kHiOff);
+                        e0 = hsub2(e0, kLoOff), e2 = hsub2(e2, kLoOff), e1 = hsub2(e1, kHiOff), e3 = hsub2(e3, kHiOff);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float y0 = x[n][4 * c] * s0, y1 = x[n][4 * c + 1] * s1;
+                        const float y2 = x[n][4 * c + 2] * s2, y3 = x[n][4 * c + 3] * s3;
+                        const uint32_t b0 = pack(y0, y1), b1 = pack(y2, y3);
+                        mma(O[n][b][0], a0, a1, a2, a3, b0, b1);
+                        mma(O[n][b][1], e0, e1, e2, e3, b0, b1);
+                        if constexpr (HL) {
+                            const uint32_t d0 = pack(y0 - half_lo(b0), y1 - half_hi(b0)), d1 = pack(y2 - half_lo(b1), y3 - half_hi(b1));
+                            mma(O[n][b][0], a0, a1, a2, a3, d0, d1);
+                            mma(O[n][b][1], e0, e1, e2, e3, d0, d1);
+                        } else {  // row b: -8 * 2^-24 (f16 subnormal) times the sum of the same operands
+                            const uint32_t eight = g == b ? kLoOff | 0x80008000u : 0u;
+                            mma(cs[n], eight, 0u, eight, 0u, b0, b1);
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the turned scores, before a copy over them
+        __syncwarp();
+        const bool last_of_head = at.k + 1 == at.T;
+        if (fetched < units) {
+            st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
+            ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            ++fetched;
+        }
+        stage = stage + 1 == NST ? 0 : stage + 1;
+        if (last_of_head || unit + 1 == units) {
+            const bool whole = k_first == 0 && last_of_head;
+            const int slot = unit == at.k - k_first ? 0 : 1;  // the worker's first (sequence, head), or its last
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+                const float l0 = __shfl_sync(0xffffffffu, l[n], 8 * t), l1 = __shfl_sync(0xffffffffu, l[n], 8 * t + 4);
+                // a row that saw nothing: out 0, lse -inf
+                const float i0 = whole ? (l0 == 0.f ? 0.f : 1.f / l0) : 1.f, i1 = whole ? (l1 == 0.f ? 0.f : 1.f / l1) : 1.f;
+                const int64_t pslot = (((int64_t)rb * p.workers + w) * 2 + slot) * (8 * NT) + 8 * n;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // heads (rows of the pass) 2t, 2t + 1
+                    const int row = 2 * t + c, rho = rho0 + 8 * n + row;
+                    const float inv = (c ? i1 : i0) * 16777216.f;
+                    float off[NB];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) off[b] = __shfl_sync(0xffffffffu, cs[n][c], b * 4 + t);
+                    if (rho >= p.R * p.G) continue;
+                    const int64_t orow = (((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G) * D;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const int dim = b * 32 + 8 * m + g;
+                            const float lo = (O[n][b][m][c] + off[b]) * inv;
+                            const float hi = (O[n][b][m][2 + c] * 0.0625f + off[b]) * inv;
+                            if (whole) {
+                                put(p.out, p.dtype, orow + dim, lo);
+                                put(p.out, p.dtype, orow + dim + 16, hi);
+                            } else {
+                                p.part_o[(pslot + row) * D + dim] = lo;
+                                p.part_o[(pslot + row) * D + dim + 16] = hi;
+                            }
+                        }
+                }
+                const int rho = rho0 + 8 * n + g;
+                if (t == 0 && rho < p.R * p.G) {
+                    if (!whole) p.part_rl[pslot + g] = make_float2(ref[n], l[n]);
+                    else if (p.lse)
+                        p.lse[((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G] =
+                            l[n] == 0.f ? -INFINITY : (ref[n] + log2f(l[n])) * 0.693147180559945309f;
+                }
+            }
+            fresh = true;
+        }
+        at.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+    }
+    if (st.gave_up) {  // what this worker owed is NaN: partials and whole rows of its range
+        for (int i = lane; i < 2 * 8 * NT; i += 32)
+            p.part_rl[((int64_t)rb * p.workers + w) * 2 * (8 * NT) + i] = make_float2(0.f, __int_as_float(0x7fc00000));
+        Cursor c;
+        c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+        for (int unit = 0; unit < units; ++unit) {
+            if (c.k == 0 && unit + c.T <= units)
+                for (int rho = rho0; rho < rho0 + 8 * NT && rho < p.R * p.G; ++rho) {
+                    const int64_t row = ((int64_t)c.s * p.R + rho / p.G) * p.Hq + c.h * p.G + rho % p.G;
+                    for (int d = lane; d < D; d += 32) put(p.out, p.dtype, row * D + d, __int_as_float(0x7fc00000));
+                    if (lane == 0 && p.lse) p.lse[row] = __int_as_float(0x7fc00000);
+                }
+            c.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+        }
+        // copies still in flight land in this CTA's shared memory: give them the same time again
+        st.gave_up = false;
+        for (int i = 0; i < NST; ++i) st.wait(i, phases);
+    }
+}
+
+// One warp per (sequence, kv head, row): joins the partials of a (sequence,
+// head) that several workers shared; rows of empty sequences are written here.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(const AttendParams p, int pass_rows) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    int *prefix = reinterpret_cast<int *>(smem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
+    const int W = active_workers(total, p.workers);
+    const int lane = threadIdx.x & 31;
+    const int rows = p.R * p.G;
+    const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (id >= (int64_t)p.n_seq * p.pool.Hk * rows) return;
+    const int rho = (int)(id % rows), h = (int)(id / rows % p.pool.Hk), s = (int)(id / rows / p.pool.Hk);
+    const int T = prefix[s + 1] - prefix[s];
+    const int64_t orow = ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G;
+    float o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    float lse = -INFINITY;
+    if (T > 0) {
+        const int64_t u0 = (int64_t)prefix[s] * p.pool.Hk + (int64_t)h * T, u1 = u0 + T;
+        const int w0 = worker_of(total, W, u0), w1 = worker_of(total, W, u1 - 1);
+        if (w0 == w1) return;  // one worker had it all and wrote it
+        const int rb = rho / pass_rows, row = rho % pass_rows;
+        float top = -INFINITY;
+        auto slot_of = [&](int w) {
+            const int64_t begin = range_begin(total, W, w);
+            return (((int64_t)rb * p.workers + w) * 2 + (begin >= u0 ? 0 : 1)) * pass_rows + row;
+        };
+        for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, p.part_rl[slot_of(w)].x);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float r0 = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int w = w0; w <= w1; ++w) {
+            const int64_t at = slot_of(w);
+            const float2 rl = p.part_rl[at];
+            const float f = exp2f(rl.x - r0);
+            sum = fmaf(rl.y, f, sum);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(p.part_o[at * D + i * 32 + lane], f, o[i]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] *= inv;
+        if (sum != 0.f) lse = (r0 + log2f(sum)) * 0.693147180559945309f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) put(p.out, p.dtype, orow * D + i * 32 + lane, o[i]);
+    if (lane == 0 && p.lse) p.lse[orow] = lse;
+}
+
+// ---------------------------------------------------------------- weights
+// w[t] += sum over rows of 2^(score - lse): K tiles only, no join between
+// workers (a token is one worker's).  Row passes beyond the first re-read the
+// worker's tiles and add to what the first wrote.
+struct WeightsParams {
+    AttendParams a;
+    const float *lse_in;
+    const float *prev;
+    float *w;
+    int64_t width;
+};
+
+// entries no tile covers: prev's (or zero)
+__global__ void __launch_bounds__(256) weights_rest_kernel(const WeightsParams p) {
+    const int s = blockIdx.y / p.a.pool.Hk;
+    const int len = seq_len(p.a.pool, p.a.lens, p.a.table_width, s);
+    const int64_t first = ((int64_t)len + kTile - 1) / kTile * kTile;
+    for (int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.width; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = (int64_t)blockIdx.y * p.width + i;
+        p.w[at] = p.prev ? p.prev[at] : 0.f;
+    }
+}
+
+template <int D, int NT, bool HL>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights_kernel(const WeightsParams wp) {
+    constexpr int NST = stages_of<D>(), BYTES = 18 * D;  // the K half of a tile
+    const AttendParams &p = wp.a;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps * NST];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    int *prefix = reinterpret_cast<int *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
+    const int W = active_workers(total, p.workers);
+    const int w = (int)blockIdx.x * kWarps + warp;
+    if (w >= W) return;
+    const int64_t u0 = range_begin(total, W, w), u1 = range_begin(total, W, w + 1);
+    const int lg = p.pool.lgP - 5;
+    Stages<BYTES, NST> st;
+    st.init(smem + warp * NST * BYTES, bars + warp * NST);
+    uint32_t phases = 0;
+    Query<D, NT, HL> q;
+    for (int rho0 = 0; rho0 < p.R * p.G; rho0 += 8 * NT) {
+        Cursor ahead, at;
+        ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+        at = ahead;
+        const int units = (int)(u1 - u0);
+        int fetched = 0;
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+            if (fetched < units) {
+                st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
+                ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                ++fetched;
+            }
+        }
+        bool fresh = true;
+        int stage = 0;
+        float2 lse2[NT], fac[NT];  // rows 2t, 2t + 1
+        for (int unit = 0; unit < units; ++unit) {
+            if (fresh) {
+                q.load(p, at.s, at.h, rho0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int rho = rho0 + 8 * n + g;
+                    float z = INFINITY;  // rows past the last, and rows that saw nothing, add nothing
+                    if (rho < p.R * p.G) {
+                        z = wp.lse_in[((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G] * 1.4426950408889634f;
+                        if (z == -INFINITY) z = INFINITY;
+                    }
+                    lse2[n] = make_float2(__shfl_sync(0xffffffffu, z, 8 * t), __shfl_sync(0xffffffffu, z, 8 * t + 4));
+                    fac[n] = make_float2(__shfl_sync(0xffffffffu, q.fac[n], 8 * t), __shfl_sync(0xffffffffu, q.fac[n], 8 * t + 4));
+                }
+                fresh = false;
+            }
+            const int len = seq_len(p.pool, p.lens, p.table_width, at.s);
+            const int in_tile = len - at.k * kTile;
+            float sum[4];  // tokens g, g + 8, g + 16, g + 24
+            if (!st.wait(stage, phases)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = __int_as_float(0x7fc00000);
+            } else {
+                float acc[2][NT][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) q.scores(st.buf + stage * BYTES, c, acc[c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int base = in_tile - (p.R - 1), rho = rho0 + 8 * n + 2 * t;
+                    const int see0 = base + rho / p.G, see1 = base + (rho + 1) / p.G;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float *a = &acc[i >> 1][n][2 * (i & 1)];
+                        const float e0 = ex2(fmaf(a[0], fac[n].x, -lse2[n].x)), e1 = ex2(fmaf(a[1], fac[n].y, -lse2[n].y));
+                        sum[i] += (8 * i + g < see0 ? e0 : 0.f) + (8 * i + g < see1 ? e1 : 0.f);
+                    }
+                }
+            }
+            // over the row pairs t: each exchange halves the values a lane keeps
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float give = (t & 2) ? sum[i] : sum[i + 2], keep = (t & 2) ? sum[i + 2] : sum[i];
+                sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+            }
+            {
+                const float give = (t & 1) ? sum[0] : sum[1], keep = (t & 1) ? sum[1] : sum[0];
+                sum[0] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+            }
+            const int tok = 8 * t + g;
+            const int64_t pos = (int64_t)at.k * kTile + tok;
+            if (pos < wp.width) {
+                const int64_t o = ((int64_t)at.s * p.pool.Hk + at.h) * wp.width + pos;
+                const float before = rho0 ? wp.w[o] : (wp.prev ? wp.prev[o] : 0.f);
+                wp.w[o] = before + (tok < in_tile ? sum[0] : 0.f);
+            }
+            __syncwarp();
+            if (fetched < units) {
+                if (!st.gave_up) st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
+                ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                ++fetched;
+            }
+            if (at.k + 1 == at.T) fresh = true;
+            stage = stage + 1 == NST ? 0 : stage + 1;
+            at.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+kvs_status bad(kvs_status s, const char *why) {
+    set_thread_error(why);
+    return s;
+}
+kvs_status cuda_failed(const char *what, cudaError_t e) {
+    set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return KVS_ERR_CUDA;
+}
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t elem_size(int dtype) { return dtype == KVS_F32 ? 4 : 2; }
+
+kvs_status check_pool(const kvs_q4_pool *pool, bool need_pages, Pool *out) {
+    if (!pool) return bad(KVS_ERR_INVALID, "null pool");
+    const uint32_t P = pool->page_tokens, D = pool->head_dim;
+    if (!(P == 32 || P == 64 || P == 128 || P == 256) || !(D == 64 || D == 128 || D == 256))
+        return bad(KVS_ERR_UNSUPPORTED, "page_tokens must be 32..256 (power of two), head_dim 64, 128 or 256");
+    if (pool->n_kv_head == 0 || pool->n_kv_head > 65535) return bad(KVS_ERR_INVALID, "n_kv_head must be 1 .. 65535");
+    if (need_pages) {
+        if (!pool->pages || !aligned(pool->pages, 16)) return bad(KVS_ERR_INVALID, "pages null or not 16-byte aligned");
+        if (pool->n_pages == 0 || pool->n_pages > 0x7fffffffull) return bad(KVS_ERR_INVALID, "n_pages must be 1 .. 2^31 - 1");
+    }
+    out->pages = static_cast<uint8_t *>(pool->pages);
+    out->n_pages = (int64_t)pool->n_pages;
+    out->P = (int)P;
+    out->lgP = P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : 8;
+    out->Hk = (int)pool->n_kv_head;
+    out->head_bytes = (int64_t)P * D * 9 / 8;
+    out->page_bytes = out->head_bytes * out->Hk;
+    return KVS_OK;
+}
+bool dtype_ok(int32_t t) { return t == KVS_F32 || t == KVS_F16 || t == KVS_BF16; }
+
+// How a call's query rows are passed: fp32 queries 8 rows at a time (with
+// their lo halves), 16-bit ones 8 if that is all there are, else 16.  At
+// D = 256 the 16-row accumulators do not fit the registers.
+struct Shape {
+    int nt, row_blocks, workers, ctas;
+    bool hl;
+};
+Shape shape_of(uint32_t D, uint32_t rows, int32_t dtype, int sms) {
+    Shape s;
+    s.hl = dtype == KVS_F32;
+    s.nt = (!s.hl && D <= 128 && rows > 8) ? 2 : 1;
+    s.row_blocks = ((int)rows + 8 * s.nt - 1) / (8 * s.nt);
+    const int per_sm = D == 256 ? 2 : (s.nt == 2 ? 3 : (D == 128 && s.hl ? 3 : 4));
+    int ranges = sms * per_sm / s.row_blocks;
+    if (ranges < 1) ranges = 1;
+    s.ctas = ranges * s.row_blocks;
+    s.workers = ranges * kWarps;
+    return s;
+}
+constexpr int kSmsAssumed = 152;  // sizes the workspace; a launch uses no more than that many SMs' worth
+
+uint64_t workspace_of(const Shape &s, uint32_t D) {
+    const uint64_t rows = (uint64_t)s.row_blocks * s.workers * 2 * 8 * s.nt;
+    return (rows * D * 4 + rows * 8 + 255) / 256 * 256;
+}
+
+kvs_status check_rows(uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, int Hk, uint32_t *group) {
+    if (n_seq > kMaxSeq) return bad(KVS_ERR_UNSUPPORTED, "n_seq must be at most 4096");
+    if (n_rows < 1 || n_q_head < (uint32_t)Hk || n_q_head % (uint32_t)Hk != 0)
+        return bad(KVS_ERR_INVALID, "need n_rows >= 1 and n_q_head a positive multiple of n_kv_head");
+    *group = n_q_head / (uint32_t)Hk;
+    if (*group > (uint32_t)kMaxGroupRows || n_rows > (uint32_t)kMaxGroupRows || *group * n_rows > (uint32_t)kMaxGroupRows)
+        return bad(KVS_ERR_UNSUPPORTED, "n_rows * (n_q_head / n_kv_head) must be <= 64");
+    return KVS_OK;
+}
+
+kvs_status fill_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens, uint32_t n_seq,
+                       uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype, uint64_t q_stride, float scale,
+                       AttendParams *p) {
+    kvs_status s = check_pool(pool, true, &p->pool);
+    if (s != KVS_OK) return s;
+    if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
+    uint32_t G = 0;
+    s = check_rows(n_seq, n_rows, n_q_head, p->pool.Hk, &G);
+    if (s != KVS_OK) return s;
+    if (!table || !lens || !q) return bad(KVS_ERR_INVALID, "null table, lens or q");
+    if (table_width < 1 || (uint64_t)table_width * pool->page_tokens > 0x7fffffc0ull)
+        return bad(KVS_ERR_INVALID, "table_width * page_tokens must be 1 .. 2^31 - 64");
+    if (!aligned(q, 16) || (q_stride * elem_size(dtype)) % 16 != 0 || q_stride < (uint64_t)n_q_head * pool->head_dim)
+        return bad(KVS_ERR_INVALID, "q rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
+    if (!isfinite(scale)) return bad(KVS_ERR_INVALID, "scale must be finite");
+    p->table = table;
+    p->table_width = (int)table_width;
+    p->lens = lens;
+    p->n_seq = (int)n_seq;
+    p->R = (int)n_rows;
+    p->Hq = (int)n_q_head;
+    p->G = (int)G;
+    p->q = q;
+    p->dtype = dtype;
+    p->q_stride = (int64_t)q_stride;
+    p->scale_log2 = scale * 1.4426950408889634f;
+    return KVS_OK;
+}
+
+template <typename P, typename... A>
+cudaError_t launch(void (*kernel)(P, A...), dim3 grid, int threads, int smem, cudaStream_t s, bool pdl, const P &p, A... a) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a...);
+}
+
+int smem_of(uint32_t D, int bytes, uint32_t n_seq) {
+    return kWarps * (D == 64 ? 4 * bytes + 1024 : 3 * bytes) + ((int)n_seq + 1) * 4;
+}
+
+}  // namespace
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_rows, uint32_t n_q_head, int32_t dtype,
+                                         uint64_t *page_bytes, uint64_t *workspace_bytes) {
+    Pool p = {};
+    kvs_status s = check_pool(pool, false, &p);
+    if (s != KVS_OK) return s;
+    if (workspace_bytes) {
+        if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
+        uint32_t G = 0;
+        s = check_rows(1, n_rows, n_q_head, p.Hk, &G);
+        if (s != KVS_OK) return s;
+        *workspace_bytes = workspace_of(shape_of(pool->head_dim, n_rows * G, dtype, kSmsAssumed), pool->head_dim);
+    }
+    if (page_bytes) *page_bytes = (uint64_t)p.page_bytes;
+    return KVS_OK;
+}
+
+static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, int32_t dtype, RowsParams *p, unsigned *blocks) {
+    kvs_status s = check_pool(pool, true, &p->pool);
+    if (s != KVS_OK) return s;
+    if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
+    if (n && (!slots || !aligned(slots, 8))) return bad(KVS_ERR_INVALID, "slots null or misaligned");
+    const uint64_t units = (uint64_t)pool->n_kv_head * (pool->head_dim / 32);
+    if (n > (0x7fffffffull * 256) / units) return bad(KVS_ERR_INVALID, "too many rows");
+    p->slots = slots;
+    p->n = (int64_t)n;
+    p->dtype = dtype;
+    *blocks = (unsigned)((n * units + 255) / 256);
+    return KVS_OK;
+}
+
+extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, const void *k, const void *v,
+                                    int32_t dtype, uint64_t k_stride, uint64_t v_stride, void *stream) {
+    RowsParams p = {};
+    unsigned blocks = 0;
+    kvs_status s = rows_call(pool, slots, n, dtype, &p, &blocks);
+    if (s != KVS_OK) return s;
+    if (n == 0) return KVS_OK;
+    const uint64_t row = (uint64_t)pool->n_kv_head * pool->head_dim, e = elem_size(dtype);
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || k_stride < row || v_stride < row || k_stride * e % 16 || v_stride * e % 16)
+        return bad(KVS_ERR_INVALID, "k and v rows must start on 16-byte boundaries, at least n_kv_head * head_dim apart");
+    p.k = k;
+    p.v = v;
+    p.k_stride = (int64_t)k_stride;
+    p.v_stride = (int64_t)v_stride;
+    auto kernel = pool->head_dim == 64 ? append_kernel<64> : pool->head_dim == 128 ? append_kernel<128> : append_kernel<256>;
+    const cudaError_t ce = launch(kernel, dim3(blocks, 2), 256, 0, static_cast<cudaStream_t>(stream), false, p);
+    return ce == cudaSuccess ? KVS_OK : cuda_failed("append launch", ce);
+}
+
+extern "C" kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, void *k, void *v, int32_t dtype,
+                                  void *stream) {
+    RowsParams p = {};
+    unsigned blocks = 0;
+    kvs_status s = rows_call(pool, slots, n, dtype, &p, &blocks);
+    if (s != KVS_OK) return s;
+    if (!aligned(k, 16) || !aligned(v, 16)) return bad(KVS_ERR_INVALID, "k and v must be 16-byte aligned");
+    if (n == 0 || (!k && !v)) return KVS_OK;
+    p.ko = k;
+    p.vo = v;
+    auto kernel = pool->head_dim == 64 ? read_kernel<64> : pool->head_dim == 128 ? read_kernel<128> : read_kernel<256>;
+    const cudaError_t ce = launch(kernel, dim3(blocks, 2), 256, 0, static_cast<cudaStream_t>(stream), false, p);
+    return ce == cudaSuccess ? KVS_OK : cuda_failed("read launch", ce);
+}
+
+extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                    uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                                    uint64_t q_stride, float scale, void *out, float *lse, void *workspace,
+                                    uint64_t workspace_bytes, void *stream) {
+    AttendParams p = {};
+    kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p);
+    if (s != KVS_OK) return s;
+    if (!out || !aligned(out, 16)) return bad(KVS_ERR_INVALID, "out null or not 16-byte aligned");
+    if (n_seq == 0) return KVS_OK;
+    const uint32_t D = pool->head_dim;
+    const uint64_t need = workspace_of(shape_of(D, n_rows * p.G, dtype, kSmsAssumed), D);
+    if (!workspace || !aligned(workspace, 256)) return bad(KVS_ERR_INVALID, "workspace null or not 256-byte aligned");
+    if (workspace_bytes < need) return bad(KVS_ERR_CAPACITY, "workspace smaller than kvs_q4_query_sizes asks for");
+    const int sms = current_device_sms();
+    const Shape sh = shape_of(D, n_rows * p.G, dtype, sms < kSmsAssumed ? sms : kSmsAssumed);
+    p.out = out;
+    p.lse = lse;
+    p.row_blocks = sh.row_blocks;
+    p.workers = sh.workers;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_rl = reinterpret_cast<float2 *>(p.part_o + (uint64_t)sh.row_blocks * sh.workers * 2 * 8 * sh.nt * D);
+    void (*k)(AttendParams) = nullptr;
+    if (D == 64) k = sh.hl ? attend_kernel<64, 1, true> : sh.nt == 2 ? attend_kernel<64, 2, false> : attend_kernel<64, 1, false>;
+    if (D == 128) k = sh.hl ? attend_kernel<128, 1, true> : sh.nt == 2 ? attend_kernel<128, 2, false> : attend_kernel<128, 1, false>;
+    if (D == 256) k = sh.hl ? attend_kernel<256, 1, true> : attend_kernel<256, 1, false>;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 36 * (int)D, n_seq), st, false, p);
+    if (e != cudaSuccess) return cuda_failed("attention launch", e);
+    void (*c)(AttendParams, int) = D == 64 ? combine_kernel<64> : D == 128 ? combine_kernel<128> : combine_kernel<256>;
+    const uint64_t rows = (uint64_t)n_seq * n_q_head * n_rows;
+    e = launch(c, dim3((unsigned)((rows + 7) / 8)), 256, ((int)n_seq + 1) * 4, st, true, p, 8 * sh.nt);
+    return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
+}
+
+extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                     uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                                     uint64_t q_stride, float scale, const float *lse, const float *prev, float *weights,
+                                     uint64_t width, void *stream) {
+    WeightsParams p = {};
+    kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p.a);
+    if (s != KVS_OK) return s;
+    if (!lse || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
+    if ((uint64_t)n_seq * pool->n_kv_head > 65535) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head must be at most 65535");
+    if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
+    if (n_seq == 0 || width == 0) return KVS_OK;
+    const uint32_t D = pool->head_dim;
+    const int sms = current_device_sms();
+    Shape sh = shape_of(D, n_rows * p.a.G, dtype, sms);
+    p.a.row_blocks = 1;
+    p.a.workers = sh.ctas * kWarps;
+    p.lse_in = lse;
+    p.prev = prev;
+    p.w = weights;
+    p.width = (int64_t)width;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void (*k)(WeightsParams) = nullptr;
+    if (D == 64) k = sh.hl ? weights_kernel<64, 1, true> : sh.nt == 2 ? weights_kernel<64, 2, false> : weights_kernel<64, 1, false>;
+    if (D == 128) k = sh.hl ? weights_kernel<128, 1, true> : sh.nt == 2 ? weights_kernel<128, 2, false> : weights_kernel<128, 1, false>;
+    if (D == 256) k = sh.hl ? weights_kernel<256, 1, true> : weights_kernel<256, 1, false>;
+    cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 18 * (int)D, n_seq), st, false, p);
+    if (e != cudaSuccess) return cuda_failed("weights launch", e);
+    if (prev != weights) {
+        const unsigned gx = (unsigned)((width + 8191) / 8192);
+        e = launch(weights_rest_kernel, dim3(gx < 64 ? gx : 64, n_seq * pool->n_kv_head), 256, 0, st, false, p);
+        if (e != cudaSuccess) return cuda_failed("weights launch", e);
+    }
+    return KVS_OK;
+}

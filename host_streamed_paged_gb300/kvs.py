@@ -32,6 +32,7 @@ KVS_TYPE_Q4_0 = 2
 KVS_TYPE_Q8_0 = 8
 KVS_F32 = 0
 KVS_F16 = 1
+KVS_BF16 = 2
 KVS_FLAG_PLAN_ONLY = 1
 KVS_FLAG_DMA_FILL = 2
 KVS_FLAG_F16_OPERANDS = 4
@@ -123,6 +124,19 @@ class kvs_policy_decision(ctypes.Structure):
 KVS_POLICY_INIT, KVS_POLICY_FITS, KVS_POLICY_HOLD, KVS_POLICY_GROW, KVS_POLICY_SHRINK, KVS_POLICY_CLAMP = range(1, 7)
 
 
+class kvs_prompt(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_uint64), ("k_stride", ctypes.c_uint64), ("v_stride", ctypes.c_uint64),
+                ("cu", ctypes.c_void_p), ("n_seq", ctypes.c_uint32), ("total_rows", ctypes.c_uint32),
+                ("n_q_head", ctypes.c_uint32), ("n_kv_head", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class kvs_q4_pool(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_uint64), ("page_tokens", ctypes.c_uint32),
+                ("n_kv_head", ctypes.c_uint32), ("head_dim", ctypes.c_uint32)]
+
+
 # every symbol include/kvs.h declares, with its ctypes signature
 _P, _U32, _U64, _I32, _I64, _F32 = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64,
                                     ctypes.c_int32, ctypes.c_int64, ctypes.c_float)
@@ -164,6 +178,14 @@ SIGNATURES = {
     "kvs_attend_pages_noalloc": ([_P, _U64, _P, _U64, _U32, _U32, _U32, _P, _I32, _U32, _U32, _U64, _F32,
                                   _P, _P, _P], _I32),
     "kvs_policy_step": ([_P, _P, _P, _P, _P], _I32),
+    "kvs_prompt_attend": ([_P, _P, _U64, _P, _P], _I32),
+    "kvs_prompt_weights": ([_P, _P, _U32, _P, _P, _U64, _P], _I32),
+    "kvs_q4_query_sizes": ([_P, _U32, _U32, _I32, _P, _P], _I32),
+    "kvs_q4_append": ([_P, _P, _U64, _P, _P, _I32, _U64, _U64, _P], _I32),
+    "kvs_q4_read": ([_P, _P, _U64, _P, _P, _I32, _P], _I32),
+    "kvs_q4_attend": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
+    "kvs_q4_weights": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
+    "kvs_q4_evict": ([_P, _P, _U32, _P, _U32, _P, _U32, _P, _U64, _U32, _U32, _U32, _P, _P, _P, _P], _I32),
 }
 KVS_TIME_RESIDENT = 1
 KVS_TIME_RING = 2
@@ -390,6 +412,52 @@ def kvs_graph_destroy(ctx) -> int:
     return _check(ctx, load().kvs_graph_destroy(ctx))
 
 
+
+def kvs_prompt_attend(prompt: kvs_prompt, out, out_stride, lse=None, stream=0) -> int:
+    return _check(None, load().kvs_prompt_attend(ctypes.byref(prompt), _ptr(out), out_stride, _ptr(lse), stream))
+
+
+def kvs_prompt_weights(prompt: kvs_prompt, lse, last_rows, prev, weights, width, stream=0) -> int:
+    return _check(None, load().kvs_prompt_weights(ctypes.byref(prompt), _ptr(lse), last_rows, _ptr(prev),
+                                                  _ptr(weights), width, stream))
+
+
+def kvs_q4_query_sizes(pool: kvs_q4_pool, n_rows=1, n_q_head=None, dtype=KVS_F32):
+    """(page_bytes, workspace_bytes) of a 4-bit pool and an attend of n_rows rows of n_q_head heads."""
+    page, ws = ctypes.c_uint64(), ctypes.c_uint64()
+    _check(None, load().kvs_q4_query_sizes(ctypes.byref(pool), n_rows, pool.n_kv_head if n_q_head is None else n_q_head,
+                                           dtype, ctypes.byref(page), ctypes.byref(ws)))
+    return page.value, ws.value
+
+
+def kvs_q4_append(pool, slots, n, k, v, dtype, k_stride, v_stride, stream=0) -> int:
+    return _check(None, load().kvs_q4_append(ctypes.byref(pool), _ptr(slots), n, _ptr(k), _ptr(v), dtype, k_stride,
+                                             v_stride, stream))
+
+
+def kvs_q4_read(pool, slots, n, k, v, dtype, stream=0) -> int:
+    return _check(None, load().kvs_q4_read(ctypes.byref(pool), _ptr(slots), n, _ptr(k), _ptr(v), dtype, stream))
+
+
+def kvs_q4_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, out, lse,
+                  workspace, workspace_bytes, stream=0) -> int:
+    return _check(None, load().kvs_q4_attend(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), n_seq, n_rows,
+                                             n_q_head, _ptr(q), dtype, q_stride, scale, _ptr(out), _ptr(lse),
+                                             _ptr(workspace), workspace_bytes, stream))
+
+
+def kvs_q4_weights(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, lse, prev,
+                   weights, width, stream=0) -> int:
+    return _check(None, load().kvs_q4_weights(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), n_seq, n_rows,
+                                              n_q_head, _ptr(q), dtype, q_stride, scale, _ptr(lse), _ptr(prev),
+                                              _ptr(weights), width, stream))
+
+
+def kvs_q4_evict(pool, table, table_width, dst_table, dst_width, lens, n_seq, weights, width, keep, sinks, recent,
+                 kept, kept_weights, new_lens, stream=0) -> int:
+    return _check(None, load().kvs_q4_evict(ctypes.byref(pool), _ptr(table), table_width, _ptr(dst_table), dst_width,
+                                            _ptr(lens), n_seq, _ptr(weights), width, keep, sinks, recent, _ptr(kept),
+                                            _ptr(kept_weights), _ptr(new_lens), stream))
 
 
 def kvs_last_error(ctx) -> str:
@@ -641,3 +709,234 @@ class KVStream:
 
     def last_error(self):
         return kvs_last_error(self.ctx)
+
+
+# ------------------------------------------------------------ batch operators on torch tensors
+
+def _dtype_of(t) -> int:
+    import torch
+    try:
+        return {torch.float32: KVS_F32, torch.float16: KVS_F16, torch.bfloat16: KVS_BF16}[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+def _row_stride(t, what):
+    """Elements between rows of a [..., heads, D] tensor whose heads are contiguous and whose rows lie in one line."""
+    d = t.shape[-1]
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != d):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{what}: rows must lie at one stride")
+    if t.dim() == 4 and t.shape[1] == 1:
+        rows, stride = t.shape[0], t.stride(0)
+    else:
+        rows, stride = t.shape[-3], t.stride(-3)
+    return stride if rows > 1 else max(stride, t.shape[-2] * d)
+
+
+def _need(t, name, dtype, device, shape=None):
+    """t is a contiguous tensor of that type, device and shape (None entries: any size)."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if shape is not None and (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+class _On:
+    """The device of a call's tensors as the current one, and its current stream."""
+
+    def __init__(self, t):
+        import torch
+        if t.device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        self.dev, self.cuda = t.device, torch.cuda
+
+    def __enter__(self):
+        self.prev = self.cuda.current_device()
+        if self.dev.index != self.prev:
+            self.cuda.set_device(self.dev)
+        return self.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.dev.index != self.prev:
+            self.cuda.set_device(self.prev)
+
+
+def _prompt(q, k, v, cu, scale) -> kvs_prompt:
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q, k and v must be [rows][heads][head_dim] with the same rows and head_dim")
+    if k.dtype != q.dtype or k.device != q.device:
+        raise ValueError("q, k and v must have one dtype and device")
+    if v is not None and (v.shape != k.shape or v.dtype != q.dtype or v.device != q.device):
+        raise ValueError("v must be as k")
+    _need(cu, "cu", torch.int32, q.device, (None,))
+    if cu.numel() < 1:
+        raise ValueError("cu must hold n_seq + 1 offsets")
+    return kvs_prompt(_ptr(q), _ptr(k), _ptr(v), _row_stride(q, "q"), _row_stride(k, "k"),
+                      0 if v is None else _row_stride(v, "v"), _ptr(cu), cu.numel() - 1, q.shape[0], q.shape[1],
+                      k.shape[1], q.shape[2], _dtype_of(q), 1.0 / math.sqrt(q.shape[2]) if scale is None else scale)
+
+
+def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
+    """Causal attention of packed prompts over themselves (kvs_prompt_attend): (out, lse).
+
+    q [rows][Hq][D], k and v [rows][Hk][D] in float16 or bfloat16 (rows may be strided), cu int32 [n + 1]: prompt i is
+    rows cu[i] .. cu[i + 1] - 1.  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
+    (undefined where those are allocated here).
+    """
+    import torch
+    p = _prompt(q, k, v, cu, scale)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must be as q")
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", torch.float32, q.device, q.shape[:2])
+    with _On(q) as stream:
+        kvs_prompt_attend(p, out, _row_stride(out, "out"), lse, stream)
+    return out, lse
+
+
+def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=None):
+    """The attention weight each key of packed prompts received (kvs_prompt_weights): float32 [n][Hk][width].
+
+    lse is prompt_attend's; window > 0 counts only each prompt's last window rows; prev (same shape) is added, and
+    may be out.
+    """
+    import torch
+    p = _prompt(q, k, None, cu, scale)
+    _need(lse, "lse", torch.float32, q.device, q.shape[:2])
+    shape = (p.n_seq, p.n_kv_head, int(width))
+    for name, t in (("prev", prev), ("out", out)):
+        if t is not None:
+            _need(t, name, torch.float32, q.device, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    with _On(q) as stream:
+        kvs_prompt_weights(p, lse, int(window), prev, out, shape[2], stream)
+    return out
+
+
+class Q4Cache:
+    """A page cache held in 4 bits (K and V as Q4_0) and the calls on it (kvs_q4_*).
+
+    ``pages`` is a uint8 CUDA tensor of whole pages in the layout include/kvs.h states (or give ``n_pages`` and
+    ``device`` to have one allocated, zeroed).  Page tables (int32 [n_seq][width]), lengths (int32 [n_seq]) and slots
+    (int64: page * page_tokens + token) are CUDA tensors that the caller keeps.  Every call runs on the current
+    stream; attend's workspace is allocated per call from torch's caching allocator, so calls on several streams and
+    captured graphs do not share one.
+    """
+
+    def __init__(self, *, page_tokens, n_kv_head, head_dim, pages=None, n_pages=None, device="cuda"):
+        pool = kvs_q4_pool(0, 1, page_tokens, n_kv_head, head_dim)
+        self.page_bytes = kvs_q4_query_sizes(pool)[0]
+        if pages is None:
+            import torch
+            pages = torch.zeros(int(n_pages) * self.page_bytes, dtype=torch.uint8, device=device)
+        if pages.element_size() != 1 or not pages.is_contiguous() or pages.numel() % self.page_bytes:
+            raise ValueError("pages must be a contiguous uint8 tensor of whole pages")
+        self.pages, self.n_pages = pages, pages.numel() // self.page_bytes
+        pool.pages, pool.n_pages = pages.data_ptr(), self.n_pages
+        self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
+        self._workspace = {}  # bytes by (rows, heads, dtype)
+
+    def _slots(self, slots):
+        import torch
+        _need(slots, "slots", torch.int64, self.pages.device, (None,))
+        return slots.numel()
+
+    def append(self, slots, k, v):
+        """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
+        n = self._slots(slots)
+        if k.shape != (n, self.n_kv_head, self.head_dim) or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be [n][n_kv_head][head_dim] of one dtype")
+        if k.device != self.pages.device or v.device != self.pages.device:
+            raise ValueError("k and v must be on the cache's device")
+        with _On(self.pages) as stream:
+            kvs_q4_append(self.pool, slots, n, k, v, _dtype_of(k), _row_stride(k, "k"), _row_stride(v, "v"), stream)
+
+    def read(self, slots, dtype=None):
+        """The values held in slots: (k, v), each [n][Hk][D] in dtype (default float32, which holds them exactly)."""
+        import torch
+        n = self._slots(slots)
+        dtype = torch.float32 if dtype is None else dtype
+        k, v = (torch.empty((n, self.n_kv_head, self.head_dim), dtype=dtype, device=self.pages.device) for _ in range(2))
+        with _On(self.pages) as stream:
+            kvs_q4_read(self.pool, slots, n, k, v, _dtype_of(k), stream)
+        return k, v
+
+    def _batch(self, table, lens, q):
+        import torch
+        dev = self.pages.device
+        if q.dim() != 4 or q.shape[3] != self.head_dim or q.device != dev:
+            raise ValueError("q must be [n_seq][rows][n_q_head][head_dim] on the cache's device")
+        _need(table, "table", torch.int32, dev, (q.shape[0], None))
+        _need(lens, "lens", torch.int32, dev, (q.shape[0],))
+        return _dtype_of(q), _row_stride(q, "q")
+
+    def attend(self, table, lens, q, scale=None, out=None, lse=None):
+        """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens."""
+        import torch
+        dt, stride = self._batch(table, lens, q)
+        n, rows, hq, d = q.shape
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _need(out, "out", q.dtype, q.device, q.shape)
+        if lse is None:
+            lse = torch.empty((n, rows, hq), dtype=torch.float32, device=q.device)
+        else:
+            _need(lse, "lse", torch.float32, q.device, (n, rows, hq))
+        need = self._workspace.get((rows, hq, dt))
+        if need is None:
+            need = self._workspace[(rows, hq, dt)] = kvs_q4_query_sizes(self.pool, rows, hq, dt)[1]
+        with _On(q) as stream:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            kvs_q4_attend(self.pool, table, table.shape[1], lens, n, rows, hq, q, dt, stride,
+                          1.0 / math.sqrt(d) if scale is None else scale, out, lse, ws, need, stream)
+        return out, lse
+
+    def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
+        """The attention weight each cached token received from those rows, added to prev: float32 [n_seq][Hk][width].
+
+        lse is attend's; width defaults to prev's, or to the tokens the table can hold; out may be prev.
+        """
+        import torch
+        dt, stride = self._batch(table, lens, q)
+        n, rows, hq, d = q.shape
+        _need(lse, "lse", torch.float32, q.device, (n, rows, hq))
+        given = prev if prev is not None else out
+        if width is None:
+            width = given.shape[-1] if given is not None else table.shape[1] * self.page_tokens
+        shape = (n, self.n_kv_head, int(width))
+        for name, t in (("prev", prev), ("out", out)):
+            if t is not None:
+                _need(t, name, torch.float32, q.device, shape)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        with _On(q) as stream:
+            kvs_q4_weights(self.pool, table, table.shape[1], lens, n, rows, hq, q, dt, stride,
+                           1.0 / math.sqrt(d) if scale is None else scale, lse, prev, out, shape[2], stream)
+        return out
+
+    def evict(self, table, dst_table, lens, weights, keep, sinks=0, recent=0):
+        """Keep the `keep` tokens of largest weight per sequence and kv head (kvs_q4_evict), compacted into dst_table's
+        pages: (kept int32 [n_seq][Hk][keep], new_lens, kept_weights)."""
+        import torch
+        dev = self.pages.device
+        _need(weights, "weights", torch.float32, dev, (None, self.n_kv_head, None))
+        n = weights.shape[0]
+        _need(table, "table", torch.int32, dev, (n, None))
+        _need(dst_table, "dst_table", torch.int32, dev, (n, None))
+        _need(lens, "lens", torch.int32, dev, (n,))
+        with _On(self.pages) as stream:
+            kept = torch.empty((n, self.n_kv_head, keep), dtype=torch.int32, device=dev)
+            new_w = torch.empty((n, self.n_kv_head, keep), dtype=torch.float32, device=dev)
+            new_lens = torch.empty((n,), dtype=torch.int32, device=dev)
+            kvs_q4_evict(self.pool, table, table.shape[1], dst_table, dst_table.shape[1], lens, n, weights,
+                         weights.shape[2], keep, sinks, recent, kept, new_w, new_lens, stream)
+        return kept, new_lens, new_w

@@ -71,8 +71,9 @@ typedef enum {
 
 /* Block types, numbered as the ggml type ids of the same formats. */
 typedef enum { KVS_TYPE_Q4_0 = 2, KVS_TYPE_Q8_0 = 8 } kvs_qtype;
-/* Query element types accepted by kvs_attend. */
-typedef enum { KVS_F32 = 0, KVS_F16 = 1 } kvs_dtype;
+/* Element types.  kvs_attend takes KVS_F32 and KVS_F16 queries; the batch
+ * operators (kvs_prompt_*, kvs_q4_*) state theirs. */
+typedef enum { KVS_F32 = 0, KVS_F16 = 1, KVS_BF16 = 2 } kvs_dtype;
 
 /* kvs_config.flags */
 #define KVS_FLAG_PLAN_ONLY 1u /* host scheduling only: no CUDA call is made, no
@@ -711,6 +712,190 @@ kvs_status kvs_attend_pages_noalloc(const void *pages_dev, uint64_t pages_bytes,
                                     const void *q_dev, int32_t q_dtype, uint32_t n_rows,
                                     uint32_t n_q_head, uint64_t pos0, float scale, float *out_dev,
                                     float *lse_dev, void *stream);
+
+/*
+ * Batch operators.  The calls below serve many sequences at once and have no
+ * context: attention over packed prompts whose K and V are still 16-bit rows
+ * (kvs_prompt_attend), a page cache held in 4 bits that such prompts and
+ * later tokens are written to and attended over (kvs_q4_*), and eviction from
+ * that cache by accumulated attention weight (kvs_prompt_weights and
+ * kvs_q4_weights collect the weights, kvs_q4_evict applies them).  (The pages
+ * describe no such calls.)
+ *
+ * Conventions:
+ *  - Every pointer marked "device" is device memory of the current device;
+ *    all work is enqueued on `stream` (a cudaStream_t of that device) and the
+ *    call returns at once.  Nothing is allocated, nothing is read back and no
+ *    state is kept between calls, so every call may be captured into a CUDA
+ *    graph; a replay reads the lengths, tables and slots found in device
+ *    memory then.  Calls on different streams may overlap unless they write
+ *    the same memory (a workspace counts: give each its own).
+ *  - Arguments that the host can see are checked before any work:
+ *    KVS_ERR_INVALID (null pointer, misaligned pointer or stride, unknown
+ *    type, bad count), KVS_ERR_UNSUPPORTED (geometry), KVS_ERR_CAPACITY
+ *    (workspace too small), KVS_ERR_CUDA (a launch failed); message:
+ *    kvs_last_error(NULL).
+ *  - Arguments only the device can see are bounded there: lengths and offsets
+ *    are clamped to the arrays they index, a row addressed to a slot outside
+ *    the pool is not written, and a page number outside the pool is never
+ *    dereferenced (each call says what comes out instead).
+ *  - A bounded device-side wait that gives up makes the outputs it would have
+ *    produced NaN.
+ *  - Query head h reads kv head h / (n_q_head / n_kv_head); head_dim D is 64,
+ *    128 or 256.  Row strides are in elements and may exceed heads x D (a
+ *    slice of a fused projection); the heads of one row are contiguous.  Rows
+ *    start on 16-byte boundaries (base address and stride).
+ *  - K and V rows are finite.  A non-finite value in a row reaches only the
+ *    outputs of query rows of the same sequence and kv head.
+ */
+
+/*
+ * A set of prompts packed one after another: the rows of prompt i are
+ * cu[i] .. cu[i+1] - 1 of q, k and v (cu: device int32 [n_seq + 1], ascending;
+ * prompts may be empty).  Rows outside cu[0] .. cu[n_seq] belong to no prompt.
+ */
+typedef struct {
+    const void *q;       /* device [total_rows][n_q_head][D] */
+    const void *k;       /* device [total_rows][n_kv_head][D] */
+    const void *v;       /* device [total_rows][n_kv_head][D] */
+    uint64_t q_stride, k_stride, v_stride; /* elements between rows, multiples of 8 */
+    const int32_t *cu;   /* device [n_seq + 1] */
+    uint32_t n_seq;      /* 1 .. 4096 */
+    uint32_t total_rows; /* rows of q, k and v, at most 2^31 - 1 - 256 */
+    uint32_t n_q_head, n_kv_head; /* n_q_head / n_kv_head at most 64 */
+    uint32_t head_dim;
+    int32_t dtype;       /* KVS_F16 or KVS_BF16: q, k, v and out */
+    float scale;         /* scores are scale * q . k; scale > 0 */
+} kvs_prompt;
+
+/*
+ * kvs_prompt_attend -- causal attention of every prompt over itself, before
+ * any of it is cached:
+ *   s_ij = scale q_i . k_j for j <= i in the same prompt,
+ *   lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j.
+ * out: device [total_rows][n_q_head][D] in dtype, rows out_stride apart; lse
+ * (nullable): device fp32 [total_rows][n_q_head].  Rows of no prompt are left
+ * as they were.  Products run on the tensor cores with fp32 accumulation, the
+ * softmax in fp32; the softmax weights are rounded to dtype before the second
+ * product.
+ */
+kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream);
+
+/*
+ * kvs_prompt_weights -- the attention weight each key of each prompt received:
+ *   w[i][g][j] = prev[i][g][j] + sum over rows r >= j and query heads h of kv
+ *                head g of exp(scale q_rh . k_jg - lse_rh)
+ * with j counted from the prompt's first row and, for last_rows > 0, only the
+ * prompt's last last_rows rows r (an observation window); 0: every row.  lse
+ * is kvs_prompt_attend's.  prev (nullable: zeros) and weights: device fp32
+ * [n_seq][n_kv_head][width]; keys beyond width are not counted, entries beyond
+ * a prompt's length are prev's.  prev may be weights.  Sums run in a fixed
+ * order.
+ */
+kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,
+                              float *weights, uint64_t width, void *stream);
+
+/*
+ * The 4-bit page cache.  K and V are both Q4_0 (32-dim blocks, fp16 scale, the
+ * codes kvs_append gives V), 9/16 byte per element.  Pages lie in one device
+ * buffer; slot s (int64) is token s % P of page s / P.
+ *
+ * Q4 page layout.  A page is Hk head sections of P*D*9/8 bytes; a section is
+ * P/32 tiles of 36*D bytes, one per 32 tokens.  With NB = D/32 blocks, for
+ * token t of the tile, block b and byte j (0..15) of the block (dims 32b + j
+ * in the low nibble, 32b + j + 16 in the high):
+ *   K codes  at ((u/4*32) + t%8*4 + j/4)*16 + u%4*4 + j%4, u = t/8*NB + b
+ *   V codes  at 18*D + ((w/4*32) + j%8*4 + t%16/4)*16 + w%4*4 + t%2*2 + j/8,
+ *            w = (t/16*NB + b)*2 + t%4/2
+ *   K scales at 16*D, fp16 number ((t/16*8 + t%8)*NB + b)*2 + t/8%2
+ *   V scales at 34*D, fp16 number (t/4*NB + b)*4 + t%4
+ * Value = (nibble - 8) * scale.  One 16-byte load per lane feeds a tensor-core
+ * fragment, a tile is one bulk copy, and no byte holds two tokens.
+ */
+typedef struct {
+    void *pages;          /* device, 16-byte aligned */
+    uint64_t n_pages;     /* at most 2^31 - 1 */
+    uint32_t page_tokens; /* P: 32, 64, 128 or 256 */
+    uint32_t n_kv_head;
+    uint32_t head_dim;
+} kvs_q4_pool;
+
+/* kvs_q4_query_sizes -- bytes of one page (Hk * P * D * 9/8) and the workspace
+ * kvs_q4_attend needs for n_rows query rows of n_q_head heads in dtype (it
+ * does not depend on the lengths).  pool->pages may be null.  Either output
+ * may be NULL. */
+kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_rows, uint32_t n_q_head, int32_t dtype,
+                              uint64_t *page_bytes, uint64_t *workspace_bytes);
+
+/*
+ * kvs_q4_append -- encode n rows of K and V (device [n][Hk][D], dtype KVS_F32,
+ * KVS_F16 or KVS_BF16, rows k_stride / v_stride elements apart) into the
+ * slots slots[i] (device int64).  A slot outside the pool (a negative one
+ * marks padding) is skipped.  The slots of one call are distinct; a slot named
+ * twice holds parts of either row.
+ */
+kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, const void *k, const void *v,
+                         int32_t dtype, uint64_t k_stride, uint64_t v_stride, void *stream);
+
+/* kvs_q4_read -- the values held in slots[i] (device int64): k and v (device
+ * [n][Hk][D], either may be NULL) in dtype KVS_F32 (exact), KVS_F16 or
+ * KVS_BF16 (rounded once).  Rows of slots outside the pool are zero. */
+kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, void *k, void *v, int32_t dtype,
+                       void *stream);
+
+/*
+ * kvs_q4_attend -- attention of n_rows query rows of each of n_seq sequences
+ * over their cached tokens.  table: device int32 [n_seq][table_width], page
+ * numbers in order; lens: device int32 [n_seq], cached tokens T including the
+ * rows' own.  q: device [n_seq][n_rows][n_q_head][D] (KVS_F32, KVS_F16 or
+ * KVS_BF16), rows q_stride elements apart; row r sees tokens 0 .. T - n_rows +
+ * r.  out: device, contiguous, in the type of q; lse (nullable): device fp32
+ * [n_seq][n_rows][n_q_head].  A row that sees nothing (T = 0: a padding
+ * sequence) gets out 0 and lse -inf.  A page number outside the pool within
+ * T makes the sequence's outputs NaN.  T is clamped to table_width * P.
+ * Queries of 16-bit types and the weights of their second product enter the
+ * tensor cores as single f16 values (exact for such queries up to 2^-28 of
+ * a row's largest element), KVS_F32 ones as hi + lo pairs; sums are fp32.
+ * n_rows * (n_q_head / n_kv_head) at most 64, n_seq at most 4096.
+ */
+kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                         uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                         uint64_t q_stride, float scale, void *out, float *lse, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
+
+/*
+ * kvs_q4_weights -- the attention weight each cached token received from those
+ * rows: w[i][g][t] = prev[i][g][t] + sum over rows r that see t and query
+ * heads h of kv head g of exp(scale q_irh . k_tg - lse_irh), with
+ * kvs_q4_attend's lse.  prev (nullable: zeros) and weights: device fp32
+ * [n_seq][Hk][width]; tokens beyond width are not counted, entries beyond T
+ * are prev's; prev may be weights.  Reads only K.  Tokens of a page outside
+ * the pool become NaN.
+ */
+kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                          uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                          uint64_t q_stride, float scale, const float *lse, const float *prev, float *weights,
+                          uint64_t width, void *stream);
+
+/*
+ * kvs_q4_evict -- cut every sequence back to `keep` tokens per kv head.  Of a
+ * sequence with T > keep, the first `sinks` and last `recent` tokens stay
+ * (sinks + recent <= keep) and, of the others, those of largest weights[i][g][t]
+ * (equal ones: the lowest t; NaN below every number); with T <= keep all stay.
+ * The tokens that stay are copied in their order to tokens 0 .. of dst_table's
+ * pages.  weights: device fp32 [n_seq][Hk][width], T clamped to width and to
+ * table_width * P.  Outputs: kept (device int32 [n_seq][Hk][keep], ascending,
+ * -1 past the count), kept_weights (nullable, device fp32 [n_seq][Hk][keep],
+ * 0 past the count), new_lens (device int32 [n_seq], min(T, keep)).
+ * dst_width * P >= keep.  The pages of dst_table are no pages of table, except
+ * that a sequence with T <= keep may name its own again; kept_weights is not
+ * weights, and new_lens is not lens.  A token whose destination page lies
+ * outside the pool is not copied; one from outside the pool becomes zeros.
+ */
+kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width,
+                        const int32_t *dst_table, uint32_t dst_width, const int32_t *lens, uint32_t n_seq,
+                        const float *weights, uint64_t width, uint32_t keep, uint32_t sinks, uint32_t recent,
+                        int32_t *kept, float *kept_weights, int32_t *new_lens, void *stream);
 
 #ifdef __cplusplus
 }
