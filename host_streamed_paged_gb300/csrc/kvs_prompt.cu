@@ -47,8 +47,33 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     *abort = 1;
     return false;
 }
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// a warp's bounded wait until ready() holds in every lane.  A poll's answer takes some 150 clocks even when the
+// phase is complete, so several barriers are polled in one ready(), one after the other without waiting in between.
+template <typename F>
+__device__ __forceinline__ bool wait_warp(volatile int *abort, F ready) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (__all_sync(0xffffffffu, ready())) return true;
+        if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort)) return false;
+    }
+    *abort = 1;
+    return false;
+}
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    return wait_warp(abort, [&] { return mbar_done(bar, parity); });
+}
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -179,65 +204,113 @@ __device__ __forceinline__ int cu_end(const PromptParams &p, int s) {
     return b < a ? a : (b < p.total ? b : p.total);
 }
 
-// The unit-th group of `per` tokens over all prompts: prompt s, group x of it
-// (place = {s, x, begin, end}; s < 0 past the last).  Every thread calls it;
-// `place` and `sums` are in shared memory.
-__device__ void find_unit(const PromptParams &p, int64_t unit, int per, int *place, int64_t *sums) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-    const int each = (p.n_seq + nt - 1) / nt;
-    int64_t mine = 0;
-    for (int k = 0; k < each; ++k) {
-        const int s = tid * each + k;
-        if (s < p.n_seq) mine += (cu_end(p, s) - cu_begin(p, s) + per - 1) / per;
-    }
-    int64_t inc = mine;
+// Where unit `c` of the launch lies: prompt s, group x of its `per`-token groups
+// counted so that a larger x is more work (place = {s, x, begin, end, groups};
+// s < 0 past the last).  Units go out heaviest first over all prompts, since a
+// causal tile's work grows with x and a heavy one begun late would run alone
+// at the end: level by level from the longest prompt's last group down.  (Up
+// to 256 prompts, which a warp holds in registers; of more prompts each is a
+// small part of the launch and they go one after another.)  Called by a warp.
+constexpr int kSortedSeq = 256;
+__device__ void find_unit(const PromptParams &p, int64_t c, int per, int *place) {
+    const int lane = threadIdx.x & 31;
+    auto groups = [&](int s) { return s < p.n_seq ? (cu_end(p, s) - cu_begin(p, s) + per - 1) / per : 0; };
+    int s = -1, x = 0;
+    if (p.n_seq <= kSortedSeq) {
+        constexpr int kEach = kSortedSeq / 32;
+        int t[kEach], most = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) sums[warp] = inc;
-    if (tid == 0) place[0] = -1;
-    __syncthreads();
-    int64_t base = inc - mine;
-    for (int w = 0; w < warp; ++w) base += sums[w];
-    if (unit >= base && unit < base + mine) {
-        for (int k = 0; k < each; ++k) {
-            const int s = tid * each + k;
-            if (s >= p.n_seq) break;
-            const int a = cu_begin(p, s), b = cu_end(p, s), n = (b - a + per - 1) / per;
-            if (unit < base + n) {
-                place[0] = s;
-                place[1] = (int)(unit - base);
-                place[2] = a;
-                place[3] = b;
-                break;
+        for (int i = 0; i < kEach; ++i) {
+            t[i] = 32 * i < p.n_seq ? groups(32 * i + lane) : 0;
+            most = max(most, t[i]);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        auto from = [&](int level) {  // units at this level or above (per prompt max(0, t - level))
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) n += max(0, t[i] - level);
+            return (int64_t)__reduce_add_sync(0xffffffffu, n);
+        };
+        if (c < from(0)) {
+            int lo = 0, hi = most - 1;  // the largest level with c < from(level)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (c < from(mid)) lo = mid;
+                else hi = mid - 1;
             }
-            base += n;
+            x = lo;
+            int nth = (int)(c - from(lo + 1));  // among the prompts with a group at this level
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const uint32_t has = __ballot_sync(0xffffffffu, t[i] > x);
+                if (s < 0 && nth < __popc(has)) {
+                    uint32_t rest = has;
+                    for (; nth > 0; --nth) rest &= rest - 1;
+                    s = 32 * i + __ffs(rest) - 1;
+                }
+                if (s < 0) nth -= __popc(has);
+            }
+        }
+    } else {
+        int64_t base = 0;
+        for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
+            const int t = groups(s0 + lane);
+            int inc = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, base + inc > c);
+            if (past) {
+                const int who = __ffs(past) - 1;
+                s = s0 + who;
+                x = (int)(__shfl_sync(0xffffffffu, base + inc, who) - 1 - c);
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
-    __syncthreads();
+    if (lane == 0) {
+        place[0] = s;
+        if (s >= 0) {
+            place[1] = x;
+            place[2] = cu_begin(p, s);
+            place[3] = cu_end(p, s);
+            place[4] = groups(s);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- attention
 // Per CTA and kv head: two 128-row query tiles (D <= 128) or one (D = 256: its
 // O takes the tensor memory of two) against the prompt's key blocks.
-//   warp 9 loads Q, then K_j, V_j through a ring of block-sized stages (TMA);
-//   warp 8 issues S = Q K^T into tensor memory and O += P V, P as the
-//     tensor-memory A operand over S's columns; the two tiles (or the two score
-//     buffers of one) alternate, so one's softmax runs under the other's MMAs;
+//   warp 9 loads Q, then K and V through a ring (TMA);
+//   warp 8 + 2 i issues tile i's S = Q K^T into tensor memory and O += P V, P as
+//     the tensor-memory A operand over S's columns (one issuing warp per tile:
+//     a warp's MMAs leave it only as the pipe takes them, and it then needs
+//     200 clocks to see the next barrier; two warps fill each other's gaps);
 //   each softmax warpgroup (one thread per row) turns its tile's S into P and
 //     rescales O only when a row's maximum grew by more than 2^8.
+// Each tile has two score buffers and its S runs two blocks ahead, so that a
+// warpgroup finds the next scores ready when it is done with the last and the
+// tensor pipe never waits for a softmax.  Tensor memory (512 columns) then
+// allows blocks of 64 keys for two tiles, and 128 for the one of D = 256.  An
+// S MMA of N = 64 takes 50 clocks for 2/3 of the work of one of N = 128 (66
+// clocks: it reads its A tile from shared memory anew), which costs less than
+// the one 128-key buffer per tile that would fit: its softmax waits for its
+// own P V and Q K^T each time.
 template <int D>
 struct AttendShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;
-    static constexpr int BN = D <= 128 ? 128 : 64;
+    static constexpr int BN = D <= 128 ? 64 : 128;
     static constexpr int kQBytes = kTileRows * D * 2;
-    static constexpr int kBlock = BN * D * 2;
-    static constexpr int kStages = D == 64 ? 6 : 5;
+    static constexpr int kPieces = D == 256 ? 4 : 1;  // ring stages of a block: K by 64 dims (D = 256), V by keys
+    static constexpr int kPiece = BN * D * 2 / kPieces;
+    static constexpr int kVKeys = BN / kPieces;       // keys of a V piece
+    static constexpr int kStages = D == 64 ? 12 : 10;
     static constexpr int kOffRing = NQ * kQBytes;
-    static constexpr int kOffBar = kOffRing + kStages * kBlock;
-    static constexpr int kSmem = kOffBar + 256 + 128 + 1024;
+    static constexpr int kOffBar = kOffRing + kStages * kPiece;
+    static constexpr int kSmem = kOffBar + 512 + 1024;
     static constexpr uint32_t kColO = 256;
 };
 
@@ -249,24 +322,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NQ = S::NQ, BN = S::BN, NST = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = smem_u32(smem + S::kOffBar);
-    // barriers: ring full / empty, Q full, S full (2), P full (2), O done (2 x parity), final
+    // barriers: ring full / empty, Q full, final; per tile and score buffer: S full, P full, O done (by the same parity)
     auto b_full = [&](int s) { return bars + 8u * s; };
-    auto b_empty = [&](int s) { return bars + 8u * (6 + s); };
-    const uint32_t b_q = bars + 8u * 12, b_final = bars + 8u * 13;
-    auto b_s = [&](int i) { return bars + 8u * (14 + i); };
-    auto b_p = [&](int i) { return bars + 8u * (16 + i); };
-    auto b_o = [&](int i, int par) { return bars + 8u * (18 + 2 * i + par); };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
-    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
-    int64_t *sums = reinterpret_cast<int64_t *>(smem + S::kOffBar + 256);
+    auto b_empty = [&](int s) { return bars + 8u * (12 + s); };
+    const uint32_t b_q = bars + 8u * 24, b_final = bars + 8u * 25;
+    auto b_s = [&](int i, int buf) { return bars + 8u * (26 + 2 * i + buf); };
+    auto b_p = [&](int i, int buf) { return bars + 8u * (30 + 2 * i + buf); };
+    auto b_o = [&](int i, int buf) { return bars + 8u * (34 + 2 * i + buf); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 38);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 39);
+    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 40);
 
     const int G = p.G, TQ = kTileRows / G;
     const int head = blockIdx.x % p.Hk;
-    const int64_t n_units = gridDim.x / p.Hk;
-    find_unit(p, n_units - 1 - blockIdx.x / p.Hk, NQ * TQ, place, sums);
+    if (warp == 0) find_unit(p, blockIdx.x / p.Hk, NQ * TQ, place);
+    if (tid == 32) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(b_full(s), 1);
+            mbar_init(b_empty(s), NQ);
+        }
+        mbar_init(b_q, 1);
+        mbar_init(b_final, NQ);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(b_s(0, i), 1);
+            mbar_init(b_p(0, i), 4);
+            mbar_init(b_o(0, i), 1);
+        }
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     if (place[0] < 0) return;
     const int begin = place[2], L = place[3] - begin;
     const int t0 = place[1] * NQ * TQ;  // first token of tile 0, within the prompt
@@ -277,62 +364,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         nblk[i] = a < L ? last / BN + 1 : 0;
         n_max = nblk[i] > n_max ? nblk[i] : n_max;
     }
-
-    if (tid == 0) {
-        for (int s = 0; s < NST; ++s) {
-            mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), 1);
-        }
-        mbar_init(b_q, 1);
-        mbar_init(b_final, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(b_s(i), 1);
-            mbar_init(b_p(i), 4);
-            mbar_init(b_o(i, 0), 1);
-            mbar_init(b_o(i, 1), 1);
-        }
-        *abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // the ring's blocks in the order the MMAs take them: K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
+    // kPieces stages each
+    const int n_ring = 2 * n_max * S::kPieces;
+    auto ring_k = [&](int j) { return (j < 2 ? j : 2 * j - 1) * S::kPieces; };
+    auto ring_v = [&](int j) { return (j == n_max - 1 ? 2 * n_max - 1 : 2 * j + 2) * S::kPieces; };
+    auto load_piece = [&](int r) {
+        const int st = r % NST, q = r / S::kPieces, c = r % S::kPieces, end = 2 * n_max - 1;
+        const bool is_v = q == end || (q >= 2 && !(q & 1));
+        const int j = q == end ? n_max - 1 : (q < 2 ? q : (q & 1 ? (q + 1) / 2 : q / 2 - 1));
+        const uint32_t dst = smem_u32(smem + S::kOffRing + st * S::kPiece);
+        mbar_expect(b_full(st), (uint32_t)S::kPiece);
+        if (is_v) {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+                tma_load(dst + x * S::kVKeys * 128, &mv, b_full(st), x * 64, head, begin + j * BN + c * S::kVKeys);
+        } else {
+#pragma unroll
+            for (int x = 0; x < D / 64 / S::kPieces; ++x)
+                tma_load(dst + x * BN * 128, &mk, b_full(st), (c + x) * 64, head, begin + j * BN);
+        }
+    };
+    int preloaded = 0;
+    if (warp == 9) {  // the first loads run under the tensor-memory allocation
+        preloaded = n_ring < NST ? n_ring : NST;
+        if (lane == 0) {
+            mbar_expect(b_q, (uint32_t)(NQ * (D / 64) * 128 * G * TQ));
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
+            for (int r = 0; r < preloaded; ++r) load_piece(r);
+        }
     }
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = *tmem_slot;
-    // ring order: K_0, then (D <= 128) V_0, K_1, V_1, ... or (D = 256, scores one block ahead) K_1, V_0, K_2, V_1, ...
-    auto ring_k = [&](int j) { return NQ == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
-    auto ring_v = [&](int j) { return NQ == 2 ? 2 * j + 1 : (j == n_max - 1 ? 2 * j + 1 : 2 * j + 2); };
 
     if (warp == 9) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            constexpr int kChunks = D / 64;
-            mbar_expect(b_q, (uint32_t)(NQ * kChunks * 128 * G * TQ));
-            for (int i = 0; i < NQ; ++i)
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
-            const int n = 2 * n_max;
-            int issued = 0;
-            for (int r = 0; r < n; ++r) {
-                const int st = r % NST, use = r / NST;
-                if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort)) break;
-                // the r-th block of the ring
-                bool is_v;
-                int j;
-                if (NQ == 2) {
-                    is_v = r & 1;
-                    j = r >> 1;
-                } else {
-                    is_v = r == n - 1 || (r >= 2 && !(r & 1));
-                    j = r == 0 ? 0 : (r == n - 1 ? n_max - 1 : (r & 1 ? (r + 1) / 2 : r / 2 - 1));
-                }
-                mbar_expect(b_full(st), (uint32_t)S::kBlock);
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(smem_u32(smem + S::kOffRing + st * S::kBlock + c * BN * 128), is_v ? &mv : &mk, b_full(st), c * 64,
-                             head, begin + j * BN);
+            int issued = preloaded;
+            for (int r = preloaded; r < n_ring; ++r) {
+                if (!mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort)) break;
+                load_piece(r);
                 issued = r + 1;
             }
             if (*abort) {  // copies in flight still land in this CTA's shared memory
@@ -342,71 +422,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
             }
         }
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            const uint32_t id_s = idesc(BF16, kTileRows, BN, false), id_o = idesc(BF16, kTileRows, D, true);
-            const uint32_t sq = smem_u32(smem), sr = smem_u32(smem + S::kOffRing);
-            bool ok = mbar_wait(b_q, 0, abort);
-            auto wait_ring = [&](int r) { return mbar_wait(b_full(r % NST), (uint32_t)((r / NST) & 1), abort); };
-            auto issue_s = [&](int i, int buf, int r) {
-                const uint64_t da = smem_desc(sq + (uint32_t)(i * S::kQBytes), 16), db = smem_desc(sr + (uint32_t)(r % NST * S::kBlock), 16);
+    } else if (warp == 8 || (NQ == 2 && warp == 10)) {
+        const int i = (warp - 8) >> 1, n = nblk[i];
+        // ------------------------------------------------------------ MMA issue (the warp in step, one elected lane issues)
+        constexpr uint32_t id_s = idesc(BF16, kTileRows, BN, false), id_o = idesc(BF16, kTileRows, D, true);
+        constexpr int NP = S::kPieces;
+        const bool one = elect_one();
+        const uint64_t dq = smem_desc(smem_u32(smem), 16), dk = smem_desc(smem_u32(smem + S::kOffRing), 16);
+        const uint64_t dv = smem_desc(smem_u32(smem + S::kOffRing), S::kVKeys * 128);
+        auto stage = [&](int r, int c) { return (r + c) % NST; };
+        auto loaded = [&](int r) {  // a block's pieces
+            bool all = true;
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t oa = (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4);
-                    const uint64_t ob = (uint64_t)(((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4);
-                    mma_ss(tmem + (uint32_t)(buf * BN), da + oa, db + ob, id_s, s > 0);
-                }
-                mma_commit(b_s(buf));
-            };
-            auto issue_o = [&](int i, int buf, int r, int j) {
-                const uint64_t db = smem_desc(sr + (uint32_t)(r % NST * S::kBlock), BN * 128);
+            for (int c = 0; c < NP; ++c) all &= mbar_done(b_full(stage(r, c)), (uint32_t)(((r + c) / NST) & 1));
+            return all;
+        };
+        auto freed = [&](int r) {
 #pragma unroll
-                for (int s = 0; s < BN / 16; ++s)
-                    mma_ts(tmem + S::kColO + (uint32_t)(i * D), tmem + (uint32_t)(buf * BN + 8 * s), db + (uint64_t)(s * 2048 >> 4),
-                           id_o, (j > 0 || s > 0) ? 1u : 0u);
-                mma_commit(b_o(i, j & 1));
-            };
-            if (NQ == 2) {
-                for (int j = 0; j <= n_max && ok; ++j) {
-                    if (j >= 1) ok = wait_ring(ring_v(j - 1));
-                    if (ok && j < n_max) ok = wait_ring(ring_k(j));
-                    if (!ok) break;
-                    tc_after();
+            for (int c = 0; c < NP; ++c) mma_commit(b_empty(stage(r, c)));
+        };
+        auto issue_s = [&](int j) {
+            const uint32_t d = tmem + (uint32_t)((2 * i + (j & 1)) * BN);
+            const uint64_t da = dq + (uint64_t)(i * S::kQBytes >> 4);
+            const int r = ring_k(j);
 #pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        if (j >= 1 && j - 1 < nblk[i]) {
-                            ok = ok && mbar_wait(b_p(i), (uint32_t)((j - 1) & 1), abort);
-                            if (!ok) break;
-                            tc_after();
-                            issue_o(i, i, ring_v(j - 1), j - 1);
-                        }
-                        if (j < nblk[i]) issue_s(i, i, ring_k(j));
-                    }
-                    if (!ok) break;
-                    if (j >= 1) mma_commit(b_empty(ring_v(j - 1) % NST));
-                    if (j < n_max) mma_commit(b_empty(ring_k(j) % NST));
-                }
-            } else {
-                for (int j = 0; j <= n_max && ok; ++j) {
-                    if (j < n_max) {
-                        ok = wait_ring(ring_k(j));
-                        if (!ok) break;
-                        tc_after();
-                        issue_s(0, j & 1, ring_k(j));
-                        mma_commit(b_empty(ring_k(j) % NST));
-                    }
-                    if (j >= 1) {
-                        ok = wait_ring(ring_v(j - 1)) && mbar_wait(b_p((j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
-                        if (!ok) break;
-                        tc_after();
-                        issue_o(0, (j - 1) & 1, ring_v(j - 1), j - 1);
-                        mma_commit(b_empty(ring_v(j - 1) % NST));
-                    }
-                }
+            for (int s = 0; s < D / 16; ++s) {
+                constexpr int kPer = D / 16 / NP;  // 16-dim steps of a piece
+                const uint64_t db = dk + (uint64_t)((stage(r, s / kPer) * S::kPiece + (s % kPer >> 2) * (BN * 128) + (s & 3) * 32) >> 4);
+                mma_ss(d, da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4), db, id_s, s > 0);
             }
-            mma_commit(b_final);  // on every path: tensor memory is freed only after it
+            mma_commit(b_s(i, j & 1));
+        };
+        auto issue_o = [&](int j) {
+            const uint32_t d = tmem + S::kColO + (uint32_t)(i * D), a = tmem + (uint32_t)((2 * i + (j & 1)) * BN);
+            const int r = ring_v(j);
+#pragma unroll
+            for (int s = 0; s < BN / 16; ++s) {
+                constexpr int kPer = BN / 16 / NP;  // 16-key steps of a piece
+                const uint64_t db = dv + (uint64_t)((stage(r, s / kPer) * S::kPiece + s % kPer * 2048) >> 4);
+                mma_ts(d, a + (uint32_t)(8 * s), db, id_o, (j > 0 || s > 0) ? 1u : 0u);
+            }
+            mma_commit(b_o(i, j & 1));
+        };
+        // a block past this tile's last one is freed as it comes, for the other tile's sake
+        bool ok = true;
+        for (int j = 0; j < 2 && j < n_max && ok; ++j) {
+            ok = wait_warp(abort, [&] { return mbar_done(b_q, 0) & loaded(ring_k(j)); });
+            if (!ok) break;
+            tc_after();
+            if (one) {
+                if (j < n) issue_s(j);
+                freed(ring_k(j));
+            }
         }
+        // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
+        for (int j = 0; j < n_max && ok; ++j) {
+            const bool more = j + 2 < n_max;
+            ok = wait_warp(abort, [&] {
+                bool all = loaded(ring_v(j));
+                if (j < n) all &= mbar_done(b_p(i, j & 1), (uint32_t)((j >> 1) & 1));
+                if (more) all &= loaded(ring_k(j + 2));
+                return all;
+            });
+            if (!ok) break;
+            tc_after();
+            if (one) {
+                if (j < n) issue_o(j);
+                freed(ring_v(j));
+                if (j + 2 < n) issue_s(j + 2);
+                if (more) freed(ring_k(j + 2));
+            }
+        }
+        if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
     } else if (warp < 4 * NQ) {
         // ------------------------------------------------------------ softmax, one thread per row
         const int i = warp >> 2, row = tid & 127, n = nblk[i];
@@ -419,12 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const int first_tok = t0 + i * TQ;
         for (int j = 0; j < n; ++j) {
-            const int buf = NQ == 2 ? i : (j & 1);
-            const uint32_t par = NQ == 2 ? (uint32_t)(j & 1) : (uint32_t)((j >> 1) & 1);
-            ok = mbar_wait_warp(b_s(buf), par, abort);
+            const int buf = j & 1;
+            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((j >> 1) & 1), abort);
             if (!ok) break;
             tc_after();
-            const uint32_t ts = lanes + (uint32_t)(buf * BN);
+            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
             uint32_t sr[BN];
 #pragma unroll
             for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, sr + c);
@@ -438,73 +524,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < BN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
-            bool grow = false;
-            float alpha = 1.f;
-            if (mx > m + 8.f || (m == -INFINITY && mx != -INFINITY)) {
-                alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+            const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sc;
+            const bool grow = mx > m + 8.f || (m == -INFINITY && mx != -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float to = grow ? mx : m;
+                const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
                 l2.x *= alpha;
                 l2.y *= alpha;
-                m = mx;
-                grow = true;
+                m = to;
+                if (j > 0) {
+                    ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
+                    if (!ok) break;
+                    tc_after();
+                    const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(to_o + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                        tmem_st32(to_o + c, v);
+                    }
+                }
             }
             const float neg = m == -INFINITY ? 0.f : -m;
             const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
-            uint32_t pk[BN / 2];
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int half = 0; half < BN / 64; ++half) {
+            for (int part = 0; part < BN / 64; ++part) {
+                uint32_t pk[32];
 #pragma unroll
-                for (int c = half * 64; c < half * 64 + 64; c += 2) {
-                    const float2 y = fma2(make_float2(s[c], s[c + 1]), sc2, neg2);
+                for (int c = 0; c < 64; c += 2) {
+                    const float2 y = fma2(make_float2(s[64 * part + c], s[64 * part + c + 1]), sc2, neg2);
                     const float2 e = make_float2(ex2(y.x), ex2(y.y));
                     sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
                     pk[c / 2] = pack<BF16>(e.x, e.y);
                 }
-                tmem_st32(ts + 32 * half, pk + 32 * half);
+                tmem_st32(ts + 32 * part, pk);
             }
             l2 = add2(l2, add2(sum[0], sum[1]));
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
-                if (!ok) {
-                    tmem_wait_st();
-                    break;
-                }
-                tc_after();
-                const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(to + c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-                    tmem_st32(to + c, v);
-                }
-            }
             if ((j + 1) * BN > L) {
                 // the block reaches past the prompt: its last rows are another prompt's (or nobody's), and a weight
                 // of zero times what stands there must be zero
-                const int r = ring_v(j), st = r % NST;
-                ok = mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
-                if (!ok) {
-                    tmem_wait_st();
-                    break;
-                }
-                if (row < BN && j * BN + row >= L) {
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
+                for (int c = 0; c < S::kPieces; ++c) {
+                    const int r = ring_v(j) + c, st = r % NST;
+                    ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
+                    if (ok && row < S::kVKeys && j * BN + c * S::kVKeys + row >= L) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4 *>(smem + S::kOffRing + st * S::kBlock + c * BN * 128 + row * 128 + k * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                *reinterpret_cast<uint4 *>(smem + S::kOffRing + st * S::kPiece + (x * S::kVKeys + row) * 128 + k * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    }
                 }
                 proxy_fence();
             }
             tmem_wait_st();
+            if (!ok) break;
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_p(buf));
+            if (lane == 0) mbar_arrive(b_p(i, buf));
         }
         if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), abort);
         if (n > 0) {
@@ -559,7 +641,7 @@ struct WeightShape {
     static constexpr int kOffRing = 2 * kKBytes;
     static constexpr int kOffLse = kOffRing + kStages * kBlock;
     static constexpr int kOffBar = kOffLse + 2 * 2 * BQ * 4;
-    static constexpr int kSmem = kOffBar + 256 + 128 + 1024;
+    static constexpr int kSmem = kOffBar + 256 + 1024;
 };
 
 template <int D, bool BF16>
@@ -570,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int BQ = S::BQ, NST = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = smem_u32(smem + S::kOffBar);
     auto b_full = [&](int s) { return bars + 8u * s; };
     auto b_empty = [&](int s) { return bars + 8u * (4 + s); };
@@ -580,14 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
     int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
-    int64_t *sums = reinterpret_cast<int64_t *>(smem + S::kOffBar + 256);
 
     const int G = p.G, TQ = BQ / G;
     const int head = blockIdx.x % p.Hk;
-    find_unit(p, blockIdx.x / p.Hk, 2 * kTileRows, place, sums);
+    if (warp == 0) find_unit(p, blockIdx.x / p.Hk, 2 * kTileRows, place);
+    __syncthreads();
     if (place[0] < 0) return;
     const int seq = place[0], begin = place[2], L = place[3] - begin;
-    const int k0 = place[1] * 2 * kTileRows;
+    const int k0 = (place[4] - 1 - place[1]) * 2 * kTileRows;  // the first keys are seen by the most rows
     int start = p.last_rows > 0 && L > p.last_rows ? L - p.last_rows : 0;  // first query token counted
     if (start < k0) start = k0;
     const int ntile = (L - start + TQ - 1) / TQ;
@@ -596,10 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), 1);
+            mbar_init(b_empty(s), second ? 2 : 1);
         }
         mbar_init(b_k, 1);
-        mbar_init(b_final, 1);
+        mbar_init(b_final, second ? 2 : 1);
         for (int i = 0; i < 2; ++i)
             for (int b = 0; b < 2; ++b) {
                 mbar_init(b_s(i, b), 1);
@@ -647,32 +729,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
             }
         }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            const uint32_t id = idesc(BF16, kTileRows, BQ, false);
-            const uint32_t sk = smem_u32(smem), sr = smem_u32(smem + S::kOffRing);
-            bool ok = mbar_wait(b_k, 0, abort);
-            for (int r = 0; r < ntile && ok; ++r) {
-                const int st = r % NST, buf = r & 1;
-                ok = mbar_wait(b_full(st), (uint32_t)((r / NST) & 1), abort);
-                if (!ok) break;
-                for (int i = 0; i < (second ? 2 : 1); ++i) {
-                    if (r >= 2) ok = mbar_wait(b_read(i, buf), (uint32_t)(((r - 2) >> 1) & 1), abort);
-                    if (!ok) break;
-                    tc_after();
-                    const uint64_t da = smem_desc(sk + (uint32_t)(i * S::kKBytes), 16), db = smem_desc(sr + (uint32_t)(st * S::kBlock), 16);
+    } else if (warp == 8 || (warp == 10 && second)) {  // one issuing warp per key tile
+        const int i = (warp - 8) >> 1;
+        constexpr uint32_t id = idesc(BF16, kTileRows, BQ, false);
+        const bool one = elect_one();
+        const uint64_t da = smem_desc(smem_u32(smem + i * S::kKBytes), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
+        bool ok = mbar_wait_warp(b_k, 0, abort);
+        for (int r = 0; r < ntile && ok; ++r) {
+            const int st = r % NST, buf = r & 1;
+            ok = wait_warp(abort, [&] {
+                bool all = mbar_done(b_full(st), (uint32_t)((r / NST) & 1));
+                if (r >= 2) all &= mbar_done(b_read(i, buf), (uint32_t)(((r - 2) >> 1) & 1));
+                return all;
+            });
+            if (!ok) break;
+            tc_after();
+            if (one) {
+                const uint64_t db = dq + (uint64_t)(st * S::kBlock >> 4);
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint64_t oa = (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4);
-                        const uint64_t ob = (uint64_t)(((s >> 2) * (BQ * 128) + (s & 3) * 32) >> 4);
-                        mma_ss(tmem + (uint32_t)((2 * i + buf) * BQ), da + oa, db + ob, id, s > 0);
-                    }
-                    mma_commit(b_s(i, buf));
-                }
+                for (int s = 0; s < D / 16; ++s)
+                    mma_ss(tmem + (uint32_t)((2 * i + buf) * BQ), da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4),
+                           db + (uint64_t)(((s >> 2) * (BQ * 128) + (s & 3) * 32) >> 4), id, s > 0);
+                mma_commit(b_s(i, buf));
                 mma_commit(b_empty(st));
             }
-            mma_commit(b_final);
         }
+        if (one) mma_commit(b_final);
     } else if (warp < 8 && (warp < 4 || second)) {
         const int i = warp >> 2, row = tid & 127;
         const int key = k0 + i * kTileRows + row;
@@ -702,8 +784,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok0 = start + r * TQ;
             // columns this key counts: rows of tokens from the key on, and none past the prompt
             const bool edge = tok0 < k0 + (i + 1) * kTileRows - 1 || tok0 + TQ > L;
-            int c_lo = (key - tok0) * G, c_hi = (L - tok0) * G;
-            if (c_hi > TQ * G) c_hi = TQ * G;
             const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ);
             uint32_t sr[BQ];
 #pragma unroll
@@ -715,19 +795,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *s = reinterpret_cast<const float *>(sr);
             const float4 *z4 = reinterpret_cast<const float4 *>(sl + buf * BQ);
             const float2 sc2 = make_float2(sc, sc);
+            if (!edge) {
 #pragma unroll
-            for (int c = 0; c < BQ; c += 4) {
-                const float4 z = z4[c / 4];
-                float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z.x, z.y));
-                float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z.z, z.w));
-                if (edge) {
-                    a.x = c >= c_lo && c < c_hi ? a.x : -INFINITY;
-                    a.y = c + 1 >= c_lo && c + 1 < c_hi ? a.y : -INFINITY;
-                    b.x = c + 2 >= c_lo && c + 2 < c_hi ? b.x : -INFINITY;
-                    b.y = c + 3 >= c_lo && c + 3 < c_hi ? b.y : -INFINITY;
+                for (int c = 0; c < BQ; c += 4) {
+                    const float4 z = z4[c / 4];
+                    const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z.x, z.y));
+                    const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z.z, z.w));
+                    sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
+                    sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
                 }
-                sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
-                sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+            } else {
+                const int c_lo = (key - tok0) * G;
+                const int c_hi = (L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G;
+#pragma unroll
+                for (int c = 0; c < BQ; ++c) {
+                    const float e = ex2(fmaf(s[c], sc, sl[buf * BQ + c]));
+                    sum[c & 1].x += c >= c_lo && c < c_hi ? e : 0.f;
+                }
             }
         }
         if (key < L && key < p.width) {
@@ -847,7 +931,7 @@ kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t 
     CUtensorMap mq, mk, mv;
     kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, TQ);
     if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, S::BN);
-    if (r == KVS_OK) r = make_map(&mv, p->v, bf, p->total_rows, p->n_kv_head, D, p->v_stride, 1, S::BN);
+    if (r == KVS_OK) r = make_map(&mv, p->v, bf, p->total_rows, p->n_kv_head, D, p->v_stride, 1, S::kVKeys);
     if (r != KVS_OK) return r;
     const uint64_t units = (uint64_t)p->total_rows / (S::NQ * TQ) + p->n_seq;  // at least the prompts' tile groups
     if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");

@@ -249,61 +249,89 @@ __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, in
     return n < 0 ? 0 : (int)(n < cap ? n : cap);
 }
 
-// prefix[s] = tiles of one head of sequences 0 .. s-1; every thread of the CTA calls it
-__device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_width, int n_seq, int *prefix) {
-    __shared__ int warp_sum[32];
+// prefix[s] = {tiles of one head, sequences with tokens} of sequences 0 .. s-1;
+// every thread of the CTA calls it
+__device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_width, int n_seq, int2 *prefix) {
+    __shared__ int2 warp_sum[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int per = (n_seq + nt - 1) / nt;
-    int sum = 0;
+    int2 sum = make_int2(0, 0);
     for (int k = 0; k < per; ++k) {
         const int s = tid * per + k;
-        if (s < n_seq) sum += (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+        if (s < n_seq) {
+            const int t = (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+            sum.x += t;
+            sum.y += t > 0;
+        }
     }
-    int inc = sum;
+    int2 inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+        if (lane >= o) inc.x += x, inc.y += y;
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    int2 base = make_int2(inc.x - sum.x, inc.y - sum.y);
+    for (int w = 0; w < warp; ++w) base.x += warp_sum[w].x, base.y += warp_sum[w].y;
     for (int k = 0; k < per; ++k) {
         const int s = tid * per + k;
         if (s < n_seq) {
             prefix[s] = base;
-            base += (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+            const int t = (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+            base.x += t;
+            base.y += t > 0;
         }
     }
     if (tid == nt - 1) prefix[n_seq] = base;
     __syncthreads();
 }
 
-// largest s with prefix[s] * Hk <= unit (and tiles of its own)
-__device__ __forceinline__ int find_seq(const int *prefix, int n_seq, int Hk, int64_t unit) {
+// Ranges.  Beginning and ending a (sequence, head) costs a warp about as much
+// as kHeadCost tiles (the query is fetched, results leave), so the line that is
+// cut evenly is of cost: each (sequence, head) is kHeadCost units and its
+// tiles.  (Cut by tiles alone, a worker with thirty one-tile heads took twice
+// as long as all the others.)
+constexpr int kHeadCost = 6;
+constexpr int kMinTiles = 2;  // per worker, while that leaves some idle
+struct Cut {
+    int64_t tiles, cost;  // in all
+    int W;                // workers in use
+    __device__ __forceinline__ Cut(const int2 *prefix, int n_seq, int Hk, int workers) {
+        tiles = (int64_t)prefix[n_seq].x * Hk;
+        cost = tiles + (int64_t)kHeadCost * prefix[n_seq].y * Hk;
+        const int64_t w = (tiles + kMinTiles - 1) / kMinTiles;
+        W = (int)(w < workers ? w : workers);
+    }
+    __device__ __forceinline__ int64_t begin(int w) const {  // cost unit at which worker w begins
+        const int64_t q = cost / W, r = cost % W;
+        return w * q + (w < r ? w : r);
+    }
+    __device__ __forceinline__ int worker_of(int64_t unit) const {
+        const int64_t q = cost / W, r = cost % W, cut = r * (q + 1);
+        return (int)(unit < cut ? unit / (q + 1) : r + (unit - cut) / q);
+    }
+};
+__device__ __forceinline__ int64_t head_cost(int2 prefix, int Hk) { return ((int64_t)prefix.x + (int64_t)kHeadCost * prefix.y) * Hk; }
+// the last sequence whose tiles (cost) begin at or before `unit`
+template <bool COST>
+__device__ __forceinline__ int find_seq(const int2 *prefix, int n_seq, int Hk, int64_t unit) {
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)prefix[mid] * Hk <= unit) lo = mid;
+        if ((COST ? head_cost(prefix[mid], Hk) : (int64_t)prefix[mid].x * Hk) <= unit) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
-
-// Ranges: W workers share `total` units; at least kMinUnits each while that leaves some idle.
-constexpr int kMinUnits = 2;
-__device__ __forceinline__ int active_workers(int64_t total, int workers) {
-    const int64_t w = (total + kMinUnits - 1) / kMinUnits;
-    return (int)(w < workers ? w : workers);
-}
-__device__ __forceinline__ int64_t range_begin(int64_t total, int W, int w) {
-    const int64_t q = total / W, r = total % W;
-    return w * q + (w < r ? w : r);
-}
-__device__ __forceinline__ int worker_of(int64_t total, int W, int64_t unit) {
-    const int64_t q = total / W, r = total % W, cut = r * (q + 1);
-    return (int)(unit < cut ? unit / (q + 1) : r + (unit - cut) / q);
+// tiles before the cost unit `unit`
+__device__ __forceinline__ int64_t tiles_before(const int2 *prefix, int n_seq, int Hk, int64_t unit, int64_t all) {
+    if (unit >= head_cost(prefix[n_seq], Hk)) return all;
+    const int s = find_seq<true>(prefix, n_seq, Hk, unit);
+    const int T = prefix[s + 1].x - prefix[s].x;
+    const int64_t in = unit - head_cost(prefix[s], Hk);
+    const int64_t h = in / (T + kHeadCost), o = in % (T + kHeadCost);
+    return (int64_t)prefix[s].x * Hk + h * T + (o > kHeadCost ? o - kHeadCost : 0);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -499,17 +527,16 @@ struct Stages {
         if (gave_up || (bad >> stage & 1)) return false;
         const uint32_t parity = phases >> stage & 1;
         phases ^= 1u << stage;
-        for (uint32_t i = 0; i < kWaitLimit; ++i) {
-            uint32_t done;
-            asm volatile(
-                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                : "=r"(done)
-                : "r"(bar0 + 8 * stage), "r"(parity)
-                : "memory");
-            if (__all_sync(0xffffffffu, done)) return true;
-        }
-        gave_up = true;
-        return false;
+        uint32_t done = 0;
+        if ((threadIdx.x & 31) == 0)  // one lane polls: a poll by 32 lanes holds the warp for 200 clocks
+            for (uint32_t i = 0; i < kWaitLimit && !done; ++i)
+                asm volatile(
+                    "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                    : "=r"(done)
+                    : "r"(bar0 + 8 * stage), "r"(parity)
+                    : "memory");
+        gave_up = __shfl_sync(0xffffffffu, done, 0) == 0;
+        return !gave_up;
     }
 };
 
@@ -523,11 +550,11 @@ struct Cursor {
         const int at = page_base + lane;
         page = at < width ? table[(int64_t)s * width + at] : -1;
     }
-    __device__ __forceinline__ void seek(const Pool &pool, const int *prefix, const int32_t *table, int width, int n_seq,
+    __device__ __forceinline__ void seek(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq,
                                          int64_t unit, int lg) {
-        s = find_seq(prefix, n_seq, pool.Hk, unit);
-        T = prefix[s + 1] - prefix[s];
-        const int64_t in = unit - (int64_t)prefix[s] * pool.Hk;
+        s = find_seq<false>(prefix, n_seq, pool.Hk, unit);
+        T = prefix[s + 1].x - prefix[s].x;
+        const int64_t in = unit - (int64_t)prefix[s].x * pool.Hk;
         h = (int)(in / T);
         k = (int)(in % T);
         load_pages(pool, table, width, lg);
@@ -540,7 +567,7 @@ struct Cursor {
         if (pg < 0 || pg >= pool.n_pages) return nullptr;
         return pool.pages + pg * pool.page_bytes + h * pool.head_bytes + (int64_t)(k & ((1 << lg) - 1)) * tile_bytes;
     }
-    __device__ __forceinline__ void next(const Pool &pool, const int *prefix, const int32_t *table, int width, int n_seq, int lg) {
+    __device__ __forceinline__ void next(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq, int lg) {
         if (++k < T) return;
         k = 0;
         if (++h < pool.Hk) {
@@ -550,13 +577,13 @@ struct Cursor {
         h = 0;
         do {
             ++s;
-        } while (s < n_seq && prefix[s + 1] == prefix[s]);
+        } while (s < n_seq && prefix[s + 1].x == prefix[s].x);
         if (s >= n_seq) {  // past the last tile: never fetched
             s = n_seq - 1;
             T = 1 << 30;
             return;
         }
-        T = prefix[s + 1] - prefix[s];
+        T = prefix[s + 1].x - prefix[s].x;
         load_pages(pool, table, width, lg);
     }
 };
@@ -576,15 +603,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * NST];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int *prefix = reinterpret_cast<int *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
-    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
-    const int W = active_workers(total, p.workers);
+    const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int rb = blockIdx.x % p.row_blocks;
     const int w = (int)(blockIdx.x / p.row_blocks) * kWarps + warp;
-    if (w >= W) return;
-    const int64_t u0 = range_begin(total, W, w), u1 = range_begin(total, W, w + 1);
+    if (w >= cut.W) return;
+    const int64_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
+    const int64_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
+    if (u0 >= u1) return;
     const int lg = p.pool.lgP - 5;
     const int rho0 = rb * 8 * NT;
 
@@ -607,12 +635,13 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     Query<D, NT, HL> q;
     float O[NT][NB][2][4], cs[NT][4], ref[NT], l[NT];  // cs: row b (< 8) holds block b's -8 * 2^-24 * sum p s
     bool fresh = true;
-    int k_first = 0;
+    int k_first = 0, len = 0;
     int stage = 0;
     for (int unit = 0; unit < units; ++unit) {
         if (fresh) {  // a new (sequence, head)
             q.load(p, at.s, at.h, rho0);
             k_first = at.k;
+            len = seq_len(p.pool, p.lens, p.table_width, at.s);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 ref[n] = -INFINITY;
@@ -634,7 +663,6 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
             const uint8_t *tile = st.buf + stage * BYTES;
             // the turned scores take the place of the tile's K codes once those are read (at D = 64 they are too small)
             float *turned = reinterpret_cast<float *>(D == 64 ? smem + kWarps * NST * BYTES + warp * 1024 : const_cast<uint8_t *>(tile));
-            const int len = seq_len(p.pool, p.lens, p.table_width, at.s);
             const int in_tile = len - at.k * kTile;  // tokens of the sequence from this tile on
             float x[NT][8];  // row g, tokens 16 c + 4 t + (0 .. 3) at 4 c
             {
@@ -660,16 +688,25 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                     }
                 }
             }
-            // V scales: tokens 16 c + 4 t + (0 .. 3)
-            uint2 vs[2][NB];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
+            // V scales of tokens 16 c + 4 t + (0 .. 3); of tokens never written they may be anything and count as 0
+            auto v_scales = [&](int c, uint2 *vs) {
 #pragma unroll
                 for (int b = 0; b < NB; b += 2) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(tile + 34 * D + ((c * 4 + t) * NB + b) * 8);
-                    vs[c][b] = make_uint2(v.x, v.y);
-                    vs[c][b + 1] = make_uint2(v.z, v.w);
+                    vs[b] = make_uint2(v.x, v.y);
+                    vs[b + 1] = make_uint2(v.z, v.w);
                 }
+                if (in_tile < kTile) {
+                    const int left = in_tile - 16 * c - 4 * t;
+                    const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                    const uint32_t k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        vs[b].x &= k0;
+                        vs[b].y &= k1;
+                    }
+                }
+            };
             if (in_tile - (p.R - 1) < kTile) {  // some row does not see the whole tile
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -678,29 +715,19 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                     for (int i = 0; i < 8; ++i)
                         if (16 * (i >> 2) + 4 * t + (i & 3) >= see) x[n][i] = -INFINITY;
                 }
-                if (in_tile < kTile) {  // tokens never written: their scales may be anything
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int left = in_tile - 16 * c - 4 * t;
-                        const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-                        const uint32_t k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            vs[c][b].x &= k0;
-                            vs[c][b].y &= k1;
-                        }
-                    }
-                }
             }
             // the tile's largest |V scale| as a power of two, rounded up
             __half2 sm = __float2half2_rn(0.f);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c) {
+                uint2 vs[NB];
+                v_scales(c, vs);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[c][b].x)));
-                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[c][b].y)));
+                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[b].x)));
+                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[b].y)));
                 }
+            }
             float smax = fmaxf(__low2float(sm), __high2float(sm));
             smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 1));
             smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 2));
@@ -742,6 +769,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
             // O^T += V^T (p s)^T, 16 tokens at a time
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                uint2 vs[NB];
+                v_scales(c, vs);
                 uint32_t vw[2 * NB];
 #pragma unroll
                 for (int i = 0; i < NB / 2; ++i) {
@@ -750,8 +779,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const float s0 = half_lo(vs[c][b].x), s1 = half_hi(vs[c][b].x);
-                    const float s2 = half_lo(vs[c][b].y), s3 = half_hi(vs[c][b].y);
+                    const float s0 = half_lo(vs[b].x), s1 = half_hi(vs[b].x);
+                    const float s2 = half_lo(vs[b].y), s3 = half_hi(vs[b].y);
                     const uint32_t w0 = vw[2 * b], w1 = vw[2 * b + 1];
                     uint32_t a0 = w0 & kLoNib, a1 = w0 & kHiNib, a2 = w1 & kLoNib, a3 = w1 & kHiNib;
                     uint32_t e0 = (w0 >> 8) & kLoNib, e1 = (w0 >> 8) & kHiNib, e2 = (w1 >> 8) & kLoNib, e3 = (w1 >> 8) & kHiNib;
@@ -860,32 +889,30 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const AttendParams p, int pass_rows) {
     extern __shared__ __align__(128) uint8_t smem[];
-    int *prefix = reinterpret_cast<int *>(smem);
+    int2 *prefix = reinterpret_cast<int2 *>(smem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
-    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
-    const int W = active_workers(total, p.workers);
+    const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int lane = threadIdx.x & 31;
     const int rows = p.R * p.G;
     const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (id >= (int64_t)p.n_seq * p.pool.Hk * rows) return;
     const int rho = (int)(id % rows), h = (int)(id / rows % p.pool.Hk), s = (int)(id / rows / p.pool.Hk);
-    const int T = prefix[s + 1] - prefix[s];
+    const int T = prefix[s + 1].x - prefix[s].x;
     const int64_t orow = ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G;
     float o[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
     float lse = -INFINITY;
     if (T > 0) {
-        const int64_t u0 = (int64_t)prefix[s] * p.pool.Hk + (int64_t)h * T, u1 = u0 + T;
-        const int w0 = worker_of(total, W, u0), w1 = worker_of(total, W, u1 - 1);
+        const int64_t c0 = head_cost(prefix[s], p.pool.Hk) + (int64_t)h * (T + kHeadCost);
+        const int w0 = cut.worker_of(c0 + kHeadCost), w1 = cut.worker_of(c0 + kHeadCost + T - 1);
         if (w0 == w1) return;  // one worker had it all and wrote it
         const int rb = rho / pass_rows, row = rho % pass_rows;
         float top = -INFINITY;
-        auto slot_of = [&](int w) {
-            const int64_t begin = range_begin(total, W, w);
-            return (((int64_t)rb * p.workers + w) * 2 + (begin >= u0 ? 0 : 1)) * pass_rows + row;
-        };
+        // the head is its last one for w0 if w0 also has the tile before it
+        const int after = c0 > 0 && cut.worker_of(c0 - 1) == w0;
+        auto slot_of = [&](int w) { return (((int64_t)rb * p.workers + w) * 2 + (w == w0 ? after : 0)) * pass_rows + row; };
         for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, p.part_rl[slot_of(w)].x);
 #pragma unroll
         for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -939,13 +966,14 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * NST];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int *prefix = reinterpret_cast<int *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
-    const int64_t total = (int64_t)prefix[p.n_seq] * p.pool.Hk;
-    const int W = active_workers(total, p.workers);
+    const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int w = (int)blockIdx.x * kWarps + warp;
-    if (w >= W) return;
-    const int64_t u0 = range_begin(total, W, w), u1 = range_begin(total, W, w + 1);
+    if (w >= cut.W) return;
+    const int64_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
+    const int64_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
+    if (u0 >= u1) return;
     const int lg = p.pool.lgP - 5;
     Stages<BYTES, NST> st;
     st.init(smem + warp * NST * BYTES, bars + warp * NST);
@@ -968,9 +996,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
         bool fresh = true;
         int stage = 0;
         float2 lse2[NT], fac[NT];  // rows 2t, 2t + 1
+        int len = 0;
         for (int unit = 0; unit < units; ++unit) {
             if (fresh) {
                 q.load(p, at.s, at.h, rho0);
+                len = seq_len(p.pool, p.lens, p.table_width, at.s);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int rho = rho0 + 8 * n + g;
@@ -984,7 +1014,6 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
                 }
                 fresh = false;
             }
-            const int len = seq_len(p.pool, p.lens, p.table_width, at.s);
             const int in_tile = len - at.k * kTile;
             float sum[4];  // tokens g, g + 8, g + 16, g + 24
             if (!st.wait(stage, phases)) {
@@ -1157,7 +1186,7 @@ cudaError_t launch(void (*kernel)(P, A...), dim3 grid, int threads, int smem, cu
 }
 
 int smem_of(uint32_t D, int bytes, uint32_t n_seq) {
-    return kWarps * (D == 64 ? 4 * bytes + 1024 : 3 * bytes) + ((int)n_seq + 1) * 4;
+    return kWarps * (D == 64 ? 4 * bytes + 1024 : 3 * bytes) + ((int)n_seq + 1) * 8;
 }
 
 }  // namespace
@@ -1259,7 +1288,7 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     if (e != cudaSuccess) return cuda_failed("attention launch", e);
     void (*c)(AttendParams, int) = D == 64 ? combine_kernel<64> : D == 128 ? combine_kernel<128> : combine_kernel<256>;
     const uint64_t rows = (uint64_t)n_seq * n_q_head * n_rows;
-    e = launch(c, dim3((unsigned)((rows + 7) / 8)), 256, ((int)n_seq + 1) * 4, st, true, p, 8 * sh.nt);
+    e = launch(c, dim3((unsigned)((rows + 7) / 8)), 256, ((int)n_seq + 1) * 8, st, true, p, 8 * sh.nt);
     return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
 }
 
