@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <string>
+#include <type_traits>
 
 #include "kvs.h"
 #include "kvs_internal.h"
@@ -16,9 +17,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kMaxSeq = 4096;
 constexpr int kBins = 256;
+constexpr int kCopies = 16;
 
 struct EvictParams {
     uint8_t *pages;
@@ -32,7 +34,6 @@ struct EvictParams {
     int32_t *kept;
     float *kept_weights;
     int32_t *new_lens;
-    int cached;  // keys of a CTA's share that fit its shared memory
 };
 
 __device__ __forceinline__ int seq_len(const EvictParams &p, int s) {
@@ -50,17 +51,22 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // One cluster per (sequence, kv head); each CTA has a contiguous share of the
-// candidates (tokens between the sinks and the recent ones).  The smallest key
-// that stays is found digit by digit, 8 bits at a time from the top: a
-// histogram of the candidates that match the digits so far, summed over the
-// cluster, gives the next digit.  Then every CTA writes its tokens in order:
-// keys above the threshold, and of those equal to it the first ones.
+// candidates (tokens between the sinks and the recent ones), K keys per thread
+// in registers (key m of thread x is candidate 1024 m + x of the share).  The
+// smallest key that stays is found digit by digit, 8 bits at a time from the
+// top: a histogram of the candidates that match the digits so far, summed over
+// the cluster, gives the next digit.  Then every CTA writes its tokens in
+// order: keys above the threshold, and of those equal to it the first ones.
+// K = 0 is for shares beyond 32768 keys: the keys are read again each time.
+template <int K>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[2][kBins];  // a digit's counts; the other is being cleared
+    constexpr int kW = kThreads / 32;
+    __shared__ uint32_t hist[kCopies][kBins + 1];  // a digit's counts; lanes of a warp count in different copies, since
+                                                   // most weights share a few top digits
+    __shared__ uint32_t sums[2][kBins];  // of the copies, read by the whole cluster; two, for digits in turn
     __shared__ uint32_t total[kBins];
-    __shared__ uint32_t warp_count[2][kThreads / 32];
-    __shared__ uint32_t mine[2];  // this CTA's tokens above the threshold, and equal to it
+    __shared__ uint32_t count[K > 0 ? K : 1][kW];  // tokens above the threshold (high half) and equal to it, by row of 1024 and warp
+    __shared__ uint32_t mine[2];         // this CTA's tokens above the threshold, and equal to it
     __shared__ uint32_t digit[2];
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -78,35 +84,57 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
         }
         return;
     }
-    const int n = T - p.sinks - p.recent;       // candidates
+    const int n = T - p.sinks - p.recent;          // candidates
     const int want = p.keep - p.sinks - p.recent;  // of which these stay
     const int share = (n + ranks - 1) / ranks;
     const int c0 = min(rank * share, n), c1 = min(c0 + share, n), cn = c1 - c0;
     const float *wc = w + p.sinks + c0;
-    auto key_at = [&](int i) { return i < p.cached ? keys[i] : key_of(wc[i]); };
-    for (int i = tid; i < kBins; i += kThreads) hist[0][i] = hist[1][i] = 0;
+    const int rows = (cn + kThreads - 1) / kThreads;
+    uint32_t key[K > 0 ? K : 1];
+    if (K > 0) {
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+            const int i = m * kThreads + tid;
+            key[m] = i < cn ? key_of(wc[i]) : 0u;
+        }
+    }
+    // every candidate of this thread, as f(row, key)
+    auto each = [&](auto f) {
+        if (K > 0) {
+#pragma unroll
+            for (int m = 0; m < K; ++m)
+                if (m * kThreads + tid < cn) f(m, key[m]);
+        } else {
+            for (int m = 0; m < rows; ++m)
+                if (m * kThreads + tid < cn) f(m, key_of(wc[m * kThreads + tid]));
+        }
+    };
+    for (int i = tid; i < kCopies * (kBins + 1); i += kThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
+    uint32_t *mine_h = hist[lane & (kCopies - 1)];
     uint32_t prefix = 0;
     uint32_t left = (uint32_t)want;  // still to be found among the keys that match the prefix
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-        uint32_t *hs = hist[pass & 1];
-        for (int i = tid; i < cn; i += kThreads) {
-            uint32_t k;
-            if (pass == 0) {
-                k = key_of(wc[i]);
-                if (i < p.cached) keys[i] = k;
-            } else {
-                k = key_at(i);
+        each([&](int, uint32_t k) {
+            if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&mine_h[k >> shift & 255], 1u);
+        });
+        __syncthreads();
+        uint32_t *own = sums[pass & 1];
+        if (tid < kBins) {
+            uint32_t sum = 0;
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                sum += hist[c][tid];
+                hist[c][tid] = 0;
             }
-            if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hs[k >> shift & 255], 1u);
+            own[tid] = sum;
         }
         cl.sync();
         if (tid < kBins) {
             uint32_t sum = 0;
-            for (int r = 0; r < ranks; ++r) sum += *cl.map_shared_rank(&hs[tid], r);
+            for (int r = 0; r < ranks; ++r) sum += *cl.map_shared_rank(&own[tid], r);
             total[tid] = sum;
-            hist[(pass + 1) & 1][tid] = 0;
         }
         __syncthreads();
         if (warp == 0) {  // from the top: the digit at which the count reaches `left`
@@ -135,20 +163,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     }
     // prefix is the threshold key; `left` tokens equal to it stay
     if (want == 0) prefix = 0xffffffffu, left = 0;
-    uint32_t above = 0, equal = 0;
-    for (int i = tid; i < cn; i += kThreads) {
-        const uint32_t k = key_at(i);
-        above += k > prefix;
-        equal += k == prefix;
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if (lane == 0) warp_count[0][warp] = above, warp_count[1][warp] = equal;
+    uint32_t mine_a = 0, mine_e = 0;
+    each([&](int, uint32_t k) {
+        mine_a += k > prefix;
+        mine_e += k == prefix;
+    });
+    mine_a = __reduce_add_sync(0xffffffffu, mine_a);
+    mine_e = __reduce_add_sync(0xffffffffu, mine_e);
+    if (tid < 2) mine[tid] = 0;
     __syncthreads();
-    if (tid < 2) {
-        uint32_t sum = 0;
-        for (int i = 0; i < kThreads / 32; ++i) sum += warp_count[tid][i];
-        mine[tid] = sum;
+    if (lane == 0) {
+        atomicAdd(&mine[0], mine_a);
+        atomicAdd(&mine[1], mine_e);
     }
     cl.sync();
     uint32_t out = (uint32_t)p.sinks, eq_before = 0;  // places taken and equals seen before this CTA's share
@@ -158,31 +184,70 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
         eq_before += m[1];
     }
     out += min(eq_before, left);
-    for (int i0 = 0; i0 < cn; i0 += kThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < cn ? key_at(i) : 0u;
-        const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
-        const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
-        __syncthreads();
-        if (lane == 0) warp_count[0][warp] = __popc(ba), warp_count[1][warp] = __popc(be);
-        __syncthreads();
-        uint32_t na = 0, ne = 0, ta = 0, te = 0;
-        for (int x = 0; x < kThreads / 32; ++x) {
-            if (x < warp) na += warp_count[0][x], ne += warp_count[1][x];
-            ta += warp_count[0][x];
-            te += warp_count[1][x];
-        }
-        const uint32_t below = (1u << lane) - 1;
-        na += __popc(ba & below);
-        ne += eq_before + __popc(be & below);
+    const uint32_t below = (1u << lane) - 1;
+    // candidate (row, k) with na above and ne equal ones before it in the share
+    auto place = [&](int i, bool a, bool e, uint32_t na, uint32_t ne) {
+        ne += eq_before;
         if (a || (e && ne < left)) {
             const uint32_t at = out + na + min(ne, left) - min(eq_before, left);
             const int tok = p.sinks + c0 + i;
             kept[at] = tok;
             if (kw) kw[at] = w[tok];
         }
-        out += ta + min(eq_before + te, left) - min(eq_before, left);
-        eq_before += te;
+    };
+    if (K > 0) {
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+            const bool in = m * kThreads + tid < cn;
+            const uint32_t a = __ballot_sync(0xffffffffu, in && key[m] > prefix), e = __ballot_sync(0xffffffffu, in && key[m] == prefix);
+            if (lane == 0) count[m][warp] = (uint32_t)__popc(a) << 16 | (uint32_t)__popc(e);  // below 2^16 in all
+        }
+        __syncthreads();
+        if (warp == 0) {  // counts -> counts before, over rows and warps in order; lane l has K entries in a row
+            uint32_t *c = &count[0][0];
+            uint32_t sum = 0;
+#pragma unroll
+            for (int m = 0; m < K; ++m) sum += c[lane * K + m];
+            uint32_t inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            uint32_t run = inc - sum;
+#pragma unroll
+            for (int m = 0; m < K; ++m) {
+                const uint32_t x = c[lane * K + m];
+                c[lane * K + m] = run;
+                run += x;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+            const bool in = m * kThreads + tid < cn, a = in && key[m] > prefix, e = in && key[m] == prefix;
+            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e), base = count[m][warp];
+            place(m * kThreads + tid, a, e, (base >> 16) + __popc(ba & below), (base & 0xffffu) + __popc(be & below));
+        }
+    } else {
+        uint32_t row_a = 0, row_e = 0;  // of the rows before
+        for (int m = 0; m < rows; ++m) {
+            const int i = m * kThreads + tid;
+            const uint32_t k = i < cn ? key_of(wc[i]) : 0u;
+            const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
+            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+            __syncthreads();
+            if (lane == 0) count[0][warp] = (uint32_t)__popc(ba) << 16 | (uint32_t)__popc(be);
+            __syncthreads();
+            uint32_t before = 0, all = 0;
+            for (int x = 0; x < kW; ++x) {
+                if (x < warp) before += count[0][x];
+                all += count[0][x];
+            }
+            place(i, a, e, row_a + (before >> 16) + __popc(ba & below), row_e + (before & 0xffffu) + __popc(be & below));
+            row_a += all >> 16;
+            row_e += all & 0xffffu;
+        }
     }
     // the ones that always stay
     for (int i = rank * kThreads + tid; i < p.sinks + p.recent; i += ranks * kThreads) {
@@ -224,30 +289,47 @@ __global__ void __launch_bounds__(128) gather_kernel(const EvictParams p) {
     }
     uint8_t *out = stage[warp];
     const int t = lane;
+    // K codes: 4 pieces of min(16, NB * 4) bytes per 4 blocks (D = 64: two octets share a 16-byte vector)
+    using Piece = typename std::conditional<NB == 2, uint2, uint4>::type;
+    constexpr int kGroups = NB <= 4 ? 1 : NB / 4;
+    auto k_at = [&](int tok, int grp, int q) {
+        const int u = (tok >> 3) * NB + grp * 4;
+        return (((u >> 2) * 32) + (tok & 7) * 4 + q) * 16 + (u & 3) * 4;
+    };
+    auto v_at = [&](int tok, int bp, int j) { return 18 * D + ((((tok >> 4) * (NB / 2) + bp) * 32) + j * 4 + ((tok & 15) >> 2)) * 16; };
+    Piece kp[kGroups][4];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) kp[g][q] = src ? *reinterpret_cast<const Piece *>(src + k_at(st, g, q)) : Piece{};
+    uint16_t ks[NB], vs[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        uint32_t kw[4];
-        uint16_t vw[8], ks = 0, vs = 0;
-        const int su = (st >> 3) * NB + b, sw = ((st >> 4) * NB + b) * 2 + ((st & 3) >> 1);
-        const int k_src = ((su >> 2) * 32 + (st & 7) * 4) * 16 + (su & 3) * 4;
-        const int v_src = 18 * D + ((sw >> 2) * 32 + ((st & 15) >> 2)) * 16 + (sw & 3) * 4 + (st & 1) * 2;
+        ks[b] = src ? reinterpret_cast<const uint16_t *>(src + 16 * D)[((st >> 4) * 8 + (st & 7)) * NB * 2 + b * 2 + (st >> 3 & 1)] : (uint16_t)0;
+        vs[b] = src ? reinterpret_cast<const uint16_t *>(src + 34 * D)[((st >> 2) * NB + b) * 4 + (st & 3)] : (uint16_t)0;
+    }
+    // V codes: of each 16-byte unit (4 tokens x 2 blocks) this token's two bytes of either block
+    const int s_half = (st & 3) >> 1, s_sh = (st & 1) * 16, d_half = (t & 3) >> 1, d_par = t & 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) kw[q] = src ? *reinterpret_cast<const uint32_t *>(src + k_src + q * 16) : 0u;
+    for (int bp = 0; bp < NB / 2; ++bp) {
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) vw[j] = src ? *reinterpret_cast<const uint16_t *>(src + v_src + j * 64) : (uint16_t)0;
-        if (src) {
-            ks = reinterpret_cast<const uint16_t *>(src + 16 * D)[((st >> 4) * 8 + (st & 7)) * NB * 2 + b * 2 + (st >> 3 & 1)];
-            vs = reinterpret_cast<const uint16_t *>(src + 34 * D)[((st >> 2) * NB + b) * 4 + (st & 3)];
+        for (int j = 0; j < 8; ++j) v[j] = src ? *reinterpret_cast<const uint4 *>(src + v_at(st, bp, j)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint16_t *dst = reinterpret_cast<uint16_t *>(out + v_at(t, bp, j)) + 2 * d_half + d_par;
+            dst[0] = (uint16_t)((s_half ? v[j].y : v[j].x) >> s_sh);
+            dst[4] = (uint16_t)((s_half ? v[j].w : v[j].z) >> s_sh);
         }
-        const int u = (t >> 3) * NB + b, w = ((t >> 4) * NB + b) * 2 + ((t & 3) >> 1);
-        const int k_dst = ((u >> 2) * 32 + (t & 7) * 4) * 16 + (u & 3) * 4;
-        const int v_dst = 18 * D + ((w >> 2) * 32 + ((t & 15) >> 2)) * 16 + (w & 3) * 4 + (t & 1) * 2;
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(out + k_dst + q * 16) = kw[q];
+    for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint16_t *>(out + v_dst + j * 64) = vw[j];
-        reinterpret_cast<uint16_t *>(out + 16 * D)[((t >> 4) * 8 + (t & 7)) * NB * 2 + b * 2 + (t >> 3 & 1)] = ks;
-        reinterpret_cast<uint16_t *>(out + 34 * D)[((t >> 2) * NB + b) * 4 + (t & 3)] = vs;
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<Piece *>(out + k_at(t, g, q)) = kp[g][q];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        reinterpret_cast<uint16_t *>(out + 16 * D)[((t >> 4) * 8 + (t & 7)) * NB * 2 + b * 2 + (t >> 3 & 1)] = ks[b];
+        reinterpret_cast<uint16_t *>(out + 34 * D)[((t >> 2) * NB + b) * 4 + (t & 3)] = vs[b];
     }
     __syncwarp();
     for (int x = lane; x < BYTES / 16; x += 32) reinterpret_cast<uint4 *>(dst)[x] = reinterpret_cast<const uint4 *>(out)[x];
@@ -310,22 +392,21 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     p.kept_weights = kept_weights;
     p.new_lens = new_lens;
     const uint64_t sh = (uint64_t)n_seq * pool->n_kv_head;
-    // a cluster that gives each CTA about 8192 keys, up to the 8 CTAs every launch may have
+    // Up to 4096 keys per CTA (4 a thread) one CTA is enough; beyond, a cluster of up to the 8 CTAs that every launch
+    // may have, then more keys a thread.
     uint64_t most = (uint64_t)table_width * P;
     if (width < most) most = width;
     int ranks = 1;
-    while (ranks < 8 && (uint64_t)ranks * 8192 < most) ranks *= 2;
+    while (ranks < 8 && (uint64_t)ranks * 4096 < most) ranks *= 2;
     if (sh * ranks > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head too large");
-    uint64_t share = (most + ranks - 1) / ranks;
-    p.cached = (int)(share < 49152 ? share : 49152);  // 192 KB of keys at most; the rest are read again
-    const int smem = (p.cached * 4 + 15) / 16 * 16;
+    const uint64_t share = (most + ranks - 1) / ranks;
+    void (*select)(EvictParams) = share <= 4096 ? select_kernel<4> : share <= 8192 ? select_kernel<8> : share <= 16384 ? select_kernel<16>
+                                  : share <= 32768 ? select_kernel<32> : select_kernel<0>;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(select_kernel), smem);
-    if (e != cudaSuccess) return cuda_failed("evict launch", e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sh * ranks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = 0;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -333,7 +414,7 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, select, p);
     if (e != cudaSuccess) return cuda_failed("evict launch", e);
     const uint64_t tiles = sh * ((keep + 31) / 32);
     if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");

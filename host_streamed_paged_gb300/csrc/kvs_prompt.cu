@@ -640,7 +640,8 @@ struct WeightShape {
     static constexpr int kStages = D == 64 ? 4 : (D == 128 ? 4 : 3);
     static constexpr int kOffRing = 2 * kKBytes;
     static constexpr int kOffLse = kOffRing + kStages * kBlock;
-    static constexpr int kOffBar = kOffLse + 2 * 2 * BQ * 4;
+    static constexpr bool kOwnLse = D <= 128;
+    static constexpr int kOffBar = kOffLse + (kOwnLse ? 8 : 2) * 2 * BQ * 4;
     static constexpr int kSmem = kOffBar + 256 + 1024;
 };
 
@@ -759,58 +760,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = warp >> 2, row = tid & 127;
         const int key = k0 + i * kTileRows + row;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + i * 2 * BQ;  // this warpgroup's two buffers of -lse
         const float sc = p.scale_log2;
-        auto lse_of = [&](int r) {  // -lse (log2 units) of query row `row` of tile r; rows that count for nothing: -inf
-            const int tok = start + r * TQ + row / G;
-            float z = INFINITY;
-            if (row < TQ * G && tok < L) {
-                z = p.lse_in[(int64_t)(begin + tok) * (p.Hk * G) + head * G + row % G] * 1.4426950408889634f;
-                if (z == -INFINITY) z = INFINITY;
-            }
-            return -z;
-        };
-        float next = row < BQ ? lse_of(0) : 0.f;
+        // every warp keeps its own copy of a tile's -lse, so that the warps run apart (D = 256: no room, one copy per
+        // warpgroup); the next tile's are on their way from memory meanwhile
+        constexpr int kRows = S::kOwnLse ? BQ / 32 : 1;
+        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + (S::kOwnLse ? warp : i) * 2 * BQ;
+        const int Hq = p.Hk * G;
+        int t_of[kRows];                // token of the tile that this thread's x-th row belongs to (TQ: none)
+        const float *src[kRows];        // its lse in the current tile
+        float next[kRows];
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+            const int q = S::kOwnLse ? 32 * x + lane : row;
+            t_of[x] = q < TQ * G ? q / G : TQ;
+            src[x] = p.lse_in + (int64_t)(begin + start + q / G) * Hq + head * G + q % G;
+            next[x] = t_of[x] < TQ && start + t_of[x] < L ? *src[x] : INFINITY;
+        }
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool ok = true;
         for (int r = 0; r < ntile; ++r) {
             const int buf = r & 1;
-            if (row < BQ) sl[buf * BQ + row] = next;
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
-            if (r + 1 < ntile && row < BQ) next = lse_of(r + 1);
+            float *z = sl + buf * BQ;
+#pragma unroll
+            for (int x = 0; x < kRows; ++x) {
+                // -lse (log2 units); rows that count for nothing: -inf
+                const float v = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
+                if (S::kOwnLse || row < BQ) z[S::kOwnLse ? 32 * x + lane : row] = v;
+                src[x] += (int64_t)TQ * Hq;
+                next[x] = t_of[x] < TQ && r + 1 < ntile && start + (r + 1) * TQ + t_of[x] < L ? *src[x] : INFINITY;
+            }
+            if constexpr (S::kOwnLse) __syncwarp();
+            else asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
             ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((r >> 1) & 1), abort);
             if (!ok) break;
             tc_after();
             const int tok0 = start + r * TQ;
             // columns this key counts: rows of tokens from the key on, and none past the prompt
             const bool edge = tok0 < k0 + (i + 1) * kTileRows - 1 || tok0 + TQ > L;
+            const int c_lo = (key - tok0) * G;
+            const int c_hi = (L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G;
             const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ);
-            uint32_t sr[BQ];
+            // 32 columns at a time, the next 32 on their way from tensor memory
+            uint32_t sr[2][32];
+            tmem_ld32(ts, sr[0]);
 #pragma unroll
-            for (int c = 0; c < BQ; c += 32) tmem_ld32(ts + c, sr + c);
-            tmem_wait_ld();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_read(i, buf));
-            const float *s = reinterpret_cast<const float *>(sr);
-            const float4 *z4 = reinterpret_cast<const float4 *>(sl + buf * BQ);
-            const float2 sc2 = make_float2(sc, sc);
-            if (!edge) {
+            for (int c0 = 0; c0 < BQ; c0 += 32) {
+                const float *s = reinterpret_cast<const float *>(sr[c0 / 32 & 1]);
+                float4 z4[8];
 #pragma unroll
-                for (int c = 0; c < BQ; c += 4) {
-                    const float4 z = z4[c / 4];
-                    const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z.x, z.y));
-                    const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z.z, z.w));
-                    sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
-                    sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+                for (int c = 0; c < 8; ++c) z4[c] = reinterpret_cast<const float4 *>(z + c0)[c];
+                tmem_wait_ld();
+                if (c0 + 32 < BQ) {
+                    tmem_ld32(ts + c0 + 32, sr[c0 / 32 + 1 & 1]);
+                } else {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_read(i, buf));
                 }
-            } else {
-                const int c_lo = (key - tok0) * G;
-                const int c_hi = (L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G;
+                const float2 sc2 = make_float2(sc, sc);
+                if (!edge) {
 #pragma unroll
-                for (int c = 0; c < BQ; ++c) {
-                    const float e = ex2(fmaf(s[c], sc, sl[buf * BQ + c]));
-                    sum[c & 1].x += c >= c_lo && c < c_hi ? e : 0.f;
+                    for (int c = 0; c < 32; c += 4) {
+                        const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z4[c / 4].x, z4[c / 4].y));
+                        const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z4[c / 4].z, z4[c / 4].w));
+                        sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
+                        sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float zc = c & 2 ? (c & 1 ? z4[c / 4].w : z4[c / 4].z) : (c & 1 ? z4[c / 4].y : z4[c / 4].x);
+                        const float e = ex2(fmaf(s[c], sc, zc));
+                        sum[c & 1].x += c0 + c >= c_lo && c0 + c < c_hi ? e : 0.f;
+                    }
                 }
             }
         }

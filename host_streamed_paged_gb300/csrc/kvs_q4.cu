@@ -92,35 +92,9 @@ __device__ __forceinline__ int k_scale(int t, int b, int NB) { return (((t >> 4)
 __device__ __forceinline__ int v_scale(int t, int b, int NB) { return ((t >> 2) * NB + b) * 4 + (t & 3); }
 
 // ---------------------------------------------------------------- append / read
-// One thread per (row, head, block of 32, K or V).  Bound by bytes: rows in at
-// 2 or 4 bytes per element, 9/16 byte out.
-
-// Q4_0 in IEEE fp32 steps in a fixed order, the same as kvs_append's V: m = the
-// element of largest |x| (lowest index on ties), d = m / -8, id = 1/d (0 if
-// d == 0), code = trunc(x * id + 8.5) within 0 .. 15.
-__device__ __forceinline__ float q4_block(const float *x, uint32_t *w) {
-    float best = x[0], mag = fabsf(x[0]);
-#pragma unroll
-    for (int i = 1; i < 32; ++i) {
-        const float a = fabsf(x[i]);
-        if (a > mag) {
-            mag = a;
-            best = x[i];
-        }
-    }
-    const float d = __fdiv_rn(best, -8.0f);
-    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        int c = __float2int_rz(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
-        c = c > 15 ? 15 : (c < 0 ? 0 : c);
-        const int j = i & 15;
-        w[j >> 2] |= (uint32_t)c << ((j & 3) * 8 + (i >> 4) * 4);
-    }
-    return d;
-}
+// Bound by bytes: rows at 2 or 4 bytes per element on one side, 9/16 byte on
+// the other.  Four lanes share a 32-dim block, 8 dims each, so that rows are
+// read and written in whole lines.
 
 struct RowsParams {
     Pool pool;
@@ -132,89 +106,275 @@ struct RowsParams {
     int dtype;
 };
 
-template <int D>
-__global__ void __launch_bounds__(256) append_kernel(const RowsParams p) {
-    constexpr int NB = D / 32;
-    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const bool is_v = blockIdx.y != 0;
-    const int b = (int)(u % NB);
-    const int h = (int)(u / NB % p.pool.Hk);
-    const int64_t i = u / NB / p.pool.Hk;
-    if (i >= p.n) return;
-    const int64_t slot = p.slots[i];
-    if (slot < 0 || (slot >> p.pool.lgP) >= p.pool.n_pages) return;
-    float x[32];
-    load_row<32>(is_v ? p.v : p.k, p.dtype, i * (is_v ? p.v_stride : p.k_stride) + (int64_t)h * D + b * 32, x);
-    uint32_t w[4];
-    const float d = q4_block(x, w);
-    const int tp = (int)(slot & (p.pool.P - 1)), t = tp & 31;
-    uint8_t *tile = p.pool.pages + (slot >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes +
-                    (int64_t)(tp >> 5) * (36 * D);
-    if (!is_v) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(tile + k_word(t, b, q, NB)) = w[q];
-        reinterpret_cast<__half *>(tile + 16 * D)[k_scale(t, b, NB)] = __float2half_rn(d);
+__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, float *x) {
+    if (dtype == KVS_F32) {
+        load_row<8>(p, dtype, i, x);
     } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+        const float2 a = two(v.x, dtype), b = two(v.y, dtype), c = two(v.z, dtype), d = two(v.w, dtype);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+    }
+}
+
+// Q4_0 of a block whose dims 8 q .. 8 q + 7 lane q of its quad holds, in IEEE
+// fp32 steps in a fixed order, the same as kvs_append's V: m = the element of
+// largest |x| (lowest index on ties), d = m / -8, id = 1/d (0 if d == 0), code
+// = trunc(x * id + 8.5) within 0 .. 15.  Lane q gets bytes 4 w .. 4 w + 3 of
+// the block, w = 0, 2, 1, 3 for q = 0 .. 3.
+__device__ __forceinline__ uint32_t q4_word(const float *x, int q, float &d) {
+    float best = x[0], mag = fabsf(x[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t lo = w[j >> 2] >> ((j & 3) * 8) & 0xff, hi = w[(j + 8) >> 2] >> ((j & 3) * 8) & 0xff;
-            *reinterpret_cast<uint16_t *>(tile + 18 * D + v_half(t, b, j, NB)) = (uint16_t)(lo | hi << 8);
+    for (int i = 1; i < 8; ++i) {
+        const float a = fabsf(x[i]);
+        if (a > mag) mag = a, best = x[i];
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, mag, o), b2 = __shfl_xor_sync(0xffffffffu, best, o);
+        if (m2 > mag || (m2 == mag && (q & o))) mag = m2, best = b2;
+    }
+    d = __fdiv_rn(best, -8.0f);
+    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
+    uint32_t c[2] = {0, 0};  // a code per byte
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        int k = __float2int_rz(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
+        k = k > 15 ? 15 : (k < 0 ? 0 : k);
+        c[i >> 2] |= (uint32_t)k << (8 * (i & 3));
+    }
+    // lanes 0, 1 have the low nibbles of bytes 0-7, 8-15; lanes 2, 3 the high ones
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, q < 2 ? c[1] : c[0], 2);
+    return q < 2 ? c[0] | got << 4 : got | c[1] << 4;
+}
+__device__ __forceinline__ int word_of(int q) { return q < 2 ? 2 * q : 2 * q - 3; }  // 0, 2, 1, 3
+
+// K: one quad per (row, head, block), stored as it comes (a row's codes of one
+// head are whole lines); kInFlight of them per thread, loaded before the first
+// is encoded.
+constexpr int kInFlight = 4;
+
+// Where the 64 kInFlight (row, head, block) units of a CTA lie: unit x of it is
+// unit (rem + x) % per_row of row `row` + (rem + x) / per_row, in 32 bits.
+struct Units {
+    int64_t row;
+    uint32_t rem, per_row;
+    __device__ __forceinline__ Units(int64_t cta, uint32_t per) : per_row(per) {
+        const int64_t u = cta * (64 * kInFlight);
+        row = u / per;
+        rem = (uint32_t)(u - row * per);
+    }
+};
+
+template <int D>
+__device__ void append_k(const RowsParams &p, int64_t block) {
+    constexpr int NB = D / 32;
+    const int q = threadIdx.x & 3;
+    const Units units(block, NB * p.pool.Hk);
+    int64_t row[kInFlight];
+    uint32_t in_row[kInFlight];
+    float x[kInFlight][8];
+    int64_t slot[kInFlight];
+#pragma unroll
+    for (int m = 0; m < kInFlight; ++m) {
+        const uint32_t u = units.rem + 64 * m + (threadIdx.x >> 2), r = u / units.per_row;
+        row[m] = units.row + r;
+        in_row[m] = u - r * units.per_row;
+        slot[m] = row[m] < p.n ? p.slots[row[m]] : -1;
+        if ((slot[m] >> p.pool.lgP) >= p.pool.n_pages) slot[m] = -1;
+    }
+#pragma unroll
+    for (int m = 0; m < kInFlight; ++m) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[m][e] = 0.f;
+        if (slot[m] >= 0) load8(p.k, p.dtype, row[m] * p.k_stride + in_row[m] * 32 + 8 * q, x[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < kInFlight; ++m) {
+        const int b = in_row[m] % NB, h = in_row[m] / NB;
+        float d;
+        const uint32_t w = q4_word(x[m], q, d);
+        if (slot[m] < 0) continue;
+        const int tp = (int)(slot[m] & (p.pool.P - 1)), t = tp & 31;
+        uint8_t *tile = p.pool.pages + (slot[m] >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes + (int64_t)(tp >> 5) * (36 * D);
+        *reinterpret_cast<uint32_t *>(tile + k_word(t, b, word_of(q), NB)) = w;
+        if (q == 0) reinterpret_cast<__half *>(tile + 16 * D)[k_scale(t, b, NB)] = __float2half_rn(d);
+    }
+}
+
+// V: a byte of four tokens' codes makes up a 16-byte unit of the layout, so a
+// CTA encodes 32 rows of a head (and up to 3 more) into shared memory and then
+// stores units: groups of four consecutive rows that fill tokens 4 m .. 4 m + 3
+// of a page, begun in the CTA's 32, whole; other rows two bytes at a time.
+template <int D>
+__device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
+    constexpr int NB = D / 32, kRows = 32, kAll = kRows + 3, kPass = (kAll * NB + 63) / 64;
+    __shared__ uint32_t code[kAll][NB * 4 + 1];  // padded: neighbouring rows on neighbouring banks
+    __shared__ uint16_t scale[kAll][NB];
+    __shared__ int64_t slot[kAll + 3];  // of rows i0 - 3 .. i0 + 34
+    __shared__ int groups[9];           // rows at which whole groups begin; [8]: how many
+    const int64_t i0 = chunk * kRows;
+    const int tid = threadIdx.x, q = tid & 3;
+    if (tid < kAll + 3) {
+        const int64_t i = i0 - 3 + tid;
+        const int64_t s = i >= 0 && i < p.n ? p.slots[i] : -1;
+        slot[tid] = (s >> p.pool.lgP) < p.pool.n_pages ? s : -1;
+    }
+    __syncthreads();
+    // whether row r (from i0) begins four rows that fill an aligned group of four tokens
+    auto begins = [&](int r) {
+        const int64_t s = slot[r + 3];
+        return s >= 0 && (s & 3) == 0 && slot[r + 4] == s + 1 && slot[r + 5] == s + 2 && slot[r + 6] == s + 3;
+    };
+    float v[kPass][8];
+#pragma unroll
+    for (int m = 0; m < kPass; ++m) {
+        const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[m][e] = 0.f;
+        if (r < kAll && i0 + r < p.n && slot[r + 3] >= 0) load8(p.v, p.dtype, (i0 + r) * p.v_stride + (int64_t)h * D + b * 32 + 8 * q, v[m]);
+    }
+    if (tid < 32) {
+        const uint32_t at = __ballot_sync(0xffffffffu, begins(tid));
+        if (begins(tid)) groups[__popc(at & ((1u << tid) - 1))] = tid;
+        if (tid == 0) groups[8] = __popc(at);
+    }
+#pragma unroll
+    for (int m = 0; m < kPass; ++m) {
+        const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
+        float d;
+        const uint32_t w = q4_word(v[m], q, d);
+        if (r < kAll) {
+            code[r][b * 4 + word_of(q)] = w;
+            if (q == 0) scale[r][b] = __half_as_ushort(__float2half_rn(d));
         }
-        reinterpret_cast<__half *>(tile + 34 * D)[v_scale(t, b, NB)] = __float2half_rn(d);
+    }
+    __syncthreads();
+    auto tile_of = [&](int64_t s) {
+        const int tp = (int)(s & (p.pool.P - 1));
+        return p.pool.pages + (s >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes + (int64_t)(tp >> 5) * (36 * D);
+    };
+    // units: (group, block pair, j); neighbouring threads have neighbouring groups' units of one j
+    for (int x = tid; x < 8 * (NB / 2) * 8; x += 256) {
+        if ((x & 7) >= groups[8]) continue;
+        const int r = groups[x & 7], j = x >> 3 & 7, bp = x >> 6;
+        const int64_t s = slot[r + 3];
+        const int t = (int)(s & 31);
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // word k: block 2 bp + k / 2, tokens 2 (k % 2) and + 1
+            const int at = (2 * bp + (k >> 1)) * 4 + (j >> 2), ra = r + 2 * (k & 1);
+            const uint32_t sel = (j & 3) | (uint32_t)(4 + (j & 3)) << 4;  // byte j and byte j + 8
+            const uint32_t a0 = __byte_perm(code[ra][at], code[ra][at + 2], sel);
+            const uint32_t a1 = __byte_perm(code[ra + 1][at], code[ra + 1][at + 2], sel);
+            o[k] = (a0 & 0xffffu) | a1 << 16;
+        }
+        const int unit = (t >> 4) * (NB / 2) + bp;
+        *reinterpret_cast<uint4 *>(tile_of(s) + 18 * D + (unit * 32 + j * 4 + ((t & 15) >> 2)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    for (int x = tid; x < 8 * NB; x += 256) {
+        const int b = x % NB;
+        if (x / NB >= groups[8]) continue;
+        const int r = groups[x / NB];
+        const int64_t s = slot[r + 3];
+        *reinterpret_cast<uint2 *>(tile_of(s) + 34 * D + v_scale((int)(s & 31), b, NB) * 2) =
+            make_uint2(scale[r][b] | (uint32_t)scale[r + 1][b] << 16, scale[r + 2][b] | (uint32_t)scale[r + 3][b] << 16);
+    }
+    if (groups[8] == 8 && groups[0] == 0 && groups[7] == 28) return;  // they have every row
+    for (int x = tid; x < kRows * NB * 8; x += 256) {  // rows of no whole group
+        const int j = x & 7, b = (x >> 3) % NB, r = (x >> 3) / NB;
+        const int64_t s = slot[r + 3];
+        if (s < 0 || begins(r - (int)(s & 3))) continue;
+        uint8_t *tile = tile_of(s);
+        const int t = (int)(s & 31), at = b * 4 + (j >> 2);
+        if (j == 0) reinterpret_cast<uint16_t *>(tile + 34 * D)[v_scale(t, b, NB)] = scale[r][b];
+        const uint32_t lo = code[r][at] >> (8 * (j & 3)) & 0xff, hi = code[r][at + 2] >> (8 * (j & 3)) & 0xff;
+        *reinterpret_cast<uint16_t *>(tile + 18 * D + v_half(t, b, j, NB)) = (uint16_t)(lo | hi << 8);
+    }
+}
+
+// CTAs 0 .. k_blocks - 1 encode K, the others V (32 rows of a head each).
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const RowsParams p, int k_blocks) {
+    if ((int)blockIdx.x < k_blocks) {
+        append_k<D>(p, blockIdx.x);
+    } else {
+        const int64_t c = blockIdx.x - k_blocks;
+        append_v<D>(p, c / p.pool.Hk, (int)(c % p.pool.Hk));
     }
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
     constexpr int NB = D / 32;
-    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const bool is_v = blockIdx.y != 0;
     void *out = is_v ? p.vo : p.ko;
-    const int b = (int)(u % NB);
-    const int h = (int)(u / NB % p.pool.Hk);
-    const int64_t i = u / NB / p.pool.Hk;
-    if (i >= p.n || !out) return;
-    const int64_t slot = p.slots[i], at = (i * p.pool.Hk + h) * D + b * 32;
-    uint32_t w[4] = {0, 0, 0, 0};
-    float d = 0.f;
-    if (slot >= 0 && (slot >> p.pool.lgP) < p.pool.n_pages) {
-        const int tp = (int)(slot & (p.pool.P - 1)), t = tp & 31;
-        const uint8_t *tile = p.pool.pages + (slot >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes +
-                              (int64_t)(tp >> 5) * (36 * D);
-        d = __half2float(reinterpret_cast<const __half *>(tile + (is_v ? 34 : 16) * D)[is_v ? v_scale(t, b, NB) : k_scale(t, b, NB)]);
+    if (!out) return;
+    const int q = threadIdx.x & 3;
+    const Units units(blockIdx.x, NB * p.pool.Hk);
+    int64_t row[kInFlight], slot[kInFlight];
+    uint32_t in_row[kInFlight];
+    uint32_t w[kInFlight][2];  // K: bytes 8 (q % 2) .. + 7 of the block; V: [0] bytes 2q, 2q + 8, 2q + 1, 2q + 9
+    float d[kInFlight];
+#pragma unroll
+    for (int m = 0; m < kInFlight; ++m) {
+        const uint32_t u = units.rem + 64 * m + (threadIdx.x >> 2), r = u / units.per_row;
+        row[m] = units.row + r;
+        in_row[m] = u - r * units.per_row;
+        slot[m] = row[m] < p.n ? p.slots[row[m]] : -1;
+        if ((slot[m] >> p.pool.lgP) >= p.pool.n_pages) slot[m] = -1;
+    }
+#pragma unroll
+    for (int m = 0; m < kInFlight; ++m) {
+        w[m][0] = w[m][1] = 0;
+        d[m] = 0.f;
+        if (slot[m] < 0) continue;
+        const int b = in_row[m] % NB, h = in_row[m] / NB;
+        const int tp = (int)(slot[m] & (p.pool.P - 1)), t = tp & 31;
+        const uint8_t *tile = p.pool.pages + (slot[m] >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes + (int64_t)(tp >> 5) * (36 * D);
         if (!is_v) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, q, NB));
+            w[m][0] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1), NB));
+            w[m][1] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1) + 1, NB));
+            d[m] = __half2float(reinterpret_cast<const __half *>(tile + 16 * D)[k_scale(t, b, NB)]);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t x = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, j, NB));
-                w[j >> 2] |= (x & 0xff) << ((j & 3) * 8);
-                w[(j + 8) >> 2] |= (x >> 8) << ((j & 3) * 8);
-            }
+            w[m][0] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q, NB));
+            w[m][1] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q + 1, NB));
+            d[m] = __half2float(reinterpret_cast<const __half *>(tile + 34 * D)[v_scale(t, b, NB)]);
         }
     }
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        float f[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int j = (e + m) & 15;
-            f[m] = (float)((int)(w[j >> 2] >> ((j & 3) * 8 + ((e + m) >> 4) * 4) & 15) - 8) * d;
+    for (int m = 0; m < kInFlight; ++m) {
+        if (is_v) {
+            const uint32_t mine = w[m][0] | w[m][1] << 16;
+            const int base = threadIdx.x & 28;
+            const uint32_t sel = q & 1 ? 0x7531u : 0x6420u;  // bytes 8 .. 15 or 0 .. 7
+            const uint32_t m0 = __shfl_sync(0xffffffffu, mine, base), m1 = __shfl_sync(0xffffffffu, mine, base + 1);
+            const uint32_t m2 = __shfl_sync(0xffffffffu, mine, base + 2), m3 = __shfl_sync(0xffffffffu, mine, base + 3);
+            w[m][0] = __byte_perm(m0, m1, sel);
+            w[m][1] = __byte_perm(m2, m3, sel);
         }
-        if (d == 0.f) f[0] = f[1] = f[2] = f[3] = 0.f;
+        const int64_t at = (row[m] * units.per_row + in_row[m]) * 32 + 8 * q;
+        if (row[m] >= p.n) continue;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = d[m] == 0.f ? 0.f : (float)((int)(w[m][e >> 2] >> (8 * (e & 3) + (q < 2 ? 0 : 4)) & 15) - 8) * d[m];
         if (p.dtype == KVS_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(out) + at + e) = make_float4(f[0], f[1], f[2], f[3]);
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-            uint2 o;
-            if (p.dtype == KVS_F16) {
-                const __half2 a = __floats2half2_rn(f[0], f[1]), c = __floats2half2_rn(f[2], f[3]);
-                o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
-            } else {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), c = __floats2bfloat162_rn(f[2], f[3]);
-                o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (p.dtype == KVS_F16) {
+                    const __half2 a = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+                    o[e] = *reinterpret_cast<const uint32_t *>(&a);
+                } else {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                    o[e] = *reinterpret_cast<const uint32_t *>(&a);
+                }
             }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at + e) = o;
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -884,56 +1044,78 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     }
 }
 
-// One warp per (sequence, kv head, row): joins the partials of a (sequence,
-// head) that several workers shared; rows of empty sequences are written here.
+// One CTA per (sequence, kv head, row): joins the partials of a (sequence,
+// head) that several workers shared, its warps each a part of them; rows of
+// empty sequences are written here.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(256) combine_kernel(const AttendParams p, int pass_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendParams p, int pass_rows) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float part[kJoinWarps][D + 1];
     int2 *prefix = reinterpret_cast<int2 *>(smem);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
-    const int lane = threadIdx.x & 31;
     const int rows = p.R * p.G;
-    const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (id >= (int64_t)p.n_seq * p.pool.Hk * rows) return;
-    const int rho = (int)(id % rows), h = (int)(id / rows % p.pool.Hk), s = (int)(id / rows / p.pool.Hk);
+    const int rho = blockIdx.x % rows, h = blockIdx.x / rows % p.pool.Hk, s = blockIdx.x / rows / p.pool.Hk;
     const int T = prefix[s + 1].x - prefix[s].x;
     const int64_t orow = ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G;
-    float o[D / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: the call ends after the attention has
+    if (T == 0) {
+        for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) put(p.out, p.dtype, orow * D + i, 0.f);
+        if (threadIdx.x == 0 && p.lse) p.lse[orow] = -INFINITY;
+        return;
+    }
+    const int64_t c0 = head_cost(prefix[s], p.pool.Hk) + (int64_t)h * (T + kHeadCost);
+    const int w0 = cut.worker_of(c0 + kHeadCost), w1 = cut.worker_of(c0 + kHeadCost + T - 1);
+    if (w0 == w1) return;  // one worker had it all and wrote it
+    const int rb = rho / pass_rows, row = rho % pass_rows;
+    // the head is its last one for w0 if w0 also has the tile before it
+    const int after = c0 > 0 && cut.worker_of(c0 - 1) == w0;
+    auto slot_of = [&](int w) { return (((int64_t)rb * p.workers + w) * 2 + (w == w0 ? after : 0)) * pass_rows + row; };
+    float top = -INFINITY;
+    for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, p.part_rl[slot_of(w)].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    const float r0 = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, o[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    float lse = -INFINITY;
-    if (T > 0) {
-        const int64_t c0 = head_cost(prefix[s], p.pool.Hk) + (int64_t)h * (T + kHeadCost);
-        const int w0 = cut.worker_of(c0 + kHeadCost), w1 = cut.worker_of(c0 + kHeadCost + T - 1);
-        if (w0 == w1) return;  // one worker had it all and wrote it
-        const int rb = rho / pass_rows, row = rho % pass_rows;
-        float top = -INFINITY;
-        // the head is its last one for w0 if w0 also has the tile before it
-        const int after = c0 > 0 && cut.worker_of(c0 - 1) == w0;
-        auto slot_of = [&](int w) { return (((int64_t)rb * p.workers + w) * 2 + (w == w0 ? after : 0)) * pass_rows + row; };
-        for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, p.part_rl[slot_of(w)].x);
+    constexpr int kAtOnce = 4;  // partials a warp has in flight
+    for (int wb = w0 + warp; wb <= w1; wb += kJoinWarps * kAtOnce) {
+        float2 rl[kAtOnce];
+        float x[kAtOnce][D / 32];
 #pragma unroll
-        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        const float r0 = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-            const int64_t at = slot_of(w);
-            const float2 rl = p.part_rl[at];
-            const float f = exp2f(rl.x - r0);
-            sum = fmaf(rl.y, f, sum);
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int w = wb + u * kJoinWarps;
+            const int64_t at = slot_of(w <= w1 ? w : w1);
+            rl[u] = w <= w1 ? p.part_rl[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(p.part_o[at * D + i * 32 + lane], f, o[i]);
+            for (int i = 0; i < D / 32; ++i) x[u][i] = w <= w1 ? p.part_o[at * D + i * 32 + lane] : 0.f;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] *= inv;
-        if (sum != 0.f) lse = (r0 + log2f(sum)) * 0.693147180559945309f;
+        for (int u = 0; u < kAtOnce; ++u) {
+            const float f = exp2f(rl[u].x - r0);
+            sum = fmaf(rl[u].y, f, sum);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(x[u][i], f, o[i]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) put(p.out, p.dtype, orow * D + i * 32 + lane, o[i]);
-    if (lane == 0 && p.lse) p.lse[orow] = lse;
+    for (int i = 0; i < D / 32; ++i) part[warp][i * 32 + lane] = o[i];
+    if (lane == 0) part[warp][D] = sum;
+    __syncthreads();
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) total += part[w][D];
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) x += part[w][i];
+        put(p.out, p.dtype, orow * D + i, x * inv);
+    }
+    if (threadIdx.x == 0 && p.lse) p.lse[orow] = total == 0.f ? -INFINITY : (r0 + log2f(total)) * 0.693147180559945309f;
 }
 
 // ---------------------------------------------------------------- weights
@@ -1216,11 +1398,12 @@ static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint6
     if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
     if (n && (!slots || !aligned(slots, 8))) return bad(KVS_ERR_INVALID, "slots null or misaligned");
     const uint64_t units = (uint64_t)pool->n_kv_head * (pool->head_dim / 32);
-    if (n > (0x7fffffffull * 256) / units) return bad(KVS_ERR_INVALID, "too many rows");
+    // (so that the launch's CTAs, 256 of K's and V's blocks each or 32 V rows of a head, stay below 2^31)
+    if (n > (1ull << 36) / units) return bad(KVS_ERR_INVALID, "too many rows");
     p->slots = slots;
     p->n = (int64_t)n;
     p->dtype = dtype;
-    *blocks = (unsigned)((n * units + 255) / 256);
+    *blocks = (unsigned)((n * units + 64 * kInFlight - 1) / (64 * kInFlight));
     return KVS_OK;
 }
 
@@ -1238,8 +1421,11 @@ extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slot
     p.v = v;
     p.k_stride = (int64_t)k_stride;
     p.v_stride = (int64_t)v_stride;
-    auto kernel = pool->head_dim == 64 ? append_kernel<64> : pool->head_dim == 128 ? append_kernel<128> : append_kernel<256>;
-    const cudaError_t ce = launch(kernel, dim3(blocks, 2), 256, 0, static_cast<cudaStream_t>(stream), false, p);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const uint32_t D = pool->head_dim;
+    const uint64_t v_blocks = (n + 31) / 32 * pool->n_kv_head;
+    const cudaError_t ce = launch(D == 64 ? append_kernel<64> : D == 128 ? append_kernel<128> : append_kernel<256>,
+                                  dim3((unsigned)(blocks + v_blocks)), 256, 0, st, false, p, (int)blocks);
     return ce == cudaSuccess ? KVS_OK : cuda_failed("append launch", ce);
 }
 
@@ -1288,7 +1474,7 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     if (e != cudaSuccess) return cuda_failed("attention launch", e);
     void (*c)(AttendParams, int) = D == 64 ? combine_kernel<64> : D == 128 ? combine_kernel<128> : combine_kernel<256>;
     const uint64_t rows = (uint64_t)n_seq * n_q_head * n_rows;
-    e = launch(c, dim3((unsigned)((rows + 7) / 8)), 256, ((int)n_seq + 1) * 8, st, true, p, 8 * sh.nt);
+    e = launch(c, dim3((unsigned)rows), kJoinWarps * 32, ((int)n_seq + 1) * 8, st, true, p, 8 * sh.nt);
     return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
 }
 

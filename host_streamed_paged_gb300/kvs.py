@@ -712,71 +712,97 @@ class KVStream:
 
 
 # ------------------------------------------------------------ batch operators on torch tensors
+# These run once or more per layer of a decode step, so their host cost counts: checks are plain comparisons and
+# the library's functions are called directly.
+
+_torch = None
+_DTYPES = {}
+
+
+def _t():
+    """torch, imported on first use (the context API above works without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.float32: KVS_F32, torch.float16: KVS_F16, torch.bfloat16: KVS_BF16})
+        _torch = torch
+    return _torch
+
 
 def _dtype_of(t) -> int:
-    import torch
-    try:
-        return {torch.float32: KVS_F32, torch.float16: KVS_F16, torch.bfloat16: KVS_BF16}[t.dtype]
-    except KeyError:
-        raise ValueError(f"unsupported dtype {t.dtype}") from None
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return dt
 
 
 def _row_stride(t, what):
     """Elements between rows of a [..., heads, D] tensor whose heads are contiguous and whose rows lie in one line."""
-    d = t.shape[-1]
-    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != d):
+    shape, stride = t.shape, t.stride()
+    heads, d = shape[-2], shape[-1]
+    if stride[-1] != 1 or (heads > 1 and stride[-2] != d):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
-    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
-        raise ValueError(f"{what}: rows must lie at one stride")
-    if t.dim() == 4 and t.shape[1] == 1:
-        rows, stride = t.shape[0], t.stride(0)
-    else:
-        rows, stride = t.shape[-3], t.stride(-3)
-    return stride if rows > 1 else max(stride, t.shape[-2] * d)
+    if len(shape) == 4:
+        if shape[1] == 1:
+            return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+        if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
+            raise ValueError(f"{what}: rows must lie at one stride")
+    return stride[-3] if shape[-3] > 1 else max(stride[-3], heads * d)
 
 
-def _need(t, name, dtype, device, shape=None):
-    """t is a contiguous tensor of that type, device and shape (None entries: any size)."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+def _need(t, name, dtype, device, shape):
+    """t is a contiguous tensor of that type, device and shape."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if shape is not None and (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-class _On:
-    """The device of a call's tensors as the current one, and its current stream."""
+def _need_rows(t, name, dtype, device, rows, dims):
+    """The same with `dims` dimensions, the first of size `rows` (None: any)."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if t.dim() != dims or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have {dims} dimensions{'' if rows is None else f', the first of size {rows}'}")
 
-    def __init__(self, t):
-        import torch
-        if t.device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        self.dev, self.cuda = t.device, torch.cuda
 
-    def __enter__(self):
-        self.prev = self.cuda.current_device()
-        if self.dev.index != self.prev:
-            self.cuda.set_device(self.dev)
-        return self.cuda.current_stream().cuda_stream
+def _stream_of(index) -> int:
+    """The current stream's handle on a device (without building a Stream object, which costs 3 us)."""
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else _torch.cuda.current_stream(index).cuda_stream
 
-    def __exit__(self, *exc):
-        if self.dev.index != self.prev:
-            self.cuda.set_device(self.prev)
+
+def _run(device, fn, *args):
+    """Call a library function on the device of its tensors and that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    cuda, here = _torch.cuda, device.index
+    if cuda.current_device() == here:
+        status = fn(*args, _stream_of(here))
+    else:
+        with cuda.device(device):
+            status = fn(*args, _stream_of(here))
+    if status != KVS_OK:
+        _check(None, status)
 
 
 def _prompt(q, k, v, cu, scale) -> kvs_prompt:
-    import torch
-    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    torch = _t()
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
         raise ValueError("q, k and v must be [rows][heads][head_dim] with the same rows and head_dim")
-    if k.dtype != q.dtype or k.device != q.device:
+    dt, dev = q.dtype, q.device
+    if k.dtype != dt or k.device != dev:
         raise ValueError("q, k and v must have one dtype and device")
-    if v is not None and (v.shape != k.shape or v.dtype != q.dtype or v.device != q.device):
+    if v is not None and (v.shape != ks or v.dtype != dt or v.device != dev):
         raise ValueError("v must be as k")
-    _need(cu, "cu", torch.int32, q.device, (None,))
-    if cu.numel() < 1:
+    _need_rows(cu, "cu", torch.int32, dev, None, 1)
+    n = cu.shape[0]
+    if n < 1:
         raise ValueError("cu must hold n_seq + 1 offsets")
-    return kvs_prompt(_ptr(q), _ptr(k), _ptr(v), _row_stride(q, "q"), _row_stride(k, "k"),
-                      0 if v is None else _row_stride(v, "v"), _ptr(cu), cu.numel() - 1, q.shape[0], q.shape[1],
-                      k.shape[1], q.shape[2], _dtype_of(q), 1.0 / math.sqrt(q.shape[2]) if scale is None else scale)
+    return kvs_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else None, _row_stride(q, "q"),
+                      _row_stride(k, "k"), _row_stride(v, "v") if v is not None else 0, cu.data_ptr(), n - 1, qs[0], qs[1],
+                      ks[1], qs[2], _dtype_of(q), qs[2] ** -0.5 if scale is None else scale)
 
 
 def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
@@ -786,18 +812,20 @@ def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
     rows cu[i] .. cu[i + 1] - 1.  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
     (undefined where those are allocated here).
     """
-    import torch
     p = _prompt(q, k, v, cu, scale)
+    shape = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
-        raise ValueError("out must be as q")
-    if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        out = _torch.empty(shape, dtype=q.dtype, device=q.device)
+        stride = shape[1] * shape[2]
     else:
-        _need(lse, "lse", torch.float32, q.device, q.shape[:2])
-    with _On(q) as stream:
-        kvs_prompt_attend(p, out, _row_stride(out, "out"), lse, stream)
+        if out.shape != shape or out.dtype != q.dtype or out.device != q.device:
+            raise ValueError("out must be as q")
+        stride = _row_stride(out, "out")
+    if lse is None:
+        lse = _torch.empty(shape[:2], dtype=_torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", _torch.float32, q.device, shape[:2])
+    _run(q.device, load().kvs_prompt_attend, ctypes.byref(p), out.data_ptr(), stride, lse.data_ptr())
     return out, lse
 
 
@@ -807,17 +835,18 @@ def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=No
     lse is prompt_attend's; window > 0 counts only each prompt's last window rows; prev (same shape) is added, and
     may be out.
     """
-    import torch
     p = _prompt(q, k, None, cu, scale)
-    _need(lse, "lse", torch.float32, q.device, q.shape[:2])
+    f32, dev = _torch.float32, q.device
+    _need(lse, "lse", f32, dev, q.shape[:2])
     shape = (p.n_seq, p.n_kv_head, int(width))
-    for name, t in (("prev", prev), ("out", out)):
-        if t is not None:
-            _need(t, name, torch.float32, q.device, shape)
+    if prev is not None:
+        _need(prev, "prev", f32, dev, shape)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
-    with _On(q) as stream:
-        kvs_prompt_weights(p, lse, int(window), prev, out, shape[2], stream)
+        out = _torch.empty(shape, dtype=f32, device=dev)
+    else:
+        _need(out, "out", f32, dev, shape)
+    _run(dev, load().kvs_prompt_weights, ctypes.byref(p), lse.data_ptr(), int(window),
+         prev.data_ptr() if prev is not None else None, out.data_ptr(), shape[2])
     return out
 
 
@@ -832,72 +861,69 @@ class Q4Cache:
     """
 
     def __init__(self, *, page_tokens, n_kv_head, head_dim, pages=None, n_pages=None, device="cuda"):
+        torch = _t()
         pool = kvs_q4_pool(0, 1, page_tokens, n_kv_head, head_dim)
         self.page_bytes = kvs_q4_query_sizes(pool)[0]
         if pages is None:
-            import torch
             pages = torch.zeros(int(n_pages) * self.page_bytes, dtype=torch.uint8, device=device)
         if pages.element_size() != 1 or not pages.is_contiguous() or pages.numel() % self.page_bytes:
             raise ValueError("pages must be a contiguous uint8 tensor of whole pages")
-        self.pages, self.n_pages = pages, pages.numel() // self.page_bytes
+        self.pages, self.n_pages, self.device = pages, pages.numel() // self.page_bytes, pages.device
         pool.pages, pool.n_pages = pages.data_ptr(), self.n_pages
         self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
+        self._ref, self._lib = ctypes.byref(pool), load()
         self._workspace = {}  # bytes by (rows, heads, dtype)
-
-    def _slots(self, slots):
-        import torch
-        _need(slots, "slots", torch.int64, self.pages.device, (None,))
-        return slots.numel()
 
     def append(self, slots, k, v):
         """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
-        n = self._slots(slots)
+        dev = self.device
+        _need_rows(slots, "slots", _torch.int64, dev, None, 1)
+        n = slots.shape[0]
         if k.shape != (n, self.n_kv_head, self.head_dim) or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v must be [n][n_kv_head][head_dim] of one dtype")
-        if k.device != self.pages.device or v.device != self.pages.device:
+        if k.device != dev or v.device != dev:
             raise ValueError("k and v must be on the cache's device")
-        with _On(self.pages) as stream:
-            kvs_q4_append(self.pool, slots, n, k, v, _dtype_of(k), _row_stride(k, "k"), _row_stride(v, "v"), stream)
+        _run(dev, self._lib.kvs_q4_append, self._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dtype_of(k),
+             _row_stride(k, "k"), _row_stride(v, "v"))
 
     def read(self, slots, dtype=None):
         """The values held in slots: (k, v), each [n][Hk][D] in dtype (default float32, which holds them exactly)."""
-        import torch
-        n = self._slots(slots)
-        dtype = torch.float32 if dtype is None else dtype
-        k, v = (torch.empty((n, self.n_kv_head, self.head_dim), dtype=dtype, device=self.pages.device) for _ in range(2))
-        with _On(self.pages) as stream:
-            kvs_q4_read(self.pool, slots, n, k, v, _dtype_of(k), stream)
+        dev = self.device
+        _need_rows(slots, "slots", _torch.int64, dev, None, 1)
+        n = slots.shape[0]
+        shape, dtype = (n, self.n_kv_head, self.head_dim), _torch.float32 if dtype is None else dtype
+        k, v = _torch.empty(shape, dtype=dtype, device=dev), _torch.empty(shape, dtype=dtype, device=dev)
+        _run(dev, self._lib.kvs_q4_read, self._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dtype_of(k))
         return k, v
 
     def _batch(self, table, lens, q):
-        import torch
-        dev = self.pages.device
-        if q.dim() != 4 or q.shape[3] != self.head_dim or q.device != dev:
+        dev = self.device
+        if len(q.shape) != 4 or q.shape[3] != self.head_dim or q.device != dev:
             raise ValueError("q must be [n_seq][rows][n_q_head][head_dim] on the cache's device")
-        _need(table, "table", torch.int32, dev, (q.shape[0], None))
-        _need(lens, "lens", torch.int32, dev, (q.shape[0],))
+        i32, n = _torch.int32, q.shape[0]
+        _need_rows(table, "table", i32, dev, n, 2)
+        _need_rows(lens, "lens", i32, dev, n, 1)
         return _dtype_of(q), _row_stride(q, "q")
 
     def attend(self, table, lens, q, scale=None, out=None, lse=None):
         """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens."""
-        import torch
         dt, stride = self._batch(table, lens, q)
-        n, rows, hq, d = q.shape
+        shape = q.shape
+        n, rows, hq, d = shape
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _torch.empty(shape, dtype=q.dtype, device=self.device)
         else:
-            _need(out, "out", q.dtype, q.device, q.shape)
+            _need(out, "out", q.dtype, q.device, shape)
         if lse is None:
-            lse = torch.empty((n, rows, hq), dtype=torch.float32, device=q.device)
+            lse = _torch.empty(shape[:3], dtype=_torch.float32, device=self.device)
         else:
-            _need(lse, "lse", torch.float32, q.device, (n, rows, hq))
+            _need(lse, "lse", _torch.float32, q.device, shape[:3])
         need = self._workspace.get((rows, hq, dt))
         if need is None:
             need = self._workspace[(rows, hq, dt)] = kvs_q4_query_sizes(self.pool, rows, hq, dt)[1]
-        with _On(q) as stream:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            kvs_q4_attend(self.pool, table, table.shape[1], lens, n, rows, hq, q, dt, stride,
-                          1.0 / math.sqrt(d) if scale is None else scale, out, lse, ws, need, stream)
+        ws = _torch.empty(need, dtype=_torch.uint8, device=self.device)
+        _run(self.device, self._lib.kvs_q4_attend, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows, hq,
+             q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), need)
         return out, lse
 
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
@@ -905,38 +931,40 @@ class Q4Cache:
 
         lse is attend's; width defaults to prev's, or to the tokens the table can hold; out may be prev.
         """
-        import torch
         dt, stride = self._batch(table, lens, q)
         n, rows, hq, d = q.shape
-        _need(lse, "lse", torch.float32, q.device, (n, rows, hq))
-        given = prev if prev is not None else out
+        f32, dev = _torch.float32, self.device
+        _need(lse, "lse", f32, dev, q.shape[:3])
         if width is None:
+            given = prev if prev is not None else out
             width = given.shape[-1] if given is not None else table.shape[1] * self.page_tokens
         shape = (n, self.n_kv_head, int(width))
-        for name, t in (("prev", prev), ("out", out)):
-            if t is not None:
-                _need(t, name, torch.float32, q.device, shape)
+        if prev is not None:
+            _need(prev, "prev", f32, dev, shape)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=q.device)
-        with _On(q) as stream:
-            kvs_q4_weights(self.pool, table, table.shape[1], lens, n, rows, hq, q, dt, stride,
-                           1.0 / math.sqrt(d) if scale is None else scale, lse, prev, out, shape[2], stream)
+            out = _torch.empty(shape, dtype=f32, device=dev)
+        else:
+            _need(out, "out", f32, dev, shape)
+        _run(dev, self._lib.kvs_q4_weights, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows, hq,
+             q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, lse.data_ptr(),
+             prev.data_ptr() if prev is not None else None, out.data_ptr(), shape[2])
         return out
 
     def evict(self, table, dst_table, lens, weights, keep, sinks=0, recent=0):
         """Keep the `keep` tokens of largest weight per sequence and kv head (kvs_q4_evict), compacted into dst_table's
         pages: (kept int32 [n_seq][Hk][keep], new_lens, kept_weights)."""
-        import torch
-        dev = self.pages.device
-        _need(weights, "weights", torch.float32, dev, (None, self.n_kv_head, None))
-        n = weights.shape[0]
-        _need(table, "table", torch.int32, dev, (n, None))
-        _need(dst_table, "dst_table", torch.int32, dev, (n, None))
-        _need(lens, "lens", torch.int32, dev, (n,))
-        with _On(self.pages) as stream:
-            kept = torch.empty((n, self.n_kv_head, keep), dtype=torch.int32, device=dev)
-            new_w = torch.empty((n, self.n_kv_head, keep), dtype=torch.float32, device=dev)
-            new_lens = torch.empty((n,), dtype=torch.int32, device=dev)
-            kvs_q4_evict(self.pool, table, table.shape[1], dst_table, dst_table.shape[1], lens, n, weights,
-                         weights.shape[2], keep, sinks, recent, kept, new_w, new_lens, stream)
+        dev, i32, hk = self.device, _torch.int32, self.n_kv_head
+        f32 = _torch.float32
+        _need_rows(weights, "weights", f32, dev, None, 3)
+        n, heads, width = weights.shape
+        if heads != hk:
+            raise ValueError("weights must be [n_seq][n_kv_head][width]")
+        _need_rows(table, "table", i32, dev, n, 2)
+        _need_rows(dst_table, "dst_table", i32, dev, n, 2)
+        _need_rows(lens, "lens", i32, dev, n, 1)
+        kept = _torch.empty((n, hk, keep), dtype=i32, device=dev)
+        new_w = _torch.empty((n, hk, keep), dtype=f32, device=dev)
+        new_lens = _torch.empty(n, dtype=i32, device=dev)
+        _run(dev, self._lib.kvs_q4_evict, self._ref, table.data_ptr(), table.shape[1], dst_table.data_ptr(), dst_table.shape[1],
+             lens.data_ptr(), n, weights.data_ptr(), width, keep, sinks, recent, kept.data_ptr(), new_w.data_ptr(), new_lens.data_ptr())
         return kept, new_lens, new_w
