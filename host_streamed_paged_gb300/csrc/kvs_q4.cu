@@ -78,6 +78,12 @@ __device__ __forceinline__ void load_row(const void *p, int dtype, int64_t i, fl
     }
 }
 
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------- layout (include/kvs.h, "Q4 page layout")
 
 __device__ __forceinline__ int k_word(int t, int b, int q, int NB) {  // byte offset of K bytes 4q .. 4q+3
@@ -116,32 +122,62 @@ __device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, float
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Q4_0 of a block whose dims 8 q .. 8 q + 7 lane q of its quad holds, in IEEE
 // fp32 steps in a fixed order, the same as kvs_append's V: m = the element of
 // largest |x| (lowest index on ties), d = m / -8, id = 1/d (0 if d == 0), code
 // = trunc(x * id + 8.5) within 0 .. 15.  Lane q gets bytes 4 w .. 4 w + 3 of
-// the block, w = 0, 2, 1, 3 for q = 0 .. 3.
+// the block, w = 0, 2, 1, 3 for q = 0 .. 3.  (The kernels below are bound by
+// instructions, so: m from the largest and the smallest element, in order only
+// where those tie; x / -8 is x * -0.125; the code is read off the mantissa of
+// the sum rounded down onto 2^23.)
 __device__ __forceinline__ uint32_t q4_word(const float *x, int q, float &d) {
-    float best = x[0], mag = fabsf(x[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        const float a = fabsf(x[i]);
-        if (a > mag) mag = a, best = x[i];
-    }
+    float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+    float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), fminf(x[6], x[7]));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, mag, o), b2 = __shfl_xor_sync(0xffffffffu, best, o);
-        if (m2 > mag || (m2 == mag && (q & o))) mag = m2, best = b2;
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     }
-    d = __fdiv_rn(best, -8.0f);
-    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
-    uint32_t c[2] = {0, 0};  // a code per byte
+    float m = hi > -lo ? hi : lo;
+    if (__any_sync(0xffffffffu, hi == -lo && hi != 0.f)) {  // both signs (some block of the warp): the first one decides
+        int first = 32;
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+            if (fabsf(x[i]) == hi) first = 8 * q + i;
+        const int mine = first;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+        float at = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (mine == 8 * q + i) at = x[i];
+        at = __shfl_sync(0xffffffffu, at, (threadIdx.x & 28) + (first >> 3 & 3));
+        if (hi == -lo) m = at;
+    }
+    d = __fmul_rn(m, -0.125f);
+    const float id = (d != 0.0f) ? __frcp_rn(d) : 0.0f;
+    uint32_t k[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        int k = __float2int_rz(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
-        k = k > 15 ? 15 : (k < 0 ? 0 : k);
-        c[i >> 2] |= (uint32_t)k << (8 * (i & 3));
+        const float u = fmaxf(__fadd_rn(__fmul_rn(x[i], id), 8.5f), 0.f);  // (NaN, of 0 / a scale below 2^-128: code 0)
+        const int r = __float_as_int(__fadd_rz(u, 8388608.f));
+        k[i] = (uint32_t)(r < 0x4b00000f ? r : 0x4b00000f);
     }
+    uint32_t c[2];  // a code per byte
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        c[i] = __byte_perm(__byte_perm(k[4 * i], k[4 * i + 1], 0x0040), __byte_perm(k[4 * i + 2], k[4 * i + 3], 0x0040), 0x5410);
     // lanes 0, 1 have the low nibbles of bytes 0-7, 8-15; lanes 2, 3 the high ones
     const uint32_t got = __shfl_xor_sync(0xffffffffu, q < 2 ? c[1] : c[0], 2);
     return q < 2 ? c[0] | got << 4 : got | c[1] << 4;
@@ -314,7 +350,7 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
     int64_t row[kInFlight], slot[kInFlight];
     uint32_t in_row[kInFlight];
     uint32_t w[kInFlight][2];  // K: bytes 8 (q % 2) .. + 7 of the block; V: [0] bytes 2q, 2q + 8, 2q + 1, 2q + 9
-    float d[kInFlight];
+    __half d[kInFlight];
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
         const uint32_t u = units.rem + 64 * m + (threadIdx.x >> 2), r = u / units.per_row;
@@ -325,8 +361,8 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
     }
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
-        w[m][0] = w[m][1] = 0;
-        d[m] = 0.f;
+        w[m][0] = w[m][1] = 0x88888888u;  // no slot: zeros
+        d[m] = __ushort_as_half(0);
         if (slot[m] < 0) continue;
         const int b = in_row[m] % NB, h = in_row[m] / NB;
         const int tp = (int)(slot[m] & (p.pool.P - 1)), t = tp & 31;
@@ -334,17 +370,17 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
         if (!is_v) {
             w[m][0] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1), NB));
             w[m][1] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1) + 1, NB));
-            d[m] = __half2float(reinterpret_cast<const __half *>(tile + 16 * D)[k_scale(t, b, NB)]);
+            d[m] = reinterpret_cast<const __half *>(tile + 16 * D)[k_scale(t, b, NB)];
         } else {
             w[m][0] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q, NB));
             w[m][1] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q + 1, NB));
-            d[m] = __half2float(reinterpret_cast<const __half *>(tile + 34 * D)[v_scale(t, b, NB)]);
+            d[m] = reinterpret_cast<const __half *>(tile + 34 * D)[v_scale(t, b, NB)];
         }
     }
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
         if (is_v) {
-            const uint32_t mine = w[m][0] | w[m][1] << 16;
+            const uint32_t mine = (w[m][0] & 0xffffu) | w[m][1] << 16;
             const int base = threadIdx.x & 28;
             const uint32_t sel = q & 1 ? 0x7531u : 0x6420u;  // bytes 8 .. 15 or 0 .. 7
             const uint32_t m0 = __shfl_sync(0xffffffffu, mine, base), m1 = __shfl_sync(0xffffffffu, mine, base + 1);
@@ -354,10 +390,32 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
         }
         const int64_t at = (row[m] * units.per_row + in_row[m]) * 32 + 8 * q;
         if (row[m] >= p.n) continue;
+        // a nibble in the mantissa under exponent 0x64 is 1024 + n: minus 1032, exact; times the scale, rounded once
+        uint32_t code[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t nib = (q < 2 ? w[m][e] : w[m][e] >> 4) & 0x0f0f0f0fu;
+            code[2 * e] = hsub2(__byte_perm(nib, 0x64646464u, 0x4140), 0x64086408u);
+            code[2 * e + 1] = hsub2(__byte_perm(nib, 0x64646464u, 0x4342), 0x64086408u);
+        }
+        if (p.dtype == KVS_F16) {
+            const __half2 s2 = __half2half2(d[m]);
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&code[e]), s2);
+                o[e] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            continue;
+        }
+        const float s1 = __half2float(d[m]);
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = d[m] == 0.f ? 0.f : (float)((int)(w[m][e >> 2] >> (8 * (e & 3) + (q < 2 ? 0 : 4)) & 15) - 8) * d[m];
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&code[e]));
+            f[2 * e] = v.x * s1, f[2 * e + 1] = v.y * s1;
+        }
         if (p.dtype == KVS_F32) {
             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
             dst[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -366,13 +424,8 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (p.dtype == KVS_F16) {
-                    const __half2 a = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
-                    o[e] = *reinterpret_cast<const uint32_t *>(&a);
-                } else {
-                    const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-                    o[e] = *reinterpret_cast<const uint32_t *>(&a);
-                }
+                const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                o[e] = *reinterpret_cast<const uint32_t *>(&a);
             }
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -516,11 +569,6 @@ __device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(*rein
 
 constexpr uint32_t kLoNib = 0x000f000fu, kHiNib = 0x00f000f0u;
 constexpr uint32_t kLoOff = 0x00080008u, kHiOff = 0x00800080u;  // 8 * 2^-24 and 128 * 2^-24 as f16 subnormals
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 
 // Query fragments of one pass: NT times 8 rows as the N side of the MMAs,
 // fp32 queries as f16 hi + lo (HL).
