@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     __shared__ uint32_t hist[kCopies][kBins + 1];  // a digit's counts; lanes of a warp count in different copies, since
                                                    // most weights share a few top digits
     __shared__ uint32_t sums[2][kBins];  // of the copies, read by the whole cluster; two, for digits in turn
-    __shared__ uint32_t total[kBins];
+    __shared__ uint32_t part[4][kBins];  // the cluster's counts, by two CTAs each
     __shared__ uint32_t count[K > 0 ? K : 1][kW];  // tokens above the threshold (high half) and equal to it, by row of 1024 and warp
     __shared__ uint32_t mine[2];         // this CTA's tokens above the threshold, and equal to it
     __shared__ uint32_t digit[2];
@@ -131,16 +131,20 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
             own[tid] = sum;
         }
         cl.sync();
-        if (tid < kBins) {
-            uint32_t sum = 0;
-            for (int r = 0; r < ranks; ++r) sum += *cl.map_shared_rank(&own[tid], r);
-            total[tid] = sum;
+        {
+            const int r = tid >> 8 << 1, bin = tid & 255;
+            const uint32_t a = r < ranks ? *cl.map_shared_rank(&own[bin], r) : 0u;
+            const uint32_t b = r + 1 < ranks ? *cl.map_shared_rank(&own[bin], r + 1) : 0u;
+            part[tid >> 8][bin] = a + b;
         }
         __syncthreads();
         if (warp == 0) {  // from the top: the digit at which the count reaches `left`
             uint32_t v[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += v[i] = total[255 - (lane * 8 + i)];
+            for (int i = 0; i < 8; ++i) {
+                const int bin = 255 - (lane * 8 + i);
+                sum += v[i] = part[0][bin] + part[1][bin] + part[2][bin] + part[3][bin];
+            }
             uint32_t inc = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

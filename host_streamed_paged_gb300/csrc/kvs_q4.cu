@@ -12,13 +12,14 @@
 //    factors are powers of two, taken back from the query (high-nibble dims
 //    / 16) and once from the result.
 //  - The codes' offset 8 leaves the sum: sum q (n - 8) = sum q n - 8 sum q.
-//    For scores -8 sum q is the accumulator's initial value per block; for
-//    outputs -8 sum p is one more MMA per block, over the same rounded p.
+//    For scores -8 sum q is the accumulator's initial value per block (with
+//    more than one tile of query rows it is taken off the codes); for outputs -8 sum p is one more MMA per block, over the same rounded p.
 //    (fp32 calls subtract it from V's codes: over a long flat softmax sum p n
 //    exceeds sum p (n - 8) a hundredfold, and its fp32 rounding would show.)
 //  - K's block scales multiply the fp32 block sums; V's multiply the softmax
 //    weights before those are rounded to f16, with a running power-of-two
-//    reference that keeps weight x scale at 2^8 .. 2^14 at its largest.
+//    reference that keeps weight x scale below 2^14 and, for scales of usual
+//    size, far above f16's smallest.
 // Scores are S^T = K Q^T (16 tokens x 8 query rows per MMA), outputs O^T = V^T P^T
 // (16 dims x 8 query rows): the query rows are the narrow side of both, so 8 rows
 // fill them.  Between the two a tile's scores turn from a thread's (token, two
@@ -449,8 +450,8 @@ struct AttendParams {
     const void *q;
     void *out;
     float *lse;
-    float *part_o;   // [row block][worker][2][8 NT][D]
-    float2 *part_rl; // [row block][worker][2][8 NT]
+    float *part_o;   // [row block][worker][2][NT][2 D / 32][lane][4]: accumulators of 8 rows, see attend_kernel
+    float2 *part_rl; // [row block][worker][2][NT][8]: reference exponent and sum of a row
     int table_width, n_seq, R, Hq, G;
     int dtype, row_blocks, workers;
     float scale_log2;
@@ -507,53 +508,58 @@ __device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_wid
 // as long as all the others.)
 constexpr int kHeadCost = 6;
 constexpr int kMinTiles = 2;  // per worker, while that leaves some idle
+// (The host refuses calls whose line could reach 2^31 units.)
 struct Cut {
-    int64_t tiles, cost;  // in all
-    int W;                // workers in use
+    uint32_t tiles, cost;  // in all
+    uint32_t W, q, r;      // workers in use; units of each, and how many have one more
     __device__ __forceinline__ Cut(const int2 *prefix, int n_seq, int Hk, int workers) {
-        tiles = (int64_t)prefix[n_seq].x * Hk;
-        cost = tiles + (int64_t)kHeadCost * prefix[n_seq].y * Hk;
-        const int64_t w = (tiles + kMinTiles - 1) / kMinTiles;
-        W = (int)(w < workers ? w : workers);
+        tiles = (uint32_t)prefix[n_seq].x * Hk;
+        cost = tiles + (uint32_t)(kHeadCost * prefix[n_seq].y * Hk);
+        W = min((tiles + kMinTiles - 1) / kMinTiles, (uint32_t)workers);
+        q = W ? cost / W : 0;
+        r = cost - q * W;
     }
-    __device__ __forceinline__ int64_t begin(int w) const {  // cost unit at which worker w begins
-        const int64_t q = cost / W, r = cost % W;
-        return w * q + (w < r ? w : r);
-    }
-    __device__ __forceinline__ int worker_of(int64_t unit) const {
-        const int64_t q = cost / W, r = cost % W, cut = r * (q + 1);
+    __device__ __forceinline__ uint32_t begin(uint32_t w) const { return w * q + min(w, r); }  // cost unit at which worker w begins
+    __device__ __forceinline__ int worker_of(uint32_t unit) const {
+        const uint32_t cut = r * (q + 1);
         return (int)(unit < cut ? unit / (q + 1) : r + (unit - cut) / q);
     }
 };
-__device__ __forceinline__ int64_t head_cost(int2 prefix, int Hk) { return ((int64_t)prefix.x + (int64_t)kHeadCost * prefix.y) * Hk; }
+__device__ __forceinline__ uint32_t head_cost(int2 prefix, int Hk) { return (uint32_t)(prefix.x + kHeadCost * prefix.y) * Hk; }
 // the last sequence whose tiles (cost) begin at or before `unit`
 template <bool COST>
-__device__ __forceinline__ int find_seq(const int2 *prefix, int n_seq, int Hk, int64_t unit) {
+__device__ __forceinline__ int find_seq(const int2 *prefix, int n_seq, int Hk, uint32_t unit) {
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((COST ? head_cost(prefix[mid], Hk) : (int64_t)prefix[mid].x * Hk) <= unit) lo = mid;
+        if ((COST ? head_cost(prefix[mid], Hk) : (uint32_t)prefix[mid].x * Hk) <= unit) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
 // tiles before the cost unit `unit`
-__device__ __forceinline__ int64_t tiles_before(const int2 *prefix, int n_seq, int Hk, int64_t unit, int64_t all) {
+__device__ __forceinline__ uint32_t tiles_before(const int2 *prefix, int n_seq, int Hk, uint32_t unit, uint32_t all) {
     if (unit >= head_cost(prefix[n_seq], Hk)) return all;
     const int s = find_seq<true>(prefix, n_seq, Hk, unit);
-    const int T = prefix[s + 1].x - prefix[s].x;
-    const int64_t in = unit - head_cost(prefix[s], Hk);
-    const int64_t h = in / (T + kHeadCost), o = in % (T + kHeadCost);
-    return (int64_t)prefix[s].x * Hk + h * T + (o > kHeadCost ? o - kHeadCost : 0);
+    const uint32_t T = prefix[s + 1].x - prefix[s].x;
+    const uint32_t in = unit - head_cost(prefix[s], Hk);
+    const uint32_t h = in / (T + kHeadCost), o = in - h * (T + kHeadCost);
+    return (uint32_t)prefix[s].x * Hk + h * T + (o > kHeadCost ? o - kHeadCost : 0);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = a * b + c, c kept
+__device__ __forceinline__ void mma_from(float *d, const float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -575,53 +581,82 @@ constexpr uint32_t kLoOff = 0x00080008u, kHiOff = 0x00800080u;  // 8 * 2^-24 and
 template <int D, int NT, bool HL>
 struct Query {
     static constexpr int NB = D / 32;
-    uint32_t hi[NT][NB][2][2];             // row g: [block][k-step][low nibbles' dims, high nibbles' dims / 16]
+    static constexpr bool kBias = NT == 1;  // else the offset leaves the codes: one subtraction then serves NT row tiles
+    uint32_t hi[NT][NB][2][2];              // row g: [block][k-step][low nibbles' dims, high nibbles' dims / 16]
     uint32_t lo[HL ? NT : 1][NB][2][2];
-    float2 bias[NT][NB];                   // rows 2t, 2t + 1: -8 * 2^-24 * sum of the block's operands
-    float fac[NT];                         // row g: accumulator -> log2 units
+    float bias[kBias ? NB : 1][4];          // as an accumulator: -8 * 2^-24 * sum of the block's operands
+    float fac[NT];                          // row g: accumulator -> log2 units (not negative)
 
-    // row rho of (sequence, kv head): query row rho / G, head h G + rho % G
-    __device__ __forceinline__ void load(const AttendParams &p, int s, int h, int rho0) {
+    // The rows of (sequence, kv head) from rho0 on as they lie in memory: row rho
+    // is query row rho / G, head h G + rho % G.  All loads are issued at once and
+    // without a branch (a row past the last is the last one again).
+    struct Raw {
+        uint4 f[HL ? NT : 1][HL ? NB : 1][2];
+        uint2 x[HL ? 1 : NT][HL ? 1 : NB][2];
+        __device__ __forceinline__ void load(const AttendParams &p, int s, int h, int rho0) {
+            const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int rho = min(rho0 + 8 * n + g, p.R * p.G - 1), r = rho / p.G;
+                const int64_t base = ((int64_t)s * p.R + r) * p.q_stride + (int64_t)(h * p.G + rho - r * p.G) * D + 4 * t;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if constexpr (HL) f[n][b][k] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + base + b * 32 + 16 * k);
+                        else x[n][b][k] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + base + b * 32 + 16 * k);
+                    }
+            }
+        }
+        // dims 4t .. 4t + 3 (k = 0), 16 + 4t .. (k = 1) of block b
+        __device__ __forceinline__ void get(int n, int b, int k, int dtype, float *y) const {
+            if constexpr (HL) {
+                const uint4 v = f[n][b][k];
+                y[0] = __uint_as_float(v.x), y[1] = __uint_as_float(v.y), y[2] = __uint_as_float(v.z), y[3] = __uint_as_float(v.w);
+            } else {
+                const float2 a = two(x[n][b][k].x, dtype), c = two(x[n][b][k].y, dtype);
+                y[0] = a.x, y[1] = a.y, y[2] = c.x, y[3] = c.y;
+            }
+        }
+    };
+
+    __device__ __forceinline__ void form(const AttendParams &p, const Raw &raw, int rho0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int rho = rho0 + 8 * n + g;
-            const bool valid = rho < p.R * p.G;
-            const int r = rho / p.G, hq = h * p.G + rho % p.G;
-            const int64_t base = ((int64_t)s * p.R + r) * p.q_stride + (int64_t)hq * D + 4 * t;
-            float x[NB][8], top = 0.f;
+            const bool valid = rho0 + 8 * n + g < p.R * p.G;
+            float top = 0.f;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if (valid) {
-                    load_row<4>(p.q, p.dtype, base + b * 32, x[b]);
-                    load_row<4>(p.q, p.dtype, base + b * 32 + 16, x[b] + 4);
-                } else {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
+                for (int k = 0; k < 2; ++k) {
+                    float y[4];
+                    raw.get(n, b, k, p.dtype, y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(y[i]));
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
-            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // a power of two that brings the row's largest element to 2^14 .. 2^15 (exact for
             // 16-bit elements down to 2^-28 of it; f16 then holds 2^-24 more below)
             int e = (int)(__float_as_uint(top) >> 23) - 127;
             e = e < -100 ? -100 : (e > 100 ? 100 : e);
-            const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            fac[n] = p.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - 14 + e) << 23);
+            const float f = valid ? copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2) : 0.f;
+            fac[n] = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + 24 - 14 + e) << 23);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float sum = 0.f;
+                float sum = 0.f, x[8];
+                raw.get(n, b, 0, p.dtype, x);
+                raw.get(n, b, 1, p.dtype, x + 4);
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     // k-step ks: low nibbles are dims 4t + ks and 4t + 2 + ks, high ones 16 further
-                    const float y[4] = {x[b][ks] * f, x[b][2 + ks] * f, x[b][4 + ks] * f, x[b][6 + ks] * f};
+                    const float y[4] = {x[ks] * f, x[2 + ks] * f, x[4 + ks] * f, x[6 + ks] * f};
                     const uint32_t a0 = pack(y[0], y[1]), a1 = pack(y[2] * 0.0625f, y[3] * 0.0625f);
                     sum += half_lo(a0) + half_hi(a0) + 16.f * (half_lo(a1) + half_hi(a1));
                     hi[n][b][ks][0] = a0;
                     hi[n][b][ks][1] = a1;
-                    if (HL) {
+                    if constexpr (HL) {
                         const uint32_t l0 = pack(y[0] - half_lo(a0), y[1] - half_hi(a0));
                         const uint32_t l1 = pack(y[2] * 0.0625f - half_lo(a1), y[3] * 0.0625f - half_hi(a1));
                         sum += half_lo(l0) + half_hi(l0) + 16.f * (half_lo(l1) + half_hi(l1));
@@ -629,10 +664,15 @@ struct Query {
                         lo[n][b][ks][1] = l1;
                     }
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum *= -8.f * 5.9604644775390625e-8f;
-                bias[n][b] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+                if constexpr (kBias) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum *= -8.f * 5.9604644775390625e-8f;
+                    bias[b][0] = bias[b][2] = __shfl_sync(0xffffffffu, sum, 8 * t);
+                    bias[b][1] = bias[b][3] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                    // (four registers, ready to be an MMA's C: the compiler would fold the pairs and copy them each time)
+                    asm volatile("" : "+f"(bias[b][0]), "+f"(bias[b][1]), "+f"(bias[b][2]), "+f"(bias[b][3]));
+                }
             }
         }
     }
@@ -641,48 +681,55 @@ struct Query {
     // acc[n] = {(g, row 2t), (g, row 2t + 1), (g + 8, row 2t), (g + 8, row 2t + 1)}
     __device__ __forceinline__ void scores(const uint8_t *tile, int c, float (*acc)[4]) const {
         const int lane = threadIdx.x & 31, g = lane >> 2;
-        uint32_t sc[NB], w[2][NB];
         const uint8_t *ps = tile + 16 * D + (c * 8 + g) * NB * 4;
-        if constexpr (NB == 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(ps);
-            sc[0] = v.x, sc[1] = v.y;
-            const uint4 k = *reinterpret_cast<const uint4 *>(tile + (c * 32 + lane) * 16);
-            w[0][0] = k.x, w[0][1] = k.y, w[1][0] = k.z, w[1][1] = k.w;
-        } else {
-#pragma unroll
-            for (int b = 0; b < NB; b += 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(ps + b * 4);
-                sc[b] = v.x, sc[b + 1] = v.y, sc[b + 2] = v.z, sc[b + 3] = v.w;
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const uint4 k = *reinterpret_cast<const uint4 *>(tile + (((2 * c + o) * (NB / 4) + b / 4) * 32 + lane) * 16);
-                    w[o][b] = k.x, w[o][b + 1] = k.y, w[o][b + 2] = k.z, w[o][b + 3] = k.w;
-                }
-            }
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        constexpr int kGroup = NB < 4 ? NB : 4;  // blocks fetched together
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t x0 = w[0][b] >> 8, x1 = w[1][b] >> 8;
-            const uint32_t a0 = w[0][b] & kLoNib, a1 = w[1][b] & kLoNib, a2 = w[0][b] & kHiNib, a3 = w[1][b] & kHiNib;
-            const uint32_t e0 = x0 & kLoNib, e1 = x1 & kLoNib, e2 = x0 & kHiNib, e3 = x1 & kHiNib;
-            const float s0 = half_lo(sc[b]), s1 = half_hi(sc[b]);
+        for (int b0 = 0; b0 < NB; b0 += kGroup) {
+            uint32_t sc[kGroup], w[2][kGroup];
+            if constexpr (NB == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(ps);
+                sc[0] = v.x, sc[1] = v.y;
+                const uint4 k = *reinterpret_cast<const uint4 *>(tile + (c * 32 + lane) * 16);
+                w[0][0] = k.x, w[0][1] = k.y, w[1][0] = k.z, w[1][1] = k.w;
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4 *>(ps + b0 * 4);
+                sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float d[4] = {bias[n][b].x, bias[n][b].y, bias[n][b].x, bias[n][b].y};
-                mma(d, a0, a1, a2, a3, hi[n][b][0][0], hi[n][b][0][1]);
-                mma(d, e0, e1, e2, e3, hi[n][b][1][0], hi[n][b][1][1]);
-                if constexpr (HL) {
-                    mma(d, a0, a1, a2, a3, lo[n][b][0][0], lo[n][b][0][1]);
-                    mma(d, e0, e1, e2, e3, lo[n][b][1][0], lo[n][b][1][1]);
+                for (int o = 0; o < 2; ++o) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(tile + (((2 * c + o) * (NB / 4) + b0 / 4) * 32 + lane) * 16);
+                    w[o][0] = k.x, w[o][1] = k.y, w[o][2] = k.z, w[o][3] = k.w;
                 }
-                acc[n][0] = fmaf(d[0], s0, acc[n][0]);
-                acc[n][1] = fmaf(d[1], s0, acc[n][1]);
-                acc[n][2] = fmaf(d[2], s1, acc[n][2]);
-                acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                const int b = b0 + i;
+                const uint32_t x0 = w[0][i] >> 8, x1 = w[1][i] >> 8;
+                uint32_t a0 = w[0][i] & kLoNib, a1 = w[1][i] & kLoNib, a2 = w[0][i] & kHiNib, a3 = w[1][i] & kHiNib;
+                uint32_t e0 = x0 & kLoNib, e1 = x1 & kLoNib, e2 = x0 & kHiNib, e3 = x1 & kHiNib;
+                if constexpr (!kBias) {
+                    a0 = hsub2(a0, kLoOff), a1 = hsub2(a1, kLoOff), a2 = hsub2(a2, kHiOff), a3 = hsub2(a3, kHiOff);
+                    e0 = hsub2(e0, kLoOff), e1 = hsub2(e1, kLoOff), e2 = hsub2(e2, kHiOff), e3 = hsub2(e3, kHiOff);
+                }
+                const float s0 = half_lo(sc[i]), s1 = half_hi(sc[i]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float d[4];
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_from(d, kBias ? bias[kBias ? b : 0] : zero, a0, a1, a2, a3, hi[n][b][0][0], hi[n][b][0][1]);
+                    mma(d, e0, e1, e2, e3, hi[n][b][1][0], hi[n][b][1][1]);
+                    if constexpr (HL) {
+                        mma(d, a0, a1, a2, a3, lo[n][b][0][0], lo[n][b][0][1]);
+                        mma(d, e0, e1, e2, e3, lo[n][b][1][0], lo[n][b][1][1]);
+                    }
+                    acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+                    acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+                    acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+                    acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+                }
             }
         }
     }
@@ -692,6 +739,35 @@ struct Query {
 // place c ^ turn(r).  Writes (rows 2t or 2t + 1, tokens g) and reads (rows g,
 // chunks t) of a warp both hit every bank once.
 __device__ __forceinline__ int turn(int r) { return (r & 6) ^ ((r & 1) << 2); }
+
+// A power of two above the V scales a worker has met in a (sequence, head), by
+// the highest bit that any of their exponent fields has set: the field is below
+// 16, 8, 4, 2 or 1, so that one OR of the packed scales and one AND test them.
+// (Scales of 2 and more share that bit and are bounded one by one.)
+struct ScaleBound {
+    uint32_t over;  // exponent bits (of both halves) that no scale so far has; all ones: no scale yet
+    float lg;       // |scale| < 2^lg
+    __device__ __forceinline__ void reset() {
+        over = ~0u;
+        lg = -14.f;
+    }
+    // bits: the OR of scales over the warp; most: of this lane's scales the largest (for those of 2 and more)
+    __device__ __forceinline__ void raise(uint32_t bits, float most) {
+        const uint32_t e = (bits | bits >> 16) & 0x7c00u;
+        float to = e & 0x2000u ? 1.f : e & 0x1000u ? -7.f : e & 0x0800u ? -11.f : e & 0x0400u ? -13.f : -14.f;
+        uint32_t o = e & 0x2000u ? 0x4000u : e & 0x1000u ? 0x6000u : e & 0x0800u ? 0x7000u : e & 0x0400u ? 0x7800u : 0x7c00u;
+        if (e & 0x4000u) {
+#pragma unroll
+            for (int k = 16; k; k >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+            to = fminf(fmaxf((float)((int)(__float_as_uint(most) >> 23) - 126), 1.f), 16.f);  // (f16 ends below 2^16)
+            o = 0x4000u;
+        }
+        if (to >= lg) {
+            lg = to;
+            over = o | o << 16;
+        }
+    }
+};
 
 // A warp's stages in shared memory and the bulk copies into them.
 template <int BYTES, int NST>
@@ -748,40 +824,13 @@ struct Stages {
     }
 };
 
-// A worker's place in the line of tiles: sequence, head, tile, and the pages ahead.
-struct Cursor {
-    int s, h, k, T;       // tile k of T of (s, h)
-    int page_base, page;  // lane l holds page number page_base + l of the sequence
-    __device__ __forceinline__ void load_pages(const Pool &pool, const int32_t *table, int width, int tiles_per_page_lg) {
-        const int lane = threadIdx.x & 31;
-        page_base = k >> tiles_per_page_lg;
-        const int at = page_base + lane;
-        page = at < width ? table[(int64_t)s * width + at] : -1;
-    }
-    __device__ __forceinline__ void seek(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq,
-                                         int64_t unit, int lg) {
-        s = find_seq<false>(prefix, n_seq, pool.Hk, unit);
-        T = prefix[s + 1].x - prefix[s].x;
-        const int64_t in = unit - (int64_t)prefix[s].x * pool.Hk;
-        h = (int)(in / T);
-        k = (int)(in % T);
-        load_pages(pool, table, width, lg);
-    }
-    // the tile's bytes (null: a page number outside the pool), warp-uniform
-    __device__ __forceinline__ const uint8_t *tile(const Pool &pool, const int32_t *table, int width, int lg, int tile_bytes) {
-        const int at = k >> lg;
-        if (at - page_base >= 32) load_pages(pool, table, width, lg);
-        const int pg = __shfl_sync(0xffffffffu, page, at - page_base);
-        if (pg < 0 || pg >= pool.n_pages) return nullptr;
-        return pool.pages + pg * pool.page_bytes + h * pool.head_bytes + (int64_t)(k & ((1 << lg) - 1)) * tile_bytes;
-    }
-    __device__ __forceinline__ void next(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq, int lg) {
-        if (++k < T) return;
+// A place in the line of tiles: tile k of T of (sequence, head).
+struct Place {
+    int s, h, k, T;
+    __device__ __forceinline__ bool next(const int2 *prefix, int n_seq, int Hk) {  // whether (s, h) changed
+        if (++k < T) return false;
         k = 0;
-        if (++h < pool.Hk) {
-            load_pages(pool, table, width, lg);
-            return;
-        }
+        if (++h < Hk) return true;
         h = 0;
         do {
             ++s;
@@ -789,10 +838,47 @@ struct Cursor {
         if (s >= n_seq) {  // past the last tile: never fetched
             s = n_seq - 1;
             T = 1 << 30;
-            return;
+            return false;
         }
         T = prefix[s + 1].x - prefix[s].x;
+        return true;
+    }
+};
+
+// The same with the pages ahead, for the copies.
+struct Cursor : Place {
+    int page_base, page;  // lane l holds page number page_base + l of the sequence
+    int page_at;          // the page (of the sequence) that base points into; -1: none yet
+    const uint8_t *base;
+    __device__ __forceinline__ void load_pages(const Pool &pool, const int32_t *table, int width, int tiles_per_page_lg) {
+        const int lane = threadIdx.x & 31;
+        page_base = k >> tiles_per_page_lg;
+        page_at = -1;
+        const int at = page_base + lane;
+        page = at < width ? table[(int64_t)s * width + at] : -1;
+    }
+    __device__ __forceinline__ void seek(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq,
+                                         uint32_t unit, int lg) {
+        s = find_seq<false>(prefix, n_seq, pool.Hk, unit);
+        T = prefix[s + 1].x - prefix[s].x;
+        const uint32_t in = unit - (uint32_t)prefix[s].x * pool.Hk;
+        h = (int)(in / (uint32_t)T);
+        k = (int)(in - (uint32_t)h * (uint32_t)T);
         load_pages(pool, table, width, lg);
+    }
+    // the tile's bytes (null: a page number outside the pool), warp-uniform
+    __device__ __forceinline__ const uint8_t *tile(const Pool &pool, const int32_t *table, int width, int lg, int tile_bytes) {
+        const int at = k >> lg;
+        if (at != page_at) {
+            if (at - page_base >= 32) load_pages(pool, table, width, lg);
+            const int pg = __shfl_sync(0xffffffffu, page, at - page_base);
+            base = pg < 0 || pg >= pool.n_pages ? nullptr : pool.pages + pg * pool.page_bytes + h * pool.head_bytes;
+            page_at = at;
+        }
+        return base ? base + (k & ((1 << lg) - 1)) * tile_bytes : nullptr;
+    }
+    __device__ __forceinline__ void advance(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq, int lg) {
+        if (next(prefix, n_seq, pool.Hk)) load_pages(pool, table, width, lg);
     }
 };
 
@@ -800,26 +886,28 @@ template <int D>
 __host__ __device__ constexpr int stages_of() {
     return D == 64 ? 4 : 3;
 }
+// bytes per warp for turned scores beyond the tile's own
+__host__ __device__ constexpr int turn_bytes(int D, int NT) { return NT * 1024 > 8 * D ? NT * 1024 : 0; }
 template <int D, int NT, bool HL>
 __host__ __device__ constexpr int ctas_per_sm() {
-    return D == 256 ? 2 : (NT == 2 ? 3 : (D == 128 && HL ? 3 : 4));
+    return D == 256 ? 2 : (D == 128 || NT == 2 ? 3 : 4);
 }
 
 template <int D, int NT, bool HL>
 __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_kernel(const AttendParams p) {
-    constexpr int NB = D / 32, NST = stages_of<D>(), BYTES = 36 * D;
+    constexpr int NB = D / 32, NST = stages_of<D>(), BYTES = 36 * D, kTurnBytes = turn_bytes(D, NT);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * NST];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + kTurnBytes));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int rb = blockIdx.x % p.row_blocks;
     const int w = (int)(blockIdx.x / p.row_blocks) * kWarps + warp;
-    if (w >= cut.W) return;
-    const int64_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
-    const int64_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
+    if (w >= (int)cut.W) return;
+    const uint32_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
+    const uint32_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
     if (u0 >= u1) return;
     const int lg = p.pool.lgP - 5;
     const int rho0 = rb * 8 * NT;
@@ -827,35 +915,44 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     Stages<BYTES, NST> st;
     st.init(smem + warp * NST * BYTES, bars + warp * NST);
     uint32_t phases = 0;
-    Cursor ahead, at;
+    Cursor ahead;
     ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
-    at = ahead;
+    Place at = ahead;
     const int units = (int)(u1 - u0);
     int fetched = 0;
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
         if (fetched < units) {
             st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
-            ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
             ++fetched;
         }
     }
     Query<D, NT, HL> q;
-    float O[NT][NB][2][4], cs[NT][4], ref[NT], l[NT];  // cs: row b (< 8) holds block b's -8 * 2^-24 * sum p s
+    // cs: block b's -8 * 2^-24 * sum p s, in an accumulator of its own or in row b of one
+    constexpr bool kOwnSum = NT == 1 && D <= 128;
+    constexpr int kSums = kOwnSum ? NB : 1;
+    float O[NT][NB][2][4], cs[NT][kSums][4], ref[NT], l[NT];
     bool fresh = true;
     int k_first = 0, len = 0;
+    ScaleBound bound;
     int stage = 0;
     for (int unit = 0; unit < units; ++unit) {
         if (fresh) {  // a new (sequence, head)
-            q.load(p, at.s, at.h, rho0);
-            k_first = at.k;
+            typename Query<D, NT, HL>::Raw raw;
+            raw.load(p, at.s, at.h, rho0);  // the tiles' copies are under way
             len = seq_len(p.pool, p.lens, p.table_width, at.s);
+            q.form(p, raw, rho0);
+            k_first = at.k;
+            bound.reset();
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 ref[n] = -INFINITY;
                 l[n] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cs[n][i] = 0.f;
+                for (int b = 0; b < kSums; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cs[n][b][i] = 0.f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -869,86 +966,63 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
             if (st.gave_up) break;
         } else {
             const uint8_t *tile = st.buf + stage * BYTES;
-            // the turned scores take the place of the tile's K codes once those are read (at D = 64 they are too small)
-            float *turned = reinterpret_cast<float *>(D == 64 ? smem + kWarps * NST * BYTES + warp * 1024 : const_cast<uint8_t *>(tile));
+            // the turned scores (1 KB per 8 rows) take the place of the K codes that are read first, where those are as
+            // many bytes (8 D), else an area of their own
+            float *turned = reinterpret_cast<float *>(kTurnBytes ? smem + kWarps * NST * BYTES + warp * kTurnBytes : const_cast<uint8_t *>(tile));
             const int in_tile = len - at.k * kTile;  // tokens of the sequence from this tile on
-            float x[NT][8];  // row g, tokens 16 c + 4 t + (0 .. 3) at 4 c
-            {
-                float acc[2][NT][4];
+            // Scores, 16 tokens at a time, into the turned tile.  (With 16 rows a pass the loops over the halves stay
+            // rolled: unrolled, the live values exceed the registers, 237 against 175 us.)
+            constexpr int kUnroll = NT == 1 ? 2 : 1;
+#pragma unroll kUnroll
+            for (int c = 0; c < 2; ++c) {
+                float acc[NT][4];
+                q.scores(tile, c, acc);
+                __syncwarp();  // the K codes of these tokens have been read by every lane
 #pragma unroll
-                for (int c = 0; c < 2; ++c) q.scores(tile, c, acc[c]);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    __syncwarp();  // the area's last readers are done (for n = 0: of the K codes)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = 2 * t + (i & 1), tok = 16 * c + 8 * (i >> 1) + g;
-                            turned[row * 32 + (((tok >> 2) ^ turn(row)) << 2) + (tok & 3)] = acc[c][n][i];
-                        }
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float4 v = *reinterpret_cast<const float4 *>(turned + g * 32 + (((4 * c + t) ^ turn(g)) << 2));
-                        x[n][4 * c] = v.x * q.fac[n], x[n][4 * c + 1] = v.y * q.fac[n];
-                        x[n][4 * c + 2] = v.z * q.fac[n], x[n][4 * c + 3] = v.w * q.fac[n];
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 2 * t + (i & 1), tok = 16 * c + 8 * (i >> 1) + g;
+                        turned[n * 256 + row * 32 + (((tok >> 2) ^ turn(row)) << 2) + (tok & 3)] = acc[n][i];
                     }
-                }
             }
-            // V scales of tokens 16 c + 4 t + (0 .. 3); of tokens never written they may be anything and count as 0
-            auto v_scales = [&](int c, uint2 *vs) {
+            __syncwarp();
+            // row g, tokens 16 c + 4 t + (0 .. 3), not yet times fac; -inf for those the row does not see
+            const bool masked = in_tile - (p.R - 1) < kTile;
+            auto row_scores = [&](int n, int c, float *x) {
+                const float4 v = *reinterpret_cast<const float4 *>(turned + n * 256 + g * 32 + (((4 * c + t) ^ turn(g)) << 2));
+                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                if (masked) {
+                    const int see = in_tile - (p.R - 1) + (rho0 + 8 * n + g) / p.G - 16 * c - 4 * t;
 #pragma unroll
-                for (int b = 0; b < NB; b += 2) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + 34 * D + ((c * 4 + t) * NB + b) * 8);
-                    vs[b] = make_uint2(v.x, v.y);
-                    vs[b + 1] = make_uint2(v.z, v.w);
-                }
-                if (in_tile < kTile) {
-                    const int left = in_tile - 16 * c - 4 * t;
-                    const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-                    const uint32_t k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        vs[b].x &= k0;
-                        vs[b].y &= k1;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (i >= see) x[i] = -INFINITY;
                 }
             };
-            if (in_tile - (p.R - 1) < kTile) {  // some row does not see the whole tile
+            if (bound.over == ~0u) {  // the head's first tile sets the bound
+                uint32_t any = 0;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int see = in_tile - (p.R - 1) + (rho0 + 8 * n + g) / p.G;  // tokens of the tile this row sees
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (16 * (i >> 2) + 4 * t + (i & 3) >= see) x[n][i] = -INFINITY;
+                for (int i = lane; i < NB * 8; i += 32) {
+                    uint2 v = reinterpret_cast<const uint2 *>(tile + 34 * D)[i];
+                    const int left = in_tile - 4 * (i / NB);  // of its four tokens
+                    if (left < 4) {
+                        v.x &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                        v.y &= left > 2 ? 0xffffu : 0u;
+                    }
+                    any |= v.x | v.y;
                 }
+                bound.raise(__reduce_or_sync(0xffffffffu, any), 0.f);
             }
-            // the tile's largest |V scale| as a power of two, rounded up
-            __half2 sm = __float2half2_rn(0.f);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint2 vs[NB];
-                v_scales(c, vs);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[b].x)));
-                    sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2 *>(&vs[b].y)));
-                }
-            }
-            float smax = fmaxf(__low2float(sm), __high2float(sm));
-            smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 1));
-            smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 2));
-            const float lg_s = (float)((int)(__float_as_uint(fmaxf(smax, 5.9604644775390625e-8f)) >> 23) - 126);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float mx = x[n][0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[n][i]);
+                float x[8];
+                row_scores(n, 0, x);
+                row_scores(n, 1, x + 4);
+                float mx = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // largest weight x scale of the tile is below 2^(need - ref): kept at 2^14 at most
-                const float need = mx + lg_s;
+                // weight x scale is below 2^(need - ref): kept at 2^14 at most
+                const float need = mx * q.fac[n] + bound.lg;
                 const bool grow = need - 14.f > ref[n];
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to = grow ? need - 8.f : ref[n];
@@ -959,7 +1033,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float al = (i & 1) ? a1 : a0;
-                        cs[n][i] *= al;
+#pragma unroll
+                        for (int b = 0; b < kSums; ++b) cs[n][b][i] *= al;
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             O[n][b][0][i] *= al;
@@ -967,49 +1042,88 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                         }
                     }
                 }
-                const float r0 = ref[n] == -INFINITY ? 0.f : ref[n];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[n][i] = ex2(x[n][i] - r0);
-                    l[n] += x[n][i];
-                }
             }
-            // O^T += V^T (p s)^T, 16 tokens at a time
-#pragma unroll
+            // O^T += V^T (p s)^T, 16 tokens and two blocks at a time
+#pragma unroll kUnroll
             for (int c = 0; c < 2; ++c) {
-                uint2 vs[NB];
-                v_scales(c, vs);
-                uint32_t vw[2 * NB];
+                float x[NT][4];
 #pragma unroll
-                for (int i = 0; i < NB / 2; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + 18 * D + ((c * (NB / 2) + i) * 32 + lane) * 16);
-                    vw[4 * i] = v.x, vw[4 * i + 1] = v.y, vw[4 * i + 2] = v.z, vw[4 * i + 3] = v.w;
+                for (int n = 0; n < NT; ++n) {
+                    row_scores(n, c, x[n]);
+                    const float r0 = ref[n] == -INFINITY ? 0.f : ref[n];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[n][i] = ex2(fmaf(x[n][i], q.fac[n], -r0));
+                        l[n] += x[n][i];
+                    }
                 }
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const float s0 = half_lo(vs[b].x), s1 = half_hi(vs[b].x);
-                    const float s2 = half_lo(vs[b].y), s3 = half_hi(vs[b].y);
-                    const uint32_t w0 = vw[2 * b], w1 = vw[2 * b + 1];
-                    uint32_t a0 = w0 & kLoNib, a1 = w0 & kHiNib, a2 = w1 & kLoNib, a3 = w1 & kHiNib;
-                    uint32_t e0 = (w0 >> 8) & kLoNib, e1 = (w0 >> 8) & kHiNib, e2 = (w1 >> 8) & kLoNib, e3 = (w1 >> 8) & kHiNib;
-                    if constexpr (HL) {  // n - 8 as it stands: sums of 0 .. 15 codes would leave their own rounding
-                        a0 = hsub2(a0, kLoOff), a2 = hsub2(a2, kLoOff), a1 = hsub2(a1, kHiOff), a3 = hsub2(a3, kHiOff);
-                        e0 = hsub2(e0, kLoOff), e2 = hsub2(e2, kLoOff), e1 = hsub2(e1, kHiOff), e3 = hsub2(e3, kHiOff);
+                for (int b0 = 0; b0 < NB; b0 += 2) {
+                    const uint4 sv = *reinterpret_cast<const uint4 *>(tile + 34 * D + ((c * 4 + t) * NB + b0) * 8);
+                    const uint4 vw = *reinterpret_cast<const uint4 *>(tile + 18 * D + ((c * (NB / 2) + b0 / 2) * 32 + lane) * 16);
+                    uint32_t vs[2][2] = {{sv.x, sv.y}, {sv.z, sv.w}};  // [block]: tokens 16 c + 4 t + (0, 1), (2, 3)
+                    if (in_tile < kTile) {  // scales of tokens never written may be anything and count as 0
+                        const int left = in_tile - 16 * c - 4 * t;
+                        const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                        const uint32_t k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+                        vs[0][0] &= k0, vs[1][0] &= k0, vs[0][1] &= k1, vs[1][1] &= k1;
+                    }
+                    // a scale beyond the bound kept so far (rare): everything so far is brought to the larger one
+                    const uint32_t any = vs[0][0] | vs[0][1] | vs[1][0] | vs[1][1];
+                    if (__any_sync(0xffffffffu, any & bound.over)) {
+                        float most = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            most = fmaxf(most, fmaxf(fabsf(half_lo(vs[i >> 1][i & 1])), fabsf(half_hi(vs[i >> 1][i & 1]))));
+                        const float was = bound.lg;
+                        bound.raise(__reduce_or_sync(0xffffffffu, any), most);
+                        const float up = bound.lg - was;
+                        if (up > 0.f) {
+                            const float f = __uint_as_float((uint32_t)(127 - (int)up) << 23);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                ref[n] += up;
+                                l[n] *= f;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[n][i] *= f;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                    for (int b = 0; b < kSums; ++b) cs[n][b][i] *= f;
+#pragma unroll
+                                    for (int b = 0; b < NB; ++b) O[n][b][0][i] *= f, O[n][b][1][i] *= f;
+                                }
+                            }
+                        }
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float y0 = x[n][4 * c] * s0, y1 = x[n][4 * c + 1] * s1;
-                        const float y2 = x[n][4 * c + 2] * s2, y3 = x[n][4 * c + 3] * s3;
-                        const uint32_t b0 = pack(y0, y1), b1 = pack(y2, y3);
-                        mma(O[n][b][0], a0, a1, a2, a3, b0, b1);
-                        mma(O[n][b][1], e0, e1, e2, e3, b0, b1);
-                        if constexpr (HL) {
-                            const uint32_t d0 = pack(y0 - half_lo(b0), y1 - half_hi(b0)), d1 = pack(y2 - half_lo(b1), y3 - half_hi(b1));
-                            mma(O[n][b][0], a0, a1, a2, a3, d0, d1);
-                            mma(O[n][b][1], e0, e1, e2, e3, d0, d1);
-                        } else {  // row b: -8 * 2^-24 (f16 subnormal) times the sum of the same operands
-                            const uint32_t eight = g == b ? kLoOff | 0x80008000u : 0u;
-                            mma(cs[n], eight, 0u, eight, 0u, b0, b1);
+                    for (int i = 0; i < 2; ++i) {
+                        const int b = b0 + i;
+                        const float s0 = half_lo(vs[i][0]), s1 = half_hi(vs[i][0]), s2 = half_lo(vs[i][1]), s3 = half_hi(vs[i][1]);
+                        const uint32_t w0 = i ? vw.z : vw.x, w1 = i ? vw.w : vw.y;
+                        uint32_t a0 = w0 & kLoNib, a1 = w0 & kHiNib, a2 = w1 & kLoNib, a3 = w1 & kHiNib;
+                        uint32_t e0 = (w0 >> 8) & kLoNib, e1 = (w0 >> 8) & kHiNib, e2 = (w1 >> 8) & kLoNib, e3 = (w1 >> 8) & kHiNib;
+                        if constexpr (HL) {  // n - 8 as it stands: sums of 0 .. 15 codes would leave their own rounding
+                            a0 = hsub2(a0, kLoOff), a2 = hsub2(a2, kLoOff), a1 = hsub2(a1, kHiOff), a3 = hsub2(a3, kHiOff);
+                            e0 = hsub2(e0, kLoOff), e2 = hsub2(e2, kLoOff), e1 = hsub2(e1, kHiOff), e3 = hsub2(e3, kHiOff);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float y0 = x[n][0] * s0, y1 = x[n][1] * s1, y2 = x[n][2] * s2, y3 = x[n][3] * s3;
+                            const uint32_t p0 = pack(y0, y1), p1 = pack(y2, y3);
+                            mma(O[n][b][0], a0, a1, a2, a3, p0, p1);
+                            mma(O[n][b][1], e0, e1, e2, e3, p0, p1);
+                            if constexpr (HL) {
+                                const uint32_t d0 = pack(y0 - half_lo(p0), y1 - half_hi(p0)), d1 = pack(y2 - half_lo(p1), y3 - half_hi(p1));
+                                mma(O[n][b][0], a0, a1, a2, a3, d0, d1);
+                                mma(O[n][b][1], e0, e1, e2, e3, d0, d1);
+                            } else if constexpr (kOwnSum) {  // -8 * 2^-24 (f16 subnormal) times the sum of the same operands
+                                constexpr uint32_t eight = kLoOff | 0x80008000u;
+                                mma(cs[n][b], eight, eight, eight, eight, p0, p1);
+                            } else {  // the same in row b
+                                const uint32_t eight = g == b ? kLoOff | 0x80008000u : 0u;
+                                mma(cs[n][0], eight, 0u, eight, 0u, p0, p1);
+                            }
                         }
                     }
                 }
@@ -1020,7 +1134,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
         const bool last_of_head = at.k + 1 == at.T;
         if (fetched < units) {
             st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
-            ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
             ++fetched;
         }
         stage = stage + 1 == NST ? 0 : stage + 1;
@@ -1034,14 +1148,29 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                 const float l0 = __shfl_sync(0xffffffffu, l[n], 8 * t), l1 = __shfl_sync(0xffffffffu, l[n], 8 * t + 4);
                 // a row that saw nothing: out 0, lse -inf
                 const float i0 = whole ? (l0 == 0.f ? 0.f : 1.f / l0) : 1.f, i1 = whole ? (l1 == 0.f ? 0.f : 1.f / l1) : 1.f;
-                const int64_t pslot = (((int64_t)rb * p.workers + w) * 2 + slot) * (8 * NT) + 8 * n;
+                float off[NB][2];  // of rows 2t, 2t + 1
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {  // heads (rows of the pass) 2t, 2t + 1
-                    const int row = 2 * t + c, rho = rho0 + 8 * n + row;
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        off[b][c] = kOwnSum ? cs[n][kOwnSum ? b : 0][c] : __shfl_sync(0xffffffffu, cs[n][0][c], b * 4 + t);
+                if (!whole) {  // the accumulators as they are, 16 bytes a lane
+                    const int64_t pslot = (((int64_t)rb * p.workers + w) * 2 + slot) * NT + n;
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o) + pslot * (2 * NB * 32) + lane;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            dst[(2 * b + m) * 32] = make_float4((O[n][b][m][0] + off[b][0]) * 16777216.f, (O[n][b][m][1] + off[b][1]) * 16777216.f,
+                                                                (O[n][b][m][2] * 0.0625f + off[b][0]) * 16777216.f,
+                                                                (O[n][b][m][3] * 0.0625f + off[b][1]) * 16777216.f);
+                    if (t == 0) p.part_rl[pslot * 8 + g] = make_float2(ref[n], l[n]);
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int rho = rho0 + 8 * n + 2 * t + c;
                     const float inv = (c ? i1 : i0) * 16777216.f;
-                    float off[NB];
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) off[b] = __shfl_sync(0xffffffffu, cs[n][c], b * 4 + t);
                     if (rho >= p.R * p.G) continue;
                     const int64_t orow = (((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G) * D;
 #pragma unroll
@@ -1049,32 +1178,22 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const int dim = b * 32 + 8 * m + g;
-                            const float lo = (O[n][b][m][c] + off[b]) * inv;
-                            const float hi = (O[n][b][m][2 + c] * 0.0625f + off[b]) * inv;
-                            if (whole) {
-                                put(p.out, p.dtype, orow + dim, lo);
-                                put(p.out, p.dtype, orow + dim + 16, hi);
-                            } else {
-                                p.part_o[(pslot + row) * D + dim] = lo;
-                                p.part_o[(pslot + row) * D + dim + 16] = hi;
-                            }
+                            put(p.out, p.dtype, orow + dim, (O[n][b][m][c] + off[b][c]) * inv);
+                            put(p.out, p.dtype, orow + dim + 16, (O[n][b][m][2 + c] * 0.0625f + off[b][c]) * inv);
                         }
                 }
                 const int rho = rho0 + 8 * n + g;
-                if (t == 0 && rho < p.R * p.G) {
-                    if (!whole) p.part_rl[pslot + g] = make_float2(ref[n], l[n]);
-                    else if (p.lse)
-                        p.lse[((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G] =
-                            l[n] == 0.f ? -INFINITY : (ref[n] + log2f(l[n])) * 0.693147180559945309f;
-                }
+                if (t == 0 && rho < p.R * p.G && p.lse)
+                    p.lse[((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G] =
+                        l[n] == 0.f ? -INFINITY : (ref[n] + log2f(l[n])) * 0.693147180559945309f;
             }
             fresh = true;
         }
-        at.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+        at.next(prefix, p.n_seq, p.pool.Hk);
     }
     if (st.gave_up) {  // what this worker owed is NaN: partials and whole rows of its range
         for (int i = lane; i < 2 * 8 * NT; i += 32)
-            p.part_rl[((int64_t)rb * p.workers + w) * 2 * (8 * NT) + i] = make_float2(0.f, __int_as_float(0x7fc00000));
+            p.part_rl[((int64_t)rb * p.workers + w) * 2 * (8 * NT) + i] = make_float2(0.f, __int_as_float(0x7fc00000));  // (the sum: NaN)
         Cursor c;
         c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
         for (int unit = 0; unit < units; ++unit) {
@@ -1084,7 +1203,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                     for (int d = lane; d < D; d += 32) put(p.out, p.dtype, row * D + d, __int_as_float(0x7fc00000));
                     if (lane == 0 && p.lse) p.lse[row] = __int_as_float(0x7fc00000);
                 }
-            c.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            c.next(prefix, p.n_seq, p.pool.Hk);
         }
         // copies still in flight land in this CTA's shared memory: give them the same time again
         st.gave_up = false;
@@ -1092,78 +1211,100 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     }
 }
 
-// One CTA per (sequence, kv head, row): joins the partials of a (sequence,
-// head) that several workers shared, its warps each a part of them; rows of
-// empty sequences are written here.
+// One CTA per (sequence, kv head, 8 rows of a pass, 64 dims): joins the
+// partials of a (sequence, head) that several workers shared, its warps each a
+// part of them, in the accumulators' own layout; rows of empty sequences are
+// written here.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinVecs = 4;    // of the 2 D / 32 vectors of a partial: 64 dims
+constexpr int kJoinAtOnce = 4;  // partials a warp has on their way
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendParams p, int pass_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendParams p, int nt) {
+    constexpr int kVec = 2 * D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float part[kJoinWarps][D + 1];
+    __shared__ float4 part[kJoinWarps][kJoinVecs * 32];
+    __shared__ float sums[kJoinWarps][8], refs[8];
     int2 *prefix = reinterpret_cast<int2 *>(smem);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
-    const int rows = p.R * p.G;
-    const int rho = blockIdx.x % rows, h = blockIdx.x / rows % p.pool.Hk, s = blockIdx.x / rows / p.pool.Hk;
+    const int rows = p.R * p.G, groups = (rows + 7) / 8, v0 = blockIdx.y * kJoinVecs, d0 = v0 * 16;
+    const int grp = blockIdx.x % groups, h = blockIdx.x / groups % p.pool.Hk, s = blockIdx.x / groups / p.pool.Hk;
     const int T = prefix[s + 1].x - prefix[s].x;
-    const int64_t orow = ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G;
+    auto row_at = [&](int rho) { return ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G; };
     asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: the call ends after the attention has
     if (T == 0) {
-        for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) put(p.out, p.dtype, orow * D + i, 0.f);
-        if (threadIdx.x == 0 && p.lse) p.lse[orow] = -INFINITY;
+        const int rho = 8 * grp + warp;
+        if (rho < rows) {
+            const int64_t orow = row_at(rho);
+            put(p.out, p.dtype, orow * D + d0 + lane, 0.f);
+            put(p.out, p.dtype, orow * D + d0 + 32 + lane, 0.f);
+            if (d0 == 0 && lane == 0 && p.lse) p.lse[orow] = -INFINITY;
+        }
         return;
     }
-    const int64_t c0 = head_cost(prefix[s], p.pool.Hk) + (int64_t)h * (T + kHeadCost);
+    const uint32_t c0 = head_cost(prefix[s], p.pool.Hk) + (uint32_t)h * (T + kHeadCost);
     const int w0 = cut.worker_of(c0 + kHeadCost), w1 = cut.worker_of(c0 + kHeadCost + T - 1);
     if (w0 == w1) return;  // one worker had it all and wrote it
-    const int rb = rho / pass_rows, row = rho % pass_rows;
+    const int rb = grp / nt, n = grp % nt;
     // the head is its last one for w0 if w0 also has the tile before it
     const int after = c0 > 0 && cut.worker_of(c0 - 1) == w0;
-    auto slot_of = [&](int w) { return (((int64_t)rb * p.workers + w) * 2 + (w == w0 ? after : 0)) * pass_rows + row; };
+    auto slot_of = [&](int w) { return (((int64_t)rb * p.workers + w) * 2 + (w == w0 ? after : 0)) * nt + n; };
+    // row g's largest reference
     float top = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, p.part_rl[slot_of(w)].x);
-#pragma unroll
-    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    for (int w = w0 + t; w <= w1; w += 4) top = fmaxf(top, p.part_rl[slot_of(w) * 8 + g].x);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float r0 = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o[D / 32];
+    float sum = 0.f;  // row g's (the same in the four lanes)
+    float4 o[kJoinVecs];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    constexpr int kAtOnce = 4;  // partials a warp has in flight
-    for (int wb = w0 + warp; wb <= w1; wb += kJoinWarps * kAtOnce) {
-        float2 rl[kAtOnce];
-        float x[kAtOnce][D / 32];
+    for (int i = 0; i < kJoinVecs; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int wb = w0 + warp; wb <= w1; wb += kJoinWarps * kJoinAtOnce) {
+        float2 rl[kJoinAtOnce];
+        float4 x[kJoinAtOnce][kJoinVecs];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
+        for (int u = 0; u < kJoinAtOnce; ++u) {
             const int w = wb + u * kJoinWarps;
             const int64_t at = slot_of(w <= w1 ? w : w1);
-            rl[u] = w <= w1 ? p.part_rl[at] : make_float2(-INFINITY, 0.f);
+            rl[u] = p.part_rl[at * 8 + g];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) x[u][i] = w <= w1 ? p.part_o[at * D + i * 32 + lane] : 0.f;
+            for (int i = 0; i < kJoinVecs; ++i)
+                x[u][i] = reinterpret_cast<const float4 *>(p.part_o)[at * (kVec * 32) + (v0 + i) * 32 + lane];
         }
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
+        for (int u = 0; u < kJoinAtOnce; ++u) {
+            if (wb + u * kJoinWarps > w1) break;
             const float f = exp2f(rl[u].x - r0);
             sum = fmaf(rl[u].y, f, sum);
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(x[u][i], f, o[i]);
+            for (int i = 0; i < kJoinVecs; ++i) {
+                o[i].x = fmaf(x[u][i].x, f0, o[i].x), o[i].y = fmaf(x[u][i].y, f1, o[i].y);
+                o[i].z = fmaf(x[u][i].z, f0, o[i].z), o[i].w = fmaf(x[u][i].w, f1, o[i].w);
+            }
         }
     }
+    if (t == 0) sums[warp][g] = sum;
+    if (warp == 0 && t == 0) refs[g] = r0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) part[warp][i * 32 + lane] = o[i];
-    if (lane == 0) part[warp][D] = sum;
+    for (int i = 0; i < kJoinVecs; ++i) part[warp][i * 32 + lane] = o[i];
     __syncthreads();
-    float total = 0.f;
+    for (int x = threadIdx.x; x < 8 * 64; x += kJoinWarps * 32) {
+        const int row = x >> 6, dim = x & 63, rho = 8 * grp + row;
+        if (rho >= rows) continue;
+        float total = 0.f, v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) total += part[w][D];
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) {
-        float x = 0.f;
+        for (int k = 0; k < kJoinWarps; ++k) total += sums[k][row];
+        // dim 32 b + 16 z + 8 m + g' of row 2 t' + c is component 2 z + c of lane 4 g' + t' of vector 2 b + m
+        const int vec = (dim >> 5) * 2 + (dim >> 3 & 1), at = (vec * 32 + (dim & 7) * 4 + (row >> 1)) * 4 + 2 * (dim >> 4 & 1) + (row & 1);
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) x += part[w][i];
-        put(p.out, p.dtype, orow * D + i, x * inv);
+        for (int k = 0; k < kJoinWarps; ++k) v += reinterpret_cast<const float *>(part[k])[at];
+        const int64_t orow = row_at(rho);
+        put(p.out, p.dtype, orow * D + d0 + dim, total == 0.f ? 0.f : v * (1.f / total));
+        if (d0 + dim == 0 && p.lse)
+            p.lse[orow] = total == 0.f ? -INFINITY : (refs[row] + log2f(total)) * 0.693147180559945309f;
     }
-    if (threadIdx.x == 0 && p.lse) p.lse[orow] = total == 0.f ? -INFINITY : (r0 + log2f(total)) * 0.693147180559945309f;
 }
 
 // ---------------------------------------------------------------- weights
@@ -1176,33 +1317,57 @@ struct WeightsParams {
     const float *prev;
     float *w;
     int64_t width;
+    int main_ctas;
 };
 
-// entries no tile covers: prev's (or zero)
-__global__ void __launch_bounds__(256) weights_rest_kernel(const WeightsParams p) {
-    const int s = blockIdx.y / p.a.pool.Hk;
-    const int len = seq_len(p.a.pool, p.a.lens, p.a.table_width, s);
-    const int64_t first = ((int64_t)len + kTile - 1) / kTile * kTile;
-    for (int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.width; i += (int64_t)gridDim.x * 256) {
-        const int64_t at = (int64_t)blockIdx.y * p.width + i;
-        p.w[at] = p.prev ? p.prev[at] : 0.f;
+// Entries no tile covers are prev's (or zero): the CTAs past main_ctas copy
+// them, kRest of a (sequence, head) each.
+constexpr int kRest = 4096;
+__device__ void weights_rest(const WeightsParams &p, int block) {
+    const int per = (int)((p.width + kRest - 1) / kRest);
+    const int sh = block / per, s = sh / p.a.pool.Hk;
+    const int64_t first = ((int64_t)seq_len(p.a.pool, p.a.lens, p.a.table_width, s) + kTile - 1) / kTile * kTile;
+    const int64_t from = (int64_t)(block % per) * kRest, row = (int64_t)sh * p.width;
+    constexpr int kAtOnce = 8;
+    for (int i0 = threadIdx.x; i0 < kRest; i0 += kWarps * 32 * kAtOnce) {
+        float v[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int64_t i = from + i0 + u * kWarps * 32;
+            v[u] = p.prev && i >= first && i < p.width ? p.prev[row + i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int64_t i = from + i0 + u * kWarps * 32;
+            if (i >= first && i < p.width) p.w[row + i] = v[u];
+        }
     }
 }
 
+// No accumulators but a tile's scores: more rows fit a pass than in attention.
 template <int D, int NT, bool HL>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights_kernel(const WeightsParams wp) {
+__host__ __device__ constexpr int weights_ctas_per_sm() {
+    return D == 256 ? 2 : (D == 128 ? (NT * (HL ? 2 : 1) >= 4 ? 2 : (NT > 1 || HL ? 3 : 4)) : (NT * (HL ? 2 : 1) >= 4 ? 3 : 4));
+}
+
+template <int D, int NT, bool HL>
+__global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>()) weights_kernel(const WeightsParams wp) {
     constexpr int NST = stages_of<D>(), BYTES = 18 * D;  // the K half of a tile
     const AttendParams &p = wp.a;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * NST];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + (D == 64 ? 1024 : 0)));
+    int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * NST * BYTES);
+    if ((int)blockIdx.x >= wp.main_ctas) {
+        weights_rest(wp, (int)blockIdx.x - wp.main_ctas);
+        return;
+    }
     tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int w = (int)blockIdx.x * kWarps + warp;
-    if (w >= cut.W) return;
-    const int64_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
-    const int64_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
+    if (w >= (int)cut.W) return;
+    const uint32_t u0 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w), cut.tiles);
+    const uint32_t u1 = tiles_before(prefix, p.n_seq, p.pool.Hk, cut.begin(w + 1), cut.tiles);
     if (u0 >= u1) return;
     const int lg = p.pool.lgP - 5;
     Stages<BYTES, NST> st;
@@ -1210,16 +1375,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
     uint32_t phases = 0;
     Query<D, NT, HL> q;
     for (int rho0 = 0; rho0 < p.R * p.G; rho0 += 8 * NT) {
-        Cursor ahead, at;
+        Cursor ahead;
         ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
-        at = ahead;
+        Place at = ahead;
         const int units = (int)(u1 - u0);
         int fetched = 0;
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             if (fetched < units) {
                 st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
-                ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
                 ++fetched;
             }
         }
@@ -1229,8 +1394,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
         int len = 0;
         for (int unit = 0; unit < units; ++unit) {
             if (fresh) {
-                q.load(p, at.s, at.h, rho0);
+                typename Query<D, NT, HL>::Raw raw;
+                raw.load(p, at.s, at.h, rho0);
                 len = seq_len(p.pool, p.lens, p.table_width, at.s);
+                q.form(p, raw, rho0);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int rho = rho0 + 8 * n + g;
@@ -1287,12 +1454,12 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) weights
             __syncwarp();
             if (fetched < units) {
                 if (!st.gave_up) st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
-                ahead.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
                 ++fetched;
             }
             if (at.k + 1 == at.T) fresh = true;
             stage = stage + 1 == NST ? 0 : stage + 1;
-            at.next(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            at.next(prefix, p.n_seq, p.pool.Hk);
         }
     }
 }
@@ -1343,7 +1510,7 @@ Shape shape_of(uint32_t D, uint32_t rows, int32_t dtype, int sms) {
     s.hl = dtype == KVS_F32;
     s.nt = (!s.hl && D <= 128 && rows > 8) ? 2 : 1;
     s.row_blocks = ((int)rows + 8 * s.nt - 1) / (8 * s.nt);
-    const int per_sm = D == 256 ? 2 : (s.nt == 2 ? 3 : (D == 128 && s.hl ? 3 : 4));
+    const int per_sm = D == 256 ? 2 : (D == 128 || s.nt == 2 ? 3 : 4);
     int ranges = sms * per_sm / s.row_blocks;
     if (ranges < 1) ranges = 1;
     s.ctas = ranges * s.row_blocks;
@@ -1379,6 +1546,8 @@ kvs_status fill_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t t
     if (!table || !lens || !q) return bad(KVS_ERR_INVALID, "null table, lens or q");
     if (table_width < 1 || (uint64_t)table_width * pool->page_tokens > 0x7fffffc0ull)
         return bad(KVS_ERR_INVALID, "table_width * page_tokens must be 1 .. 2^31 - 64");
+    const uint64_t line = (uint64_t)n_seq * pool->n_kv_head * ((uint64_t)table_width * (pool->page_tokens / 32) + kHeadCost);
+    if (line > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head * (table_width * page_tokens / 32 + 6) must be below 2^31");
     if (!aligned(q, 16) || (q_stride * elem_size(dtype)) % 16 != 0 || q_stride < (uint64_t)n_q_head * pool->head_dim)
         return bad(KVS_ERR_INVALID, "q rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
     if (!isfinite(scale)) return bad(KVS_ERR_INVALID, "scale must be finite");
@@ -1415,8 +1584,8 @@ cudaError_t launch(void (*kernel)(P, A...), dim3 grid, int threads, int smem, cu
     return cudaLaunchKernelEx(&cfg, kernel, p, a...);
 }
 
-int smem_of(uint32_t D, int bytes, uint32_t n_seq) {
-    return kWarps * (D == 64 ? 4 * bytes + 1024 : 3 * bytes) + ((int)n_seq + 1) * 8;
+int smem_of(uint32_t D, int bytes, int turn, uint32_t n_seq) {
+    return kWarps * ((D == 64 ? 4 : 3) * bytes + turn) + ((int)n_seq + 1) * 8;
 }
 
 }  // namespace
@@ -1518,11 +1687,11 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     if (D == 128) k = sh.hl ? attend_kernel<128, 1, true> : sh.nt == 2 ? attend_kernel<128, 2, false> : attend_kernel<128, 1, false>;
     if (D == 256) k = sh.hl ? attend_kernel<256, 1, true> : attend_kernel<256, 1, false>;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 36 * (int)D, n_seq), st, false, p);
+    cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 36 * (int)D, turn_bytes((int)D, sh.nt), n_seq), st, false, p);
     if (e != cudaSuccess) return cuda_failed("attention launch", e);
     void (*c)(AttendParams, int) = D == 64 ? combine_kernel<64> : D == 128 ? combine_kernel<128> : combine_kernel<256>;
-    const uint64_t rows = (uint64_t)n_seq * n_q_head * n_rows;
-    e = launch(c, dim3((unsigned)rows), kJoinWarps * 32, ((int)n_seq + 1) * 8, st, true, p, 8 * sh.nt);
+    const uint64_t groups = (uint64_t)n_seq * pool->n_kv_head * ((n_rows * p.G + 7) / 8);
+    e = launch(c, dim3((unsigned)groups, D / 64), kJoinWarps * 32, ((int)n_seq + 1) * 8, st, true, p, sh.nt);
     return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
 }
 
@@ -1537,26 +1706,31 @@ extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *tab
     if ((uint64_t)n_seq * pool->n_kv_head > 65535) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head must be at most 65535");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (n_seq == 0 || width == 0) return KVS_OK;
-    const uint32_t D = pool->head_dim;
-    const int sms = current_device_sms();
-    Shape sh = shape_of(D, n_rows * p.a.G, dtype, sms);
+    const uint32_t D = pool->head_dim, rows = n_rows * p.a.G;
+    const bool hl = dtype == KVS_F32;
+    // 8, 16 or (16-bit queries) 32 rows a pass: the fewer passes, the fewer times a tile is read
+    const int nt = rows <= 8 ? 1 : (rows <= 16 || hl ? 2 : 4);
+    void (*k)(WeightsParams) = nullptr;
+    int per_sm = 0;
+#define KVS_PICK(d, n, h)                 \
+    if (D == d && nt == n && hl == h) {   \
+        k = weights_kernel<d, n, h>;      \
+        per_sm = weights_ctas_per_sm<d, n, h>(); \
+    }
+    KVS_PICK(64, 1, false) KVS_PICK(64, 2, false) KVS_PICK(64, 4, false) KVS_PICK(64, 1, true) KVS_PICK(64, 2, true)
+    KVS_PICK(128, 1, false) KVS_PICK(128, 2, false) KVS_PICK(128, 4, false) KVS_PICK(128, 1, true) KVS_PICK(128, 2, true)
+    KVS_PICK(256, 1, false) KVS_PICK(256, 2, false) KVS_PICK(256, 4, false) KVS_PICK(256, 1, true) KVS_PICK(256, 2, true)
+#undef KVS_PICK
+    p.main_ctas = current_device_sms() * per_sm;
     p.a.row_blocks = 1;
-    p.a.workers = sh.ctas * kWarps;
+    p.a.workers = p.main_ctas * kWarps;
     p.lse_in = lse;
     p.prev = prev;
     p.w = weights;
     p.width = (int64_t)width;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    void (*k)(WeightsParams) = nullptr;
-    if (D == 64) k = sh.hl ? weights_kernel<64, 1, true> : sh.nt == 2 ? weights_kernel<64, 2, false> : weights_kernel<64, 1, false>;
-    if (D == 128) k = sh.hl ? weights_kernel<128, 1, true> : sh.nt == 2 ? weights_kernel<128, 2, false> : weights_kernel<128, 1, false>;
-    if (D == 256) k = sh.hl ? weights_kernel<256, 1, true> : weights_kernel<256, 1, false>;
-    cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 18 * (int)D, n_seq), st, false, p);
-    if (e != cudaSuccess) return cuda_failed("weights launch", e);
-    if (prev != weights) {
-        const unsigned gx = (unsigned)((width + 8191) / 8192);
-        e = launch(weights_rest_kernel, dim3(gx < 64 ? gx : 64, n_seq * pool->n_kv_head), 256, 0, st, false, p);
-        if (e != cudaSuccess) return cuda_failed("weights launch", e);
-    }
-    return KVS_OK;
+    const uint64_t rest = prev != weights ? (uint64_t)n_seq * pool->n_kv_head * ((width + kRest - 1) / kRest) : 0;
+    if (rest > 0x7fffffffull - (uint64_t)p.main_ctas) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head * width too large for one launch");
+    const cudaError_t e = launch(k, dim3((unsigned)(p.main_ctas + rest)), kWarps * 32, smem_of(D, 18 * (int)D, 0, n_seq),
+                                 static_cast<cudaStream_t>(stream), false, p);
+    return e == cudaSuccess ? KVS_OK : cuda_failed("weights launch", e);
 }

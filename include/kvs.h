@@ -856,7 +856,8 @@ kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n
  * Queries of 16-bit types and the weights of their second product enter the
  * tensor cores as single f16 values (exact for such queries up to 2^-28 of
  * a row's largest element), KVS_F32 ones as hi + lo pairs; sums are fp32.
- * n_rows * (n_q_head / n_kv_head) at most 64, n_seq at most 4096.
+ * n_rows * (n_q_head / n_kv_head) at most 64, n_seq at most 4096, n_seq * Hk *
+ * (table_width * P / 32 + 6) below 2^31.
  */
 kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
                          uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
