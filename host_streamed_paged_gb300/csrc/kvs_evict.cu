@@ -17,7 +17,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kShare = 49152;  // keys of a CTA that fit its shared memory (192 KB)
 constexpr int kMaxSeq = 4096;
 constexpr int kBins = 256;
 constexpr int kCopies = 16;
@@ -51,21 +52,24 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // One cluster per (sequence, kv head); each CTA has a contiguous share of the
-// candidates (tokens between the sinks and the recent ones), K keys per thread
-// in registers (key m of thread x is candidate 1024 m + x of the share).  The
+// candidates (tokens between the sinks and the recent ones), their keys in
+// shared memory.  (In registers, 16 a thread, they leave an SM one CTA of 1024
+// threads: 75 us against 47 on the batch of 131072 to 700 tokens.)  The
 // smallest key that stays is found digit by digit, 8 bits at a time from the
 // top: a histogram of the candidates that match the digits so far, summed over
 // the cluster, gives the next digit.  Then every CTA writes its tokens in
 // order: keys above the threshold, and of those equal to it the first ones.
-// K = 0 is for shares beyond 32768 keys: the keys are read again each time.
-template <int K>
+// KEPT = false is for shares beyond kShare keys: they are read again each time.
+template <bool KEPT>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
     constexpr int kW = kThreads / 32;
     __shared__ uint32_t hist[kCopies][kBins + 1];  // a digit's counts; lanes of a warp count in different copies, since
                                                    // most weights share a few top digits
     __shared__ uint32_t sums[2][kBins];  // of the copies, read by the whole cluster; two, for digits in turn
-    __shared__ uint32_t part[4][kBins];  // the cluster's counts, by two CTAs each
-    __shared__ uint32_t count[K > 0 ? K : 1][kW];  // tokens above the threshold (high half) and equal to it, by row of 1024 and warp
+    __shared__ uint32_t part[2][kBins];  // the cluster's counts, by four CTAs each
+    __shared__ uint32_t count[KEPT ? kShare / kThreads : 1][kW];  // tokens above the threshold (high half) and equal to
+                                                                 // it, by row of 512 candidates and warp
     __shared__ uint32_t mine[2];         // this CTA's tokens above the threshold, and equal to it
     __shared__ uint32_t digit[2];
     cg::cluster_group cl = cg::this_cluster();
@@ -90,25 +94,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     const int c0 = min(rank * share, n), c1 = min(c0 + share, n), cn = c1 - c0;
     const float *wc = w + p.sinks + c0;
     const int rows = (cn + kThreads - 1) / kThreads;
-    uint32_t key[K > 0 ? K : 1];
-    if (K > 0) {
-#pragma unroll
-        for (int m = 0; m < K; ++m) {
-            const int i = m * kThreads + tid;
-            key[m] = i < cn ? key_of(wc[i]) : 0u;
-        }
+    if (KEPT) {
+#pragma unroll 8
+        for (int i = tid; i < cn; i += kThreads) keys[i] = key_of(wc[i]);
     }
-    // every candidate of this thread, as f(row, key)
-    auto each = [&](auto f) {
-        if (K > 0) {
-#pragma unroll
-            for (int m = 0; m < K; ++m)
-                if (m * kThreads + tid < cn) f(m, key[m]);
-        } else {
-            for (int m = 0; m < rows; ++m)
-                if (m * kThreads + tid < cn) f(m, key_of(wc[m * kThreads + tid]));
-        }
-    };
+    auto key_at = [&](int i) { return KEPT ? keys[i] : key_of(wc[i]); };  // (this thread's candidates: i = tid + 512 m)
     for (int i = tid; i < kCopies * (kBins + 1); i += kThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     uint32_t *mine_h = hist[lane & (kCopies - 1)];
@@ -116,9 +106,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     uint32_t left = (uint32_t)want;  // still to be found among the keys that match the prefix
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-        each([&](int, uint32_t k) {
+#pragma unroll 4
+        for (int i = tid; i < cn; i += kThreads) {
+            const uint32_t k = key_at(i);
             if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&mine_h[k >> shift & 255], 1u);
-        });
+        }
         __syncthreads();
         uint32_t *own = sums[pass & 1];
         if (tid < kBins) {
@@ -132,10 +124,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
         }
         cl.sync();
         {
-            const int r = tid >> 8 << 1, bin = tid & 255;
-            const uint32_t a = r < ranks ? *cl.map_shared_rank(&own[bin], r) : 0u;
-            const uint32_t b = r + 1 < ranks ? *cl.map_shared_rank(&own[bin], r + 1) : 0u;
-            part[tid >> 8][bin] = a + b;
+            const int r0 = tid >> 8 << 2, bin = tid & 255;
+            uint32_t v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = r0 + r < ranks ? *cl.map_shared_rank(&own[bin], r0 + r) : 0u;
+            part[tid >> 8][bin] = v[0] + v[1] + v[2] + v[3];
         }
         __syncthreads();
         if (warp == 0) {  // from the top: the digit at which the count reaches `left`
@@ -143,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int bin = 255 - (lane * 8 + i);
-                sum += v[i] = part[0][bin] + part[1][bin] + part[2][bin] + part[3][bin];
+                sum += v[i] = part[0][bin] + part[1][bin];
             }
             uint32_t inc = sum;
 #pragma unroll
@@ -168,10 +161,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     // prefix is the threshold key; `left` tokens equal to it stay
     if (want == 0) prefix = 0xffffffffu, left = 0;
     uint32_t mine_a = 0, mine_e = 0;
-    each([&](int, uint32_t k) {
+#pragma unroll 4
+    for (int i = tid; i < cn; i += kThreads) {
+        const uint32_t k = key_at(i);
         mine_a += k > prefix;
         mine_e += k == prefix;
-    });
+    }
     mine_a = __reduce_add_sync(0xffffffffu, mine_a);
     mine_e = __reduce_add_sync(0xffffffffu, mine_e);
     if (tid < 2) mine[tid] = 0;
@@ -199,19 +194,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
             if (kw) kw[at] = w[tok];
         }
     };
-    if (K > 0) {
-#pragma unroll
-        for (int m = 0; m < K; ++m) {
-            const bool in = m * kThreads + tid < cn;
-            const uint32_t a = __ballot_sync(0xffffffffu, in && key[m] > prefix), e = __ballot_sync(0xffffffffu, in && key[m] == prefix);
+    if (KEPT) {
+        for (int m = 0; m < rows; ++m) {
+            const int i = m * kThreads + tid;
+            const uint32_t k = i < cn ? keys[i] : 0u;
+            const uint32_t a = __ballot_sync(0xffffffffu, i < cn && k > prefix), e = __ballot_sync(0xffffffffu, i < cn && k == prefix);
             if (lane == 0) count[m][warp] = (uint32_t)__popc(a) << 16 | (uint32_t)__popc(e);  // below 2^16 in all
         }
         __syncthreads();
-        if (warp == 0) {  // counts -> counts before, over rows and warps in order; lane l has K entries in a row
+        if (warp == 0) {  // counts -> counts before, over rows and warps in order; lane l has rows / 2 entries in a row
             uint32_t *c = &count[0][0];
+            const int each = (rows * kW + 31) / 32, at = lane * each, end = min(at + each, rows * kW);
             uint32_t sum = 0;
-#pragma unroll
-            for (int m = 0; m < K; ++m) sum += c[lane * K + m];
+            for (int m = at; m < end; ++m) sum += c[m];
             uint32_t inc = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -219,19 +214,20 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
                 if (lane >= o) inc += x;
             }
             uint32_t run = inc - sum;
-#pragma unroll
-            for (int m = 0; m < K; ++m) {
-                const uint32_t x = c[lane * K + m];
-                c[lane * K + m] = run;
+            for (int m = at; m < end; ++m) {
+                const uint32_t x = c[m];
+                c[m] = run;
                 run += x;
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < K; ++m) {
-            const bool in = m * kThreads + tid < cn, a = in && key[m] > prefix, e = in && key[m] == prefix;
-            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e), base = count[m][warp];
-            place(m * kThreads + tid, a, e, (base >> 16) + __popc(ba & below), (base & 0xffffu) + __popc(be & below));
+#pragma unroll 2
+        for (int m = 0; m < rows; ++m) {
+            const int i = m * kThreads + tid;
+            const uint32_t k = i < cn ? keys[i] : 0u, base = count[m][warp];
+            const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
+            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+            place(i, a, e, (base >> 16) + __popc(ba & below), (base & 0xffffu) + __popc(be & below));
         }
     } else {
         uint32_t row_a = 0, row_e = 0;  // of the rows before
@@ -396,21 +392,23 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     p.kept_weights = kept_weights;
     p.new_lens = new_lens;
     const uint64_t sh = (uint64_t)n_seq * pool->n_kv_head;
-    // Up to 4096 keys per CTA (4 a thread) one CTA is enough; beyond, a cluster of up to the 8 CTAs that every launch
-    // may have, then more keys a thread.
+    // Up to 4096 keys one CTA is enough; beyond, a cluster of up to the 8 CTAs that every launch may have.
     uint64_t most = (uint64_t)table_width * P;
     if (width < most) most = width;
     int ranks = 1;
     while (ranks < 8 && (uint64_t)ranks * 4096 < most) ranks *= 2;
     if (sh * ranks > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head too large");
     const uint64_t share = (most + ranks - 1) / ranks;
-    void (*select)(EvictParams) = share <= 4096 ? select_kernel<4> : share <= 8192 ? select_kernel<8> : share <= 16384 ? select_kernel<16>
-                                  : share <= 32768 ? select_kernel<32> : select_kernel<0>;
+    const bool kept_keys = share <= (uint64_t)kShare;
+    auto select = kept_keys ? select_kernel<true> : select_kernel<false>;
+    const int smem = kept_keys ? (int)(share * 4 + 15) / 16 * 16 : 0;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(select), smem);
+    if (e != cudaSuccess) return cuda_failed("evict launch", e);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sh * ranks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -418,7 +416,7 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, select, p);
+    e = cudaLaunchKernelEx(&cfg, select, p);
     if (e != cudaSuccess) return cuda_failed("evict launch", e);
     const uint64_t tiles = sh * ((keep + 31) / 32);
     if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");

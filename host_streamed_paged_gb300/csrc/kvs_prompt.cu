@@ -5,6 +5,7 @@
 // a 128-row MMA tile holds floor(128 / G) tokens of all G heads, read by one
 // TMA box.  So K and V are read once per kv head, short prompts fill tiles,
 // and the causal edge of a tile spans 128 / G keys instead of 128.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,6 +20,8 @@
 
 namespace kvs {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 384;  // warps 0-3, 4-7: one softmax warpgroup per tile; warp 8: MMA issue; warp 9: TMA
 constexpr int kMaxSeq = 4096;
@@ -134,6 +137,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -169,6 +179,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=l"(*reinterpret_cast<uint64_t *>(&r))
         : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
     return r;
+}
+// 2^y of two values on the FMA pipes, for part of the exponentials where the
+// exponential unit (16 a clock and SM) is what a kernel waits for: y = n + f
+// with n = floor(y), read off a sum rounded down onto 1.5 * 2^23; 2^f as 1 + f
+// q(f), q the least-maximum fit of degree 4 to (2^f - 1) / f on [0, 1) in
+// relative error of 2^f (8.2e-8); n added to the exponent.  y is taken as -127
+// where it is below, which gives exactly 0 (2^0 less 127 exponents).
+__device__ __forceinline__ float2 exp2_fma(float2 y) {
+    y.x = fmaxf(y.x, -127.f), y.y = fmaxf(y.y, -127.f);
+    const float2 magic = make_float2(12582912.f, 12582912.f);
+    float2 t;
+    asm("add.rm.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&t))
+        : "l"(*reinterpret_cast<const uint64_t *>(&y)), "l"(*reinterpret_cast<const uint64_t *>(&magic)));
+    const float2 n = add2(t, make_float2(-12582912.f, -12582912.f));
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), y);
+    float2 q = fma2(make_float2(0.0018671309808269143f, 0.0018671309808269143f), f, make_float2(0.009017028845846653f, 0.009017028845846653f));
+    q = fma2(q, f, make_float2(0.05579991638660431f, 0.05579991638660431f));
+    q = fma2(q, f, make_float2(0.24016444385051727f, 0.24016444385051727f));
+    q = fma2(q, f, make_float2(0.6931512951850891f, 0.6931512951850891f));
+    q = fma2(q, f, make_float2(1.f, 1.f));
+    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -631,26 +664,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 // w_j = sum over rows of exp(s_ij - lse_i).  Keys are the M rows here, so a
 // thread owns one key: S^T = K Q^T, two 128-key tiles per CTA against a stream
 // of query tiles, each read from tensor memory once, exponentiated against
-// the rows' lse and added up in one register; nothing is joined between CTAs.
+// the rows' lse and added up in a register.  Two warpgroups share a key tile,
+// half of the columns each (one per tile did not keep the exponential unit
+// fed: 2200 clocks a tile against its 1024).  The first keys of a prompt are
+// seen by all its rows; so that such a unit does not hold up the launch, a
+// cluster shares it, every CTA a part of the query tiles, and adds its sums up
+// in rank order.
+constexpr int kWThreads = 640;  // warps 0-15: sums; 16, 18: MMA issue (one per key tile); 17: TMA
 template <int D>
 struct WeightShape {
     static constexpr int BQ = D <= 128 ? 128 : 64;  // query rows per tile
+    static constexpr int kCols = BQ / 2;            // of them a warpgroup's
     static constexpr int kKBytes = kTileRows * D * 2;
     static constexpr int kBlock = BQ * D * 2;
-    static constexpr int kStages = D == 64 ? 4 : (D == 128 ? 4 : 3);
+    static constexpr int kStages = D == 256 ? 3 : 4;
     static constexpr int kOffRing = 2 * kKBytes;
     static constexpr int kOffLse = kOffRing + kStages * kBlock;
-    static constexpr bool kOwnLse = D <= 128;
-    static constexpr int kOffBar = kOffLse + (kOwnLse ? 8 : 2) * 2 * BQ * 4;
+    static constexpr bool kOwnLse = D <= 128;       // a copy of the columns' lse per warp, else per warpgroup
+    static constexpr int kOffSum = kOffLse + (kOwnLse ? 16 : 4) * 2 * kCols * 4;
+    static constexpr int kOffBar = D == 256 ? kOffSum : kOffSum + 2 * 2 * kTileRows * 4;
     static constexpr int kSmem = kOffBar + 256 + 1024;
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kWThreads, 1)
     prompt_weights_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk) {
     using S = WeightShape<D>;
-    constexpr int BQ = S::BQ, NST = S::kStages;
+    constexpr int BQ = S::BQ, NST = S::kStages, kCols = S::kCols;
+    // of each 16 exponentials 6 are computed on the FMA pipes
+    constexpr int kFma = 12;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -663,17 +706,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
     int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
+    // sums by [warpgroup of a tile][key] at the end; at D = 256 over the query ring, which is then done with
+    float *fin = reinterpret_cast<float *>(smem + (D == 256 ? S::kOffRing : S::kOffSum));
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
+    const int block = blockIdx.x / ranks;
 
     const int G = p.G, TQ = BQ / G;
-    const int head = blockIdx.x % p.Hk;
-    if (warp == 0) find_unit(p, blockIdx.x / p.Hk, 2 * kTileRows, place);
+    const int head = block % p.Hk;
+    if (warp == 0) find_unit(p, block / p.Hk, 2 * kTileRows, place);
     __syncthreads();
     if (place[0] < 0) return;
     const int seq = place[0], begin = place[2], L = place[3] - begin;
     const int k0 = (place[4] - 1 - place[1]) * 2 * kTileRows;  // the first keys are seen by the most rows
     int start = p.last_rows > 0 && L > p.last_rows ? L - p.last_rows : 0;  // first query token counted
     if (start < k0) start = k0;
-    const int ntile = (L - start + TQ - 1) / TQ;
+    const int all = (L - start + TQ - 1) / TQ, ntile = (all - rank + ranks - 1) / ranks;  // this CTA: tiles rank, rank + ranks, ...
     const bool second = k0 + kTileRows < L;
 
     if (tid == 0) {
@@ -686,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i)
             for (int b = 0; b < 2; ++b) {
                 mbar_init(b_s(i, b), 1);
-                mbar_init(b_read(i, b), 4);
+                mbar_init(b_read(i, b), 8);
             }
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -696,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     // query-tile rows that no box writes (BQ not a multiple of G) stay zero: their scores are finite
-    for (int x = tid; x < NST * (D / 64) * (BQ - TQ * G) * 8; x += kThreads) {
+    for (int x = tid; x < NST * (D / 64) * (BQ - TQ * G) * 8; x += kWThreads) {
         const int c = x & 7, r = (x >> 3) % (BQ - TQ * G), a = (x >> 3) / (BQ - TQ * G);
         *reinterpret_cast<uint4 *>(smem + S::kOffRing + a * (BQ * 128) + (TQ * G + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -705,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after();
     const uint32_t tmem = *tmem_slot;
+    float mine = 0.f;  // this thread's part of its key's sum
 
-    if (warp == 9) {
+    if (warp == 17) {
         if (lane == 0) {
             constexpr int kChunks = D / 64;
             mbar_expect(b_k, (uint32_t)((second ? 2 : 1) * S::kKBytes));
@@ -720,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_expect(b_full(st), (uint32_t)(kChunks * 128 * G * TQ));
                 for (int c = 0; c < kChunks; ++c)
                     tma_load(smem_u32(smem + S::kOffRing + st * S::kBlock + c * BQ * 128), &mq, b_full(st), c * 64, head * G,
-                             begin + start + r * TQ);
+                             begin + start + (rank + r * ranks) * TQ);
                 issued = r + 1;
             }
             if (*abort) {
@@ -730,8 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
             }
         }
-    } else if (warp == 8 || (warp == 10 && second)) {  // one issuing warp per key tile
-        const int i = (warp - 8) >> 1;
+    } else if (warp == 16 || (warp == 18 && second)) {
+        const int i = (warp - 16) >> 1;
         constexpr uint32_t id = idesc(BF16, kTileRows, BQ, false);
         const bool one = elect_one();
         const uint64_t da = smem_desc(smem_u32(smem + i * S::kKBytes), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
@@ -756,62 +805,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (one) mma_commit(b_final);
-    } else if (warp < 8 && (warp < 4 || second)) {
-        const int i = warp >> 2, row = tid & 127;
+    } else if (warp < 16 && ((warp & 4) == 0 || second)) {
+        const int i = warp >> 2 & 1, half = warp >> 3, row = tid & 127;
         const int key = k0 + i * kTileRows + row;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale_log2;
-        // every warp keeps its own copy of a tile's -lse, so that the warps run apart (D = 256: no room, one copy per
-        // warpgroup); the next tile's are on their way from memory meanwhile
-        constexpr int kRows = S::kOwnLse ? BQ / 32 : 1;
-        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + (S::kOwnLse ? warp : i) * 2 * BQ;
+        // every warp keeps its own copy of its columns' -lse, so that the warps run apart (D = 256: no room, one copy
+        // per warpgroup); the next tile's are on their way from memory meanwhile
+        constexpr int kRows = S::kOwnLse ? kCols / 32 : 1;
+        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + (S::kOwnLse ? warp : warp >> 2) * 2 * kCols;
         const int Hq = p.Hk * G;
         int t_of[kRows];                // token of the tile that this thread's x-th row belongs to (TQ: none)
         const float *src[kRows];        // its lse in the current tile
         float next[kRows];
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
-            const int q = S::kOwnLse ? 32 * x + lane : row;
-            t_of[x] = q < TQ * G ? q / G : TQ;
-            src[x] = p.lse_in + (int64_t)(begin + start + q / G) * Hq + head * G + q % G;
-            next[x] = t_of[x] < TQ && start + t_of[x] < L ? *src[x] : INFINITY;
+            const int c = S::kOwnLse ? 32 * x + lane : row, q = half * kCols + c;
+            t_of[x] = c < kCols && q < TQ * G ? q / G : TQ;
+            src[x] = p.lse_in + (int64_t)(begin + start + rank * TQ + q / G) * Hq + head * G + q % G;
+            next[x] = t_of[x] < TQ && start + rank * TQ + t_of[x] < L ? *src[x] : INFINITY;
         }
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool ok = true;
         for (int r = 0; r < ntile; ++r) {
-            const int buf = r & 1;
-            float *z = sl + buf * BQ;
+            const int buf = r & 1, tok0 = start + (rank + r * ranks) * TQ;
+            float *z = sl + buf * kCols;
 #pragma unroll
             for (int x = 0; x < kRows; ++x) {
                 // -lse (log2 units); rows that count for nothing: -inf
                 const float v = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
-                if (S::kOwnLse || row < BQ) z[S::kOwnLse ? 32 * x + lane : row] = v;
-                src[x] += (int64_t)TQ * Hq;
-                next[x] = t_of[x] < TQ && r + 1 < ntile && start + (r + 1) * TQ + t_of[x] < L ? *src[x] : INFINITY;
+                if (S::kOwnLse || row < kCols) z[S::kOwnLse ? 32 * x + lane : row] = v;
+                src[x] += (int64_t)ranks * TQ * Hq;
+                next[x] = t_of[x] < TQ && r + 1 < ntile && tok0 + ranks * TQ + t_of[x] < L ? *src[x] : INFINITY;
             }
             if constexpr (S::kOwnLse) __syncwarp();
-            else asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+            else asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp >> 2)) : "memory");
             ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((r >> 1) & 1), abort);
             if (!ok) break;
             tc_after();
-            const int tok0 = start + r * TQ;
             // columns this key counts: rows of tokens from the key on, and none past the prompt
             const bool edge = tok0 < k0 + (i + 1) * kTileRows - 1 || tok0 + TQ > L;
-            const int c_lo = (key - tok0) * G;
-            const int c_hi = (L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G;
-            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ);
-            // 32 columns at a time, the next 32 on their way from tensor memory
-            uint32_t sr[2][32];
-            tmem_ld32(ts, sr[0]);
+            const int c_lo = (key - tok0) * G - half * kCols;
+            const int c_hi = ((L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G) - half * kCols;
+            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ + half * kCols);
+            uint32_t sr[2][16];  // 16 columns at a time, the next on their way
+            tmem_ld16(ts, sr[0]);
 #pragma unroll
-            for (int c0 = 0; c0 < BQ; c0 += 32) {
-                const float *s = reinterpret_cast<const float *>(sr[c0 / 32 & 1]);
-                float4 z4[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) z4[c] = reinterpret_cast<const float4 *>(z + c0)[c];
+            for (int c0 = 0; c0 < kCols; c0 += 16) {
+                const float *s = reinterpret_cast<const float *>(sr[c0 / 16 & 1]);
                 tmem_wait_ld();
-                if (c0 + 32 < BQ) {
-                    tmem_ld32(ts + c0 + 32, sr[c0 / 32 + 1 & 1]);
+                if (c0 + 16 < kCols) {
+                    tmem_ld16(ts + c0 + 16, sr[c0 / 16 + 1 & 1]);
                 } else {
                     tc_before();
                     __syncwarp();
@@ -820,28 +864,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 sc2 = make_float2(sc, sc);
                 if (!edge) {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(z4[c / 4].x, z4[c / 4].y));
-                        const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(z4[c / 4].z, z4[c / 4].w));
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 zc = reinterpret_cast<const float4 *>(z + c0)[c / 4];
+                        const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(zc.x, zc.y));
+                        const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(zc.z, zc.w));
                         sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
-                        sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+                        sum[1] = add2(sum[1], c < kFma ? exp2_fma(b) : make_float2(ex2(b.x), ex2(b.y)));
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float zc = c & 2 ? (c & 1 ? z4[c / 4].w : z4[c / 4].z) : (c & 1 ? z4[c / 4].y : z4[c / 4].x);
-                        const float e = ex2(fmaf(s[c], sc, zc));
+                    for (int c = 0; c < 16; ++c) {
+                        const float e = ex2(fmaf(s[c], sc, z[c0 + c]));
                         sum[c & 1].x += c0 + c >= c_lo && c0 + c < c_hi ? e : 0.f;
                     }
                 }
             }
         }
-        if (key < L && key < p.width) {
-            const int64_t at = ((int64_t)seq * p.Hk + head) * p.width + key;
-            const float2 t2 = add2(sum[0], sum[1]);
-            p.w[at] = (p.prev ? p.prev[at] : 0.f) + (ok ? t2.x + t2.y : __int_as_float(0x7fc00000));
-        }
+        const float2 t2 = add2(sum[0], sum[1]);
+        mine = ok ? t2.x + t2.y : __int_as_float(0x7fc00000);
     }
+    // every MMA is done, every score read: the sums of a key meet in shared memory, then over the cluster
     if (tid == 0) {
         volatile int none = 0;
         mbar_wait(b_final, 0, &none);
@@ -850,15 +892,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after();
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp < 16) fin[(warp >> 3) * 2 * kTileRows + (tid & 255)] = mine;
+    cl.sync();
+    if (rank == 0 && tid < 2 * kTileRows) {
+        const int key = k0 + tid;
+        if (key < L && key < p.width) {
+            float total = 0.f;
+            for (int r = 0; r < ranks; ++r) {
+                const float *f = cl.map_shared_rank(fin, r);
+                total += f[tid] + f[2 * kTileRows + tid];
+            }
+            const int64_t at = ((int64_t)seq * p.Hk + head) * p.width + key;
+            p.w[at] = (p.prev ? p.prev[at] : 0.f) + total;
+        }
+    }
+    cl.sync();  // no CTA leaves while another may read its sums
 }
 
-// entries past a prompt's length: prev's (or zero)
+// entries past a prompt's length: prev's (or zero); 2048 of a (prompt, head) per CTA
+constexpr int kRest = 2048;
 __global__ void __launch_bounds__(256) prompt_rest_kernel(const PromptParams p) {
     const int s = blockIdx.y / p.Hk;
     const int len = cu_end(p, s) - cu_begin(p, s);
-    for (int64_t i = len + (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.width; i += (int64_t)gridDim.x * 256) {
-        const int64_t at = (int64_t)blockIdx.y * p.width + i;
-        p.w[at] = p.prev ? p.prev[at] : 0.f;
+    const int64_t from = (int64_t)blockIdx.x * kRest + threadIdx.x, row = (int64_t)blockIdx.y * p.width;
+    float v[kRest / 256];
+#pragma unroll
+    for (int u = 0; u < kRest / 256; ++u) {
+        const int64_t i = from + 256 * u;
+        v[u] = p.prev && i >= len && i < p.width ? p.prev[row + i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kRest / 256; ++u) {
+        const int64_t i = from + 256 * u;
+        if (i >= len && i < p.width) p.w[row + i] = v[u];
     }
 }
 
@@ -971,9 +1037,26 @@ kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t
     if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
     if (r != KVS_OK) return r;
     const uint64_t units = (uint64_t)p->total_rows / (2 * kTileRows) + p->n_seq;
-    if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
-    const cudaError_t e = launch(bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>,
-                                 dim3((unsigned)(units * p->n_kv_head)), S::kSmem, s, pp, mq, mk);
+    if (units * p->n_kv_head > 0x1fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
+    // Over all rows, a unit's work goes from one query tile to the whole prompt's: while a launch has few units per SM,
+    // clusters of 4 (2) share each, so that the longest ends with the rest.  An observation window is even work.
+    const uint64_t ctas = units * p->n_kv_head, sms = (uint64_t)current_device_sms();
+    const unsigned ranks = pp.last_rows > 0 ? 1 : ctas < 4 * sms ? 4 : ctas < 16 * sms ? 2 : 1;
+    auto kernel = bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), S::kSmem);
+    if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas * ranks);
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, pp, mq, mk);
     return e == cudaSuccess ? KVS_OK : cuda_failed("prompt weights launch", e);
 }
 
@@ -1016,8 +1099,7 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
         if (s != KVS_OK) return s;
     }
     if (prev != weights) {
-        const unsigned gx = (unsigned)((width + 8191) / 8192);
-        prompt_rest_kernel<<<dim3(gx < 64 ? gx : 64, p->n_seq * p->n_kv_head), 256, 0, st>>>(pp);
+        prompt_rest_kernel<<<dim3((unsigned)((width + kRest - 1) / kRest), p->n_seq * p->n_kv_head), 256, 0, st>>>(pp);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
     }

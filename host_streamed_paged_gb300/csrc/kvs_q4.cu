@@ -12,10 +12,13 @@
 //    factors are powers of two, taken back from the query (high-nibble dims
 //    / 16) and once from the result.
 //  - The codes' offset 8 leaves the sum: sum q (n - 8) = sum q n - 8 sum q.
-//    For scores -8 sum q is the accumulator's initial value per block (with
-//    more than one tile of query rows it is taken off the codes); for outputs -8 sum p is one more MMA per block, over the same rounded p.
-//    (fp32 calls subtract it from V's codes: over a long flat softmax sum p n
-//    exceeds sum p (n - 8) a hundredfold, and its fp32 rounding would show.)
+//    For scores -8 sum q is the accumulator's initial value per block; for
+//    outputs -8 sum p is one more MMA per block, over the same rounded p.
+//  - The tensor core cuts a product off some 24 bits below the largest
+//    exponent of its sum, and takes a subnormal's for 2^-14: codes like that
+//    leave 17 bits, enough beside f16 weights, not for fp32 calls.  These (and
+//    the scores of more than 8 rows a pass, where one conversion serves all
+//    the rows) take n - 8 as a normal f16, two instructions per two elements.
 //  - K's block scales multiply the fp32 block sums; V's multiply the softmax
 //    weights before those are rounded to f16, with a running power-of-two
 //    reference that keeps weight x scale below 2^14 and, for scales of usual
@@ -466,7 +469,7 @@ __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, in
 // prefix[s] = {tiles of one head, sequences with tokens} of sequences 0 .. s-1;
 // every thread of the CTA calls it
 __device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_width, int n_seq, int2 *prefix) {
-    __shared__ int2 warp_sum[8];
+    __shared__ int2 warp_sum[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int per = (n_seq + nt - 1) / nt;
     int2 sum = make_int2(0, 0);
@@ -570,18 +573,24 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// the nearest multiple of 2^k, for c = 1.5 * 2^(23 + k) and |x| well below it
+__device__ __forceinline__ float on_grid(float x, float c) { return __fadd_rn(__fadd_rn(x, c), -c); }
 __device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(*reinterpret_cast<const __half2 *>(&w)); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(*reinterpret_cast<const __half2 *>(&w)); }
 
 constexpr uint32_t kLoNib = 0x000f000fu, kHiNib = 0x00f000f0u;
-constexpr uint32_t kLoOff = 0x00080008u, kHiOff = 0x00800080u;  // 8 * 2^-24 and 128 * 2^-24 as f16 subnormals
+constexpr uint32_t kLoOff = 0x00080008u, kHiOff = 0x00800080u;  // the offset 8 in place of a low and of a high nibble
+// an ANDed nibble pair as the f16 numbers n - 8 (or 16 (n - 8)): under exponent 0x64 it is 1024 + n
+__device__ __forceinline__ uint32_t centred(uint32_t nib, uint32_t off) { return hsub2(nib | 0x64006400u, off | 0x64006400u); }
 
 // Query fragments of one pass: NT times 8 rows as the N side of the MMAs,
 // fp32 queries as f16 hi + lo (HL).
 template <int D, int NT, bool HL>
 struct Query {
     static constexpr int NB = D / 32;
-    static constexpr bool kBias = NT == 1;  // else the offset leaves the codes: one subtraction then serves NT row tiles
+    // else the offset leaves the codes: one subtraction then serves NT row tiles, and sums of 0 .. 15 codes would leave
+    // fp32 calls their own rounding
+    static constexpr bool kBias = NT == 1 && !HL;
     uint32_t hi[NT][NB][2][2];              // row g: [block][k-step][low nibbles' dims, high nibbles' dims / 16]
     uint32_t lo[HL ? NT : 1][NB][2][2];
     float bias[kBias ? NB : 1][4];          // as an accumulator: -8 * 2^-24 * sum of the block's operands
@@ -642,7 +651,7 @@ struct Query {
             int e = (int)(__float_as_uint(top) >> 23) - 127;
             e = e < -100 ? -100 : (e > 100 ? 100 : e);
             const float f = valid ? copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2) : 0.f;
-            fac[n] = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + 24 - 14 + e) << 23);
+            fac[n] = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + (kBias ? 24 : 0) - 14 + e) << 23);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float sum = 0.f, x[8];
@@ -651,18 +660,24 @@ struct Query {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     // k-step ks: low nibbles are dims 4t + ks and 4t + 2 + ks, high ones 16 further
-                    const float y[4] = {x[ks] * f, x[2 + ks] * f, x[4 + ks] * f, x[6 + ks] * f};
+                    float y[4] = {x[ks] * f, x[2 + ks] * f, x[4 + ks] * f, x[6 + ks] * f};
+                    if constexpr (HL) {
+                        // hi on a grid of 2^4 (2^11 steps of the row's largest element), so that its sums are exact in
+                        // the tensor core, which cuts off products far below the largest; lo the rest
+                        float z[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float h = on_grid(y[i], 201326592.f);  // 1.5 * 2^27
+                            z[i] = y[i] - h;
+                            y[i] = h;
+                        }
+                        lo[n][b][ks][0] = pack(z[0], z[1]);
+                        lo[n][b][ks][1] = pack(z[2] * 0.0625f, z[3] * 0.0625f);
+                    }
                     const uint32_t a0 = pack(y[0], y[1]), a1 = pack(y[2] * 0.0625f, y[3] * 0.0625f);
-                    sum += half_lo(a0) + half_hi(a0) + 16.f * (half_lo(a1) + half_hi(a1));
+                    if constexpr (kBias) sum += half_lo(a0) + half_hi(a0) + 16.f * (half_lo(a1) + half_hi(a1));
                     hi[n][b][ks][0] = a0;
                     hi[n][b][ks][1] = a1;
-                    if constexpr (HL) {
-                        const uint32_t l0 = pack(y[0] - half_lo(a0), y[1] - half_hi(a0));
-                        const uint32_t l1 = pack(y[2] * 0.0625f - half_lo(a1), y[3] * 0.0625f - half_hi(a1));
-                        sum += half_lo(l0) + half_hi(l0) + 16.f * (half_lo(l1) + half_hi(l1));
-                        lo[n][b][ks][0] = l0;
-                        lo[n][b][ks][1] = l1;
-                    }
                 }
                 if constexpr (kBias) {
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -711,8 +726,8 @@ struct Query {
                 uint32_t a0 = w[0][i] & kLoNib, a1 = w[1][i] & kLoNib, a2 = w[0][i] & kHiNib, a3 = w[1][i] & kHiNib;
                 uint32_t e0 = x0 & kLoNib, e1 = x1 & kLoNib, e2 = x0 & kHiNib, e3 = x1 & kHiNib;
                 if constexpr (!kBias) {
-                    a0 = hsub2(a0, kLoOff), a1 = hsub2(a1, kLoOff), a2 = hsub2(a2, kHiOff), a3 = hsub2(a3, kHiOff);
-                    e0 = hsub2(e0, kLoOff), e1 = hsub2(e1, kLoOff), e2 = hsub2(e2, kHiOff), e3 = hsub2(e3, kHiOff);
+                    a0 = centred(a0, kLoOff), a1 = centred(a1, kLoOff), a2 = centred(a2, kHiOff), a3 = centred(a3, kHiOff);
+                    e0 = centred(e0, kLoOff), e1 = centred(e1, kLoOff), e2 = centred(e2, kHiOff), e3 = centred(e3, kHiOff);
                 }
                 const float s0 = half_lo(sc[i]), s1 = half_hi(sc[i]);
 #pragma unroll
@@ -721,9 +736,12 @@ struct Query {
                     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
                     mma_from(d, kBias ? bias[kBias ? b : 0] : zero, a0, a1, a2, a3, hi[n][b][0][0], hi[n][b][0][1]);
                     mma(d, e0, e1, e2, e3, hi[n][b][1][0], hi[n][b][1][1]);
-                    if constexpr (HL) {
-                        mma(d, a0, a1, a2, a3, lo[n][b][0][0], lo[n][b][0][1]);
-                        mma(d, e0, e1, e2, e3, lo[n][b][1][0], lo[n][b][1][1]);
+                    if constexpr (HL) {  // summed apart, below the cut of hi's sums
+                        float r[4];
+                        mma_from(r, zero, a0, a1, a2, a3, lo[n][b][0][0], lo[n][b][0][1]);
+                        mma(r, e0, e1, e2, e3, lo[n][b][1][0], lo[n][b][1][1]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) d[k] += r[k];
                     }
                     acc[n][0] = fmaf(d[0], s0, acc[n][0]);
                     acc[n][1] = fmaf(d[1], s0, acc[n][1]);
@@ -888,13 +906,13 @@ __host__ __device__ constexpr int stages_of() {
 }
 // bytes per warp for turned scores beyond the tile's own
 __host__ __device__ constexpr int turn_bytes(int D, int NT) { return NT * 1024 > 8 * D ? NT * 1024 : 0; }
+// CTAs of an SM.  A warp's tile takes it some 3000 clocks whatever the others
+// do, so what counts is how many warps the registers allow without spills: 16
+// at 128 registers each (D = 64), 12 at 168 (D = 128; 16 that spill: 95 us for
+// 12's 89), 8 at 255.
+__host__ __device__ constexpr int attend_ctas(int D, int NT) { return D == 256 ? 2 : (D == 128 || NT == 2 ? 3 : 4); }
 template <int D, int NT, bool HL>
-__host__ __device__ constexpr int ctas_per_sm() {
-    return D == 256 ? 2 : (D == 128 || NT == 2 ? 3 : 4);
-}
-
-template <int D, int NT, bool HL>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel(const AttendParams p) {
     constexpr int NB = D / 32, NST = stages_of<D>(), BYTES = 36 * D, kTurnBytes = turn_bytes(D, NT);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * NST];
@@ -930,6 +948,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
     }
     Query<D, NT, HL> q;
     // cs: block b's -8 * 2^-24 * sum p s, in an accumulator of its own or in row b of one
+    constexpr float kUnit = HL ? 1.f : 16777216.f;  // V's codes are subnormal, or n - 8 as it stands
     constexpr bool kOwnSum = NT == 1 && D <= 128;
     constexpr int kSums = kOwnSum ? NB : 1;
     float O[NT][NB][2][4], cs[NT][kSums][4], ref[NT], l[NT];
@@ -1103,9 +1122,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                         const uint32_t w0 = i ? vw.z : vw.x, w1 = i ? vw.w : vw.y;
                         uint32_t a0 = w0 & kLoNib, a1 = w0 & kHiNib, a2 = w1 & kLoNib, a3 = w1 & kHiNib;
                         uint32_t e0 = (w0 >> 8) & kLoNib, e1 = (w0 >> 8) & kHiNib, e2 = (w1 >> 8) & kLoNib, e3 = (w1 >> 8) & kHiNib;
-                        if constexpr (HL) {  // n - 8 as it stands: sums of 0 .. 15 codes would leave their own rounding
-                            a0 = hsub2(a0, kLoOff), a2 = hsub2(a2, kLoOff), a1 = hsub2(a1, kHiOff), a3 = hsub2(a3, kHiOff);
-                            e0 = hsub2(e0, kLoOff), e2 = hsub2(e2, kLoOff), e1 = hsub2(e1, kHiOff), e3 = hsub2(e3, kHiOff);
+                        if constexpr (HL) {
+                            a0 = centred(a0, kLoOff), a2 = centred(a2, kLoOff), a1 = centred(a1, kHiOff), a3 = centred(a3, kHiOff);
+                            e0 = centred(e0, kLoOff), e2 = centred(e2, kLoOff), e1 = centred(e1, kHiOff), e3 = centred(e3, kHiOff);
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -1161,16 +1180,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
-                            dst[(2 * b + m) * 32] = make_float4((O[n][b][m][0] + off[b][0]) * 16777216.f, (O[n][b][m][1] + off[b][1]) * 16777216.f,
-                                                                (O[n][b][m][2] * 0.0625f + off[b][0]) * 16777216.f,
-                                                                (O[n][b][m][3] * 0.0625f + off[b][1]) * 16777216.f);
+                            dst[(2 * b + m) * 32] = make_float4((O[n][b][m][0] + off[b][0]) * kUnit, (O[n][b][m][1] + off[b][1]) * kUnit,
+                                                                (O[n][b][m][2] * 0.0625f + off[b][0]) * kUnit,
+                                                                (O[n][b][m][3] * 0.0625f + off[b][1]) * kUnit);
                     if (t == 0) p.part_rl[pslot * 8 + g] = make_float2(ref[n], l[n]);
                     continue;
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int rho = rho0 + 8 * n + 2 * t + c;
-                    const float inv = (c ? i1 : i0) * 16777216.f;
+                    const float inv = (c ? i1 : i0) * kUnit;
                     if (rho >= p.R * p.G) continue;
                     const int64_t orow = (((int64_t)at.s * p.R + rho / p.G) * p.Hq + at.h * p.G + rho % p.G) * D;
 #pragma unroll
@@ -1215,10 +1234,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, NT, HL>()) attend_
 // partials of a (sequence, head) that several workers shared, its warps each a
 // part of them, in the accumulators' own layout; rows of empty sequences are
 // written here.
-constexpr int kJoinWarps = 8;
 constexpr int kJoinVecs = 4;    // of the 2 D / 32 vectors of a partial: 64 dims
 constexpr int kJoinAtOnce = 4;  // partials a warp has on their way
-template <int D>
+template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendParams p, int nt) {
     constexpr int kVec = 2 * D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -1234,8 +1252,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendPa
     auto row_at = [&](int rho) { return ((int64_t)s * p.R + rho / p.G) * p.Hq + h * p.G + rho % p.G; };
     asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: the call ends after the attention has
     if (T == 0) {
-        const int rho = 8 * grp + warp;
-        if (rho < rows) {
+        for (int rho = 8 * grp + warp; rho < rows && rho < 8 * grp + 8; rho += kJoinWarps) {
             const int64_t orow = row_at(rho);
             put(p.out, p.dtype, orow * D + d0 + lane, 0.f);
             put(p.out, p.dtype, orow * D + d0 + 32 + lane, 0.f);
@@ -1510,8 +1527,7 @@ Shape shape_of(uint32_t D, uint32_t rows, int32_t dtype, int sms) {
     s.hl = dtype == KVS_F32;
     s.nt = (!s.hl && D <= 128 && rows > 8) ? 2 : 1;
     s.row_blocks = ((int)rows + 8 * s.nt - 1) / (8 * s.nt);
-    const int per_sm = D == 256 ? 2 : (D == 128 || s.nt == 2 ? 3 : 4);
-    int ranges = sms * per_sm / s.row_blocks;
+    int ranges = sms * attend_ctas((int)D, s.nt) / s.row_blocks;
     if (ranges < 1) ranges = 1;
     s.ctas = ranges * s.row_blocks;
     s.workers = ranges * kWarps;
@@ -1689,9 +1705,13 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 36 * (int)D, turn_bytes((int)D, sh.nt), n_seq), st, false, p);
     if (e != cudaSuccess) return cuda_failed("attention launch", e);
-    void (*c)(AttendParams, int) = D == 64 ? combine_kernel<64> : D == 128 ? combine_kernel<128> : combine_kernel<256>;
+    // 16 warps where few CTAs join many partials each (one sequence: 68 us for 8 warps' 63), 4 in a batch, where a
+    // head has a handful of them
     const uint64_t groups = (uint64_t)n_seq * pool->n_kv_head * ((n_rows * p.G + 7) / 8);
-    e = launch(c, dim3((unsigned)groups, D / 64), kJoinWarps * 32, ((int)n_seq + 1) * 8, st, true, p, sh.nt);
+    const bool few = groups * (D / 64) < (uint64_t)sms;
+    void (*c)(AttendParams, int) = few ? (D == 64 ? combine_kernel<64, 16> : D == 128 ? combine_kernel<128, 16> : combine_kernel<256, 16>)
+                                       : (D == 64 ? combine_kernel<64, 4> : D == 128 ? combine_kernel<128, 4> : combine_kernel<256, 4>);
+    e = launch(c, dim3((unsigned)groups, D / 64), few ? 512 : 128, ((int)n_seq + 1) * 8, st, true, p, sh.nt);
     return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
 }
 

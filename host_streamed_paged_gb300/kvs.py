@@ -856,8 +856,8 @@ class Q4Cache:
     ``pages`` is a uint8 CUDA tensor of whole pages in the layout include/kvs.h states (or give ``n_pages`` and
     ``device`` to have one allocated, zeroed).  Page tables (int32 [n_seq][width]), lengths (int32 [n_seq]) and slots
     (int64: page * page_tokens + token) are CUDA tensors that the caller keeps.  Every call runs on the current
-    stream; attend's workspace is allocated per call from torch's caching allocator, so calls on several streams and
-    captured graphs do not share one.
+    stream; attend keeps a workspace per stream, and takes one of its own for each captured call, so calls on several
+    streams and captured graphs do not share one.
     """
 
     def __init__(self, *, page_tokens, n_kv_head, head_dim, pages=None, n_pages=None, device="cuda"):
@@ -872,7 +872,8 @@ class Q4Cache:
         pool.pages, pool.n_pages = pages.data_ptr(), self.n_pages
         self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
         self._ref, self._lib = ctypes.byref(pool), load()
-        self._workspace = {}  # bytes by (rows, heads, dtype)
+        self._need_bytes = {}  # by (rows, heads, dtype)
+        self._spaces = {}      # workspaces by stream
 
     def append(self, slots, k, v):
         """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
@@ -918,13 +919,24 @@ class Q4Cache:
             lse = _torch.empty(shape[:3], dtype=_torch.float32, device=self.device)
         else:
             _need(lse, "lse", _torch.float32, q.device, shape[:3])
-        need = self._workspace.get((rows, hq, dt))
+        need = self._need_bytes.get((rows, hq, dt))
         if need is None:
-            need = self._workspace[(rows, hq, dt)] = kvs_q4_query_sizes(self.pool, rows, hq, dt)[1]
-        ws = _torch.empty(need, dtype=_torch.uint8, device=self.device)
+            need = self._need_bytes[(rows, hq, dt)] = kvs_q4_query_sizes(self.pool, rows, hq, dt)[1]
+        ws = self._workspace(need)
         _run(self.device, self._lib.kvs_q4_attend, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows, hq,
              q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), need)
         return out, lse
+
+    def _workspace(self, need):
+        """attend's workspace: one per stream, whose calls run in order; a call being captured gets one of its own from
+        the graph's memory, since graphs of one stream may be replayed side by side."""
+        if _torch.cuda.is_current_stream_capturing():
+            return _torch.empty(need, dtype=_torch.uint8, device=self.device)
+        stream = _stream_of(self.device.index) if self.device.type == "cuda" else 0
+        ws = self._spaces.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = self._spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=self.device)
+        return ws
 
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
         """The attention weight each cached token received from those rows, added to prev: float32 [n_seq][Hk][width].
