@@ -180,29 +180,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
     return r;
 }
-// 2^y of two values on the FMA pipes, for part of the exponentials where the
-// exponential unit (16 a clock and SM) is what a kernel waits for: y = n + f
-// with n = floor(y), read off a sum rounded down onto 1.5 * 2^23; 2^f as 1 + f
-// q(f), q the least-maximum fit of degree 4 to (2^f - 1) / f on [0, 1) in
-// relative error of 2^f (8.2e-8); n added to the exponent.  y is taken as -127
-// where it is below, which gives exactly 0 (2^0 less 127 exponents).
-__device__ __forceinline__ float2 exp2_fma(float2 y) {
-    y.x = fmaxf(y.x, -127.f), y.y = fmaxf(y.y, -127.f);
-    const float2 magic = make_float2(12582912.f, 12582912.f);
-    float2 t;
-    asm("add.rm.f32x2 %0, %1, %2;"
-        : "=l"(*reinterpret_cast<uint64_t *>(&t))
-        : "l"(*reinterpret_cast<const uint64_t *>(&y)), "l"(*reinterpret_cast<const uint64_t *>(&magic)));
-    const float2 n = add2(t, make_float2(-12582912.f, -12582912.f));
-    const float2 f = fma2(n, make_float2(-1.f, -1.f), y);
-    float2 q = fma2(make_float2(0.0018671309808269143f, 0.0018671309808269143f), f, make_float2(0.009017028845846653f, 0.009017028845846653f));
-    q = fma2(q, f, make_float2(0.05579991638660431f, 0.05579991638660431f));
-    q = fma2(q, f, make_float2(0.24016444385051727f, 0.24016444385051727f));
-    q = fma2(q, f, make_float2(0.6931512951850891f, 0.6931512951850891f));
-    q = fma2(q, f, make_float2(1.f, 1.f));
-    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
-}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -245,63 +222,76 @@ __device__ __forceinline__ int cu_end(const PromptParams &p, int s) {
 // to 256 prompts, which a warp holds in registers; of more prompts each is a
 // small part of the launch and they go one after another.)  Called by a warp.
 constexpr int kSortedSeq = 256;
-__device__ void find_unit(const PromptParams &p, int64_t c, int per, int *place) {
+template <int kEach>
+__device__ __forceinline__ void find_sorted(const PromptParams &p, int c, int per, int *place) {
     const int lane = threadIdx.x & 31;
+    int from_[kEach], to[kEach], t[kEach], most = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int s = 32 * i + lane;
+        from_[i] = s < p.n_seq ? p.cu[s] : 0;
+        to[i] = s < p.n_seq ? p.cu[s + 1] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        from_[i] = max(0, min(from_[i], p.total));
+        to[i] = max(from_[i], min(to[i], p.total));
+        t[i] = (to[i] - from_[i] + per - 1) / per;
+        most = max(most, t[i]);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    auto units = [&](int level) {  // at this level or above (per prompt max(0, t - level))
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) n += max(0, t[i] - level);
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    int lo = 0, hi = most - 1, above = 0;  // the largest level with c < units(level); above: units(lo + 1) at the end
+    if (c >= units(0)) {
+        if (lane == 0) place[0] = -1;
+        return;
+    }
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1, n = units(mid);
+        if (c < n) lo = mid;
+        else hi = mid - 1, above = n;
+    }
+    int nth = c - above;  // among the prompts with a group at this level
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t has = __ballot_sync(0xffffffffu, t[i] > lo);
+        const int n = __popc(has);
+        if (nth >= 0 && nth < n && __popc(has & ((1u << lane) - 1)) == nth && (has >> lane & 1)) {
+            place[0] = 32 * i + lane;
+            place[1] = lo;
+            place[2] = from_[i];
+            place[3] = to[i];
+            place[4] = t[i];
+        }
+        nth -= n;
+    }
+}
+__device__ __forceinline__ void find_unit(const PromptParams &p, int c, int per, int *place) {
+    const int lane = threadIdx.x & 31;
+    if (p.n_seq <= 32) return find_sorted<1>(p, c, per, place);
+    if (p.n_seq <= kSortedSeq) return find_sorted<kSortedSeq / 32>(p, c, per, place);
     auto groups = [&](int s) { return s < p.n_seq ? (cu_end(p, s) - cu_begin(p, s) + per - 1) / per : 0; };
-    int s = -1, x = 0;
-    if (p.n_seq <= kSortedSeq) {
-        constexpr int kEach = kSortedSeq / 32;
-        int t[kEach], most = 0;
+    int s = -1, x = 0, base = 0;
+    for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
+        const int t = groups(s0 + lane);
+        int inc = t;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            t[i] = 32 * i < p.n_seq ? groups(32 * i + lane) : 0;
-            most = max(most, t[i]);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        auto from = [&](int level) {  // units at this level or above (per prompt max(0, t - level))
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) n += max(0, t[i] - level);
-            return (int64_t)__reduce_add_sync(0xffffffffu, n);
-        };
-        if (c < from(0)) {
-            int lo = 0, hi = most - 1;  // the largest level with c < from(level)
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (c < from(mid)) lo = mid;
-                else hi = mid - 1;
-            }
-            x = lo;
-            int nth = (int)(c - from(lo + 1));  // among the prompts with a group at this level
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const uint32_t has = __ballot_sync(0xffffffffu, t[i] > x);
-                if (s < 0 && nth < __popc(has)) {
-                    uint32_t rest = has;
-                    for (; nth > 0; --nth) rest &= rest - 1;
-                    s = 32 * i + __ffs(rest) - 1;
-                }
-                if (s < 0) nth -= __popc(has);
-            }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + inc > c);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            s = s0 + who;
+            x = __shfl_sync(0xffffffffu, base + inc, who) - 1 - c;
         }
-    } else {
-        int64_t base = 0;
-        for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
-            const int t = groups(s0 + lane);
-            int inc = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const uint32_t past = __ballot_sync(0xffffffffu, base + inc > c);
-            if (past) {
-                const int who = __ffs(past) - 1;
-                s = s0 + who;
-                x = (int)(__shfl_sync(0xffffffffu, base + inc, who) - 1 - c);
-            }
-            base += __shfl_sync(0xffffffffu, inc, 31);
-        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (lane == 0) {
         place[0] = s;
@@ -370,7 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int G = p.G, TQ = kTileRows / G;
     const int head = blockIdx.x % p.Hk;
-    if (warp == 0) find_unit(p, blockIdx.x / p.Hk, NQ * TQ, place);
+    // the work is found, tensor memory allocated and the barriers set up by three warps at once
+    if (warp == 9) find_unit(p, blockIdx.x / p.Hk, NQ * TQ, place);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
     if (tid == 32) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(b_full(s), 1);
@@ -386,8 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    tc_before();
     __syncthreads();
-    if (place[0] < 0) return;
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    if (place[0] < 0) {
+        if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        return;
+    }
     const int begin = place[2], L = place[3] - begin;
     const int t0 = place[1] * NQ * TQ;  // first token of tile 0, within the prompt
     int nblk[2] = {0, 0}, n_max = 0;
@@ -396,10 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int a = t0 + i * TQ, last = (a + TQ < L ? a + TQ : L) - 1;
         nblk[i] = a < L ? last / BN + 1 : 0;
         n_max = nblk[i] > n_max ? nblk[i] : n_max;
-    }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     // the ring's blocks in the order the MMAs take them: K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
     // kPieces stages each
@@ -422,29 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load(dst + x * BN * 128, &mk, b_full(st), (c + x) * 64, head, begin + j * BN);
         }
     };
-    int preloaded = 0;
-    if (warp == 9) {  // the first loads run under the tensor-memory allocation
-        preloaded = n_ring < NST ? n_ring : NST;
+    if (warp == 9) {
+        // ------------------------------------------------------------ loads
         if (lane == 0) {
             mbar_expect(b_q, (uint32_t)(NQ * (D / 64) * 128 * G * TQ));
             for (int i = 0; i < NQ; ++i)
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                     tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
-            for (int r = 0; r < preloaded; ++r) load_piece(r);
-        }
-    }
-    tc_before();
-    __syncthreads();
-    tc_after();
-    const uint32_t tmem = *tmem_slot;
-
-    if (warp == 9) {
-        // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            int issued = preloaded;
-            for (int r = preloaded; r < n_ring; ++r) {
-                if (!mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort)) break;
+            int issued = 0;
+            for (int r = 0; r < n_ring; ++r) {
+                if (r >= NST && !mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort)) break;
                 load_piece(r);
                 issued = r + 1;
             }
@@ -662,114 +647,114 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- weights
 // w_j = sum over rows of exp(s_ij - lse_i).  Keys are the M rows here, so a
-// thread owns one key: S^T = K Q^T, two 128-key tiles per CTA against a stream
-// of query tiles, each read from tensor memory once, exponentiated against
-// the rows' lse and added up in a register.  Two warpgroups share a key tile,
-// half of the columns each (one per tile did not keep the exponential unit
-// fed: 2200 clocks a tile against its 1024).  The first keys of a prompt are
-// seen by all its rows; so that such a unit does not hold up the launch, a
-// cluster shares it, every CTA a part of the query tiles, and adds its sums up
-// in rank order.
-constexpr int kWThreads = 640;  // warps 0-15: sums; 16, 18: MMA issue (one per key tile); 17: TMA
+// thread owns one key: S^T = K Q^T, a 128-key tile per CTA against a stream of
+// query tiles, each read from tensor memory once, exponentiated against the
+// rows' lse and added up in a register.  Two warpgroups share the tile, half of
+// the columns each.  Two CTAs fit an SM, so that one's start, end and waits
+// pass under the other's exponentials, which bound this kernel (16 a clock and
+// SM: 1024 clocks for 128 x 128 scores, twice their MMAs at D = 128).  The
+// first keys of a prompt are seen by all its rows; so that such a unit does not
+// hold up the launch, a cluster shares it, every CTA a part of the query tiles,
+// and adds its sums up in rank order.
+constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA
 template <int D>
 struct WeightShape {
     static constexpr int BQ = D <= 128 ? 128 : 64;  // query rows per tile
     static constexpr int kCols = BQ / 2;            // of them a warpgroup's
+    static constexpr int kChunks = D / 64;          // a tile's ring stages: 64 dims each
+    static constexpr int kStep = kChunks < 2 ? 1 : 2;  // stages waited for at once
     static constexpr int kKBytes = kTileRows * D * 2;
-    static constexpr int kBlock = BQ * D * 2;
-    static constexpr int kStages = D == 256 ? 3 : 4;
-    static constexpr int kOffRing = 2 * kKBytes;
-    static constexpr int kOffLse = kOffRing + kStages * kBlock;
-    static constexpr bool kOwnLse = D <= 128;       // a copy of the columns' lse per warp, else per warpgroup
-    static constexpr int kOffSum = kOffLse + (kOwnLse ? 16 : 4) * 2 * kCols * 4;
-    static constexpr int kOffBar = D == 256 ? kOffSum : kOffSum + 2 * 2 * kTileRows * 4;
+    static constexpr int kChunk = BQ * 128;
+    static constexpr int kStages = D == 256 ? 5 : 4;
+    static constexpr uint32_t kColumns = 2 * BQ;    // tensor memory: two score buffers
+    static constexpr int kOffRing = kKBytes;
+    static constexpr int kOffLse = kOffRing + kStages * kChunk;
+    static constexpr int kOffSum = kOffLse + 8 * 2 * kCols * 4;
+    static constexpr int kOffBar = kOffSum + 2 * kTileRows * 4;
     static constexpr int kSmem = kOffBar + 256 + 1024;
+    static_assert(kSmem + 1024 <= 114 * 1024, "two CTAs per SM");
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kWThreads, 1)
+__global__ void __launch_bounds__(kWThreads, 2)
     prompt_weights_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mk) {
     using S = WeightShape<D>;
     constexpr int BQ = S::BQ, NST = S::kStages, kCols = S::kCols;
-    // of each 16 exponentials 6 are computed on the FMA pipes
-    constexpr int kFma = 12;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = smem_u32(smem + S::kOffBar);
     auto b_full = [&](int s) { return bars + 8u * s; };
-    auto b_empty = [&](int s) { return bars + 8u * (4 + s); };
-    const uint32_t b_k = bars + 8u * 8, b_final = bars + 8u * 9;
-    auto b_s = [&](int i, int buf) { return bars + 8u * (10 + 2 * i + buf); };     // scores in tensor memory
-    auto b_read = [&](int i, int buf) { return bars + 8u * (14 + 2 * i + buf); };  // scores read
+    auto b_empty = [&](int s) { return bars + 8u * (8 + s); };
+    const uint32_t b_k = bars + 8u * 16, b_final = bars + 8u * 17;
+    auto b_s = [&](int buf) { return bars + 8u * (18 + buf); };     // scores in tensor memory
+    auto b_read = [&](int buf) { return bars + 8u * (20 + buf); };  // scores read
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 22);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 23);
     int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 24);
-    // sums by [warpgroup of a tile][key] at the end; at D = 256 over the query ring, which is then done with
-    float *fin = reinterpret_cast<float *>(smem + (D == 256 ? S::kOffRing : S::kOffSum));
+    float *fin = reinterpret_cast<float *>(smem + S::kOffSum);  // sums by [warpgroup][key] at the end
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
     const int block = blockIdx.x / ranks;
 
     const int G = p.G, TQ = BQ / G;
     const int head = block % p.Hk;
-    if (warp == 0) find_unit(p, block / p.Hk, 2 * kTileRows, place);
-    __syncthreads();
-    if (place[0] < 0) return;
-    const int seq = place[0], begin = place[2], L = place[3] - begin;
-    const int k0 = (place[4] - 1 - place[1]) * 2 * kTileRows;  // the first keys are seen by the most rows
-    int start = p.last_rows > 0 && L > p.last_rows ? L - p.last_rows : 0;  // first query token counted
-    if (start < k0) start = k0;
-    const int all = (L - start + TQ - 1) / TQ, ntile = (all - rank + ranks - 1) / ranks;  // this CTA: tiles rank, rank + ranks, ...
-    const bool second = k0 + kTileRows < L;
-
+    if (warp == 9) find_unit(p, block / p.Hk, kTileRows, place);
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(S::kColumns));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), second ? 2 : 1);
+            mbar_init(b_empty(s), 1);
         }
         mbar_init(b_k, 1);
-        mbar_init(b_final, second ? 2 : 1);
-        for (int i = 0; i < 2; ++i)
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(b_s(i, b), 1);
-                mbar_init(b_read(i, b), 8);
-            }
+        mbar_init(b_final, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(b_s(b), 1);
+            mbar_init(b_read(b), 8);
+        }
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
     // query-tile rows that no box writes (BQ not a multiple of G) stay zero: their scores are finite
-    for (int x = tid; x < NST * (D / 64) * (BQ - TQ * G) * 8; x += kWThreads) {
+    for (int x = tid; x < NST * (BQ - TQ * G) * 8; x += kWThreads) {
         const int c = x & 7, r = (x >> 3) % (BQ - TQ * G), a = (x >> 3) / (BQ - TQ * G);
-        *reinterpret_cast<uint4 *>(smem + S::kOffRing + a * (BQ * 128) + (TQ * G + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(smem + S::kOffRing + a * S::kChunk + (TQ * G + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
     }
     proxy_fence();
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = *tmem_slot;
+    if (place[0] < 0) {  // the whole cluster
+        if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
+        return;
+    }
+    const int seq = place[0], begin = place[2], L = place[3] - begin;
+    const int k0 = (place[4] - 1 - place[1]) * kTileRows;  // the first keys are seen by the most rows
+    int start = p.last_rows > 0 && L > p.last_rows ? L - p.last_rows : 0;  // first query token counted
+    if (start < k0) start = k0;
+    const int all = (L - start + TQ - 1) / TQ, ntile = (all - rank + ranks - 1) / ranks;  // this CTA: tiles rank, rank + ranks, ...
+    const int64_t at = ((int64_t)seq * p.Hk + head) * p.width + k0 + tid;  // rank 0's threads: a key each at the end
+    const bool writes = rank == 0 && tid < kTileRows && k0 + tid < L && k0 + tid < p.width;
+    const float before = writes && p.prev ? p.prev[at] : 0.f;
     float mine = 0.f;  // this thread's part of its key's sum
 
-    if (warp == 17) {
+    if (warp == 9) {
         if (lane == 0) {
-            constexpr int kChunks = D / 64;
-            mbar_expect(b_k, (uint32_t)((second ? 2 : 1) * S::kKBytes));
-            for (int i = 0; i < (second ? 2 : 1); ++i)
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(smem_u32(smem + i * S::kKBytes + c * kTileRows * 128), &mk, b_k, c * 64, head, begin + k0 + i * kTileRows);
+            mbar_expect(b_k, (uint32_t)S::kKBytes);
+            for (int c = 0; c < S::kChunks; ++c)
+                tma_load(smem_u32(smem + c * kTileRows * 128), &mk, b_k, c * 64, head, begin + k0);
             int issued = 0;
-            for (int r = 0; r < ntile; ++r) {
+            for (int r = 0; r < ntile * S::kChunks; ++r) {
                 const int st = r % NST, use = r / NST;
                 if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort)) break;
-                mbar_expect(b_full(st), (uint32_t)(kChunks * 128 * G * TQ));
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(smem_u32(smem + S::kOffRing + st * S::kBlock + c * BQ * 128), &mq, b_full(st), c * 64, head * G,
-                             begin + start + (rank + r * ranks) * TQ);
+                mbar_expect(b_full(st), (uint32_t)(128 * G * TQ));
+                tma_load(smem_u32(smem + S::kOffRing + st * S::kChunk), &mq, b_full(st), r % S::kChunks * 64, head * G,
+                         begin + start + (rank + r / S::kChunks * ranks) * TQ);
                 issued = r + 1;
             }
             if (*abort) {
@@ -779,49 +764,58 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     if (issued > st) mbar_wait(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1), &none);
             }
         }
-    } else if (warp == 16 || (warp == 18 && second)) {
-        const int i = (warp - 16) >> 1;
+    } else if (warp == 8) {
         constexpr uint32_t id = idesc(BF16, kTileRows, BQ, false);
         const bool one = elect_one();
-        const uint64_t da = smem_desc(smem_u32(smem + i * S::kKBytes), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
+        const uint64_t da = smem_desc(smem_u32(smem), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
         bool ok = mbar_wait_warp(b_k, 0, abort);
         for (int r = 0; r < ntile && ok; ++r) {
-            const int st = r % NST, buf = r & 1;
-            ok = wait_warp(abort, [&] {
-                bool all = mbar_done(b_full(st), (uint32_t)((r / NST) & 1));
-                if (r >= 2) all &= mbar_done(b_read(i, buf), (uint32_t)(((r - 2) >> 1) & 1));
-                return all;
-            });
-            if (!ok) break;
-            tc_after();
-            if (one) {
-                const uint64_t db = dq + (uint64_t)(st * S::kBlock >> 4);
+            const int buf = r & 1;
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_ss(tmem + (uint32_t)((2 * i + buf) * BQ), da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4),
-                           db + (uint64_t)(((s >> 2) * (BQ * 128) + (s & 3) * 32) >> 4), id, s > 0);
-                mma_commit(b_s(i, buf));
-                mma_commit(b_empty(st));
+            for (int c0 = 0; c0 < S::kChunks; c0 += S::kStep) {
+                ok = ok && wait_warp(abort, [&] {
+                    bool all = true;
+#pragma unroll
+                    for (int c = c0; c < c0 + S::kStep; ++c) {
+                        const int x = r * S::kChunks + c;
+                        all &= mbar_done(b_full(x % NST), (uint32_t)((x / NST) & 1));
+                    }
+                    if (c0 == 0 && r >= 2) all &= mbar_done(b_read(buf), (uint32_t)(((r - 2) >> 1) & 1));
+                    return all;
+                });
+                if (!ok) break;
+                tc_after();
+                if (one) {
+#pragma unroll
+                    for (int c = c0; c < c0 + S::kStep; ++c) {
+                        const int st = (r * S::kChunks + c) % NST;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma_ss(tmem + (uint32_t)(buf * BQ), da + (uint64_t)((c * (kTileRows * 128) + s * 32) >> 4),
+                                   dq + (uint64_t)((st * S::kChunk + s * 32) >> 4), id, c > 0 || s > 0);
+                        mma_commit(b_empty(st));
+                    }
+                    if (c0 + S::kStep == S::kChunks) mma_commit(b_s(buf));
+                }
             }
         }
         if (one) mma_commit(b_final);
-    } else if (warp < 16 && ((warp & 4) == 0 || second)) {
-        const int i = warp >> 2 & 1, half = warp >> 3, row = tid & 127;
-        const int key = k0 + i * kTileRows + row;
+    } else {
+        const int half = warp >> 2, key = k0 + (tid & 127);
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale_log2;
-        // every warp keeps its own copy of its columns' -lse, so that the warps run apart (D = 256: no room, one copy
-        // per warpgroup); the next tile's are on their way from memory meanwhile
-        constexpr int kRows = S::kOwnLse ? kCols / 32 : 1;
-        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + (S::kOwnLse ? warp : warp >> 2) * 2 * kCols;
+        // every warp keeps its own copy of its columns' -lse, so that the warps run apart; the next tile's are on their
+        // way from memory meanwhile
+        constexpr int kRows = kCols / 32;
+        float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + warp * 2 * kCols;
         const int Hq = p.Hk * G;
         int t_of[kRows];                // token of the tile that this thread's x-th row belongs to (TQ: none)
         const float *src[kRows];        // its lse in the current tile
         float next[kRows];
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
-            const int c = S::kOwnLse ? 32 * x + lane : row, q = half * kCols + c;
-            t_of[x] = c < kCols && q < TQ * G ? q / G : TQ;
+            const int q = half * kCols + 32 * x + lane;
+            t_of[x] = q < TQ * G ? q / G : TQ;
             src[x] = p.lse_in + (int64_t)(begin + start + rank * TQ + q / G) * Hq + head * G + q % G;
             next[x] = t_of[x] < TQ && start + rank * TQ + t_of[x] < L ? *src[x] : INFINITY;
         }
@@ -833,21 +827,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
             for (int x = 0; x < kRows; ++x) {
                 // -lse (log2 units); rows that count for nothing: -inf
-                const float v = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
-                if (S::kOwnLse || row < kCols) z[S::kOwnLse ? 32 * x + lane : row] = v;
+                z[32 * x + lane] = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
                 src[x] += (int64_t)ranks * TQ * Hq;
                 next[x] = t_of[x] < TQ && r + 1 < ntile && tok0 + ranks * TQ + t_of[x] < L ? *src[x] : INFINITY;
             }
-            if constexpr (S::kOwnLse) __syncwarp();
-            else asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp >> 2)) : "memory");
-            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((r >> 1) & 1), abort);
+            __syncwarp();
+            ok = mbar_wait_warp(b_s(buf), (uint32_t)((r >> 1) & 1), abort);
             if (!ok) break;
             tc_after();
             // columns this key counts: rows of tokens from the key on, and none past the prompt
-            const bool edge = tok0 < k0 + (i + 1) * kTileRows - 1 || tok0 + TQ > L;
+            const bool edge = tok0 < k0 + kTileRows - 1 || tok0 + TQ > L;
             const int c_lo = (key - tok0) * G - half * kCols;
             const int c_hi = ((L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G) - half * kCols;
-            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BQ + half * kCols);
+            const uint32_t ts = lanes + (uint32_t)(buf * BQ + half * kCols);
             uint32_t sr[2][16];  // 16 columns at a time, the next on their way
             tmem_ld16(ts, sr[0]);
 #pragma unroll
@@ -859,7 +851,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 } else {
                     tc_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(b_read(i, buf));
+                    if (lane == 0) mbar_arrive(b_read(buf));
                 }
                 const float2 sc2 = make_float2(sc, sc);
                 if (!edge) {
@@ -869,7 +861,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                         const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(zc.x, zc.y));
                         const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(zc.z, zc.w));
                         sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
-                        sum[1] = add2(sum[1], c < kFma ? exp2_fma(b) : make_float2(ex2(b.x), ex2(b.y)));
+                        sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
                     }
                 } else {
 #pragma unroll
@@ -891,22 +883,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-    if (warp < 16) fin[(warp >> 3) * 2 * kTileRows + (tid & 255)] = mine;
-    cl.sync();
-    if (rank == 0 && tid < 2 * kTileRows) {
-        const int key = k0 + tid;
-        if (key < L && key < p.width) {
-            float total = 0.f;
-            for (int r = 0; r < ranks; ++r) {
-                const float *f = cl.map_shared_rank(fin, r);
-                total += f[tid] + f[2 * kTileRows + tid];
-            }
-            const int64_t at = ((int64_t)seq * p.Hk + head) * p.width + key;
-            p.w[at] = (p.prev ? p.prev[at] : 0.f) + total;
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
+    if (warp < 8) fin[tid] = mine;
+    if (ranks > 1) cl.sync();
+    else __syncthreads();
+    if (writes) {
+        float total = 0.f;
+        for (int r = 0; r < ranks; ++r) {
+            const float *f = cl.map_shared_rank(fin, r);
+            total += f[tid] + f[kTileRows + tid];
         }
+        p.w[at] = before + total;
     }
-    cl.sync();  // no CTA leaves while another may read its sums
+    if (ranks > 1) cl.sync();  // no CTA leaves while another may read its sums
 }
 
 // entries past a prompt's length: prev's (or zero); 2048 of a (prompt, head) per CTA
@@ -1036,12 +1025,12 @@ kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t
     kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, (uint32_t)(S::BQ / pp.G));
     if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
     if (r != KVS_OK) return r;
-    const uint64_t units = (uint64_t)p->total_rows / (2 * kTileRows) + p->n_seq;
+    const uint64_t units = (uint64_t)p->total_rows / kTileRows + p->n_seq;
     if (units * p->n_kv_head > 0x1fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
     // Over all rows, a unit's work goes from one query tile to the whole prompt's: while a launch has few units per SM,
     // clusters of 4 (2) share each, so that the longest ends with the rest.  An observation window is even work.
     const uint64_t ctas = units * p->n_kv_head, sms = (uint64_t)current_device_sms();
-    const unsigned ranks = pp.last_rows > 0 ? 1 : ctas < 4 * sms ? 4 : ctas < 16 * sms ? 2 : 1;
+    const unsigned ranks = pp.last_rows > 0 ? 1 : ctas < 32 * sms ? 2 : 1;
     auto kernel = bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), S::kSmem);
     if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
