@@ -659,14 +659,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA
 template <int D>
 struct WeightShape {
-    static constexpr int BQ = D <= 128 ? 128 : 64;  // query rows per tile
+    static constexpr int BQ = D <= 128 ? 128 : 96;  // query rows per tile
     static constexpr int kCols = BQ / 2;            // of them a warpgroup's
     static constexpr int kChunks = D / 64;          // a tile's ring stages: 64 dims each
-    static constexpr int kStep = kChunks < 2 ? 1 : 2;  // stages waited for at once
+    static constexpr int kStep = D == 128 ? 2 : 1;  // stages waited for at once
     static constexpr int kKBytes = kTileRows * D * 2;
     static constexpr int kChunk = BQ * 128;
-    static constexpr int kStages = D == 256 ? 5 : 4;
-    static constexpr uint32_t kColumns = 2 * BQ;    // tensor memory: two score buffers
+    static constexpr int kStages = D == 256 ? 3 : 4;
+    static constexpr uint32_t kColumns = 256;       // tensor memory: two score buffers
     static constexpr int kOffRing = kKBytes;
     static constexpr int kOffLse = kOffRing + kStages * kChunk;
     static constexpr int kOffSum = kOffLse + 8 * 2 * kCols * 4;
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
         const float sc = p.scale_log2;
         // every warp keeps its own copy of its columns' -lse, so that the warps run apart; the next tile's are on their
         // way from memory meanwhile
-        constexpr int kRows = kCols / 32;
+        constexpr int kRows = (kCols + 31) / 32;
         float *sl = reinterpret_cast<float *>(smem + S::kOffLse) + warp * 2 * kCols;
         const int Hq = p.Hk * G;
         int t_of[kRows];                // token of the tile that this thread's x-th row belongs to (TQ: none)
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #pragma unroll
         for (int x = 0; x < kRows; ++x) {
             const int q = half * kCols + 32 * x + lane;
-            t_of[x] = q < TQ * G ? q / G : TQ;
+            t_of[x] = 32 * x + lane < kCols && q < TQ * G ? q / G : TQ;
             src[x] = p.lse_in + (int64_t)(begin + start + rank * TQ + q / G) * Hq + head * G + q % G;
             next[x] = t_of[x] < TQ && start + rank * TQ + t_of[x] < L ? *src[x] : INFINITY;
         }
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #pragma unroll
             for (int x = 0; x < kRows; ++x) {
                 // -lse (log2 units); rows that count for nothing: -inf
-                z[32 * x + lane] = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
+                if (kCols % 32 == 0 || 32 * x + lane < kCols) z[32 * x + lane] = next[x] == -INFINITY ? -INFINITY : next[x] * -1.4426950408889634f;
                 src[x] += (int64_t)ranks * TQ * Hq;
                 next[x] = t_of[x] < TQ && r + 1 < ntile && tok0 + ranks * TQ + t_of[x] < L ? *src[x] : INFINITY;
             }
