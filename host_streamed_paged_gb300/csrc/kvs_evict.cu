@@ -52,14 +52,18 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // One cluster per (sequence, kv head); each CTA has a contiguous share of the
-// candidates (tokens between the sinks and the recent ones), their keys in
-// shared memory.  (In registers, 16 a thread, they leave an SM one CTA of 1024
-// threads: 75 us against 47 on the batch of 131072 to 700 tokens.)  The
-// smallest key that stays is found digit by digit, 8 bits at a time from the
-// top: a histogram of the candidates that match the digits so far, summed over
-// the cluster, gives the next digit.  Then every CTA writes its tokens in
-// order: keys above the threshold, and of those equal to it the first ones.
+// candidates (tokens between the sinks and the recent ones), each of its warps
+// a contiguous part of that, their keys in shared memory.  (In registers, 16 a
+// thread, they leave an SM one CTA of 1024 threads: 75 us against 47 on the
+// batch of 131072 to 700 tokens.)  The smallest key that stays is found digit
+// by digit, 8 bits at a time from the top: a histogram of the candidates that
+// match the digits so far, summed over the cluster, gives the next digit.  Then
+// every warp, from the counts of those before it, writes its tokens in order:
+// keys above the threshold, and of those equal to it the first ones.
 // KEPT = false is for shares beyond kShare keys: they are read again each time.
+// What bounds it is the longest sequence's chain of loads, passes and cluster
+// barriers (34 us on that batch with rows of 512 tokens counted and placed by
+// the CTA in step, their weights read again).
 template <bool KEPT>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     extern __shared__ uint32_t keys[];
@@ -68,8 +72,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
                                                    // most weights share a few top digits
     __shared__ uint32_t sums[2][kBins];  // of the copies, read by the whole cluster; two, for digits in turn
     __shared__ uint32_t part[2][kBins];  // the cluster's counts, by four CTAs each
-    __shared__ uint32_t count[KEPT ? kShare / kThreads : 1][kW];  // tokens above the threshold (high half) and equal to
-                                                                 // it, by row of 512 candidates and warp
+    __shared__ uint32_t count[2][kW];    // a warp's tokens above the threshold, and equal to it
     __shared__ uint32_t mine[2];         // this CTA's tokens above the threshold, and equal to it
     __shared__ uint32_t digit[2];
     cg::cluster_group cl = cg::this_cluster();
@@ -93,12 +96,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     const int share = (n + ranks - 1) / ranks;
     const int c0 = min(rank * share, n), c1 = min(c0 + share, n), cn = c1 - c0;
     const float *wc = w + p.sinks + c0;
-    const int rows = (cn + kThreads - 1) / kThreads;
+    const int part_n = (share + 32 * kW - 1) / (32 * kW) * 32;  // this warp's candidates: i = at, at + 32, ... below end
+    const int at = min(warp * part_n, cn) + lane, end = min((warp + 1) * part_n, cn);
     if (KEPT) {
-#pragma unroll 8
-        for (int i = tid; i < cn; i += kThreads) keys[i] = key_of(wc[i]);
+#pragma unroll 16
+        for (int i = at; i < end; i += 32) keys[i] = key_of(wc[i]);
     }
-    auto key_at = [&](int i) { return KEPT ? keys[i] : key_of(wc[i]); };  // (this thread's candidates: i = tid + 512 m)
+    auto key_at = [&](int i) { return KEPT ? keys[i] : key_of(wc[i]); };
     for (int i = tid; i < kCopies * (kBins + 1); i += kThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     uint32_t *mine_h = hist[lane & (kCopies - 1)];
@@ -106,8 +110,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     uint32_t left = (uint32_t)want;  // still to be found among the keys that match the prefix
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-#pragma unroll 4
-        for (int i = tid; i < cn; i += kThreads) {
+#pragma unroll 8
+        for (int i = at; i < end; i += 32) {
             const uint32_t k = key_at(i);
             if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&mine_h[k >> shift & 255], 1u);
         }
@@ -161,100 +165,57 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     // prefix is the threshold key; `left` tokens equal to it stay
     if (want == 0) prefix = 0xffffffffu, left = 0;
     uint32_t mine_a = 0, mine_e = 0;
-#pragma unroll 4
-    for (int i = tid; i < cn; i += kThreads) {
+#pragma unroll 8
+    for (int i = at; i < end; i += 32) {
         const uint32_t k = key_at(i);
         mine_a += k > prefix;
         mine_e += k == prefix;
     }
     mine_a = __reduce_add_sync(0xffffffffu, mine_a);
     mine_e = __reduce_add_sync(0xffffffffu, mine_e);
-    if (tid < 2) mine[tid] = 0;
+    if (lane == 0) count[0][warp] = mine_a, count[1][warp] = mine_e;
     __syncthreads();
-    if (lane == 0) {
-        atomicAdd(&mine[0], mine_a);
-        atomicAdd(&mine[1], mine_e);
+    if (tid < 2) {
+        uint32_t sum = 0;
+        for (int x = 0; x < kW; ++x) sum += count[tid][x];
+        mine[tid] = sum;
     }
     cl.sync();
-    uint32_t out = (uint32_t)p.sinks, eq_before = 0;  // places taken and equals seen before this CTA's share
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t *m = cl.map_shared_rank(mine, r);
-        out += m[0];
-        eq_before += m[1];
+    // places taken, and equals seen, before this warp's part
+    uint32_t out = (uint32_t)p.sinks, equal = 0;
+    if (lane < 2) {
+        uint32_t sum = 0;
+        for (int r = 0; r < rank; ++r) sum += cl.map_shared_rank(mine, r)[lane];
+        for (int x = 0; x < warp; ++x) sum += count[lane][x];
+        out += sum;
+        equal = sum;
     }
-    out += min(eq_before, left);
+    out = __shfl_sync(0xffffffffu, out, 0);
+    equal = __shfl_sync(0xffffffffu, equal, 1);
     const uint32_t below = (1u << lane) - 1;
-    // candidate (row, k) with na above and ne equal ones before it in the share
-    auto place = [&](int i, bool a, bool e, uint32_t na, uint32_t ne) {
-        ne += eq_before;
+#pragma unroll 4
+    for (int i0 = at - lane; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < end ? key_at(i) : 0u;
+        const bool a = i < end && k > prefix, e = i < end && k == prefix;
+        const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+        const uint32_t ne = equal + __popc(be & below);
         if (a || (e && ne < left)) {
-            const uint32_t at = out + na + min(ne, left) - min(eq_before, left);
+            const uint32_t to = out + __popc(ba & below) + min(ne, left);
             const int tok = p.sinks + c0 + i;
-            kept[at] = tok;
-            if (kw) kw[at] = w[tok];
+            kept[to] = tok;
+            // the key is the weight, but for NaN and the two zeros
+            if (kw) kw[to] = k == 0u || k == 0x80000000u ? w[tok] : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
         }
-    };
-    if (KEPT) {
-        for (int m = 0; m < rows; ++m) {
-            const int i = m * kThreads + tid;
-            const uint32_t k = i < cn ? keys[i] : 0u;
-            const uint32_t a = __ballot_sync(0xffffffffu, i < cn && k > prefix), e = __ballot_sync(0xffffffffu, i < cn && k == prefix);
-            if (lane == 0) count[m][warp] = (uint32_t)__popc(a) << 16 | (uint32_t)__popc(e);  // below 2^16 in all
-        }
-        __syncthreads();
-        if (warp == 0) {  // counts -> counts before, over rows and warps in order; lane l has rows / 2 entries in a row
-            uint32_t *c = &count[0][0];
-            const int each = (rows * kW + 31) / 32, at = lane * each, end = min(at + each, rows * kW);
-            uint32_t sum = 0;
-            for (int m = at; m < end; ++m) sum += c[m];
-            uint32_t inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            uint32_t run = inc - sum;
-            for (int m = at; m < end; ++m) {
-                const uint32_t x = c[m];
-                c[m] = run;
-                run += x;
-            }
-        }
-        __syncthreads();
-#pragma unroll 2
-        for (int m = 0; m < rows; ++m) {
-            const int i = m * kThreads + tid;
-            const uint32_t k = i < cn ? keys[i] : 0u, base = count[m][warp];
-            const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
-            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
-            place(i, a, e, (base >> 16) + __popc(ba & below), (base & 0xffffu) + __popc(be & below));
-        }
-    } else {
-        uint32_t row_a = 0, row_e = 0;  // of the rows before
-        for (int m = 0; m < rows; ++m) {
-            const int i = m * kThreads + tid;
-            const uint32_t k = i < cn ? key_of(wc[i]) : 0u;
-            const bool a = i < cn && k > prefix, e = i < cn && k == prefix;
-            const uint32_t ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
-            __syncthreads();
-            if (lane == 0) count[0][warp] = (uint32_t)__popc(ba) << 16 | (uint32_t)__popc(be);
-            __syncthreads();
-            uint32_t before = 0, all = 0;
-            for (int x = 0; x < kW; ++x) {
-                if (x < warp) before += count[0][x];
-                all += count[0][x];
-            }
-            place(i, a, e, row_a + (before >> 16) + __popc(ba & below), row_e + (before & 0xffffu) + __popc(be & below));
-            row_a += all >> 16;
-            row_e += all & 0xffffu;
-        }
+        out += __popc(ba);
+        equal += __popc(be);
     }
     // the ones that always stay
     for (int i = rank * kThreads + tid; i < p.sinks + p.recent; i += ranks * kThreads) {
         const int tok = i < p.sinks ? i : T - p.recent + (i - p.sinks);
-        const int at = i < p.sinks ? i : p.keep - p.recent + (i - p.sinks);
-        kept[at] = tok;
-        if (kw) kw[at] = w[tok];
+        const int to = i < p.sinks ? i : p.keep - p.recent + (i - p.sinks);
+        kept[to] = tok;
+        if (kw) kw[to] = w[tok];
     }
     cl.sync();  // no CTA leaves while another may read its shared memory
 }
