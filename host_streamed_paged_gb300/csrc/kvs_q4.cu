@@ -1400,7 +1400,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             if (fetched < units) {
-                st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
+                if (!st.gave_up) st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
                 ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
                 ++fetched;
             }
@@ -1478,6 +1478,10 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
             stage = stage + 1 == NST ? 0 : stage + 1;
             at.next(prefix, p.n_seq, p.pool.Hk);
         }
+    }
+    if (st.gave_up) {  // copies still in flight land in this CTA's shared memory: give them the same time again
+        st.gave_up = false;
+        for (int i = 0; i < NST; ++i) st.wait(i, phases);
     }
 }
 

@@ -106,6 +106,7 @@ ROWS_BAD = [
     (dict(q=0), kvs.KVS_ERR_INVALID), (dict(q=FAKE + 4), kvs.KVS_ERR_INVALID), (dict(dtype=3), kvs.KVS_ERR_INVALID),
     (dict(q_stride=1000), kvs.KVS_ERR_INVALID), (dict(q_stride=1026), kvs.KVS_ERR_INVALID), (dict(scale=float("inf")), kvs.KVS_ERR_INVALID),
     (dict(lse=0), None), (dict(n_rows=(1 << 32) - 1), kvs.KVS_ERR_UNSUPPORTED),
+    (dict(n_seq=4096, table_width=1 << 20), kvs.KVS_ERR_UNSUPPORTED),  # 2^34 tiles: their line counts in 31 bits
 ]
 
 
