@@ -666,7 +666,9 @@ struct WeightShape {
     static constexpr int kKBytes = kTileRows * D * 2;
     static constexpr int kChunk = BQ * 128;
     static constexpr int kStages = D == 256 ? 3 : 4;
-    static constexpr uint32_t kColumns = 256;       // tensor memory: two score buffers
+    static constexpr int kParts = D == 256 ? 2 : 1;    // sums of a score: over 128 dims each
+    static constexpr int kBufs = D == 256 ? 1 : 2;     // score buffers
+    static constexpr uint32_t kColumns = 256;          // tensor memory for them (a power of two)
     static constexpr int kOffRing = kKBytes;
     static constexpr int kOffLse = kOffRing + kStages * kChunk;
     static constexpr int kOffSum = kOffLse + 8 * 2 * kCols * 4;
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
         }
         mbar_init(b_k, 1);
         mbar_init(b_final, 1);
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < S::kBufs; ++b) {
             mbar_init(b_s(b), 1);
             mbar_init(b_read(b), 8);
         }
@@ -766,11 +768,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
         }
     } else if (warp == 8) {
         constexpr uint32_t id = idesc(BF16, kTileRows, BQ, false);
+        constexpr int kPer = S::kChunks / S::kParts;
         const bool one = elect_one();
         const uint64_t da = smem_desc(smem_u32(smem), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
         bool ok = mbar_wait_warp(b_k, 0, abort);
         for (int r = 0; r < ntile && ok; ++r) {
-            const int buf = r & 1;
+            const int buf = r % S::kBufs;
 #pragma unroll
             for (int c0 = 0; c0 < S::kChunks; c0 += S::kStep) {
                 ok = ok && wait_warp(abort, [&] {
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
                         const int x = r * S::kChunks + c;
                         all &= mbar_done(b_full(x % NST), (uint32_t)((x / NST) & 1));
                     }
-                    if (c0 == 0 && r >= 2) all &= mbar_done(b_read(buf), (uint32_t)(((r - 2) >> 1) & 1));
+                    if (c0 == 0 && r >= S::kBufs) all &= mbar_done(b_read(buf), (uint32_t)((r / S::kBufs - 1) & 1));
                     return all;
                 });
                 if (!ok) break;
@@ -791,8 +794,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
                         const int st = (r * S::kChunks + c) % NST;
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            mma_ss(tmem + (uint32_t)(buf * BQ), da + (uint64_t)((c * (kTileRows * 128) + s * 32) >> 4),
-                                   dq + (uint64_t)((st * S::kChunk + s * 32) >> 4), id, c > 0 || s > 0);
+                            mma_ss(tmem + (uint32_t)((buf * S::kParts + c / kPer) * BQ), da + (uint64_t)((c * (kTileRows * 128) + s * 32) >> 4),
+                                   dq + (uint64_t)((st * S::kChunk + s * 32) >> 4), id, c % kPer > 0 || s > 0);
                         mma_commit(b_empty(st));
                     }
                     if (c0 + S::kStep == S::kChunks) mma_commit(b_s(buf));
@@ -822,8 +825,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool ok = true;
         for (int r = 0; r < ntile; ++r) {
-            const int buf = r & 1, tok0 = start + (rank + r * ranks) * TQ;
-            float *z = sl + buf * kCols;
+            const int buf = r % S::kBufs, tok0 = start + (rank + r * ranks) * TQ;
+            float *z = sl + (r & 1) * kCols;
 #pragma unroll
             for (int x = 0; x < kRows; ++x) {
                 // -lse (log2 units); rows that count for nothing: -inf
@@ -832,22 +835,35 @@ __global__ void __launch_bounds__(kWThreads, 2)
                 next[x] = t_of[x] < TQ && r + 1 < ntile && tok0 + ranks * TQ + t_of[x] < L ? *src[x] : INFINITY;
             }
             __syncwarp();
-            ok = mbar_wait_warp(b_s(buf), (uint32_t)((r >> 1) & 1), abort);
+            ok = mbar_wait_warp(b_s(buf), (uint32_t)((r / S::kBufs) & 1), abort);
             if (!ok) break;
             tc_after();
             // columns this key counts: rows of tokens from the key on, and none past the prompt
             const bool edge = tok0 < k0 + kTileRows - 1 || tok0 + TQ > L;
             const int c_lo = (key - tok0) * G - half * kCols;
             const int c_hi = ((L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G) - half * kCols;
-            const uint32_t ts = lanes + (uint32_t)(buf * BQ + half * kCols);
-            uint32_t sr[2][16];  // 16 columns at a time, the next on their way
+            const uint32_t ts = lanes + (uint32_t)(buf * S::kParts * BQ + half * kCols);
+            uint32_t sr[2][16];  // 16 columns at a time: the next on their way, or both parts
             tmem_ld16(ts, sr[0]);
+            if (S::kParts == 2) tmem_ld16(ts + BQ, sr[1]);
 #pragma unroll
             for (int c0 = 0; c0 < kCols; c0 += 16) {
-                const float *s = reinterpret_cast<const float *>(sr[c0 / 16 & 1]);
+                float s[16];
                 tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    const uint32_t *a = &sr[S::kParts == 2 ? 0 : c0 / 16 & 1][c];
+                    float2 v = make_float2(__uint_as_float(a[0]), __uint_as_float(a[1]));
+                    if (S::kParts == 2) v = add2(v, make_float2(__uint_as_float(sr[1][c]), __uint_as_float(sr[1][c + 1])));
+                    s[c] = v.x, s[c + 1] = v.y;
+                }
                 if (c0 + 16 < kCols) {
-                    tmem_ld16(ts + c0 + 16, sr[c0 / 16 + 1 & 1]);
+                    if (S::kParts == 2) {
+                        tmem_ld16(ts + c0 + 16, sr[0]);
+                        tmem_ld16(ts + BQ + c0 + 16, sr[1]);
+                    } else {
+                        tmem_ld16(ts + c0 + 16, sr[c0 / 16 + 1 & 1]);
+                    }
                 } else {
                     tc_before();
                     __syncwarp();
