@@ -221,7 +221,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
 }
 
 // Gather: a warp builds one destination tile (32 tokens of one head) in shared
-// memory, lane = token, and stores it in whole lines.
+// memory and stores it in whole lines.  Its reads are pieces of 16 bytes; lanes
+// that read one token's sit side by side, as many to a line as the layout has.
+// Bound by what a token's rows take from memory: its V codes share 32-byte
+// sectors with seven other tokens, so up to eight times their bytes are read.
+// (8 sequences, 8 heads, D 128, up to 4096 tokens kept of each, 66 MB of rows
+// moved: 31 us, 144 MB read; 34 with a token to a lane, 900 line accesses a
+// tile for 400.)
 template <int D>
 __global__ void __launch_bounds__(128) gather_kernel(const EvictParams p) {
     constexpr int NB = D / 32, BYTES = 36 * D;
@@ -249,48 +255,88 @@ __global__ void __launch_bounds__(128) gather_kernel(const EvictParams p) {
         st = tok & 31;
     }
     uint8_t *out = stage[warp];
-    const int t = lane;
-    // K codes: 4 pieces of min(16, NB * 4) bytes per 4 blocks (D = 64: two octets share a 16-byte vector)
+    // scales, lane = token: K's of a token lie within NB words (the other halves are those of the token 8 on), V's within
+    // NB / 2 16-byte units
+    {
+        const uint32_t *kw = reinterpret_cast<const uint32_t *>(src + 16 * D) + ((st >> 4) * 8 + (st & 7)) * NB;
+        const uint4 *vw = reinterpret_cast<const uint4 *>(src + 34 * D) + (st >> 2) * (NB / 2);
+        uint32_t ks[NB];
+        uint4 vs[NB / 2];
+        using Words = typename std::conditional<NB == 2, uint2, uint4>::type;
+        constexpr int kWords = sizeof(Words) / 4;
+#pragma unroll
+        for (int b = 0; b < NB; b += kWords) {
+            const Words x = src ? *reinterpret_cast<const Words *>(kw + b) : Words{};
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) ks[b + c] = reinterpret_cast<const uint32_t *>(&x)[c];
+        }
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) vs[b] = src ? vw[b] : make_uint4(0, 0, 0, 0);
+        uint16_t *ko = reinterpret_cast<uint16_t *>(out + 16 * D) + ((lane >> 4) * 8 + (lane & 7)) * NB * 2 + (lane >> 3 & 1);
+        uint16_t *vo = reinterpret_cast<uint16_t *>(out + 34 * D) + (lane >> 2) * NB * 4 + (lane & 3);
+        const int k_sh = (st >> 3 & 1) * 16, v_sh = (st & 1) * 16;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) ko[2 * b] = (uint16_t)(ks[b] >> k_sh);
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) {
+            vo[8 * b] = (uint16_t)(((st & 2) ? vs[b].y : vs[b].x) >> v_sh);
+            vo[8 * b + 4] = (uint16_t)(((st & 2) ? vs[b].w : vs[b].z) >> v_sh);
+        }
+    }
+    const unsigned long long from = reinterpret_cast<unsigned long long>(src);
+    auto source = [&](int token, int *row) {  // of another lane's token
+        *row = __shfl_sync(0xffffffffu, st, token);
+        return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, from, token));
+    };
+    // K codes: 4 lanes a token, which read 4 neighbouring pieces of min(16, NB * 4) bytes per 4 blocks (D = 64: two octets
+    // share a 16-byte vector)
     using Piece = typename std::conditional<NB == 2, uint2, uint4>::type;
     constexpr int kGroups = NB <= 4 ? 1 : NB / 4;
     auto k_at = [&](int tok, int grp, int q) {
         const int u = (tok >> 3) * NB + grp * 4;
         return (((u >> 2) * 32) + (tok & 7) * 4 + q) * 16 + (u & 3) * 4;
     };
+    Piece kp[4][kGroups];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        int row;
+        const uint8_t *at = source(8 * r + (lane >> 2), &row);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) kp[r][g] = at ? *reinterpret_cast<const Piece *>(at + k_at(row, g, lane & 3)) : Piece{};
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) *reinterpret_cast<Piece *>(out + k_at(8 * r + (lane >> 2), g, lane & 3)) = kp[r][g];
+    // V codes: a 16-byte unit is 4 tokens x 2 blocks x 2 bytes, and a token's 8 units of two blocks lie 64 bytes apart: 8
+    // lanes a token, 4 tokens at a time, which are those of a destination unit.  A lane has two bytes of either block; it
+    // and the next token's lane exchange halves, the even one then has a word of the first block, the odd one of the second.
     auto v_at = [&](int tok, int bp, int j) { return 18 * D + ((((tok >> 4) * (NB / 2) + bp) * 32) + j * 4 + ((tok & 15) >> 2)) * 16; };
-    Piece kp[kGroups][4];
+    const int j = lane & 7, odd = lane >> 3 & 1, half = lane >> 4;
+    constexpr int kRounds = NB == 8 ? 2 : 4;  // rounds whose loads are in flight together
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
+    for (int r0 = 0; r0 < 8; r0 += kRounds) {
+        uint4 v[kRounds][NB / 2];
+        int row[kRounds];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) kp[g][q] = src ? *reinterpret_cast<const Piece *>(src + k_at(st, g, q)) : Piece{};
-    uint16_t ks[NB], vs[NB];
+        for (int r = 0; r < kRounds; ++r) {
+            const uint8_t *at = source(4 * (r0 + r) + (lane >> 3), &row[r]);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        ks[b] = src ? reinterpret_cast<const uint16_t *>(src + 16 * D)[((st >> 4) * 8 + (st & 7)) * NB * 2 + b * 2 + (st >> 3 & 1)] : (uint16_t)0;
-        vs[b] = src ? reinterpret_cast<const uint16_t *>(src + 34 * D)[((st >> 2) * NB + b) * 4 + (st & 3)] : (uint16_t)0;
-    }
-    // V codes: of each 16-byte unit (4 tokens x 2 blocks) this token's two bytes of either block
-    const int s_half = (st & 3) >> 1, s_sh = (st & 1) * 16, d_half = (t & 3) >> 1, d_par = t & 1;
-#pragma unroll
-    for (int bp = 0; bp < NB / 2; ++bp) {
-        uint4 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = src ? *reinterpret_cast<const uint4 *>(src + v_at(st, bp, j)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint16_t *dst = reinterpret_cast<uint16_t *>(out + v_at(t, bp, j)) + 2 * d_half + d_par;
-            dst[0] = (uint16_t)((s_half ? v[j].y : v[j].x) >> s_sh);
-            dst[4] = (uint16_t)((s_half ? v[j].w : v[j].z) >> s_sh);
+            for (int bp = 0; bp < NB / 2; ++bp)
+                v[r][bp] = at ? *reinterpret_cast<const uint4 *>(at + v_at(row[r], bp, j)) : make_uint4(0, 0, 0, 0);
         }
-    }
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
+        for (int r = 0; r < kRounds; ++r) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<Piece *>(out + k_at(t, g, q)) = kp[g][q];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        reinterpret_cast<uint16_t *>(out + 16 * D)[((t >> 4) * 8 + (t & 7)) * NB * 2 + b * 2 + (t >> 3 & 1)] = ks[b];
-        reinterpret_cast<uint16_t *>(out + 34 * D)[((t >> 2) * NB + b) * 4 + (t & 3)] = vs[b];
+            for (int bp = 0; bp < NB / 2; ++bp) {
+                const int sh = (row[r] & 1) * 16;
+                const uint32_t first = ((row[r] & 2) ? v[r][bp].y : v[r][bp].x) >> sh & 0xffffu;
+                const uint32_t second = ((row[r] & 2) ? v[r][bp].w : v[r][bp].z) >> sh & 0xffffu;
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? first : second, 8);
+                *reinterpret_cast<uint32_t *>(out + v_at(4 * (r0 + r), bp, j) + 8 * odd + 4 * half) =
+                    odd ? other | second << 16 : first | other << 16;
+            }
+        }
     }
     __syncwarp();
     for (int x = lane; x < BYTES / 16; x += 32) reinterpret_cast<uint4 *>(dst)[x] = reinterpret_cast<const uint4 *>(out)[x];

@@ -220,7 +220,9 @@ __device__ __forceinline__ int cu_end(const PromptParams &p, int s) {
 // causal tile's work grows with x and a heavy one begun late would run alone
 // at the end: level by level from the longest prompt's last group down.  (Up
 // to 256 prompts, which a warp holds in registers; of more prompts each is a
-// small part of the launch and they go one after another.)  Called by a warp.
+// small part of the launch and they go one after another.)  Called by a warp,
+// before anything else of a CTA can begin, so kept short: one round of loads and
+// few instructions (some 1000 clocks; 3000 with 256 prompts' registers always).
 constexpr int kSortedSeq = 256;
 template <int kEach>
 __device__ __forceinline__ void find_sorted(const PromptParams &p, int c, int per, int *place) {
@@ -322,6 +324,11 @@ __device__ __forceinline__ void find_unit(const PromptParams &p, int c, int per,
 // clocks: it reads its A tile from shared memory anew), which costs less than
 // the one 128-key buffer per tile that would fit: its softmax waits for its
 // own P V and Q K^T each time.
+// The tensor pipe bounds long prompts: 16755 rows of prompts of 8192 .. 1
+// tokens, 32 / 8 heads, D 128, bf16, take 576 us, 1.53 PFLOP/s of causal work
+// (80% of the measured bf16 rate; 790 us with one issuing warp and S one block
+// ahead).  Short prompts take a CTA's chain of starts and waits: five of 1 ..
+// 300 tokens, 24 / 4 heads, D 256, 16 us, as long as the rate allows 3 us.
 template <int D>
 struct AttendShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;
@@ -656,6 +663,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // first keys of a prompt are seen by all its rows; so that such a unit does not
 // hold up the launch, a cluster shares it, every CTA a part of the query tiles,
 // and adds its sums up in rank order.
+// At D = 256 a tile is 96 rows: K leaves the ring of two CTAs 36 KB, which are
+// two stages of 128 rows, and 64 rows pay the 50-clock MMA of N = 64 (52 us on
+// the window below, 46 with 96).  Its scores are summed over 128 dims each, in
+// two accumulators: the tensor core drops what lies below an accumulator's last
+// place at every 16 dims, always towards zero, and with 256 dims in a row the
+// weights came out 1.1e-6 low, 6.5e-7 like this (for 46 -> 50 us).
+// Prompts of 4096 .. 33 tokens, 32 / 8 heads, D 128, over all rows: 122 us
+// (exponential unit busy 64%; 143 us with two key tiles in one CTA of 16 sum
+// warps; with 2 to all of 16 exponentials as polynomials on the FMA pipes those
+// took 147 to 173).  The last 64 rows of 32768, 24 / 4 heads, D 256: 50 us.
 constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA
 template <int D>
 struct WeightShape {

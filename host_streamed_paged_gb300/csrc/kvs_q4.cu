@@ -104,7 +104,9 @@ __device__ __forceinline__ int v_scale(int t, int b, int NB) { return ((t >> 2) 
 // ---------------------------------------------------------------- append / read
 // Bound by bytes: rows at 2 or 4 bytes per element on one side, 9/16 byte on
 // the other.  Four lanes share a 32-dim block, 8 dims each, so that rows are
-// read and written in whole lines.
+// read and written in whole lines.  22161 rows of 4 x 256 bf16, 116 MB on both
+// sides: read 29 us (4.0 TB/s); append 55 us, bound by the instructions of the
+// encoding (2.1 TB/s).
 
 struct RowsParams {
     Pool pool;
@@ -444,6 +446,10 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
 // two per worker, and the combine joins them in range order.  Query rows
 // beyond one pass's 8 or 16 go to further workers over the same ranges, next
 // to each other in the grid so that they share the tiles through L2.
+// 32 sequences of 32768 .. 0 tokens, 32 / 8 heads, D 128, bf16: 89 us, 3.7 TB/s
+// of the cache (55% of the measured copy rate), bound by the instructions of a
+// tile, some 700 of a warp.  One of 4096 tokens, 8 / 2 heads, fp32: 14 us, a
+// chain of two launches.
 
 struct AttendParams {
     Pool pool;
@@ -1327,7 +1333,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendPa
 // ---------------------------------------------------------------- weights
 // w[t] += sum over rows of 2^(score - lse): K tiles only, no join between
 // workers (a token is one worker's).  Row passes beyond the first re-read the
-// worker's tiles and add to what the first wrote.
+// worker's tiles and add to what the first wrote.  Six sequences of 65536 .. 0
+// tokens, 4 rows, 24 / 4 heads, D 256, f16: 52 us, 1.7 TB/s of K, bound by the
+// 24 rows' matrix and exponential instructions (90 us in passes of 8 rows).
 struct WeightsParams {
     AttendParams a;
     const float *lse_in;
