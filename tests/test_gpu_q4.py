@@ -296,7 +296,8 @@ def test_two_streams_at_once():
 # ------------------------------------------------------------------ weights
 
 @pytest.mark.parametrize("dt", DT)
-@pytest.mark.parametrize("D,P,Hk,G,R", [(64, 32, 2, 1, 1), (128, 64, 2, 4, 1), (128, 128, 1, 8, 5), (256, 256, 2, 6, 3), (64, 64, 1, 9, 7)])
+@pytest.mark.parametrize("D,P,Hk,G,R", [(64, 32, 2, 1, 1), (128, 64, 2, 4, 1), (128, 128, 1, 8, 5), (256, 256, 2, 6, 3), (64, 64, 1, 9, 7),
+                                         (64, 32, 2, 12, 2), (128, 64, 2, 6, 4), (128, 32, 1, 10, 4), (256, 128, 1, 20, 2)])
 def test_weights_are_added_to_prev(D, P, Hk, G, R, dt):
     """exp(s - lse) with the scores' error S_ERR (relative), the lse as given, fp32 sums of R G terms."""
     import torch
