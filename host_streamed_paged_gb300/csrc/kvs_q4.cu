@@ -105,7 +105,7 @@ __device__ __forceinline__ int v_scale(int t, int b, int NB) { return ((t >> 2) 
 // Bound by bytes: rows at 2 or 4 bytes per element on one side, 9/16 byte on
 // the other.  Four lanes share a 32-dim block, 8 dims each, so that rows are
 // read and written in whole lines.  22161 rows of 4 x 256 bf16, 116 MB on both
-// sides: read 29 us (4.0 TB/s); append 55 us, bound by the instructions of the
+// sides: read 26 us (4.5 TB/s); append 55 us, bound by the instructions of the
 // encoding (2.1 TB/s).
 
 struct RowsParams {
@@ -195,13 +195,13 @@ __device__ __forceinline__ int word_of(int q) { return q < 2 ? 2 * q : 2 * q - 3
 // is encoded.
 constexpr int kInFlight = 4;
 
-// Where the 64 kInFlight (row, head, block) units of a CTA lie: unit x of it is
+// Where the 64 `each` (row, head, block or pair of blocks) units of a CTA lie: unit x of it is
 // unit (rem + x) % per_row of row `row` + (rem + x) / per_row, in 32 bits.
 struct Units {
     int64_t row;
     uint32_t rem, per_row;
-    __device__ __forceinline__ Units(int64_t cta, uint32_t per) : per_row(per) {
-        const int64_t u = cta * (64 * kInFlight);
+    __device__ __forceinline__ Units(int64_t cta, int each, uint32_t per) : per_row(per) {
+        const int64_t u = cta * (64 * each);
         row = u / per;
         rem = (uint32_t)(u - row * per);
     }
@@ -211,7 +211,7 @@ template <int D>
 __device__ void append_k(const RowsParams &p, int64_t block) {
     constexpr int NB = D / 32;
     const int q = threadIdx.x & 3;
-    const Units units(block, NB * p.pool.Hk);
+    const Units units(block, kInFlight, NB * p.pool.Hk);
     int64_t row[kInFlight];
     uint32_t in_row[kInFlight];
     float x[kInFlight][8];
@@ -345,20 +345,27 @@ __global__ void __launch_bounds__(256) append_kernel(const RowsParams p, int k_b
     }
 }
 
+// One quad per (row, head, pair of blocks): lanes q / 2 = 0 and 1 have a block
+// each, and of it the dims 8 (q % 2) .. + 7 and the 8 that are 16 on, which are
+// the low and the high nibbles of the same 8 bytes.  (With 8 dims of one block
+// to a lane, its places worked out for half as many values: 29 us for 26 on the
+// rows above; with four pairs in flight instead of two, as fast there and 20%
+// slower on few rows.)
+constexpr int kPairs = 2;  // per thread, loaded before the first is decoded
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
     constexpr int NB = D / 32;
     const bool is_v = blockIdx.y != 0;
     void *out = is_v ? p.vo : p.ko;
     if (!out) return;
-    const int q = threadIdx.x & 3;
-    const Units units(blockIdx.x, NB * p.pool.Hk);
-    int64_t row[kInFlight], slot[kInFlight];
-    uint32_t in_row[kInFlight];
-    uint32_t w[kInFlight][2];  // K: bytes 8 (q % 2) .. + 7 of the block; V: [0] bytes 2q, 2q + 8, 2q + 1, 2q + 9
-    __half d[kInFlight];
+    const int q = threadIdx.x & 3, side = q & 1;
+    const Units units(blockIdx.x, kPairs, NB / 2 * p.pool.Hk);
+    int64_t row[kPairs], slot[kPairs];
+    uint32_t in_row[kPairs];
+    uint32_t w[kPairs][2];  // bytes 8 side .. + 7 of the block; of V at first bytes j and j + 8 for j = 4 side .. + 3
+    __half d[kPairs];
 #pragma unroll
-    for (int m = 0; m < kInFlight; ++m) {
+    for (int m = 0; m < kPairs; ++m) {
         const uint32_t u = units.rem + 64 * m + (threadIdx.x >> 2), r = u / units.per_row;
         row[m] = units.row + r;
         in_row[m] = u - r * units.per_row;
@@ -366,74 +373,77 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
         if ((slot[m] >> p.pool.lgP) >= p.pool.n_pages) slot[m] = -1;
     }
 #pragma unroll
-    for (int m = 0; m < kInFlight; ++m) {
+    for (int m = 0; m < kPairs; ++m) {
         w[m][0] = w[m][1] = 0x88888888u;  // no slot: zeros
         d[m] = __ushort_as_half(0);
         if (slot[m] < 0) continue;
-        const int b = in_row[m] % NB, h = in_row[m] / NB;
+        const int b = in_row[m] % (NB / 2) * 2 + (q >> 1), h = in_row[m] / (NB / 2);
         const int tp = (int)(slot[m] & (p.pool.P - 1)), t = tp & 31;
         const uint8_t *tile = p.pool.pages + (slot[m] >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes + (int64_t)(tp >> 5) * (36 * D);
         if (!is_v) {
-            w[m][0] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1), NB));
-            w[m][1] = *reinterpret_cast<const uint32_t *>(tile + k_word(t, b, 2 * (q & 1) + 1, NB));
+            const uint8_t *at = tile + k_word(t, b, 2 * side, NB);
+            w[m][0] = *reinterpret_cast<const uint32_t *>(at);
+            w[m][1] = *reinterpret_cast<const uint32_t *>(at + k_word(0, 0, 1, NB));
             d[m] = reinterpret_cast<const __half *>(tile + 16 * D)[k_scale(t, b, NB)];
         } else {
-            w[m][0] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q, NB));
-            w[m][1] = *reinterpret_cast<const uint16_t *>(tile + 18 * D + v_half(t, b, 2 * q + 1, NB));
+            const uint8_t *at = tile + 18 * D + v_half(t, b, 4 * side, NB);
+            uint32_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint16_t *>(at + v_half(0, 0, j, NB));
+            w[m][0] = x[0] | x[1] << 16;
+            w[m][1] = x[2] | x[3] << 16;
             d[m] = reinterpret_cast<const __half *>(tile + 34 * D)[v_scale(t, b, NB)];
         }
     }
 #pragma unroll
-    for (int m = 0; m < kInFlight; ++m) {
-        if (is_v) {
-            const uint32_t mine = (w[m][0] & 0xffffu) | w[m][1] << 16;
-            const int base = threadIdx.x & 28;
-            const uint32_t sel = q & 1 ? 0x7531u : 0x6420u;  // bytes 8 .. 15 or 0 .. 7
-            const uint32_t m0 = __shfl_sync(0xffffffffu, mine, base), m1 = __shfl_sync(0xffffffffu, mine, base + 1);
-            const uint32_t m2 = __shfl_sync(0xffffffffu, mine, base + 2), m3 = __shfl_sync(0xffffffffu, mine, base + 3);
-            w[m][0] = __byte_perm(m0, m1, sel);
-            w[m][1] = __byte_perm(m2, m3, sel);
+    for (int m = 0; m < kPairs; ++m) {
+        if (is_v) {  // the lane next to it has the other half of the low bytes and of the high ones
+            const uint32_t low = __byte_perm(w[m][0], w[m][1], 0x6420u), high = __byte_perm(w[m][0], w[m][1], 0x7531u);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, side ? low : high, 1);
+            w[m][0] = side ? got : low;
+            w[m][1] = side ? high : got;
         }
-        const int64_t at = (row[m] * units.per_row + in_row[m]) * 32 + 8 * q;
         if (row[m] >= p.n) continue;
+        const int64_t at = (row[m] * units.per_row + in_row[m]) * 64 + 32 * (q >> 1) + 8 * side;
         // a nibble in the mantissa under exponent 0x64 is 1024 + n: minus 1032, exact; times the scale, rounded once
-        uint32_t code[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t nib = (q < 2 ? w[m][e] : w[m][e] >> 4) & 0x0f0f0f0fu;
-            code[2 * e] = hsub2(__byte_perm(nib, 0x64646464u, 0x4140), 0x64086408u);
-            code[2 * e + 1] = hsub2(__byte_perm(nib, 0x64646464u, 0x4342), 0x64086408u);
-        }
-        if (p.dtype == KVS_F16) {
-            const __half2 s2 = __half2half2(d[m]);
-            uint32_t o[4];
+        for (int part = 0; part < 2; ++part) {  // dims 8 side .. + 7, then those + 16
+            uint32_t code[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&code[e]), s2);
-                o[e] = *reinterpret_cast<const uint32_t *>(&v);
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t nib = (part ? w[m][e] >> 4 : w[m][e]) & 0x0f0f0f0fu;
+                code[2 * e] = hsub2(__byte_perm(nib, 0x64646464u, 0x4140), 0x64086408u);
+                code[2 * e + 1] = hsub2(__byte_perm(nib, 0x64646464u, 0x4342), 0x64086408u);
             }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
-            continue;
-        }
-        const float s1 = __half2float(d[m]);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&code[e]));
-            f[2 * e] = v.x * s1, f[2 * e + 1] = v.y * s1;
-        }
-        if (p.dtype == KVS_F32) {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
-            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
             uint32_t o[4];
+            if (p.dtype == KVS_F16) {
+                const __half2 s2 = __half2half2(d[m]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-                o[e] = *reinterpret_cast<const uint32_t *>(&a);
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&code[e]), s2);
+                    o[e] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+            } else {
+                const float s1 = __half2float(d[m]);
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&code[e]));
+                    f[2 * e] = v.x * s1, f[2 * e + 1] = v.y * s1;
+                }
+                if (p.dtype == KVS_F32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at + 16 * part);
+                    dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                    o[e] = *reinterpret_cast<const uint32_t *>(&a);
+                }
             }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at + 16 * part) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -1637,7 +1647,7 @@ extern "C" kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_row
     return KVS_OK;
 }
 
-static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, int32_t dtype, RowsParams *p, unsigned *blocks) {
+static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, int32_t dtype, RowsParams *p) {
     kvs_status s = check_pool(pool, true, &p->pool);
     if (s != KVS_OK) return s;
     if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
@@ -1648,15 +1658,13 @@ static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint6
     p->slots = slots;
     p->n = (int64_t)n;
     p->dtype = dtype;
-    *blocks = (unsigned)((n * units + 64 * kInFlight - 1) / (64 * kInFlight));
     return KVS_OK;
 }
 
 extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, const void *k, const void *v,
                                     int32_t dtype, uint64_t k_stride, uint64_t v_stride, void *stream) {
     RowsParams p = {};
-    unsigned blocks = 0;
-    kvs_status s = rows_call(pool, slots, n, dtype, &p, &blocks);
+    kvs_status s = rows_call(pool, slots, n, dtype, &p);
     if (s != KVS_OK) return s;
     if (n == 0) return KVS_OK;
     const uint64_t row = (uint64_t)pool->n_kv_head * pool->head_dim, e = elem_size(dtype);
@@ -1668,6 +1676,7 @@ extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slot
     p.v_stride = (int64_t)v_stride;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint32_t D = pool->head_dim;
+    const uint64_t blocks = (n * (row / 32) + 64 * kInFlight - 1) / (64 * kInFlight);
     const uint64_t v_blocks = (n + 31) / 32 * pool->n_kv_head;
     const cudaError_t ce = launch(D == 64 ? append_kernel<64> : D == 128 ? append_kernel<128> : append_kernel<256>,
                                   dim3((unsigned)(blocks + v_blocks)), 256, 0, st, false, p, (int)blocks);
@@ -1677,15 +1686,15 @@ extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slot
 extern "C" kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, void *k, void *v, int32_t dtype,
                                   void *stream) {
     RowsParams p = {};
-    unsigned blocks = 0;
-    kvs_status s = rows_call(pool, slots, n, dtype, &p, &blocks);
+    kvs_status s = rows_call(pool, slots, n, dtype, &p);
     if (s != KVS_OK) return s;
     if (!aligned(k, 16) || !aligned(v, 16)) return bad(KVS_ERR_INVALID, "k and v must be 16-byte aligned");
     if (n == 0 || (!k && !v)) return KVS_OK;
     p.ko = k;
     p.vo = v;
+    const uint64_t pairs = n * pool->n_kv_head * (pool->head_dim / 64);
     auto kernel = pool->head_dim == 64 ? read_kernel<64> : pool->head_dim == 128 ? read_kernel<128> : read_kernel<256>;
-    const cudaError_t ce = launch(kernel, dim3(blocks, 2), 256, 0, static_cast<cudaStream_t>(stream), false, p);
+    const cudaError_t ce = launch(kernel, dim3((unsigned)((pairs + 64 * kPairs - 1) / (64 * kPairs)), 2), 256, 0, static_cast<cudaStream_t>(stream), false, p);
     return ce == cudaSuccess ? KVS_OK : cuda_failed("read launch", ce);
 }
 
