@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from threading import get_ident as _get_ident
 
 import numpy as np
 
@@ -856,8 +857,8 @@ class Q4Cache:
     ``pages`` is a uint8 CUDA tensor of whole pages in the layout include/kvs.h states (or give ``n_pages`` and
     ``device`` to have one allocated, zeroed).  Page tables (int32 [n_seq][width]), lengths (int32 [n_seq]) and slots
     (int64: page * page_tokens + token) are CUDA tensors that the caller keeps.  Every call runs on the current
-    stream; attend keeps a workspace per stream, and takes one of its own for each captured call, so calls on several
-    streams and captured graphs do not share one.
+    stream; attend keeps a workspace per stream and thread, and takes one of its own for each captured call, so calls
+    on several streams, from several threads and in captured graphs do not share one.
     """
 
     def __init__(self, *, page_tokens, n_kv_head, head_dim, pages=None, n_pages=None, device="cuda"):
@@ -873,7 +874,7 @@ class Q4Cache:
         self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
         self._ref, self._lib = ctypes.byref(pool), load()
         self._need_bytes = {}  # by (rows, heads, dtype)
-        self._spaces = {}      # workspaces by stream
+        self._spaces = {}      # workspaces by stream and thread
 
     def append(self, slots, k, v):
         """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
@@ -928,11 +929,12 @@ class Q4Cache:
         return out, lse
 
     def _workspace(self, need):
-        """attend's workspace: one per stream, whose calls run in order; a call being captured gets one of its own from
-        the graph's memory, since graphs of one stream may be replayed side by side."""
+        """attend's workspace: one per stream and thread, whose calls run in order (another thread's may come between the
+        two launches of one); a call being captured gets one of its own from the graph's memory, since graphs of one
+        stream may be replayed side by side."""
         if _torch.cuda.is_current_stream_capturing():
             return _torch.empty(need, dtype=_torch.uint8, device=self.device)
-        stream = _stream_of(self.device.index) if self.device.type == "cuda" else 0
+        stream = (_stream_of(self.device.index) if self.device.type == "cuda" else 0, _get_ident())
         ws = self._spaces.get(stream)
         if ws is None or ws.numel() < need:
             ws = self._spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=self.device)

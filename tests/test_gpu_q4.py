@@ -293,6 +293,30 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, want[i][0]) and torch.equal(z, want[i][1]) for o, z in got[i])
 
 
+def test_two_threads_on_one_stream():
+    """A call is two launches; another thread's may come between them."""
+    import threading
+    import torch
+    f = Filled([9000, 70], 2, 128, 64, seed=15, dt="f16")
+    qs = [torch.randn(2, 1, 8, 128, generator=torch.Generator().manual_seed(i)).half().cuda() for i in range(2)]
+    want = [f.cache.attend(f.table_t, f.lens_t, q) for q in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(300):
+            got[i].append(f.cache.attend(f.table_t, f.lens_t, qs[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 300 and all(torch.equal(o, want[i][0]) and torch.equal(z, want[i][1]) for o, z in got[i])
+
+
 # ------------------------------------------------------------------ weights
 
 @pytest.mark.parametrize("dt", DT)
