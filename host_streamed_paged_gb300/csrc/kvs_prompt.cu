@@ -249,10 +249,9 @@ __device__ __forceinline__ void find_sorted(const PromptParams &p, int c, int pe
         return __reduce_add_sync(0xffffffffu, n);
     };
     int lo = 0, hi = most - 1, above = 0;  // the largest level with c < units(level); above: units(lo + 1) at the end
-    if (c >= units(0)) {
-        if (lane == 0) place[0] = -1;
-        return;
-    }
+    if (lane == 0) place[0] = -1;
+    __syncwarp();
+    if (c >= units(0)) return;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1, n = units(mid);
         if (c < n) lo = mid;

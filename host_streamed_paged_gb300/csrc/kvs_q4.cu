@@ -1744,7 +1744,6 @@ extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *tab
     kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p.a);
     if (s != KVS_OK) return s;
     if (!lse || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
-    if ((uint64_t)n_seq * pool->n_kv_head > 65535) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head must be at most 65535");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (n_seq == 0 || width == 0) return KVS_OK;
     const uint32_t D = pool->head_dim, rows = n_rows * p.a.G;

@@ -775,9 +775,9 @@ typedef struct {
  *   lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j.
  * out: device [total_rows][n_q_head][D] in dtype, rows out_stride apart; lse
  * (nullable): device fp32 [total_rows][n_q_head].  Rows of no prompt are left
- * as they were.  Products run on the tensor cores with fp32 accumulation, the
- * softmax in fp32; the softmax weights are rounded to dtype before the second
- * product.
+ * as they were.  out overlaps none of q, k and v.  Products run on the tensor
+ * cores with fp32 accumulation, the softmax in fp32; the softmax weights are
+ * rounded to dtype before the second product.
  */
 kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream);
 
@@ -790,7 +790,7 @@ kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride
  * is kvs_prompt_attend's.  prev (nullable: zeros) and weights: device fp32
  * [n_seq][n_kv_head][width]; keys beyond width are not counted, entries beyond
  * a prompt's length are prev's.  prev may be weights.  Sums run in a fixed
- * order.
+ * order.  n_seq * n_kv_head is at most 65535.
  */
 kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,
                               float *weights, uint64_t width, void *stream);

@@ -53,7 +53,7 @@ def test_ties_go_to_the_lowest_index_and_odd_values_have_an_order():
     run(lens, 1, 64, 64, 130, 3, 17, w)
 
 
-@pytest.mark.parametrize("T", [9000, 40000, 140001, 300007])
+@pytest.mark.parametrize("T", [9000, 40000, 140001, 300007, 400001])
 def test_long_sequences_shared_by_a_cluster(T):
     lens = [T, 8191, 60]
     rng = np.random.default_rng(T)

@@ -64,6 +64,8 @@ CASES = [  # D, Hk, G, lens
     (256, 1, 6, [1, 37, 64, 65, 300]),
     (256, 2, 1, [127, 129, 400]),
     (256, 1, 7, [90, 33, 18]),
+    (256, 1, 50, [7, 30]),
+    (256, 2, 5, [19, 20, 39, 200]),
 ]
 
 
@@ -80,6 +82,27 @@ def test_attend(D, Hk, G, lens, dt):
     # rows of no prompt, and what lies between the rows, are left as they were
     assert (wide[:3] == 7).all() and (wide[-5:] == 7).all() and (wide[:, Hk * G:] == 7).all()
     assert (lse[:3] == 7).all() and (lse[-5:] == 7).all()
+
+
+@pytest.mark.parametrize("n", [33, 256, 300])
+def test_many_prompts(n):
+    """More prompts than a warp has lanes, up to and past those that are ordered by work; the keys' weights as well."""
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    lens = np.random.default_rng(n).integers(0, 60, n).tolist()
+    lens[n // 2] = 400
+    q, k, v, cu = make(lens, 2, 3, 64, "f16", seed=n)
+    out, lse = kvs.prompt_attend(q, k, v, cu)
+    check(out, lse, q, k, v, cu, "f16", 1 / 8)
+    got = kvs.prompt_weights(q, k, lse, cu, 400).double().cpu().numpy()
+    qn, kn, zn = (x.double().cpu().numpy() for x in (q, k, lse))
+    c = cu.tolist()
+    for i, L in enumerate(lens):
+        w = np.zeros((2, 400))
+        if L:
+            s = slice(c[i], c[i + 1])
+            w[:, :L] = ref.prompt_weights(qn[s], kn[s], zn[s], 1 / 8, 0)
+        assert (np.abs(got[i] - w) <= (5e-5 + L * 3 / 4 * 2.0 ** -24) * w + 1e-37).all(), i
 
 
 def test_large_scores_move_the_maximum_late():
