@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kPer = D / 16 / NP;  // 16-dim steps of a piece
                 const uint64_t db = dk + (uint64_t)((stage(r, s / kPer) * S::kPiece + (s % kPer >> 2) * (BN * 128) + (s & 3) * 32) >> 4);
                 mma_ss(d, da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4), db, id_s, s > 0);
+                if (s % kPer == kPer - 1) mma_commit(b_empty(stage(r, s / kPer)));  // its loads need not wait for the rest
             }
             mma_commit(b_s(i, j & 1));
         };
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kPer = BN / 16 / NP;  // 16-key steps of a piece
                 const uint64_t db = dv + (uint64_t)((stage(r, s / kPer) * S::kPiece + s % kPer * 2048) >> 4);
                 mma_ts(d, a + (uint32_t)(8 * s), db, id_o, (j > 0 || s > 0) ? 1u : 0u);
+                if (s % kPer == kPer - 1) mma_commit(b_empty(stage(r, s / kPer)));
             }
             mma_commit(b_o(i, j & 1));
         };
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_after();
             if (one) {
                 if (j < n) issue_s(j);
-                freed(ring_k(j));
+                else freed(ring_k(j));
             }
         }
         // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
@@ -512,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_after();
             if (one) {
                 if (j < n) issue_o(j);
-                freed(ring_v(j));
+                else freed(ring_v(j));
                 if (j + 2 < n) issue_s(j + 2);
-                if (more) freed(ring_k(j + 2));
+                else if (more) freed(ring_k(j + 2));
             }
         }
         if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
