@@ -1051,6 +1051,27 @@ kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t 
     return e == cudaSuccess ? KVS_OK : cuda_failed("prompt attention launch", e);
 }
 
+// How many CTAs share a key tile's rows.  A CTA costs kStart tiles before and after its own; a unit's tiles go from none
+// to the prompt's over all rows (half of them on average; the longest of several prompts is taken for 1.5 times the
+// mean, which is all the host knows), or are the window's.  The launch ends no sooner than its whole cost spread over the
+// slots, and than its longest CTA: the least of that over 1, 2, 4 and 8.  Measured on 7 batches, in us for 1 / 2 / 4 / 8:
+// 33 units of 256 tiles 220 / 114 / 61 / 38, 64 of 8 13 / 11 / 9.5 / 15, 154 of 196 432 / 224 / 134 / 143, 488 of 57
+// 140 / 122 / 139 / 179, 616 of 18 41 / 50 / 72 / 114.
+unsigned sharing_ctas(uint64_t units, uint64_t slots, uint64_t tiles, bool several, uint64_t window) {
+    constexpr double kStart = 8;
+    const bool windowed = window > 0 && window < tiles;
+    const double all = (double)(windowed ? window : tiles), mean = windowed ? all : all / 2;
+    const double longest = windowed || !several ? all : 1.5 * all;
+    unsigned best = 1;
+    double least = 0;
+    for (unsigned r = 1; r <= 8; r *= 2) {
+        const double spread = (double)units * (r * kStart + mean) / (double)slots, end = kStart + longest / r;
+        const double cost = spread > end ? spread : end;
+        if (r == 1 || cost < least) best = r, least = cost;
+    }
+    return best;
+}
+
 template <int D>
 kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
     using S = WeightShape<D>;
@@ -1060,11 +1081,10 @@ kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t
     if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
     if (r != KVS_OK) return r;
     const uint64_t units = (uint64_t)p->total_rows / kTileRows + p->n_seq;
-    if (units * p->n_kv_head > 0x1fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
-    // Over all rows, a unit's work goes from one query tile to the whole prompt's: while a launch has few units per SM,
-    // clusters of 4 (2) share each, so that the longest ends with the rest.  An observation window is even work.
-    const uint64_t ctas = units * p->n_kv_head, sms = (uint64_t)current_device_sms();
-    const unsigned ranks = pp.last_rows > 0 ? 1 : ctas < 32 * sms ? 2 : 1;
+    if (units * p->n_kv_head > 0xfffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
+    const uint64_t ctas = units * p->n_kv_head, slots = 2 * (uint64_t)current_device_sms();
+    const unsigned ranks = sharing_ctas(ctas, slots, (uint64_t)p->total_rows * pp.G / S::BQ / p->n_seq, p->n_seq > 1,
+                                        (uint64_t)pp.last_rows * pp.G / S::BQ);
     auto kernel = bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), S::kSmem);
     if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
