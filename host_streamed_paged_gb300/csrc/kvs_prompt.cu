@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // place at every 16 dims, always towards zero, and with 256 dims in a row the
 // weights came out 1.1e-6 low, 6.5e-7 like this (for 46 -> 50 us).
 // Prompts of 4096 .. 33 tokens, 32 / 8 heads, D 128, over all rows: 122 us
-// (exponential unit busy 64%; 143 us with two key tiles in one CTA of 16 sum
+// (66% of 16 exponentials a clock and SM; 143 us with two key tiles in one CTA of 16 sum
 // warps; with 2 to all of 16 exponentials as polynomials on the FMA pipes those
 // took 147 to 173).  The last 64 rows of 32768, 24 / 4 heads, D 256: 50 us.
 constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA

@@ -146,7 +146,18 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 // the block, w = 0, 2, 1, 3 for q = 0 .. 3.  (The kernels below are bound by
 // instructions, so: m from the largest and the smallest element, in order only
 // where those tie; x / -8 is x * -0.125; the code is read off the mantissa of
-// the sum rounded down onto 2^23.)
+// the sum rounded down onto 2^23, two values an instruction.)
+// x * id + 8.5, each rounded to nearest, then rounded down onto 2^23: a code in the low bits.  Two values an instruction.
+// (The product is a multiply-add of 0: a plain multiply and the add after it may be joined into one rounding.)
+__device__ __forceinline__ float2 scaled_rz(float2 x, float id) {
+    float2 r;
+    const float2 s = make_float2(id, id), h = make_float2(8.5f, 8.5f), big = make_float2(8388608.f, 8388608.f);
+    asm("{\n .reg .b64 t;\n fma.rn.f32x2 t, %1, %2, %5;\n add.rn.f32x2 t, t, %3;\n add.rz.f32x2 %0, t, %4;\n}\n"
+        : "=l"(*reinterpret_cast<uint64_t *>(&r))
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&s)),
+          "l"(*reinterpret_cast<const uint64_t *>(&h)), "l"(*reinterpret_cast<const uint64_t *>(&big)), "l"(0ull));
+    return r;
+}
 __device__ __forceinline__ uint32_t q4_word(const float *x, int q, float &d) {
     float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
     float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), fminf(x[6], x[7]));
@@ -173,17 +184,26 @@ __device__ __forceinline__ uint32_t q4_word(const float *x, int q, float &d) {
     }
     d = __fmul_rn(m, -0.125f);
     const float id = (d != 0.0f) ? __frcp_rn(d) : 0.0f;
-    uint32_t k[8];
+    uint32_t k[4];  // a code per half
+    if (__any_sync(0xffffffffu, isinf(id))) {  // 1/d overflows below 2^-128: the other elements' codes are 0 or 15, 0 / d is 0's
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float u = fmaxf(__fadd_rn(__fmul_rn(x[i], id), 8.5f), 0.f);  // (NaN, of 0 / a scale below 2^-128: code 0)
-        const int r = __float_as_int(__fadd_rz(u, 8388608.f));
-        k[i] = (uint32_t)(r < 0x4b00000f ? r : 0x4b00000f);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t c[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float u = fmaxf(__fadd_rn(__fmul_rn(x[2 * i + e], id), 8.5f), 0.f);
+                c[e] = __float_as_uint(__fadd_rz(fminf(u, 15.f), 8388608.f)) & 15u;
+            }
+            k[i] = c[0] | c[1] << 16;
+        }
+    } else {  // x / d is within -8 .. 8 but for a rounding: the sum is positive and the code at most 16
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 r = scaled_rz(make_float2(x[2 * i], x[2 * i + 1]), id);
+            k[i] = __vminu2(__byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x5410), 0x000f000fu);
+        }
     }
-    uint32_t c[2];  // a code per byte
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        c[i] = __byte_perm(__byte_perm(k[4 * i], k[4 * i + 1], 0x0040), __byte_perm(k[4 * i + 2], k[4 * i + 3], 0x0040), 0x5410);
+    const uint32_t c[2] = {__byte_perm(k[0], k[1], 0x6420), __byte_perm(k[2], k[3], 0x6420)};  // a code per byte
     // lanes 0, 1 have the low nibbles of bytes 0-7, 8-15; lanes 2, 3 the high ones
     const uint32_t got = __shfl_xor_sync(0xffffffffu, q < 2 ? c[1] : c[0], 2);
     return q < 2 ? c[0] | got << 4 : got | c[1] << 4;
@@ -267,13 +287,14 @@ __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
         const int64_t s = slot[r + 3];
         return s >= 0 && (s & 3) == 0 && slot[r + 4] == s + 1 && slot[r + 5] == s + 2 && slot[r + 6] == s + 3;
     };
+    const int rows = begins(kRows - 3) || begins(kRows - 2) || begins(kRows - 1) ? kAll : kRows;
     float v[kPass][8];
 #pragma unroll
     for (int m = 0; m < kPass; ++m) {
         const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[m][e] = 0.f;
-        if (r < kAll && i0 + r < p.n && slot[r + 3] >= 0) load8(p.v, p.dtype, (i0 + r) * p.v_stride + (int64_t)h * D + b * 32 + 8 * q, v[m]);
+        if (r < rows && i0 + r < p.n && slot[r + 3] >= 0) load8(p.v, p.dtype, (i0 + r) * p.v_stride + (int64_t)h * D + b * 32 + 8 * q, v[m]);
     }
     if (tid < 32) {
         const uint32_t at = __ballot_sync(0xffffffffu, begins(tid));
@@ -283,9 +304,10 @@ __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
 #pragma unroll
     for (int m = 0; m < kPass; ++m) {
         const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
+        if ((x & ~7) >= rows * NB) break;  // (the same in a warp)
         float d;
         const uint32_t w = q4_word(v[m], q, d);
-        if (r < kAll) {
+        if (r < rows) {
             code[r][b * 4 + word_of(q)] = w;
             if (q == 0) scale[r][b] = __half_as_ushort(__float2half_rn(d));
         }
