@@ -203,6 +203,7 @@ struct PromptParams {
     float *w;
     int64_t width;
     int last_rows;
+    int main_ctas;  // those past them copy what no key writes
 };
 
 __device__ __forceinline__ int cu_begin(const PromptParams &p, int s) {
@@ -695,6 +696,26 @@ struct WeightShape {
     static_assert(kSmem + 1024 <= 114 * 1024, "two CTAs per SM");
 };
 
+// entries past a prompt's length: prev's (or zero); kRest of a (prompt, head) per CTA
+constexpr int kRestEach = 8, kRest = kWThreads * kRestEach;
+__device__ void weights_rest(const PromptParams &p, int64_t block) {
+    const int64_t per = (p.width + kRest - 1) / kRest, sh = block / per;
+    if (sh >= (int64_t)p.n_seq * p.Hk) return;
+    const int s = (int)(sh / p.Hk), len = cu_end(p, s) - cu_begin(p, s);
+    const int64_t from = (block - sh * per) * kRest + threadIdx.x, row = sh * p.width;
+    float v[kRestEach];
+#pragma unroll
+    for (int u = 0; u < kRestEach; ++u) {
+        const int64_t i = from + kWThreads * u;
+        v[u] = p.prev && i >= len && i < p.width ? p.prev[row + i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kRestEach; ++u) {
+        const int64_t i = from + kWThreads * u;
+        if (i >= len && i < p.width) p.w[row + i] = v[u];
+    }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kWThreads, 2)
     prompt_weights_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
@@ -703,6 +724,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
     constexpr int BQ = S::BQ, NST = S::kStages, kCols = S::kCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    if ((int)blockIdx.x >= p.main_ctas) return weights_rest(p, (int)blockIdx.x - p.main_ctas);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = smem_u32(smem + S::kOffBar);
     auto b_full = [&](int s) { return bars + 8u * s; };
@@ -932,25 +954,6 @@ __global__ void __launch_bounds__(kWThreads, 2)
     if (ranks > 1) cl.sync();  // no CTA leaves while another may read its sums
 }
 
-// entries past a prompt's length: prev's (or zero); 2048 of a (prompt, head) per CTA
-constexpr int kRest = 2048;
-__global__ void __launch_bounds__(256) prompt_rest_kernel(const PromptParams p) {
-    const int s = blockIdx.y / p.Hk;
-    const int len = cu_end(p, s) - cu_begin(p, s);
-    const int64_t from = (int64_t)blockIdx.x * kRest + threadIdx.x, row = (int64_t)blockIdx.y * p.width;
-    float v[kRest / 256];
-#pragma unroll
-    for (int u = 0; u < kRest / 256; ++u) {
-        const int64_t i = from + 256 * u;
-        v[u] = p.prev && i >= len && i < p.width ? p.prev[row + i] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kRest / 256; ++u) {
-        const int64_t i = from + 256 * u;
-        if (i >= len && i < p.width) p.w[row + i] = v[u];
-    }
-}
-
 // ---------------------------------------------------------------- host side
 
 kvs_status bad(kvs_status s, const char *why) {
@@ -1073,23 +1076,30 @@ unsigned sharing_ctas(uint64_t units, uint64_t slots, uint64_t tiles, bool sever
 }
 
 template <int D>
-kvs_status weights_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
+kvs_status weights_for(const kvs_prompt *p, PromptParams pp, cudaStream_t s) {
     using S = WeightShape<D>;
     const bool bf = p->dtype == KVS_BF16;
-    CUtensorMap mq, mk;
-    kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, (uint32_t)(S::BQ / pp.G));
-    if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
-    if (r != KVS_OK) return r;
-    const uint64_t units = (uint64_t)p->total_rows / kTileRows + p->n_seq;
-    if (units * p->n_kv_head > 0xfffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
-    const uint64_t ctas = units * p->n_kv_head, slots = 2 * (uint64_t)current_device_sms();
-    const unsigned ranks = sharing_ctas(ctas, slots, (uint64_t)p->total_rows * pp.G / S::BQ / p->n_seq, p->n_seq > 1,
-                                        (uint64_t)pp.last_rows * pp.G / S::BQ);
+    CUtensorMap mq = {}, mk = {};
+    uint64_t ctas = 0;
+    unsigned ranks = 1;
+    if (p->total_rows) {
+        kvs_status r = make_map(&mq, p->q, bf, p->total_rows, p->n_q_head, D, p->q_stride, (uint32_t)pp.G, (uint32_t)(S::BQ / pp.G));
+        if (r == KVS_OK) r = make_map(&mk, p->k, bf, p->total_rows, p->n_kv_head, D, p->k_stride, 1, kTileRows);
+        if (r != KVS_OK) return r;
+        ctas = ((uint64_t)p->total_rows / kTileRows + p->n_seq) * p->n_kv_head;
+        ranks = sharing_ctas(ctas, 2 * (uint64_t)current_device_sms(), (uint64_t)p->total_rows * pp.G / S::BQ / p->n_seq, p->n_seq > 1,
+                             (uint64_t)pp.last_rows * pp.G / S::BQ);
+    }
+    const uint64_t rest = pp.prev != pp.w ? (uint64_t)p->n_seq * p->n_kv_head * (((uint64_t)pp.width + kRest - 1) / kRest) : 0;
+    const uint64_t grid = (ctas * ranks + rest + ranks - 1) / ranks * ranks;
+    if (grid > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "total_rows or n_seq * n_kv_head * width too large for one launch");
+    if (grid == 0) return KVS_OK;
+    pp.main_ctas = (int)(ctas * ranks);
     auto kernel = bf ? prompt_weights_kernel<D, true> : prompt_weights_kernel<D, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), S::kSmem);
     if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas * ranks);
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kWThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -1127,8 +1137,7 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
     PromptParams pp = {};
     kvs_status s = check_prompt(p, false, &pp);
     if (s != KVS_OK) return s;
-    if (!lse || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
-    if ((uint64_t)p->n_seq * p->n_kv_head > 65535) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head must be at most 65535");
+    if ((p->total_rows && !lse) || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (p->n_seq == 0 || width == 0) return KVS_OK;
     pp.lse_in = lse;
@@ -1137,14 +1146,5 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
     pp.width = (int64_t)width;
     pp.last_rows = last_rows > 0x7fffffffu ? 0x7fffffff : (int)last_rows;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (p->total_rows) {
-        s = p->head_dim == 64 ? weights_for<64>(p, pp, st) : p->head_dim == 128 ? weights_for<128>(p, pp, st) : weights_for<256>(p, pp, st);
-        if (s != KVS_OK) return s;
-    }
-    if (prev != weights) {
-        prompt_rest_kernel<<<dim3((unsigned)((width + kRest - 1) / kRest), p->n_seq * p->n_kv_head), 256, 0, st>>>(pp);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_failed("prompt weights launch", e);
-    }
-    return KVS_OK;
+    return p->head_dim == 64 ? weights_for<64>(p, pp, st) : p->head_dim == 128 ? weights_for<128>(p, pp, st) : weights_for<256>(p, pp, st);
 }

@@ -790,7 +790,7 @@ kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride
  * is kvs_prompt_attend's.  prev (nullable: zeros) and weights: device fp32
  * [n_seq][n_kv_head][width]; keys beyond width are not counted, entries beyond
  * a prompt's length are prev's.  prev may be weights.  Sums run in a fixed
- * order.  n_seq * n_kv_head is at most 65535.
+ * order.
  */
 kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,
                               float *weights, uint64_t width, void *stream);

@@ -165,6 +165,19 @@ def test_weights(D, Hk, G, lens, window, dt):
         assert (np.abs(summed[i].double().cpu().numpy() - w - pn[i]) <= tol + 2.0 ** -22 * (w + pn[i])).all(), i
 
 
+def test_weights_of_empty_prompts_are_what_was_there():
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    prev = torch.rand(3, 2, 5000, generator=torch.Generator().manual_seed(2)).cuda()
+    for rows in (0, 4):  # no rows at all; rows of no prompt
+        q, k = (torch.zeros(rows, h, 64, dtype=torch.float16, device="cuda") for h in (4, 2))
+        cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+        lse = torch.zeros(rows, 4, device="cuda")
+        assert torch.equal(kvs.prompt_weights(q, k, lse, cu, 5000, prev=prev), prev)
+        assert not kvs.prompt_weights(q, k, lse, cu, 5000).any()
+        assert kvs.prompt_attend(q, k, k, cu)[0].shape == q.shape
+
+
 def test_replayed_graph_follows_the_offsets():
     import torch
     from host_streamed_paged_gb300 import kvs
