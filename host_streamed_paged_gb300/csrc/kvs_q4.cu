@@ -63,24 +63,6 @@ __device__ __forceinline__ float2 two(uint32_t w, int dtype) {
     if (dtype == KVS_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
-// N consecutive elements from a 16-byte (8-byte for N = 4 of 16 bits) aligned place
-template <int N>
-__device__ __forceinline__ void load_row(const void *p, int dtype, int64_t i, float *x) {
-    if (dtype == KVS_F32) {
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + j);
-            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i + j);
-            const float2 a = two(v.x, dtype), b = two(v.y, dtype);
-            x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
-        }
-    }
-}
 
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -118,15 +100,26 @@ struct RowsParams {
     int dtype;
 };
 
-__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, float *x) {
-    if (dtype == KVS_F32) {
-        load_row<8>(p, dtype, i, x);
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-        const float2 a = two(v.x, dtype), b = two(v.y, dtype), c = two(v.z, dtype), d = two(v.w, dtype);
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+// 8 consecutive elements as they lie in memory, and as fp32
+template <bool F32>
+struct Eight {
+    uint4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (F32 ? 4 : 2));
+        w[0] = at[0];
+        if (F32) w[F32 ? 1 : 0] = at[1];
     }
-}
+    __device__ __forceinline__ void zero() { w[0] = w[F32 ? 1 : 0] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(int dtype, float *x) const {
+        if constexpr (F32) {
+            x[0] = __uint_as_float(w[0].x), x[1] = __uint_as_float(w[0].y), x[2] = __uint_as_float(w[0].z), x[3] = __uint_as_float(w[0].w);
+            x[4] = __uint_as_float(w[1].x), x[5] = __uint_as_float(w[1].y), x[6] = __uint_as_float(w[1].z), x[7] = __uint_as_float(w[1].w);
+        } else {
+            const float2 a = two(w[0].x, dtype), b = two(w[0].y, dtype), c = two(w[0].z, dtype), d = two(w[0].w, dtype);
+            x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+        }
+    }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -227,14 +220,14 @@ struct Units {
     }
 };
 
-template <int D>
+template <int D, bool F32>
 __device__ void append_k(const RowsParams &p, int64_t block) {
     constexpr int NB = D / 32;
     const int q = threadIdx.x & 3;
     const Units units(block, kInFlight, NB * p.pool.Hk);
     int64_t row[kInFlight];
     uint32_t in_row[kInFlight];
-    float x[kInFlight][8];
+    Eight<F32> x[kInFlight];
     int64_t slot[kInFlight];
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
@@ -246,15 +239,15 @@ __device__ void append_k(const RowsParams &p, int64_t block) {
     }
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[m][e] = 0.f;
-        if (slot[m] >= 0) load8(p.k, p.dtype, row[m] * p.k_stride + in_row[m] * 32 + 8 * q, x[m]);
+        x[m].zero();
+        if (slot[m] >= 0) x[m].load(p.k, row[m] * p.k_stride + in_row[m] * 32 + 8 * q);
     }
 #pragma unroll
     for (int m = 0; m < kInFlight; ++m) {
         const int b = in_row[m] % NB, h = in_row[m] / NB;
-        float d;
-        const uint32_t w = q4_word(x[m], q, d);
+        float d, f[8];
+        x[m].get(p.dtype, f);
+        const uint32_t w = q4_word(f, q, d);
         if (slot[m] < 0) continue;
         const int tp = (int)(slot[m] & (p.pool.P - 1)), t = tp & 31;
         uint8_t *tile = p.pool.pages + (slot[m] >> p.pool.lgP) * p.pool.page_bytes + h * p.pool.head_bytes + (int64_t)(tp >> 5) * (36 * D);
@@ -267,7 +260,7 @@ __device__ void append_k(const RowsParams &p, int64_t block) {
 // CTA encodes 32 rows of a head (and up to 3 more) into shared memory and then
 // stores units: groups of four consecutive rows that fill tokens 4 m .. 4 m + 3
 // of a page, begun in the CTA's 32, whole; other rows two bytes at a time.
-template <int D>
+template <int D, bool F32>
 __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
     constexpr int NB = D / 32, kRows = 32, kAll = kRows + 3, kPass = (kAll * NB + 63) / 64;
     __shared__ uint32_t code[kAll][NB * 4 + 1];  // padded: neighbouring rows on neighbouring banks
@@ -288,13 +281,12 @@ __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
         return s >= 0 && (s & 3) == 0 && slot[r + 4] == s + 1 && slot[r + 5] == s + 2 && slot[r + 6] == s + 3;
     };
     const int rows = begins(kRows - 3) || begins(kRows - 2) || begins(kRows - 1) ? kAll : kRows;
-    float v[kPass][8];
+    Eight<F32> v[kPass];
 #pragma unroll
     for (int m = 0; m < kPass; ++m) {
         const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[m][e] = 0.f;
-        if (r < rows && i0 + r < p.n && slot[r + 3] >= 0) load8(p.v, p.dtype, (i0 + r) * p.v_stride + (int64_t)h * D + b * 32 + 8 * q, v[m]);
+        v[m].zero();
+        if (r < rows && i0 + r < p.n && slot[r + 3] >= 0) v[m].load(p.v, (i0 + r) * p.v_stride + (int64_t)h * D + b * 32 + 8 * q);
     }
     if (tid < 32) {
         const uint32_t at = __ballot_sync(0xffffffffu, begins(tid));
@@ -305,8 +297,9 @@ __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
     for (int m = 0; m < kPass; ++m) {
         const int x = (tid >> 2) + 64 * m, r = x / NB, b = x % NB;
         if ((x & ~7) >= rows * NB) break;  // (the same in a warp)
-        float d;
-        const uint32_t w = q4_word(v[m], q, d);
+        float d, f[8];
+        v[m].get(p.dtype, f);
+        const uint32_t w = q4_word(f, q, d);
         if (r < rows) {
             code[r][b * 4 + word_of(q)] = w;
             if (q == 0) scale[r][b] = __half_as_ushort(__float2half_rn(d));
@@ -357,13 +350,13 @@ __device__ void append_v(const RowsParams &p, int64_t chunk, int h) {
 }
 
 // CTAs 0 .. k_blocks - 1 encode K, the others V (32 rows of a head each).
-template <int D>
-__global__ void __launch_bounds__(256) append_kernel(const RowsParams p, int k_blocks) {
+template <int D, bool F32>
+__global__ void __launch_bounds__(256, F32 ? 3 : 5) append_kernel(const RowsParams p, int k_blocks) {
     if ((int)blockIdx.x < k_blocks) {
-        append_k<D>(p, blockIdx.x);
+        append_k<D, F32>(p, blockIdx.x);
     } else {
         const int64_t c = blockIdx.x - k_blocks;
-        append_v<D>(p, c / p.pool.Hk, (int)(c % p.pool.Hk));
+        append_v<D, F32>(p, c / p.pool.Hk, (int)(c % p.pool.Hk));
     }
 }
 
@@ -1700,8 +1693,9 @@ extern "C" kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slot
     const uint32_t D = pool->head_dim;
     const uint64_t blocks = (n * (row / 32) + 64 * kInFlight - 1) / (64 * kInFlight);
     const uint64_t v_blocks = (n + 31) / 32 * pool->n_kv_head;
-    const cudaError_t ce = launch(D == 64 ? append_kernel<64> : D == 128 ? append_kernel<128> : append_kernel<256>,
-                                  dim3((unsigned)(blocks + v_blocks)), 256, 0, st, false, p, (int)blocks);
+    auto kernel = D == 64 ? append_kernel<64, false> : D == 128 ? append_kernel<128, false> : append_kernel<256, false>;
+    if (dtype == KVS_F32) kernel = D == 64 ? append_kernel<64, true> : D == 128 ? append_kernel<128, true> : append_kernel<256, true>;
+    const cudaError_t ce = launch(kernel, dim3((unsigned)(blocks + v_blocks)), 256, 0, st, false, p, (int)blocks);
     return ce == cudaSuccess ? KVS_OK : cuda_failed("append launch", ce);
 }
 
