@@ -87,8 +87,9 @@ __device__ __forceinline__ int v_scale(int t, int b, int NB) { return ((t >> 2) 
 // Bound by bytes: rows at 2 or 4 bytes per element on one side, 9/16 byte on
 // the other.  Four lanes share a 32-dim block, 8 dims each, so that rows are
 // read and written in whole lines.  22161 rows of 4 x 256 bf16, 116 MB on both
-// sides: read 26 us (4.5 TB/s); append 55 us, bound by the instructions of the
-// encoding (2.1 TB/s).
+// sides: read 25 us (4.6 TB/s); append 38 us (3.1 TB/s), bound by the
+// instructions of the encoding and the wait for its rows, which 40 warps of 48
+// registers hide best (53 us with both element sizes in one kernel of 64).
 
 struct RowsParams {
     Pool pool;
