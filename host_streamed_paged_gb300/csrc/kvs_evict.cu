@@ -368,13 +368,13 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     if (!pool->pages || (reinterpret_cast<uintptr_t>(pool->pages) & 15)) return bad(KVS_ERR_INVALID, "pages null or not 16-byte aligned");
     if (pool->n_pages == 0 || pool->n_pages > 0x7fffffffull) return bad(KVS_ERR_INVALID, "n_pages must be 1 .. 2^31 - 1");
     if (n_seq > (uint32_t)kMaxSeq) return bad(KVS_ERR_UNSUPPORTED, "n_seq must be at most 4096");
-    if (!table || !dst_table || !lens || !weights || !kept || !new_lens) return bad(KVS_ERR_INVALID, "null table, dst_table, lens, weights, kept or new_lens");
+    if (n_seq && (!table || !dst_table || !lens || !weights || !kept || !new_lens)) return bad(KVS_ERR_INVALID, "null table, dst_table, lens, weights, kept or new_lens");
     if (table_width < 1 || (uint64_t)table_width * P > 0x7fffffc0ull) return bad(KVS_ERR_INVALID, "table_width * page_tokens must be 1 .. 2^31 - 64");
     if (width < 1 || width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be 1 .. 2^31 - 1");
     if (keep < 1 || (uint64_t)sinks + recent > keep) return bad(KVS_ERR_INVALID, "need keep >= 1 and sinks + recent <= keep");
     if (keep > 0x7fffffc0u || (uint64_t)dst_width * P < keep) return bad(KVS_ERR_CAPACITY, "dst_width * page_tokens must reach keep");
-    if (kept_weights == weights) return bad(KVS_ERR_INVALID, "kept_weights must not be weights");
-    if (new_lens == lens) return bad(KVS_ERR_INVALID, "new_lens must not be lens");
+    if (n_seq && kept_weights == weights) return bad(KVS_ERR_INVALID, "kept_weights must not be weights");
+    if (n_seq && new_lens == lens) return bad(KVS_ERR_INVALID, "new_lens must not be lens");
     if (n_seq == 0) return KVS_OK;
     EvictParams p = {};
     p.pages = static_cast<uint8_t *>(pool->pages);

@@ -1137,7 +1137,7 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
     PromptParams pp = {};
     kvs_status s = check_prompt(p, false, &pp);
     if (s != KVS_OK) return s;
-    if ((p->total_rows && !lse) || !weights) return bad(KVS_ERR_INVALID, "null lse or weights");
+    if (p->n_seq && width && ((p->total_rows && !lse) || !weights)) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (p->n_seq == 0 || width == 0) return KVS_OK;
     pp.lse_in = lse;

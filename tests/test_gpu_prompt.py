@@ -178,6 +178,28 @@ def test_weights_of_empty_prompts_are_what_was_there():
         assert kvs.prompt_attend(q, k, k, cu)[0].shape == q.shape
 
 
+def test_batches_of_nothing():
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    cache = kvs.Q4Cache(page_tokens=32, n_kv_head=2, head_dim=64, n_pages=2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none, table = torch.zeros(0, **i32), torch.zeros(0, 4, **i32)
+    q = torch.zeros(0, 1, 4, 64, device="cuda")
+    out, lse = cache.attend(table, none, q)
+    assert out.shape == q.shape and lse.shape == q.shape[:3]
+    w = cache.weights(table, none, q, lse)
+    assert w.shape == (0, 2, 128)
+    kept, lens, kw = cache.evict(table, table, none, w, 64)
+    assert kept.shape == kw.shape == (0, 2, 64) and lens.shape == (0,)
+    slots, rows = torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros(0, 2, 64, device="cuda")
+    cache.append(slots, rows, rows)
+    assert cache.read(slots)[0].shape == rows.shape
+    p, c = torch.zeros(0, 4, 64, dtype=torch.float16, device="cuda"), torch.zeros(1, **i32)
+    o, z = kvs.prompt_attend(p, p[:, :2], p[:, :2], c)
+    assert kvs.prompt_weights(p, p[:, :2], z, c, 9).shape == (0, 2, 9)
+    torch.cuda.synchronize()
+
+
 def test_replayed_graph_follows_the_offsets():
     import torch
     from host_streamed_paged_gb300 import kvs
