@@ -660,21 +660,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 // query tiles, each read from tensor memory once, exponentiated against the
 // rows' lse and added up in a register.  Two warpgroups share the tile, half of
 // the columns each.  Two CTAs fit an SM, so that one's start, end and waits
-// pass under the other's exponentials, which bound this kernel (16 a clock and
-// SM: 1024 clocks for 128 x 128 scores, twice their MMAs at D = 128).  The
-// first keys of a prompt are seen by all its rows; so that such a unit does not
-// hold up the launch, a cluster shares it, every CTA a part of the query tiles,
-// and adds its sums up in rank order.
+// pass under the other's work.  What bounds it is a sum warp's chain (scores
+// from tensor memory, multiply-add, exponential, add): 1450 clocks of an SM for
+// 128 x 128 scores, of which the exponentials are 512 (32 a clock) and the MMAs
+// 530 at D = 128.  The first keys of a prompt are seen by all its rows; so that
+// such a unit does not hold up the launch, a cluster shares it, every CTA a
+// part of the query tiles, and adds its sums up in rank order.
 // At D = 256 a tile is 96 rows: K leaves the ring of two CTAs 36 KB, which are
 // two stages of 128 rows, and 64 rows pay the 50-clock MMA of N = 64 (52 us on
 // the window below, 46 with 96).  Its scores are summed over 128 dims each, in
 // two accumulators: the tensor core drops what lies below an accumulator's last
 // place at every 16 dims, always towards zero, and with 256 dims in a row the
 // weights came out 1.1e-6 low, 6.5e-7 like this (for 46 -> 50 us).
-// Prompts of 4096 .. 33 tokens, 32 / 8 heads, D 128, over all rows: 122 us
-// (66% of 16 exponentials a clock and SM; 143 us with two key tiles in one CTA of 16 sum
-// warps; with 2 to all of 16 exponentials as polynomials on the FMA pipes those
-// took 147 to 173).  The last 64 rows of 32768, 24 / 4 heads, D 256: 50 us.
+// Prompts of 4096 .. 33 tokens, 32 / 8 heads, D 128, over all rows: 114 us (121
+// with the causal edge's test among the columns of every tile, 143 with two key
+// tiles in one CTA of 16 sum warps, 147 to 173 of those with 2 to all of 16
+// exponentials as polynomials on the FMA pipes).  The last 64 rows of 32768, 24
+// / 4 heads, D 256: 39 us a call, 47 with a cold cache.
 constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA
 template <int D>
 struct WeightShape {
@@ -883,12 +885,13 @@ __global__ void __launch_bounds__(kWThreads, 2)
             const int c_lo = (key - tok0) * G - half * kCols;
             const int c_hi = ((L - tok0) * G < TQ * G ? (L - tok0) * G : TQ * G) - half * kCols;
             const uint32_t ts = lanes + (uint32_t)(buf * S::kParts * BQ + half * kCols);
+            const float2 sc2 = make_float2(sc, sc);
             uint32_t sr[2][16];  // 16 columns at a time: the next on their way, or both parts
-            tmem_ld16(ts, sr[0]);
-            if (S::kParts == 2) tmem_ld16(ts + BQ, sr[1]);
-#pragma unroll
-            for (int c0 = 0; c0 < kCols; c0 += 16) {
-                float s[16];
+            auto fetch = [&](int c0) {
+                tmem_ld16(ts + c0, sr[S::kParts == 2 ? 0 : c0 / 16 & 1]);
+                if (S::kParts == 2) tmem_ld16(ts + BQ + c0, sr[1]);
+            };
+            auto scores = [&](int c0, float *s) {  // those of 16 columns, with the next ones (or the buffer's release) on their way
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
@@ -898,28 +901,39 @@ __global__ void __launch_bounds__(kWThreads, 2)
                     s[c] = v.x, s[c + 1] = v.y;
                 }
                 if (c0 + 16 < kCols) {
-                    if (S::kParts == 2) {
-                        tmem_ld16(ts + c0 + 16, sr[0]);
-                        tmem_ld16(ts + BQ + c0 + 16, sr[1]);
-                    } else {
-                        tmem_ld16(ts + c0 + 16, sr[c0 / 16 + 1 & 1]);
-                    }
+                    fetch(c0 + 16);
                 } else {
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_read(buf));
                 }
-                const float2 sc2 = make_float2(sc, sc);
-                if (!edge) {
+            };
+            fetch(0);
+            if (!edge) {
+#pragma unroll
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    float s[16];
+                    float4 zc[4];  // (read before the wait for the scores where the registers allow)
+                    auto read = [&] {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) zc[c] = reinterpret_cast<const float4 *>(z + c0)[c];
+                    };
+                    if (S::kParts == 1) read();
+                    scores(c0, s);
+                    if (S::kParts == 2) read();
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
-                        const float4 zc = reinterpret_cast<const float4 *>(z + c0)[c / 4];
-                        const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(zc.x, zc.y));
-                        const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(zc.z, zc.w));
+                        const float2 a = fma2(make_float2(s[c], s[c + 1]), sc2, make_float2(zc[c / 4].x, zc[c / 4].y));
+                        const float2 b = fma2(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(zc[c / 4].z, zc[c / 4].w));
                         sum[0] = add2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
                         sum[1] = add2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
                     }
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    float s[16];
+                    scores(c0, s);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const float e = ex2(fmaf(s[c], sc, z[c0 + c]));
