@@ -683,7 +683,9 @@ struct Query {
             int e = (int)(__float_as_uint(top) >> 23) - 127;
             e = e < -100 ? -100 : (e > 100 ? 100 : e);
             const float f = valid ? copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2) : 0.f;
-            fac[n] = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + (kBias ? 24 : 0) - 14 + e) << 23);
+            // never 0, so that a masked score stays -inf times it (what a scale of 0, or one that vanishes here, takes
+            // to 2^-126 instead is below 2^-80)
+            fac[n] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + (kBias ? 24 : 0) - 14 + e) << 23), 1.17549435e-38f);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float sum = 0.f, x[8];

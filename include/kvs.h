@@ -849,7 +849,8 @@ kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n
  * numbers in order; lens: device int32 [n_seq], cached tokens T including the
  * rows' own.  q: device [n_seq][n_rows][n_q_head][D] (KVS_F32, KVS_F16 or
  * KVS_BF16), rows q_stride elements apart; row r sees tokens 0 .. T - n_rows +
- * r.  out: device, contiguous, in the type of q; lse (nullable): device fp32
+ * r.  Any finite scale is taken (at 0 every seen token weighs the same).  out:
+ * device, contiguous, in the type of q; lse (nullable): device fp32
  * [n_seq][n_rows][n_q_head].  A row that sees nothing (T = 0: a padding
  * sequence) gets out 0 and lse -inf.  A page number outside the pool within
  * T makes the sequence's outputs NaN.  T is clamped to table_width * P.
