@@ -1623,7 +1623,7 @@ kvs_status fill_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t t
 
 template <typename P, typename... A>
 cudaError_t launch(void (*kernel)(P, A...), dim3 grid, int threads, int smem, cudaStream_t s, bool pdl, const P &p, A... a) {
-    if (smem > 48 * 1024) {
+    if (smem > 0) {  // (whatever the size: the 48 KB that need no opt-in are of dynamic and static bytes together)
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
         if (e != cudaSuccess) return e;
     }
