@@ -347,6 +347,7 @@ kvs_status bad(kvs_status s, const char *why) {
     return s;
 }
 kvs_status cuda_failed(const char *what, cudaError_t e) {
+    cudaGetLastError();  // the call's own: no later one is to find it
     set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
     return KVS_ERR_CUDA;
 }
@@ -428,7 +429,10 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     const uint64_t tiles = sh * ((keep + 31) / 32);
     if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
     void (*g)(EvictParams) = D == 64 ? gather_kernel<64> : D == 128 ? gather_kernel<128> : gather_kernel<256>;
-    g<<<(unsigned)((tiles + 3) / 4), 128, 0, st>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t gather = {};
+    gather.gridDim = dim3((unsigned)((tiles + 3) / 4));
+    gather.blockDim = dim3(128);
+    gather.stream = st;
+    e = cudaLaunchKernelEx(&gather, g, p);
     return e == cudaSuccess ? KVS_OK : cuda_failed("evict launch", e);
 }

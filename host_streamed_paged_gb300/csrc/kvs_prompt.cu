@@ -975,6 +975,7 @@ kvs_status bad(kvs_status s, const char *why) {
     return s;
 }
 kvs_status cuda_failed(const char *what, cudaError_t e) {
+    cudaGetLastError();  // the call's own: no later one is to find it
     set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
     return KVS_ERR_CUDA;
 }
@@ -1047,8 +1048,12 @@ template <typename... A>
 cudaError_t launch(void (*kernel)(A...), dim3 grid, int smem, cudaStream_t s, const A &...a) {
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, s>>>(a...);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
 template <int D>

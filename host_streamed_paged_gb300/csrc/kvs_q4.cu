@@ -1528,6 +1528,7 @@ kvs_status bad(kvs_status s, const char *why) {
     return s;
 }
 kvs_status cuda_failed(const char *what, cudaError_t e) {
+    cudaGetLastError();  // the call's own: no later one is to find it
     set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
     return KVS_ERR_CUDA;
 }
