@@ -406,6 +406,8 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     int ranks = 1;
     while (ranks < 8 && (uint64_t)ranks * 4096 < most) ranks *= 2;
     if (sh * ranks > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head too large");
+    const uint64_t tiles = sh * ((keep + 31) / 32);
+    if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "n_seq * n_kv_head * keep too large");
     const uint64_t share = (most + ranks - 1) / ranks;
     const bool kept_keys = share <= (uint64_t)kShare;
     auto select = kept_keys ? select_kernel<true> : select_kernel<false>;
@@ -426,8 +428,6 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, select, p);
     if (e != cudaSuccess) return cuda_failed("evict launch", e);
-    const uint64_t tiles = sh * ((keep + 31) / 32);
-    if ((tiles + 3) / 4 > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
     void (*g)(EvictParams) = D == 64 ? gather_kernel<64> : D == 128 ? gather_kernel<128> : gather_kernel<256>;
     cudaLaunchConfig_t gather = {};
     gather.gridDim = dim3((unsigned)((tiles + 3) / 4));
