@@ -718,6 +718,7 @@ class KVStream:
 
 _torch = None
 _DTYPES = {}
+_MOST = 2 ** 31 - 1  # of the library's 32-bit counts
 
 
 def _t():
@@ -836,6 +837,8 @@ def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=No
     lse is prompt_attend's; window > 0 counts only each prompt's last window rows; prev (same shape) is added, and
     may be out.
     """
+    if window < 0:
+        raise ValueError("window must not be negative")
     p = _prompt(q, k, None, cu, scale)
     f32, dev = _torch.float32, q.device
     _need(lse, "lse", f32, dev, q.shape[:2])
@@ -846,7 +849,7 @@ def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=No
         out = _torch.empty(shape, dtype=f32, device=dev)
     else:
         _need(out, "out", f32, dev, shape)
-    _run(dev, load().kvs_prompt_weights, ctypes.byref(p), lse.data_ptr(), int(window),
+    _run(dev, load().kvs_prompt_weights, ctypes.byref(p), lse.data_ptr(), min(int(window), _MOST),
          prev.data_ptr() if prev is not None else None, out.data_ptr(), shape[2])
     return out
 
@@ -970,6 +973,9 @@ class Q4Cache:
         dev, i32, hk = self.device, _torch.int32, self.n_kv_head
         f32 = _torch.float32
         _need_rows(weights, "weights", f32, dev, None, 3)
+        for name, x in (("keep", keep), ("sinks", sinks), ("recent", recent)):  # (ctypes takes any, modulo 2^32)
+            if not 0 <= x <= _MOST:
+                raise ValueError(f"{name} must be 0 .. 2^31 - 1")
         n, heads, width = weights.shape
         if heads != hk:
             raise ValueError("weights must be [n_seq][n_kv_head][width]")

@@ -9,3 +9,37 @@ def test_evict_refuses_too_many_tiles_before_any_launch():
     """2^26 tiles of each of 129 (sequence, head) pairs: more CTAs than a launch may have."""
     keep = 0x7fffffc0
     assert status(evict, pool(n_kv_head=1, page_tokens=32), n_seq=129, keep=keep, dst_width=1 << 26) == kvs.KVS_ERR_UNSUPPORTED
+
+
+def _rows(*shape):
+    import torch
+    return torch.zeros(*shape, dtype=torch.float16)
+
+
+@pytest.mark.parametrize("window", [-1, -(1 << 32) + 5])
+def test_a_negative_window_is_refused(window):
+    """(It would reach the library as its value modulo 2^32: every row, or five of them.)"""
+    import torch
+    q, k, cu = _rows(10, 4, 64), _rows(10, 2, 64), torch.tensor([0, 10], dtype=torch.int32)
+    with pytest.raises(ValueError, match="window"):
+        kvs.prompt_weights(q, k, torch.zeros(10, 4), cu, 10, window=window)
+
+
+def test_a_window_beyond_31_bits_is_every_row(monkeypatch):
+    import torch
+    q, k, cu = _rows(10, 4, 64), _rows(10, 2, 64), torch.tensor([0, 10], dtype=torch.int32)
+    seen = []
+    monkeypatch.setattr(kvs, "_run", lambda dev, fn, *a: seen.append(a))
+    for window in (7, (1 << 32) + 5):
+        kvs.prompt_weights(q, k, torch.zeros(10, 4), cu, 10, window=window)
+    assert [a[2] for a in seen] == [7, (1 << 31) - 1]
+
+
+@pytest.mark.parametrize("kw", [dict(keep=-1), dict(sinks=-1), dict(recent=-1), dict(sinks=(1 << 32) + 2), dict(recent=1 << 32),
+                                dict(keep=(1 << 32) + 8)])
+def test_evict_counts_out_of_range_are_refused(kw):
+    import torch
+    c = kvs.Q4Cache(page_tokens=32, n_kv_head=2, head_dim=64, n_pages=2, device="cpu")
+    table, lens = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        c.evict(table, table, lens, torch.zeros(1, 2, 32), **dict(dict(keep=16), **kw))
