@@ -746,10 +746,10 @@ def _row_stride(t, what):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     if len(shape) == 4:
         if shape[1] == 1:
-            return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+            return stride[0] if shape[0] > 1 else heads * d
         if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
             raise ValueError(f"{what}: rows must lie at one stride")
-    return stride[-3] if shape[-3] > 1 else max(stride[-3], heads * d)
+    return stride[-3] if shape[-3] > 1 else heads * d
 
 
 def _need(t, name, dtype, device, shape):

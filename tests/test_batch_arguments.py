@@ -43,3 +43,15 @@ def test_evict_counts_out_of_range_are_refused(kw):
     table, lens = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match=next(iter(kw))):
         c.evict(table, table, lens, torch.zeros(1, 2, 32), **dict(dict(keep=16), **kw))
+
+
+def test_one_row_has_no_stride():
+    """A row alone may be cut from rows that lie any number of elements apart."""
+    import torch
+    wide = torch.zeros(3, 4 * 64 + 3, dtype=torch.float16)
+    one = wide[:, :256].unflatten(1, (4, 64))[:1]
+    assert one.stride(0) == 259 and kvs._row_stride(one, "x") == 256
+    assert kvs._row_stride(one[None], "x") == 256 and kvs._row_stride(one[:, None], "x") == 256
+    assert kvs._row_stride(wide[:, :256].unflatten(1, (4, 64)), "x") == 259  # which the library then refuses
+    assert kvs._row_stride(torch.zeros(5, 2, 4, 64)[:1], "x") == 256 and kvs._row_stride(torch.zeros(5, 2, 4, 64)[:, :1], "x") == 512
+    assert kvs._row_stride(torch.zeros(0, 4, 64), "x") == 256 and kvs._row_stride(torch.zeros(0, 3, 4, 64), "x") == 256
