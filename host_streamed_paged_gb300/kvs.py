@@ -935,12 +935,18 @@ class Q4Cache:
         """attend's workspace: one per stream and thread, whose calls run in order (another thread's may come between the
         two launches of one); a call being captured gets one of its own from the graph's memory, since graphs of one
         stream may be replayed side by side."""
-        if _torch.cuda.is_current_stream_capturing():
-            return _torch.empty(need, dtype=_torch.uint8, device=self.device)
-        stream = (_stream_of(self.device.index) if self.device.type == "cuda" else 0, _get_ident())
+        cuda, dev = _torch.cuda, self.device
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if cuda.current_device() != dev.index:  # a capture is one of the device that the call runs on
+            with cuda.device(dev):
+                return self._workspace(need)
+        if cuda.is_current_stream_capturing():
+            return _torch.empty(need, dtype=_torch.uint8, device=dev)
+        stream = (_stream_of(dev.index), _get_ident())
         ws = self._spaces.get(stream)
         if ws is None or ws.numel() < need:
-            ws = self._spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=self.device)
+            ws = self._spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=dev)
         return ws
 
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):

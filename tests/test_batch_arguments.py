@@ -55,3 +55,36 @@ def test_one_row_has_no_stride():
     assert kvs._row_stride(wide[:, :256].unflatten(1, (4, 64)), "x") == 259  # which the library then refuses
     assert kvs._row_stride(torch.zeros(5, 2, 4, 64)[:1], "x") == 256 and kvs._row_stride(torch.zeros(5, 2, 4, 64)[:, :1], "x") == 512
     assert kvs._row_stride(torch.zeros(0, 4, 64), "x") == 256 and kvs._row_stride(torch.zeros(0, 3, 4, 64), "x") == 256
+
+
+def test_a_capture_is_looked_for_on_the_caches_device(monkeypatch):
+    """Whether a call is being captured is asked of the current stream of the device that it runs on."""
+    import torch
+
+    class Device:
+        type, index = "cuda", 1
+
+    class On:
+        def __init__(self, d):
+            self.d = d.index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.d
+
+        def __exit__(self, *a):
+            now[0] = self.was
+
+    now, capturing, made = [0], {0: False, 1: True}, []
+    c = kvs.Q4Cache(page_tokens=32, n_kv_head=2, head_dim=64, n_pages=2, device="cpu")
+    c.device = Device()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[now[0]])
+    monkeypatch.setattr(kvs, "_stream_of", lambda index: 7)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: made.append(n) or empty(n, dtype=dtype))
+    assert c._workspace(512) is not c._workspace(512) and made == [512, 512]  # captured: one each
+    capturing.update({0: True, 1: False})
+    assert c._workspace(512) is c._workspace(512) and made == [512, 512, 512]
+    now[0] = 1
+    assert c._workspace(512) is c._workspace(512) and made == [512, 512, 512]
