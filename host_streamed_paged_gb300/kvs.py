@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from threading import get_ident as _get_ident
+from threading import local as _thread_local
 
 import numpy as np
 
@@ -877,7 +877,7 @@ class Q4Cache:
         self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
         self._ref, self._lib = ctypes.byref(pool), load()
         self._need_bytes = {}  # by (rows, heads, dtype)
-        self._spaces = {}      # workspaces by stream and thread
+        self._spaces = _thread_local()  # of each thread, workspaces by stream: they go with the thread
 
     def append(self, slots, k, v):
         """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
@@ -943,10 +943,10 @@ class Q4Cache:
                 return self._workspace(need)
         if cuda.is_current_stream_capturing():
             return _torch.empty(need, dtype=_torch.uint8, device=dev)
-        stream = (_stream_of(dev.index), _get_ident())
-        ws = self._spaces.get(stream)
+        spaces, stream = self._spaces.__dict__, _stream_of(dev.index)
+        ws = spaces.get(stream)
         if ws is None or ws.numel() < need:
-            ws = self._spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=dev)
+            ws = spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=dev)
         return ws
 
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
