@@ -208,6 +208,10 @@ cudaError_t launch_fill(const FillParams &p, cudaStream_t s, bool pdl = false);
 int current_device_sms();
 cudaError_t ensure_smem_limit(const void *kernel, int bytes);
 
+// Whether this call of a batch operator is the one that kvs_debug_inject(NULL,
+// KVS_FAULT_DEVICE_WAIT, nth) armed on this thread (counts the call).
+bool batch_wait_fault();
+
 // Message returned by kvs_last_error(NULL) on this thread.
 void set_thread_error(const std::string &msg);
 

@@ -490,6 +490,7 @@ struct AttendParams {
     int table_width, n_seq, R, Hq, G;
     int dtype, row_blocks, workers;
     float scale_log2;
+    int give_up;  // test hook: a worker's first wait gives up at once, as if its copy never landed
 };
 
 __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, int table_width, int s) {
@@ -858,11 +859,8 @@ struct Stages {
                 : "memory");
         }
     }
-    // the stage's tile, or false: bad page, or the copy never landed
-    __device__ __forceinline__ bool wait(int stage, uint32_t &phases) {
-        if (gave_up || (bad >> stage & 1)) return false;
-        const uint32_t parity = phases >> stage & 1;
-        phases ^= 1u << stage;
+    // whether the copy into a stage that completes the phase of this parity lands in time
+    __device__ __forceinline__ bool landed(int stage, uint32_t parity) const {
         uint32_t done = 0;
         if ((threadIdx.x & 31) == 0)  // one lane polls: a poll by 32 lanes holds the warp for 200 clocks
             for (uint32_t i = 0; i < kWaitLimit && !done; ++i)
@@ -871,8 +869,29 @@ struct Stages {
                     : "=r"(done)
                     : "r"(bar0 + 8 * stage), "r"(parity)
                     : "memory");
-        gave_up = __shfl_sync(0xffffffffu, done, 0) == 0;
+        done = __shfl_sync(0xffffffffu, done, 0);
+        __syncwarp();  // what lane 0 saw complete, the others may read
+        return done != 0;
+    }
+    // the stage's tile, or false: bad page, or the copy never landed.  phases: per stage the parity of its next wait.
+    __device__ __forceinline__ bool wait(int stage, uint32_t &phases) {
+        if (gave_up || (bad >> stage & 1)) return false;
+        const uint32_t parity = phases >> stage & 1;
+        phases ^= 1u << stage;
+        gave_up = !landed(stage, parity);
         return !gave_up;
+    }
+    // what a wait on `stage` that gives up leaves (test hook)
+    __device__ __forceinline__ void give_up(int stage, uint32_t &phases) {
+        phases ^= 1u << stage;
+        gave_up = true;
+    }
+    // After the wait on stage `first` gave up: its copy and those of the stages after it, n in all, were begun and not seen
+    // to land; they still write this CTA's shared memory.  Each gets the whole time again, whatever became of the one before.
+    __device__ __forceinline__ void drain(int first, int n, uint32_t phases) const {
+        phases ^= 1u << first;  // (turned by the wait that gave up)
+        for (int i = 0, s = first; i < n; ++i, s = s + 1 == NST ? 0 : s + 1)
+            if (!(bad >> s & 1)) landed(s, phases >> s & 1);
     }
 };
 
@@ -989,8 +1008,9 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
     bool fresh = true;
     int k_first = 0, len = 0;
     ScaleBound bound;
-    int stage = 0;
-    for (int unit = 0; unit < units; ++unit) {
+    int stage = 0, unit = 0;
+    if (p.give_up) st.give_up(stage, phases);
+    for (; unit < units; ++unit) {
         if (fresh) {  // a new (sequence, head)
             typename Query<D, NT, HL>::Raw raw;
             raw.load(p, at.s, at.h, rho0);  // the tiles' copies are under way
@@ -1245,12 +1265,13 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
         at.next(prefix, p.n_seq, p.pool.Hk);
     }
     if (st.gave_up) {  // what this worker owed is NaN: partials and whole rows of its range
+        st.drain(stage, fetched - unit, phases);
         for (int i = lane; i < 2 * 8 * NT; i += 32)
             p.part_rl[((int64_t)rb * p.workers + w) * 2 * (8 * NT) + i] = make_float2(0.f, __int_as_float(0x7fc00000));  // (the sum: NaN)
         Cursor c;
         c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
-        for (int unit = 0; unit < units; ++unit) {
-            if (c.k == 0 && unit + c.T <= units)
+        for (int x = 0; x < units; ++x) {
+            if (c.k == 0 && x + c.T <= units)
                 for (int rho = rho0; rho < rho0 + 8 * NT && rho < p.R * p.G; ++rho) {
                     const int64_t row = ((int64_t)c.s * p.R + rho / p.G) * p.Hq + c.h * p.G + rho % p.G;
                     for (int d = lane; d < D; d += 32) put(p.out, p.dtype, row * D + d, __int_as_float(0x7fc00000));
@@ -1258,9 +1279,6 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
                 }
             c.next(prefix, p.n_seq, p.pool.Hk);
         }
-        // copies still in flight land in this CTA's shared memory: give them the same time again
-        st.gave_up = false;
-        for (int i = 0; i < NST; ++i) st.wait(i, phases);
     }
 }
 
@@ -1436,16 +1454,17 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             if (fetched < units) {
-                if (!st.gave_up) st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
+                st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
                 ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
                 ++fetched;
             }
         }
         bool fresh = true;
-        int stage = 0;
+        int stage = 0, unit = 0;
+        if (p.give_up) st.give_up(stage, phases);
         float2 lse2[NT], fac[NT];  // rows 2t, 2t + 1
         int len = 0;
-        for (int unit = 0; unit < units; ++unit) {
+        for (; unit < units; ++unit) {
             if (fresh) {
                 typename Query<D, NT, HL>::Raw raw;
                 raw.load(p, at.s, at.h, rho0);
@@ -1469,6 +1488,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
             if (!st.wait(stage, phases)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[i] = __int_as_float(0x7fc00000);
+                if (st.gave_up) break;
             } else {
                 float acc[2][NT][4];
 #pragma unroll
@@ -1506,7 +1526,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
             }
             __syncwarp();
             if (fetched < units) {
-                if (!st.gave_up) st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
+                st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
                 ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
                 ++fetched;
             }
@@ -1514,10 +1534,18 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
             stage = stage + 1 == NST ? 0 : stage + 1;
             at.next(prefix, p.n_seq, p.pool.Hk);
         }
-    }
-    if (st.gave_up) {  // copies still in flight land in this CTA's shared memory: give them the same time again
-        st.gave_up = false;
-        for (int i = 0; i < NST; ++i) st.wait(i, phases);
+        if (st.gave_up) {  // every token of this worker's range is NaN, the entries past a sequence's length are prev's
+            st.drain(stage, fetched - unit, phases);
+            Cursor c;
+            c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+            for (int x = 0; x < units; ++x) {
+                const int64_t pos = (int64_t)c.k * kTile + lane, o = ((int64_t)c.s * p.pool.Hk + c.h) * wp.width + pos;
+                if (pos < wp.width)
+                    wp.w[o] = pos < seq_len(p.pool, p.lens, p.table_width, c.s) ? __int_as_float(0x7fc00000) : wp.prev ? wp.prev[o] : 0.f;
+                c.next(prefix, p.n_seq, p.pool.Hk);
+            }
+            return;
+        }
     }
 }
 
@@ -1733,6 +1761,7 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     if (workspace_bytes < need) return bad(KVS_ERR_CAPACITY, "workspace smaller than kvs_q4_query_sizes asks for");
     const int sms = current_device_sms();
     const Shape sh = shape_of(D, n_rows * p.G, dtype, sms < kSmsAssumed ? sms : kSmsAssumed);
+    p.give_up = batch_wait_fault();
     p.out = out;
     p.lse = lse;
     p.row_blocks = sh.row_blocks;
@@ -1766,6 +1795,7 @@ extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *tab
     if (n_seq && width && (!lse || !weights)) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (n_seq == 0 || width == 0) return KVS_OK;
+    p.a.give_up = batch_wait_fault();
     const uint32_t D = pool->head_dim, rows = n_rows * p.a.G;
     const bool hl = dtype == KVS_F32;
     // up to 16 or (16-bit queries) 32 rows a pass: the fewer passes, the fewer times a tile is read; the passes as even as

@@ -803,6 +803,9 @@ void sizes_of(const kvs_config *cfg, uint64_t *page_bytes, uint64_t *host_bytes,
 
 namespace kvs {
 void set_thread_error(const std::string &msg) { g_create_error = msg; }
+
+static thread_local uint64_t g_batch_fault = 0;  // batch calls until the armed one
+bool batch_wait_fault() { return g_batch_fault && --g_batch_fault == 0; }
 }  // namespace kvs
 
 // ======================================================================= C ABI
@@ -2193,7 +2196,14 @@ kvs_status kvs_graph_destroy(kvs_ctx *c) {
 
 
 kvs_status kvs_debug_inject(kvs_ctx *c, uint32_t fault, uint64_t nth) {
-    if (!c) return KVS_ERR_INVALID;
+    if (!c) {
+        if (fault != KVS_FAULT_NONE && fault != KVS_FAULT_DEVICE_WAIT) {
+            kvs::set_thread_error("without a context only KVS_FAULT_DEVICE_WAIT can be armed");
+            return KVS_ERR_INVALID;
+        }
+        kvs::g_batch_fault = fault == KVS_FAULT_NONE ? 0 : nth;
+        return KVS_OK;
+    }
     if (fault > KVS_FAULT_DEVICE_WAIT) return fail(c, KVS_ERR_INVALID, "unknown fault kind");
     c->fault = nth ? fault : (uint32_t)KVS_FAULT_NONE;
     c->fault_nth = nth;
