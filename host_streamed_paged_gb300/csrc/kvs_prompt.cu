@@ -865,9 +865,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
             src[x] = p.lse_in + (int64_t)(begin + start + rank * TQ + q / G) * Hq + head * G + q % G;
             next[x] = t_of[x] < TQ && start + rank * TQ + t_of[x] < L ? *src[x] : INFINITY;
         }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // Two levels: a tile's terms, then the tiles.  (In one chain, thousands of terms of a long prompt's first keys lost
+        // up to 1e-4 of their sum.)
+        float2 total = make_float2(0.f, 0.f);
         bool ok = true;
         for (int r = 0; r < ntile; ++r) {
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const int buf = r % S::kBufs, tok0 = start + (rank + r * ranks) * TQ;
             float *z = sl + (r & 1) * kCols;
 #pragma unroll
@@ -942,9 +945,9 @@ __global__ void __launch_bounds__(kWThreads, 2)
                     }
                 }
             }
+            total = add2(total, add2(sum[0], sum[1]));
         }
-        const float2 t2 = add2(sum[0], sum[1]);
-        mine = ok ? t2.x + t2.y : __int_as_float(0x7fc00000);
+        mine = ok ? total.x + total.y : __int_as_float(0x7fc00000);
     }
     // every MMA is done, every score read: the sums of a key meet in shared memory, then over the cluster
     if (tid == 0) mbar_drain(b_final, 0);
