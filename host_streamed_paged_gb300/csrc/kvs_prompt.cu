@@ -36,8 +36,8 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
 // bounded wait for phase `parity`; false on timeout or once *abort is raised (a timeout raises it)
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit) {
-    for (uint32_t i = 0; i < limit; ++i) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -61,21 +61,21 @@ __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
 // the same on its own: whatever has been given up elsewhere, the whole time is waited
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     volatile int none = 0;
-    mbar_wait(bar, parity, &none, kSpinLimit);
+    mbar_wait(bar, parity, &none);
 }
 // a warp's bounded wait until ready() holds in every lane.  A poll's answer takes some 150 clocks even when the
 // phase is complete, so several barriers are polled in one ready(), one after the other without waiting in between.
 template <typename F>
-__device__ __forceinline__ bool wait_warp(volatile int *abort, uint32_t limit, F ready) {
-    for (uint32_t i = 0; i < limit; ++i) {
+__device__ __forceinline__ bool wait_warp(volatile int *abort, F ready) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
         if (__all_sync(0xffffffffu, ready())) return true;
         if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort)) return false;
     }
     *abort = 1;
     return false;
 }
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit) {
-    return wait_warp(abort, limit, [&] { return mbar_done(bar, parity); });
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return wait_warp(abort, [&] { return mbar_done(bar, parity); });
 }
 // true in one lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -209,7 +209,7 @@ struct PromptParams {
     int64_t width;
     int last_rows;
     int main_ctas;  // those past them copy what no key writes
-    uint32_t spin_limit;  // polls of a wait (0: every one gives up at once, for tests; drains keep theirs)
+    int give_up;    // test hook: every role gives up at its first wait, as if its copy never landed
 };
 
 __device__ __forceinline__ int cu_begin(const PromptParams &p, int s) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(b_p(0, i), 4);
             mbar_init(b_o(0, i), 1);
         }
-        *abort = 0;
+        *abort = p.give_up;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_before();
@@ -442,15 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
             int issued = 0;
             for (int r = 0; r < n_ring; ++r) {
-                if (r >= NST && !mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort, p.spin_limit)) break;
+                if (r >= NST && !mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort)) break;
                 load_piece(r);
                 issued = r + 1;
             }
-            // Every copy has landed before the CTA ends, also those that a role which gave up, then or later, did not
-            // wait for: they write this CTA's shared memory.  (Otherwise the MMAs have waited for them.)
-            mbar_drain(b_q, 0);
-            for (int st = 0; st < NST; ++st)
-                if (issued > st) mbar_drain(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1));
+            place[5] = issued;
         }
     } else if (warp == 8 || (NQ == 2 && warp == 10)) {
         const int i = (warp - 8) >> 1, n = nblk[i];
@@ -497,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(b_o(i, j & 1));
         };
         // a block past this tile's last one is freed as it comes, for the other tile's sake
-        bool ok = true;
+        bool ok = !p.give_up;
         for (int j = 0; j < 2 && j < n_max && ok; ++j) {
-            ok = wait_warp(abort, p.spin_limit, [&] { return mbar_done(b_q, 0) & loaded(ring_k(j)); });
+            ok = wait_warp(abort, [&] { return mbar_done(b_q, 0) & loaded(ring_k(j)); });
             if (!ok) break;
             tc_after();
             if (one) {
@@ -510,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
         for (int j = 0; j < n_max && ok; ++j) {
             const bool more = j + 2 < n_max;
-            ok = wait_warp(abort, p.spin_limit, [&] {
+            ok = wait_warp(abort, [&] {
                 bool all = loaded(ring_v(j));
                 if (j < n) all &= mbar_done(b_p(i, j & 1), (uint32_t)((j >> 1) & 1));
                 if (more) all &= loaded(ring_k(j + 2));
@@ -535,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sc = p.scale_log2;
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
-        bool ok = true;
+        bool ok = !p.give_up;
         const int first_tok = t0 + i * TQ;
-        for (int j = 0; j < n; ++j) {
+        for (int j = ok ? 0 : n; j < n; ++j) {
             const int buf = j & 1;
-            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((j >> 1) & 1), abort, p.spin_limit);
+            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((j >> 1) & 1), abort);
             if (!ok) break;
             tc_after();
             const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
@@ -565,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l2.y *= alpha;
                 m = to;
                 if (j > 0) {
-                    ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort, p.spin_limit);
+                    ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
                     if (!ok) break;
                     tc_after();
                     const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
@@ -602,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < S::kPieces; ++c) {
                     const int r = ring_v(j) + c, st = r % NST;
-                    ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort, p.spin_limit);
+                    ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
                     if (ok && row < S::kVKeys && j * BN + c * S::kVKeys + row >= L) {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
@@ -620,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(b_p(i, buf));
         }
-        if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), abort, p.spin_limit);
+        if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), abort);
         if (n > 0) {
             tc_after();
             const float l = l2.x + l2.y;
@@ -655,6 +651,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
+    // Every role is done.  If one gave up, copies that no one waited for may still be under way into this CTA's shared
+    // memory, which is its own while this lane stays.  (Otherwise the MMAs have waited for all of them.)
+    if (tid == 9 * 32 && *abort) {
+        const int issued = place[5];
+        mbar_drain(b_q, 0);
+        for (int st = 0; st < NST; ++st)
+            if (issued > st) mbar_drain(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1));
+    }
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
             mbar_init(b_s(b), 1);
             mbar_init(b_read(b), 8);
         }
-        *abort = 0;
+        *abort = p.give_up;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // query-tile rows that no box writes (BQ not a multiple of G) stay zero: their scores are finite
@@ -799,27 +803,25 @@ __global__ void __launch_bounds__(kWThreads, 2)
             int issued = 0;
             for (int r = 0; r < ntile * S::kChunks; ++r) {
                 const int st = r % NST, use = r / NST;
-                if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort, p.spin_limit)) break;
+                if (use > 0 && !mbar_wait(b_empty(st), (uint32_t)((use - 1) & 1), abort)) break;
                 mbar_expect(b_full(st), (uint32_t)(128 * G * TQ));
                 tma_load(smem_u32(smem + S::kOffRing + st * S::kChunk), &mq, b_full(st), r % S::kChunks * 64, head * G,
                          begin + start + (rank + r / S::kChunks * ranks) * TQ);
                 issued = r + 1;
             }
-            mbar_drain(b_k, 0);  // every copy has landed before the CTA ends (as in the attention)
-            for (int st = 0; st < NST; ++st)
-                if (issued > st) mbar_drain(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1));
+            place[5] = issued;
         }
     } else if (warp == 8) {
         constexpr uint32_t id = idesc(BF16, kTileRows, BQ, false);
         constexpr int kPer = S::kChunks / S::kParts;
         const bool one = elect_one();
         const uint64_t da = smem_desc(smem_u32(smem), 16), dq = smem_desc(smem_u32(smem + S::kOffRing), 16);
-        bool ok = mbar_wait_warp(b_k, 0, abort, p.spin_limit);
+        bool ok = !p.give_up && mbar_wait_warp(b_k, 0, abort);
         for (int r = 0; r < ntile && ok; ++r) {
             const int buf = r % S::kBufs;
 #pragma unroll
             for (int c0 = 0; c0 < S::kChunks; c0 += S::kStep) {
-                ok = ok && wait_warp(abort, p.spin_limit, [&] {
+                ok = ok && wait_warp(abort, [&] {
                     bool all = true;
 #pragma unroll
                     for (int c = c0; c < c0 + S::kStep; ++c) {
@@ -868,8 +870,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
         // Two levels: a tile's terms, then the tiles.  (In one chain, thousands of terms of a long prompt's first keys lost
         // up to 1e-4 of their sum.)
         float2 total = make_float2(0.f, 0.f);
-        bool ok = true;
-        for (int r = 0; r < ntile; ++r) {
+        bool ok = !p.give_up;
+        for (int r = ok ? 0 : ntile; r < ntile; ++r) {
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const int buf = r % S::kBufs, tok0 = start + (rank + r * ranks) * TQ;
             float *z = sl + (r & 1) * kCols;
@@ -881,7 +883,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
                 next[x] = t_of[x] < TQ && r + 1 < ntile && tok0 + ranks * TQ + t_of[x] < L ? *src[x] : INFINITY;
             }
             __syncwarp();
-            ok = mbar_wait_warp(b_s(buf), (uint32_t)((r / S::kBufs) & 1), abort, p.spin_limit);
+            ok = mbar_wait_warp(b_s(buf), (uint32_t)((r / S::kBufs) & 1), abort);
             if (!ok) break;
             tc_after();
             // columns this key counts: rows of tokens from the key on, and none past the prompt
@@ -954,6 +956,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
     tc_before();
     __syncthreads();
     tc_after();
+    if (tid == 9 * 32 && *abort) {  // copies that no one waited for (as in the attention)
+        const int issued = place[5];
+        mbar_drain(b_k, 0);
+        for (int st = 0; st < NST; ++st)
+            if (issued > st) mbar_drain(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1));
+    }
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
     if (warp < 8) fin[tid] = mine;
     if (ranks > 1) cl.sync();
@@ -1042,7 +1050,6 @@ kvs_status check_prompt(const kvs_prompt *p, bool need_v, PromptParams *o) {
     o->Hk = (int)p->n_kv_head;
     o->G = (int)(p->n_q_head / p->n_kv_head);
     o->scale_log2 = p->scale * 1.4426950408889634f;
-    o->spin_limit = kSpinLimit;
     return KVS_OK;
 }
 
@@ -1146,7 +1153,7 @@ extern "C" kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t
     if (p->total_rows && (!out || !aligned(out, 16) || out_stride % 8 || out_stride < (uint64_t)p->n_q_head * p->head_dim))
         return bad(KVS_ERR_INVALID, "out rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
     if (p->total_rows == 0 || p->n_seq == 0) return KVS_OK;
-    if (batch_wait_fault()) pp.spin_limit = 0;
+    pp.give_up = batch_wait_fault();
     pp.out = out;
     pp.out_stride = (int64_t)out_stride;
     pp.lse = lse;
@@ -1162,7 +1169,7 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
     if (p->n_seq && width && ((p->total_rows && !lse) || !weights)) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (p->n_seq == 0 || width == 0) return KVS_OK;
-    if (batch_wait_fault()) pp.spin_limit = 0;
+    pp.give_up = batch_wait_fault();
     pp.lse_in = lse;
     pp.prev = prev;
     pp.w = weights;
