@@ -529,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = row < TQ * G && tok < L;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale_log2;
+        // P is 2^(s - m + kUp), at most 2^(8 + kUp): as high as f16 reaches, so that its smallest step is 2^-31 of the largest
+        // weight or less (2^-24 without, and thousands of keys below it are lost from the output); bf16 has the exponents
+        constexpr float kUp = BF16 ? 0.f : 7.f;
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = !p.give_up;
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const float neg = m == -INFINITY ? 0.f : -m;
+            const float neg = m == -INFINITY ? 0.f : kUp - m;
             const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -643,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (valid && p.lse) p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l)) * 0.693147180559945309f : inv;
+            if (valid && p.lse)
+                p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l * (BF16 ? 1.f : 0.0078125f))) * 0.693147180559945309f : inv;
         }
     }
     // tensor memory is freed once every MMA is done and every row was read
