@@ -4,6 +4,9 @@ import math
 import numpy as np
 import pytest
 
+import batch_ref as ref
+from test_gpu_q4 import Filled
+
 pytestmark = pytest.mark.gpu
 
 
@@ -48,3 +51,28 @@ def test_many_small_prompt_weights_reach_the_output(D):
     # keys (128 at D 256); each is off by at most half a step, 2^-24 of a sum that the small weights never double, and all
     # blocks may be off to the same side
     assert np.abs(lse[:, 0].double().cpu().numpy() - np.log(total[:, 0])).max() <= 1e-6 + math.ceil(L / 64) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("D,Hk,G,R", [(64, 1, 4, 1), (128, 2, 4, 1), (128, 1, 8, 2), (256, 1, 6, 1)])
+def test_fp32_attention_keeps_fp32(D, Hk, G, R):
+    """Norm-wise.  An output is sum p v over tokens whose errors are independent, so ||err|| / ||out|| is the root mean
+    square of the weights' relative errors.  Those of an fp32 call, for unit-normal rows and queries of 1.5:
+      scores: a query is f16 hi + lo, cut 2^-22 of the row's largest element (4.5) and, uniform in it, 2^-24 on
+        average; over sqrt(D) products of 1 and a scale of 1 / sqrt(D): 3e-7; fp32 block sums of up to 4 sqrt(D)
+        (2^-24 of them, 1 / sqrt(D)): 2e-7;
+      exponent: half a step of an argument below 16, uniform: 2^-20 / 2 ln 2 / sqrt(3) = 2e-7; ex2: 2^-22 = 2.4e-7;
+      weight x scale as hi + lo pairs: 2^-22 / sqrt(3) = 1.4e-7; sums of O cut at 2^-23 of it a step, over the tens of
+        tiles of a worker: 5e-7.
+    Together below 1e-6 (root of the squares; 1.6e-6 added up): 2e-6.  (Codes of 0 .. 15 as f16 subnormals, the form of
+    16-bit calls, leave 17 bits of a sum: 7e-6.)  lse: three roundings at up to 16 (2^-21 each) and the scores': 3e-6."""
+    import torch
+    f = Filled([4096, 1031, 70], Hk, D, 64, seed=D + R)
+    q = (1.5 * torch.randn(3, R, Hk * G, D, generator=torch.Generator().manual_seed(6))).cuda()
+    out, lse = f.cache.attend(f.table_t, f.lens_t, q)
+    o, z, qn = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    for i in range(3):
+        k, v, _ = f.seq(i)
+        ro, rz, _ = ref.attend(qn[i], k, v, 1 / math.sqrt(D))
+        rel = np.linalg.norm(o[i] - ro) / np.linalg.norm(ro)
+        assert rel <= 2e-6, (i, rel)
+        assert np.abs(z[i] - rz).max() <= 3e-6, (i, np.abs(z[i] - rz).max())
