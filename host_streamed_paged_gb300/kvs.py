@@ -714,7 +714,8 @@ class KVStream:
 
 # ------------------------------------------------------------ batch operators on torch tensors
 # These run once or more per layer of a decode step, so their host cost counts: checks are plain comparisons and
-# the library's functions are called directly.
+# the library's functions are called directly.  Inference only: the results take part in no autograd graph, whatever
+# the inputs require.
 
 _torch = None
 _DTYPES = {}
@@ -812,7 +813,7 @@ def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
 
     q [rows][Hq][D], k and v [rows][Hk][D] in float16 or bfloat16 (rows may be strided), cu int32 [n + 1]: prompt i is
     rows cu[i] .. cu[i + 1] - 1.  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
-    (undefined where those are allocated here).
+    (undefined where those are allocated here).  The results carry no gradient.
     """
     p = _prompt(q, k, v, cu, scale)
     shape = q.shape
@@ -911,7 +912,10 @@ class Q4Cache:
         return _dtype_of(q), _row_stride(q, "q")
 
     def attend(self, table, lens, q, scale=None, out=None, lse=None):
-        """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens."""
+        """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens.
+
+        out may be q.  The results carry no gradient.
+        """
         dt, stride = self._batch(table, lens, q)
         shape = q.shape
         n, rows, hq, d = shape
@@ -975,7 +979,11 @@ class Q4Cache:
 
     def evict(self, table, dst_table, lens, weights, keep, sinks=0, recent=0):
         """Keep the `keep` tokens of largest weight per sequence and kv head (kvs_q4_evict), compacted into dst_table's
-        pages: (kept int32 [n_seq][Hk][keep], new_lens, kept_weights)."""
+        pages: (kept int32 [n_seq][Hk][keep], new_lens, kept_weights [n_seq][Hk][keep]).
+
+        To go on accumulating, write kept_weights into the first `keep` columns of zeros as wide as the new pages hold and
+        give that to weights as prev.
+        """
         dev, i32, hk = self.device, _torch.int32, self.n_kv_head
         f32 = _torch.float32
         _need_rows(weights, "weights", f32, dev, None, 3)

@@ -836,7 +836,9 @@ kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_rows, uint32_t
  * KVS_F16 or KVS_BF16, rows k_stride / v_stride elements apart) into the
  * slots slots[i] (device int64).  A slot outside the pool (a negative one
  * marks padding) is skipped.  The slots of one call are distinct; a slot named
- * twice holds parts of either row.
+ * twice holds parts of either row.  A block whose largest magnitude passes
+ * 8 * 65504 has no fp16 scale: it is infinite, and the row counts as one that
+ * is not finite.
  */
 kvs_status kvs_q4_append(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, const void *k, const void *v,
                          int32_t dtype, uint64_t k_stride, uint64_t v_stride, void *stream);
@@ -854,10 +856,11 @@ kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n
  * rows' own.  q: device [n_seq][n_rows][n_q_head][D] (KVS_F32, KVS_F16 or
  * KVS_BF16), rows q_stride elements apart; row r sees tokens 0 .. T - n_rows +
  * r.  Any finite scale is taken (at 0 every seen token weighs the same).  out:
- * device, contiguous, in the type of q; lse (nullable): device fp32
- * [n_seq][n_rows][n_q_head].  A row that sees nothing (T = 0: a padding
- * sequence) gets out 0 and lse -inf.  A page number outside the pool within
- * T makes the sequence's outputs NaN.  T is clamped to table_width * P.
+ * device, contiguous, in the type of q (it may be q, if that is contiguous);
+ * lse (nullable): device fp32 [n_seq][n_rows][n_q_head].  A row that sees
+ * nothing (T = 0: a padding sequence) gets out 0 and lse -inf.  A page number
+ * outside the pool within T makes the sequence's outputs NaN.  T is clamped to
+ * table_width * P.
  * Queries of 16-bit types and the weights of their second product enter the
  * tensor cores as single f16 values (exact for such queries up to 2^-28 of
  * a row's largest element), KVS_F32 ones as hi + lo pairs; sums are fp32.
@@ -889,10 +892,12 @@ kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *table, uint32_
  * (sinks + recent <= keep) and, of the others, those of largest weights[i][g][t]
  * (equal ones: the lowest t; NaN below every number); with T <= keep all stay.
  * The tokens that stay are copied in their order to tokens 0 .. of dst_table's
- * pages.  weights: device fp32 [n_seq][Hk][width], T clamped to width and to
- * table_width * P.  Outputs: kept (device int32 [n_seq][Hk][keep], ascending,
- * -1 past the count), kept_weights (nullable, device fp32 [n_seq][Hk][keep],
- * 0 past the count), new_lens (device int32 [n_seq], min(T, keep)).
+ * pages, and the rest of the last group of 32 becomes zeros.  weights: device
+ * fp32 [n_seq][Hk][width], T clamped to width and to table_width * P.  Outputs:
+ * kept (device int32 [n_seq][Hk][keep], ascending, -1 past the count),
+ * kept_weights (nullable, device fp32 [n_seq][Hk][keep], 0 past the count; the
+ * first columns of kvs_q4_weights' next prev, wherever accumulation goes on),
+ * new_lens (device int32 [n_seq], min(T, keep)).
  * dst_width * P >= keep.  The pages of dst_table are no pages of table, except
  * that a sequence with T <= keep may name its own again; kept_weights is not
  * weights, and new_lens is not lens.  A token whose destination page lies
