@@ -209,7 +209,7 @@ struct PromptParams {
     int64_t width;
     int last_rows;
     int main_ctas;  // those past them copy what no key writes
-    int give_up;    // test hook: every role gives up at its first wait, as if its copy never landed
+    int give_up;    // test hook: the MMA warps give up at their first wait, as if its copy never landed, and *abort is up
 };
 
 __device__ __forceinline__ int cu_begin(const PromptParams &p, int s) {
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr float kUp = BF16 ? 0.f : 7.f;
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
-        bool ok = !p.give_up;
+        bool ok = true;
         const int first_tok = t0 + i * TQ;
-        for (int j = ok ? 0 : n; j < n; ++j) {
+        for (int j = 0; j < n; ++j) {
             const int buf = j & 1;
             ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((j >> 1) & 1), abort);
             if (!ok) break;
@@ -874,8 +874,8 @@ __global__ void __launch_bounds__(kWThreads, 2)
         // Two levels: a tile's terms, then the tiles.  (In one chain, thousands of terms of a long prompt's first keys lost
         // up to 1e-4 of their sum.)
         float2 total = make_float2(0.f, 0.f);
-        bool ok = !p.give_up;
-        for (int r = ok ? 0 : ntile; r < ntile; ++r) {
+        bool ok = true;
+        for (int r = 0; r < ntile; ++r) {
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const int buf = r % S::kBufs, tok0 = start + (rank + r * ranks) * TQ;
             float *z = sl + (r & 1) * kCols;
