@@ -54,16 +54,18 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 // One cluster per (sequence, kv head); each CTA has a contiguous share of the
 // candidates (tokens between the sinks and the recent ones), each of its warps
 // a contiguous part of that, their keys in shared memory.  (In registers, 16 a
-// thread, they leave an SM one CTA of 1024 threads: 75 us against 47 on the
-// batch of 131072 to 700 tokens.)  The smallest key that stays is found digit
-// by digit, 8 bits at a time from the top: a histogram of the candidates that
+// thread, they leave an SM one CTA of 1024 threads, which took 1.6 times as
+// long on the batch below.)  The smallest key that stays is found digit by
+// digit, 8 bits at a time from the top: a histogram of the candidates that
 // match the digits so far, summed over the cluster, gives the next digit.  Then
 // every warp, from the counts of those before it, writes its tokens in order:
 // keys above the threshold, and of those equal to it the first ones.
 // KEPT = false is for shares beyond kShare keys: they are read again each time.
 // What bounds it is the longest sequence's chain of loads, passes and cluster
-// barriers (34 us on that batch with rows of 512 tokens counted and placed by
-// the CTA in step, their weights read again).
+// barriers: 36 us on 8 sequences of 131072 to 700 tokens, 8 heads, of which
+// 4096 stay.  The host sizes the keys' memory by what a table can hold (it does
+// not know the lengths), 64 KB a CTA there beside 21 KB of counts: two CTAs fit
+// an SM, and the 512 of that batch begin in two waves.
 template <bool KEPT>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
     extern __shared__ uint32_t keys[];
@@ -225,9 +227,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams p) {
 // that read one token's sit side by side, as many to a line as the layout has.
 // Bound by what a token's rows take from memory: its V codes share 32-byte
 // sectors with seven other tokens, so up to eight times their bytes are read.
-// (8 sequences, 8 heads, D 128, up to 4096 tokens kept of each, 66 MB of rows
-// moved: 31 us, 144 MB read; 34 with a token to a lane, 900 line accesses a
-// tile for 400.)
+// (The batch above, D 128, 66 MB of rows moved: 33 us, 144 MB read; 3 us more
+// with a token to a lane, 900 line accesses a tile for 400.)
 template <int D>
 __global__ void __launch_bounds__(128) gather_kernel(const EvictParams p) {
     constexpr int NB = D / 32, BYTES = 36 * D;

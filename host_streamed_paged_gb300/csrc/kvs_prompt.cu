@@ -331,10 +331,13 @@ __device__ __forceinline__ void find_unit(const PromptParams &p, int c, int per,
 // the one 128-key buffer per tile that would fit: its softmax waits for its
 // own P V and Q K^T each time.
 // The tensor pipe bounds long prompts: 16755 rows of prompts of 8192 .. 1
-// tokens, 32 / 8 heads, D 128, bf16, take 576 us, 1.53 PFLOP/s of causal work
-// (80% of the measured bf16 rate; 790 us with one issuing warp and S one block
-// ahead).  Short prompts take a CTA's chain of starts and waits: five of 1 ..
-// 300 tokens, 24 / 4 heads, D 256, 16 us, as long as the rate allows 3 us.
+// tokens, 32 / 8 heads, D 128, bf16, take 577 us, 1.53 PFLOP/s of causal work
+// (79% of the measured bf16 rate; 600 to 620 in a long run, under the power
+// cap; a third longer with one issuing warp and S one block ahead).  8192 +
+// 6001 tokens, 24 / 4 heads, D 256: 1310 us, 0.97 PFLOP/s, bound by K and V
+// through L2, 128 KB per 128 keys for one tile.  Short prompts take a CTA's
+// chain of starts and waits: five of 1 .. 300 tokens, 24 / 4 heads, D 256, 16
+// us, as long as the rate allows 3 us.
 template <int D>
 struct AttendShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;
@@ -683,12 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the window below, 46 with 96).  Its scores are summed over 128 dims each, in
 // two accumulators: the tensor core drops what lies below an accumulator's last
 // place at every 16 dims, always towards zero, and with 256 dims in a row the
-// weights came out 1.1e-6 low, 6.5e-7 like this (for 46 -> 50 us).
+// weights came out 1.1e-6 low, 6e-7 like this (4 us more).
 // Prompts of 4096 .. 33 tokens, 32 / 8 heads, D 128, over all rows: 114 us (121
-// with the causal edge's test among the columns of every tile, 143 with two key
-// tiles in one CTA of 16 sum warps, 147 to 173 of those with 2 to all of 16
-// exponentials as polynomials on the FMA pipes).  The last 64 rows of 32768, 24
-// / 4 heads, D 256: 39 us a call, 47 with a cold cache.
+// with the causal edge's test among the columns of every tile; a quarter longer
+// with two key tiles in one CTA of 16 sum warps, up to a half with 2 to all of
+// 16 exponentials of those as polynomials on the FMA pipes).  The last 64 rows
+// of 32768, 24 / 4 heads, D 256: 40 to 45 us a call, 48 with a cold cache.
 constexpr int kWThreads = 320;  // warps 0-7: sums; 8: MMA issue; 9: TMA
 template <int D>
 struct WeightShape {
@@ -1089,7 +1092,7 @@ kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t 
 // How many CTAs share a key tile's rows.  A CTA costs kStart tiles before and after its own; a unit's tiles go from none
 // to the prompt's over all rows (half of them on average; the longest of several prompts is taken for 1.5 times the
 // mean, which is all the host knows), or are the window's.  The launch ends no sooner than its whole cost spread over the
-// slots, and than its longest CTA: the least of that over 1, 2, 4 and 8.  Measured on 7 batches, in us for 1 / 2 / 4 / 8:
+// slots, and than its longest CTA: the least of that over 1, 2, 4 and 8.  Measured on 5 batches, in us for 1 / 2 / 4 / 8:
 // 33 units of 256 tiles 220 / 114 / 61 / 38, 64 of 8 13 / 11 / 9.5 / 15, 154 of 196 432 / 224 / 134 / 143, 488 of 57
 // 140 / 122 / 139 / 179, 616 of 18 41 / 50 / 72 / 114.
 unsigned sharing_ctas(uint64_t units, uint64_t slots, uint64_t tiles, bool several, uint64_t window) {

@@ -472,10 +472,12 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
 // two per worker, and the combine joins them in range order.  Query rows
 // beyond one pass's 8 or 16 go to further workers over the same ranges, next
 // to each other in the grid so that they share the tiles through L2.
-// 32 sequences of 32768 .. 0 tokens, 32 / 8 heads, D 128, bf16: 89 us, 3.7 TB/s
+// 32 sequences of 32768 .. 0 tokens, 32 / 8 heads, D 128, bf16: 90 us, 3.6 TB/s
 // of the cache (55% of the measured copy rate), bound by the instructions of a
-// tile, some 700 of a warp.  One of 4096 tokens, 8 / 2 heads, fp32: 14 us, a
-// chain of two launches.
+// tile, some 700 of a warp; with 4 rows each, 16 a pass, 146 us.  One of 4096
+// tokens, 8 / 2 heads, fp32: 14 us, a chain of two launches.  Six of 65536 .. 0
+// tokens, 24 / 4 heads, D 256, f16: 57 us for one row each (2.6 TB/s, 8 warps
+// an SM), 121 for 4, whose 24 rows are three passes over the tiles.
 
 struct AttendParams {
     Pool pool;
@@ -962,7 +964,8 @@ __host__ __device__ constexpr int turn_bytes(int D, int NT) { return NT * 1024 >
 // CTAs of an SM.  A warp's tile takes it some 3000 clocks whatever the others
 // do, so what counts is how many warps the registers allow without spills: 16
 // at 128 registers each (D = 64), 12 at 168 (D = 128; 16 that spill: 95 us for
-// 12's 89), 8 at 255.
+// 12's 89), 8 at 255.  (Shared memory allows as many up to some 600 sequences:
+// their prefix sums are 8 bytes each.  At D = 256 a larger batch has one CTA.)
 __host__ __device__ constexpr int attend_ctas(int D, int NT) { return D == 256 ? 2 : (D == 128 || NT == 2 ? 3 : 4); }
 template <int D, int NT, bool HL>
 __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel(const AttendParams p) {
@@ -1380,8 +1383,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendPa
 // w[t] += sum over rows of 2^(score - lse): K tiles only, no join between
 // workers (a token is one worker's).  Row passes beyond the first re-read the
 // worker's tiles and add to what the first wrote.  Six sequences of 65536 .. 0
-// tokens, 4 rows, 24 / 4 heads, D 256, f16: 47 us, 1.9 TB/s of K, bound by the
-// 24 rows' matrix and exponential instructions (90 us in passes of 8 rows).
+// tokens, 4 rows, 24 / 4 heads, D 256, f16: 47 us, 1.9 TB/s of K (90 us in
+// passes of 8 rows), bound by latency: 24 rows' query fragments take a warp to
+// 255 registers, 8 warps an SM then issue on 40% of the cycles.
 struct WeightsParams {
     AttendParams a;
     const float *lse_in;

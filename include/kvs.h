@@ -780,8 +780,8 @@ typedef struct {
  * (nullable): device fp32 [total_rows][n_q_head].  Rows of no prompt are left
  * as they were.  out overlaps none of q, k and v.  Products run on the tensor
  * cores with fp32 accumulation, the softmax in fp32; the softmax weights are
- * rounded to dtype before the second product (KVS_F16: in steps of no less than
- * 2^-31 of a row's largest weight).
+ * rounded to dtype before the second product (KVS_F16: those below 2^-21 of a
+ * row's largest in steps of 2^-31 of it or less).
  */
 kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream);
 
