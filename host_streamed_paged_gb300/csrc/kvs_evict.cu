@@ -430,10 +430,7 @@ extern "C" kvs_status kvs_q4_evict(const kvs_q4_pool *pool, const int32_t *table
     e = cudaLaunchKernelEx(&cfg, select, p);
     if (e != cudaSuccess) return cuda_failed("evict launch", e);
     void (*g)(EvictParams) = D == 64 ? gather_kernel<64> : D == 128 ? gather_kernel<128> : gather_kernel<256>;
-    cudaLaunchConfig_t gather = {};
-    gather.gridDim = dim3((unsigned)((tiles + 3) / 4));
-    gather.blockDim = dim3(128);
-    gather.stream = st;
-    e = cudaLaunchKernelEx(&gather, g, p);
+    void *args[] = {&p};
+    e = cudaLaunchKernel(reinterpret_cast<const void *>(g), dim3((unsigned)((tiles + 3) / 4)), dim3(128), args, 0, st);
     return e == cudaSuccess ? KVS_OK : cuda_failed("evict launch", e);
 }

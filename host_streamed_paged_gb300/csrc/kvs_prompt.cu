@@ -1064,12 +1064,8 @@ template <typename... A>
 cudaError_t launch(void (*kernel)(A...), dim3 grid, int smem, cudaStream_t s, const A &...a) {
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kernel, a...);
+    void *args[] = {const_cast<void *>(static_cast<const void *>(&a))...};
+    return cudaLaunchKernel(reinterpret_cast<const void *>(kernel), grid, dim3(kThreads), args, smem, s);
 }
 
 template <int D>

@@ -947,7 +947,11 @@ class Q4Cache:
                 return self._workspace(need)
         if cuda.is_current_stream_capturing():
             return _torch.empty(need, dtype=_torch.uint8, device=dev)
-        spaces, stream = self._spaces.__dict__, _stream_of(dev.index)
+        try:
+            spaces = self._spaces.by_stream
+        except AttributeError:
+            spaces = self._spaces.by_stream = {}
+        stream = _stream_of(dev.index)
         ws = spaces.get(stream)
         if ws is None or ws.numel() < need:
             ws = spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=dev)
@@ -987,9 +991,8 @@ class Q4Cache:
         dev, i32, hk = self.device, _torch.int32, self.n_kv_head
         f32 = _torch.float32
         _need_rows(weights, "weights", f32, dev, None, 3)
-        for name, x in (("keep", keep), ("sinks", sinks), ("recent", recent)):  # (ctypes takes any, modulo 2^32)
-            if not 0 <= x <= _MOST:
-                raise ValueError(f"{name} must be 0 .. 2^31 - 1")
+        if not (0 <= keep <= _MOST and 0 <= sinks <= _MOST and 0 <= recent <= _MOST):  # (ctypes takes any, modulo 2^32)
+            raise ValueError("keep, sinks and recent must be 0 .. 2^31 - 1")
         n, heads, width = weights.shape
         if heads != hk:
             raise ValueError("weights must be [n_seq][n_kv_head][width]")
