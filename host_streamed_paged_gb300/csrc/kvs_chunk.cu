@@ -1,0 +1,1035 @@
+// Attention of packed chunks of new rows over the 4-bit page cache, on the
+// 5th-generation tensor cores (include/kvs.h, kvs_q4_attend_chunk).
+//
+// A unit of work is (sequence, kv head, query tiles): 128 rows a tile, token by
+// token with the G query heads of the kv head beside each other, two tiles a
+// CTA at D <= 128 and one at D = 256, against the blocks of 64 keys that some
+// row of the unit sees (all up to its last row; under a window the first
+// tokens' blocks, then those of the window).
+//
+// One CTA per SM.  All units' blocks lie in one line of cost, cut into equal
+// contiguous ranges, one per CTA, whatever the sequences' lengths: a long
+// history with few rows is split along its keys, short chunks share a CTA.
+// Where a cut falls inside a unit its pieces leave partials (O, reference
+// exponent, sum), at most two per CTA, which a second kernel joins in order.
+//
+// Roles (512 threads):
+//   softmax warps, one thread a row: load the unit's queries, then turn each
+//     block's scores S in tensor memory into weights P over them, O rescaled
+//     only when a row's maximum grew by more than 2^8;
+//   dequantising warps: codes and scales straight from the pages to registers
+//     a block ahead, f16 values into 128-byte-swizzled stages;
+//   an issuing warp per tile: S = Q K^T two blocks ahead of O += P V.
+//
+// Values.  A cached value is (n - 8) * scale.  The tensor core takes K and V as
+// f16 values rounded once, each group of 16 tokens brought to a common power of
+// two (its largest scale to 2 .. 4) so that any scale the cache holds keeps
+// f16's precision; the power of two returns in the softmax, K's on the scores
+// and V's on the weights before those are rounded to f16.  Queries enter as f16
+// times a power of two per row (exact down to 2^-28 of the row's largest).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "kvs.h"
+#include "kvs_internal.h"
+#include "kvs_tcgen05.cuh"
+
+namespace kvs {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr int kMaxSeq = 4096;
+constexpr int kMaxGroup = 64;
+constexpr int kWorkers = 152;  // sizes the workspace; a launch has no more CTAs
+constexpr int BN = 64;         // keys of a block
+constexpr int kFacs = 16;      // blocks whose factors are held: more than the stages and score buffers between the roles
+constexpr float kUp = 7.f;     // weights are held as high as f16 reaches, 2^(8 + kUp) at most
+
+struct ChunkParams {
+    Q4Pool pool;
+    const int32_t *table, *lens, *cu;
+    int table_width, n_seq, total, G, Hq, workers;
+    int window, sinks;  // window 0: none
+    const void *q;
+    int64_t q_stride;
+    int bf16;
+    float scale_log2;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    float *part_o;    // [2 * worker + (0: its first unit, begun by another; 1: its last, not ended)][tile][D / 4][row][4]
+    float2 *part_ml;  // [the same][tile][row]: reference exponent and sum
+    struct ChunkMeta *meta;
+    int give_up;  // test hook: the MMA warps give up at their first wait, and *abort is up
+};
+
+// What a worker left for the join.
+struct ChunkMeta {
+    int head;  // of the unit that another worker began: 0 nothing, 1 its end, 2 a part, 3 nothing yet, it goes on
+    int tail;  // 1: it began a unit that it did not end
+    int h, row0, tokens;  // of that unit: kv head, first row in q, tokens
+};
+
+// ---------------------------------------------------------------- the line of work
+
+// A unit costs kUnitCost for its beginning and end, and its keys, twice for two tiles.
+constexpr int kUnitCost = 512;
+constexpr int kMinCost = 512;  // of a worker, while that leaves some idle
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+struct Seq {
+    int begin, n, T, X;  // first row, rows, cached tokens, units of a head
+    int wt;
+    int64_t pos0, cap;   // position of the first row; most keys of a unit
+    int TU;
+    __device__ __forceinline__ void load(const ChunkParams &p, int s, int tile_tokens, int tiles) {
+        begin = clampi(p.cu[s], 0, p.total);
+        n = clampi(p.cu[s + 1], begin, p.total) - begin;
+        const int64_t most = (int64_t)p.table_width << p.pool.lgP;
+        const int len = p.lens[s];
+        T = len < 0 ? 0 : (int)(len < most ? len : most);
+        TU = tile_tokens * tiles;
+        X = (n + TU - 1) / TU;
+        wt = n > tile_tokens ? 2 : 1;
+        pos0 = (int64_t)T - n;
+        cap = p.window ? (int64_t)p.window + TU + p.sinks : (int64_t)1 << 31;
+    }
+    __device__ __forceinline__ int64_t keys(int x) const {
+        const int64_t k = pos0 + (int64_t)(x + 1) * TU;
+        return k < 0 ? 0 : (k < cap ? k : cap);
+    }
+    __device__ __forceinline__ int64_t cost(int x) const { return kUnitCost + wt * keys(x); }
+    __device__ __forceinline__ int64_t before(int x) const {  // cost of units 0 .. x - 1 of a head
+        int64_t a = pos0 >= 0 ? 0 : -pos0 / TU;                // the first with keys
+        int64_t b = (cap - pos0 + TU - 1) / TU - 1;            // the first with the most
+        a = a < x ? a : x;
+        b = b < a ? a : (b < x ? b : x);
+        const int64_t sum = (b - a) * pos0 + TU * ((a + 1 + b) * (b - a) / 2) + (x - b) * cap;
+        return (int64_t)x * kUnitCost + wt * sum;
+    }
+};
+
+// blocks lo .. hi - 1 of a unit's nblk
+struct Piece {
+    int kind;  // 0: nothing, 1: rows that see nothing, 2: work
+    int lo, hi, nblk, first, front;  // block b is keys 64 b .. for b < front, then 64 (first + b - front) ..
+    int s, h, begin, n, T, x;
+    int begun;  // by another worker (o1 > 0)
+};
+
+struct Line {
+    Seq q;
+    int s, h, x;
+    int64_t ustart, pos, end;
+
+    // worker w of W: the equal part of the whole line that is its own.  prefix: costs of the sequences before each.
+    __device__ __forceinline__ bool seek(const ChunkParams &p, const int64_t *prefix, int w, int tile_tokens, int tiles) {
+        const int64_t total = prefix[p.n_seq];
+        int64_t W = (total + kMinCost - 1) / kMinCost;
+        W = W < p.workers ? W : p.workers;
+        if (w >= W) return false;
+        const int64_t each = total / W, more = total - each * W;
+        pos = w * each + (w < more ? w : more);
+        end = (w + 1) * each + (w + 1 < more ? w + 1 : more);
+        int lo = 0, hi = p.n_seq - 1;  // the last sequence that begins at or before pos (one with rows: the next begins after)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= pos) lo = mid;
+            else hi = mid - 1;
+        }
+        s = lo;
+        q.load(p, s, tile_tokens, tiles);
+        const int64_t in = pos - prefix[s], per = q.before(q.X);
+        h = (int)(in / per);
+        const int64_t rem = in - h * per;
+        lo = 0, hi = q.X - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (q.before(mid) <= rem) lo = mid;
+            else hi = mid - 1;
+        }
+        x = lo;
+        ustart = pos - rem + q.before(x);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const ChunkParams &p, int tile_tokens, int tiles, Piece *o) {
+        if (pos >= end) return false;
+        const int64_t c = q.cost(x), o1 = pos - ustart, o2 = c < end - ustart ? c : end - ustart;
+        const int r0 = x * q.TU, r1 = r0 + q.TU < q.n ? r0 + q.TU : q.n;
+        const int64_t last = q.pos0 + r1 - 1;
+        int nblk = 0, first = 0, front = 0;
+        if (last >= 0) {
+            const int64_t p0 = q.pos0 + r0 < 0 ? 0 : q.pos0 + r0;
+            if (p.window && p0 >= p.window) {
+                first = (int)((p0 - p.window + 1) / BN);
+                front = (p.sinks + BN - 1) / BN;
+                front = front < first ? front : first;
+            }
+            nblk = front + (int)(last / BN) + 1 - first;
+        }
+        auto block = [&](int64_t at) { return at <= kUnitCost ? 0 : (int)((at - kUnitCost) * nblk / (c - kUnitCost)); };
+        o->lo = block(o1);
+        o->hi = block(o2);
+        o->nblk = nblk;
+        o->first = first;
+        o->front = front;
+        o->kind = o->hi > o->lo ? 2 : (nblk == 0 && o1 == 0 ? 1 : 0);
+        o->begun = o1 > 0;
+        o->s = s;
+        o->h = h;
+        o->x = x;
+        o->begin = q.begin;
+        o->n = q.n;
+        o->T = q.T;
+        pos = ustart + o2;
+        if (o2 == c) {
+            ustart += c;
+            if (++x == q.X) {
+                x = 0;
+                if (++h == p.pool.Hk) {
+                    h = 0;
+                    while (++s < p.n_seq) {
+                        q.load(p, s, tile_tokens, tiles);
+                        if (q.X > 0) break;
+                    }
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// prefix[s] = cost of the sequences before s; every thread calls it
+__device__ void line_prefix(const ChunkParams &p, int tile_tokens, int tiles, int64_t *prefix) {
+    __shared__ int64_t warp_sum[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.n_seq + kThreads - 1) / kThreads;
+    auto cost = [&](int s) {
+        Seq q;
+        q.load(p, s, tile_tokens, tiles);
+        return q.before(q.X) * p.pool.Hk;
+    };
+    int64_t sum = 0;
+    for (int k = 0; k < per; ++k)
+        if (tid * per + k < p.n_seq) sum += cost(tid * per + k);
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s < p.n_seq) {
+            prefix[s] = base;
+            base += cost(s);
+        }
+    }
+    if (tid == kThreads - 1) prefix[p.n_seq] = base;
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- values
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// a nibble pair in place as f16 n - 8 (low nibbles of the bytes), 16 (n - 8) (high ones): under exponent 0x64 it is 1024 + n
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u); }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return hsub2((w & 0x00f000f0u) | 0x64006400u, 0x64806480u); }
+
+template <bool TRANS>
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    if (TRANS)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                     "r"(d)
+                     : "memory");
+    else
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                     : "memory");
+}
+// a word of codes in each lane, its elements' scales in s2: four 8 x 8 matrices
+template <bool TRANS>
+__device__ __forceinline__ void store_word(uint32_t addr, uint32_t w, uint32_t s2) {
+    const uint32_t x = w >> 8, s16 = hmul2(s2, 0x2c002c00u);  // s / 16, for 16 (n - 8)
+    store_matrices<TRANS>(addr, hmul2(low_codes(w), s2), hmul2(low_codes(x), s2), hmul2(high_codes(w), s16), hmul2(high_codes(x), s16));
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+struct ChunkShape {
+    static constexpr int NQ = D <= 128 ? 2 : 1;         // query tiles of a CTA
+    static constexpr bool kQInTmem = D != 128;          // the queries as the tensor-memory A operand, where there is room
+    static constexpr int NB = D / 32;
+    static constexpr int kHalves = D == 256 ? 2 : 1;    // warps that share a group of 16 tokens
+    static constexpr int kBlocks = NB / kHalves;        // 32-dim blocks of a warp
+    static constexpr int kDeqWarps = 4 * kHalves, kFirstDeq = 4 * NQ, kFirstMma = 12;
+    static constexpr int kVecs = D == 64 ? 1 : 2;       // 16-byte words of codes of a lane
+    static constexpr int kKScales = D == 256 ? 2 : 1, kVScales = D / 64;  // 16-byte words of scales
+    static constexpr int kStage = BN * D * 2;
+    static constexpr int kStages = D == 256 ? 6 : 8;
+    static constexpr int kQBytes = kQInTmem ? 0 : kTileRows * D * 2;
+    static constexpr int kOffRing = NQ * kQBytes;
+    static constexpr int kOffFac = kOffRing + kStages * kStage;  // K factors, V exponents, V factors [kFacs][4]
+    static constexpr int kOffPiece = kOffFac + 3 * kFacs * 16;
+    static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)((sizeof(Piece) + 15) / 16 * 16);
+    static constexpr int kSmem = kOffBar + 320 + 1024;
+    static constexpr uint32_t kColO = 256, kColQ = D == 256 ? 128 : 384;
+    static_assert(kStages * kStage >= (kMaxSeq + 1) * 8, "the line's prefix sums lie in the ring");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using S = ChunkShape<D>;
+    constexpr int NQ = S::NQ, NST = S::kStages, NB = S::NB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t bars = smem_u32(smem + S::kOffBar);
+    // barriers: ring full / empty; per tile: queries there; per tile and score buffer: S full, P full, O done; the end
+    auto b_full = [&](int s) { return bars + 8u * s; };
+    auto b_empty = [&](int s) { return bars + 8u * (8 + s); };
+    auto b_q = [&](int i) { return bars + 8u * (16 + i); };
+    auto b_s = [&](int i, int buf) { return bars + 8u * (18 + 2 * i + buf); };
+    auto b_p = [&](int i, int buf) { return bars + 8u * (22 + 2 * i + buf); };
+    auto b_o = [&](int i, int buf) { return bars + 8u * (26 + 2 * i + buf); };
+    const uint32_t b_final = bars + 8u * 30;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 32);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 33);
+    float *fac_k = reinterpret_cast<float *>(smem + S::kOffFac), *exp_v = fac_k + 4 * kFacs, *fac_v = exp_v + 4 * kFacs;
+
+    const int G = p.G, TQ = kTileRows / G, TU = NQ * TQ;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 32) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(b_full(s), S::kDeqWarps);
+            mbar_init(b_empty(s), NQ);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(b_q(i), 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(b_s(0, i), 1);
+            mbar_init(b_p(0, i), 4);
+            mbar_init(b_o(0, i), 1);
+        }
+        mbar_init(b_final, NQ);
+        *abort = p.give_up;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    int64_t *prefix = reinterpret_cast<int64_t *>(smem + S::kOffRing);
+    line_prefix(p, TQ, NQ, prefix);
+    Line line;
+    const bool any = line.seek(p, prefix, blockIdx.x, TQ, NQ);
+    tc_before();
+    __syncthreads();  // the prefix sums are read, the ring may be written
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    Piece *piece = reinterpret_cast<Piece *>(smem + S::kOffPiece + warp * ((sizeof(Piece) + 15) / 16 * 16));
+    auto next_piece = [&] {  // every warp walks the line by itself; its lanes agree
+        bool more = false;
+        __syncwarp();
+        if (any && lane == 0) more = line.next(p, TQ, NQ, piece);
+        more = __shfl_sync(0xffffffffu, more, 0);
+        __syncwarp();
+        return more;
+    };
+    // the ring's blocks in the order the MMAs take them, of a piece of n blocks: K_0, K_1, V_0, K_2, V_1, ..., V_{n-1}
+    auto ring_k = [](int j) { return j < 2 ? j : 2 * j - 1; };
+    auto ring_v = [](int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+
+    if (warp >= S::kFirstMma && warp < S::kFirstMma + NQ) {
+        // ------------------------------------------------------------ MMA issue (the warp in step, one elected lane issues)
+        const int i = warp - S::kFirstMma;
+        constexpr uint32_t id_s = idesc(false, kTileRows, BN, false), id_o = idesc(false, kTileRows, D, true);
+        const bool one = elect_one();
+        const uint64_t dq = smem_desc(smem_u32(smem), 16), dk = smem_desc(smem_u32(smem + S::kOffRing), 16);
+        const uint64_t dv = smem_desc(smem_u32(smem + S::kOffRing), BN * 128);
+        const uint32_t tq = tmem + S::kColQ + (uint32_t)(i * D / 2);
+        uint32_t ring = 0, blocks = 0, loads = 0;  // so far: stages of both tiles; blocks, query tiles of this one
+        auto issue_s = [&](uint32_t r, uint32_t g) {
+            const uint32_t d = tmem + (uint32_t)((2 * i + (g & 1)) * BN);
+            const uint64_t db0 = dk + (uint64_t)(r % NST * S::kStage >> 4), da = dq + (uint64_t)(i * S::kQBytes >> 4);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint64_t db = db0 + (uint64_t)(((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4);
+                if constexpr (S::kQInTmem) mma_ts(d, tq + 8 * s, db, id_s, s > 0);
+                else mma_ss(d, da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4), db, id_s, s > 0);
+            }
+            mma_commit(b_empty(r % NST));
+            mma_commit(b_s(i, g & 1));
+        };
+        auto issue_o = [&](uint32_t r, uint32_t g, bool from_zero) {
+            const uint32_t d = tmem + S::kColO + (uint32_t)(i * D), a = tmem + (uint32_t)((2 * i + (g & 1)) * BN);
+            const uint64_t db = dv + (uint64_t)(r % NST * S::kStage >> 4);
+#pragma unroll
+            for (int s = 0; s < BN / 16; ++s) mma_ts(d, a + 8u * s, db + (uint64_t)(s * 2048 >> 4), id_o, !from_zero || s > 0);
+            mma_commit(b_empty(r % NST));
+            mma_commit(b_o(i, g & 1));
+        };
+        auto loaded = [&](uint32_t r) { return mbar_done(b_full(r % NST), (r / NST) & 1); };
+        bool ok = !p.give_up;
+        while (ok && next_piece()) {
+            if (piece->kind != 2) continue;
+            const int n = piece->hi - piece->lo;
+            const bool active = piece->x * TU + i * TQ < piece->n;  // (else its stages are freed as they come)
+            for (int j = 0; j < 2 && j < n && ok; ++j) {
+                ok = wait_warp(abort, [&] { return (!active || mbar_done(b_q(i), loads & 1)) & loaded(ring + ring_k(j)); });
+                if (!ok) break;
+                tc_after();
+                if (one) {
+                    if (active) issue_s(ring + ring_k(j), blocks + j);
+                    else mma_commit(b_empty((ring + ring_k(j)) % NST));
+                }
+            }
+            // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
+            for (int j = 0; j < n && ok; ++j) {
+                const bool more = j + 2 < n;
+                const uint32_t rv = ring + ring_v(j, n), rk = ring + ring_k(j + 2);
+                ok = wait_warp(abort, [&] {
+                    bool all = loaded(rv);
+                    if (active) all &= mbar_done(b_p(i, (blocks + j) & 1), ((blocks + j) >> 1) & 1);
+                    if (more) all &= loaded(rk);
+                    return all;
+                });
+                if (!ok) break;
+                tc_after();
+                if (one) {
+                    if (active) {
+                        issue_o(rv, blocks + j, j == 0);
+                        if (more) issue_s(rk, blocks + j + 2);
+                    } else {
+                        mma_commit(b_empty(rv % NST));
+                        if (more) mma_commit(b_empty(rk % NST));
+                    }
+                }
+            }
+            ring += 2 * n;
+            if (active) blocks += n, ++loads;
+        }
+        if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
+    } else if (warp >= S::kFirstDeq && warp < S::kFirstDeq + S::kDeqWarps) {
+        // ------------------------------------------------------------ pages to f16 stages: 16 tokens a warp (half of their dims at D 256)
+        const int dw = warp - S::kFirstDeq, grp = dw & 3, half = dw >> 2, c = grp & 1;
+        const int g = lane >> 2, t = lane & 3, m = lane >> 3, r8 = lane & 7;
+        const int lg = p.pool.lgP - 5, D36 = 36 * D;
+        // where a lane's row of a matrix goes: K, tokens r8 of a group of 8; V, tokens 4 (r8 / 2) + r8 % 2 of the 16 (+ 2)
+        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(half * 2 * BN * 128 + grp * 16 * 128);
+        const int vt = 4 * (r8 >> 1) + (r8 & 1);
+        const uint32_t at_k = (uint32_t)(r8 * 128 + ((m ^ r8) << 4));
+        const uint32_t at_v0 = (uint32_t)(vt * 128 + ((m ^ (vt & 7)) << 4)), at_v1 = (uint32_t)((vt + 2) * 128 + ((m ^ ((vt + 2) & 7)) << 4));
+        uint32_t ring = 0, blocks = 0;
+        bool ok = true;
+        while (ok && next_piece()) {
+            if (piece->kind != 2) continue;
+            const int lo = piece->lo, n = piece->hi - lo, front = piece->front, first = piece->first, T = piece->T, h = piece->h;
+            const int32_t *table = p.table + (int64_t)piece->s * p.table_width;
+            int page_base = -32, page = -1;
+            // tile of block j's group: its bytes (null: a page outside the pool), tokens from the group's first on
+            struct Where {
+                const uint8_t *at;
+                int left;
+            };
+            auto where = [&](int j) {
+                const int b = lo + j, kt = 2 * (b < front ? b : first + b - front) + (grp >> 1);
+                Where w;
+                w.left = T - kt * 32 - 16 * c;
+                w.at = nullptr;
+                if (w.left > 0) {
+                    const int pg = kt >> lg;
+                    if (pg < page_base || pg >= page_base + 32) {
+                        page_base = pg;
+                        page = pg + lane < p.table_width ? table[pg + lane] : -1;
+                    }
+                    const int num = __shfl_sync(0xffffffffu, page, pg - page_base);
+                    if (num >= 0 && num < p.pool.n_pages)
+                        w.at = p.pool.pages + num * p.pool.page_bytes + h * p.pool.head_bytes + (kt & ((1 << lg) - 1)) * D36;
+                }
+                return w;
+            };
+            uint4 kc[S::kVecs], ks[S::kKScales], vc[S::kVecs], vs[S::kVScales];
+            const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+            auto fetch_k = [&](const Where &w) {
+                if (w.at) {
+                    const uint4 *code = reinterpret_cast<const uint4 *>(w.at) + lane;
+#pragma unroll
+                    for (int x = 0; x < S::kVecs; ++x) kc[x] = __ldg(code + (D == 64 ? c : ((2 * c + x) * (NB / 4) + half)) * 32);
+                    const uint8_t *sc = w.at + 16 * D + (c * 8 + g) * NB * 4;
+                    if constexpr (D == 64) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(sc));
+                        ks[0] = make_uint4(v.x, v.y, v.x, v.y);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < S::kKScales; ++x) ks[x] = __ldg(reinterpret_cast<const uint4 *>(sc) + (x ^ half));
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < S::kVecs; ++x) kc[x] = zero;
+#pragma unroll
+                    for (int x = 0; x < S::kKScales; ++x) ks[x] = nan;  // (zero where the sequence has no token)
+                }
+            };
+            auto fetch_v = [&](const Where &w) {
+                if (w.at) {
+                    const uint4 *code = reinterpret_cast<const uint4 *>(w.at + 18 * D) + lane;
+#pragma unroll
+                    for (int x = 0; x < S::kVecs; ++x) vc[x] = __ldg(code + (c * (NB / 2) + 2 * half + x) * 32);
+                    const uint4 *sc = reinterpret_cast<const uint4 *>(w.at + 34 * D + (c * 4 + t) * NB * 8);
+#pragma unroll
+                    for (int x = 0; x < S::kVScales; ++x) vs[x] = __ldg(sc + (x ^ (2 * half)));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < S::kVecs; ++x) vc[x] = zero;
+#pragma unroll
+                    for (int x = 0; x < S::kVScales; ++x) vs[x] = nan;
+                }
+            };
+            // the group's largest scale is below 2^(E + 1): factor 2^(1 - E) as two f16
+            auto common = [&](uint32_t most, int &E) {
+                uint32_t x = (most & 0xffffu) > (most >> 16) ? (most & 0xffffu) : (most >> 16);
+                x = __reduce_max_sync(0xffffffffu, x);
+                const int field = (int)(x >> 10) > 1 ? (int)(x >> 10) : 1;
+                E = field - 15;
+                const uint32_t f = field == 31 ? 0x0200u : (uint32_t)(31 - field) << 10;
+                return f | f << 16;
+            };
+            auto wait_free = [&](uint32_t r) {
+                if (r >= (uint32_t)NST) ok = mbar_wait_warp(b_empty(r % NST), (r / NST - 1) & 1, abort);
+                return ok;
+            };
+            auto publish = [&](uint32_t r) {
+                proxy_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_full(r % NST));
+            };
+            auto convert_k = [&](uint32_t r, int left, int slot) {
+                const uint32_t keep = (g < left ? 0xffffu : 0u) | (g + 8 < left ? 0xffff0000u : 0u);
+                uint32_t most = 0;
+                auto take = [&](uint32_t &w) {
+                    w &= keep;
+                    most = __vmaxu2(most, w & 0x7fff7fffu);
+                };
+#pragma unroll
+                for (int x = 0; x < S::kKScales; ++x) take(ks[x].x), take(ks[x].y), take(ks[x].z), take(ks[x].w);
+                int E;
+                const uint32_t f2 = common(most, E);
+                const uint32_t dst = ring_base + r % NST * S::kStage;
+                const uint32_t sc[4] = {hmul2(ks[0].x, f2), hmul2(ks[0].y, f2), hmul2(ks[0].z, f2), hmul2(ks[0].w, f2)};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // 8 tokens
+#pragma unroll
+                    for (int b = 0; b < S::kBlocks; ++b) {
+                        const uint4 &v = kc[D == 64 ? 0 : (x < S::kVecs ? x : 0)];
+                        const int at = D == 64 ? 2 * x + b : b;
+                        const uint32_t w = at == 0 ? v.x : at == 1 ? v.y : at == 2 ? v.z : v.w;
+                        const uint32_t s2 = __byte_perm(sc[b], 0, x ? 0x3232 : 0x1010);
+                        store_word<false>(dst + (b >> 1) * (BN * 128) + x * 1024 + (at_k ^ ((b & 1) << 6)), w, s2);
+                    }
+                }
+                if (lane == 0 && half == 0) fac_k[slot * 4 + grp] = __uint_as_float((uint32_t)(127 + E - 1) << 23);
+                publish(r);
+            };
+            auto convert_v = [&](uint32_t r, int left, int slot) {
+                const uint32_t k0 = (4 * t < left ? 0xffffu : 0u) | (4 * t + 1 < left ? 0xffff0000u : 0u);
+                const uint32_t k1 = (4 * t + 2 < left ? 0xffffu : 0u) | (4 * t + 3 < left ? 0xffff0000u : 0u);
+                uint32_t most = 0;
+#pragma unroll
+                for (int x = 0; x < S::kVScales; ++x) {
+                    vs[x].x &= k0, vs[x].y &= k1, vs[x].z &= k0, vs[x].w &= k1;
+                    most = __vmaxu2(__vmaxu2(most, vs[x].x & 0x7fff7fffu), vs[x].y & 0x7fff7fffu);
+                    most = __vmaxu2(__vmaxu2(most, vs[x].z & 0x7fff7fffu), vs[x].w & 0x7fff7fffu);
+                }
+                int E;
+                const uint32_t f2 = common(most, E);
+                const uint32_t dst = ring_base + r % NST * S::kStage;
+#pragma unroll
+                for (int x = 0; x < S::kVecs; ++x) {  // two 32-dim blocks
+                    const uint4 v = vc[x], s = vs[x];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {  // block y / 2 of them, token pairs y % 2
+                        const uint32_t w = y == 0 ? v.x : y == 1 ? v.y : y == 2 ? v.z : v.w;
+                        const uint32_t s2 = hmul2(y == 0 ? s.x : y == 1 ? s.y : y == 2 ? s.z : s.w, f2);
+                        store_word<true>(dst + x * (BN * 128) + (((y & 1) ? at_v1 : at_v0) ^ ((y >> 1) << 6)), w, s2);
+                    }
+                }
+                if (lane == 0 && half == 0) {
+                    exp_v[slot * 4 + grp] = (float)(E - 1);
+                    fac_v[slot * 4 + grp] = __uint_as_float((uint32_t)(127 + 1 - E) << 23);
+                }
+                publish(r);
+            };
+            // K_{j+1} and V_{j+1} are fetched as soon as K_j and V_j are converted
+            Where cur_k = where(0), cur_v = cur_k;
+            fetch_k(cur_k);
+            fetch_v(cur_v);
+            auto do_k = [&](int j) {
+                const uint32_t r = ring + ring_k(j);
+                if (!wait_free(r)) return;
+                convert_k(r, cur_k.left, (blocks + j) % kFacs);
+                if (j + 1 < n) {
+                    cur_k = where(j + 1);
+                    fetch_k(cur_k);
+                }
+            };
+            Where ahead[2] = {cur_k, cur_k};  // of block j at j % 2
+            auto do_v = [&](int j) {
+                const uint32_t r = ring + ring_v(j, n);
+                if (!wait_free(r)) return;
+                convert_v(r, cur_v.left, (blocks + j) % kFacs);
+                if (j + 1 < n) {
+                    cur_v = (j & 1) ? ahead[0] : ahead[1];
+                    fetch_v(cur_v);
+                }
+            };
+            do_k(0);
+            ahead[1] = cur_k;
+            if (ok && n > 1) {
+                do_k(1);
+                ahead[0] = cur_k;
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                do_v(j);
+                if (j + 2 < n && ok) {
+                    do_k(j + 2);
+                    if (j & 1) ahead[0] = cur_k;  // block j + 3
+                    else ahead[1] = cur_k;
+                }
+            }
+            ring += 2 * n;
+            blocks += n;
+        }
+    } else if (warp < 4 * NQ) {
+        // ------------------------------------------------------------ softmax, one thread per row
+        const int i = warp >> 2, row = tid & 127, hg = row % G;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float nan = __int_as_float(0x7fc00000);
+        float fac = 0.f;
+        uint32_t ring = 0, blocks = 0, all_blocks = 0;  // stages, blocks of this tile, blocks of the CTA so far
+        bool ok = true;
+        ChunkMeta meta = {};
+        // the row's queries as f16 times a power of two, dims of each 32-dim block in the order of a K row: even ones
+        // of the first 16, odd ones, even ones of the last 16, odd ones
+        auto load_queries = [&](const Piece &c) {
+            const int tok = c.x * TU + i * TQ + row / G;
+            const bool valid = row < TQ * G && tok < c.n;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + hg) * D : 0);
+            uint32_t top2 = 0;
+#pragma unroll 4
+            for (int x = 0; x < D / 8; ++x) {
+                const uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + x) : make_uint4(0, 0, 0, 0);
+                top2 = __vmaxu2(__vmaxu2(top2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+                top2 = __vmaxu2(__vmaxu2(top2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+            }
+            const uint32_t top = (top2 & 0xffffu) > (top2 >> 16) ? (top2 & 0xffffu) : (top2 >> 16);
+            const float top_f = p.bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+            int e = (int)(__float_as_uint(top_f) >> 23) - 127;
+            e = e < -100 ? -100 : (e > 100 ? 100 : e);
+            const float f = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2);
+            // never 0, so that a masked score stays -inf times it
+            fac = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 1.17549435e-38f);
+            auto two = [&](uint32_t w) {
+                float2 y = p.bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                                  : __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                return make_float2(y.x * f, y.y * f);
+            };
+#pragma unroll 1
+            for (int b2 = 0; b2 < D / 64; ++b2) {
+                uint32_t o[32];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {  // 8 dims: half of the even and of the odd chunk of 16
+                    const uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + b2 * 8 + x) : make_uint4(0, 0, 0, 0);
+                    const float2 a = two(v.x), b = two(v.y), c2 = two(v.z), d = two(v.w);
+                    uint32_t *at = o + (x >> 1) * 8 + (x & 1) * 2;
+                    at[0] = pack<false>(a.x, b.x), at[1] = pack<false>(c2.x, d.x);
+                    at[4] = pack<false>(a.y, b.y), at[5] = pack<false>(c2.y, d.y);
+                }
+                if constexpr (S::kQInTmem) {
+                    tmem_st32(lanes + S::kColQ + (uint32_t)(i * D / 2 + b2 * 32), o);
+                } else {
+                    uint8_t *dst = smem + i * S::kQBytes + b2 * (kTileRows * 128) + row * 128;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<uint4 *>(dst + ((x ^ (row & 7)) << 4)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                }
+            }
+            if constexpr (S::kQInTmem) {
+                tmem_wait_st();
+                tc_before();
+            } else {
+                proxy_fence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_q(i));
+        };
+        auto has_rows = [&](const Piece &c) { return c.x * TU + i * TQ < c.n; };
+        auto out_row = [&](int64_t trow, int hq) { return static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D); };
+        // the next piece with work, rows that see nothing written on the way
+        auto find_work = [&] {
+            while (next_piece()) {
+                const Piece &c = *piece;
+                if (warp == 0) {
+                    if (c.begun && c.lo > 0) meta.head = c.kind == 2 ? (c.hi == c.nblk ? 1 : 2) : (c.lo < c.nblk ? 3 : 0);
+                    if (c.kind == 2 && c.lo == 0 && c.hi < c.nblk) {
+                        meta.tail = 1;
+                        meta.h = c.h;
+                        meta.row0 = c.begin + c.x * TU;
+                        meta.tokens = min(TU, c.n - c.x * TU);
+                    }
+                }
+                if (c.kind == 2) return true;
+                const int tok = c.x * TU + i * TQ + row / G;
+                if (c.kind == 1 && row < TQ * G && tok < c.n) {
+                    const int64_t trow = c.begin + tok;
+                    const int hq = c.h * G + hg;
+                    uint4 *dst = reinterpret_cast<uint4 *>(out_row(trow, hq));
+                    for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[trow * p.Hq + hq] = -INFINITY;
+                }
+            }
+            return false;
+        };
+        bool work = find_work();
+        if (work && has_rows(*piece)) load_queries(*piece);
+        while (work) {
+            const Piece c = *piece;
+            const int n = c.hi - c.lo, ft = c.x * TU + i * TQ, tok = ft + row / G;
+            const bool rows = has_rows(c), valid = row < TQ * G && tok < c.n;
+            const int pos0 = c.T - c.n, pos = pos0 + tok;
+            const int pf = pos0 + ft, pl = max(pos0 + min(ft + TQ, c.n) - 1, -1);  // positions of the tile's first and last row
+            float m = -INFINITY;
+            float l = 0.f;
+            for (int j = 0; rows && j < n && ok; ++j) {
+                const uint32_t gb = blocks + j;
+                const int buf = gb & 1, slot = (all_blocks + j) % kFacs;
+                const uint32_t rv = ring + ring_v(j, n);
+                ok = wait_warp(abort, [&] { return mbar_done(b_s(i, buf), (gb >> 1) & 1) & mbar_done(b_full(rv % NST), (rv / NST) & 1); });
+                if (!ok) break;
+                tc_after();
+                const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
+                uint32_t sr[BN];
+#pragma unroll
+                for (int x = 0; x < BN; x += 32) tmem_ld32(ts + x, sr + x);
+                const float4 kf = *reinterpret_cast<const float4 *>(fac_k + 4 * slot), ve = *reinterpret_cast<const float4 *>(exp_v + 4 * slot);
+                const float4 vf = *reinterpret_cast<const float4 *>(fac_v + 4 * slot);
+                tmem_wait_ld();
+                float *s = reinterpret_cast<float *>(sr);
+                const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN;
+                if (k0 + BN - 1 > pf) {  // some row of the tile ends inside the block
+                    const int lim = pos - k0;
+#pragma unroll
+                    for (int x = 0; x < BN; ++x) s[x] = x <= lim ? s[x] : -INFINITY;
+                }
+                if (p.window && k0 <= pl - p.window && k0 + BN > p.sinks) {  // some row's window begins inside the block or after
+                    const int from = (pos > -1 ? pos : -1) - p.window - k0, sk = p.sinks - k0;
+#pragma unroll
+                    for (int x = 0; x < BN; ++x) s[x] = x > from || x < sk ? s[x] : -INFINITY;
+                }
+                const float sc[4] = {fac * kf.x, fac * kf.y, fac * kf.z, fac * kf.w}, ex[4] = {ve.x, ve.y, ve.z, ve.w};
+                float m4[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float a = fmax3(s[16 * x], s[16 * x + 1], s[16 * x + 2]), z = fmax3(s[16 * x + 3], s[16 * x + 4], s[16 * x + 5]);
+#pragma unroll
+                    for (int y = 6; y < 16; y += 4) a = fmax3(a, s[16 * x + y], s[16 * x + y + 1]);
+#pragma unroll
+                    for (int y = 8; y < 16; y += 4) z = fmax3(z, s[16 * x + y], s[16 * x + y + 1]);
+                    m4[x] = fmaf(fmaxf(a, z), sc[x], ex[x]);
+                }
+                const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+                const bool grow = mx > m + 8.f || (m == -INFINITY && mx != -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? mx : m;
+                    const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
+                    l *= alpha;
+                    m = to;
+                    if (j > 0) {
+                        ok = mbar_wait_warp(b_o(i, (gb - 1) & 1), ((gb - 1) >> 1) & 1, abort);
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(to_o + x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                            tmem_st32(to_o + x, v);
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.f : kUp - m;
+                uint32_t pk[32];
+                float part[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float2 sc2 = make_float2(sc[x], sc[x]), neg2 = make_float2(neg + ex[x], neg + ex[x]);
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int y = 0; y < 16; y += 2) {
+                        const float2 z = fma2(make_float2(s[16 * x + y], s[16 * x + y + 1]), sc2, neg2);
+                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                        sum = add2(sum, e);
+                        pk[8 * x + y / 2] = pack<false>(e.x, e.y);
+                    }
+                    part[x] = sum.x + sum.y;
+                }
+                tmem_st32(ts, pk);
+                l += (part[0] * vf.x + part[1] * vf.y) + (part[2] * vf.z + part[3] * vf.w);  // (without V's powers of two)
+                tmem_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p(i, buf));
+            }
+            ring += 2 * n;
+            all_blocks += n;
+            if (rows) blocks += n;
+            // the next queries go in before this unit's output comes out: its scores are all read
+            work = find_work();
+            if (ok && work && has_rows(*piece)) load_queries(*piece);
+            if (!rows) continue;
+            if (ok) ok = mbar_wait_warp(b_o(i, (blocks - 1) & 1), ((blocks - 1) >> 1) & 1, abort);
+            tc_after();
+            const bool whole = c.lo == 0 && c.hi == c.nblk;
+            const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
+            if (!ok) l = nan;
+            if (whole) {
+                const int64_t trow = c.begin + tok;
+                const int hq = c.h * G + hg;
+                const float inv = 1.f / l;
+                uint4 *dst = reinterpret_cast<uint4 *>(out_row(trow, hq));
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t v[32] = {};
+                    if (ok) {  // (the same in a warp; else MMAs may be under way, and what they have is not wanted)
+                        tmem_ld32(to + x, v);
+                        tmem_wait_ld();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                // a row that saw nothing: out 0, lse -inf
+                                const float a = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y]) * inv;
+                                const float z = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y + 1]) * inv;
+                                o[y] = p.bf16 ? pack<true>(a, z) : pack<false>(a, z);
+                            }
+                            dst[(x + k) / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+                if (valid && p.lse) p.lse[trow * p.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l) - kUp) * 0.693147180559945309f;
+            } else {
+                const int64_t at = (int64_t)(2 * (int)blockIdx.x + (c.lo == 0)) * NQ + i;
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o) + at * (D / 4 * kTileRows) + row;
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t v[32] = {};
+                    if (ok) {
+                        tmem_ld32(to + x, v);
+                        tmem_wait_ld();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            dst[(x + k) / 4 * kTileRows] = make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
+                                                                       __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                    }
+                }
+                if (valid) p.part_ml[at * kTileRows + row] = make_float2(m, l);
+            }
+        }
+        if (tid == 0) p.meta[blockIdx.x] = meta;
+    }
+    // tensor memory is freed once every MMA is done and every row was read
+    if (tid == 0) mbar_drain(b_final, 0);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Joins the partials of a unit that several workers shared, in the line's
+// order.  blockIdx.x: the worker that began it, blockIdx.y: tile and 16 dims;
+// one thread per row.
+constexpr int kJoinDims = 16;
+template <int D>
+__global__ void __launch_bounds__(kTileRows) join_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int NQ = ChunkShape<D>::NQ;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: the call ends after the attention has
+    const int w = blockIdx.x, i = (int)blockIdx.y % NQ, d0 = (int)blockIdx.y / NQ * kJoinDims, row = threadIdx.x;
+    const ChunkMeta meta = p.meta[w];
+    const int TQ = kTileRows / p.G, tok = i * TQ + row / p.G;
+    if (!meta.tail || row >= TQ * p.G || tok >= meta.tokens) return;
+    float m = -INFINITY, l = 0.f;
+    float4 o[kJoinDims / 4] = {};
+    auto add = [&](int slot) {
+        const int64_t at = (int64_t)slot * NQ + i;
+        const float2 ml = p.part_ml[at * kTileRows + row];
+        float4 v[kJoinDims / 4];
+#pragma unroll
+        for (int x = 0; x < kJoinDims / 4; ++x)
+            v[x] = reinterpret_cast<const float4 *>(p.part_o)[at * (D / 4 * kTileRows) + (d0 / 4 + x) * kTileRows + row];
+        if (ml.y == 0.f) return;  // saw nothing there
+        const float to = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : exp2f(m - to), b = ml.x == -INFINITY ? 1.f : exp2f(ml.x - to);
+        m = to;
+        l = l * a + ml.y * b;
+#pragma unroll
+        for (int x = 0; x < kJoinDims / 4; ++x)
+            o[x] = make_float4(o[x].x * a + v[x].x * b, o[x].y * a + v[x].y * b, o[x].z * a + v[x].z * b, o[x].w * a + v[x].w * b);
+    };
+    add(2 * w + 1);
+    for (int u = w + 1; u < p.workers; ++u) {
+        const int head = p.meta[u].head;
+        if (head == 1 || head == 2) add(2 * u);
+        if (head <= 1) break;
+    }
+    const int64_t trow = meta.row0 + tok;
+    const int hq = meta.h * p.G + row % p.G;
+    const float inv = 1.f / l;
+    uint32_t r[kJoinDims / 2];
+#pragma unroll
+    for (int x = 0; x < kJoinDims / 4; ++x) {
+        const float4 y = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
+        r[2 * x] = p.bf16 ? pack<true>(y.x, y.y) : pack<false>(y.x, y.y);
+        r[2 * x + 1] = p.bf16 ? pack<true>(y.z, y.w) : pack<false>(y.z, y.w);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D + d0));
+#pragma unroll
+    for (int x = 0; x < kJoinDims / 8; ++x) dst[x] = make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
+    if (d0 == 0 && p.lse) p.lse[trow * p.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l) - kUp) * 0.693147180559945309f;
+}
+
+// ---------------------------------------------------------------- host side
+
+kvs_status bad(kvs_status s, const char *why) {
+    set_thread_error(why);
+    return s;
+}
+kvs_status cuda_failed(const char *what, cudaError_t e) {
+    cudaGetLastError();  // the call's own: no later one is to find it
+    set_thread_error(std::string(what) + ": " + cudaGetErrorString(e));
+    return KVS_ERR_CUDA;
+}
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+uint64_t part_rows(uint32_t D) { return 2ull * kWorkers * (D <= 128 ? 2 : 1) * kTileRows; }
+uint64_t workspace_of(uint32_t D) { return (part_rows(D) * (D * 4 + 8) + kWorkers * sizeof(ChunkMeta) + 255) / 256 * 256; }
+
+template <int D>
+kvs_status launch_chunk(const ChunkParams &p, cudaStream_t s) {
+    using S = ChunkShape<D>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(chunk_kernel<D>), S::kSmem);
+    if (e != cudaSuccess) return cuda_failed("chunk attention launch", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.workers);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
+    if (e != cudaSuccess) return cuda_failed("chunk attention launch", e);
+    cfg.gridDim = dim3((unsigned)p.workers, S::NQ * D / kJoinDims);
+    cfg.blockDim = dim3(kTileRows);
+    cfg.dynamicSmemBytes = 0;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+    return e == cudaSuccess ? KVS_OK : cuda_failed("chunk join launch", e);
+}
+
+}  // namespace
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_q4_chunk_workspace(const kvs_q4_pool *pool, uint64_t *workspace_bytes) {
+    Q4Pool p = {};
+    const kvs_status s = check_q4_pool(pool, false, &p);
+    if (s != KVS_OK) return s;
+    if (!workspace_bytes) return bad(KVS_ERR_INVALID, "null workspace_bytes");
+    *workspace_bytes = workspace_of(pool->head_dim);
+    return KVS_OK;
+}
+
+extern "C" kvs_status kvs_q4_attend_chunk(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                          const int32_t *cu, uint32_t n_seq, uint32_t total_rows, uint32_t n_q_head, const void *q,
+                                          int32_t dtype, uint64_t q_stride, float scale, uint32_t window, uint32_t sinks, void *out,
+                                          uint64_t out_stride, float *lse, void *workspace, uint64_t workspace_bytes, void *stream) {
+    ChunkParams p = {};
+    kvs_status s = check_q4_pool(pool, true, &p.pool);
+    if (s != KVS_OK) return s;
+    if (dtype == KVS_F32) return bad(KVS_ERR_UNSUPPORTED, "chunks are KVS_F16 or KVS_BF16");
+    if (dtype != KVS_F16 && dtype != KVS_BF16) return bad(KVS_ERR_INVALID, "dtype must be KVS_F16 or KVS_BF16");
+    const uint32_t D = pool->head_dim, Hk = pool->n_kv_head;
+    if (n_q_head < Hk || n_q_head % Hk != 0 || n_q_head > 65535)
+        return bad(KVS_ERR_INVALID, "n_q_head must be a positive multiple of n_kv_head, at most 65535");
+    if (n_q_head / Hk > (uint32_t)kMaxGroup) return bad(KVS_ERR_UNSUPPORTED, "n_q_head / n_kv_head must be at most 64");
+    if (n_seq > (uint32_t)kMaxSeq) return bad(KVS_ERR_UNSUPPORTED, "n_seq must be at most 4096");
+    if (total_rows > 0x7fffffffu - 256u) return bad(KVS_ERR_INVALID, "total_rows must be at most 2^31 - 1 - 256");
+    if (table_width < 1 || (uint64_t)table_width * pool->page_tokens > 0x7fffffc0ull)
+        return bad(KVS_ERR_INVALID, "table_width * page_tokens must be 1 .. 2^31 - 64");
+    if (!isfinite(scale)) return bad(KVS_ERR_INVALID, "scale must be finite");
+    if (window > 0x7fffffffu || sinks > 0x7fffffffu - 64u) return bad(KVS_ERR_INVALID, "window and sinks must be at most 2^31 - 65");
+    if (n_seq && (!table || !lens || !cu)) return bad(KVS_ERR_INVALID, "null table, lens or cu");
+    const uint64_t row = (uint64_t)n_q_head * D;
+    if (n_seq && total_rows) {
+        if (!q || !out) return bad(KVS_ERR_INVALID, "null q or out");
+        if (!aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8 || q_stride < row || out_stride < row)
+            return bad(KVS_ERR_INVALID, "rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
+        if (q_stride > (1ull << 31) || out_stride > (1ull << 31)) return bad(KVS_ERR_INVALID, "row stride too large");
+        if (!workspace || !aligned(workspace, 256)) return bad(KVS_ERR_INVALID, "workspace null or not 256-byte aligned");
+        if (workspace_bytes < workspace_of(D)) return bad(KVS_ERR_CAPACITY, "workspace smaller than kvs_q4_chunk_workspace asks for");
+    }
+    if (n_seq == 0 || total_rows == 0) return KVS_OK;
+    const int sms = current_device_sms();
+    p.give_up = batch_wait_fault();
+    p.table = table;
+    p.lens = lens;
+    p.cu = cu;
+    p.table_width = (int)table_width;
+    p.n_seq = (int)n_seq;
+    p.total = (int)total_rows;
+    p.Hq = (int)n_q_head;
+    p.G = (int)(n_q_head / Hk);
+    p.workers = sms < kWorkers ? sms : kWorkers;
+    const bool windowed = window > 0 && window < (uint64_t)table_width * pool->page_tokens;  // (else every token is inside)
+    p.window = windowed ? (int)window : 0;
+    p.sinks = windowed ? (int)sinks : 0;
+    p.q = q;
+    p.q_stride = (int64_t)q_stride;
+    p.bf16 = dtype == KVS_BF16;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out;
+    p.out_stride = (int64_t)out_stride;
+    p.lse = lse;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_rows(D) * D);
+    p.meta = reinterpret_cast<ChunkMeta *>(p.part_ml + part_rows(D));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return D == 64 ? launch_chunk<64>(p, st) : D == 128 ? launch_chunk<128>(p, st) : launch_chunk<256>(p, st);
+}

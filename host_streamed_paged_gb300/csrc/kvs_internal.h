@@ -7,6 +7,8 @@
 
 #include <string>
 
+#include "kvs.h"
+
 namespace kvs {
 
 // Byte layout of one page (kvs_query_sizes in include/kvs.h states it).  Inside a
@@ -207,6 +209,16 @@ cudaError_t launch_fill(const FillParams &p, cudaStream_t s, bool pdl = false);
 // least `bytes` (made once per kernel and device).
 int current_device_sms();
 cudaError_t ensure_smem_limit(const void *kernel, int bytes);
+
+// The 4-bit page pool of a call (kvs_q4_pool), with what the kernels derive
+// from it.  check_q4_pool fills it, or says what is wrong with the pool
+// (need_pages: its buffer too).
+struct Q4Pool {
+    uint8_t *pages;
+    int64_t n_pages, page_bytes, head_bytes;
+    int P, lgP, Hk;
+};
+kvs_status check_q4_pool(const kvs_q4_pool *pool, bool need_pages, Q4Pool *out);
 
 // Whether this call of a batch operator is the one that kvs_debug_inject(NULL,
 // KVS_FAULT_DEVICE_WAIT, nth) armed on this thread (counts the call).

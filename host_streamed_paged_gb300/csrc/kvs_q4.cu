@@ -46,11 +46,7 @@ constexpr int kMaxSeq = 4096;      // sequences per call (their prefix sums live
 constexpr int kMaxGroupRows = 64;  // n_rows * group bound
 constexpr uint32_t kWaitLimit = 1u << 22;
 
-struct Pool {
-    uint8_t *pages;
-    int64_t n_pages, page_bytes, head_bytes;
-    int P, lgP, Hk;
-};
+using Pool = Q4Pool;
 
 // ---------------------------------------------------------------- elements
 
@@ -1567,25 +1563,6 @@ kvs_status cuda_failed(const char *what, cudaError_t e) {
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t elem_size(int dtype) { return dtype == KVS_F32 ? 4 : 2; }
 
-kvs_status check_pool(const kvs_q4_pool *pool, bool need_pages, Pool *out) {
-    if (!pool) return bad(KVS_ERR_INVALID, "null pool");
-    const uint32_t P = pool->page_tokens, D = pool->head_dim;
-    if (!(P == 32 || P == 64 || P == 128 || P == 256) || !(D == 64 || D == 128 || D == 256))
-        return bad(KVS_ERR_UNSUPPORTED, "page_tokens must be 32..256 (power of two), head_dim 64, 128 or 256");
-    if (pool->n_kv_head == 0 || pool->n_kv_head > 65535) return bad(KVS_ERR_INVALID, "n_kv_head must be 1 .. 65535");
-    if (need_pages) {
-        if (!pool->pages || !aligned(pool->pages, 16)) return bad(KVS_ERR_INVALID, "pages null or not 16-byte aligned");
-        if (pool->n_pages == 0 || pool->n_pages > 0x7fffffffull) return bad(KVS_ERR_INVALID, "n_pages must be 1 .. 2^31 - 1");
-    }
-    out->pages = static_cast<uint8_t *>(pool->pages);
-    out->n_pages = (int64_t)pool->n_pages;
-    out->P = (int)P;
-    out->lgP = P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : 8;
-    out->Hk = (int)pool->n_kv_head;
-    out->head_bytes = (int64_t)P * D * 9 / 8;
-    out->page_bytes = out->head_bytes * out->Hk;
-    return KVS_OK;
-}
 bool dtype_ok(int32_t t) { return t == KVS_F32 || t == KVS_F16 || t == KVS_BF16; }
 
 // How a call's query rows are passed: fp32 queries 8 rows at a time (with
@@ -1626,7 +1603,7 @@ kvs_status check_rows(uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, int Hk
 kvs_status fill_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens, uint32_t n_seq,
                        uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype, uint64_t q_stride, float scale,
                        AttendParams *p) {
-    kvs_status s = check_pool(pool, true, &p->pool);
+    kvs_status s = check_q4_pool(pool, true, &p->pool);
     if (s != KVS_OK) return s;
     if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
     uint32_t G = 0;
@@ -1681,6 +1658,27 @@ int smem_of(uint32_t D, int bytes, int turn, uint32_t n_seq) {
 }
 
 }  // namespace
+
+kvs_status check_q4_pool(const kvs_q4_pool *pool, bool need_pages, Q4Pool *out) {
+    if (!pool) return bad(KVS_ERR_INVALID, "null pool");
+    const uint32_t P = pool->page_tokens, D = pool->head_dim;
+    if (!(P == 32 || P == 64 || P == 128 || P == 256) || !(D == 64 || D == 128 || D == 256))
+        return bad(KVS_ERR_UNSUPPORTED, "page_tokens must be 32..256 (power of two), head_dim 64, 128 or 256");
+    if (pool->n_kv_head == 0 || pool->n_kv_head > 65535) return bad(KVS_ERR_INVALID, "n_kv_head must be 1 .. 65535");
+    if (need_pages) {
+        if (!pool->pages || !aligned(pool->pages, 16)) return bad(KVS_ERR_INVALID, "pages null or not 16-byte aligned");
+        if (pool->n_pages == 0 || pool->n_pages > 0x7fffffffull) return bad(KVS_ERR_INVALID, "n_pages must be 1 .. 2^31 - 1");
+    }
+    out->pages = static_cast<uint8_t *>(pool->pages);
+    out->n_pages = (int64_t)pool->n_pages;
+    out->P = (int)P;
+    out->lgP = P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : 8;
+    out->Hk = (int)pool->n_kv_head;
+    out->head_bytes = (int64_t)P * D * 9 / 8;
+    out->page_bytes = out->head_bytes * out->Hk;
+    return KVS_OK;
+}
+
 }  // namespace kvs
 
 using namespace kvs;
@@ -1688,7 +1686,7 @@ using namespace kvs;
 extern "C" kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_rows, uint32_t n_q_head, int32_t dtype,
                                          uint64_t *page_bytes, uint64_t *workspace_bytes) {
     Pool p = {};
-    kvs_status s = check_pool(pool, false, &p);
+    kvs_status s = check_q4_pool(pool, false, &p);
     if (s != KVS_OK) return s;
     if (workspace_bytes) {
         if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
@@ -1702,7 +1700,7 @@ extern "C" kvs_status kvs_q4_query_sizes(const kvs_q4_pool *pool, uint32_t n_row
 }
 
 static kvs_status rows_call(const kvs_q4_pool *pool, const int64_t *slots, uint64_t n, int32_t dtype, RowsParams *p) {
-    kvs_status s = check_pool(pool, true, &p->pool);
+    kvs_status s = check_q4_pool(pool, true, &p->pool);
     if (s != KVS_OK) return s;
     if (!dtype_ok(dtype)) return bad(KVS_ERR_INVALID, "dtype must be KVS_F32, KVS_F16 or KVS_BF16");
     if (n && (!slots || !aligned(slots, 8))) return bad(KVS_ERR_INVALID, "slots null or misaligned");

@@ -184,6 +184,9 @@ SIGNATURES = {
     "kvs_q4_query_sizes": ([_P, _U32, _U32, _I32, _P, _P], _I32),
     "kvs_q4_append": ([_P, _P, _U64, _P, _P, _I32, _U64, _U64, _P], _I32),
     "kvs_q4_read": ([_P, _P, _U64, _P, _P, _I32, _P], _I32),
+    "kvs_q4_chunk_workspace": ([_P, _P], _I32),
+    "kvs_q4_attend_chunk": ([_P, _P, _U32, _P, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _U32, _U32, _P, _U64, _P, _P, _U64,
+                             _P], _I32),
     "kvs_q4_attend": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
     "kvs_q4_weights": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
     "kvs_q4_evict": ([_P, _P, _U32, _P, _U32, _P, _U32, _P, _U64, _U32, _U32, _U32, _P, _P, _P, _P], _I32),
@@ -445,6 +448,20 @@ def kvs_q4_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dt
     return _check(None, load().kvs_q4_attend(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), n_seq, n_rows,
                                              n_q_head, _ptr(q), dtype, q_stride, scale, _ptr(out), _ptr(lse),
                                              _ptr(workspace), workspace_bytes, stream))
+
+
+def kvs_q4_chunk_workspace(pool: kvs_q4_pool) -> int:
+    """Workspace bytes of kvs_q4_attend_chunk."""
+    ws = ctypes.c_uint64()
+    _check(None, load().kvs_q4_chunk_workspace(ctypes.byref(pool), ctypes.byref(ws)))
+    return ws.value
+
+
+def kvs_q4_attend_chunk(pool, table, table_width, lens, cu, n_seq, total_rows, n_q_head, q, dtype, q_stride, scale, window,
+                        sinks, out, out_stride, lse, workspace, workspace_bytes, stream=0) -> int:
+    return _check(None, load().kvs_q4_attend_chunk(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), _ptr(cu), n_seq,
+                                                   total_rows, n_q_head, _ptr(q), dtype, q_stride, scale, window, sinks,
+                                                   _ptr(out), out_stride, _ptr(lse), _ptr(workspace), workspace_bytes, stream))
 
 
 def kvs_q4_weights(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, lse, prev,
@@ -769,6 +786,13 @@ def _need_rows(t, name, dtype, device, rows, dims):
         raise ValueError(f"{name} must have {dims} dimensions{'' if rows is None else f', the first of size {rows}'}")
 
 
+def _window(window, sinks):
+    """Both as the library takes them (a window past every length is one that never ends)."""
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    return min(int(window), _MOST), min(int(sinks), _MOST - 64)
+
+
 def _stream_of(index) -> int:
     """The current stream's handle on a device (without building a Stream object, which costs 3 us)."""
     raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
@@ -934,6 +958,40 @@ class Q4Cache:
         _run(self.device, self._lib.kvs_q4_attend, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows, hq,
              q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), need)
         return out, lse
+
+    def attend_chunk(self, table, lens, cu, q, scale=None, out=None, lse=None, window=0, sinks=0):
+        """Attention of packed chunks of new rows over the cached tokens (kvs_q4_attend_chunk): out, as q.
+
+        q [rows][Hq][D] in float16 or bfloat16 (rows may be strided), cu int32 [n_seq + 1]: rows cu[i] .. cu[i + 1] - 1 are
+        the last tokens of sequence i, whose lens count them (append them first).  A row sees the tokens up to its own;
+        with window > 0 the last window of those and the first sinks tokens of the sequence.  lse, where given (float32
+        [rows][Hq]), is written too.  out may be q.  Rows of no sequence are left as they are (undefined where out is
+        allocated here).  The results carry no gradient.
+        """
+        dev, i32, shape = self.device, _torch.int32, q.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or q.device != dev:
+            raise ValueError("q must be [rows][n_q_head][head_dim] on the cache's device")
+        _need_rows(cu, "cu", i32, dev, None, 1)
+        n = cu.shape[0] - 1
+        if n < 0:
+            raise ValueError("cu must hold n_seq + 1 offsets")
+        _need_rows(table, "table", i32, dev, n, 2)
+        _need_rows(lens, "lens", i32, dev, n, 1)
+        window, sinks = _window(window, sinks)
+        if out is None:
+            out = _torch.empty(shape, dtype=q.dtype, device=dev)
+        elif out.shape != shape or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must be as q")
+        if lse is not None:
+            _need(lse, "lse", _torch.float32, dev, shape[:2])
+        need = self._need_bytes.get("chunk")
+        if need is None:
+            need = self._need_bytes["chunk"] = kvs_q4_chunk_workspace(self.pool)
+        ws = self._workspace(need)
+        _run(dev, self._lib.kvs_q4_attend_chunk, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), cu.data_ptr(), n,
+             shape[0], shape[1], q.data_ptr(), _dtype_of(q), _row_stride(q, "q"), shape[2] ** -0.5 if scale is None else scale,
+             window, sinks, out.data_ptr(), _row_stride(out, "out"), lse.data_ptr() if lse is not None else None, ws.data_ptr(), need)
+        return out
 
     def _workspace(self, need):
         """attend's workspace: one per stream and thread, whose calls run in order (another thread's may come between the

@@ -873,6 +873,34 @@ kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t
                          uint64_t workspace_bytes, void *stream);
 
 /*
+ * kvs_q4_attend_chunk -- attention of chunks of new rows, packed one after
+ * another as prompts are, over the cached tokens: rows cu[i] .. cu[i+1] - 1 of
+ * q (cu: device int32 [n_seq + 1], ascending) are the last tokens of sequence
+ * i, whose table and length lens[i] (T, the rows' own tokens included) are as
+ * kvs_q4_attend takes them.  Of n rows, row r stands at position T - n + r and
+ * sees the tokens up to its own; with window > 0 only the last `window` of
+ * those and the first `sinks` tokens.  A sequence may have no row, one (a
+ * decode step) or thousands.  q and out: device [total_rows][n_q_head][D]
+ * (KVS_F16 or KVS_BF16), rows q_stride / out_stride elements apart; out may be
+ * q (with its stride), else overlaps it nowhere.  lse (nullable): device fp32
+ * [total_rows][n_q_head].  Rows of no sequence are left as they were.  A row at
+ * a negative position (T < n) sees nothing: out 0, lse -inf.  Any finite scale
+ * is taken.  A page number outside the pool makes the outputs of the rows that
+ * see it NaN (it may those of other rows of its sequence).
+ * K and V enter the tensor cores as f16 values rounded once, whatever their
+ * scale, queries as in kvs_q4_attend, weights as f16; sums are fp32.  So lse
+ * carries the rounding of K: up to 2^-11 |scale| sum |q k| for a row's largest
+ * terms, where kvs_q4_attend's has none.
+ * workspace: device, kvs_q4_chunk_workspace's bytes (they depend on head_dim
+ * alone).  n_q_head / n_kv_head at most 64, n_seq at most 4096.
+ */
+kvs_status kvs_q4_chunk_workspace(const kvs_q4_pool *pool, uint64_t *workspace_bytes);
+kvs_status kvs_q4_attend_chunk(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                               const int32_t *cu, uint32_t n_seq, uint32_t total_rows, uint32_t n_q_head, const void *q,
+                               int32_t dtype, uint64_t q_stride, float scale, uint32_t window, uint32_t sinks, void *out,
+                               uint64_t out_stride, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
  * kvs_q4_weights -- the attention weight each cached token received from those
  * rows: w[i][g][t] = prev[i][g][t] + sum over rows r that see t and query
  * heads h of kv head g of exp(scale q_irh . k_tg - lse_irh), with
