@@ -44,6 +44,7 @@ struct PromptParams {
     float *w;
     int64_t width;
     int last_rows;
+    int window, sinks;  // of the windowed kernels
     int main_ctas;  // those past them copy what no key writes
     int give_up;    // test hook: the MMA warps give up at their first wait, as if its copy never landed, and *abort is up
 };
@@ -189,7 +190,7 @@ struct AttendShape {
     static constexpr uint32_t kColO = 256;
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attend_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
                          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -243,11 +244,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int begin = place[2], L = place[3] - begin;
     const int t0 = place[1] * NQ * TQ;  // first token of tile 0, within the prompt
+    // under a window the blocks of the first tokens, `front` of them, then those from the first row's window on: block j is
+    // j, or j + skip from `front` on
+    int front = 0, skip = 0;
+    if constexpr (WIN) {
+        const int first = t0 >= p.window ? (t0 - p.window + 1) / BN : 0;
+        front = min((p.sinks + BN - 1) / BN, first);
+        skip = first - front;
+    }
+    auto key_block = [&](int j) { return WIN && j >= front ? j + skip : j; };
     int nblk[2] = {0, 0}, n_max = 0;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         const int a = t0 + i * TQ, last = (a + TQ < L ? a + TQ : L) - 1;
-        nblk[i] = a < L ? last / BN + 1 : 0;
+        nblk[i] = a < L ? last / BN + 1 - skip : 0;
         n_max = nblk[i] > n_max ? nblk[i] : n_max;
     }
     // the ring's blocks in the order the MMAs take them: K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_piece = [&](int r) {
         const int st = r % NST, q = r / S::kPieces, c = r % S::kPieces, end = 2 * n_max - 1;
         const bool is_v = q == end || (q >= 2 && !(q & 1));
-        const int j = q == end ? n_max - 1 : (q < 2 ? q : (q & 1 ? (q + 1) / 2 : q / 2 - 1));
+        const int j = key_block(q == end ? n_max - 1 : (q < 2 ? q : (q & 1 ? (q + 1) / 2 : q / 2 - 1)));
         const uint32_t dst = smem_u32(smem + S::kOffRing + st * S::kPiece);
         mbar_expect(b_full(st), (uint32_t)S::kPiece);
         if (is_v) {
@@ -386,10 +396,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, sr + c);
             tmem_wait_ld();
             float *s = reinterpret_cast<float *>(sr);
-            if ((j + 1) * BN > first_tok + 1) {  // some row of the tile ends inside the block
-                const int lim = tok - j * BN;
+            const int kb = key_block(j);
+            if ((kb + 1) * BN > first_tok + 1) {  // some row of the tile ends inside the block
+                const int lim = tok - kb * BN;
 #pragma unroll
                 for (int c = 0; c < BN; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+            }
+            if constexpr (WIN) {
+                // some row's window begins behind the block's first key, and not all of its keys are of the first that stay
+                if (kb * BN <= first_tok + TQ - 1 - p.window && (kb + 1) * BN > p.sinks) {
+                    const int from = tok - p.window - kb * BN, stay = p.sinks - kb * BN;
+#pragma unroll
+                    for (int c = 0; c < BN; ++c) s[c] = c > from || c < stay ? s[c] : -INFINITY;
+                }
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -434,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st32(ts + 32 * part, pk);
             }
             l2 = add2(l2, add2(sum[0], sum[1]));
-            if ((j + 1) * BN > L) {
+            if ((kb + 1) * BN > L) {
                 // the block reaches past the prompt: its last rows are another prompt's (or nobody's), and a weight
                 // of zero times what stands there must be zero
 #pragma unroll
                 for (int c = 0; c < S::kPieces; ++c) {
                     const int r = ring_v(j) + c, st = r % NST;
                     ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
-                    if (ok && row < S::kVKeys && j * BN + c * S::kVKeys + row >= L) {
+                    if (ok && row < S::kVKeys && kb * BN + c * S::kVKeys + row >= L) {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
 #pragma unroll
@@ -904,7 +923,7 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, int smem, cudaStream_t s, co
     return cudaLaunchKernel(reinterpret_cast<const void *>(kernel), grid, dim3(kThreads), args, smem, s);
 }
 
-template <int D>
+template <int D, bool WIN>
 kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
     using S = AttendShape<D>;
     const bool bf = p->dtype == KVS_BF16;
@@ -916,7 +935,7 @@ kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t 
     if (r != KVS_OK) return r;
     const uint64_t units = (uint64_t)p->total_rows / (S::NQ * TQ) + p->n_seq;  // at least the prompts' tile groups
     if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
-    const cudaError_t e = launch(bf ? prompt_attend_kernel<D, true> : prompt_attend_kernel<D, false>,
+    const cudaError_t e = launch(bf ? prompt_attend_kernel<D, true, WIN> : prompt_attend_kernel<D, false, WIN>,
                                  dim3((unsigned)(units * p->n_kv_head)), S::kSmem, s, pp, mq, mk, mv);
     return e == cudaSuccess ? KVS_OK : cuda_failed("prompt attention launch", e);
 }
@@ -985,7 +1004,8 @@ kvs_status weights_for(const kvs_prompt *p, PromptParams pp, cudaStream_t s) {
 
 using namespace kvs;
 
-extern "C" kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream) {
+template <bool WIN>
+static kvs_status attend_call(const kvs_prompt *p, uint32_t window, uint32_t sinks, void *out, uint64_t out_stride, float *lse, void *stream) {
     PromptParams pp = {};
     const kvs_status s = check_prompt(p, true, &pp);
     if (s != KVS_OK) return s;
@@ -996,8 +1016,25 @@ extern "C" kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t
     pp.out = out;
     pp.out_stride = (int64_t)out_stride;
     pp.lse = lse;
+    pp.window = (int)window;
+    pp.sinks = (int)sinks;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return p->head_dim == 64 ? attend_for<64>(p, pp, st) : p->head_dim == 128 ? attend_for<128>(p, pp, st) : attend_for<256>(p, pp, st);
+    return p->head_dim == 64    ? attend_for<64, WIN>(p, pp, st)
+           : p->head_dim == 128 ? attend_for<128, WIN>(p, pp, st)
+                                : attend_for<256, WIN>(p, pp, st);
+}
+
+extern "C" kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream) {
+    return attend_call<false>(p, 0, 0, out, out_stride, lse, stream);
+}
+
+extern "C" kvs_status kvs_prompt_attend_window(const kvs_prompt *p, uint32_t window, uint32_t sinks, void *out, uint64_t out_stride,
+                                               float *lse, void *stream) {
+    if (!p) return bad(KVS_ERR_INVALID, "null prompt");
+    if (window > 0x7fffffffu || sinks > 0x7fffffffu - 64u) return bad(KVS_ERR_INVALID, "window must be at most 2^31 - 1, sinks 2^31 - 65");
+    if (window == 0 || window >= p->total_rows) return attend_call<false>(p, 0, 0, out, out_stride, lse, stream);  // every key is inside
+    // (sinks past the rows stand for all of them)
+    return attend_call<true>(p, window, sinks < p->total_rows ? sinks : p->total_rows, out, out_stride, lse, stream);
 }
 
 extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,

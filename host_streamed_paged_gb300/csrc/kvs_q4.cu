@@ -489,6 +489,7 @@ struct AttendParams {
     int dtype, row_blocks, workers;
     float scale_log2;
     int give_up;  // test hook: a worker's first wait gives up at once, as if its copy never landed
+    int window, sinks;  // of the windowed kernels
 };
 
 __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, int table_width, int s) {
@@ -497,9 +498,37 @@ __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, in
     return n < 0 ? 0 : (int)(n < cap ? n : cap);
 }
 
+// Which tiles of a sequence of len tokens its rows see: all (WIN false), or
+// under a window the first tokens' and those from the first row's window on:
+// tile k of that line is k, or k + skip from `front` on.
+template <bool WIN>
+struct Seen {
+    __device__ __forceinline__ Seen() {}
+    __device__ __forceinline__ Seen(const AttendParams &, int) {}
+    __device__ __forceinline__ int tiles(int len) const { return (len + kTile - 1) / kTile; }
+    __device__ __forceinline__ int at(int k) const { return k; }
+};
+template <>
+struct Seen<true> {
+    int front, skip;
+    __device__ __forceinline__ Seen() {}
+    __device__ __forceinline__ Seen(const AttendParams &p, int len) {
+        const int64_t from = (int64_t)len - p.R + 1 - p.window;  // the first row's window begins here
+        const int first = from > 0 ? (int)(from / kTile) : 0, sink_tiles = (int)(((int64_t)p.sinks + kTile - 1) / kTile);
+        front = sink_tiles < first ? sink_tiles : first;
+        skip = first - front;
+    }
+    __device__ __forceinline__ int tiles(int len) const { return (len + kTile - 1) / kTile - skip; }
+    __device__ __forceinline__ int at(int k) const { return k < front ? k : k + skip; }
+};
+
 // prefix[s] = {tiles of one head, sequences with tokens} of sequences 0 .. s-1;
 // every thread of the CTA calls it
-__device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_width, int n_seq, int2 *prefix) {
+template <bool WIN = false>
+__device__ void tile_prefix(const AttendParams &p, int2 *prefix) {
+    const Pool &pool = p.pool;
+    const int32_t *lens = p.lens;
+    const int table_width = p.table_width, n_seq = p.n_seq;
     __shared__ int2 warp_sum[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int per = (n_seq + nt - 1) / nt;
@@ -507,7 +536,7 @@ __device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_wid
     for (int k = 0; k < per; ++k) {
         const int s = tid * per + k;
         if (s < n_seq) {
-            const int t = (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+            const int len = seq_len(pool, lens, table_width, s), t = Seen<WIN>(p, len).tiles(len);
             sum.x += t;
             sum.y += t > 0;
         }
@@ -526,7 +555,7 @@ __device__ void tile_prefix(const Pool &pool, const int32_t *lens, int table_wid
         const int s = tid * per + k;
         if (s < n_seq) {
             prefix[s] = base;
-            const int t = (seq_len(pool, lens, table_width, s) + kTile - 1) / kTile;
+            const int len = seq_len(pool, lens, table_width, s), t = Seen<WIN>(p, len).tiles(len);
             base.x += t;
             base.y += t > 0;
         }
@@ -915,39 +944,44 @@ struct Place {
 };
 
 // The same with the pages ahead, for the copies.
+template <bool WIN = false>
 struct Cursor : Place {
     int page_base, page;  // lane l holds page number page_base + l of the sequence
     int page_at;          // the page (of the sequence) that base points into; -1: none yet
     const uint8_t *base;
-    __device__ __forceinline__ void load_pages(const Pool &pool, const int32_t *table, int width, int tiles_per_page_lg) {
+    Seen<WIN> seen;
+    __device__ __forceinline__ void load_pages(const AttendParams &p, int tiles_per_page_lg) {
         const int lane = threadIdx.x & 31;
-        page_base = k >> tiles_per_page_lg;
+        page_base = seen.at(k) >> tiles_per_page_lg;
         page_at = -1;
         const int at = page_base + lane;
-        page = at < width ? table[(int64_t)s * width + at] : -1;
+        page = at < p.table_width ? p.table[(int64_t)s * p.table_width + at] : -1;
     }
-    __device__ __forceinline__ void seek(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq,
-                                         uint32_t unit, int lg) {
-        s = find_seq<false>(prefix, n_seq, pool.Hk, unit);
+    __device__ __forceinline__ void begin(const AttendParams &p, int lg) {  // of a (sequence, head)
+        if constexpr (WIN) seen = Seen<WIN>(p, seq_len(p.pool, p.lens, p.table_width, s));
+        load_pages(p, lg);
+    }
+    __device__ __forceinline__ void seek(const AttendParams &p, const int2 *prefix, uint32_t unit, int lg) {
+        s = find_seq<false>(prefix, p.n_seq, p.pool.Hk, unit);
         T = prefix[s + 1].x - prefix[s].x;
-        const uint32_t in = unit - (uint32_t)prefix[s].x * pool.Hk;
+        const uint32_t in = unit - (uint32_t)prefix[s].x * p.pool.Hk;
         h = (int)(in / (uint32_t)T);
         k = (int)(in - (uint32_t)h * (uint32_t)T);
-        load_pages(pool, table, width, lg);
+        begin(p, lg);
     }
     // the tile's bytes (null: a page number outside the pool), warp-uniform
-    __device__ __forceinline__ const uint8_t *tile(const Pool &pool, const int32_t *table, int width, int lg, int tile_bytes) {
-        const int at = k >> lg;
+    __device__ __forceinline__ const uint8_t *tile(const AttendParams &p, int lg, int tile_bytes) {
+        const int kt = seen.at(k), at = kt >> lg;
         if (at != page_at) {
-            if (at - page_base >= 32) load_pages(pool, table, width, lg);
+            if (at - page_base >= 32) load_pages(p, lg);
             const int pg = __shfl_sync(0xffffffffu, page, at - page_base);
-            base = pg < 0 || pg >= pool.n_pages ? nullptr : pool.pages + pg * pool.page_bytes + h * pool.head_bytes;
+            base = pg < 0 || pg >= p.pool.n_pages ? nullptr : p.pool.pages + pg * p.pool.page_bytes + h * p.pool.head_bytes;
             page_at = at;
         }
-        return base ? base + (k & ((1 << lg) - 1)) * tile_bytes : nullptr;
+        return base ? base + (kt & ((1 << lg) - 1)) * tile_bytes : nullptr;
     }
-    __device__ __forceinline__ void advance(const Pool &pool, const int2 *prefix, const int32_t *table, int width, int n_seq, int lg) {
-        if (next(prefix, n_seq, pool.Hk)) load_pages(pool, table, width, lg);
+    __device__ __forceinline__ void advance(const AttendParams &p, const int2 *prefix, int lg) {
+        if (next(prefix, p.n_seq, p.pool.Hk)) begin(p, lg);
     }
 };
 
@@ -963,7 +997,7 @@ __host__ __device__ constexpr int turn_bytes(int D, int NT) { return NT * 1024 >
 // 12's 89), 8 at 255.  (Shared memory allows as many up to some 600 sequences:
 // their prefix sums are 8 bytes each.  At D = 256 a larger batch has one CTA.)
 __host__ __device__ constexpr int attend_ctas(int D, int NT) { return D == 256 ? 2 : (D == 128 || NT == 2 ? 3 : 4); }
-template <int D, int NT, bool HL>
+template <int D, int NT, bool HL, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel(const AttendParams p) {
     constexpr int NB = D / 32, NST = stages_of<D>(), BYTES = 36 * D, kTurnBytes = turn_bytes(D, NT);
     extern __shared__ __align__(128) uint8_t smem[];
@@ -971,7 +1005,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int2 *prefix = reinterpret_cast<int2 *>(smem + kWarps * (NST * BYTES + kTurnBytes));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    tile_prefix<WIN>(p, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int rb = blockIdx.x % p.row_blocks;
     const int w = (int)(blockIdx.x / p.row_blocks) * kWarps + warp;
@@ -985,16 +1019,16 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
     Stages<BYTES, NST> st;
     st.init(smem + warp * NST * BYTES, bars + warp * NST);
     uint32_t phases = 0;
-    Cursor ahead;
-    ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+    Cursor<WIN> ahead;
+    ahead.seek(p, prefix, u0, lg);
     Place at = ahead;
     const int units = (int)(u1 - u0);
     int fetched = 0;
 #pragma unroll
     for (int i = 0; i < NST; ++i) {
         if (fetched < units) {
-            st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
-            ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            st.fetch(i, ahead.tile(p, lg, BYTES));
+            ahead.advance(p, prefix, lg);
             ++fetched;
         }
     }
@@ -1006,6 +1040,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
     float O[NT][NB][2][4], cs[NT][kSums][4], ref[NT], l[NT];
     bool fresh = true;
     int k_first = 0, len = 0;
+    Seen<WIN> seen;
     ScaleBound bound;
     int stage = 0, unit = 0;
     if (p.give_up) st.give_up(stage, phases);
@@ -1014,6 +1049,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
             typename Query<D, NT, HL>::Raw raw;
             raw.load(p, at.s, at.h, rho0);  // the tiles' copies are under way
             len = seq_len(p.pool, p.lens, p.table_width, at.s);
+            if constexpr (WIN) seen = Seen<WIN>(p, len);
             q.form(p, raw, rho0);
             k_first = at.k;
             bound.reset();
@@ -1041,7 +1077,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
             // the turned scores (1 KB per 8 rows) take the place of the K codes that are read first, where those are as
             // many bytes (8 D), else an area of their own
             float *turned = reinterpret_cast<float *>(kTurnBytes ? smem + kWarps * NST * BYTES + warp * kTurnBytes : const_cast<uint8_t *>(tile));
-            const int in_tile = len - at.k * kTile;  // tokens of the sequence from this tile on
+            const int in_tile = len - seen.at(at.k) * kTile;  // tokens of the sequence from this tile on
             // Scores, 16 tokens at a time, into the turned tile.  (With 16 rows a pass the loops over the halves stay
             // rolled: unrolled, the live values exceed the registers, 237 against 175 us.)
             constexpr int kUnroll = NT == 1 ? 2 : 1;
@@ -1061,6 +1097,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
             __syncwarp();
             // row g, tokens 16 c + 4 t + (0 .. 3), not yet times fac; -inf for those the row does not see
             const bool masked = in_tile - (p.R - 1) < kTile;
+            // the last row's window begins behind this tile's first token, and not all of it is of the first that stay
+            const bool behind = WIN && in_tile > p.window && len - in_tile + kTile > p.sinks;
             auto row_scores = [&](int n, int c, float *x) {
                 const float4 v = *reinterpret_cast<const float4 *>(turned + n * 256 + g * 32 + (((4 * c + t) ^ turn(g)) << 2));
                 x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -1069,6 +1107,15 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (i >= see) x[i] = -INFINITY;
+                }
+                if constexpr (WIN) {
+                    if (behind) {
+                        const int at0 = 16 * c + 4 * t, from = in_tile - p.R + (rho0 + 8 * n + g) / p.G + 1 - p.window - at0;
+                        const int stay = p.sinks - (len - in_tile) - at0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < from && i >= stay) x[i] = -INFINITY;
+                    }
                 }
             };
             if (bound.over == ~0u) {  // the head's first tile sets the bound
@@ -1205,8 +1252,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
         __syncwarp();
         const bool last_of_head = at.k + 1 == at.T;
         if (fetched < units) {
-            st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, BYTES));
-            ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+            st.fetch(stage, ahead.tile(p, lg, BYTES));
+            ahead.advance(p, prefix, lg);
             ++fetched;
         }
         stage = stage + 1 == NST ? 0 : stage + 1;
@@ -1267,8 +1314,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
         st.drain(stage, fetched - unit, phases);
         for (int i = lane; i < 2 * 8 * NT; i += 32)
             p.part_rl[((int64_t)rb * p.workers + w) * 2 * (8 * NT) + i] = make_float2(0.f, __int_as_float(0x7fc00000));  // (the sum: NaN)
-        Cursor c;
-        c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+        Cursor<WIN> c;
+        c.seek(p, prefix, u0, lg);
         for (int x = 0; x < units; ++x) {
             if (c.k == 0 && x + c.T <= units)
                 for (int rho = rho0; rho < rho0 + 8 * NT && rho < p.R * p.G; ++rho) {
@@ -1287,7 +1334,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_ctas(D, NT)) attend_kernel
 // written here.
 constexpr int kJoinVecs = 4;    // of the 2 D / 32 vectors of a partial: 64 dims
 constexpr int kJoinAtOnce = 4;  // partials a warp has on their way
-template <int D, int kJoinWarps>
+template <int D, int kJoinWarps, bool WIN>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendParams p, int nt) {
     constexpr int kVec = 2 * D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -1295,7 +1342,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const AttendPa
     __shared__ float sums[kJoinWarps][8], refs[8];
     int2 *prefix = reinterpret_cast<int2 *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    tile_prefix<WIN>(p, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int rows = p.R * p.G, groups = (rows + 7) / 8, v0 = blockIdx.y * kJoinVecs, d0 = v0 * 16;
     const int grp = blockIdx.x % groups, h = blockIdx.x / groups % p.pool.Hk, s = blockIdx.x / groups / p.pool.Hk;
@@ -1433,7 +1480,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
         weights_rest(wp, (int)blockIdx.x - wp.main_ctas);
         return;
     }
-    tile_prefix(p.pool, p.lens, p.table_width, p.n_seq, prefix);
+    tile_prefix(p, prefix);
     const Cut cut(prefix, p.n_seq, p.pool.Hk, p.workers);
     const int w = (int)blockIdx.x * kWarps + warp;
     if (w >= (int)cut.W) return;
@@ -1446,16 +1493,16 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
     uint32_t phases = 0;
     Query<D, NT, HL> q;
     for (int rho0 = 0; rho0 < p.R * p.G; rho0 += 8 * NT) {
-        Cursor ahead;
-        ahead.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+        Cursor<> ahead;
+        ahead.seek(p, prefix, u0, lg);
         Place at = ahead;
         const int units = (int)(u1 - u0);
         int fetched = 0;
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             if (fetched < units) {
-                st.fetch(i, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
-                ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                st.fetch(i, ahead.tile(p, lg, 36 * D));
+                ahead.advance(p, prefix, lg);
                 ++fetched;
             }
         }
@@ -1526,8 +1573,8 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
             }
             __syncwarp();
             if (fetched < units) {
-                st.fetch(stage, ahead.tile(p.pool, p.table, p.table_width, lg, 36 * D));
-                ahead.advance(p.pool, prefix, p.table, p.table_width, p.n_seq, lg);
+                st.fetch(stage, ahead.tile(p, lg, 36 * D));
+                ahead.advance(p, prefix, lg);
                 ++fetched;
             }
             if (at.k + 1 == at.T) fresh = true;
@@ -1536,8 +1583,8 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm<D, NT, HL>())
         }
         if (st.gave_up) {  // every token of this worker's range is NaN, the entries past a sequence's length are prev's
             st.drain(stage, fetched - unit, phases);
-            Cursor c;
-            c.seek(p.pool, prefix, p.table, p.table_width, p.n_seq, u0, lg);
+            Cursor<> c;
+            c.seek(p, prefix, u0, lg);
             for (int x = 0; x < units; ++x) {
                 const int64_t pos = (int64_t)c.k * kTile + lane, o = ((int64_t)c.s * p.pool.Hk + c.h) * wp.width + pos;
                 if (pos < wp.width)
@@ -1751,16 +1798,11 @@ extern "C" kvs_status kvs_q4_read(const kvs_q4_pool *pool, const int64_t *slots,
     return ce == cudaSuccess ? KVS_OK : cuda_failed("read launch", ce);
 }
 
-extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
-                                    uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
-                                    uint64_t q_stride, float scale, void *out, float *lse, void *workspace,
-                                    uint64_t workspace_bytes, void *stream) {
-    AttendParams p = {};
-    kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p);
-    if (s != KVS_OK) return s;
-    if (n_seq == 0) return KVS_OK;
-    if (!out || !aligned(out, 16)) return bad(KVS_ERR_INVALID, "out null or not 16-byte aligned");
-    const uint32_t D = pool->head_dim;
+template <bool WIN>
+static kvs_status attend_call(const kvs_q4_pool *pool, AttendParams &p, void *out, float *lse, void *workspace, uint64_t workspace_bytes,
+                              void *stream) {
+    const uint32_t D = pool->head_dim, n_seq = (uint32_t)p.n_seq, n_rows = (uint32_t)p.R;
+    const int32_t dtype = p.dtype;
     const uint64_t need = workspace_of(shape_of(D, n_rows * p.G, dtype, kSmsAssumed), D);
     if (!workspace || !aligned(workspace, 256)) return bad(KVS_ERR_INVALID, "workspace null or not 256-byte aligned");
     if (workspace_bytes < need) return bad(KVS_ERR_CAPACITY, "workspace smaller than kvs_q4_query_sizes asks for");
@@ -1774,9 +1816,9 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     p.part_o = static_cast<float *>(workspace);
     p.part_rl = reinterpret_cast<float2 *>(p.part_o + (uint64_t)sh.row_blocks * sh.workers * 2 * 8 * sh.nt * D);
     void (*k)(AttendParams) = nullptr;
-    if (D == 64) k = sh.hl ? attend_kernel<64, 1, true> : sh.nt == 2 ? attend_kernel<64, 2, false> : attend_kernel<64, 1, false>;
-    if (D == 128) k = sh.hl ? attend_kernel<128, 1, true> : sh.nt == 2 ? attend_kernel<128, 2, false> : attend_kernel<128, 1, false>;
-    if (D == 256) k = sh.hl ? attend_kernel<256, 1, true> : attend_kernel<256, 1, false>;
+    if (D == 64) k = sh.hl ? attend_kernel<64, 1, true, WIN> : sh.nt == 2 ? attend_kernel<64, 2, false, WIN> : attend_kernel<64, 1, false, WIN>;
+    if (D == 128) k = sh.hl ? attend_kernel<128, 1, true, WIN> : sh.nt == 2 ? attend_kernel<128, 2, false, WIN> : attend_kernel<128, 1, false, WIN>;
+    if (D == 256) k = sh.hl ? attend_kernel<256, 1, true, WIN> : attend_kernel<256, 1, false, WIN>;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch(k, dim3(sh.ctas), kWarps * 32, smem_of(D, 36 * (int)D, turn_bytes((int)D, sh.nt), n_seq), st, false, p);
     if (e != cudaSuccess) return cuda_failed("attention launch", e);
@@ -1784,10 +1826,39 @@ extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *tabl
     // warps), 4 in a batch, where a head has a handful of them (32 sequences: 90.8 us, 96.7 with 16)
     const uint64_t groups = (uint64_t)n_seq * pool->n_kv_head * ((n_rows * p.G + 7) / 8);
     const bool few = groups * (D / 64) < (uint64_t)sms;
-    void (*c)(AttendParams, int) = few ? (D == 64 ? combine_kernel<64, 16> : D == 128 ? combine_kernel<128, 16> : combine_kernel<256, 16>)
-                                       : (D == 64 ? combine_kernel<64, 4> : D == 128 ? combine_kernel<128, 4> : combine_kernel<256, 4>);
+    void (*c)(AttendParams, int) = few ? (D == 64 ? combine_kernel<64, 16, WIN> : D == 128 ? combine_kernel<128, 16, WIN> : combine_kernel<256, 16, WIN>)
+                                       : (D == 64 ? combine_kernel<64, 4, WIN> : D == 128 ? combine_kernel<128, 4, WIN> : combine_kernel<256, 4, WIN>);
     e = launch(c, dim3((unsigned)groups, D / 64), few ? 512 : 128, ((int)n_seq + 1) * 8, st, true, p, sh.nt);
     return e == cudaSuccess ? KVS_OK : cuda_failed("combine launch", e);
+}
+
+extern "C" kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                    uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                                    uint64_t q_stride, float scale, void *out, float *lse, void *workspace,
+                                    uint64_t workspace_bytes, void *stream) {
+    AttendParams p = {};
+    kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p);
+    if (s != KVS_OK) return s;
+    if (n_seq == 0) return KVS_OK;
+    if (!out || !aligned(out, 16)) return bad(KVS_ERR_INVALID, "out null or not 16-byte aligned");
+    return attend_call<false>(pool, p, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" kvs_status kvs_q4_attend_window(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                           uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                                           uint64_t q_stride, float scale, uint32_t window, uint32_t sinks, void *out, float *lse,
+                                           void *workspace, uint64_t workspace_bytes, void *stream) {
+    AttendParams p = {};
+    kvs_status s = fill_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, &p);
+    if (s != KVS_OK) return s;
+    if (window > 0x7fffffffu || sinks > 0x7fffffffu - 64u) return bad(KVS_ERR_INVALID, "window must be at most 2^31 - 1, sinks 2^31 - 65");
+    if (n_seq == 0) return KVS_OK;
+    if (!out || !aligned(out, 16)) return bad(KVS_ERR_INVALID, "out null or not 16-byte aligned");
+    if (window == 0 || window >= (uint64_t)table_width * pool->page_tokens)  // every token is inside
+        return attend_call<false>(pool, p, out, lse, workspace, workspace_bytes, stream);
+    p.window = (int)window;
+    p.sinks = (int)sinks;
+    return attend_call<true>(pool, p, out, lse, workspace, workspace_bytes, stream);
 }
 
 extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,

@@ -180,6 +180,7 @@ SIGNATURES = {
                                   _P, _P, _P], _I32),
     "kvs_policy_step": ([_P, _P, _P, _P, _P], _I32),
     "kvs_prompt_attend": ([_P, _P, _U64, _P, _P], _I32),
+    "kvs_prompt_attend_window": ([_P, _U32, _U32, _P, _U64, _P, _P], _I32),
     "kvs_prompt_weights": ([_P, _P, _U32, _P, _P, _U64, _P], _I32),
     "kvs_q4_query_sizes": ([_P, _U32, _U32, _I32, _P, _P], _I32),
     "kvs_q4_append": ([_P, _P, _U64, _P, _P, _I32, _U64, _U64, _P], _I32),
@@ -188,6 +189,7 @@ SIGNATURES = {
     "kvs_q4_attend_chunk": ([_P, _P, _U32, _P, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _U32, _U32, _P, _U64, _P, _P, _U64,
                              _P], _I32),
     "kvs_q4_attend": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
+    "kvs_q4_attend_window": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _U32, _U32, _P, _P, _P, _U64, _P], _I32),
     "kvs_q4_weights": ([_P, _P, _U32, _P, _U32, _U32, _U32, _P, _I32, _U64, _F32, _P, _P, _P, _U64, _P], _I32),
     "kvs_q4_evict": ([_P, _P, _U32, _P, _U32, _P, _U32, _P, _U64, _U32, _U32, _U32, _P, _P, _P, _P], _I32),
 }
@@ -421,6 +423,11 @@ def kvs_prompt_attend(prompt: kvs_prompt, out, out_stride, lse=None, stream=0) -
     return _check(None, load().kvs_prompt_attend(ctypes.byref(prompt), _ptr(out), out_stride, _ptr(lse), stream))
 
 
+def kvs_prompt_attend_window(prompt: kvs_prompt, window, sinks, out, out_stride, lse=None, stream=0) -> int:
+    return _check(None, load().kvs_prompt_attend_window(ctypes.byref(prompt), window, sinks, _ptr(out), out_stride, _ptr(lse),
+                                                        stream))
+
+
 def kvs_prompt_weights(prompt: kvs_prompt, lse, last_rows, prev, weights, width, stream=0) -> int:
     return _check(None, load().kvs_prompt_weights(ctypes.byref(prompt), _ptr(lse), last_rows, _ptr(prev),
                                                   _ptr(weights), width, stream))
@@ -448,6 +455,13 @@ def kvs_q4_attend(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dt
     return _check(None, load().kvs_q4_attend(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), n_seq, n_rows,
                                              n_q_head, _ptr(q), dtype, q_stride, scale, _ptr(out), _ptr(lse),
                                              _ptr(workspace), workspace_bytes, stream))
+
+
+def kvs_q4_attend_window(pool, table, table_width, lens, n_seq, n_rows, n_q_head, q, dtype, q_stride, scale, window, sinks,
+                         out, lse, workspace, workspace_bytes, stream=0) -> int:
+    return _check(None, load().kvs_q4_attend_window(ctypes.byref(pool), _ptr(table), table_width, _ptr(lens), n_seq, n_rows,
+                                                    n_q_head, _ptr(q), dtype, q_stride, scale, window, sinks, _ptr(out),
+                                                    _ptr(lse), _ptr(workspace), workspace_bytes, stream))
 
 
 def kvs_q4_chunk_workspace(pool: kvs_q4_pool) -> int:
@@ -832,11 +846,12 @@ def _prompt(q, k, v, cu, scale) -> kvs_prompt:
                       ks[1], qs[2], _dtype_of(q), qs[2] ** -0.5 if scale is None else scale)
 
 
-def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
+def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None, window=0, sinks=0):
     """Causal attention of packed prompts over themselves (kvs_prompt_attend): (out, lse).
 
     q [rows][Hq][D], k and v [rows][Hk][D] in float16 or bfloat16 (rows may be strided), cu int32 [n + 1]: prompt i is
-    rows cu[i] .. cu[i + 1] - 1.  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
+    rows cu[i] .. cu[i + 1] - 1.  With window > 0 a row sees the last window keys up to its own and the first sinks keys
+    of its prompt (kvs_prompt_attend_window).  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
     (undefined where those are allocated here).  The results carry no gradient.
     """
     p = _prompt(q, k, v, cu, scale)
@@ -852,7 +867,11 @@ def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None):
         lse = _torch.empty(shape[:2], dtype=_torch.float32, device=q.device)
     else:
         _need(lse, "lse", _torch.float32, q.device, shape[:2])
-    _run(q.device, load().kvs_prompt_attend, ctypes.byref(p), out.data_ptr(), stride, lse.data_ptr())
+    if window or sinks:
+        window, sinks = _window(window, sinks)
+        _run(q.device, load().kvs_prompt_attend_window, ctypes.byref(p), window, sinks, out.data_ptr(), stride, lse.data_ptr())
+    else:
+        _run(q.device, load().kvs_prompt_attend, ctypes.byref(p), out.data_ptr(), stride, lse.data_ptr())
     return out, lse
 
 
@@ -935,10 +954,11 @@ class Q4Cache:
         _need_rows(lens, "lens", i32, dev, n, 1)
         return _dtype_of(q), _row_stride(q, "q")
 
-    def attend(self, table, lens, q, scale=None, out=None, lse=None):
+    def attend(self, table, lens, q, scale=None, out=None, lse=None, window=0, sinks=0):
         """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens.
 
-        out may be q.  The results carry no gradient.
+        With window > 0 a row sees the last window tokens up to its own and the first sinks tokens of its sequence
+        (kvs_q4_attend_window).  out may be q.  The results carry no gradient.
         """
         dt, stride = self._batch(table, lens, q)
         shape = q.shape
@@ -955,6 +975,12 @@ class Q4Cache:
         if need is None:
             need = self._need_bytes[(rows, hq, dt)] = kvs_q4_query_sizes(self.pool, rows, hq, dt)[1]
         ws = self._workspace(need)
+        if window or sinks:
+            window, sinks = _window(window, sinks)
+            _run(self.device, self._lib.kvs_q4_attend_window, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows,
+                 hq, q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), lse.data_ptr(),
+                 ws.data_ptr(), need)
+            return out, lse
         _run(self.device, self._lib.kvs_q4_attend, self._ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n, rows, hq,
              q.data_ptr(), dt, stride, d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), need)
         return out, lse

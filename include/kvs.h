@@ -786,6 +786,14 @@ typedef struct {
 kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride, float *lse, void *stream);
 
 /*
+ * kvs_prompt_attend_window -- kvs_prompt_attend where a row sees, of the keys
+ * up to its own, the last `window` (its own among them) and the first `sinks`
+ * of its prompt; window 0: all of them.  lse is over what the row sees.
+ */
+kvs_status kvs_prompt_attend_window(const kvs_prompt *p, uint32_t window, uint32_t sinks, void *out, uint64_t out_stride,
+                                    float *lse, void *stream);
+
+/*
  * kvs_prompt_weights -- the attention weight each key of each prompt received:
  *   w[i][g][j] = prev[i][g][j] + sum over rows r >= j and query heads h of kv
  *                head g of exp(scale q_rh . k_jg - lse_rh)
@@ -871,6 +879,17 @@ kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t
                          uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
                          uint64_t q_stride, float scale, void *out, float *lse, void *workspace,
                          uint64_t workspace_bytes, void *stream);
+
+/*
+ * kvs_q4_attend_window -- kvs_q4_attend where a row sees, of the tokens up to
+ * its own, the last `window` (its own among them) and the first `sinks`;
+ * window 0: all of them.  Pages that hold no token that a row sees are not
+ * read (their numbers may be anything).
+ */
+kvs_status kvs_q4_attend_window(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
+                                uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
+                                uint64_t q_stride, float scale, uint32_t window, uint32_t sinks, void *out, float *lse,
+                                void *workspace, uint64_t workspace_bytes, void *stream);
 
 /*
  * kvs_q4_attend_chunk -- attention of chunks of new rows, packed one after
