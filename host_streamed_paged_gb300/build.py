@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvs.so")
 SOURCES = ["kvs_decode.cu", "kvs_prefill.cu", "kvs_copy.cu", "kvs_noalloc.cu", "kvs_prompt.cu", "kvs_q4.cu", "kvs_chunk.cu",
-           "kvs_evict.cu", "kvs_runtime.cpp", "kvs_policy.cpp"]
+           "kvs_evict.cu", "kvs_rotary.cu", "kvs_runtime.cpp", "kvs_policy.cpp"]
 HEADERS = [os.path.join(CSRC, "kvs_internal.h"), os.path.join(CSRC, "kvs_tcgen05.cuh"),
            os.path.join(ROOT, "include", "kvs.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -133,6 +133,27 @@ class kvs_prompt(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class kvs_rotary(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("head_dim", ctypes.c_uint32),
+        ("rot_dim", ctypes.c_uint32),
+        ("interleaved", ctypes.c_int32),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class kvs_head_rows(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("x_stride", ctypes.c_uint64),
+        ("y_stride", ctypes.c_uint64),
+        ("n_head", ctypes.c_uint32),
+        ("weight", ctypes.c_void_p),
+    ]
+
+
 class kvs_q4_pool(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_uint64), ("page_tokens", ctypes.c_uint32),
                 ("n_kv_head", ctypes.c_uint32), ("head_dim", ctypes.c_uint32)]
@@ -182,6 +203,8 @@ SIGNATURES = {
     "kvs_prompt_attend": ([_P, _P, _U64, _P, _P], _I32),
     "kvs_prompt_attend_window": ([_P, _U32, _U32, _P, _U64, _P, _P], _I32),
     "kvs_prompt_weights": ([_P, _P, _U32, _P, _P, _U64, _P], _I32),
+    "kvs_rotate": ([_P, _P, _U32, _U64, _I32, _P, _P, _P], _I32),
+    "kvs_norm_rotate": ([_P, _P, _U32, _U64, _I32, _P, _P, _I32, _F32, _P], _I32),
     "kvs_q4_query_sizes": ([_P, _U32, _U32, _I32, _P, _P], _I32),
     "kvs_q4_append": ([_P, _P, _U64, _P, _P, _I32, _U64, _U64, _P], _I32),
     "kvs_q4_read": ([_P, _P, _U64, _P, _P, _I32, _P], _I32),
@@ -431,6 +454,19 @@ def kvs_prompt_attend_window(prompt: kvs_prompt, window, sinks, out, out_stride,
 def kvs_prompt_weights(prompt: kvs_prompt, lse, last_rows, prev, weights, width, stream=0) -> int:
     return _check(None, load().kvs_prompt_weights(ctypes.byref(prompt), _ptr(lse), last_rows, _ptr(prev),
                                                   _ptr(weights), width, stream))
+
+
+def _ref_of(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def kvs_rotate(rotary: kvs_rotary, positions, position_bytes, n, dtype, q: kvs_head_rows, k=None, stream=0) -> int:
+    return _check(None, load().kvs_rotate(_ref_of(rotary), _ptr(positions), position_bytes, n, dtype, _ref_of(q), _ref_of(k), stream))
+
+
+def kvs_norm_rotate(rotary: kvs_rotary, positions, position_bytes, n, dtype, q: kvs_head_rows, k, weight_dtype, eps, stream=0) -> int:
+    return _check(None, load().kvs_norm_rotate(_ref_of(rotary), _ptr(positions), position_bytes, n, dtype, _ref_of(q), _ref_of(k),
+                                               weight_dtype, eps, stream))
 
 
 def kvs_q4_query_sizes(pool: kvs_q4_pool, n_rows=1, n_q_head=None, dtype=KVS_F32):
@@ -896,6 +932,134 @@ def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=No
     _run(dev, load().kvs_prompt_weights, ctypes.byref(p), lse.data_ptr(), min(int(window), _MOST),
          prev.data_ptr() if prev is not None else None, out.data_ptr(), shape[2])
     return out
+
+
+class Rotary:
+    """Rotary positions: a plan of frequencies on the device, and the calls that turn query and key rows by it
+    (kvs_rotate, kvs_norm_rotate).
+
+    Pair i of the head's first ``rot_dim`` dims (default: all; a multiple of 16) turns by position * f_i radians, f_i =
+    base^(-2 i / rot_dim).  Pairs are dims (i, i + rot_dim / 2), or with ``interleaved`` (2 i, 2 i + 1).  Scaled for
+    contexts ``factor`` times as long as ``context``, the one the frequencies were trained for, by ``scaling``:
+
+    - "linear": f_i / factor
+    - "ntk": a base of base * factor^(rot_dim / (rot_dim - 2)), which leaves the fastest pair and divides the slowest
+    - "yarn": f_i / factor where a pair makes less than ``slow`` turns in the context, f_i where more than ``fast``, a
+      ramp over the pairs between; values are multiplied by ``magnitude``, 0.1 ln(factor) + 1 unless given
+    - "bands": the same with the ramp over the turns themselves, from ``slow`` to ``fast``
+
+    (fast, slow: 32 and 1 for "yarn", 4 and 1 for "bands", unless given.)  ``freqs`` gives the f_i themselves instead.
+    """
+
+    def __init__(self, head_dim, rot_dim=None, base=10000.0, interleaved=False, scaling=None, factor=1.0, context=None, fast=None,
+                 slow=None, freqs=None, magnitude=None, device="cuda"):
+        torch = _t()
+        if freqs is not None:
+            if scaling is not None:
+                raise ValueError("freqs are taken as they are: scaling must be None")
+            rot = 2 * len(freqs)
+            if rot_dim is not None and rot_dim != rot:
+                raise ValueError("freqs must hold rot_dim / 2 numbers")
+            freqs = [float(f) for f in freqs]
+        else:
+            rot = head_dim if rot_dim is None else rot_dim
+            freqs, scale = _rotary_freqs(rot, float(base), scaling, float(factor), context, fast, slow)
+            magnitude = scale if magnitude is None else magnitude
+        if head_dim not in (64, 128, 256) or not 0 <= rot <= head_dim or rot % 16:
+            raise ValueError("head_dim must be 64, 128 or 256, rot_dim a multiple of 16 up to it")
+        if not all(math.isfinite(f) for f in freqs):
+            raise ValueError("frequencies must be finite")
+        magnitude = 1.0 if magnitude is None else float(magnitude)
+        if not math.isfinite(magnitude):
+            raise ValueError("magnitude must be finite")
+        turns = [int(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64)) % 2 ** 64 for f in freqs]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64).to(device)
+        self.freqs, self.magnitude, self.device = freqs, magnitude, self.turns.device
+        self.head_dim, self.rot_dim, self.interleaved = head_dim, rot, bool(interleaved)
+        self._plan = kvs_rotary(self.turns.data_ptr(), head_dim, rot, self.interleaved, magnitude)
+        self._ref, self._lib = ctypes.byref(self._plan), load()
+
+    def rotate(self, pos, q, k=None, out=None):
+        """Rows q [..., Hq, D] and k [..., Hk, D] (float32, float16 or bfloat16; rows may be strided) turned to pos [...]
+        (int32 or int64): (q', k'), new tensors or those of out = (q', k'), which may be q and k themselves.  k' is None
+        without k.  The results carry no gradient."""
+        n, dt, sides, outs = self._rows(pos, q, k, out, None, None)
+        _run(self.device, self._lib.kvs_rotate, self._ref, pos.data_ptr(), pos.element_size(), n, dt, *sides)
+        return outs
+
+    def norm_rotate(self, pos, q, k=None, q_weight=None, k_weight=None, eps=1e-6, out=None):
+        """The same after the norm of every head, x / sqrt(mean(x^2) + eps) * weight: weights [D], None for ones."""
+        n, dt, sides, outs = self._rows(pos, q, k, out, q_weight, k_weight)
+        w = q_weight if q_weight is not None else k_weight
+        _run(self.device, self._lib.kvs_norm_rotate, self._ref, pos.data_ptr(), pos.element_size(), n, dt, *sides,
+             KVS_F32 if w is None else _dtype_of(w), eps)
+        return outs
+
+    def _rows(self, pos, q, k, out, q_weight, k_weight):
+        dev, d, lead = self.device, self.head_dim, pos.shape
+        if pos.dtype not in (_torch.int32, _torch.int64) or pos.device != dev or not pos.is_contiguous() or not 1 <= len(lead) <= 2:
+            raise ValueError(f"pos must be a contiguous int32 or int64 tensor on {dev}, of one or two dimensions")
+        if out is not None and len(out) != 2:
+            raise ValueError("out must be (q', k')")
+        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError("q_weight and k_weight must have one dtype")
+        dt, refs, outs = _dtype_of(q), [], []
+        for i, (x, w) in enumerate(((q, q_weight), (k, k_weight))):
+            if x is None:
+                if out is not None and out[i] is not None:
+                    raise ValueError("out has a tensor for rows that are not given")
+                refs.append(None)
+                outs.append(None)
+                continue
+            shape = x.shape
+            if shape[:-2] != lead or len(shape) != len(lead) + 2 or shape[-1] != d or x.dtype != q.dtype or x.device != dev:
+                raise ValueError("q and k must be [..., heads, head_dim] of one dtype on the plan's device, pos their leading sizes")
+            if w is not None:
+                _need(w, "weight", w.dtype, dev, (d,))
+                _dtype_of(w)
+            if out is None:
+                y = _torch.empty(shape, dtype=x.dtype, device=dev)
+                y_stride = shape[-2] * d
+            else:
+                y = out[i]
+                if y is None or y.shape != shape or y.dtype != x.dtype or y.device != dev:
+                    raise ValueError("out must be as q and k")
+                y_stride = _row_stride(y, "out")
+            refs.append(ctypes.byref(kvs_head_rows(x.data_ptr(), y.data_ptr(), _row_stride(x, "k" if i else "q"), y_stride, shape[-2],
+                                                   w.data_ptr() if w is not None else None)))
+            outs.append(y)
+        return pos.numel(), dt, refs, tuple(outs)
+
+
+def _rotary_freqs(rot, base, scaling, factor, context, fast, slow):
+    """(f_i, magnitude) of Rotary's scalings, in 64 bits."""
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive")
+    if scaling not in (None, "linear", "ntk", "yarn", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "ntk" and rot > 2:
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling not in ("yarn", "bands"):
+        return f, 1.0
+    if context is None or not context > 0:
+        raise ValueError(f"{scaling!r} needs the context that the frequencies were trained for")
+    fast, slow = (32.0 if scaling == "yarn" else 4.0) if fast is None else fast, 1.0 if slow is None else slow
+    if not fast > slow > 0:
+        raise ValueError("need fast > slow > 0")
+    if scaling == "bands":
+        keep = [min(max((context * x / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for x in f]
+        return [x * k + x / factor * (1 - k) for x, k in zip(f, keep)], 1.0
+    if base == 1.0:
+        raise ValueError("'yarn' needs a base other than 1")
+    # the pairs that make so many turns in the context, rounded outwards: between them the ramp
+    low, high = (rot * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (fast, slow))
+    low, high = max(math.floor(low), 0), min(math.ceil(high), rot - 1)
+    span = max(high - low, 0.001)
+    far = [min(max((i - low) / span, 0.0), 1.0) for i in range(rot // 2)]
+    return [x / factor * r + x * (1 - r) for x, r in zip(f, far)], 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
 
 
 class Q4Cache:

@@ -72,7 +72,7 @@ typedef enum {
 /* Block types, numbered as the ggml type ids of the same formats. */
 typedef enum { KVS_TYPE_Q4_0 = 2, KVS_TYPE_Q8_0 = 8 } kvs_qtype;
 /* Element types.  kvs_attend takes KVS_F32 and KVS_F16 queries; the batch
- * operators (kvs_prompt_*, kvs_q4_*) state theirs. */
+ * operators (kvs_prompt_*, kvs_q4_*, kvs_rotate) state theirs. */
 typedef enum { KVS_F32 = 0, KVS_F16 = 1, KVS_BF16 = 2 } kvs_dtype;
 
 /* kvs_config.flags */
@@ -806,6 +806,51 @@ kvs_status kvs_prompt_attend_window(const kvs_prompt *p, uint32_t window, uint32
  */
 kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t last_rows, const float *prev,
                               float *weights, uint64_t width, void *stream);
+
+/*
+ * Rotary positions, for the query and key rows of a layer before they are
+ * attended with or cached.  Pair i of a head's first rot_dim dims is turned by
+ * the angle position * f_i and multiplied by magnitude:
+ *   (u, v) -> magnitude (u cos - v sin, v cos + u sin),
+ * where the pair is dims (i, i + rot_dim / 2), or with `interleaved` (2i, 2i +
+ * 1).  The other dims are copied.  turns[i] is f_i / (2 pi) * 2^64 modulo 2^64
+ * (frequencies as fractions of a turn per position): position * turns[i] modulo
+ * 2^64 is then the exact angle at any position, negative ones too.
+ */
+typedef struct {
+    const uint64_t *turns; /* device [rot_dim / 2] */
+    uint32_t head_dim;
+    uint32_t rot_dim;      /* a multiple of 16, 0 .. head_dim */
+    int32_t interleaved;
+    float magnitude;       /* finite; 1 where frequencies are not scaled */
+} kvs_rotary;
+
+/* Rows of heads: x and y (device, 16-byte aligned) are [n][n_head][D], rows
+ * x_stride / y_stride elements apart (a row starts on a 16-byte boundary).  y
+ * may be x with the same stride, and overlaps it nowhere else. */
+typedef struct {
+    const void *x;
+    void *y;
+    uint64_t x_stride, y_stride;
+    uint32_t n_head;
+    const void *weight;    /* kvs_norm_rotate: device [D], 16-byte aligned; null: ones */
+} kvs_head_rows;
+
+/*
+ * kvs_rotate -- turn n rows of queries and (k nullable) keys, of type dtype
+ * (KVS_F32, KVS_F16 or KVS_BF16), at positions[i] (device int32 or int64, of
+ * position_bytes 4 or 8).  Computed in fp32, rounded once.
+ */
+kvs_status kvs_rotate(const kvs_rotary *r, const void *positions, uint32_t position_bytes, uint64_t n, int32_t dtype,
+                      const kvs_head_rows *q, const kvs_head_rows *k, void *stream);
+
+/*
+ * kvs_norm_rotate -- the same after a norm of every head: x / sqrt(mean(x^2) +
+ * eps) * weight, over all D dims, weights of type weight_dtype; one pass over
+ * the rows, rounded once.  eps >= 0 (0 makes a head of zeros NaN).
+ */
+kvs_status kvs_norm_rotate(const kvs_rotary *r, const void *positions, uint32_t position_bytes, uint64_t n, int32_t dtype,
+                           const kvs_head_rows *q, const kvs_head_rows *k, int32_t weight_dtype, float eps, void *stream);
 
 /*
  * The 4-bit page cache.  K and V are both Q4_0 (32-dim blocks, fp16 scale, the
