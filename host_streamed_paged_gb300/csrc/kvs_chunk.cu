@@ -122,6 +122,7 @@ struct Piece {
     int lo, hi, nblk, first, front;  // block b is keys 64 b .. for b < front, then 64 (first + b - front) ..
     int s, h, begin, n, T, x;
     int begun;  // by another worker (o1 > 0)
+    int from;   // the first row's window begins here: tokens before it, but for the first `sinks`, no row of the unit sees
 };
 
 struct Line {
@@ -164,11 +165,12 @@ struct Line {
         const int64_t c = q.cost(x), o1 = pos - ustart, o2 = c < end - ustart ? c : end - ustart;
         const int r0 = x * q.TU, r1 = r0 + q.TU < q.n ? r0 + q.TU : q.n;
         const int64_t last = q.pos0 + r1 - 1;
-        int nblk = 0, first = 0, front = 0;
+        int nblk = 0, first = 0, front = 0, from = 0;
         if (last >= 0) {
             const int64_t p0 = q.pos0 + r0 < 0 ? 0 : q.pos0 + r0;
             if (p.window && p0 >= p.window) {
-                first = (int)((p0 - p.window + 1) / BN);
+                from = (int)(p0 - p.window + 1);
+                first = from / BN;
                 front = (p.sinks + BN - 1) / BN;
                 front = front < first ? front : first;
             }
@@ -182,6 +184,7 @@ struct Line {
         o->front = front;
         o->kind = o->hi > o->lo ? 2 : (nblk == 0 && o1 == 0 ? 1 : 0);
         o->begun = o1 > 0;
+        o->from = from;
         o->s = s;
         o->h = h;
         o->x = x;
@@ -443,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         while (ok && next_piece()) {
             if (piece->kind != 2) continue;
             const int lo = piece->lo, n = piece->hi - lo, front = piece->front, first = piece->first, T = piece->T, h = piece->h;
+            const int from = piece->from;
             const int32_t *table = p.table + (int64_t)piece->s * p.table_width;
             int page_base = -32, page = -1;
             // tile of block j's group: its bytes (null: a page outside the pool), tokens from the group's first on
@@ -454,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const int b = lo + j, kt = 2 * (b < front ? b : first + b - front) + (grp >> 1);
                 Where w;
                 w.left = T - kt * 32 - 16 * c;
+                if ((kt + 1) * 32 <= from && kt * 32 >= p.sinks) w.left = 0;  // no row sees it: its page may be gone
                 w.at = nullptr;
                 if (w.left > 0) {
                     const int pg = kt >> lg;

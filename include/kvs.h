@@ -949,8 +949,9 @@ kvs_status kvs_q4_attend_window(const kvs_q4_pool *pool, const int32_t *table, u
  * q (with its stride), else overlaps it nowhere.  lse (nullable): device fp32
  * [total_rows][n_q_head].  Rows of no sequence are left as they were.  A row at
  * a negative position (T < n) sees nothing: out 0, lse -inf.  Any finite scale
- * is taken.  A page number outside the pool makes the outputs of the rows that
- * see it NaN (it may those of other rows of its sequence).
+ * is taken.  Pages that hold no token that a row sees are not read; a page
+ * number outside the pool makes the outputs of the rows that see one of its
+ * tokens NaN (it may those of other rows of its sequence).
  * K and V enter the tensor cores as f16 values rounded once, whatever their
  * scale, queries as in kvs_q4_attend, weights as f16; sums are fp32.  So lse
  * carries the rounding of K: up to 2^-11 |scale| sum |q k| for a row's largest
