@@ -13,7 +13,7 @@
 // Where a cut falls inside a unit its pieces leave partials (O, reference
 // exponent, sum), at most two per CTA, which a second kernel joins in order.
 //
-// Roles (512 threads):
+// Roles:
 //   softmax warps, one thread a row: load the unit's queries, then turn each
 //     block's scores S in tensor memory into weights P over them, O rescaled
 //     only when a row's maximum grew by more than 2^8;
@@ -23,8 +23,8 @@
 //
 // Values.  A cached value is (n - 8) * scale.  The tensor core takes K and V as
 // f16 values rounded once, each group of 16 tokens brought to a common power of
-// two (its largest scale to 2 .. 4) so that any scale the cache holds keeps
-// f16's precision; the power of two returns in the softmax, K's on the scores
+// two, so that any scale the cache holds keeps f16's precision (down to 2^-12 of
+// what the group's largest scale reaches, and 2^-23 of it below); the power of two returns in the softmax, K's on the scores
 // and V's on the weights before those are rounded to f16.  Queries enter as f16
 // times a power of two per row (exact down to 2^-28 of the row's largest).
 #include <cuda_bf16.h>
@@ -43,7 +43,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
 constexpr int kMaxSeq = 4096;
 constexpr int kMaxGroup = 64;
 constexpr int kWorkers = 152;  // sizes the workspace; a launch has no more CTAs
@@ -209,7 +208,13 @@ struct Line {
     }
 };
 
+struct Walk {
+    Line line;
+    Piece piece;
+};
+
 // prefix[s] = cost of the sequences before s; every thread calls it
+template <int kThreads>
 __device__ void line_prefix(const ChunkParams &p, int tile_tokens, int tiles, int64_t *prefix) {
     __shared__ int64_t warp_sum[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -245,19 +250,17 @@ __device__ void line_prefix(const ChunkParams &p, int tile_tokens, int tiles, in
 
 // ---------------------------------------------------------------- values
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// a nibble pair in place as f16 n - 8 (low nibbles of the bytes), 16 (n - 8) (high ones): under exponent 0x64 it is 1024 + n
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u); }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return hsub2((w & 0x00f000f0u) | 0x64006400u, 0x64806480u); }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) { return w & 0x00f000f0u; }
 
 template <bool TRANS>
 __device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -269,11 +272,15 @@ __device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32
         asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                      : "memory");
 }
-// a word of codes in each lane, its elements' scales in s2: four 8 x 8 matrices
+// A word of codes in each lane, its elements' scales t (times a power of two, 4 at most) in s2: four 8 x 8 matrices of
+// (n - 8) t 2^-7.  A nibble ANDed out at bits 4 .. 7 and read as f16 is the subnormal n 2^-20, exactly; one fused multiply-add
+// makes the value of it, rounded once: n 2^-20 * (t 2^13) - t 2^-4.  (Values below 2^-12 of the largest a group may hold are
+// subnormal: off by 2^-23 of it.)
 template <bool TRANS>
 __device__ __forceinline__ void store_word(uint32_t addr, uint32_t w, uint32_t s2) {
-    const uint32_t x = w >> 8, s16 = hmul2(s2, 0x2c002c00u);  // s / 16, for 16 (n - 8)
-    store_matrices<TRANS>(addr, hmul2(low_codes(w), s2), hmul2(low_codes(x), s2), hmul2(high_codes(w), s16), hmul2(high_codes(x), s16));
+    const uint32_t up = hmul2(s2, 0x70007000u), off = hmul2(s2, 0xac00ac00u);  // 2^13, -2^-4
+    store_matrices<TRANS>(addr, hfma2(nibbles(w << 4), up, off), hfma2(nibbles(w >> 4), up, off), hfma2(nibbles(w), up, off),
+                          hfma2(nibbles(w >> 8), up, off));
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -283,25 +290,28 @@ struct ChunkShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;         // query tiles of a CTA
     static constexpr bool kQInTmem = D != 128;          // the queries as the tensor-memory A operand, where there is room
     static constexpr int NB = D / 32;
-    static constexpr int kHalves = D == 256 ? 2 : 1;    // warps that share a group of 16 tokens
-    static constexpr int kBlocks = NB / kHalves;        // 32-dim blocks of a warp
-    static constexpr int kDeqWarps = 4 * kHalves, kFirstDeq = 4 * NQ, kFirstMma = 12;
-    static constexpr int kVecs = D == 64 ? 1 : 2;       // 16-byte words of codes of a lane
-    static constexpr int kKScales = D == 256 ? 2 : 1, kVScales = D / 64;  // 16-byte words of scales
+    // warpgroups: softmax (one a tile), two that dequantise, one whose first warps issue the MMAs
+    static constexpr int kThreads = 128 * (NQ + 3);
+    static constexpr int kDeqWarps = 8, kFirstDeq = 4 * NQ, kFirstMma = kFirstDeq + kDeqWarps;
+    // of the registers of 640 threads at launch (96 each) the softmax takes what the others leave
+    static constexpr bool kSplitRegs = NQ == 2;
+    static constexpr int kSoftmaxRegs = 136, kDeqRegs = 72, kMmaRegs = 56;
+    static_assert(!kSplitRegs || 128 * (NQ * kSoftmaxRegs + 2 * kDeqRegs + kMmaRegs) <= kThreads * 96, "registers at launch");
+    static constexpr int kLines = D / 64;               // 16-byte words of codes of a lane: of 16 tokens, K or V
     static constexpr int kStage = BN * D * 2;
     static constexpr int kStages = D == 256 ? 6 : 8;
     static constexpr int kQBytes = kQInTmem ? 0 : kTileRows * D * 2;
     static constexpr int kOffRing = NQ * kQBytes;
     static constexpr int kOffFac = kOffRing + kStages * kStage;  // K factors, V exponents, V factors [kFacs][4]
     static constexpr int kOffPiece = kOffFac + 3 * kFacs * 16;
-    static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)((sizeof(Piece) + 15) / 16 * 16);
+    static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)sizeof(Walk);
     static constexpr int kSmem = kOffBar + 320 + 1024;
     static constexpr uint32_t kColO = 256, kColQ = D == 256 ? 128 : 384;
     static_assert(kStages * kStage >= (kMaxSeq + 1) * 8, "the line's prefix sums lie in the ring");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
     using S = ChunkShape<D>;
     constexpr int NQ = S::NQ, NST = S::kStages, NB = S::NB;
     extern __shared__ uint8_t smem_raw[];
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     if (tid == 32) {
         for (int s = 0; s < NST; ++s) {
-            mbar_init(b_full(s), S::kDeqWarps);
+            mbar_init(b_full(s), 4);
             mbar_init(b_empty(s), NQ);
         }
         for (int i = 0; i < 2; ++i) mbar_init(b_q(i), 4);
@@ -341,18 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     int64_t *prefix = reinterpret_cast<int64_t *>(smem + S::kOffRing);
-    line_prefix(p, TQ, NQ, prefix);
-    Line line;
-    const bool any = line.seek(p, prefix, blockIdx.x, TQ, NQ);
+    line_prefix<S::kThreads>(p, TQ, NQ, prefix);
+    // every warp walks the line by itself, its state in shared memory: lane 0 steps, the others read the piece
+    Walk *walk = reinterpret_cast<Walk *>(smem + S::kOffPiece) + warp;
+    bool any;
+    {
+        Line line;
+        any = line.seek(p, prefix, blockIdx.x, TQ, NQ);
+        if (lane == 0) walk->line = line;
+    }
     tc_before();
     __syncthreads();  // the prefix sums are read, the ring may be written
     tc_after();
     const uint32_t tmem = *tmem_slot;
-    Piece *piece = reinterpret_cast<Piece *>(smem + S::kOffPiece + warp * ((sizeof(Piece) + 15) / 16 * 16));
-    auto next_piece = [&] {  // every warp walks the line by itself; its lanes agree
+    const Piece *piece = &walk->piece;
+    auto next_piece = [&] {
         bool more = false;
         __syncwarp();
-        if (any && lane == 0) more = line.next(p, TQ, NQ, piece);
+        if (any && lane == 0) more = walk->line.next(p, TQ, NQ, &walk->piece);
         more = __shfl_sync(0xffffffffu, more, 0);
         __syncwarp();
         return more;
@@ -361,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     auto ring_k = [](int j) { return j < 2 ? j : 2 * j - 1; };
     auto ring_v = [](int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
 
-    if (warp >= S::kFirstMma && warp < S::kFirstMma + NQ) {
+    if (warp >= S::kFirstMma) {
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMmaRegs));
+        if (warp < S::kFirstMma + NQ) {
         // ------------------------------------------------------------ MMA issue (the warp in step, one elected lane issues)
         const int i = warp - S::kFirstMma;
         constexpr uint32_t id_s = idesc(false, kTileRows, BN, false), id_o = idesc(false, kTileRows, D, true);
@@ -431,16 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (active) blocks += n, ++loads;
         }
         if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
-    } else if (warp >= S::kFirstDeq && warp < S::kFirstDeq + S::kDeqWarps) {
-        // ------------------------------------------------------------ pages to f16 stages: 16 tokens a warp (half of their dims at D 256)
-        const int dw = warp - S::kFirstDeq, grp = dw & 3, half = dw >> 2, c = grp & 1;
+        }
+    } else if (warp >= S::kFirstDeq) {
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDeqRegs));
+        // ------------------------------------------------------------ pages to f16 stages: four warps K, four V, 16 tokens each
+        const int dw = warp - S::kFirstDeq, grp = dw & 3, c = grp & 1;
+        const bool is_v = dw >= 4;
         const int g = lane >> 2, t = lane & 3, m = lane >> 3, r8 = lane & 7;
         const int lg = p.pool.lgP - 5, D36 = 36 * D;
-        // where a lane's row of a matrix goes: K, tokens r8 of a group of 8; V, tokens 4 (r8 / 2) + r8 % 2 of the 16 (+ 2)
-        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(half * 2 * BN * 128 + grp * 16 * 128);
-        const int vt = 4 * (r8 >> 1) + (r8 & 1);
-        const uint32_t at_k = (uint32_t)(r8 * 128 + ((m ^ r8) << 4));
-        const uint32_t at_v0 = (uint32_t)(vt * 128 + ((m ^ (vt & 7)) << 4)), at_v1 = (uint32_t)((vt + 2) * 128 + ((m ^ ((vt + 2) & 7)) << 4));
+        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(grp * 16 * 128);
         uint32_t ring = 0, blocks = 0;
         bool ok = true;
         while (ok && next_piece()) {
@@ -449,17 +466,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int from = piece->from;
             const int32_t *table = p.table + (int64_t)piece->s * p.table_width;
             int page_base = -32, page = -1;
-            // tile of block j's group: its bytes (null: a page outside the pool), tokens from the group's first on
+            // tile of block j's group: its bytes, tokens from the group's first on (0 and less: none that counts), and whether
+            // its page lies outside the pool.  Bytes are always some of the pool's, so that the loads need no branch: values
+            // merged from two sides are copied, and a copy waits for its load.
             struct Where {
                 const uint8_t *at;
                 int left;
+                bool bad;
             };
             auto where = [&](int j) {
                 const int b = lo + j, kt = 2 * (b < front ? b : first + b - front) + (grp >> 1);
                 Where w;
                 w.left = T - kt * 32 - 16 * c;
                 if ((kt + 1) * 32 <= from && kt * 32 >= p.sinks) w.left = 0;  // no row sees it: its page may be gone
-                w.at = nullptr;
+                w.at = p.pool.pages;
+                w.bad = false;
                 if (w.left > 0) {
                     const int pg = kt >> lg;
                     if (pg < page_base || pg >= page_base + 32) {
@@ -467,47 +488,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         page = pg + lane < p.table_width ? table[pg + lane] : -1;
                     }
                     const int num = __shfl_sync(0xffffffffu, page, pg - page_base);
-                    if (num >= 0 && num < p.pool.n_pages)
-                        w.at = p.pool.pages + num * p.pool.page_bytes + h * p.pool.head_bytes + (kt & ((1 << lg) - 1)) * D36;
+                    w.bad = num < 0 || num >= p.pool.n_pages;
+                    if (!w.bad) w.at += num * p.pool.page_bytes + h * p.pool.head_bytes + (kt & ((1 << lg) - 1)) * D36;
                 }
                 return w;
             };
-            uint4 kc[S::kVecs], ks[S::kKScales], vc[S::kVecs], vs[S::kVScales];
-            const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
-            auto fetch_k = [&](const Where &w) {
-                if (w.at) {
-                    const uint4 *code = reinterpret_cast<const uint4 *>(w.at) + lane;
+            uint4 code[S::kLines];
+            auto fetch_codes = [&](const uint8_t *at) {
 #pragma unroll
-                    for (int x = 0; x < S::kVecs; ++x) kc[x] = __ldg(code + (D == 64 ? c : ((2 * c + x) * (NB / 4) + half)) * 32);
-                    const uint8_t *sc = w.at + 16 * D + (c * 8 + g) * NB * 4;
-                    if constexpr (D == 64) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(sc));
-                        ks[0] = make_uint4(v.x, v.y, v.x, v.y);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < S::kKScales; ++x) ks[x] = __ldg(reinterpret_cast<const uint4 *>(sc) + (x ^ half));
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < S::kVecs; ++x) kc[x] = zero;
-#pragma unroll
-                    for (int x = 0; x < S::kKScales; ++x) ks[x] = nan;  // (zero where the sequence has no token)
-                }
-            };
-            auto fetch_v = [&](const Where &w) {
-                if (w.at) {
-                    const uint4 *code = reinterpret_cast<const uint4 *>(w.at + 18 * D) + lane;
-#pragma unroll
-                    for (int x = 0; x < S::kVecs; ++x) vc[x] = __ldg(code + (c * (NB / 2) + 2 * half + x) * 32);
-                    const uint4 *sc = reinterpret_cast<const uint4 *>(w.at + 34 * D + (c * 4 + t) * NB * 8);
-#pragma unroll
-                    for (int x = 0; x < S::kVScales; ++x) vs[x] = __ldg(sc + (x ^ (2 * half)));
-                } else {
-#pragma unroll
-                    for (int x = 0; x < S::kVecs; ++x) vc[x] = zero;
-#pragma unroll
-                    for (int x = 0; x < S::kVScales; ++x) vs[x] = nan;
-                }
+                for (int x = 0; x < S::kLines; ++x) code[x] = __ldg(reinterpret_cast<const uint4 *>(at) + (c * S::kLines + x) * 32 + lane);
             };
             // the group's largest scale is below 2^(E + 1): factor 2^(1 - E) as two f16
             auto common = [&](uint32_t most, int &E) {
@@ -527,103 +516,105 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_full(r % NST));
             };
-            auto convert_k = [&](uint32_t r, int left, int slot) {
-                const uint32_t keep = (g < left ? 0xffffu : 0u) | (g + 8 < left ? 0xffff0000u : 0u);
-                uint32_t most = 0;
-                auto take = [&](uint32_t &w) {
-                    w &= keep;
-                    most = __vmaxu2(most, w & 0x7fff7fffu);
+            auto word = [](const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+            // the next block's bytes are fetched as soon as a block's are converted (past the last, some again)
+            Where cur = where(0), next = n > 1 ? where(1) : cur;
+            fetch_codes(is_v ? cur.at + 18 * D : cur.at);
+            if (!is_v) {
+                // a lane's words: of tokens g and 8 + g, all blocks
+                uint32_t sc[NB];  // (scale of token g, of token 8 + g)
+                auto fetch_scales = [&](const uint8_t *at) {
+                    const uint8_t *src = at + 16 * D + (c * 8 + g) * NB * 4;
+                    if constexpr (D == 64) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                        sc[0] = v.x, sc[1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < NB / 4; ++x) {
+                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + x);
+                            sc[4 * x] = v.x, sc[4 * x + 1] = v.y, sc[4 * x + 2] = v.z, sc[4 * x + 3] = v.w;
+                        }
+                    }
                 };
+                fetch_scales(cur.at);
+                const uint32_t at_k = (uint32_t)(r8 * 128 + ((m ^ r8) << 4));  // a lane's row of a matrix: token r8 of 8
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t r = ring + ring_k(j);
+                    if (!wait_free(r)) break;
+                    const uint32_t keep = (g < cur.left ? 0xffffu : 0u) | (g + 8 < cur.left ? 0xffff0000u : 0u);
+                    const uint32_t wrong = cur.bad ? 0x7e007e00u : 0u;  // NaN for a page outside the pool
+                    uint32_t most = 0;
 #pragma unroll
-                for (int x = 0; x < S::kKScales; ++x) take(ks[x].x), take(ks[x].y), take(ks[x].z), take(ks[x].w);
-                int E;
-                const uint32_t f2 = common(most, E);
-                const uint32_t dst = ring_base + r % NST * S::kStage;
-                const uint32_t sc[4] = {hmul2(ks[0].x, f2), hmul2(ks[0].y, f2), hmul2(ks[0].z, f2), hmul2(ks[0].w, f2)};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {  // 8 tokens
-#pragma unroll
-                    for (int b = 0; b < S::kBlocks; ++b) {
-                        const uint4 &v = kc[D == 64 ? 0 : (x < S::kVecs ? x : 0)];
-                        const int at = D == 64 ? 2 * x + b : b;
-                        const uint32_t w = at == 0 ? v.x : at == 1 ? v.y : at == 2 ? v.z : v.w;
-                        const uint32_t s2 = __byte_perm(sc[b], 0, x ? 0x3232 : 0x1010);
-                        store_word<false>(dst + (b >> 1) * (BN * 128) + x * 1024 + (at_k ^ ((b & 1) << 6)), w, s2);
+                    for (int b = 0; b < NB; ++b) {
+                        sc[b] = (sc[b] | wrong) & keep;
+                        most = __vmaxu2(most, sc[b] & 0x7fff7fffu);
                     }
-                }
-                if (lane == 0 && half == 0) fac_k[slot * 4 + grp] = __uint_as_float((uint32_t)(127 + E - 1) << 23);
-                publish(r);
-            };
-            auto convert_v = [&](uint32_t r, int left, int slot) {
-                const uint32_t k0 = (4 * t < left ? 0xffffu : 0u) | (4 * t + 1 < left ? 0xffff0000u : 0u);
-                const uint32_t k1 = (4 * t + 2 < left ? 0xffffu : 0u) | (4 * t + 3 < left ? 0xffff0000u : 0u);
-                uint32_t most = 0;
+                    int E;
+                    const uint32_t f2 = common(most, E), dst = ring_base + r % NST * S::kStage + at_k;
 #pragma unroll
-                for (int x = 0; x < S::kVScales; ++x) {
-                    vs[x].x &= k0, vs[x].y &= k1, vs[x].z &= k0, vs[x].w &= k1;
-                    most = __vmaxu2(__vmaxu2(most, vs[x].x & 0x7fff7fffu), vs[x].y & 0x7fff7fffu);
-                    most = __vmaxu2(__vmaxu2(most, vs[x].z & 0x7fff7fffu), vs[x].w & 0x7fff7fffu);
-                }
-                int E;
-                const uint32_t f2 = common(most, E);
-                const uint32_t dst = ring_base + r % NST * S::kStage;
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t s = hmul2(sc[b], f2);
 #pragma unroll
-                for (int x = 0; x < S::kVecs; ++x) {  // two 32-dim blocks
-                    const uint4 v = vc[x], s = vs[x];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {  // block y / 2 of them, token pairs y % 2
-                        const uint32_t w = y == 0 ? v.x : y == 1 ? v.y : y == 2 ? v.z : v.w;
-                        const uint32_t s2 = hmul2(y == 0 ? s.x : y == 1 ? s.y : y == 2 ? s.z : s.w, f2);
-                        store_word<true>(dst + x * (BN * 128) + (((y & 1) ? at_v1 : at_v0) ^ ((y >> 1) << 6)), w, s2);
+                        for (int x = 0; x < 2; ++x) {  // 8 tokens
+                            const uint32_t w = D == 64 ? word(code[0], 2 * x + b) : word(code[(x * NB + b) / 4], b % 4);
+                            store_word<false>((dst + x * 1024 + (b >> 1) * (BN * 128)) ^ ((b & 1) << 6), w, __byte_perm(s, 0, x ? 0x3232 : 0x1010));
+                        }
                     }
+                    if (lane == 0) fac_k[(blocks + j) % kFacs * 4 + grp] = __uint_as_float((uint32_t)(127 + E + 6) << 23);
+                    publish(r);
+                    cur = next;
+                    fetch_codes(cur.at);
+                    fetch_scales(cur.at);
+                    if (j + 2 < n) next = where(j + 2);
                 }
-                if (lane == 0 && half == 0) {
-                    exp_v[slot * 4 + grp] = (float)(E - 1);
-                    fac_v[slot * 4 + grp] = __uint_as_float((uint32_t)(127 + 1 - E) << 23);
-                }
-                publish(r);
-            };
-            // K_{j+1} and V_{j+1} are fetched as soon as K_j and V_j are converted
-            Where cur_k = where(0), cur_v = cur_k;
-            fetch_k(cur_k);
-            fetch_v(cur_v);
-            auto do_k = [&](int j) {
-                const uint32_t r = ring + ring_k(j);
-                if (!wait_free(r)) return;
-                convert_k(r, cur_k.left, (blocks + j) % kFacs);
-                if (j + 1 < n) {
-                    cur_k = where(j + 1);
-                    fetch_k(cur_k);
-                }
-            };
-            Where ahead[2] = {cur_k, cur_k};  // of block j at j % 2
-            auto do_v = [&](int j) {
-                const uint32_t r = ring + ring_v(j, n);
-                if (!wait_free(r)) return;
-                convert_v(r, cur_v.left, (blocks + j) % kFacs);
-                if (j + 1 < n) {
-                    cur_v = (j & 1) ? ahead[0] : ahead[1];
-                    fetch_v(cur_v);
-                }
-            };
-            do_k(0);
-            ahead[1] = cur_k;
-            if (ok && n > 1) {
-                do_k(1);
-                ahead[0] = cur_k;
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                do_v(j);
-                if (j + 2 < n && ok) {
-                    do_k(j + 2);
-                    if (j & 1) ahead[0] = cur_k;  // block j + 3
-                    else ahead[1] = cur_k;
+            } else {
+                // a lane's words: dims g, g + 8, g + 16, g + 24 of a block, tokens 4 t .. 4 t + 3 in pairs
+                uint4 sc[D / 64];  // of two blocks: pairs (0, 1), (2, 3) of the first, of the second
+                auto fetch_scales = [&](const uint8_t *at) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(at + 34 * D + (c * 4 + t) * NB * 8);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) sc[x] = __ldg(src + x);
+                };
+                fetch_scales(cur.at);
+                const int vt = 4 * (r8 >> 1) + (r8 & 1);  // a lane's row of a matrix: token 4 (r8 / 2) + r8 % 2 of the 16 (+ 2)
+                const uint32_t at_v[2] = {(uint32_t)(vt * 128 + ((m ^ (vt & 7)) << 4)), (uint32_t)((vt + 2) * 128 + ((m ^ ((vt + 2) & 7)) << 4))};
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t r = ring + ring_v(j, n);
+                    if (!wait_free(r)) break;
+                    const uint32_t k0 = (4 * t < cur.left ? 0xffffu : 0u) | (4 * t + 1 < cur.left ? 0xffff0000u : 0u);
+                    const uint32_t k1 = (4 * t + 2 < cur.left ? 0xffffu : 0u) | (4 * t + 3 < cur.left ? 0xffff0000u : 0u);
+                    const uint32_t wrong = cur.bad ? 0x7e007e00u : 0u;
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        sc[x].x = (sc[x].x | wrong) & k0, sc[x].y = (sc[x].y | wrong) & k1;
+                        sc[x].z = (sc[x].z | wrong) & k0, sc[x].w = (sc[x].w | wrong) & k1;
+                        most = __vmaxu2(__vmaxu2(most, sc[x].x & 0x7fff7fffu), sc[x].y & 0x7fff7fffu);
+                        most = __vmaxu2(__vmaxu2(most, sc[x].z & 0x7fff7fffu), sc[x].w & 0x7fff7fffu);
+                    }
+                    int E;
+                    const uint32_t f2 = common(most, E), dst = ring_base + r % NST * S::kStage;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)  // two 32-dim blocks
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)  // block y / 2 of them, token pairs y % 2
+                            store_word<true>(dst + x * (BN * 128) + (at_v[y & 1] ^ ((y >> 1) << 6)), word(code[x], y), hmul2(word(sc[x], y), f2));
+                    if (lane == 0) {
+                        exp_v[(blocks + j) % kFacs * 4 + grp] = (float)(E + 6);
+                        fac_v[(blocks + j) % kFacs * 4 + grp] = __uint_as_float((uint32_t)(127 - 6 - E) << 23);
+                    }
+                    publish(r);
+                    cur = next;
+                    fetch_codes(cur.at + 18 * D);
+                    fetch_scales(cur.at);
+                    if (j + 2 < n) next = where(j + 2);
                 }
             }
             ring += 2 * n;
             blocks += n;
         }
-    } else if (warp < 4 * NQ) {
+    } else {
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
         // ------------------------------------------------------------ softmax, one thread per row
         const int i = warp >> 2, row = tid & 127, hg = row % G;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -950,7 +941,7 @@ kvs_status launch_chunk(const ChunkParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return cuda_failed("chunk attention launch", e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.workers);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
