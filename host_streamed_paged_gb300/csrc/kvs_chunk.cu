@@ -15,14 +15,15 @@
 //
 // Roles:
 //   softmax warps, one thread a row: load the unit's queries, then turn each
-//     block's scores S in tensor memory into weights P over them, O rescaled
-//     only when a row's maximum grew by more than 2^8;
+//     block's scores S in tensor memory into weights P over them; a row's
+//     reference stands until the weights' sum nears f16's end, and only then is
+//     the block's maximum looked for and O rescaled;
 //   dequantising warps: codes and scales straight from the pages to registers
 //     a block ahead, f16 values into 128-byte-swizzled stages;
 //   an issuing warp per tile: S = Q K^T two blocks ahead of O += P V.
 //
 // Values.  A cached value is (n - 8) * scale.  The tensor core takes K and V as
-// f16 values rounded once, each group of 16 tokens brought to a common power of
+// f16 values rounded once, each tile of 32 tokens brought to a common power of
 // two, so that any scale the cache holds keeps f16's precision (down to 2^-12 of
 // what the group's largest scale reaches, and 2^-23 of it below); the power of two returns in the softmax, K's on the scores
 // and V's on the weights before those are rounded to f16.  Queries enter as f16
@@ -290,23 +291,26 @@ struct ChunkShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;         // query tiles of a CTA
     static constexpr bool kQInTmem = D != 128;          // the queries as the tensor-memory A operand, where there is room
     static constexpr int NB = D / 32;
-    // warpgroups: softmax (one a tile), two that dequantise, one whose first warps issue the MMAs
-    static constexpr int kThreads = 128 * (NQ + 3);
-    static constexpr int kDeqWarps = 8, kFirstDeq = 4 * NQ, kFirstMma = kFirstDeq + kDeqWarps;
-    // of the registers of 640 threads at launch (96 each) the softmax takes what the others leave
-    static constexpr bool kSplitRegs = NQ == 2;
-    static constexpr int kSoftmaxRegs = 136, kDeqRegs = 72, kMmaRegs = 56;
-    static_assert(!kSplitRegs || 128 * (NQ * kSoftmaxRegs + 2 * kDeqRegs + kMmaRegs) <= kThreads * 96, "registers at launch");
-    static constexpr int kLines = D / 64;               // 16-byte words of codes of a lane: of 16 tokens, K or V
+    // warpgroups: softmax (one a tile), those that dequantise, one whose first warps issue the MMAs
+    static constexpr int kHalves = D == 256 ? 2 : 1;    // warps to a tile of 32 tokens, of K and of V, half of the dims each
+    static constexpr int kThreads = 128 * (NQ + 2 * kHalves + 1);
+    static constexpr int kFirstDeq = 4 * NQ, kFirstMma = kFirstDeq + 8 * kHalves;
+    // of the registers at launch the softmax takes what the others leave
+    static constexpr int kRegs = D == 256 ? 80 : 96, kSoftmaxRegs = 152, kDeqRegs = D == 256 ? 72 : 64, kMmaRegs = D == 256 ? 40 : 48;
+    static_assert(NQ * kSoftmaxRegs + 2 * kHalves * kDeqRegs + kMmaRegs <= kThreads / 128 * kRegs, "registers at launch");
+    static_assert(kRegs == 65536 / kThreads / 8 * 8, "registers at launch");
+    static constexpr int kLines = D / 32 / kHalves;     // 16-byte words of codes of a lane: of a tile's K or V
+    static constexpr int kBlocks = NB / kHalves;        // 32-dim blocks of a warp
     static constexpr int kStage = BN * D * 2;
     static constexpr int kStages = D == 256 ? 6 : 8;
     static constexpr int kQBytes = kQInTmem ? 0 : kTileRows * D * 2;
     static constexpr int kOffRing = NQ * kQBytes;
-    static constexpr int kOffFac = kOffRing + kStages * kStage;  // K factors, V exponents, V factors [kFacs][4]
-    static constexpr int kOffPiece = kOffFac + 3 * kFacs * 16;
+    static constexpr int kOffFac = kOffRing + kStages * kStage;  // K factors, V exponents, V factors [kFacs][2]
+    static constexpr int kOffPiece = kOffFac + 3 * kFacs * 8;
     static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)sizeof(Walk);
     static constexpr int kSmem = kOffBar + 320 + 1024;
     static constexpr uint32_t kColO = 256, kColQ = D == 256 ? 128 : 384;
+    static_assert(kStages > 5, "see where the dequantising warps take turns");
     static_assert(kStages * kStage >= (kMaxSeq + 1) * 8, "the line's prefix sums lie in the ring");
 };
 
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     const uint32_t b_final = bars + 8u * 30;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 32);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 33);
-    float *fac_k = reinterpret_cast<float *>(smem + S::kOffFac), *exp_v = fac_k + 4 * kFacs, *fac_v = exp_v + 4 * kFacs;
+    float *fac_k = reinterpret_cast<float *>(smem + S::kOffFac), *exp_v = fac_k + 2 * kFacs, *fac_v = exp_v + 2 * kFacs;
 
     const int G = p.G, TQ = kTileRows / G, TU = NQ * TQ;
     if (warp == 0) {
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     }
     if (tid == 32) {
         for (int s = 0; s < NST; ++s) {
-            mbar_init(b_full(s), 4);
+            mbar_init(b_full(s), 2 * S::kHalves);
             mbar_init(b_empty(s), NQ);
         }
         for (int i = 0; i < 2; ++i) mbar_init(b_q(i), 4);
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     auto ring_v = [](int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
 
     if (warp >= S::kFirstMma) {
-        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMmaRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMmaRegs));
         if (warp < S::kFirstMma + NQ) {
         // ------------------------------------------------------------ MMA issue (the warp in step, one elected lane issues)
         const int i = warp - S::kFirstMma;
@@ -451,13 +455,15 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
         }
     } else if (warp >= S::kFirstDeq) {
-        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDeqRegs));
-        // ------------------------------------------------------------ pages to f16 stages: four warps K, four V, 16 tokens each
-        const int dw = warp - S::kFirstDeq, grp = dw & 3, c = grp & 1;
-        const bool is_v = dw >= 4;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDeqRegs));
+        // ------------------------------------------------------------ pages to f16 stages: half of the warps K, half V
+        // a tile of 32 tokens at a time, every other block's first or second
+        constexpr int kB = S::kBlocks, kPer = kB / 2;  // a warp's 32-dim blocks; pairs of them
+        const int dw = warp - S::kFirstDeq, side = dw & 1, turn = dw >> 1 & 1, half = (dw >> 2) % S::kHalves;
+        const bool is_v = dw >= 4 * S::kHalves;
         const int g = lane >> 2, t = lane & 3, m = lane >> 3, r8 = lane & 7;
         const int lg = p.pool.lgP - 5, D36 = 36 * D;
-        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(grp * 16 * 128);
+        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(half * kPer * (BN * 128) + side * 32 * 128);
         uint32_t ring = 0, blocks = 0;
         bool ok = true;
         while (ok && next_piece()) {
@@ -466,18 +472,18 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             const int from = piece->from;
             const int32_t *table = p.table + (int64_t)piece->s * p.table_width;
             int page_base = -32, page = -1;
-            // tile of block j's group: its bytes, tokens from the group's first on (0 and less: none that counts), and whether
-            // its page lies outside the pool.  Bytes are always some of the pool's, so that the loads need no branch: values
-            // merged from two sides are copied, and a copy waits for its load.
+            // block j's tile: its bytes, tokens from its first on (0 and less: none that counts), and whether its page lies
+            // outside the pool.  Bytes are always some of the pool's, so that the loads need no branch: values merged from
+            // two sides are copied, and a copy waits for its load.
             struct Where {
                 const uint8_t *at;
                 int left;
                 bool bad;
             };
             auto where = [&](int j) {
-                const int b = lo + j, kt = 2 * (b < front ? b : first + b - front) + (grp >> 1);
+                const int b = lo + j, kt = 2 * (b < front ? b : first + b - front) + side;
                 Where w;
-                w.left = T - kt * 32 - 16 * c;
+                w.left = T - kt * 32;
                 if ((kt + 1) * 32 <= from && kt * 32 >= p.sinks) w.left = 0;  // no row sees it: its page may be gone
                 w.at = p.pool.pages;
                 w.bad = false;
@@ -494,19 +500,18 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 return w;
             };
             uint4 code[S::kLines];
-            auto fetch_codes = [&](const uint8_t *at) {
-#pragma unroll
-                for (int x = 0; x < S::kLines; ++x) code[x] = __ldg(reinterpret_cast<const uint4 *>(at) + (c * S::kLines + x) * 32 + lane);
-            };
-            // the group's largest scale is below 2^(E + 1): factor 2^(1 - E) as two f16
-            auto common = [&](uint32_t most, int &E) {
-                uint32_t x = (most & 0xffffu) > (most >> 16) ? (most & 0xffffu) : (most >> 16);
+            auto line = [&](const uint8_t *at, int i) { return __ldg(reinterpret_cast<const uint4 *>(at) + i * 32 + lane); };
+            // the tile's largest scale is below 2^(E + 1): factor 2^(1 - E) as two f16
+            auto common = [&](__half2 most, int &E) {
+                uint32_t x = *reinterpret_cast<uint32_t *>(&most);
+                x = (x & 0xffffu) > (x >> 16) ? (x & 0xffffu) : (x >> 16);
                 x = __reduce_max_sync(0xffffffffu, x);
-                const int field = (int)(x >> 10) > 1 ? (int)(x >> 10) : 1;
+                const int field = (int)(x >> 10) > 1 ? (int)(x >> 10) : 1;  // (31: an infinity)
                 E = field - 15;
-                const uint32_t f = field == 31 ? 0x0200u : (uint32_t)(31 - field) << 10;
+                const uint32_t f = field >= 31 ? 0x0200u : (uint32_t)(31 - field) << 10;
                 return f | f << 16;
             };
+            auto larger = [](__half2 a, uint32_t w) { return __hmax2(a, __habs2(*reinterpret_cast<const __half2 *>(&w))); };
             auto wait_free = [&](uint32_t r) {
                 if (r >= (uint32_t)NST) ok = mbar_wait_warp(b_empty(r % NST), (r / NST - 1) & 1, abort);
                 return ok;
@@ -517,104 +522,137 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 if (lane == 0) mbar_arrive(b_full(r % NST));
             };
             auto word = [](const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
-            // the next block's bytes are fetched as soon as a block's are converted (past the last, some again)
-            Where cur = where(0), next = n > 1 ? where(1) : cur;
-            fetch_codes(is_v ? cur.at + 18 * D : cur.at);
+            // Every other block of the CTA is this warp's, whichever unit it is of: a warp's items are then at most 5 places of
+            // the ring apart, and a stage that it waits for has no phase behind the last but one that it has not seen complete.
+            const int j0 = (turn ^ (int)blocks) & 1;
+            if (j0 >= n) {
+                ring += 2 * n;
+                blocks += n;
+                continue;
+            }
+            // the next tile's bytes are fetched as soon as a tile's are converted (past the last, some again)
+            Where cur = where(j0), next = j0 + 2 < n ? where(j0 + 2) : cur;
             if (!is_v) {
-                // a lane's words: of tokens g and 8 + g, all blocks
-                uint32_t sc[NB];  // (scale of token g, of token 8 + g)
-                auto fetch_scales = [&](const uint8_t *at) {
-                    const uint8_t *src = at + 16 * D + (c * 8 + g) * NB * 4;
-                    if constexpr (D == 64) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-                        sc[0] = v.x, sc[1] = v.y;
-                    } else {
+                // a lane's words: of tokens 8 x + g, the warp's blocks; scales of tokens 16 c + g and 16 c + 8 + g in a word,
+                // the warp's blocks first
+                uint32_t sc[2][NB];
+                auto fetch = [&](const uint8_t *at) {
 #pragma unroll
-                        for (int x = 0; x < NB / 4; ++x) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + x);
-                            sc[4 * x] = v.x, sc[4 * x + 1] = v.y, sc[4 * x + 2] = v.z, sc[4 * x + 3] = v.w;
+                    for (int x = 0; x < S::kLines; ++x) code[x] = line(at, x * S::kHalves + half);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint8_t *src = at + 16 * D + (c * 8 + g) * NB * 4;
+                        if constexpr (D == 64) {
+                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                            sc[c][0] = v.x, sc[c][1] = v.y;
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < NB / 4; ++x) {
+                                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + (x ^ half));
+                                sc[c][4 * x] = v.x, sc[c][4 * x + 1] = v.y, sc[c][4 * x + 2] = v.z, sc[c][4 * x + 3] = v.w;
+                            }
                         }
                     }
                 };
-                fetch_scales(cur.at);
+                fetch(cur.at);
                 const uint32_t at_k = (uint32_t)(r8 * 128 + ((m ^ r8) << 4));  // a lane's row of a matrix: token r8 of 8
-                for (int j = 0; j < n; ++j) {
+                for (int j = j0; j < n; j += 2) {
                     const uint32_t r = ring + ring_k(j);
                     if (!wait_free(r)) break;
-                    const uint32_t keep = (g < cur.left ? 0xffffu : 0u) | (g + 8 < cur.left ? 0xffff0000u : 0u);
-                    const uint32_t wrong = cur.bad ? 0x7e007e00u : 0u;  // NaN for a page outside the pool
-                    uint32_t most = 0;
+                    if (cur.left < 32 || cur.bad) {  // tokens past the last count as 0, a page outside the pool as NaN
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        sc[b] = (sc[b] | wrong) & keep;
-                        most = __vmaxu2(most, sc[b] & 0x7fff7fffu);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t keep = (16 * c + g < cur.left ? 0xffffu : 0u) | (16 * c + g + 8 < cur.left ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) sc[c][b] = (sc[c][b] | (cur.bad ? 0x7e007e00u : 0u)) & keep;
+                        }
                     }
+                    __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll
+                    for (int b = 0; b < 2 * NB; ++b) most = larger(most, sc[b / NB][b % NB]);
                     int E;
                     const uint32_t f2 = common(most, E), dst = ring_base + r % NST * S::kStage + at_k;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint32_t s = hmul2(sc[b], f2);
+                    for (int b = 0; b < kB; ++b)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {  // 8 tokens
-                            const uint32_t w = D == 64 ? word(code[0], 2 * x + b) : word(code[(x * NB + b) / 4], b % 4);
-                            store_word<false>((dst + x * 1024 + (b >> 1) * (BN * 128)) ^ ((b & 1) << 6), w, __byte_perm(s, 0, x ? 0x3232 : 0x1010));
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t s = hmul2(sc[c][b], f2);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {  // 8 tokens
+                                const int x = 2 * c + y;
+                                const uint32_t w = D == 64 ? word(code[c], 2 * y + b) : word(code[x], b);
+                                store_word<false>((dst + x * 1024 + (b >> 1) * (BN * 128)) ^ ((b & 1) << 6), w, __byte_perm(s, 0, y ? 0x3232 : 0x1010));
+                            }
                         }
-                    }
-                    if (lane == 0) fac_k[(blocks + j) % kFacs * 4 + grp] = __uint_as_float((uint32_t)(127 + E + 6) << 23);
+                    if (lane == 0 && half == 0) fac_k[(blocks + j) % kFacs * 2 + side] = __uint_as_float((uint32_t)(127 + E + 6) << 23);
                     publish(r);
                     cur = next;
-                    fetch_codes(cur.at);
-                    fetch_scales(cur.at);
-                    if (j + 2 < n) next = where(j + 2);
+                    fetch(cur.at);
+                    if (j + 4 < n) next = where(j + 4);
                 }
             } else {
-                // a lane's words: dims g, g + 8, g + 16, g + 24 of a block, tokens 4 t .. 4 t + 3 in pairs
-                uint4 sc[D / 64];  // of two blocks: pairs (0, 1), (2, 3) of the first, of the second
-                auto fetch_scales = [&](const uint8_t *at) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(at + 34 * D + (c * 4 + t) * NB * 8);
+                // a lane's words: dims g, g + 8, g + 16, g + 24 of a block, tokens 16 c + 4 t .. + 3 in pairs; scales of the
+                // pairs (0, 1), (2, 3) of a block and of the next, the warp's blocks first
+                uint4 sc[2][D / 64];
+                auto fetch = [&](const uint8_t *at) {
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x) sc[x] = __ldg(src + x);
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int x = 0; x < kPer; ++x) code[c * kPer + x] = line(at + 18 * D, c * (D / 64) + half * kPer + x);
+                        const uint4 *src = reinterpret_cast<const uint4 *>(at + 34 * D + (c * 4 + t) * NB * 8);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x) sc[c][x] = __ldg(src + (x ^ (half * kPer)));
+                    }
                 };
-                fetch_scales(cur.at);
+                fetch(cur.at);
                 const int vt = 4 * (r8 >> 1) + (r8 & 1);  // a lane's row of a matrix: token 4 (r8 / 2) + r8 % 2 of the 16 (+ 2)
                 const uint32_t at_v[2] = {(uint32_t)(vt * 128 + ((m ^ (vt & 7)) << 4)), (uint32_t)((vt + 2) * 128 + ((m ^ ((vt + 2) & 7)) << 4))};
-                for (int j = 0; j < n; ++j) {
+                for (int j = j0; j < n; j += 2) {
                     const uint32_t r = ring + ring_v(j, n);
                     if (!wait_free(r)) break;
-                    const uint32_t k0 = (4 * t < cur.left ? 0xffffu : 0u) | (4 * t + 1 < cur.left ? 0xffff0000u : 0u);
-                    const uint32_t k1 = (4 * t + 2 < cur.left ? 0xffffu : 0u) | (4 * t + 3 < cur.left ? 0xffff0000u : 0u);
-                    const uint32_t wrong = cur.bad ? 0x7e007e00u : 0u;
-                    uint32_t most = 0;
+                    if (cur.left < 32 || cur.bad) {
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {
-                        sc[x].x = (sc[x].x | wrong) & k0, sc[x].y = (sc[x].y | wrong) & k1;
-                        sc[x].z = (sc[x].z | wrong) & k0, sc[x].w = (sc[x].w | wrong) & k1;
-                        most = __vmaxu2(__vmaxu2(most, sc[x].x & 0x7fff7fffu), sc[x].y & 0x7fff7fffu);
-                        most = __vmaxu2(__vmaxu2(most, sc[x].z & 0x7fff7fffu), sc[x].w & 0x7fff7fffu);
+                        for (int c = 0; c < 2; ++c) {
+                            const int left = cur.left - 16 * c - 4 * t;
+                            const uint32_t k0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u), k1 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+                            const uint32_t wrong = cur.bad ? 0x7e007e00u : 0u;
+#pragma unroll
+                            for (int x = 0; x < D / 64; ++x) {
+                                uint4 &v = sc[c][x];
+                                v.x = (v.x | wrong) & k0, v.y = (v.y | wrong) & k1, v.z = (v.z | wrong) & k0, v.w = (v.w | wrong) & k1;
+                            }
+                        }
+                    }
+                    __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll
+                    for (int x = 0; x < 2 * (D / 64); ++x) {
+                        const uint4 &v = sc[x / (D / 64)][x % (D / 64)];
+                        most = larger(larger(larger(larger(most, v.x), v.y), v.z), v.w);
                     }
                     int E;
                     const uint32_t f2 = common(most, E), dst = ring_base + r % NST * S::kStage;
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x)  // two 32-dim blocks
+                    for (int x = 0; x < S::kLines; ++x) {  // two 32-dim blocks of 16 tokens
+                        const int c = x / kPer, pair = x % kPer;
 #pragma unroll
                         for (int y = 0; y < 4; ++y)  // block y / 2 of them, token pairs y % 2
-                            store_word<true>(dst + x * (BN * 128) + (at_v[y & 1] ^ ((y >> 1) << 6)), word(code[x], y), hmul2(word(sc[x], y), f2));
-                    if (lane == 0) {
-                        exp_v[(blocks + j) % kFacs * 4 + grp] = (float)(E + 6);
-                        fac_v[(blocks + j) % kFacs * 4 + grp] = __uint_as_float((uint32_t)(127 - 6 - E) << 23);
+                            store_word<true>(dst + c * 2048 + pair * (BN * 128) + (at_v[y & 1] ^ ((y >> 1) << 6)), word(code[x], y), hmul2(word(sc[c][pair], y), f2));
+                    }
+                    if (lane == 0 && half == 0) {
+                        exp_v[(blocks + j) % kFacs * 2 + side] = (float)(E + 6);
+                        fac_v[(blocks + j) % kFacs * 2 + side] = __uint_as_float((uint32_t)(127 - 6 - E) << 23);
                     }
                     publish(r);
                     cur = next;
-                    fetch_codes(cur.at + 18 * D);
-                    fetch_scales(cur.at);
-                    if (j + 2 < n) next = where(j + 2);
+                    fetch(cur.at);
+                    if (j + 4 < n) next = where(j + 4);
                 }
             }
             ring += 2 * n;
             blocks += n;
         }
     } else {
-        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
         // ------------------------------------------------------------ softmax, one thread per row
         const int i = warp >> 2, row = tid & 127, hg = row % G;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -712,6 +750,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             const bool rows = has_rows(c), valid = row < TQ * G && tok < c.n;
             const int pos0 = c.T - c.n, pos = pos0 + tok;
             const int pf = pos0 + ft, pl = max(pos0 + min(ft + TQ, c.n) - 1, -1);  // positions of the tile's first and last row
+            const int masked_from = ((pf + 1) >> 6) - c.first + c.front - c.lo;  // (pf + 1) / BN: blocks from there reach past a row
             float m = -INFINITY;
             float l = 0.f;
             for (int j = 0; rows && j < n && ok; ++j) {
@@ -722,76 +761,90 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 if (!ok) break;
                 tc_after();
                 const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
-                uint32_t sr[BN];
+                const float2 kf = *reinterpret_cast<const float2 *>(fac_k + 2 * slot), ex = *reinterpret_cast<const float2 *>(exp_v + 2 * slot);
+                const float2 vf = *reinterpret_cast<const float2 *>(fac_v + 2 * slot);
+                const float sc[2] = {fac * kf.x, fac * kf.y};
+                float s[BN];
+                auto load_scores = [&] {
 #pragma unroll
-                for (int x = 0; x < BN; x += 32) tmem_ld32(ts + x, sr + x);
-                const float4 kf = *reinterpret_cast<const float4 *>(fac_k + 4 * slot), ve = *reinterpret_cast<const float4 *>(exp_v + 4 * slot);
-                const float4 vf = *reinterpret_cast<const float4 *>(fac_v + 4 * slot);
-                tmem_wait_ld();
-                float *s = reinterpret_cast<float *>(sr);
-                const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN;
-                if (k0 + BN - 1 > pf) {  // some row of the tile ends inside the block
-                    const int lim = pos - k0;
+                    for (int x = 0; x < BN; x += 32) tmem_ld32(ts + x, reinterpret_cast<uint32_t *>(s) + x);
+                    tmem_wait_ld();
+                    if (j < masked_from && !p.window) return;
+                    const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN;
+                    if (j >= masked_from) {  // some row of the tile ends inside the block
+                        const int lim = pos - k0;
 #pragma unroll
-                    for (int x = 0; x < BN; ++x) s[x] = x <= lim ? s[x] : -INFINITY;
-                }
-                if (p.window && k0 <= pl - p.window && k0 + BN > p.sinks) {  // some row's window begins inside the block or after
-                    const int from = (pos > -1 ? pos : -1) - p.window - k0, sk = p.sinks - k0;
+                        for (int x = 0; x < BN; ++x) s[x] = x <= lim ? s[x] : -INFINITY;
+                    }
+                    if (p.window && k0 <= pl - p.window && k0 + BN > p.sinks) {  // some row's window begins inside the block or after
+                        const int begin = (pos > -1 ? pos : -1) - p.window - k0, sk = p.sinks - k0;
 #pragma unroll
-                    for (int x = 0; x < BN; ++x) s[x] = x > from || x < sk ? s[x] : -INFINITY;
-                }
-                const float sc[4] = {fac * kf.x, fac * kf.y, fac * kf.z, fac * kf.w}, ex[4] = {ve.x, ve.y, ve.z, ve.w};
-                float m4[4];
+                        for (int x = 0; x < BN; ++x) s[x] = x > begin || x < sk ? s[x] : -INFINITY;
+                    }
+                };
+                uint32_t pk[BN / 2];
+                float part[2];  // sums of the two tiles' weights
+                auto weights = [&] {
+                    const float ref = m == -INFINITY ? 0.f : kUp - m;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float a = fmax3(s[16 * x], s[16 * x + 1], s[16 * x + 2]), z = fmax3(s[16 * x + 3], s[16 * x + 4], s[16 * x + 5]);
+                    for (int x = 0; x < 2; ++x) {
+                        const float neg = ref + (x ? ex.y : ex.x);
+                        const float2 sc2 = make_float2(sc[x], sc[x]), neg2 = make_float2(neg, neg);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int y = 6; y < 16; y += 4) a = fmax3(a, s[16 * x + y], s[16 * x + y + 1]);
+                        for (int y = 0; y < 32; y += 2) {
+                            const float2 z = fma2(make_float2(s[32 * x + y], s[32 * x + y + 1]), sc2, neg2);
+                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                            sum[y >> 1 & 1] = add2(sum[y >> 1 & 1], e);
+                            pk[16 * x + y / 2] = pack<false>(e.x, e.y);
+                        }
+                        const float2 both = add2(sum[0], sum[1]);
+                        part[x] = both.x + both.y;
+                    }
+                };
+                load_scores();
+                weights();
+                // The weights' sum bounds each of them: while it is below 2^15 none passes f16, and the reference (a maximum seen
+                // before) stands.  Else, and for a row's first key, the block's maximum is looked for.
+                const bool over = m == -INFINITY || !(part[0] + part[1] <= 32768.f);
+                if (__any_sync(0xffffffffu, over)) {
+                    load_scores();  // (S is still there)
+                    float top[2];
 #pragma unroll
-                    for (int y = 8; y < 16; y += 4) z = fmax3(z, s[16 * x + y], s[16 * x + y + 1]);
-                    m4[x] = fmaf(fmaxf(a, z), sc[x], ex[x]);
-                }
-                const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-                const bool grow = mx > m + 8.f || (m == -INFINITY && mx != -INFINITY);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float to = grow ? mx : m;
-                    const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
-                    l *= alpha;
-                    m = to;
-                    if (j > 0) {
-                        ok = mbar_wait_warp(b_o(i, (gb - 1) & 1), ((gb - 1) >> 1) & 1, abort);
-                        if (!ok) break;
-                        tc_after();
-                        const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
+                    for (int x = 0; x < 2; ++x) {
+                        float a[2] = {fmaxf(s[32 * x], s[32 * x + 1]), fmaxf(s[32 * x + 2], s[32 * x + 3])};
+#pragma unroll
+                        for (int y = 4; y < 32; y += 2) a[y >> 1 & 1] = fmax3(a[y >> 1 & 1], s[32 * x + y], s[32 * x + y + 1]);
+                        top[x] = fmaf(fmaxf(a[0], a[1]), sc[x], x ? ex.y : ex.x);
+                    }
+                    const float mx = fmaxf(top[0], top[1]);
+                    // (from 2^1 on, so that 64 weights at the reference are far below the bound)
+                    const bool grow = over && (m == -INFINITY ? mx != -INFINITY : mx > m + 1.f);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to = grow ? mx : m;
+                        const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
+                        l *= alpha;
+                        m = to;
+                        if (j > 0) {
+                            ok = mbar_wait_warp(b_o(i, (gb - 1) & 1), ((gb - 1) >> 1) & 1, abort);
+                            if (!ok) break;
+                            tc_after();
+                            const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(to_o + x, v);
-                            tmem_wait_ld();
+                            for (int x = 0; x < D; x += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(to_o + x, v);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-                            tmem_st32(to_o + x, v);
+                                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                                tmem_st16(to_o + x, v);
+                            }
                         }
                     }
-                }
-                const float neg = m == -INFINITY ? 0.f : kUp - m;
-                uint32_t pk[32];
-                float part[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 sc2 = make_float2(sc[x], sc[x]), neg2 = make_float2(neg + ex[x], neg + ex[x]);
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int y = 0; y < 16; y += 2) {
-                        const float2 z = fma2(make_float2(s[16 * x + y], s[16 * x + y + 1]), sc2, neg2);
-                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                        sum = add2(sum, e);
-                        pk[8 * x + y / 2] = pack<false>(e.x, e.y);
-                    }
-                    part[x] = sum.x + sum.y;
+                    weights();
                 }
                 tmem_st32(ts, pk);
-                l += (part[0] * vf.x + part[1] * vf.y) + (part[2] * vf.z + part[3] * vf.w);  // (without V's powers of two)
+                l += part[0] * vf.x + part[1] * vf.y;  // (without V's powers of two)
                 tmem_wait_st();
                 tc_before();
                 __syncwarp();
