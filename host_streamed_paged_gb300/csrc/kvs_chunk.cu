@@ -15,7 +15,10 @@
 //
 // Roles:
 //   softmax warps, one thread a row: load the unit's queries, then turn each
-//     block's scores S in tensor memory into weights P over them; a row's
+//     block's scores S in tensor memory into weights P over them, a warpgroup a
+//     tile, or where there is one tile (D = 256, or few rows) both in turns, a
+//     block each: a block then waits for the one before only to learn whether
+//     the reference changed, which is rare; a row's
 //     reference stands until the weights' sum nears f16's end, and only then is
 //     the block's maximum looked for and O rescaled;
 //   dequantising warps: codes and scales straight from the pages to registers
@@ -34,6 +37,7 @@
 #include <stdint.h>
 
 #include <string>
+#include <type_traits>
 
 #include "kvs.h"
 #include "kvs_internal.h"
@@ -78,17 +82,17 @@ struct ChunkMeta {
 
 // ---------------------------------------------------------------- the line of work
 
-// A unit costs kUnitCost for its beginning and end, and its keys, twice for two tiles.
-constexpr int kUnitCost = 512;
-constexpr int kMinCost = 512;  // of a worker, while that leaves some idle
+// A unit costs kUnitCost for its beginning and end, and its keys.
+constexpr int kUnitCost = 384;
+constexpr int kMinCost = 256;  // of a worker, while that leaves some idle
+static_assert(BN == 64, "blocks of keys are found by shifts");
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 struct Seq {
     int begin, n, T, X;  // first row, rows, cached tokens, units of a head
-    int wt;
     int64_t pos0, cap;   // position of the first row; most keys of a unit
-    int TU;
+    int TU, some, full;  // the first unit with keys; the first with the most
     __device__ __forceinline__ void load(const ChunkParams &p, int s, int tile_tokens, int tiles) {
         begin = clampi(p.cu[s], 0, p.total);
         n = clampi(p.cu[s + 1], begin, p.total) - begin;
@@ -97,22 +101,20 @@ struct Seq {
         T = len < 0 ? 0 : (int)(len < most ? len : most);
         TU = tile_tokens * tiles;
         X = (n + TU - 1) / TU;
-        wt = n > tile_tokens ? 2 : 1;
         pos0 = (int64_t)T - n;
-        cap = p.window ? (int64_t)p.window + TU + p.sinks : (int64_t)1 << 31;
+        cap = (int64_t)p.window + TU + p.sinks;
+        cap = p.window && cap < (int64_t)1 << 31 ? cap : (int64_t)1 << 31;
+        some = pos0 >= 0 ? 0 : (int)((uint32_t)-pos0 / (uint32_t)TU);
+        full = cap <= pos0 ? 0 : (int)(((uint32_t)(cap - pos0) - 1) / (uint32_t)TU);  // (rounded up, less 1)
     }
     __device__ __forceinline__ int64_t keys(int x) const {
         const int64_t k = pos0 + (int64_t)(x + 1) * TU;
         return k < 0 ? 0 : (k < cap ? k : cap);
     }
-    __device__ __forceinline__ int64_t cost(int x) const { return kUnitCost + wt * keys(x); }
+    __device__ __forceinline__ int64_t cost(int x) const { return kUnitCost + keys(x); }
     __device__ __forceinline__ int64_t before(int x) const {  // cost of units 0 .. x - 1 of a head
-        int64_t a = pos0 >= 0 ? 0 : -pos0 / TU;                // the first with keys
-        int64_t b = (cap - pos0 + TU - 1) / TU - 1;            // the first with the most
-        a = a < x ? a : x;
-        b = b < a ? a : (b < x ? b : x);
-        const int64_t sum = (b - a) * pos0 + TU * ((a + 1 + b) * (b - a) / 2) + (x - b) * cap;
-        return (int64_t)x * kUnitCost + wt * sum;
+        const int64_t a = some < x ? some : x, b = full < a ? a : (full < x ? full : x);
+        return (int64_t)x * kUnitCost + (b - a) * pos0 + TU * ((a + 1 + b) * (b - a) / 2) + (x - b) * cap;
     }
 };
 
@@ -170,13 +172,15 @@ struct Line {
             const int64_t p0 = q.pos0 + r0 < 0 ? 0 : q.pos0 + r0;
             if (p.window && p0 >= p.window) {
                 from = (int)(p0 - p.window + 1);
-                first = from / BN;
-                front = (p.sinks + BN - 1) / BN;
+                first = from >> 6;
+                front = (p.sinks + BN - 1) >> 6;
                 front = front < first ? front : first;
             }
-            nblk = front + (int)(last / BN) + 1 - first;
+            nblk = front + (int)(last >> 6) + 1 - first;
         }
-        auto block = [&](int64_t at) { return at <= kUnitCost ? 0 : (int)((at - kUnitCost) * nblk / (c - kUnitCost)); };
+        auto block = [&](int64_t at) {
+            return at <= kUnitCost ? 0 : at == c ? nblk : (int)((uint64_t)((at - kUnitCost) * nblk) / (uint64_t)(c - kUnitCost));
+        };
         o->lo = block(o1);
         o->hi = block(o2);
         o->nblk = nblk;
@@ -291,16 +295,12 @@ struct ChunkShape {
     static constexpr int NQ = D <= 128 ? 2 : 1;         // query tiles of a CTA
     static constexpr bool kQInTmem = D != 128;          // the queries as the tensor-memory A operand, where there is room
     static constexpr int NB = D / 32;
-    // warpgroups: softmax (one a tile), those that dequantise, one whose first warps issue the MMAs
-    static constexpr int kHalves = D == 256 ? 2 : 1;    // warps to a tile of 32 tokens, of K and of V, half of the dims each
-    static constexpr int kThreads = 128 * (NQ + 2 * kHalves + 1);
-    static constexpr int kFirstDeq = 4 * NQ, kFirstMma = kFirstDeq + 8 * kHalves;
+    // warpgroups: two of softmax, two that dequantise, one whose first warps issue the MMAs
+    static constexpr int kThreads = 640, kFirstDeq = 8, kFirstMma = 16;
     // of the registers at launch the softmax takes what the others leave
-    static constexpr int kRegs = D == 256 ? 80 : 96, kSoftmaxRegs = 152, kDeqRegs = D == 256 ? 72 : 64, kMmaRegs = D == 256 ? 40 : 48;
-    static_assert(NQ * kSoftmaxRegs + 2 * kHalves * kDeqRegs + kMmaRegs <= kThreads / 128 * kRegs, "registers at launch");
-    static_assert(kRegs == 65536 / kThreads / 8 * 8, "registers at launch");
-    static constexpr int kLines = D / 32 / kHalves;     // 16-byte words of codes of a lane: of a tile's K or V
-    static constexpr int kBlocks = NB / kHalves;        // 32-dim blocks of a warp
+    static constexpr int kSoftmaxRegs = D == 256 ? 128 : 144, kDeqRegs = D == 256 ? 88 : 72, kMmaRegs = 48;
+    static_assert(2 * kSoftmaxRegs + 2 * kDeqRegs + kMmaRegs <= kThreads / 128 * 96, "96 registers a thread at launch");
+    static constexpr int kLines = D / 32;               // 16-byte words of codes of a lane: of a tile's K or V
     static constexpr int kStage = BN * D * 2;
     static constexpr int kStages = D == 256 ? 6 : 8;
     static constexpr int kQBytes = kQInTmem ? 0 : kTileRows * D * 2;
@@ -308,7 +308,8 @@ struct ChunkShape {
     static constexpr int kOffFac = kOffRing + kStages * kStage;  // K factors, V exponents, V factors [kFacs][2]
     static constexpr int kOffPiece = kOffFac + 3 * kFacs * 8;
     static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)sizeof(Walk);
-    static constexpr int kSmem = kOffBar + 320 + 1024;
+    static constexpr int kOffRows = (kOffBar + 320 + 15) / 16 * 16;  // by row: largest query element, sum [2], reference
+    static constexpr int kSmem = kOffRows + 5 * kTileRows * 4 + 1024;
     static constexpr uint32_t kColO = 256, kColQ = D == 256 ? 128 : 384;
     static_assert(kStages > 5, "see where the dequantising warps take turns");
     static_assert(kStages * kStage >= (kMaxSeq + 1) * 8, "the line's prefix sums lie in the ring");
@@ -341,10 +342,10 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     }
     if (tid == 32) {
         for (int s = 0; s < NST; ++s) {
-            mbar_init(b_full(s), 2 * S::kHalves);
+            mbar_init(b_full(s), 2);
             mbar_init(b_empty(s), NQ);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(b_q(i), 4);
+        for (int i = 0; i < 2; ++i) mbar_init(b_q(i), 8);
         for (int i = 0; i < 4; ++i) {
             mbar_init(b_s(0, i), 1);
             mbar_init(b_p(0, i), 4);
@@ -458,12 +459,12 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDeqRegs));
         // ------------------------------------------------------------ pages to f16 stages: half of the warps K, half V
         // a tile of 32 tokens at a time, every other block's first or second
-        constexpr int kB = S::kBlocks, kPer = kB / 2;  // a warp's 32-dim blocks; pairs of them
-        const int dw = warp - S::kFirstDeq, side = dw & 1, turn = dw >> 1 & 1, half = (dw >> 2) % S::kHalves;
-        const bool is_v = dw >= 4 * S::kHalves;
+        constexpr int kPer = NB / 2;  // pairs of 32-dim blocks
+        const int dw = warp - S::kFirstDeq, side = dw & 1, turn = dw >> 1 & 1;
+        const bool is_v = dw >= 4;
         const int g = lane >> 2, t = lane & 3, m = lane >> 3, r8 = lane & 7;
         const int lg = p.pool.lgP - 5, D36 = 36 * D;
-        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(half * kPer * (BN * 128) + side * 32 * 128);
+        const uint32_t ring_base = smem_u32(smem + S::kOffRing) + (uint32_t)(side * 32 * 128);
         uint32_t ring = 0, blocks = 0;
         bool ok = true;
         while (ok && next_piece()) {
@@ -533,32 +534,30 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             // the next tile's bytes are fetched as soon as a tile's are converted (past the last, some again)
             Where cur = where(j0), next = j0 + 2 < n ? where(j0 + 2) : cur;
             if (!is_v) {
-                // a lane's words: of tokens 8 x + g, the warp's blocks; scales of tokens 16 c + g and 16 c + 8 + g in a word,
-                // the warp's blocks first
-                uint32_t sc[2][NB];
+                // a lane's words: of tokens 8 x + g; scales of tokens 16 c + g and 16 c + 8 + g in a word
+                // (kept as loaded, and copied before they are changed: a value changed in place is moved at the loop's end, and
+                // the move waits for its load)
+                using Scales = std::conditional_t<D == 64, uint2, uint4>;
+                constexpr int kVecs = NB * 4 / (int)sizeof(Scales);
+                Scales held[2][kVecs];
                 auto fetch = [&](const uint8_t *at) {
 #pragma unroll
-                    for (int x = 0; x < S::kLines; ++x) code[x] = line(at, x * S::kHalves + half);
+                    for (int x = 0; x < S::kLines; ++x) code[x] = line(at, x);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint8_t *src = at + 16 * D + (c * 8 + g) * NB * 4;
-                        if constexpr (D == 64) {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-                            sc[c][0] = v.x, sc[c][1] = v.y;
-                        } else {
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int x = 0; x < NB / 4; ++x) {
-                                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + (x ^ half));
-                                sc[c][4 * x] = v.x, sc[c][4 * x + 1] = v.y, sc[c][4 * x + 2] = v.z, sc[c][4 * x + 3] = v.w;
-                            }
-                        }
-                    }
+                        for (int x = 0; x < kVecs; ++x) held[c][x] = __ldg(reinterpret_cast<const Scales *>(at + 16 * D + (c * 8 + g) * NB * 4) + x);
                 };
                 fetch(cur.at);
                 const uint32_t at_k = (uint32_t)(r8 * 128 + ((m ^ r8) << 4));  // a lane's row of a matrix: token r8 of 8
                 for (int j = j0; j < n; j += 2) {
                     const uint32_t r = ring + ring_k(j);
                     if (!wait_free(r)) break;
+                    uint32_t sc[2][NB];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) sc[c][b] = reinterpret_cast<const uint32_t *>(held[c])[b];
                     if (cur.left < 32 || cur.bad) {  // tokens past the last count as 0, a page outside the pool as NaN
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -573,18 +572,18 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                     int E;
                     const uint32_t f2 = common(most, E), dst = ring_base + r % NST * S::kStage + at_k;
 #pragma unroll
-                    for (int b = 0; b < kB; ++b)
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const uint32_t s = hmul2(sc[c][b], f2);
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {  // 8 tokens
                                 const int x = 2 * c + y;
-                                const uint32_t w = D == 64 ? word(code[c], 2 * y + b) : word(code[x], b);
+                                const uint32_t w = D == 64 ? word(code[c], 2 * y + b) : word(code[x * (NB / 4) + b / 4], b % 4);
                                 store_word<false>((dst + x * 1024 + (b >> 1) * (BN * 128)) ^ ((b & 1) << 6), w, __byte_perm(s, 0, y ? 0x3232 : 0x1010));
                             }
                         }
-                    if (lane == 0 && half == 0) fac_k[(blocks + j) % kFacs * 2 + side] = __uint_as_float((uint32_t)(127 + E + 6) << 23);
+                    if (lane == 0) fac_k[(blocks + j) % kFacs * 2 + side] = __uint_as_float((uint32_t)(127 + E + 6) << 23);
                     publish(r);
                     cur = next;
                     fetch(cur.at);
@@ -592,16 +591,16 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 }
             } else {
                 // a lane's words: dims g, g + 8, g + 16, g + 24 of a block, tokens 16 c + 4 t .. + 3 in pairs; scales of the
-                // pairs (0, 1), (2, 3) of a block and of the next, the warp's blocks first
-                uint4 sc[2][D / 64];
+                // pairs (0, 1), (2, 3) of a block and of the next
+                uint4 held[2][D / 64];
                 auto fetch = [&](const uint8_t *at) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int x = 0; x < kPer; ++x) code[c * kPer + x] = line(at + 18 * D, c * (D / 64) + half * kPer + x);
+                        for (int x = 0; x < kPer; ++x) code[c * kPer + x] = line(at + 18 * D, c * kPer + x);
                         const uint4 *src = reinterpret_cast<const uint4 *>(at + 34 * D + (c * 4 + t) * NB * 8);
 #pragma unroll
-                        for (int x = 0; x < D / 64; ++x) sc[c][x] = __ldg(src + (x ^ (half * kPer)));
+                        for (int x = 0; x < D / 64; ++x) held[c][x] = __ldg(src + x);
                     }
                 };
                 fetch(cur.at);
@@ -610,6 +609,9 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 for (int j = j0; j < n; j += 2) {
                     const uint32_t r = ring + ring_v(j, n);
                     if (!wait_free(r)) break;
+                    uint4 sc[2][D / 64];
+#pragma unroll
+                    for (int x = 0; x < 2 * (D / 64); ++x) sc[x / (D / 64)][x % (D / 64)] = held[x / (D / 64)][x % (D / 64)];
                     if (cur.left < 32 || cur.bad) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         for (int y = 0; y < 4; ++y)  // block y / 2 of them, token pairs y % 2
                             store_word<true>(dst + c * 2048 + pair * (BN * 128) + (at_v[y & 1] ^ ((y >> 1) << 6)), word(code[x], y), hmul2(word(sc[c][pair], y), f2));
                     }
-                    if (lane == 0 && half == 0) {
+                    if (lane == 0) {
                         exp_v[(blocks + j) % kFacs * 2 + side] = (float)(E + 6);
                         fac_v[(blocks + j) % kFacs * 2 + side] = __uint_as_float((uint32_t)(127 - 6 - E) << 23);
                     }
@@ -654,56 +656,76 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
         // ------------------------------------------------------------ softmax, one thread per row
-        const int i = warp >> 2, row = tid & 127, hg = row % G;
+        const int wg = warp >> 2, row = tid & 127, hg = row % G;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float nan = __int_as_float(0x7fc00000);
+        float *row_top = reinterpret_cast<float *>(smem + S::kOffRows) + row, *row_sum = row_top + 2 * kTileRows, *row_ref = row_sum + 2 * kTileRows;
         float fac = 0.f;
-        uint32_t ring = 0, blocks = 0, all_blocks = 0;  // stages, blocks of this tile, blocks of the CTA so far
-        bool ok = true;
+        uint32_t ring = 0, blocks0 = 0, blocks1 = 0, all_blocks = 0;  // so far: stages, blocks of tile 0, of tile 1, of the CTA
+        bool ok = true;  // (every warp goes on to the end of the line whatever it has given up: the barriers count them all)
         ChunkMeta meta = {};
-        // the row's queries as f16 times a power of two, dims of each 32-dim block in the order of a K row: even ones
-        // of the first 16, odd ones, even ones of the last 16, odd ones
-        auto load_queries = [&](const Piece &c) {
-            const int tok = c.x * TU + i * TQ + row / G;
-            const bool valid = row < TQ * G && tok < c.n;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + hg) * D : 0);
+        // barriers of both warpgroups: all; "block done" of warpgroup wg
+        auto sync_all = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        auto done_wait = [&] { asm volatile("bar.sync %0, 256;" ::"r"(3 - wg) : "memory"); };
+        auto done_tell = [&] { asm volatile("bar.arrive %0, 256;" ::"r"(2 + wg) : "memory"); };
+        auto one_tile = [&](const Piece &c) { return NQ == 1 || c.x * TU + TQ >= c.n; };  // both warpgroups on tile 0
+        // The row's queries as f16 times a power of two, dims of each 32-dim block in the order of a K row: even ones of the
+        // first 16, odd ones, even ones of the last 16, odd ones.  With one tile a warpgroup loads half of the dims (D 64: the
+        // first all).
+        auto load_dims = [&](auto dims, const Piece &c, int tile, int d0, bool mine, bool shared) {
+            constexpr int N = decltype(dims)::value;
+            const int tok = c.x * TU + tile * TQ + row / G;
+            const bool valid = mine && row < TQ * G && tok < c.n;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                               (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + hg) * D + d0 : 0));
+            uint4 v[N / 8];
+#pragma unroll
+            for (int x = 0; x < N / 8; ++x) v[x] = valid ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
             uint32_t top2 = 0;
-#pragma unroll 4
-            for (int x = 0; x < D / 8; ++x) {
-                const uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + x) : make_uint4(0, 0, 0, 0);
-                top2 = __vmaxu2(__vmaxu2(top2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-                top2 = __vmaxu2(__vmaxu2(top2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+#pragma unroll
+            for (int x = 0; x < N / 8; ++x) {
+                top2 = __vmaxu2(__vmaxu2(top2, v[x].x & 0x7fff7fffu), v[x].y & 0x7fff7fffu);
+                top2 = __vmaxu2(__vmaxu2(top2, v[x].z & 0x7fff7fffu), v[x].w & 0x7fff7fffu);
             }
             const uint32_t top = (top2 & 0xffffu) > (top2 >> 16) ? (top2 & 0xffffu) : (top2 >> 16);
-            const float top_f = p.bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+            float top_f = p.bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+            if (shared) {  // (an infinity or NaN comes out as one: by the bits)
+                row_top[wg * kTileRows] = top_f;
+                sync_all();
+                const float a = row_top[0], b = row_top[kTileRows];
+                top_f = __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+            }
             int e = (int)(__float_as_uint(top_f) >> 23) - 127;
             e = e < -100 ? -100 : (e > 100 ? 100 : e);
             const float f = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2);
             // never 0, so that a masked score stays -inf times it
             fac = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 1.17549435e-38f);
             auto two = [&](uint32_t w) {
-                float2 y = p.bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
-                                  : __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                const float2 y = p.bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                                        : __half22float2(*reinterpret_cast<const __half2 *>(&w));
                 return make_float2(y.x * f, y.y * f);
             };
-#pragma unroll 1
-            for (int b2 = 0; b2 < D / 64; ++b2) {
-                uint32_t o[32];
+            if (mine) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {  // 8 dims: half of the even and of the odd chunk of 16
-                    const uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + b2 * 8 + x) : make_uint4(0, 0, 0, 0);
-                    const float2 a = two(v.x), b = two(v.y), c2 = two(v.z), d = two(v.w);
-                    uint32_t *at = o + (x >> 1) * 8 + (x & 1) * 2;
-                    at[0] = pack<false>(a.x, b.x), at[1] = pack<false>(c2.x, d.x);
-                    at[4] = pack<false>(a.y, b.y), at[5] = pack<false>(c2.y, d.y);
-                }
-                if constexpr (S::kQInTmem) {
-                    tmem_st32(lanes + S::kColQ + (uint32_t)(i * D / 2 + b2 * 32), o);
-                } else {
-                    uint8_t *dst = smem + i * S::kQBytes + b2 * (kTileRows * 128) + row * 128;
+                for (int b2 = 0; b2 < N / 64; ++b2) {
+                    uint32_t o[32];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        *reinterpret_cast<uint4 *>(dst + ((x ^ (row & 7)) << 4)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    for (int x = 0; x < 8; ++x) {  // 8 dims: half of the even and of the odd chunk of 16
+                        const uint4 u = v[8 * b2 + x];
+                        const float2 a = two(u.x), b = two(u.y), c2 = two(u.z), d = two(u.w);
+                        uint32_t *at = o + (x >> 1) * 8 + (x & 1) * 2;
+                        at[0] = pack<false>(a.x, b.x), at[1] = pack<false>(c2.x, d.x);
+                        at[4] = pack<false>(a.y, b.y), at[5] = pack<false>(c2.y, d.y);
+                    }
+                    const int g64 = d0 / 64 + b2;
+                    if constexpr (S::kQInTmem) {
+                        tmem_st32(lanes + S::kColQ + (uint32_t)(tile * D / 2 + g64 * 32), o);
+                    } else {
+                        uint8_t *dst = smem + tile * S::kQBytes + g64 * (kTileRows * 128) + row * 128;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint4 *>(dst + ((x ^ (row & 7)) << 4)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
                 }
             }
             if constexpr (S::kQInTmem) {
@@ -713,9 +735,19 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 proxy_fence();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_q(i));
+            if (lane == 0) {  // 8 arrivals a tile
+                mbar_arrive(b_q(tile));
+                if (!shared) mbar_arrive(b_q(tile));
+            }
         };
-        auto has_rows = [&](const Piece &c) { return c.x * TU + i * TQ < c.n; };
+        auto load_queries = [&](const Piece &c) {
+            if (one_tile(c)) {
+                if constexpr (D == 64) load_dims(std::integral_constant<int, 64>{}, c, 0, 0, wg == 0, true);
+                else load_dims(std::integral_constant<int, D / 2>{}, c, 0, wg * (D / 2), true, true);
+            } else if constexpr (NQ == 2) {
+                load_dims(std::integral_constant<int, D>{}, c, wg, 0, true, false);
+            }
+        };
         auto out_row = [&](int64_t trow, int hq) { return static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D); };
         // the next piece with work, rows that see nothing written on the way
         auto find_work = [&] {
@@ -731,8 +763,8 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                     }
                 }
                 if (c.kind == 2) return true;
-                const int tok = c.x * TU + i * TQ + row / G;
-                if (c.kind == 1 && row < TQ * G && tok < c.n) {
+                const int tok = c.x * TU + wg * TQ + row / G;
+                if (c.kind == 1 && wg < NQ && row < TQ * G && tok < c.n) {
                     const int64_t trow = c.begin + tok;
                     const int hq = c.h * G + hg;
                     uint4 *dst = reinterpret_cast<uint4 *>(out_row(trow, hq));
@@ -743,132 +775,202 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             return false;
         };
         bool work = find_work();
-        if (work && has_rows(*piece)) load_queries(*piece);
+        if (work) load_queries(*piece);
         while (work) {
             const Piece c = *piece;
+            const bool shared = one_tile(c);
+            const int i = shared ? 0 : wg;  // the tile
             const int n = c.hi - c.lo, ft = c.x * TU + i * TQ, tok = ft + row / G;
-            const bool rows = has_rows(c), valid = row < TQ * G && tok < c.n;
+            const bool valid = row < TQ * G && tok < c.n;
             const int pos0 = c.T - c.n, pos = pos0 + tok;
             const int pf = pos0 + ft, pl = max(pos0 + min(ft + TQ, c.n) - 1, -1);  // positions of the tile's first and last row
             const int masked_from = ((pf + 1) >> 6) - c.first + c.front - c.lo;  // (pf + 1) / BN: blocks from there reach past a row
-            float m = -INFINITY;
-            float l = 0.f;
-            for (int j = 0; rows && j < n && ok; ++j) {
-                const uint32_t gb = blocks + j;
-                const int buf = gb & 1, slot = (all_blocks + j) % kFacs;
-                const uint32_t rv = ring + ring_v(j, n);
-                ok = wait_warp(abort, [&] { return mbar_done(b_s(i, buf), (gb >> 1) & 1) & mbar_done(b_full(rv % NST), (rv / NST) & 1); });
-                if (!ok) break;
-                tc_after();
-                const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
-                const float2 kf = *reinterpret_cast<const float2 *>(fac_k + 2 * slot), ex = *reinterpret_cast<const float2 *>(exp_v + 2 * slot);
-                const float2 vf = *reinterpret_cast<const float2 *>(fac_v + 2 * slot);
-                const float sc[2] = {fac * kf.x, fac * kf.y};
-                float s[BN];
-                auto load_scores = [&] {
+            const uint32_t first_block = i ? blocks1 : blocks0;
+            float m = -INFINITY, l = 0.f;
+            // what a block needs beside its scores: K's factors times the row's, V's exponents and their factors, of its two tiles
+            struct Factors {
+                float sc[2], ex[2], vf[2];
+            };
+            auto factors = [&](int j) {
+                const int slot = (all_blocks + j) % kFacs;
+                const float2 k = *reinterpret_cast<const float2 *>(fac_k + 2 * slot), x = *reinterpret_cast<const float2 *>(exp_v + 2 * slot);
+                const float2 v = *reinterpret_cast<const float2 *>(fac_v + 2 * slot);
+                return Factors{{fac * k.x, fac * k.y}, {x.x, x.y}, {v.x, v.y}};
+            };
+            auto scores_at = [&](int j) { return lanes + (uint32_t)((2 * i + ((first_block + j) & 1)) * BN); };
+            auto ready = [&](int j) {
+                const uint32_t gb = first_block + j, rv = ring + ring_v(j, n);
+                return mbar_done(b_s(i, gb & 1), (gb >> 1) & 1) & mbar_done(b_full(rv % NST), (rv / NST) & 1);
+            };
+            float s[BN];
+            uint32_t pk[BN / 2];
+            float part[2];  // sums of the two tiles' weights
+            auto load_half = [&](int j, int x) { tmem_ld32(scores_at(j) + 32 * x, reinterpret_cast<uint32_t *>(s) + 32 * x); };
+            auto mask = [&](int j, int h) {  // of 32 keys
+                if (j < masked_from && !p.window) return;
+                const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN + 32 * h;
+                if (j >= masked_from) {  // some row of the tile ends inside the block
+                    const int lim = pos - k0;
 #pragma unroll
-                    for (int x = 0; x < BN; x += 32) tmem_ld32(ts + x, reinterpret_cast<uint32_t *>(s) + x);
-                    tmem_wait_ld();
-                    if (j < masked_from && !p.window) return;
-                    const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN;
-                    if (j >= masked_from) {  // some row of the tile ends inside the block
-                        const int lim = pos - k0;
-#pragma unroll
-                        for (int x = 0; x < BN; ++x) s[x] = x <= lim ? s[x] : -INFINITY;
-                    }
-                    if (p.window && k0 <= pl - p.window && k0 + BN > p.sinks) {  // some row's window begins inside the block or after
-                        const int begin = (pos > -1 ? pos : -1) - p.window - k0, sk = p.sinks - k0;
-#pragma unroll
-                        for (int x = 0; x < BN; ++x) s[x] = x > begin || x < sk ? s[x] : -INFINITY;
-                    }
-                };
-                uint32_t pk[BN / 2];
-                float part[2];  // sums of the two tiles' weights
-                auto weights = [&] {
-                    const float ref = m == -INFINITY ? 0.f : kUp - m;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float neg = ref + (x ? ex.y : ex.x);
-                        const float2 sc2 = make_float2(sc[x], sc[x]), neg2 = make_float2(neg, neg);
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            const float2 z = fma2(make_float2(s[32 * x + y], s[32 * x + y + 1]), sc2, neg2);
-                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                            sum[y >> 1 & 1] = add2(sum[y >> 1 & 1], e);
-                            pk[16 * x + y / 2] = pack<false>(e.x, e.y);
-                        }
-                        const float2 both = add2(sum[0], sum[1]);
-                        part[x] = both.x + both.y;
-                    }
-                };
-                load_scores();
-                weights();
-                // The weights' sum bounds each of them: while it is below 2^15 none passes f16, and the reference (a maximum seen
-                // before) stands.  Else, and for a row's first key, the block's maximum is looked for.
-                const bool over = m == -INFINITY || !(part[0] + part[1] <= 32768.f);
-                if (__any_sync(0xffffffffu, over)) {
-                    load_scores();  // (S is still there)
-                    float top[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float a[2] = {fmaxf(s[32 * x], s[32 * x + 1]), fmaxf(s[32 * x + 2], s[32 * x + 3])};
-#pragma unroll
-                        for (int y = 4; y < 32; y += 2) a[y >> 1 & 1] = fmax3(a[y >> 1 & 1], s[32 * x + y], s[32 * x + y + 1]);
-                        top[x] = fmaf(fmaxf(a[0], a[1]), sc[x], x ? ex.y : ex.x);
-                    }
-                    const float mx = fmaxf(top[0], top[1]);
-                    // (from 2^1 on, so that 64 weights at the reference are far below the bound)
-                    const bool grow = over && (m == -INFINITY ? mx != -INFINITY : mx > m + 1.f);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float to = grow ? mx : m;
-                        const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
-                        l *= alpha;
-                        m = to;
-                        if (j > 0) {
-                            ok = mbar_wait_warp(b_o(i, (gb - 1) & 1), ((gb - 1) >> 1) & 1, abort);
-                            if (!ok) break;
-                            tc_after();
-                            const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
-#pragma unroll 1
-                            for (int x = 0; x < D; x += 16) {
-                                uint32_t v[16];
-                                tmem_ld16(to_o + x, v);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-                                tmem_st16(to_o + x, v);
-                            }
-                        }
-                    }
-                    weights();
+                    for (int x = 0; x < 32; ++x) s[32 * h + x] = x <= lim ? s[32 * h + x] : -INFINITY;
                 }
-                tmem_st32(ts, pk);
-                l += part[0] * vf.x + part[1] * vf.y;  // (without V's powers of two)
+                if (p.window && k0 <= pl - p.window && k0 + 32 > p.sinks) {  // some row's window begins inside them or after
+                    const int begin = (pos > -1 ? pos : -1) - p.window - k0, sk = p.sinks - k0;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) s[32 * h + x] = x > begin || x < sk ? s[32 * h + x] : -INFINITY;
+                }
+            };
+            auto load_scores = [&](int j) {
+                load_half(j, 0);
+                load_half(j, 1);
+                tmem_wait_ld();
+                mask(j, 0);
+                mask(j, 1);
+            };
+            auto weights = [&](const Factors &f, int x) {  // of 32 keys
+                const float neg = (m == -INFINITY ? 0.f : kUp - m) + f.ex[x];
+                const float2 sc2 = make_float2(f.sc[x], f.sc[x]), neg2 = make_float2(neg, neg);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int y = 0; y < 32; y += 2) {
+                    const float2 z = fma2(make_float2(s[32 * x + y], s[32 * x + y + 1]), sc2, neg2);
+                    const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                    sum[y >> 1 & 1] = add2(sum[y >> 1 & 1], e);
+                    pk[16 * x + y / 2] = pack<false>(e.x, e.y);
+                }
+                const float2 both = add2(sum[0], sum[1]);
+                part[x] = both.x + both.y;
+            };
+            // The weights' sum bounds each of them: while it is below 2^15 none passes f16, and the reference (a maximum seen
+            // before) stands.  Else, and for a row's first key, the block's maximum is looked for; false: a wait gave up.
+            auto must_grow = [&] { return __any_sync(0xffffffffu, m == -INFINITY || !(part[0] + part[1] <= 32768.f)); };
+            auto grow_reference = [&](int j, const Factors &f) {
+                const bool over = m == -INFINITY || !(part[0] + part[1] <= 32768.f);
+                load_scores(j);  // (S is still there)
+                float top[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float a[2] = {fmaxf(s[32 * x], s[32 * x + 1]), fmaxf(s[32 * x + 2], s[32 * x + 3])};
+#pragma unroll
+                    for (int y = 4; y < 32; y += 2) a[y >> 1 & 1] = fmax3(a[y >> 1 & 1], s[32 * x + y], s[32 * x + y + 1]);
+                    top[x] = fmaf(fmaxf(a[0], a[1]), f.sc[x], f.ex[x]);
+                }
+                const float mx = fmaxf(top[0], top[1]);
+                // (from 2^1 on, so that 64 weights at the reference are far below the bound)
+                const bool grow = over && (m == -INFINITY ? mx != -INFINITY : mx > m + 1.f);
+                bool done = true;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? mx : m;
+                    const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
+                    l *= alpha;
+                    m = to;
+                    if (j > 0) {
+                        const uint32_t before = first_block + j - 1;
+                        done = mbar_wait_warp(b_o(i, before & 1), (before >> 1) & 1, abort);
+                        tc_after();
+                        const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
+#pragma unroll 1
+                        for (int x = 0; x < D && done; x += 16) {
+                            uint32_t v[16];
+                            tmem_ld16(to_o + x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                            tmem_st16(to_o + x, v);
+                        }
+                    }
+                }
+                weights(f, 0);
+                weights(f, 1);
+                return done;
+            };
+            auto publish = [&](int j, const Factors &f) {
+                tmem_st32(scores_at(j), pk);
+                l += part[0] * f.vf[0] + part[1] * f.vf[1];  // (without V's powers of two)
                 tmem_wait_st();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_p(i, buf));
+                if (lane == 0) mbar_arrive(b_p(i, (first_block + j) & 1));
+            };
+            if (shared) {
+                for (int j = (first_block & 1) == (uint32_t)wg ? 0 : 1; j < n; j += 2) {
+                    if (ok) ok = wait_warp(abort, [&] { return ready(j); });
+                    tc_after();
+                    const Factors f = factors(j);
+                    if (ok) {
+                        load_scores(j);
+                        weights(f, 0);
+                        weights(f, 1);
+                    }
+                    bool stale = false;
+                    if (j > 0) {  // the block before is done: its reference is the one that stands
+                        done_wait();
+                        const float now = *row_ref;
+                        stale = now != m;
+                        if (stale) {
+                            l = m == -INFINITY ? l : l * ex2(m - now);
+                            m = now;
+                        }
+                    }
+                    if (ok) {
+                        if (__any_sync(0xffffffffu, stale)) {
+                            load_scores(j);
+                            weights(f, 0);
+                            weights(f, 1);
+                        }
+                        if (must_grow()) ok = grow_reference(j, f);
+                    }
+                    if (ok) publish(j, f);
+                    *row_ref = m;
+                    if (j + 1 < n) done_tell();
+                }
+            } else if (ok) {
+                for (int j = 0; j < n; ++j) {
+                    ok = wait_warp(abort, [&] { return ready(j); });
+                    if (!ok) break;
+                    tc_after();
+                    const Factors f = factors(j);
+                    load_scores(j);
+                    weights(f, 0);
+                    weights(f, 1);
+                    if (must_grow()) {
+                        ok = grow_reference(j, f);
+                        if (!ok) break;
+                    }
+                    publish(j, f);
+                }
             }
             ring += 2 * n;
             all_blocks += n;
-            if (rows) blocks += n;
+            blocks0 += n;
+            if (!shared) blocks1 += n;
+            const uint32_t last = (i ? blocks1 : blocks0) - 1;
+            if (shared) {  // both are done with the scores, the reference is the last one
+                sync_all();
+                const float now = *row_ref;
+                row_sum[wg * kTileRows] = !ok ? nan : m == -INFINITY ? 0.f : l * ex2(m - now);
+                m = now;
+            }
             // the next queries go in before this unit's output comes out: its scores are all read
             work = find_work();
-            if (ok && work && has_rows(*piece)) load_queries(*piece);
-            if (!rows) continue;
-            if (ok) ok = mbar_wait_warp(b_o(i, (blocks - 1) & 1), ((blocks - 1) >> 1) & 1, abort);
+            if (work) load_queries(*piece);
+            if (shared) {
+                sync_all();
+                l = row_sum[0] + row_sum[kTileRows];
+            }
+            if (ok) ok = mbar_wait_warp(b_o(i, last & 1), (last >> 1) & 1, abort);
             tc_after();
+            if (!ok) l = nan;
             const bool whole = c.lo == 0 && c.hi == c.nblk;
             const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
-            if (!ok) l = nan;
+            const int x0 = shared ? wg * (D / 2) : 0, x1 = shared ? x0 + D / 2 : D;
             if (whole) {
                 const int64_t trow = c.begin + tok;
                 const int hq = c.h * G + hg;
                 const float inv = 1.f / l;
                 uint4 *dst = reinterpret_cast<uint4 *>(out_row(trow, hq));
 #pragma unroll 1
-                for (int x = 0; x < D; x += 32) {
+                for (int x = x0; x < x1; x += 32) {
                     uint32_t v[32] = {};
                     if (ok) {  // (the same in a warp; else MMAs may be under way, and what they have is not wanted)
                         tmem_ld32(to + x, v);
@@ -889,12 +991,12 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         }
                     }
                 }
-                if (valid && p.lse) p.lse[trow * p.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l) - kUp) * 0.693147180559945309f;
+                if (valid && x0 == 0 && p.lse) p.lse[trow * p.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l) - kUp) * 0.693147180559945309f;
             } else {
                 const int64_t at = (int64_t)(2 * (int)blockIdx.x + (c.lo == 0)) * NQ + i;
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o) + at * (D / 4 * kTileRows) + row;
 #pragma unroll 1
-                for (int x = 0; x < D; x += 32) {
+                for (int x = x0; x < x1; x += 32) {
                     uint32_t v[32] = {};
                     if (ok) {
                         tmem_ld32(to + x, v);
@@ -907,7 +1009,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                                                                        __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
                     }
                 }
-                if (valid) p.part_ml[at * kTileRows + row] = make_float2(m, l);
+                if (valid && x0 == 0) p.part_ml[at * kTileRows + row] = make_float2(m, l);
             }
         }
         if (tid == 0) p.meta[blockIdx.x] = meta;
@@ -924,6 +1026,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
 // order.  blockIdx.x: the worker that began it, blockIdx.y: tile and 16 dims;
 // one thread per row.
 constexpr int kJoinDims = 16;
+constexpr int kJoinAtOnce = 4;  // partials a thread has on their way
 template <int D>
 __global__ void __launch_bounds__(kTileRows) join_kernel(const __grid_constant__ ChunkParams p) {
     constexpr int NQ = ChunkShape<D>::NQ;
@@ -931,30 +1034,51 @@ __global__ void __launch_bounds__(kTileRows) join_kernel(const __grid_constant__
     const int w = blockIdx.x, i = (int)blockIdx.y % NQ, d0 = (int)blockIdx.y / NQ * kJoinDims, row = threadIdx.x;
     const ChunkMeta meta = p.meta[w];
     const int TQ = kTileRows / p.G, tok = i * TQ + row / p.G;
-    if (!meta.tail || row >= TQ * p.G || tok >= meta.tokens) return;
+    if (!meta.tail) return;
+    const bool mine = row < TQ * p.G && tok < meta.tokens;
     float m = -INFINITY, l = 0.f;
     float4 o[kJoinDims / 4] = {};
-    auto add = [&](int slot) {
+    float2 ml[kJoinAtOnce];
+    float4 v[kJoinAtOnce][kJoinDims / 4];
+    auto fetch = [&](int k, int slot, bool there) {
         const int64_t at = (int64_t)slot * NQ + i;
-        const float2 ml = p.part_ml[at * kTileRows + row];
-        float4 v[kJoinDims / 4];
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (!there || !mine) return;
+        ml[k] = p.part_ml[at * kTileRows + row];
 #pragma unroll
         for (int x = 0; x < kJoinDims / 4; ++x)
-            v[x] = reinterpret_cast<const float4 *>(p.part_o)[at * (D / 4 * kTileRows) + (d0 / 4 + x) * kTileRows + row];
-        if (ml.y == 0.f) return;  // saw nothing there
-        const float to = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : exp2f(m - to), b = ml.x == -INFINITY ? 1.f : exp2f(ml.x - to);
-        m = to;
-        l = l * a + ml.y * b;
-#pragma unroll
-        for (int x = 0; x < kJoinDims / 4; ++x)
-            o[x] = make_float4(o[x].x * a + v[x].x * b, o[x].y * a + v[x].y * b, o[x].z * a + v[x].z * b, o[x].w * a + v[x].w * b);
+            v[k][x] = reinterpret_cast<const float4 *>(p.part_o)[at * (D / 4 * kTileRows) + (d0 / 4 + x) * kTileRows + row];
     };
-    add(2 * w + 1);
-    for (int u = w + 1; u < p.workers; ++u) {
-        const int head = p.meta[u].head;
-        if (head == 1 || head == 2) add(2 * u);
-        if (head <= 1) break;
+    auto merge = [&](int k) {
+        if (ml[k].y == 0.f) return;  // saw nothing there
+        const float to = fmaxf(m, ml[k].x), a = m == -INFINITY ? 0.f : exp2f(m - to), b = ml[k].x == -INFINITY ? 1.f : exp2f(ml[k].x - to);
+        m = to;
+        l = l * a + ml[k].y * b;
+#pragma unroll
+        for (int x = 0; x < kJoinDims / 4; ++x)
+            o[x] = make_float4(o[x].x * a + v[k][x].x * b, o[x].y * a + v[k][x].y * b, o[x].z * a + v[k][x].z * b, o[x].w * a + v[k][x].w * b);
+    };
+    fetch(0, 2 * w + 1, true);
+    merge(0);
+    // the workers after it, 32 at a time: those that have a part, up to the one with the unit's end
+    const int lane = threadIdx.x & 31;
+    for (int u0 = w + 1; u0 < p.workers; u0 += 32) {
+        const int head = u0 + lane < p.workers ? p.meta[u0 + lane].head : 0;
+        const uint32_t ends = __ballot_sync(0xffffffffu, head <= 1), until = ends ? __ffs(ends) - 1 : 31;
+        uint32_t parts = __ballot_sync(0xffffffffu, head == 1 || head == 2) & (0xffffffffu >> (31 - until));
+        while (parts) {
+#pragma unroll
+            for (int k = 0; k < kJoinAtOnce; ++k) {
+                const int at = __ffs(parts) - 1;
+                fetch(k, 2 * (u0 + (at < 0 ? 0 : at)), at >= 0);
+                parts &= parts - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAtOnce; ++k) merge(k);
+        }
+        if (ends) break;
     }
+    if (!mine) return;
     const int64_t trow = meta.row0 + tok;
     const int hq = meta.h * p.G + row % p.G;
     const float inv = 1.f / l;
