@@ -25,7 +25,7 @@
 namespace kvs {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Side {
     const void *x;

@@ -983,52 +983,63 @@ class Rotary:
         """Rows q [..., Hq, D] and k [..., Hk, D] (float32, float16 or bfloat16; rows may be strided) turned to pos [...]
         (int32 or int64): (q', k'), new tensors or those of out = (q', k'), which may be q and k themselves.  k' is None
         without k.  The results carry no gradient."""
-        n, dt, sides, outs = self._rows(pos, q, k, out, None, None)
-        _run(self.device, self._lib.kvs_rotate, self._ref, pos.data_ptr(), pos.element_size(), n, dt, *sides)
-        return outs
+        n, size = self._positions(pos, q)
+        to_q, to_k = (None, None) if out is None else self._out(out, k)
+        q_ref, to_q = self._side(q, to_q, None, q.dtype, pos.shape)
+        k_ref, to_k = (None, None) if k is None else self._side(k, to_k, None, q.dtype, pos.shape)
+        _run(self.device, self._lib.kvs_rotate, self._ref, pos.data_ptr(), size, n, _dtype_of(q), q_ref, k_ref)
+        return to_q, to_k
 
     def norm_rotate(self, pos, q, k=None, q_weight=None, k_weight=None, eps=1e-6, out=None):
         """The same after the norm of every head, x / sqrt(mean(x^2) + eps) * weight: weights [D], None for ones."""
-        n, dt, sides, outs = self._rows(pos, q, k, out, q_weight, k_weight)
+        n, size = self._positions(pos, q)
         w = q_weight if q_weight is not None else k_weight
-        _run(self.device, self._lib.kvs_norm_rotate, self._ref, pos.data_ptr(), pos.element_size(), n, dt, *sides,
-             KVS_F32 if w is None else _dtype_of(w), eps)
-        return outs
-
-    def _rows(self, pos, q, k, out, q_weight, k_weight):
-        dev, d, lead = self.device, self.head_dim, pos.shape
-        if pos.dtype not in (_torch.int32, _torch.int64) or pos.device != dev or not pos.is_contiguous() or not 1 <= len(lead) <= 2:
-            raise ValueError(f"pos must be a contiguous int32 or int64 tensor on {dev}, of one or two dimensions")
-        if out is not None and len(out) != 2:
-            raise ValueError("out must be (q', k')")
-        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
             raise ValueError("q_weight and k_weight must have one dtype")
-        dt, refs, outs = _dtype_of(q), [], []
-        for i, (x, w) in enumerate(((q, q_weight), (k, k_weight))):
-            if x is None:
-                if out is not None and out[i] is not None:
-                    raise ValueError("out has a tensor for rows that are not given")
-                refs.append(None)
-                outs.append(None)
-                continue
-            shape = x.shape
-            if shape[:-2] != lead or len(shape) != len(lead) + 2 or shape[-1] != d or x.dtype != q.dtype or x.device != dev:
-                raise ValueError("q and k must be [..., heads, head_dim] of one dtype on the plan's device, pos their leading sizes")
-            if w is not None:
-                _need(w, "weight", w.dtype, dev, (d,))
-                _dtype_of(w)
-            if out is None:
-                y = _torch.empty(shape, dtype=x.dtype, device=dev)
-                y_stride = shape[-2] * d
-            else:
-                y = out[i]
-                if y is None or y.shape != shape or y.dtype != x.dtype or y.device != dev:
-                    raise ValueError("out must be as q and k")
-                y_stride = _row_stride(y, "out")
-            refs.append(ctypes.byref(kvs_head_rows(x.data_ptr(), y.data_ptr(), _row_stride(x, "k" if i else "q"), y_stride, shape[-2],
-                                                   w.data_ptr() if w is not None else None)))
-            outs.append(y)
-        return pos.numel(), dt, refs, tuple(outs)
+        if k is None and k_weight is not None:
+            raise ValueError("k_weight is of rows that are not given")
+        to_q, to_k = (None, None) if out is None else self._out(out, k)
+        q_ref, to_q = self._side(q, to_q, q_weight, q.dtype, pos.shape)
+        k_ref, to_k = (None, None) if k is None else self._side(k, to_k, k_weight, q.dtype, pos.shape)
+        _run(self.device, self._lib.kvs_norm_rotate, self._ref, pos.data_ptr(), size, n, _dtype_of(q), q_ref, k_ref,
+             KVS_F32 if w is None else _dtype_of(w), eps)
+        return to_q, to_k
+
+    def _positions(self, pos, q):
+        """Rows, and bytes of a position."""
+        dtype, shape = pos.dtype, pos.shape
+        size = 8 if dtype is _torch.int64 else 4 if dtype is _torch.int32 else 0
+        dims = len(shape)
+        if not size or not 1 <= dims <= 2 or pos.device != self.device or not pos.is_contiguous():
+            raise ValueError(f"pos must be a contiguous int32 or int64 tensor on {self.device}, of one or two dimensions")
+        return shape[0] if dims == 1 else shape[0] * shape[1], size
+
+    @staticmethod
+    def _out(out, k):
+        if len(out) != 2 or out[0] is None or (out[1] is None) != (k is None):
+            raise ValueError("out must be (q', k') as the rows that are given")
+        return out
+
+    def _side(self, x, y, w, dtype, lead):
+        """The library's description of rows and their output, and the output."""
+        shape, d = x.shape, self.head_dim
+        dims = len(lead)
+        if len(shape) != dims + 2 or shape[-1] != d or shape[0] != lead[0] or (dims == 2 and shape[1] != lead[1]) or \
+                x.dtype is not dtype or x.device != self.device:
+            raise ValueError("q and k must be [..., heads, head_dim] of one dtype on the plan's device, pos their leading sizes")
+        heads = shape[-2]
+        if y is None:
+            y = x.new_empty(shape)
+            y_stride = heads * d
+        else:
+            if y.shape != shape or y.dtype is not dtype or y.device != self.device:
+                raise ValueError("out must be as q and k")
+            y_stride = _row_stride(y, "out")
+        if w is not None:
+            _need(w, "weight", w.dtype, self.device, (d,))
+            _dtype_of(w)
+            w = w.data_ptr()
+        return ctypes.byref(kvs_head_rows(x.data_ptr(), y.data_ptr(), _row_stride(x, "rows"), y_stride, heads, w)), y
 
 
 def _rotary_freqs(rot, base, scaling, factor, context, fast, slow):
