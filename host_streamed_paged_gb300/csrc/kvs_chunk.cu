@@ -53,7 +53,7 @@ constexpr int kMaxGroup = 64;
 constexpr int kWorkers = 152;  // sizes the workspace; a launch has no more CTAs
 constexpr int BN = 64;         // keys of a block
 constexpr int kFacs = 16;      // blocks whose factors are held: more than the stages and score buffers between the roles
-constexpr float kUp = 7.f;     // weights are held as high as f16 reaches, 2^(8 + kUp) at most
+constexpr float kUp = 4.f;     // a weight at the reference is 2^kUp: f16 reaches 2^11 above it and 2^28 below
 
 struct ChunkParams {
     Q4Pool pool;
@@ -83,7 +83,7 @@ struct ChunkMeta {
 // ---------------------------------------------------------------- the line of work
 
 // A unit costs kUnitCost for its beginning and end, and its keys.
-constexpr int kUnitCost = 384;
+constexpr int kUnitCost = 768;
 constexpr int kMinCost = 256;  // of a worker, while that leaves some idle
 static_assert(BN == 64, "blocks of keys are found by shifts");
 
@@ -127,6 +127,10 @@ struct Piece {
     int from;   // the first row's window begins here: tokens before it, but for the first `sinks`, no row of the unit sees
 };
 
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of numbers not below 0, short where both are
+    return (a | b) >> 32 ? (int64_t)((uint64_t)a / (uint64_t)b) : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 struct Line {
     Seq q;
     int s, h, x;
@@ -138,7 +142,7 @@ struct Line {
         int64_t W = (total + kMinCost - 1) / kMinCost;
         W = W < p.workers ? W : p.workers;
         if (w >= W) return false;
-        const int64_t each = total / W, more = total - each * W;
+        const int64_t each = quotient(total, W), more = total - each * W;
         pos = w * each + (w < more ? w : more);
         end = (w + 1) * each + (w + 1 < more ? w + 1 : more);
         int lo = 0, hi = p.n_seq - 1;  // the last sequence that begins at or before pos (one with rows: the next begins after)
@@ -150,7 +154,7 @@ struct Line {
         s = lo;
         q.load(p, s, tile_tokens, tiles);
         const int64_t in = pos - prefix[s], per = q.before(q.X);
-        h = (int)(in / per);
+        h = (int)quotient(in, per);
         const int64_t rem = in - h * per;
         lo = 0, hi = q.X - 1;
         while (lo < hi) {
@@ -179,7 +183,7 @@ struct Line {
             nblk = front + (int)(last >> 6) + 1 - first;
         }
         auto block = [&](int64_t at) {
-            return at <= kUnitCost ? 0 : at == c ? nblk : (int)((uint64_t)((at - kUnitCost) * nblk) / (uint64_t)(c - kUnitCost));
+            return at <= kUnitCost ? 0 : at == c ? nblk : (int)quotient((at - kUnitCost) * nblk, c - kUnitCost);
         };
         o->lo = block(o1);
         o->hi = block(o2);
@@ -309,7 +313,9 @@ struct ChunkShape {
     static constexpr int kOffPiece = kOffFac + 3 * kFacs * 8;
     static constexpr int kOffBar = kOffPiece + (kThreads / 32) * (int)sizeof(Walk);
     static constexpr int kOffRows = (kOffBar + 320 + 15) / 16 * 16;  // by row: largest query element, sum [2], reference
-    static constexpr int kSmem = kOffRows + 5 * kTileRows * 4 + 1024;
+    static constexpr int kOffStage = kOffRows + 5 * kTileRows * 4;  // 2 KB a softmax warp: 32 rows x 64 bytes on their way between memory and threads
+    static constexpr int kSmem = kOffStage + 8 * 2048 + 1024;
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
     static constexpr uint32_t kColO = 256, kColQ = D == 256 ? 128 : 384;
     static_assert(kStages > 5, "see where the dequantising warps take turns");
     static_assert(kStages * kStage >= (kMaxSeq + 1) * 8, "the line's prefix sums lie in the ring");
@@ -373,7 +379,13 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     auto next_piece = [&] {
         bool more = false;
         __syncwarp();
-        if (any && lane == 0) more = walk->line.next(p, TQ, NQ, &walk->piece);
+        if (any && lane == 0) {
+            Line line = walk->line;  // (in registers: its fields come in together)
+            Piece next;
+            more = line.next(p, TQ, NQ, &next);
+            if (more) walk->piece = next;
+            walk->line = line;
+        }
         more = __shfl_sync(0xffffffffu, more, 0);
         __syncwarp();
         return more;
@@ -669,18 +681,35 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         auto done_wait = [&] { asm volatile("bar.sync %0, 256;" ::"r"(3 - wg) : "memory"); };
         auto done_tell = [&] { asm volatile("bar.arrive %0, 256;" ::"r"(2 + wg) : "memory"); };
         auto one_tile = [&](const Piece &c) { return NQ == 1 || c.x * TU + TQ >= c.n; };  // both warpgroups on tile 0
+        // 16 bytes k of row r of the warp's stage, where 8 neighbours read or write all banks once
+        uint4 *stage = reinterpret_cast<uint4 *>(smem + S::kOffStage + warp * 2048);
+        auto staged = [&](int r, int k) { return stage + r * 4 + (k ^ (r >> 1 & 3)); };
         // The row's queries as f16 times a power of two, dims of each 32-dim block in the order of a K row: even ones of the
         // first 16, odd ones, even ones of the last 16, odd ones.  With one tile a warpgroup loads half of the dims (D 64: the
         // first all).
         auto load_dims = [&](auto dims, const Piece &c, int tile, int d0, bool mine, bool shared) {
             constexpr int N = decltype(dims)::value;
-            const int tok = c.x * TU + tile * TQ + row / G;
-            const bool valid = mine && row < TQ * G && tok < c.n;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                               (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + hg) * D + d0 : 0));
             uint4 v[N / 8];
+            // four lanes read 64 bytes of a row, and a row's thread gets them through the warp's stage (each thread reading its
+            // own row took 7000 clocks a unit, 32 lines to an instruction)
 #pragma unroll
-            for (int x = 0; x < N / 8; ++x) v[x] = valid ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 4; ++k) {
+                const int r = (row & 96) + 8 * k + (lane >> 2), tok = c.x * TU + tile * TQ + r / G;
+                const bool valid = mine && r < TQ * G && tok < c.n;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(p.q) + (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + r % G) * D + d0 + 8 * (lane & 3) : 0));
+#pragma unroll
+                for (int x = 0; x < N / 32; ++x) v[4 * x + k] = valid ? __ldg(src + 4 * x) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < N / 32; ++x) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) *staged(8 * k + (lane >> 2), lane & 3) = v[4 * x + k];
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * x + k] = *staged(lane, k);
+            }
             uint32_t top2 = 0;
 #pragma unroll
             for (int x = 0; x < N / 8; ++x) {
@@ -968,7 +997,13 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 const int64_t trow = c.begin + tok;
                 const int hq = c.h * G + hg;
                 const float inv = 1.f / l;
-                uint4 *dst = reinterpret_cast<uint4 *>(out_row(trow, hq));
+                // rows go out through the warp's stage as the queries came in, 64 bytes of a row by four lanes
+                uint16_t *dst[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = (row & 96) + 8 * k + (lane >> 2), rtok = ft + r / G;
+                    dst[k] = r < TQ * G && rtok < c.n ? out_row(c.begin + rtok, c.h * G + r % G) + 8 * (lane & 3) : nullptr;
+                }
 #pragma unroll 1
                 for (int x = x0; x < x1; x += 32) {
                     uint32_t v[32] = {};
@@ -976,20 +1011,23 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         tmem_ld32(to + x, v);
                         tmem_wait_ld();
                     }
-                    if (valid) {
+                    __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            uint32_t o[4];
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t o[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                // a row that saw nothing: out 0, lse -inf
-                                const float a = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y]) * inv;
-                                const float z = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y + 1]) * inv;
-                                o[y] = p.bf16 ? pack<true>(a, z) : pack<false>(a, z);
-                            }
-                            dst[(x + k) / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int y = 0; y < 4; ++y) {
+                            // a row that saw nothing: out 0, lse -inf
+                            const float a = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y]) * inv;
+                            const float z = l == 0.f ? 0.f : __uint_as_float(v[k + 2 * y + 1]) * inv;
+                            o[y] = p.bf16 ? pack<true>(a, z) : pack<false>(a, z);
                         }
+                        *staged(lane, k / 8) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + x) = *staged(8 * k + (lane >> 2), lane & 3);
                 }
                 if (valid && x0 == 0 && p.lse) p.lse[trow * p.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l) - kUp) * 0.693147180559945309f;
             } else {
