@@ -53,7 +53,7 @@ constexpr int kMaxGroup = 64;
 constexpr int kWorkers = 152;  // sizes the workspace; a launch has no more CTAs
 constexpr int BN = 64;         // keys of a block
 constexpr int kFacs = 16;      // blocks whose factors are held: more than the stages and score buffers between the roles
-constexpr float kUp = 4.f;     // a weight at the reference is 2^kUp: f16 reaches 2^11 above it and 2^28 below
+constexpr float kUp = 2.f;     // a weight at the reference is 2^kUp: f16 reaches 2^13 above it and 2^26 below
 
 struct ChunkParams {
     Q4Pool pool;
@@ -83,7 +83,7 @@ struct ChunkMeta {
 // ---------------------------------------------------------------- the line of work
 
 // A unit costs kUnitCost for its beginning and end, and its keys.
-constexpr int kUnitCost = 768;
+constexpr int kUnitCost = 1024;
 constexpr int kMinCost = 256;  // of a worker, while that leaves some idle
 static_assert(BN == 64, "blocks of keys are found by shifts");
 
@@ -302,8 +302,11 @@ struct ChunkShape {
     // warpgroups: two of softmax, two that dequantise, one whose first warps issue the MMAs
     static constexpr int kThreads = 640, kFirstDeq = 8, kFirstMma = 16;
     // of the registers at launch the softmax takes what the others leave
-    static constexpr int kSoftmaxRegs = D == 256 ? 128 : 144, kDeqRegs = D == 256 ? 88 : 72, kMmaRegs = 48;
-    static_assert(2 * kSoftmaxRegs + 2 * kDeqRegs + kMmaRegs <= kThreads / 128 * 96, "96 registers a thread at launch");
+    static constexpr int kSoftmaxRegs = D == 256 ? 120 : 144, kDeqRegs = D == 256 ? 96 : 72, kMmaRegs = 48;
+    static constexpr int kLaunchRegs = 96;
+    static_assert(2 * kSoftmaxRegs + 2 * kDeqRegs + kMmaRegs <= kThreads / 128 * kLaunchRegs, "more registers than at launch are never had");
+    // (giving back to a number above the launch's, or taking up to one below it, is an illegal instruction)
+    static_assert(kSoftmaxRegs >= kLaunchRegs && kDeqRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs, "the softmax takes, the others give");
     static constexpr int kLines = D / 32;               // 16-byte words of codes of a lane: of a tile's K or V
     static constexpr int kStage = BN * D * 2;
     static constexpr int kStages = D == 256 ? 6 : 8;
@@ -671,7 +674,9 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         const int wg = warp >> 2, row = tid & 127, hg = row % G;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float nan = __int_as_float(0x7fc00000);
-        float *row_top = reinterpret_cast<float *>(smem + S::kOffRows) + row, *row_sum = row_top + 2 * kTileRows, *row_ref = row_sum + 2 * kTileRows;
+        uint32_t *tops = reinterpret_cast<uint32_t *>(smem + S::kOffRows);
+        float *row_sum = reinterpret_cast<float *>(tops + 2 * kTileRows) + row, *row_ref = row_sum + 2 * kTileRows;
+        auto out_of_q = [&](int64_t trow, int hq) { return static_cast<const uint16_t *>(p.q) + (trow * p.q_stride + (int64_t)hq * D); };
         float fac = 0.f;
         uint32_t ring = 0, blocks0 = 0, blocks1 = 0, all_blocks = 0;  // so far: stages, blocks of tile 0, of tile 1, of the CTA
         bool ok = true;  // (every warp goes on to the end of the line whatever it has given up: the barriers count them all)
@@ -684,20 +689,18 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         // 16 bytes k of row r of the warp's stage, where 8 neighbours read or write all banks once
         uint4 *stage = reinterpret_cast<uint4 *>(smem + S::kOffStage + warp * 2048);
         auto staged = [&](int r, int k) { return stage + r * 4 + (k ^ (r >> 1 & 3)); };
-        // The row's queries as f16 times a power of two, dims of each 32-dim block in the order of a K row: even ones of the
-        // first 16, odd ones, even ones of the last 16, odd ones.  With one tile a warpgroup loads half of the dims (D 64: the
-        // first all).
+        // The unit's queries as f16 times a power of two a row, dims of each 32-dim block in the order of a K row: even ones of
+        // the first 16, odd ones, even ones of the last 16, odd ones.  A warpgroup loads its tile's; with one tile half of the
+        // dims each (D 64: the first all).  Four lanes read 64 bytes of a row, and a row's thread gets them through the warp's
+        // stage.
         auto load_dims = [&](auto dims, const Piece &c, int tile, int d0, bool mine, bool shared) {
             constexpr int N = decltype(dims)::value;
             uint4 v[N / 8];
-            // four lanes read 64 bytes of a row, and a row's thread gets them through the warp's stage (each thread reading its
-            // own row took 7000 clocks a unit, 32 lines to an instruction)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = (row & 96) + 8 * k + (lane >> 2), tok = c.x * TU + tile * TQ + r / G;
                 const bool valid = mine && r < TQ * G && tok < c.n;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const uint16_t *>(p.q) + (valid ? (int64_t)(c.begin + tok) * p.q_stride + (int64_t)(c.h * G + r % G) * D + d0 + 8 * (lane & 3) : 0));
+                const uint4 *src = reinterpret_cast<const uint4 *>(out_of_q(valid ? c.begin + tok : 0, valid ? c.h * G + r % G : 0) + d0 + 8 * (lane & 3));
 #pragma unroll
                 for (int x = 0; x < N / 32; ++x) v[4 * x + k] = valid ? __ldg(src + 4 * x) : make_uint4(0, 0, 0, 0);
             }
@@ -716,14 +719,13 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 top2 = __vmaxu2(__vmaxu2(top2, v[x].x & 0x7fff7fffu), v[x].y & 0x7fff7fffu);
                 top2 = __vmaxu2(__vmaxu2(top2, v[x].z & 0x7fff7fffu), v[x].w & 0x7fff7fffu);
             }
-            const uint32_t top = (top2 & 0xffffu) > (top2 >> 16) ? (top2 & 0xffffu) : (top2 >> 16);
-            float top_f = p.bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
-            if (shared) {  // (an infinity or NaN comes out as one: by the bits)
-                row_top[wg * kTileRows] = top_f;
+            uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+            if (shared) {
+                tops[wg * kTileRows + row] = top;
                 sync_all();
-                const float a = row_top[0], b = row_top[kTileRows];
-                top_f = __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+                top = max(tops[row], tops[kTileRows + row]);
             }
+            const float top_f = p.bf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
             int e = (int)(__float_as_uint(top_f) >> 23) - 127;
             e = e < -100 ? -100 : (e > 100 ? 100 : e);
             const float f = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), p.scale_log2);
@@ -777,6 +779,15 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 load_dims(std::integral_constant<int, D>{}, c, wg, 0, true, false);
             }
         };
+        // the queries of the piece after this one, towards the caches: a line a lane
+        auto expect_queries = [&](const Piece &c) {
+            constexpr int kLinesOfRow = D / 64;  // of 128 bytes
+            for (int x = tid & 255; x < NQ * kTileRows * kLinesOfRow; x += 256) {
+                const int r = x / kLinesOfRow, tile = r / kTileRows, tok = c.x * TU + tile * TQ + r % kTileRows / G;
+                if (r % kTileRows < TQ * G && tok < c.n)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(out_of_q(c.begin + tok, c.h * G + r % kTileRows % G) + 64 * (x % kLinesOfRow)));
+            }
+        };
         auto out_row = [&](int64_t trow, int hq) { return static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D); };
         // the next piece with work, rows that see nothing written on the way
         auto find_work = [&] {
@@ -807,6 +818,9 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         if (work) load_queries(*piece);
         while (work) {
             const Piece c = *piece;
+            __syncwarp();
+            work = find_work();  // the next
+            if (work) expect_queries(*piece);
             const bool shared = one_tile(c);
             const int i = shared ? 0 : wg;  // the tile
             const int n = c.hi - c.lo, ft = c.x * TU + i * TQ, tok = ft + row / G;
@@ -814,6 +828,8 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             const int pos0 = c.T - c.n, pos = pos0 + tok;
             const int pf = pos0 + ft, pl = max(pos0 + min(ft + TQ, c.n) - 1, -1);  // positions of the tile's first and last row
             const int masked_from = ((pf + 1) >> 6) - c.first + c.front - c.lo;  // (pf + 1) / BN: blocks from there reach past a row
+            // and under a window the first tokens' blocks and those where some row's window begins
+            const int masked_to = p.window ? max(((pl - p.window) >> 6) + 1 - c.first, 0) + c.front - c.lo : 0;
             const uint32_t first_block = i ? blocks1 : blocks0;
             float m = -INFINITY, l = 0.f;
             // what a block needs beside its scores: K's factors times the row's, V's exponents and their factors, of its two tiles
@@ -836,7 +852,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             float part[2];  // sums of the two tiles' weights
             auto load_half = [&](int j, int x) { tmem_ld32(scores_at(j) + 32 * x, reinterpret_cast<uint32_t *>(s) + 32 * x); };
             auto mask = [&](int j, int h) {  // of 32 keys
-                if (j < masked_from && !p.window) return;
+                if (j < masked_from && j >= masked_to) return;
                 const int b = c.lo + j, k0 = (b < c.front ? b : c.first + b - c.front) * BN + 32 * h;
                 if (j >= masked_from) {  // some row of the tile ends inside the block
                     const int lim = pos - k0;
@@ -871,11 +887,11 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 part[x] = both.x + both.y;
             };
             // The weights' sum bounds each of them: while it is below 2^15 none passes f16, and the reference (a maximum seen
-            // before) stands.  Else, and for a row's first key, the block's maximum is looked for; false: a wait gave up.
+            // before) stands.  Else, and for a row's first key, the block's maximum (of scores loaded again) becomes it and the weights are formed anew; false: a wait
+            // gave up.
             auto must_grow = [&] { return __any_sync(0xffffffffu, m == -INFINITY || !(part[0] + part[1] <= 32768.f)); };
             auto grow_reference = [&](int j, const Factors &f) {
                 const bool over = m == -INFINITY || !(part[0] + part[1] <= 32768.f);
-                load_scores(j);  // (S is still there)
                 float top[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -909,8 +925,6 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         }
                     }
                 }
-                weights(f, 0);
-                weights(f, 1);
                 return done;
             };
             auto publish = [&](int j, const Factors &f) {
@@ -926,29 +940,29 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                     if (ok) ok = wait_warp(abort, [&] { return ready(j); });
                     tc_after();
                     const Factors f = factors(j);
-                    if (ok) {
-                        load_scores(j);
-                        weights(f, 0);
-                        weights(f, 1);
-                    }
-                    bool stale = false;
-                    if (j > 0) {  // the block before is done: its reference is the one that stands
-                        done_wait();
-                        const float now = *row_ref;
-                        stale = now != m;
-                        if (stale) {
-                            l = m == -INFINITY ? l : l * ex2(m - now);
-                            m = now;
-                        }
-                    }
-                    if (ok) {
-                        if (__any_sync(0xffffffffu, stale)) {
-                            load_scores(j);
+                    bool before = j > 0, grown = false;  // the block before is yet to be heard of; the reference has grown for this one
+                    do {
+                        if (ok) {
+                            load_scores(j);  // (S stays until its P is stored)
                             weights(f, 0);
                             weights(f, 1);
                         }
-                        if (must_grow()) ok = grow_reference(j, f);
-                    }
+                        if (before) {  // it is done: its reference is the one that stands
+                            before = false;
+                            done_wait();
+                            const float now = *row_ref;
+                            const bool stale = now != m;
+                            if (stale) {
+                                l = m == -INFINITY ? l : l * ex2(m - now);
+                                m = now;
+                            }
+                            if (__any_sync(0xffffffffu, stale)) continue;
+                        }
+                        if (!ok || grown || !must_grow()) break;
+                        load_scores(j);
+                        ok = grow_reference(j, f);
+                        grown = true;
+                    } while (true);
                     if (ok) publish(j, f);
                     *row_ref = m;
                     if (j + 1 < n) done_tell();
@@ -959,13 +973,16 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                     if (!ok) break;
                     tc_after();
                     const Factors f = factors(j);
-                    load_scores(j);
-                    weights(f, 0);
-                    weights(f, 1);
-                    if (must_grow()) {
+                    for (bool grown = false;; grown = true) {
+                        load_scores(j);  // (S stays until its P is stored)
+                        weights(f, 0);
+                        weights(f, 1);
+                        if (grown || !must_grow()) break;
+                        load_scores(j);
                         ok = grow_reference(j, f);
                         if (!ok) break;
                     }
+                    if (!ok) break;
                     publish(j, f);
                 }
             }
@@ -981,7 +998,6 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                 m = now;
             }
             // the next queries go in before this unit's output comes out: its scores are all read
-            work = find_work();
             if (work) load_queries(*piece);
             if (shared) {
                 sync_all();

@@ -4,9 +4,11 @@ Tolerances, from the arithmetic the kernel states; A = sum p |v|, u the half ste
 - K is rounded to f16 once (2^-11 of each value) and a score's products are summed in fp32 by the tensor core, 16 at a
   time, each sum cut off below 2^-23 of it: a score is off by at most E = (2^-11 + 16 2^-22) max scale sum |q k|, its
   weight by a factor e^E, in numerator and denominator: expm1(2 E) A of the output, E of lse;
-- V and the weights are rounded to f16 once: 2 2^-11 A; weights below 2^-14 of what f16 holds lose up to 2^-25 each, where
-  the largest is at least 2^7 and V's values, brought to a common power of two, at most 2^5: n 2^-25 2^5 2^-7 in those
-  units, n 2^-28 max|v| with the largest V at 2^1 of them or more;
+- V and the weights are rounded to f16 once: 2 2^-11 A; weights below f16's 2^-14 lose up to 2^-25 each, where a row's
+  largest weight is at least 2^2 (times its tile's power of two) and V's values, brought to their tile's power of two, at
+  most 2^-2: n 2^-27 of those units; the largest weight's tile holds a value of 2^-3 of them or more, so that is at most
+  n 2^-27 2^3 2^-2 = n 2^-26 max|v| of the output; values below 2^-14 of their units, 2^-12 of the tile's largest, are off by
+  2^-25, 2^-23 of the largest, which 2^-11 of it in A's place covers where weights are as large, and n 2^-26 max|v| else;
 - outputs are summed in fp32, 16 tokens at a time, and rescaled: (n / 16 + 32) 2^-22 A;
 - out is rounded: u |out|; lse adds the exponentials' and the logarithm's 1e-5.
 """
@@ -47,7 +49,7 @@ def check(out, lse, q, cu, filled, dt, scale, window=0, sinks=0, skip=()):
         ro, rz, A, most = window_ref.rows(qn[s], k, v, T - n + np.arange(n), scale, window, sinks)
         E = (2.0 ** -11 + 2.0 ** -18) * most
         top = np.abs(v).max(initial=0)
-        tol = u * np.abs(ro) + (np.expm1(2 * E)[..., None] + 2.0 ** -10 + (T / 16 + 32) * 2.0 ** -22) * A + T * 2.0 ** -28 * top
+        tol = u * np.abs(ro) + (np.expm1(2 * E)[..., None] + 2.0 ** -10 + (T / 16 + 32) * 2.0 ** -22) * A + T * 2.0 ** -26 * top
         bad = ~(np.abs(o[s] - ro) <= tol)
         assert not bad.any(), (i, n, T, np.argwhere(bad)[:4], np.nanmax(np.abs(o[s] - ro) / np.maximum(tol, 1e-300)))
         none = rz == -np.inf
