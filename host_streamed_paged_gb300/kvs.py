@@ -1029,7 +1029,7 @@ class Rotary:
             raise ValueError("q and k must be [..., heads, head_dim] of one dtype on the plan's device, pos their leading sizes")
         heads = shape[-2]
         if y is None:
-            y = x.new_empty(shape)
+            y = _torch.empty(shape, dtype=dtype, device=self.device)
             y_stride = heads * d
         else:
             if y.shape != shape or y.dtype is not dtype or y.device != self.device:
