@@ -162,6 +162,18 @@ def test_many_sequences():
     run(Filled(lens, 2, 64, 32, seed=1, dt="bf16"), rows, 2, 3, 64, "bf16")
 
 
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 3), (256, 5)])
+def test_many_short_units(D, G):
+    """Units of one to a few blocks, of one query tile and of two, one after another in every worker: the stages' and
+    buffers' phases go on from unit to unit."""
+    rng = np.random.default_rng(D)
+    lens = rng.integers(1, 200, 300).tolist()
+    rows = [int(rng.integers(0, min(n, 90) + 1)) for n in lens]
+    f = Filled(lens, 2, D, 32, seed=1, dt="bf16")
+    run(f, rows, 2, G, D, "bf16")
+    run(f, rows, 2, G, D, "bf16", window=40, sinks=3)
+
+
 def test_the_most_sequences():
     lens = [(7 * i) % 40 for i in range(4096)]
     rows = [min(n, 1 + i % 2) for i, n in enumerate(lens)]
