@@ -21,6 +21,7 @@
 
 #include "kvs.h"
 #include "kvs_internal.h"
+#include "kvs_tcgen05.cuh"
 
 namespace kvs {
 namespace {
@@ -48,6 +49,14 @@ struct RotaryParams {
     float eps;
 };
 
+using tc::fma2;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&r))
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+    return r;
+}
 __device__ __forceinline__ float2 two(uint32_t w, bool bf16) {
     if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
@@ -172,16 +181,17 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] = 1.f;
             }
-            auto mean_square = [&](float f) {
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum = fmaf(x[j] * f, x[j] * f, sum);
+            auto over_head = [&](float sum) {
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 return sum * (1.f / D);
             };
-            const float v = mean_square(1.f) + p.eps;
-            float inv = __frsqrt_rn(v);
+            float2 *x2 = reinterpret_cast<float2 *>(x), square = mul2(x2[0], x2[0]);
+#pragma unroll
+            for (int j = 1; j < 8; ++j) square = fma2(x2[j], x2[j], square);
+            const float v = over_head(square.x + square.y) + p.eps;
+            float inv = rsqrtf(v);
+            inv = fmaf(inv * 0.5f, fmaf(-v * inv, inv, 1.f), inv);  // (one step of Newton's)
             const bool odd = !(v >= 7.9e-31f && v <= 1.3e36f);  // squares near or past fp32's ends: 2^-100, 2^120
             if (__any_sync(0xffffffffu, odd)) {
                 // again with the head's largest element brought to 1 .. 2
@@ -193,11 +203,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 int e = (int)(__float_as_uint(top) >> 23) - 127;
                 e = e < -120 ? -120 : (e > 120 ? 120 : e);
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float again = __frsqrt_rn(mean_square(f) + p.eps * f * f) * f;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum = fmaf(x[j] * f, x[j] * f, sum);
+                const float again = __frsqrt_rn(over_head(sum) + p.eps * f * f) * f;
                 if (odd) inv = again;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = x[j] * inv * w[j];
+            for (int j = 0; j < 8; ++j) x2[j] = mul2(mul2(x2[j], make_float2(inv, inv)), make_float2(w[2 * j], w[2 * j + 1]));
         }
         if (!mine) continue;
         if (turned) {
@@ -210,10 +223,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = x[j], v = x[8 + j];
-                    x[j] = u * c[j] - v * s[j];
-                    x[8 + j] = v * c[j] + u * s[j];
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 u = make_float2(x[j], x[j + 1]), v = make_float2(x[8 + j], x[9 + j]);
+                    const float2 c2 = make_float2(c[j], c[j + 1]), s2 = make_float2(s[j], s[j + 1]), n2 = make_float2(-s[j], -s[j + 1]);
+                    const float2 a2 = fma2(v, n2, mul2(u, c2)), b2 = fma2(u, s2, mul2(v, c2));
+                    x[j] = a2.x, x[j + 1] = a2.y, x[8 + j] = b2.x, x[9 + j] = b2.y;
                 }
             }
         }
