@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             inv = fmaf(inv * 0.5f, fmaf(-v * inv, inv, 1.f), inv);  // (one step of Newton's)
             const bool odd = !(v >= 7.9e-31f && v <= 1.3e36f);  // squares near or past fp32's ends: 2^-100, 2^120
             if (__any_sync(0xffffffffu, odd)) {
-                // again with the head's largest element brought to 1 .. 2
-                float top = 0.f;
+                // again with the larger of the head's largest element and eps's root brought to 1 .. 2
+                float top = sqrtf(p.eps);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
 #pragma unroll

@@ -6,6 +6,7 @@ and sums (3 2^-24), an output is off by at most magnitude (|u| + |v|) 5e-7 befor
 A norm's sum of squares has at most 20 additions in a row, its root half of that error, the products 2 more roundings:
 1.5e-6 of the value.
 """
+import ctypes
 import math
 from fractions import Fraction
 
@@ -168,6 +169,17 @@ def test_norms_of_any_size(dt, size, eps):
     q = (x / x.abs().max() * size).to(_t(dt)).cuda()
     pos = torch.arange(6)
     check(r.norm_rotate(pos.cuda(), q, eps=eps)[0], q, pos.tolist(), r, dt, None, eps)
+
+
+@pytest.mark.parametrize("size,eps", [(1e-36, 1e-32), (1e-37, 7e-31), (1e-30, 1e-38), (1e-38, 1e-45), (1e-36, 1e38)])
+def test_an_eps_of_any_size_beside_the_rows(size, eps):
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    r = kvs.Rotary(128, rot_dim=64)
+    x = torch.randn(5, 3, 128, generator=torch.Generator().manual_seed(4), dtype=torch.float64)
+    q = (x / x.abs().max() * size).float().cuda()
+    pos = torch.arange(5)
+    check(r.norm_rotate(pos.cuda(), q, eps=eps)[0], q, pos.tolist(), r, "f32", None, ctypes.c_float(eps).value)
 
 
 def test_values_that_are_not_finite_stay_with_their_head():
