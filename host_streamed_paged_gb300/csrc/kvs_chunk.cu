@@ -27,10 +27,39 @@
 //
 // Values.  A cached value is (n - 8) * scale.  The tensor core takes K and V as
 // f16 values rounded once, each tile of 32 tokens brought to a common power of
-// two, so that any scale the cache holds keeps f16's precision (down to 2^-12 of
-// what the group's largest scale reaches, and 2^-23 of it below); the power of two returns in the softmax, K's on the scores
-// and V's on the weights before those are rounded to f16.  Queries enter as f16
-// times a power of two per row (exact down to 2^-28 of the row's largest).
+// two, so that any scale the cache holds keeps f16's precision (down to 2^-12
+// of what the group's largest scale reaches, and 2^-23 of it below); the power
+// of two returns in the softmax, K's on the scores and V's on the weights
+// before those are rounded to f16.  Queries enter as f16 times a power of two
+// per row (exact down to 2^-28 of the row's largest).  (Codes as numbers, their
+// scales outside the products, as one-row attention takes them, would need the
+// weights once for every 32 dims.)
+//
+// Bound by the tensor pipe and what feeds it: 4 D operations a (row, key), the
+// cache's bytes being nothing beside them from some 100 rows on.  2048 rows over
+// 65536 tokens (32 / 8 heads, D 128) take 1497 us, 1.44 PFLOP/s, 74% of what
+// bf16 products measure; ncu sees the tensor pipe active on 50% of the cycles
+// (1024 rows over 16384), 58% of the issue slots taken.  A block of both tiles
+// takes 0.92 us; without the softmax's arithmetic and the dequantising, MMAs,
+// hand-overs and loads alone, 0.69; without the dequantising 0.85, without the
+// exponentials 0.78: the chain of a softmax warp (scores out of tensor memory,
+// 64 exponentials, weights back) is the longest.  D 64 runs at 0.82 PFLOP/s, as
+// its products are half as long beside the same exponentials; D 256 at 0.87:
+// room for one tile only, whose chain S, softmax, P V is hidden by the other
+// warpgroup's block alone.
+//
+// What each choice measured (2048 rows over 65536 tokens, unless said):
+//   dequantising by warps of their own instead of the softmax's, one fused
+//     multiply-add a pair, registers split by role: 2372 -> 1731 us;
+//   a standing reference instead of a maximum every block, and tiles of 32
+//     tokens in turns of four warps: 1731 -> 1580;
+//   both warpgroups on a lone tile: 37 rows over 4096 tokens 34 -> 23 us, a
+//     mixed batch (12 sequences, 1 to 777 rows, up to 32768 tokens) 637 -> 539;
+//   rows in and out by four lanes a row (64 bytes), the next unit's queries
+//     asked for early, masks only where a block needs them: the batch
+//     539 -> 368, chunks of up to 1024 rows under a window of 4096 213 -> 139.
+// Blocks of 64 keys: two buffers of S and P, two O of 128 columns and Q (D 64)
+// fill the 512 columns of tensor memory; 128 keys would leave one buffer each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -82,7 +111,10 @@ struct ChunkMeta {
 
 // ---------------------------------------------------------------- the line of work
 
-// A unit costs kUnitCost for its beginning and end, and its keys.
+// A unit costs kUnitCost for its beginning and end, and its keys: 1024 keys are
+// 16 blocks of 0.92 us, a unit's own steps (finding it, its queries in, its
+// outputs out) 13 blocks' time.  (At 512 the mixed batch's longest CTA took 1.02 M
+// clocks beside a median of 0.65 M.)
 constexpr int kUnitCost = 1024;
 constexpr int kMinCost = 256;  // of a worker, while that leaves some idle
 static_assert(BN == 64, "blocks of keys are found by shifts");

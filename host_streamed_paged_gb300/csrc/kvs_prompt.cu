@@ -5,6 +5,14 @@
 // a 128-row MMA tile holds floor(128 / G) tokens of all G heads, read by one
 // TMA box.  So K and V are read once per kv head, short prompts fill tiles,
 // and the causal edge of a tile spans 128 / G keys instead of 128.
+//
+// Windows.  A unit walks the key blocks of the first tokens, then those from its
+// first row's window on; a block's index is all that knows of the gap between
+// them.  The kernels without a window are compiled apart and hold none of it.
+// 8192 + 6001 + 2048 + 513 + 1 tokens under a window of 1024 (32 / 8 heads, D
+// 128, bf16) take 278 us, 0.89 PFLOP/s of seen pairs: a unit is 18 blocks, so a
+// CTA's start and end (one per SM, 14 waves of 20 us) weigh a third of it; ncu:
+// tensor pipe 41%, 36% of the issue slots.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -11,6 +11,18 @@
 // a head, both sides of its 8 pairs, so a pair never crosses lanes and a row may
 // be its own output; D / 16 lanes share a head, and the 512 / D heads that a
 // warp takes at a time share the work of the row's angles.
+//
+// A warp's job is as many of a row's steps (512 elements) as leave the card's
+// warp slots one job each, a whole row from some 5000 rows on: the angles, 8
+// sincospif a lane at most, are formed once a job and the next step's elements
+// are on their way meanwhile.  The arithmetic is in paired fp32 instructions
+// (3000 rows with norms 13.2 -> 11.8 us).
+//
+// Measured: 16755 rows of 24 + 4 heads, D 256, 64 dims rotated, f16: 75.2 us, 6.4
+// TB/s (94% of a copy's rate; ncu: DRAM 73% of its nominal).  With norms, 12001
+// rows of 32 + 8 heads, D 128, bf16: 50.3 us, 4.9 TB/s: 62% of the issue slots
+// taken at 80 registers, so the loads in flight and the instructions bound it
+// together.  A step of 64 rows takes 2.1 us of the GPU, 16 with the call.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -659,8 +659,8 @@ const char *kvs_last_error(const kvs_ctx *ctx);
  * or as a shortened device-side wait limit: no GPU fault is ever made.  With
  * ctx NULL, KVS_FAULT_DEVICE_WAIT is armed for the nth launching call that
  * this thread makes of the batch operators with such waits (kvs_prompt_attend,
- * kvs_prompt_weights, kvs_q4_attend, kvs_q4_weights).  Test API; the pages
- * describe no such call. */
+ * kvs_prompt_weights, kvs_q4_attend, kvs_q4_weights, the first and third under
+ * a window, kvs_q4_attend_chunk).  Test API; the pages describe no such call. */
 kvs_status kvs_debug_inject(kvs_ctx *ctx, uint32_t fault, uint64_t nth);
 
 /* kvs_trace_read -- test API (no counterpart on the pages) for checking the
