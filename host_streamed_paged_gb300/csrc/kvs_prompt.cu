@@ -52,7 +52,7 @@ struct PromptParams {
     float *w;
     int64_t width;
     int last_rows;
-    int window, sinks;  // of the windowed kernels
+    int window, sinks, units;  // of the windowed kernels; units: bound of (tile groups x heads)
     int main_ctas;  // those past them copy what no key writes
     int give_up;    // test hook: the MMA warps give up at their first wait, as if its copy never landed, and *abort is up
 };
@@ -194,7 +194,7 @@ struct AttendShape {
     static constexpr int kStages = D == 64 ? 12 : 10;
     static constexpr int kOffRing = NQ * kQBytes;
     static constexpr int kOffBar = kOffRing + kStages * kPiece;
-    static constexpr int kSmem = kOffBar + 512 + 1024;
+    static constexpr int kSmem = kOffBar + 1024 + 1024;
     static constexpr uint32_t kColO = 256;
 };
 
@@ -208,19 +208,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = smem_u32(smem + S::kOffBar);
-    // barriers: ring full / empty, Q full, final; per tile and score buffer: S full, P full, O done (by the same parity)
+    // barriers: ring full / empty, Q full, final; per tile and score buffer: S full, P full, O done (by the same parity); Q
+    // read by all its MMAs
     auto b_full = [&](int s) { return bars + 8u * s; };
     auto b_empty = [&](int s) { return bars + 8u * (12 + s); };
     const uint32_t b_q = bars + 8u * 24, b_final = bars + 8u * 25;
     auto b_s = [&](int i, int buf) { return bars + 8u * (26 + 2 * i + buf); };
     auto b_p = [&](int i, int buf) { return bars + 8u * (30 + 2 * i + buf); };
     auto b_o = [&](int i, int buf) { return bars + 8u * (34 + 2 * i + buf); };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 38);
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 39);
-    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 40);
+    const uint32_t b_q_read = bars + 8u * 38;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffBar + 8 * 39);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffBar + 8 * 40);
+    int *place = reinterpret_cast<int *>(smem + S::kOffBar + 8 * 41);  // the first unit; [8 (1 + warp)]: a warp's next one
 
     const int G = p.G, TQ = kTileRows / G;
-    const int head = blockIdx.x % p.Hk;
+    int unit = blockIdx.x, head = unit % p.Hk;
     // the work is found, tensor memory allocated and the barriers set up by three warps at once
     if (warp == 9) find_unit(p, blockIdx.x / p.Hk, NQ * TQ, place);
     if (warp == 0) {
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(b_q, 1);
         mbar_init(b_final, NQ);
+        if (WIN) mbar_init(b_q_read, NQ);
         for (int i = 0; i < 4; ++i) {
             mbar_init(b_s(0, i), 1);
             mbar_init(b_p(0, i), 4);
@@ -250,31 +253,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
         return;
     }
-    const int begin = place[2], L = place[3] - begin;
-    const int t0 = place[1] * NQ * TQ;  // first token of tile 0, within the prompt
+    int begin, L, t0;  // of the unit: its prompt's first row and length, tile 0's first token within the prompt
     // under a window the blocks of the first tokens, `front` of them, then those from the first row's window on: block j is
     // j, or j + skip from `front` on
-    int front = 0, skip = 0;
-    if constexpr (WIN) {
-        const int first = t0 >= p.window ? (t0 - p.window + 1) / BN : 0;
-        front = min((p.sinks + BN - 1) / BN, first);
-        skip = first - front;
-    }
+    int front = 0, skip = 0, nblk[2] = {0, 0}, n_max;
     auto key_block = [&](int j) { return WIN && j >= front ? j + skip : j; };
-    int nblk[2] = {0, 0}, n_max = 0;
+    auto set_unit = [&](const int *at) {
+        begin = at[2], L = at[3] - begin;
+        t0 = at[1] * NQ * TQ;
+        if constexpr (WIN) {
+            const int first = t0 >= p.window ? (t0 - p.window + 1) / BN : 0;
+            front = min((p.sinks + BN - 1) / BN, first);
+            skip = first - front;
+        }
+        n_max = 0;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-        const int a = t0 + i * TQ, last = (a + TQ < L ? a + TQ : L) - 1;
-        nblk[i] = a < L ? last / BN + 1 - skip : 0;
-        n_max = nblk[i] > n_max ? nblk[i] : n_max;
-    }
+        for (int i = 0; i < NQ; ++i) {
+            const int a = t0 + i * TQ, last = (a + TQ < L ? a + TQ : L) - 1;
+            nblk[i] = a < L ? last / BN + 1 - skip : 0;
+            n_max = nblk[i] > n_max ? nblk[i] : n_max;
+        }
+    };
+    set_unit(place);
+    // Under a window a CTA takes every gridDim.x-th unit, each warp finding them by itself; what it counts over them:
+    // units, ring stages, blocks of its tile (0 all along in the kernels of one unit)
+    int nth = 0, ring0 = 0, blk0 = 0;
+    auto next_unit = [&] {
+        if constexpr (WIN) {
+            ring0 += 2 * n_max * S::kPieces;
+            ++nth;
+            unit += gridDim.x;
+            if (unit >= p.units) return false;
+            int *at = place + 8 * (1 + warp);
+            __syncwarp();
+            find_unit(p, unit / p.Hk, NQ * TQ, at);
+            __syncwarp();
+            if (at[0] < 0) return false;
+            head = unit % p.Hk;
+            set_unit(at);
+            return true;
+        }
+        return false;
+    };
     // the ring's blocks in the order the MMAs take them: K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
     // kPieces stages each
-    const int n_ring = 2 * n_max * S::kPieces;
-    auto ring_k = [&](int j) { return (j < 2 ? j : 2 * j - 1) * S::kPieces; };
-    auto ring_v = [&](int j) { return (j == n_max - 1 ? 2 * n_max - 1 : 2 * j + 2) * S::kPieces; };
+    auto ring_k = [&](int j) { return ring0 + (j < 2 ? j : 2 * j - 1) * S::kPieces; };
+    auto ring_v = [&](int j) { return ring0 + (j == n_max - 1 ? 2 * n_max - 1 : 2 * j + 2) * S::kPieces; };
     auto load_piece = [&](int r) {
-        const int st = r % NST, q = r / S::kPieces, c = r % S::kPieces, end = 2 * n_max - 1;
+        const int st = (ring0 + r) % NST, q = r / S::kPieces, c = r % S::kPieces, end = 2 * n_max - 1;
         const bool is_v = q == end || (q >= 2 && !(q & 1));
         const int j = key_block(q == end ? n_max - 1 : (q < 2 ? q : (q & 1 ? (q + 1) / 2 : q / 2 - 1)));
         const uint32_t dst = smem_u32(smem + S::kOffRing + st * S::kPiece);
@@ -291,22 +317,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp == 9) {
         // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            mbar_expect(b_q, (uint32_t)(NQ * (D / 64) * 128 * G * TQ));
-            for (int i = 0; i < NQ; ++i)
+        int issued = 0;
+        bool ok = true;
+        do {
+            if (lane == 0) {
+                if (WIN && nth > 0) ok = mbar_wait(b_q_read, (uint32_t)((nth - 1) & 1), abort);
+                if (ok) {
+                    place[6] = nth;
+                    mbar_expect(b_q, (uint32_t)(NQ * (D / 64) * 128 * G * TQ));
+                    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
-            int issued = 0;
-            for (int r = 0; r < n_ring; ++r) {
-                if (r >= NST && !mbar_wait(b_empty(r % NST), (uint32_t)((r / NST - 1) & 1), abort)) break;
-                load_piece(r);
-                issued = r + 1;
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load(smem_u32(smem + i * S::kQBytes + c * kTileRows * 128), &mq, b_q, c * 64, head * G, begin + t0 + i * TQ);
+                }
+                const int n_ring = 2 * n_max * S::kPieces;
+                for (int r = 0; r < n_ring && ok; ++r) {
+                    const int at = ring0 + r;
+                    if (at >= NST && !mbar_wait(b_empty(at % NST), (uint32_t)((at / NST - 1) & 1), abort)) {
+                        ok = false;
+                        break;
+                    }
+                    load_piece(r);
+                    issued = at + 1;
+                }
             }
-            place[5] = issued;
-        }
+        } while (WIN && __shfl_sync(0xffffffffu, ok, 0) && next_unit());
+        if (lane == 0) place[5] = issued;
     } else if (warp == 8 || (NQ == 2 && warp == 10)) {
-        const int i = (warp - 8) >> 1, n = nblk[i];
+        const int i = (warp - 8) >> 1;
+        int n = nblk[i];
         // ------------------------------------------------------------ MMA issue (the warp in step, one elected lane issues)
         constexpr uint32_t id_s = idesc(BF16, kTileRows, BN, false), id_o = idesc(BF16, kTileRows, D, true);
         constexpr int NP = S::kPieces;
@@ -325,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < NP; ++c) mma_commit(b_empty(stage(r, c)));
         };
         auto issue_s = [&](int j) {
-            const uint32_t d = tmem + (uint32_t)((2 * i + (j & 1)) * BN);
+            const uint32_t d = tmem + (uint32_t)((2 * i + ((blk0 + j) & 1)) * BN);
             const uint64_t da = dq + (uint64_t)(i * S::kQBytes >> 4);
             const int r = ring_k(j);
 #pragma unroll
@@ -335,10 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_ss(d, da + (uint64_t)(((s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4), db, id_s, s > 0);
                 if (s % kPer == kPer - 1) mma_commit(b_empty(stage(r, s / kPer)));  // its loads need not wait for the rest
             }
-            mma_commit(b_s(i, j & 1));
+            mma_commit(b_s(i, (blk0 + j) & 1));
+            if (WIN && j == n - 1) mma_commit(b_q_read);
         };
         auto issue_o = [&](int j) {
-            const uint32_t d = tmem + S::kColO + (uint32_t)(i * D), a = tmem + (uint32_t)((2 * i + (j & 1)) * BN);
+            const uint32_t d = tmem + S::kColO + (uint32_t)(i * D), a = tmem + (uint32_t)((2 * i + ((blk0 + j) & 1)) * BN);
             const int r = ring_v(j);
 #pragma unroll
             for (int s = 0; s < BN / 16; ++s) {
@@ -347,174 +387,182 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_ts(d, a + (uint32_t)(8 * s), db, id_o, (j > 0 || s > 0) ? 1u : 0u);
                 if (s % kPer == kPer - 1) mma_commit(b_empty(stage(r, s / kPer)));
             }
-            mma_commit(b_o(i, j & 1));
+            mma_commit(b_o(i, (blk0 + j) & 1));
         };
         // a block past this tile's last one is freed as it comes, for the other tile's sake
         bool ok = !p.give_up;
-        for (int j = 0; j < 2 && j < n_max && ok; ++j) {
-            ok = wait_warp(abort, [&] { return mbar_done(b_q, 0) & loaded(ring_k(j)); });
-            if (!ok) break;
-            tc_after();
-            if (one) {
-                if (j < n) issue_s(j);
-                else freed(ring_k(j));
+        do {
+            n = nblk[i];
+            for (int j = 0; j < 2 && j < n_max && ok; ++j) {
+                ok = wait_warp(abort, [&] { return mbar_done(b_q, (uint32_t)(nth & 1)) & loaded(ring_k(j)); });
+                if (!ok) break;
+                tc_after();
+                if (one) {
+                    if (j < n) issue_s(j);
+                    else freed(ring_k(j));
+                    if (WIN && j == 0 && n == 0) mma_commit(b_q_read);  // (not before its Q has come: an earlier phase may be open)
+                }
             }
-        }
-        // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
-        for (int j = 0; j < n_max && ok; ++j) {
-            const bool more = j + 2 < n_max;
-            ok = wait_warp(abort, [&] {
-                bool all = loaded(ring_v(j));
-                if (j < n) all &= mbar_done(b_p(i, j & 1), (uint32_t)((j >> 1) & 1));
-                if (more) all &= loaded(ring_k(j + 2));
-                return all;
-            });
-            if (!ok) break;
-            tc_after();
-            if (one) {
-                if (j < n) issue_o(j);
-                else freed(ring_v(j));
-                if (j + 2 < n) issue_s(j + 2);
-                else if (more) freed(ring_k(j + 2));
+            // S_{j+2} takes the buffer of S_j and P_j: P_j was read by O's MMA before it, and the pipe keeps their order
+            for (int j = 0; j < n_max && ok; ++j) {
+                const bool more = j + 2 < n_max;
+                ok = wait_warp(abort, [&] {
+                    bool all = loaded(ring_v(j));
+                    if (j < n) all &= mbar_done(b_p(i, (blk0 + j) & 1), (uint32_t)(((blk0 + j) >> 1) & 1));
+                    if (more) all &= loaded(ring_k(j + 2));
+                    return all;
+                });
+                if (!ok) break;
+                tc_after();
+                if (one) {
+                    if (j < n) issue_o(j);
+                    else freed(ring_v(j));
+                    if (j + 2 < n) issue_s(j + 2);
+                    else if (more) freed(ring_k(j + 2));
+                }
             }
-        }
+            blk0 += n;
+        } while (ok && next_unit());
         if (one) mma_commit(b_final);  // on every path: tensor memory is freed only after it
     } else if (warp < 4 * NQ) {
         // ------------------------------------------------------------ softmax, one thread per row
-        const int i = warp >> 2, row = tid & 127, n = nblk[i];
-        const int tok = t0 + i * TQ + row / G;  // within the prompt
-        const bool valid = row < TQ * G && tok < L;
+        const int i = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = p.scale_log2;
         // P is 2^(s - m + kUp), at most 2^(8 + kUp): as high as f16 reaches, so that its smallest step is 2^-31 of the largest
         // weight or less (2^-24 without, and thousands of keys below it are lost from the output); bf16 has the exponents
         constexpr float kUp = BF16 ? 0.f : 7.f;
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
-        const int first_tok = t0 + i * TQ;
-        for (int j = 0; j < n; ++j) {
-            const int buf = j & 1;
-            ok = mbar_wait_warp(b_s(i, buf), (uint32_t)((j >> 1) & 1), abort);
-            if (!ok) break;
-            tc_after();
-            const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
-            uint32_t sr[BN];
+        do {
+            const int n = nblk[i], tok = t0 + i * TQ + row / G;  // within the prompt
+            const bool valid = row < TQ * G && tok < L;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            const int first_tok = t0 + i * TQ;
+            for (int j = 0; (!WIN || ok) && j < n; ++j) {
+                const int buf = (blk0 + j) & 1;
+                ok = mbar_wait_warp(b_s(i, buf), (uint32_t)(((blk0 + j) >> 1) & 1), abort);
+                if (!ok) break;
+                tc_after();
+                const uint32_t ts = lanes + (uint32_t)((2 * i + buf) * BN);
+                uint32_t sr[BN];
 #pragma unroll
-            for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, sr + c);
-            tmem_wait_ld();
-            float *s = reinterpret_cast<float *>(sr);
-            const int kb = key_block(j);
-            if ((kb + 1) * BN > first_tok + 1) {  // some row of the tile ends inside the block
-                const int lim = tok - kb * BN;
+                for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, sr + c);
+                tmem_wait_ld();
+                float *s = reinterpret_cast<float *>(sr);
+                const int kb = key_block(j);
+                if ((kb + 1) * BN > first_tok + 1) {  // some row of the tile ends inside the block
+                    const int lim = tok - kb * BN;
 #pragma unroll
-                for (int c = 0; c < BN; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
-            }
-            if constexpr (WIN) {
-                // some row's window begins behind the block's first key, and not all of its keys are of the first that stay
-                if (kb * BN <= first_tok + TQ - 1 - p.window && (kb + 1) * BN > p.sinks) {
-                    const int from = tok - p.window - kb * BN, stay = p.sinks - kb * BN;
-#pragma unroll
-                    for (int c = 0; c < BN; ++c) s[c] = c > from || c < stay ? s[c] : -INFINITY;
+                    for (int c = 0; c < BN; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
                 }
-            }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (WIN) {
+                    // some row's window begins behind the block's first key, and not all of its keys are of the first that stay
+                    if (kb * BN <= first_tok + TQ - 1 - p.window && (kb + 1) * BN > p.sinks) {
+                        const int from = tok - p.window - kb * BN, stay = p.sinks - kb * BN;
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-            const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sc;
-            const bool grow = mx > m + 8.f || (m == -INFINITY && mx != -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float to = grow ? mx : m;
-                const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
-                l2.x *= alpha;
-                l2.y *= alpha;
-                m = to;
-                if (j > 0) {
-                    ok = mbar_wait_warp(b_o(i, (j - 1) & 1), (uint32_t)(((j - 1) >> 1) & 1), abort);
-                    if (!ok) break;
-                    tc_after();
-                    const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
+                        for (int c = 0; c < BN; ++c) s[c] = c > from || c < stay ? s[c] : -INFINITY;
+                    }
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < BN; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+                const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sc;
+                const bool grow = mx > m + 8.f || (m == -INFINITY && mx != -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? mx : m;
+                    const float alpha = m == -INFINITY ? 0.f : ex2(m - to);
+                    l2.x *= alpha;
+                    l2.y *= alpha;
+                    m = to;
+                    if (j > 0) {
+                        ok = mbar_wait_warp(b_o(i, (blk0 + j - 1) & 1), (uint32_t)(((blk0 + j - 1) >> 1) & 1), abort);
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t to_o = lanes + S::kColO + (uint32_t)(i * D);
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(to_o + c, v);
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(to_o + c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                            tmem_st32(to_o + c, v);
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.f : kUp - m;
+                const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int part = 0; part < BN / 64; ++part) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const float2 y = fma2(make_float2(s[64 * part + c], s[64 * part + c + 1]), sc2, neg2);
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
+                        pk[c / 2] = pack<BF16>(e.x, e.y);
+                    }
+                    tmem_st32(ts + 32 * part, pk);
+                }
+                l2 = add2(l2, add2(sum[0], sum[1]));
+                if ((kb + 1) * BN > L) {
+                    // the block reaches past the prompt: its last rows are another prompt's (or nobody's), and a weight
+                    // of zero times what stands there must be zero
+#pragma unroll
+                    for (int c = 0; c < S::kPieces; ++c) {
+                        const int r = ring_v(j) + c, st = r % NST;
+                        ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
+                        if (ok && row < S::kVKeys && kb * BN + c * S::kVKeys + row >= L) {
+#pragma unroll
+                            for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    *reinterpret_cast<uint4 *>(smem + S::kOffRing + st * S::kPiece + (x * S::kVKeys + row) * 128 + k * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    proxy_fence();
+                }
+                tmem_wait_st();
+                if (!ok) break;
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p(i, buf));
+            }
+            if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (blk0 + n - 1) & 1), (uint32_t)(((blk0 + n - 1) >> 1) & 1), abort);
+            if (n > 0) {
+                tc_after();
+                const float l = l2.x + l2.y;
+                const float inv = ok ? 1.f / l : __int_as_float(0x7fc00000);
+                const int64_t trow = begin + tok;
+                const int hq = head * G + row % G;
+                const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D));
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32] = {};
+                    if (ok) {  // (the same in a warp; else MMAs may be under way, and what they have is not wanted)
+                        tmem_ld32(to + c, v);
                         tmem_wait_ld();
+                    }
+                    if (valid) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-                        tmem_st32(to_o + c, v);
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                o[x] = pack<BF16>(__uint_as_float(v[k + 2 * x]) * inv, __uint_as_float(v[k + 2 * x + 1]) * inv);
+                            dst[(c + k) / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
                     }
                 }
+                if (valid && p.lse)
+                    p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l * (BF16 ? 1.f : 0.0078125f))) * 0.693147180559945309f : inv;
             }
-            const float neg = m == -INFINITY ? 0.f : kUp - m;
-            const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int part = 0; part < BN / 64; ++part) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    const float2 y = fma2(make_float2(s[64 * part + c], s[64 * part + c + 1]), sc2, neg2);
-                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
-                    pk[c / 2] = pack<BF16>(e.x, e.y);
-                }
-                tmem_st32(ts + 32 * part, pk);
-            }
-            l2 = add2(l2, add2(sum[0], sum[1]));
-            if ((kb + 1) * BN > L) {
-                // the block reaches past the prompt: its last rows are another prompt's (or nobody's), and a weight
-                // of zero times what stands there must be zero
-#pragma unroll
-                for (int c = 0; c < S::kPieces; ++c) {
-                    const int r = ring_v(j) + c, st = r % NST;
-                    ok = ok && mbar_wait_warp(b_full(st), (uint32_t)((r / NST) & 1), abort);
-                    if (ok && row < S::kVKeys && kb * BN + c * S::kVKeys + row >= L) {
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<uint4 *>(smem + S::kOffRing + st * S::kPiece + (x * S::kVKeys + row) * 128 + k * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    }
-                }
-                proxy_fence();
-            }
-            tmem_wait_st();
-            if (!ok) break;
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_p(i, buf));
-        }
-        if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), abort);
-        if (n > 0) {
-            tc_after();
-            const float l = l2.x + l2.y;
-            const float inv = ok ? 1.f / l : __int_as_float(0x7fc00000);
-            const int64_t trow = begin + tok;
-            const int hq = head * G + row % G;
-            const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D));
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t v[32] = {};
-                if (ok) {  // (the same in a warp; else MMAs may be under way, and what they have is not wanted)
-                    tmem_ld32(to + c, v);
-                    tmem_wait_ld();
-                }
-                if (valid) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            o[x] = pack<BF16>(__uint_as_float(v[k + 2 * x]) * inv, __uint_as_float(v[k + 2 * x + 1]) * inv);
-                        dst[(c + k) / 8] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                }
-            }
-            if (valid && p.lse)
-                p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l * (BF16 ? 1.f : 0.0078125f))) * 0.693147180559945309f : inv;
-        }
+            blk0 += n;
+        } while (next_unit());
     }
     // tensor memory is freed once every MMA is done and every row was read
     if (tid == 0) mbar_drain(b_final, 0);
@@ -525,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // memory, which is its own while this lane stays.  (Otherwise the MMAs have waited for all of them.)
     if (tid == 9 * 32 && *abort) {
         const int issued = place[5];
-        mbar_drain(b_q, 0);
+        mbar_drain(b_q, (uint32_t)(place[6] & 1));
         for (int st = 0; st < NST; ++st)
             if (issued > st) mbar_drain(b_full(st), (uint32_t)(((issued - 1 - st) / NST) & 1));
     }
@@ -932,7 +980,7 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, int smem, cudaStream_t s, co
 }
 
 template <int D, bool WIN>
-kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t s) {
+kvs_status attend_for(const kvs_prompt *p, PromptParams pp, cudaStream_t s) {
     using S = AttendShape<D>;
     const bool bf = p->dtype == KVS_BF16;
     const uint32_t TQ = kTileRows / pp.G;
@@ -943,8 +991,14 @@ kvs_status attend_for(const kvs_prompt *p, const PromptParams &pp, cudaStream_t 
     if (r != KVS_OK) return r;
     const uint64_t units = (uint64_t)p->total_rows / (S::NQ * TQ) + p->n_seq;  // at least the prompts' tile groups
     if (units * p->n_kv_head > 0x7fffffffull) return bad(KVS_ERR_UNSUPPORTED, "too many tiles for one launch");
-    const cudaError_t e = launch(bf ? prompt_attend_kernel<D, true, WIN> : prompt_attend_kernel<D, false, WIN>,
-                                 dim3((unsigned)(units * p->n_kv_head)), S::kSmem, s, pp, mq, mk, mv);
+    unsigned ctas = (unsigned)(units * p->n_kv_head);
+    if (WIN) {
+        pp.units = (int)ctas;
+        const unsigned sms = (unsigned)current_device_sms();
+        ctas = ctas < sms ? ctas : sms;
+    }
+    const cudaError_t e = launch(bf ? prompt_attend_kernel<D, true, WIN> : prompt_attend_kernel<D, false, WIN>, dim3(ctas), S::kSmem, s,
+                                 pp, mq, mk, mv);
     return e == cudaSuccess ? KVS_OK : cuda_failed("prompt attention launch", e);
 }
 
