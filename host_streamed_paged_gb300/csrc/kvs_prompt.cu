@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P is 2^(s - m + kUp), at most 2^(8 + kUp): as high as f16 reaches, so that its smallest step is 2^-31 of the largest
         // weight or less (2^-24 without, and thousands of keys below it are lost from the output); bf16 has the exponents
         constexpr float kUp = BF16 ? 0.f : 7.f;
-        bool ok = true;
+        bool ok = true, more;
         do {
             const int n = nblk[i], tok = t0 + i * TQ + row / G;  // within the prompt
             const bool valid = row < TQ * G && tok < L;
@@ -531,13 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p(i, buf));
             }
-            if (ok && n > 0) ok = mbar_wait_warp(b_o(i, (blk0 + n - 1) & 1), (uint32_t)(((blk0 + n - 1) >> 1) & 1), abort);
+            const int last = blk0 + n - 1, there = min(TQ, L - first_tok) * G;  // there: rows of the tile
+            const int64_t trow = begin + tok;
+            const int hq = head * G + row % G;
+            uint16_t *const tile_out = static_cast<uint16_t *>(p.out) + ((int64_t)(begin + first_tok) * p.out_stride + (int64_t)(head * G) * D);
+            blk0 += n;
+            more = next_unit();  // while the last P V is under way
+            if (ok && n > 0) ok = mbar_wait_warp(b_o(i, last & 1), (uint32_t)((last >> 1) & 1), abort);
             if (n > 0) {
                 tc_after();
                 const float l = l2.x + l2.y;
                 const float inv = ok ? 1.f / l : __int_as_float(0x7fc00000);
-                const int64_t trow = begin + tok;
-                const int hq = head * G + row % G;
                 const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (trow * p.out_stride + (int64_t)hq * D));
 #pragma unroll 1
@@ -561,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (valid && p.lse)
                     p.lse[trow * (int64_t)(p.Hk * G) + hq] = ok ? (m + log2f(l * (BF16 ? 1.f : 0.0078125f))) * 0.693147180559945309f : inv;
             }
-            blk0 += n;
-        } while (next_unit());
+        } while (more);
     }
     // tensor memory is freed once every MMA is done and every row was read
     if (tid == 0) mbar_drain(b_final, 0);
