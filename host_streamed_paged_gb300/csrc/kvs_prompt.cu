@@ -8,11 +8,16 @@
 //
 // Windows.  A unit walks the key blocks of the first tokens, then those from its
 // first row's window on; a block's index is all that knows of the gap between
-// them.  The kernels without a window are compiled apart and hold none of it.
-// 8192 + 6001 + 2048 + 513 + 1 tokens under a window of 1024 (32 / 8 heads, D
-// 128, bf16) take 278 us, 0.89 PFLOP/s of seen pairs: a unit is 18 blocks, so a
-// CTA's start and end (one per SM, 14 waves of 20 us) weigh a third of it; ncu:
-// tensor pipe 41%, 36% of the issue slots.
+// them.  Units are short then and all alike, so one CTA per SM takes every
+// gridDim.x-th of them: the next one's Q comes in once the last S is done, its
+// first scores are formed under the last one's P V and output (16755 rows of 8192
+// + 6001 + 2048 + 513 + 1 tokens, window 1024, 32 / 8 heads, D 128, bf16: 280 us
+// with a CTA a unit, 262 so, 255 with the next unit found while the last P V is
+// under way; 0.98 PFLOP/s of seen pairs).  A block of both tiles takes 0.74 us,
+// which is the tensor pipe's pace, a unit's change 6 us beside 18 blocks.  (Found
+// earlier, between blocks, 273; outputs turned around among four lanes, so that
+// a store is of fewer lines, 264.)  The kernels without a window are compiled
+// apart and hold none of it.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
