@@ -37,7 +37,7 @@
 //
 // Bound by the tensor pipe and what feeds it: 4 D operations a (row, key), the
 // cache's bytes being nothing beside them from some 100 rows on.  2048 rows over
-// 65536 tokens (32 / 8 heads, D 128) take 1497 us, 1.44 PFLOP/s, 74% of what
+// 65536 tokens (32 / 8 heads, D 128) take 1490 us, 1.45 PFLOP/s, 75% of what
 // bf16 products measure; ncu sees the tensor pipe active on 50% of the cycles
 // (1024 rows over 16384), 58% of the issue slots taken.  A block of both tiles
 // takes 0.92 us; without the softmax's arithmetic and the dequantising, MMAs,
@@ -58,6 +58,9 @@
 //   rows in and out by four lanes a row (64 bytes), the next unit's queries
 //     asked for early, masks only where a block needs them: the batch
 //     539 -> 368, chunks of up to 1024 rows under a window of 4096 213 -> 139.
+//   a worker's place in the line found by one of its warps for all: the 37 rows
+//     24.2 -> 23.4, the batch 368 -> 361.  (Its first piece as well: 23.1, but
+//     the batch 366 to 410, as the registers fell.)
 // Blocks of 64 keys: two buffers of S and P, two O of 128 columns and Q (D 64)
 // fill the 512 columns of tensor memory; 128 keys would leave one buffer each.
 #include <cuda_bf16.h>
@@ -265,9 +268,9 @@ __device__ void line_prefix(const ChunkParams &p, int tile_tokens, int tiles, in
         q.load(p, s, tile_tokens, tiles);
         return q.before(q.X) * p.pool.Hk;
     };
-    int64_t sum = 0;
+    int64_t sum = 0, one = 0;
     for (int k = 0; k < per; ++k)
-        if (tid * per + k < p.n_seq) sum += cost(tid * per + k);
+        if (tid * per + k < p.n_seq) sum += one = cost(tid * per + k);
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -282,7 +285,7 @@ __device__ void line_prefix(const ChunkParams &p, int tile_tokens, int tiles, in
         const int s = tid * per + k;
         if (s < p.n_seq) {
             prefix[s] = base;
-            base += cost(s);
+            base += per == 1 ? one : cost(s);
         }
     }
     if (tid == kThreads - 1) prefix[p.n_seq] = base;
@@ -398,18 +401,19 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
     }
     int64_t *prefix = reinterpret_cast<int64_t *>(smem + S::kOffRing);
     line_prefix<S::kThreads>(p, TQ, NQ, prefix);
-    // every warp walks the line by itself, its state in shared memory: lane 0 steps, the others read the piece
+    // every warp walks the line by itself, its state in shared memory: lane 0 steps, the others read the piece.  (Where it
+    // begins is found by one for all: by twenty at once it takes the issue slots' time.)
     Walk *walk = reinterpret_cast<Walk *>(smem + S::kOffPiece) + warp;
-    bool any;
-    {
+    if (warp == S::kFirstMma) {
         Line line;
-        any = line.seek(p, prefix, blockIdx.x, TQ, NQ);
-        if (lane == 0) walk->line = line;
+        if (!line.seek(p, prefix, blockIdx.x, TQ, NQ)) line.pos = line.end = 0;
+        if (lane < S::kThreads / 32) walk[lane - warp].line = line;
     }
     tc_before();
     __syncthreads();  // the prefix sums are read, the ring may be written
     tc_after();
     const uint32_t tmem = *tmem_slot;
+    const bool any = walk->line.pos < walk->line.end;
     const Piece *piece = &walk->piece;
     auto next_piece = [&] {
         bool more = false;

@@ -19,7 +19,7 @@
 // (3000 rows with norms 13.2 -> 11.8 us).
 //
 // Measured: 16755 rows of 24 + 4 heads, D 256, 64 dims rotated, f16: 75.2 us, 6.4
-// TB/s (94% of a copy's rate; ncu: DRAM 73% of its nominal).  With norms, 12001
+// TB/s (94% of a copy's rate; ncu: DRAM 73% of its peak).  With norms, 12001
 // rows of 32 + 8 heads, D 128, bf16: 50.3 us, 4.9 TB/s: 62% of the issue slots
 // taken at 80 registers, so the loads in flight and the instructions bound it
 // together.  A step of 64 rows takes 2.1 us of the GPU, 16 with the call.
