@@ -181,3 +181,83 @@ def test_a_graph_of_a_windowed_step():
     torch.cuda.synchronize()
     want = f.cache.attend(f.table_t, f.lens_t, q, window=300, sinks=4)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+MANY = [  # lens, kv heads, group: several units of every CTA
+    ([3000, 1, 2000, 500, 35, 36, 37], 4, 7),
+    ([2500] + [(53 * i) % 150 for i in range(60)], 2, 16),
+    ([(29 * i) % 60 for i in range(400)] + [700], 2, 5),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,Hk,G", MANY)
+def test_prompts_of_many_units(lens, Hk, G, D):
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    dt = "f16" if D == 128 else "bf16"
+    q, k, v, cu = make(lens, Hk, G, D, dt, seed=D + Hk)
+    out, lse = kvs.prompt_attend(q, k, v, cu, window=90, sinks=3)
+    check_prompt(out, lse, q, k, v, cu, dt, 1 / math.sqrt(D), 90, 3)
+    # a prompt's rows do not depend on what else is in the batch, or on which CTA has them
+    c = cu.tolist()
+    for i in (0, len(lens) - 1):
+        s = slice(c[i], c[i + 1])
+        one = torch.tensor([0, lens[i]], dtype=torch.int32, device="cuda")
+        for a, b in zip(kvs.prompt_attend(q[s], k[s], v[s], one, window=90, sinks=3), (out, lse)):
+            assert torch.equal(a, b[s])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_windowed_prompts_beside_rows_that_are_not_finite(D):
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    lens = [1100, 70, 901, 33, 64, 1]
+    q, k, v, cu = make(lens, 3, 8, D, "f16", seed=D)
+    want = kvs.prompt_attend(q, k, v, cu, window=100, sinks=2)
+    c = cu.tolist()
+    for i in (1, 3, 5):
+        k[c[i]:c[i + 1]] = math.nan
+        v[c[i]:c[i + 1]] = math.inf
+    got = kvs.prompt_attend(q, k, v, cu, window=100, sinks=2)
+    for i in (0, 2, 4):
+        for a, b in zip(got, want):
+            assert torch.equal(a[c[i]:c[i + 1]], b[c[i]:c[i + 1]])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_units_after_a_wait_that_gave_up(D):
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    q, k, v, cu = make([4000, 300, 2], 4, 4, D, "bf16", seed=D)
+    want = kvs.prompt_attend(q, k, v, cu, window=200, sinks=1)
+    try:
+        for _ in range(2):
+            kvs.kvs_debug_inject(None, kvs.KVS_FAULT_DEVICE_WAIT, 1)
+            out, lse = kvs.prompt_attend(q, k, v, cu, window=200, sinks=1)
+            assert out.isnan().all() and lse.isnan().all()
+            for a, b in zip(kvs.prompt_attend(q, k, v, cu, window=200, sinks=1), want):
+                assert torch.equal(a, b)
+    finally:
+        kvs.kvs_debug_inject(None, kvs.KVS_FAULT_NONE, 0)
+
+
+def test_a_graph_of_windowed_prompts_beside_an_eager_one():
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    q, k, v, cu = make([2000, 77, 900], 4, 4, 128, "bf16", seed=2)
+    want = kvs.prompt_attend(q, k, v, cu, window=150, sinks=4)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kvs.prompt_attend(q, k, v, cu, out=out, lse=lse, window=150, sinks=4)
+    other = torch.cuda.Stream()
+    for _ in range(3):
+        out.zero_()
+        other.wait_stream(torch.cuda.current_stream())
+        g.replay()
+        with torch.cuda.stream(other):
+            beside = kvs.prompt_attend(q, k, v, cu, window=150, sinks=4)
+        torch.cuda.synchronize()
+        for a, b, c in zip((out, lse), beside, want):
+            assert torch.equal(a, c) and torch.equal(b, c)
