@@ -16,8 +16,10 @@
 // under way; 0.98 PFLOP/s of seen pairs).  A block of both tiles takes 0.74 us,
 // which is the tensor pipe's pace, a unit's change 6 us beside 18 blocks.  (Found
 // earlier, between blocks, 273; outputs turned around among four lanes, so that
-// a store is of fewer lines, 264.)  The kernels without a window are compiled
-// apart and hold none of it.
+// a store is of fewer lines, 264.)  Over more
+// than 256 prompts a warp goes through them once, not once a unit: 4096 prompts
+// of 70 tokens, window 50, 12.9 -> 2.5 ms.  The kernels without a window are
+// compiled apart and hold none of it.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -129,13 +131,16 @@ __device__ __forceinline__ void find_sorted(const PromptParams &p, int c, int pe
         nth -= n;
     }
 }
+// RESUME: of ascending c; place[6] and [7], 0 at first, hold how far the prompts
+// were gone through (from the first on each time, 4096 prompts take a unit 25 us).
+template <bool RESUME = false>
 __device__ __forceinline__ void find_unit(const PromptParams &p, int c, int per, int *place) {
     const int lane = threadIdx.x & 31;
     if (p.n_seq <= 32) return find_sorted<1>(p, c, per, place);
     if (p.n_seq <= kSortedSeq) return find_sorted<kSortedSeq / 32>(p, c, per, place);
     auto groups = [&](int s) { return s < p.n_seq ? (cu_end(p, s) - cu_begin(p, s) + per - 1) / per : 0; };
-    int s = -1, x = 0, base = 0;
-    for (int s0 = 0; s0 < p.n_seq && s < 0; s0 += 32) {
+    int s = -1, x = 0, base = RESUME ? place[7] : 0, s0 = RESUME ? place[6] : 0;
+    for (; s0 < p.n_seq; s0 += 32) {
         const int t = groups(s0 + lane);
         int inc = t;
 #pragma unroll
@@ -148,8 +153,13 @@ __device__ __forceinline__ void find_unit(const PromptParams &p, int c, int per,
             const int who = __ffs(past) - 1;
             s = s0 + who;
             x = __shfl_sync(0xffffffffu, base + inc, who) - 1 - c;
+            break;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (RESUME) {
+        __syncwarp();
+        if (lane == 0) place[6] = s0, place[7] = base;
     }
     if (lane == 0) {
         place[0] = s;
@@ -280,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     set_unit(place);
+    if (WIN && lane < 2) place[8 * (1 + warp) + 6 + lane] = 0;
     // Under a window a CTA takes every gridDim.x-th unit, each warp finding them by itself; what it counts over them:
     // units, ring stages, blocks of its tile (0 all along in the kernels of one unit)
     int nth = 0, ring0 = 0, blk0 = 0;
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (unit >= p.units) return false;
             int *at = place + 8 * (1 + warp);
             __syncwarp();
-            find_unit(p, unit / p.Hk, NQ * TQ, at);
+            find_unit<true>(p, unit / p.Hk, NQ * TQ, at);
             __syncwarp();
             if (at[0] < 0) return false;
             head = unit % p.Hk;
