@@ -22,7 +22,9 @@
 // TB/s (94% of a copy's rate; ncu: DRAM 73% of its peak).  With norms, 12001
 // rows of 32 + 8 heads, D 128, bf16: 50.3 us, 4.9 TB/s: 62% of the issue slots
 // taken at 80 registers, so the loads in flight and the instructions bound it
-// together.  A step of 64 rows takes 2.1 us of the GPU, 16 with the call.
+// together.  (Two steps on their way instead of one: 55.7 us, fewer warps fit; 28
+// warps an SM at 72 registers: 46.6, but f16 51.7 against 49.6 and fp32 92
+// against 76.)  A step of 64 rows takes 2.1 us of the GPU, 16 with the call.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
