@@ -103,6 +103,7 @@ struct ChunkParams {
     float2 *part_ml;  // [the same][tile][row]: reference exponent and sum
     struct ChunkMeta *meta;
     int give_up;  // test hook: the MMA warps give up at their first wait, and *abort is up
+    int late;     // test hook: a unit's O is read late by the warpgroup that the next unit does not begin with
 };
 
 // What a worker left for the join.
@@ -721,6 +722,21 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         auto sync_all = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         auto done_wait = [&] { asm volatile("bar.sync %0, 256;" ::"r"(3 - wg) : "memory"); };
         auto done_tell = [&] { asm volatile("bar.arrive %0, 256;" ::"r"(2 + wg) : "memory"); };
+        // "O is read", across a change of unit: the next unit's first P V writes tile 0's O anew as soon as one warpgroup has
+        // published its first weights, and where either unit is on one tile the other may have columns of that O to read.  So
+        // the one that publishes them waits for the other's word: always in a unit on one tile (the first takes it too, from
+        // nobody's reading), and in one on two tiles that follows such a unit.  (Two uses of the barrier have a sync_all between
+        // them, which both pass after the first.)
+        bool hear = false;  // of warpgroup 0: the unit on two tiles follows one on one
+        auto read_tell = [] { asm volatile("bar.arrive 4, 256;" ::: "memory"); };
+        auto read_wait = [] {
+            asm volatile("bar.sync 4, 256;" ::: "memory");
+            tc_after();
+        };
+        auto hear_read = [&] {
+            if (hear) read_wait();
+            hear = false;
+        };
         auto one_tile = [&](const Piece &c) { return NQ == 1 || c.x * TU + TQ >= c.n; };  // both warpgroups on tile 0
         // 16 bytes k of row r of the warp's stage, where 8 neighbours read or write all banks once
         uint4 *stage = reinterpret_cast<uint4 *>(smem + S::kOffStage + warp * 2048);
@@ -852,6 +868,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
         };
         bool work = find_work();
         if (work) load_queries(*piece);
+        if (work && one_tile(*piece) && wg == 1) read_tell();  // there is nothing to read yet
         while (work) {
             const Piece c = *piece;
             __syncwarp();
@@ -999,12 +1016,13 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         ok = grow_reference(j, f);
                         grown = true;
                     } while (true);
+                    if (j == 0) read_wait();
                     if (ok) publish(j, f);
                     *row_ref = m;
                     if (j + 1 < n) done_tell();
                 }
-            } else if (ok) {
-                for (int j = 0; j < n; ++j) {
+            } else {
+                for (int j = 0; j < n && ok; ++j) {
                     ok = wait_warp(abort, [&] { return ready(j); });
                     if (!ok) break;
                     tc_after();
@@ -1019,8 +1037,10 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         if (!ok) break;
                     }
                     if (!ok) break;
+                    hear_read();
                     publish(j, f);
                 }
+                hear_read();  // (a wait gave up before: the other's word is taken all the same)
             }
             ring += 2 * n;
             all_blocks += n;
@@ -1042,9 +1062,20 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             if (ok) ok = mbar_wait_warp(b_o(i, last & 1), (last >> 1) & 1, abort);
             tc_after();
             if (!ok) l = nan;
+            // the other warpgroup has tile 0's first block of the next unit: it is to know when this one has read
+            const bool next_shared = work && one_tile(*piece);
+            const bool tell = next_shared ? wg != (int)(blocks0 & 1) : work && shared && wg == 1;
+            hear = work && shared && !next_shared && wg == 0;
+            if (p.late && tell)
+                for (int k = 0; k < 50; ++k) __nanosleep(1000);
             const bool whole = c.lo == 0 && c.hi == c.nblk;
             const uint32_t to = lanes + S::kColO + (uint32_t)(i * D);
             const int x0 = shared ? wg * (D / 2) : 0, x1 = shared ? x0 + D / 2 : D;
+            auto was_read = [&](int x) {  // with the columns from x on
+                if (!tell || x + 32 < x1) return;
+                tc_before();
+                read_tell();
+            };
             if (whole) {
                 const int64_t trow = c.begin + tok;
                 const int hq = c.h * G + hg;
@@ -1063,6 +1094,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         tmem_ld32(to + x, v);
                         tmem_wait_ld();
                     }
+                    was_read(x);
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
@@ -1092,6 +1124,7 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
                         tmem_ld32(to + x, v);
                         tmem_wait_ld();
                     }
+                    was_read(x);
                     if (valid) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
@@ -1270,7 +1303,9 @@ extern "C" kvs_status kvs_q4_attend_chunk(const kvs_q4_pool *pool, const int32_t
     }
     if (n_seq == 0 || total_rows == 0) return KVS_OK;
     const int sms = current_device_sms();
-    p.give_up = batch_wait_fault();
+    const uint32_t fault = batch_fault();
+    p.give_up = fault == KVS_FAULT_DEVICE_WAIT;
+    p.late = fault == KVS_FAULT_DEVICE_LATE;
     p.table = table;
     p.lens = lens;
     p.cu = cu;

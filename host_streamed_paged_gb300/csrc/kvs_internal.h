@@ -220,9 +220,9 @@ struct Q4Pool {
 };
 kvs_status check_q4_pool(const kvs_q4_pool *pool, bool need_pages, Q4Pool *out);
 
-// Whether this call of a batch operator is the one that kvs_debug_inject(NULL,
-// KVS_FAULT_DEVICE_WAIT, nth) armed on this thread (counts the call).
-bool batch_wait_fault();
+// The fault that kvs_debug_inject(NULL, fault, nth) armed on this thread for
+// this call of a batch operator, KVS_FAULT_NONE for the others (counts the call).
+uint32_t batch_fault();
 
 // Message returned by kvs_last_error(NULL) on this thread.
 void set_thread_error(const std::string &msg);

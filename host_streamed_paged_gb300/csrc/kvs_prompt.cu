@@ -1093,7 +1093,7 @@ static kvs_status attend_call(const kvs_prompt *p, uint32_t window, uint32_t sin
     if (p->total_rows && (!out || !aligned(out, 16) || out_stride % 8 || out_stride < (uint64_t)p->n_q_head * p->head_dim))
         return bad(KVS_ERR_INVALID, "out rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
     if (p->total_rows == 0 || p->n_seq == 0) return KVS_OK;
-    pp.give_up = batch_wait_fault();
+    pp.give_up = batch_fault() == KVS_FAULT_DEVICE_WAIT;
     pp.out = out;
     pp.out_stride = (int64_t)out_stride;
     pp.lse = lse;
@@ -1126,7 +1126,7 @@ extern "C" kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, 
     if (p->n_seq && width && ((p->total_rows && !lse) || !weights)) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (p->n_seq == 0 || width == 0) return KVS_OK;
-    pp.give_up = batch_wait_fault();
+    pp.give_up = batch_fault() == KVS_FAULT_DEVICE_WAIT;
     pp.lse_in = lse;
     pp.prev = prev;
     pp.w = weights;

@@ -1812,7 +1812,7 @@ static kvs_status attend_call(const kvs_q4_pool *pool, AttendParams &p, void *ou
     if (workspace_bytes < need) return bad(KVS_ERR_CAPACITY, "workspace smaller than kvs_q4_query_sizes asks for");
     const int sms = current_device_sms();
     const Shape sh = shape_of(D, n_rows * p.G, dtype, sms < kSmsAssumed ? sms : kSmsAssumed);
-    p.give_up = batch_wait_fault();
+    p.give_up = batch_fault() == KVS_FAULT_DEVICE_WAIT;
     p.out = out;
     p.lse = lse;
     p.row_blocks = sh.row_blocks;
@@ -1875,7 +1875,7 @@ extern "C" kvs_status kvs_q4_weights(const kvs_q4_pool *pool, const int32_t *tab
     if (n_seq && width && (!lse || !weights)) return bad(KVS_ERR_INVALID, "null lse or weights");
     if (width > 0x7fffffffull) return bad(KVS_ERR_INVALID, "width must be at most 2^31 - 1");
     if (n_seq == 0 || width == 0) return KVS_OK;
-    p.a.give_up = batch_wait_fault();
+    p.a.give_up = batch_fault() == KVS_FAULT_DEVICE_WAIT;
     const uint32_t D = pool->head_dim, rows = n_rows * p.a.G;
     const bool hl = dtype == KVS_F32;
     // up to 16 or (16-bit queries) 32 rows a pass: the fewer passes, the fewer times a tile is read; the passes as even as

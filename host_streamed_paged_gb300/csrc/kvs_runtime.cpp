@@ -804,8 +804,9 @@ void sizes_of(const kvs_config *cfg, uint64_t *page_bytes, uint64_t *host_bytes,
 namespace kvs {
 void set_thread_error(const std::string &msg) { g_create_error = msg; }
 
-static thread_local uint64_t g_batch_fault = 0;  // batch calls until the armed one
-bool batch_wait_fault() { return g_batch_fault && --g_batch_fault == 0; }
+static thread_local uint64_t g_batch_calls = 0;  // batch calls until the armed one
+static thread_local uint32_t g_batch_fault = KVS_FAULT_NONE;
+uint32_t batch_fault() { return g_batch_calls && --g_batch_calls == 0 ? g_batch_fault : (uint32_t)KVS_FAULT_NONE; }
 }  // namespace kvs
 
 // ======================================================================= C ABI
@@ -2197,11 +2198,12 @@ kvs_status kvs_graph_destroy(kvs_ctx *c) {
 
 kvs_status kvs_debug_inject(kvs_ctx *c, uint32_t fault, uint64_t nth) {
     if (!c) {
-        if (fault != KVS_FAULT_NONE && fault != KVS_FAULT_DEVICE_WAIT) {
-            kvs::set_thread_error("without a context only KVS_FAULT_DEVICE_WAIT can be armed");
+        if (fault != KVS_FAULT_NONE && fault != KVS_FAULT_DEVICE_WAIT && fault != KVS_FAULT_DEVICE_LATE) {
+            kvs::set_thread_error("without a context only KVS_FAULT_DEVICE_WAIT and KVS_FAULT_DEVICE_LATE can be armed");
             return KVS_ERR_INVALID;
         }
-        kvs::g_batch_fault = fault == KVS_FAULT_NONE ? 0 : nth;
+        kvs::g_batch_fault = fault;
+        kvs::g_batch_calls = fault == KVS_FAULT_NONE ? 0 : nth;
         return KVS_OK;
     }
     if (fault > KVS_FAULT_DEVICE_WAIT) return fail(c, KVS_ERR_INVALID, "unknown fault kind");

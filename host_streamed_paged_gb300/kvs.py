@@ -40,7 +40,7 @@ KVS_FLAG_F16_OPERANDS = 4
 
 KVS_OP_RECORD, KVS_OP_WAIT, KVS_OP_FILL, KVS_OP_READ, KVS_OP_POOL_LOAD = 1, 2, 3, 4, 5
 KVS_OP_PUBLISH, KVS_OP_WRITE, KVS_OP_LAUNCH, KVS_OP_MOVE = 6, 7, 8, 9
-KVS_FAULT_NONE, KVS_FAULT_FILL_ENQUEUE, KVS_FAULT_SYNC_STALL, KVS_FAULT_DEVICE_WAIT = 0, 1, 2, 3
+KVS_FAULT_NONE, KVS_FAULT_FILL_ENQUEUE, KVS_FAULT_SYNC_STALL, KVS_FAULT_DEVICE_WAIT, KVS_FAULT_DEVICE_LATE = 0, 1, 2, 3, 4
 
 
 class kvs_config(ctypes.Structure):

@@ -202,12 +202,15 @@ enum {
     KVS_FAULT_NONE = 0,
     KVS_FAULT_FILL_ENQUEUE = 1, /* the nth ring refill enqueue fails */
     KVS_FAULT_SYNC_STALL = 2,   /* kvs_sync sees the GPU as busy until its deadline */
-    KVS_FAULT_DEVICE_WAIT = 3   /* in the split-K attention launches of the nth kvs_attend call,
+    KVS_FAULT_DEVICE_WAIT = 3,  /* in the split-K attention launches of the nth kvs_attend call,
                                    every pipeline wait gives up at once, as if its copy never
                                    landed: the CTAs drain the copies they issued (with the
                                    normal bound), set the status word and exit.  That call's
                                    outputs (and those of later calls until the next kvs_sync)
                                    are NaN, and the next kvs_sync returns KVS_ERR_CUDA */
+    KVS_FAULT_DEVICE_LATE = 4   /* without a context: warps that others have to wait for come some
+                                   50 us late wherever a kernel has such a hook; the call's outputs
+                                   are what they always are */
 };
 
 /*
@@ -657,7 +660,8 @@ const char *kvs_last_error(const kvs_ctx *ctx);
 /* kvs_debug_inject -- arm a fault (KVS_FAULT_*) that fires on the nth
  * (1-based) matching event; nth = 0 disarms.  Every fault is made on the host
  * or as a shortened device-side wait limit: no GPU fault is ever made.  With
- * ctx NULL, KVS_FAULT_DEVICE_WAIT is armed for the nth launching call that
+ * ctx NULL, KVS_FAULT_DEVICE_WAIT or KVS_FAULT_DEVICE_LATE (kvs_q4_attend_chunk
+ * has its hook) is armed for the nth launching call that
  * this thread makes of the batch operators with such waits (kvs_prompt_attend,
  * kvs_prompt_weights, kvs_q4_attend, kvs_q4_weights, the first and third under
  * a window, kvs_q4_attend_chunk).  Test API; the pages describe no such call. */
