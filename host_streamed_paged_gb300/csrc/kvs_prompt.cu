@@ -62,6 +62,7 @@ struct PromptParams {
     int window, sinks, units;  // of the windowed kernels; units: bound of (tile groups x heads)
     int main_ctas;  // those past them copy what no key writes
     int give_up;    // test hook: the MMA warps give up at their first wait, as if its copy never landed, and *abort is up
+    int late;       // test hook (windows): the one of a tile with a block at most comes late to the unit's second
 };
 
 __device__ __forceinline__ int cu_begin(const PromptParams &p, int s) {
@@ -410,7 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         do {
             n = nblk[i];
             for (int j = 0; j < 2 && j < n_max && ok; ++j) {
-                ok = wait_warp(abort, [&] { return mbar_done(b_q, (uint32_t)(nth & 1)) & loaded(ring_k(j)); });
+                if (WIN && p.late && j == 1 && n < 2)
+                    for (int k = 0; k < 50; ++k) __nanosleep(1000);
+                // (Q is asked for at the first block alone: a tile of no more blocks gives it back there, and once the next
+                // unit's has come this phase would not be seen any more)
+                ok = wait_warp(abort, [&] { return (j > 0 || mbar_done(b_q, (uint32_t)(nth & 1))) & loaded(ring_k(j)); });
                 if (!ok) break;
                 tc_after();
                 if (one) {
@@ -1093,7 +1098,9 @@ static kvs_status attend_call(const kvs_prompt *p, uint32_t window, uint32_t sin
     if (p->total_rows && (!out || !aligned(out, 16) || out_stride % 8 || out_stride < (uint64_t)p->n_q_head * p->head_dim))
         return bad(KVS_ERR_INVALID, "out rows must start on 16-byte boundaries, at least n_q_head * head_dim apart");
     if (p->total_rows == 0 || p->n_seq == 0) return KVS_OK;
-    pp.give_up = batch_fault() == KVS_FAULT_DEVICE_WAIT;
+    const uint32_t fault = batch_fault();
+    pp.give_up = fault == KVS_FAULT_DEVICE_WAIT;
+    pp.late = fault == KVS_FAULT_DEVICE_LATE;
     pp.out = out;
     pp.out_stride = (int64_t)out_stride;
     pp.lse = lse;

@@ -660,8 +660,8 @@ const char *kvs_last_error(const kvs_ctx *ctx);
 /* kvs_debug_inject -- arm a fault (KVS_FAULT_*) that fires on the nth
  * (1-based) matching event; nth = 0 disarms.  Every fault is made on the host
  * or as a shortened device-side wait limit: no GPU fault is ever made.  With
- * ctx NULL, KVS_FAULT_DEVICE_WAIT or KVS_FAULT_DEVICE_LATE (kvs_q4_attend_chunk
- * has its hook) is armed for the nth launching call that
+ * ctx NULL, KVS_FAULT_DEVICE_WAIT or KVS_FAULT_DEVICE_LATE (hooks for it are in
+ * kvs_q4_attend_chunk and kvs_prompt_attend_window) is armed for the nth launching call that
  * this thread makes of the batch operators with such waits (kvs_prompt_attend,
  * kvs_prompt_weights, kvs_q4_attend, kvs_q4_weights, the first and third under
  * a window, kvs_q4_attend_chunk).  Test API; the pages describe no such call. */
