@@ -220,8 +220,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sum = fmaf(x[j] * f, x[j] * f, sum);
-                const float again = __frsqrt_rn(over_head(sum) + p.eps * f * f) * f;
-                if (odd) inv = again;
+                const float root = __frsqrt_rn(over_head(sum) + p.eps * f * f);
+                // (elements are brought up before the root's product: root f passes fp32 where they are subnormal.  Down, f
+                // goes with the root: small elements beside a large one keep their bits)
+                if (odd) {
+                    const float up = fmaxf(f, 1.f);
+                    inv = root * fminf(f, 1.f);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] *= up;
+                }
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) x2[j] = mul2(mul2(x2[j], make_float2(inv, inv)), make_float2(w[2 * j], w[2 * j + 1]));

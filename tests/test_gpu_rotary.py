@@ -171,6 +171,31 @@ def test_norms_of_any_size(dt, size, eps):
     check(r.norm_rotate(pos.cuda(), q, eps=eps)[0], q, pos.tolist(), r, dt, None, eps)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("size,eps", [(3e-39, 0.0), (1e-40, 0.0), (1e-42, 0.0), (1e-44, 0.0), (1e-42, 1e-45), (1e-40, 1e-45), (3e38, 0.0)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_norms_of_subnormal_rows(D, size, eps, dt):
+    """Their roots' reciprocals pass fp32, the values do not; and a row with one large element beside small ones."""
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    r = kvs.Rotary(D, rot_dim=32)
+    x = torch.randn(6, 3, D, generator=torch.Generator().manual_seed(D), dtype=torch.float64)
+    x = x / x.abs().max() * size
+    x[1, 1] = 0
+    x[1, 1, 7] = -size
+    x[4, 2] = size * 2.0 ** -20
+    x[4, 2, D - 1] = size
+    q = x.to(_t(dt))
+    keep = (q != 0).any(-1)  # (a head of zeros has no norm where eps is 0)
+    q[~keep] = 1.0
+    q = q.cuda()
+    pos = torch.arange(6)
+    w = (1 + 0.1 * torch.randn(D, generator=torch.Generator().manual_seed(2))).cuda()
+    for weight in (None, w):
+        got = r.norm_rotate(pos.cuda(), q, q_weight=weight, eps=eps)[0]
+        check(got, q, pos.tolist(), r, dt, weight, ctypes.c_float(eps).value)
+
+
 @pytest.mark.parametrize("size,eps", [(1e-36, 1e-32), (1e-37, 7e-31), (1e-30, 1e-38), (1e-38, 1e-45), (1e-36, 1e38)])
 def test_an_eps_of_any_size_beside_the_rows(size, eps):
     import torch
