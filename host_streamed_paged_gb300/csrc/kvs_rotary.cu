@@ -3,7 +3,7 @@
 //
 // Angles.  A pair's angle at position p is p f.  Kept as turns in 64-bit fixed
 // point (f / 2 pi times 2^64), p times it modulo 2^64 is the angle's fraction of
-// a turn exactly, whatever the position; its top 32 bits, read as signed, are
+// a turn, exact but for p times the last bit's rounding; its top 32 bits, read as signed, are
 // the angle in half turns, -1 .. 1, for sincospif.  (p f in fp32 is off by p f
 // 2^-24: 0.06 radians at a million.)
 //

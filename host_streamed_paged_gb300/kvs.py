@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from functools import lru_cache as _lru_cache
 from threading import local as _thread_local
 
 import numpy as np
@@ -949,6 +950,8 @@ class Rotary:
     - "bands": the same with the ramp over the turns themselves, from ``slow`` to ``fast``
 
     (fast, slow: 32 and 1 for "yarn", 4 and 1 for "bands", unless given.)  ``freqs`` gives the f_i themselves instead.
+    An f_i is a double (``freqs``); its angle at a position comes within 1.2e-7 + |position| 1.8e-19 radians, before the
+    sine's and cosine's own roundings.
     """
 
     def __init__(self, head_dim, rot_dim=None, base=10000.0, interleaved=False, scaling=None, factor=1.0, context=None, fast=None,
@@ -972,7 +975,7 @@ class Rotary:
         magnitude = 1.0 if magnitude is None else float(magnitude)
         if not math.isfinite(magnitude):
             raise ValueError("magnitude must be finite")
-        turns = [int(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64)) % 2 ** 64 for f in freqs]
+        turns = [_turns(f) for f in freqs]
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64).to(device)
         self.freqs, self.magnitude, self.device = freqs, magnitude, self.turns.device
         self.head_dim, self.rot_dim, self.interleaved = head_dim, rot, bool(interleaved)
@@ -1040,6 +1043,29 @@ class Rotary:
             _dtype_of(w)
             w = w.data_ptr()
         return ctypes.byref(kvs_head_rows(x.data_ptr(), y.data_ptr(), _row_stride(x, "rows"), y_stride, heads, w)), y
+
+
+@_lru_cache(None)
+def _two_pi(bits):
+    """2 pi times 2^bits, off by some thousand at most (Machin's 16 arctan(1/5) - 4 arctan(1/239) = pi)."""
+    def arctan_of_one_over(n):
+        term = total = (1 << bits) // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+
+    return 2 * (16 * arctan_of_one_over(5) - 4 * arctan_of_one_over(239))
+
+
+def _turns(f):
+    """The double f / (2 pi) modulo 1, times 2^64, rounded once: a quotient in doubles is off by 2^-54 of it, which counts
+    position times.  (1280 bits of pi: the largest double has 1024 before the point, and 64 are wanted behind it.)"""
+    n, d = f.as_integer_ratio()
+    n, d = n << 64 + 1280, d * _two_pi(1280)
+    return (2 * n + d) // (2 * d) % 2 ** 64
 
 
 def _rotary_freqs(rot, base, scaling, factor, context, fast, slow):

@@ -819,7 +819,9 @@ kvs_status kvs_prompt_weights(const kvs_prompt *p, const float *lse, uint32_t la
  * where the pair is dims (i, i + rot_dim / 2), or with `interleaved` (2i, 2i +
  * 1).  The other dims are copied.  turns[i] is f_i / (2 pi) * 2^64 modulo 2^64
  * (frequencies as fractions of a turn per position): position * turns[i] modulo
- * 2^64 is then the exact angle at any position, negative ones too.
+ * 2^64 is then the angle, exactly that of the frequency turns[i] at any
+ * position, negative ones too.  (How near turns[i] is to f_i counts position
+ * times: rounded from f_i's whole value it is 1.8e-19 radians a position.)
  */
 typedef struct {
     const uint64_t *turns; /* device [rot_dim / 2] */

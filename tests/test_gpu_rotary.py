@@ -112,6 +112,20 @@ def test_far_and_negative_positions(interleaved):
     assert (back - q).abs().max() <= 4e-6
 
 
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_angles_of_very_far_positions(base):
+    """Turns are off by half of their last bit, 2^-65 of a turn, position times (2^-13 of a turn at 2^52)."""
+    import torch
+    from host_streamed_paged_gb300 import kvs
+    r = kvs.Rotary(128, base=base)
+    pos = [1 << 36, -(1 << 40) - 7, (1 << 44) + 12345, (1 << 48) - 1, -(1 << 52) + 3]
+    q, k = rows(len(pos), 3, 2, 128, "f32")
+    y, size = reference(q, pos, r)
+    off = np.abs(np.array(pos, dtype=np.float64))[:, None, None] * 2.0 ** -65 * 2 * math.pi
+    err = np.abs(r.rotate(torch.tensor(pos).cuda(), q)[0].double().cpu().numpy() - y)
+    assert (err <= 2.0 ** -24 * np.abs(y) + (5e-7 + off) * size).all()
+
+
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_a_row_may_be_its_own_output(D, dt):

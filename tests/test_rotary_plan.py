@@ -27,6 +27,18 @@ def test_frequencies_and_turns(D, rot):
         assert abs(Fraction(t % 2 ** 64, 2 ** 64) - exact) <= exact * Fraction(1, 2 ** 51) + Fraction(1, 2 ** 64)
 
 
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1.5])
+def test_turns_are_rounded_once(base):
+    """Half of the last of 64 bits, whatever the frequency: it counts position times."""
+    r = plan(256, base=base)
+    odd = plan(64, freqs=[-f for f in r.freqs[:26]] + [1e30, -3.7e25, 5e-324, 2.0 ** -70, 0.0, 2 * math.pi])
+    for p in (r, odd):
+        for f, t in zip(p.freqs, p.turns.tolist()):
+            off = Fraction(t, 2 ** 64) - Fraction(f) / (2 * PI)
+            off -= math.floor(off + Fraction(1, 2))
+            assert abs(off) <= Fraction(1, 2 ** 65) * Fraction(1000001, 1000000)
+
+
 def test_frequencies_of_more_than_a_turn_and_below_zero():
     r = plan(64, freqs=[7.0, -0.25, 0.0, 1.0] * 2)
     assert r.rot_dim == 16
