@@ -888,7 +888,7 @@ def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None, window=0, sinks=0
 
     q [rows][Hq][D], k and v [rows][Hk][D] in float16 or bfloat16 (rows may be strided), cu int32 [n + 1]: prompt i is
     rows cu[i] .. cu[i + 1] - 1.  With window > 0 a row sees the last window keys up to its own and the first sinks keys
-    of its prompt (kvs_prompt_attend_window).  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
+    of its prompt (kvs_prompt_attend_window; its lse is not one for prompt_weights).  Runs on the current stream.  Rows of no prompt are left as they are in out and lse
     (undefined where those are allocated here).  The results carry no gradient.
     """
     p = _prompt(q, k, v, cu, scale)
@@ -915,8 +915,8 @@ def prompt_attend(q, k, v, cu, scale=None, out=None, lse=None, window=0, sinks=0
 def prompt_weights(q, k, lse, cu, width, window=0, prev=None, out=None, scale=None):
     """The attention weight each key of packed prompts received (kvs_prompt_weights): float32 [n][Hk][width].
 
-    lse is prompt_attend's; window > 0 counts only each prompt's last window rows; prev (same shape) is added, and
-    may be out.
+    lse is prompt_attend's without a window: a row counts for every key up to its own.  window > 0 is another thing here:
+    only each prompt's last window rows count.  prev (same shape) is added, and may be out.
     """
     if window < 0:
         raise ValueError("window must not be negative")
@@ -1159,7 +1159,7 @@ class Q4Cache:
         """Attention of q [n_seq][rows][Hq][D] over the cached tokens: (out, lse); the last row sees all of lens.
 
         With window > 0 a row sees the last window tokens up to its own and the first sinks tokens of its sequence
-        (kvs_q4_attend_window).  out may be q.  The results carry no gradient.
+        (kvs_q4_attend_window; its lse is not one for weights).  out may be q.  The results carry no gradient.
         """
         dt, stride = self._batch(table, lens, q)
         shape = q.shape
@@ -1245,7 +1245,8 @@ class Q4Cache:
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
         """The attention weight each cached token received from those rows, added to prev: float32 [n_seq][Hk][width].
 
-        lse is attend's; width defaults to prev's, or to the tokens the table can hold; out may be prev.
+        lse is attend's without a window (a row counts for all the tokens it stands behind); width defaults to prev's, or to
+        the tokens the table can hold; out may be prev.
         """
         dt, stride = self._batch(table, lens, q)
         n, rows, hq, d = q.shape

@@ -792,7 +792,8 @@ kvs_status kvs_prompt_attend(const kvs_prompt *p, void *out, uint64_t out_stride
 /*
  * kvs_prompt_attend_window -- kvs_prompt_attend where a row sees, of the keys
  * up to its own, the last `window` (its own among them) and the first `sinks`
- * of its prompt; window 0: all of them.  lse is over what the row sees.
+ * of its prompt; window 0: all of them.  lse is over what the row sees (and
+ * with window > 0 none for kvs_prompt_weights).
  */
 kvs_status kvs_prompt_attend_window(const kvs_prompt *p, uint32_t window, uint32_t sinks, void *out, uint64_t out_stride,
                                     float *lse, void *stream);
@@ -803,7 +804,9 @@ kvs_status kvs_prompt_attend_window(const kvs_prompt *p, uint32_t window, uint32
  *                head g of exp(scale q_rh . k_jg - lse_rh)
  * with j counted from the prompt's first row and, for last_rows > 0, only the
  * prompt's last last_rows rows r (an observation window); 0: every row.  lse
- * is kvs_prompt_attend's.  prev (nullable: zeros) and weights: device fp32
+ * is kvs_prompt_attend's: rows count for every key up to their own, so it is
+ * not for the lse of kvs_prompt_attend_window, beside which the keys outside a
+ * row's window would get weights that no row gave them.  prev (nullable: zeros) and weights: device fp32
  * [n_seq][n_kv_head][width]; keys beyond width are not counted, entries beyond
  * a prompt's length are prev's.  prev may be weights.  Sums run in a fixed
  * order.
@@ -935,7 +938,8 @@ kvs_status kvs_q4_attend(const kvs_q4_pool *pool, const int32_t *table, uint32_t
  * kvs_q4_attend_window -- kvs_q4_attend where a row sees, of the tokens up to
  * its own, the last `window` (its own among them) and the first `sinks`;
  * window 0: all of them.  Pages that hold no token that a row sees are not
- * read (their numbers may be anything).
+ * read (their numbers may be anything).  lse is over what the row sees (and
+ * with window > 0 none for kvs_q4_weights).
  */
 kvs_status kvs_q4_attend_window(const kvs_q4_pool *pool, const int32_t *table, uint32_t table_width, const int32_t *lens,
                                 uint32_t n_seq, uint32_t n_rows, uint32_t n_q_head, const void *q, int32_t dtype,
@@ -975,7 +979,8 @@ kvs_status kvs_q4_attend_chunk(const kvs_q4_pool *pool, const int32_t *table, ui
  * kvs_q4_weights -- the attention weight each cached token received from those
  * rows: w[i][g][t] = prev[i][g][t] + sum over rows r that see t and query
  * heads h of kv head g of exp(scale q_irh . k_tg - lse_irh), with
- * kvs_q4_attend's lse.  prev (nullable: zeros) and weights: device fp32
+ * kvs_q4_attend's lse (all T tokens' sum: not one under a window, as with
+ * kvs_prompt_weights).  prev (nullable: zeros) and weights: device fp32
  * [n_seq][Hk][width]; tokens beyond width are not counted, entries beyond T
  * are prev's; prev may be weights.  Reads only K.  Tokens of a page outside
  * the pool become NaN.
