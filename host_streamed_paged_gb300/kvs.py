@@ -13,6 +13,7 @@ import math
 import os
 from functools import lru_cache as _lru_cache
 from threading import local as _thread_local
+from weakref import WeakValueDictionary as _WeakValues
 
 import numpy as np
 
@@ -1099,14 +1100,35 @@ def _rotary_freqs(rot, base, scaling, factor, context, fast, slow):
     return [x / factor * r + x * (1 - r) for x, r in zip(f, far)], 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
 
 
+class _Space:
+    """A workspace that caches share, as large as the largest call so far asked for."""
+
+    bytes = None
+
+
+_shared_spaces = _thread_local()  # of each thread, by device and stream, while a cache holds them
+
+
+def _shared_space(index, stream) -> _Space:
+    try:
+        held = _shared_spaces.held
+    except AttributeError:
+        held = _shared_spaces.held = _WeakValues()
+    space = held.get((index, stream))
+    if space is None:
+        space = held[index, stream] = _Space()
+    return space
+
+
 class Q4Cache:
     """A page cache held in 4 bits (K and V as Q4_0) and the calls on it (kvs_q4_*).
 
     ``pages`` is a uint8 CUDA tensor of whole pages in the layout include/kvs.h states (or give ``n_pages`` and
     ``device`` to have one allocated, zeroed).  Page tables (int32 [n_seq][width]), lengths (int32 [n_seq]) and slots
     (int64: page * page_tokens + token) are CUDA tensors that the caller keeps.  Every call runs on the current
-    stream; attend keeps a workspace per stream and thread, and takes one of its own for each captured call, so calls
-    on several streams, from several threads and in captured graphs do not share one.
+    stream; attend and attend_chunk keep a workspace per stream and thread (up to 15 and 41 MB), which all caches of a
+    device share, and take one of its own for each captured call, so calls on several streams, from several threads and
+    in captured graphs do not share one.
     """
 
     def __init__(self, *, page_tokens, n_kv_head, head_dim, pages=None, n_pages=None, device="cuda"):
@@ -1122,7 +1144,7 @@ class Q4Cache:
         self.pool, self.n_kv_head, self.head_dim, self.page_tokens = pool, n_kv_head, head_dim, page_tokens
         self._ref, self._lib = ctypes.byref(pool), load()
         self._need_bytes = {}  # by (rows, heads, dtype)
-        self._spaces = _thread_local()  # of each thread, workspaces by stream: they go with the thread
+        self._spaces = _thread_local()  # of each thread, the workspaces used, by stream: they go with the thread
 
     def append(self, slots, k, v):
         """Encode rows k, v [n][Hk][D] (float32, float16 or bfloat16) into slots; negative slots are skipped."""
@@ -1221,8 +1243,8 @@ class Q4Cache:
         return out
 
     def _workspace(self, need):
-        """attend's workspace: one per stream and thread, whose calls run in order (another thread's may come between the
-        two launches of one); a call being captured gets one of its own from the graph's memory, since graphs of one
+        """attend's and attend_chunk's workspace: one per stream and thread, whose calls run in order, whichever cache they
+        are on (another thread's may come between the two launches of one); a call being captured gets one of its own from the graph's memory, since graphs of one
         stream may be replayed side by side."""
         cuda, dev = _torch.cuda, self.device
         if dev.type != "cuda":
@@ -1237,9 +1259,12 @@ class Q4Cache:
         except AttributeError:
             spaces = self._spaces.by_stream = {}
         stream = _stream_of(dev.index)
-        ws = spaces.get(stream)
+        space = spaces.get(stream)
+        if space is None:
+            space = spaces[stream] = _shared_space(dev.index, stream)
+        ws = space.bytes
         if ws is None or ws.numel() < need:
-            ws = spaces[stream] = _torch.empty(need, dtype=_torch.uint8, device=dev)
+            ws = space.bytes = _torch.empty(need, dtype=_torch.uint8, device=dev)
         return ws
 
     def weights(self, table, lens, q, lse, width=None, prev=None, out=None, scale=None):
