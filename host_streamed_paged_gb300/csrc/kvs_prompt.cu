@@ -552,10 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p(i, buf));
             }
-            const int last = blk0 + n - 1, there = min(TQ, L - first_tok) * G;  // there: rows of the tile
+            const int last = blk0 + n - 1;
             const int64_t trow = begin + tok;
             const int hq = head * G + row % G;
-            uint16_t *const tile_out = static_cast<uint16_t *>(p.out) + ((int64_t)(begin + first_tok) * p.out_stride + (int64_t)(head * G) * D);
             blk0 += n;
             more = next_unit();  // while the last P V is under way
             if (ok && n > 0) ok = mbar_wait_warp(b_o(i, last & 1), (uint32_t)((last >> 1) & 1), abort);
