@@ -1050,7 +1050,8 @@ __global__ void __launch_bounds__(ChunkShape<D>::kThreads, 1) chunk_kernel(const
             if (shared) {  // both are done with the scores, the reference is the last one
                 sync_all();
                 const float now = *row_ref;
-                row_sum[wg * kTileRows] = !ok ? nan : m == -INFINITY ? 0.f : l * ex2(m - now);
+                // (without a reference the sum is 0, or NaN where every key that the row saw was)
+                row_sum[wg * kTileRows] = !ok ? nan : m == -INFINITY ? l : l * ex2(m - now);
                 m = now;
             }
             // the next queries go in before this unit's output comes out: its scores are all read
