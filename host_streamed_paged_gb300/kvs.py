@@ -813,6 +813,8 @@ def _row_stride(t, what):
     shape, stride = t.shape, t.stride()
     heads, d = shape[-2], shape[-1]
     if stride[-1] != 1 or (heads > 1 and stride[-2] != d):
+        if 0 in shape:  # no rows: strides say nothing (an empty array's are 0)
+            return heads * d
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     if len(shape) == 4:
         if shape[1] == 1:

@@ -233,3 +233,21 @@ def test_chunk_arguments_that_are_refused():
             c.attend_chunk(**{**good, **kw})
     with pytest.raises(ValueError, match="CUDA"):
         c.attend_chunk(**good)
+
+
+def test_empty_batches_with_the_strides_of_an_empty_array(monkeypatch):
+    """numpy's arrays without elements have strides of 0."""
+    import numpy as np
+    import torch
+    monkeypatch.setattr(kvs, "_run", lambda dev, fn, *a: None)
+    q, k = (torch.from_numpy(np.random.default_rng(0).standard_normal((0, n, 64), np.float32)) for n in (4, 2))
+    assert k.stride() == (0, 0, 0)
+    pos = torch.zeros(0, dtype=torch.int64)
+    assert plan(64).rotate(pos, q, k)[0].shape == q.shape and plan(64).norm_rotate(pos, q, k)[1].shape == k.shape
+    c = kvs.Q4Cache(page_tokens=32, n_kv_head=2, head_dim=64, n_pages=2, device="cpu")
+    c._workspace = lambda need: torch.empty(need, dtype=torch.uint8)
+    c.append(pos, k, k)
+    none = torch.zeros(0, dtype=torch.int32)
+    assert c.attend_chunk(none.view(0, 1), none, torch.zeros(1, dtype=torch.int32), q.half()).shape == q.shape
+    with pytest.raises(ValueError, match="contiguous"):
+        c.append(pos.new_zeros(2), torch.zeros(2, 64, 2).mT, torch.zeros(2, 2, 64))
