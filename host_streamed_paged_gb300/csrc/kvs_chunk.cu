@@ -37,16 +37,18 @@
 //
 // Bound by the tensor pipe and what feeds it: 4 D operations a (row, key), the
 // cache's bytes being nothing beside them from some 100 rows on.  2048 rows over
-// 65536 tokens (32 / 8 heads, D 128) take 1490 us, 1.45 PFLOP/s, 75% of what
-// bf16 products measure; ncu sees the tensor pipe active on 50% of the cycles
-// (1024 rows over 16384), 58% of the issue slots taken.  A block of both tiles
+// 65536 tokens (32 / 8 heads, D 128) take 1470 us, 1.47 PFLOP/s, 76% of what
+// bf16 products measure in a burst (1565 in a long run under the power cap, 80%
+// of what they hold there); ncu sees the tensor pipe active on 51% of the cycles
+// (1024 rows over 16384), 59% of the issue slots taken.  A block of both tiles
 // takes 0.92 us; without the softmax's arithmetic and the dequantising, MMAs,
 // hand-overs and loads alone, 0.69; without the dequantising 0.85, without the
 // exponentials 0.78: the chain of a softmax warp (scores out of tensor memory,
-// 64 exponentials, weights back) is the longest.  D 64 runs at 0.82 PFLOP/s, as
-// its products are half as long beside the same exponentials; D 256 at 0.87:
-// room for one tile only, whose chain S, softmax, P V is hidden by the other
-// warpgroup's block alone.
+// 64 exponentials, weights back) is the longest.  D 64 runs at 0.82 PFLOP/s: its
+// products are half as long (tensor pipe 29%), but a block has the same chain,
+// neither of whose rates is reached (31% of the exponentials', 58% of the issue
+// slots); D 256 at 0.88: room for one tile only, whose chain S, softmax, P V is
+// hidden by the other warpgroup's block alone.
 //
 // What each choice measured (2048 rows over 65536 tokens, unless said):
 //   dequantising by warps of their own instead of the softmax's, one fused

@@ -503,8 +503,9 @@ __device__ __forceinline__ int seq_len(const Pool &pool, const int32_t *lens, in
 // tile k of that line is k, or k + skip from `front` on.
 // (So the work is cut over the tiles that count, and the masks are the two ends'
 // alone: 32 sequences of up to 60000 tokens under a window of 4096, 32 / 8 heads,
-// D 128, bf16, take 44 us for 113 MB, 2.6 TB/s, bound by a tile's instructions as
-// without a window: 3.6 TB/s there, where the launches weigh less.)
+// D 128, bf16, take 44 us for 113 MB, 2.6 TB/s: 8 for the two launches, the rest
+// bound by the latency between a tile's dependent instructions, with half of the
+// issue slots taken.  3.6 TB/s without a window, where the launches weigh less.)
 template <bool WIN>
 struct Seen {
     __device__ __forceinline__ Seen() {}

@@ -20,7 +20,7 @@
 //
 // Measured: 16755 rows of 24 + 4 heads, D 256, 64 dims rotated, f16: 75.2 us, 6.4
 // TB/s (94% of a copy's rate; ncu: DRAM 73% of its peak).  With norms, 12001
-// rows of 32 + 8 heads, D 128, bf16: 50.3 us, 4.9 TB/s: 62% of the issue slots
+// rows of 32 + 8 heads, D 128, bf16: 49.2 us, 5.0 TB/s: 54% of the issue slots
 // taken at 80 registers, so the loads in flight and the instructions bound it
 // together.  (Two steps on their way instead of one: 55.7 us, fewer warps fit; 28
 // warps an SM at 72 registers: 46.6, but f16 51.7 against 49.6 and fp32 92

@@ -197,7 +197,8 @@ enum {
 
 /* kvs_debug_inject fault kinds.  None of them makes a GPU fault: each is made
  * on the host, or (KVS_FAULT_DEVICE_WAIT) as a device-side wait that gives
- * up by its own limit and reports a status. */
+ * up by its own limit and reports a status, or (KVS_FAULT_DEVICE_LATE) as a
+ * pause. */
 enum {
     KVS_FAULT_NONE = 0,
     KVS_FAULT_FILL_ENQUEUE = 1, /* the nth ring refill enqueue fails */
@@ -658,13 +659,14 @@ kvs_status kvs_graph_destroy(kvs_ctx *ctx);
 const char *kvs_last_error(const kvs_ctx *ctx);
 
 /* kvs_debug_inject -- arm a fault (KVS_FAULT_*) that fires on the nth
- * (1-based) matching event; nth = 0 disarms.  Every fault is made on the host
- * or as a shortened device-side wait limit: no GPU fault is ever made.  With
- * ctx NULL, KVS_FAULT_DEVICE_WAIT or KVS_FAULT_DEVICE_LATE (hooks for it are in
- * kvs_q4_attend_chunk and kvs_prompt_attend_window) is armed for the nth launching call that
- * this thread makes of the batch operators with such waits (kvs_prompt_attend,
- * kvs_prompt_weights, kvs_q4_attend, kvs_q4_weights, the first and third under
- * a window, kvs_q4_attend_chunk).  Test API; the pages describe no such call. */
+ * (1-based) matching event; nth = 0 disarms.  Every fault is made on the host,
+ * as a shortened device-side wait limit or as a pause: no GPU fault is ever
+ * made.  With ctx NULL, KVS_FAULT_DEVICE_WAIT or KVS_FAULT_DEVICE_LATE (whose
+ * hooks are in kvs_q4_attend_chunk and kvs_prompt_attend_window) is armed for
+ * the nth launching call that this thread makes of the batch operators with
+ * such waits (kvs_prompt_attend, kvs_prompt_weights, kvs_q4_attend,
+ * kvs_q4_weights, the first and third under a window, kvs_q4_attend_chunk).
+ * Test API; the pages describe no such call. */
 kvs_status kvs_debug_inject(kvs_ctx *ctx, uint32_t fault, uint64_t nth);
 
 /* kvs_trace_read -- test API (no counterpart on the pages) for checking the
